@@ -1,0 +1,321 @@
+// dcr_fp4_matmul.hip -- products with 4-bit weights (gfx950).
+//
+//   y[i, j] = sum_k x[i, k] w[j, k]          dcr_fp4_matmul, dcr_fp4_matmul_q
+//   dx[i, k] = sum_j dy[i, j] w[j, k]        dcr_fp4_matmul_grad
+//
+// A 4-bit value times its block's scale has at most six significant bits, so
+// it is exact as bf16 and the matrix instructions take it as an operand with
+// no loss; the tensor scale of the NV format multiplies the finished sum.
+#include "dcr_fp4.h"
+
+namespace dcr {
+namespace {
+
+struct MArgs {
+    const void* x;              // bf16 rows, or the codes of 4-bit ones
+    const uint8_t* xs;          // scales of 4-bit rows
+    const uint8_t* wc;          // codes of the weights
+    const uint8_t* ws;          // their scales
+    const float* tensor_scale;  // NV
+    const int32_t* offsets;
+    void* y;
+    uint64_t m, x_stride, xs_stride, wc_stride, ws_stride, y_stride;
+    uint32_t n, k, groups;      // of one group; k = w->cols
+    uint32_t x_vec, w_vec;      // rows of x / w start on 16-byte borders
+    uint32_t row_tiles, col_tiles;   // upper bounds of the grid
+};
+
+struct RowTile {
+    uint32_t group;
+    uint64_t begin, end;        // rows of the tile; begin = end: past the last
+};
+
+// Tile `t` of BM rows, counted through the groups in order (a tile never
+// spans two groups).  Every wave looks through the offsets, 64 groups at a
+// time: tiles of each by its lane, their running sum by lane exchange.
+template <uint32_t BM>
+__device__ __forceinline__ RowTile row_tile(const MArgs& a, uint64_t t) {
+    if (!a.offsets) {
+        const uint64_t b = t * BM;
+        return {0, min(b, a.m), min(b + BM, a.m)};
+    }
+    const uint32_t lane = threadIdx.x & 63u;
+    const int64_t top = int64_t(a.m);
+    for (uint32_t g0 = 0; g0 < a.groups; g0 += 64) {
+        const uint32_t g = g0 + lane;
+        int64_t lo = 0, hi = 0;
+        if (g < a.groups) {
+            lo = min(max(int64_t(a.offsets[g]), int64_t(0)), top);
+            hi = min(max(int64_t(a.offsets[g + 1]), lo), top);
+        }
+        const uint32_t tiles = uint32_t((uint64_t(hi - lo) + BM - 1) / BM);
+        uint32_t sum = tiles;
+#pragma unroll
+        for (uint32_t d = 1; d < 64; d <<= 1) {
+            const uint32_t o = uint32_t(__shfl_up(int(sum), d, 64));
+            if (lane >= d) sum += o;
+        }
+        const uint32_t all = uint32_t(__shfl(int(sum), 63, 64));
+        if (t < all) {
+            const uint64_t hit = __ballot(t < sum);
+            const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+            const uint32_t before = uint32_t(__shfl(int(sum - tiles), l, 64));
+            const uint64_t first = uint32_t(__shfl(int(lo), l, 64)), last = uint32_t(__shfl(int(hi), l, 64));
+            const uint64_t b = first + (t - before) * BM;
+            return {g0 + uint32_t(l), b, min(b + BM, last)};
+        }
+        t -= all;
+    }
+    return {0, 0, 0};
+}
+
+// 16 codes of a row from element c0 (a multiple of 16); zeros from `cols` on
+__device__ __forceinline__ u32x2 codes16(const uint8_t* row, uint32_t c0, uint32_t cols, bool vec) {
+    u32x2 r = {0u, 0u};
+    if (c0 + 16 <= cols) {
+        if (vec) return *reinterpret_cast<const u32x2*>(row + c0 / 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i / 4] |= uint32_t(row[c0 / 2 + i]) << (8 * (i & 3));
+        return r;
+    }
+    if (c0 >= cols) return r;
+    const uint32_t n = cols - c0;       // 1 .. 15
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+        if (2 * i >= n) break;
+        uint32_t b = row[c0 / 2 + i];
+        if (2 * i + 1 == n) b &= 15u;
+        r[i / 4] |= b << (8 * (i & 3));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// ------------------------------------------------------------ general tile
+//
+// 64 x 64 results a workgroup, sums over 64 at a time: both operands go to
+// LDS as bf16 and four waves multiply 32 x 32 each.  Takes every size, stride
+// and alignment; the kernels below take over where their rules allow.
+constexpr uint32_t kGT = 64, kGPad = 72;
+
+template <bool GRAD, bool XQ, uint32_t WF, typename OUT>
+__global__ void __launch_bounds__(256) fp4_mm_general_kernel(MArgs a) {
+    __shared__ __attribute__((aligned(16))) uint16_t xt[kGT][kGPad], wt[kGT][kGPad];
+    const uint32_t t = threadIdx.x, lane = t & 63u, wave = t >> 6;
+    const uint32_t outs = GRAD ? a.k : a.n, red = GRAD ? a.n : a.k;
+    const float s = WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f;
+    const uint64_t tiles = uint64_t(a.row_tiles) * a.col_tiles;
+    for (uint64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const uint64_t mt = tile / a.col_tiles;
+        const uint32_t o0 = uint32_t(tile - mt * a.col_tiles) * kGT;
+        const RowTile rt = row_tile<kGT>(a, mt);
+        if (rt.begin == rt.end) break;
+        const uint64_t w0 = uint64_t(rt.group) * a.n;
+        f32x4 acc[2][2] = {};
+        for (uint32_t r0 = 0; r0 < red; r0 += kGT) {
+            __syncthreads();
+            {   // x: thread = 16 elements of a row
+                const uint32_t row = t >> 2, c = r0 + (t & 3u) * 16;
+                u32x4 v[2] = {};
+                if (rt.begin + row < rt.end && c < red) {
+                    if constexpr (XQ) {
+                        const uint8_t* xr = static_cast<const uint8_t*>(a.x) + (rt.begin + row) * a.x_stride;
+                        const u32x2 q = codes16(xr, c, red, a.x_vec);
+                        const uint32_t sb = a.xs[(rt.begin + row) * a.xs_stride + c / 32];
+                        v[0] = __builtin_bit_cast(u32x4, fp4_unpack8_bf16<DCR_FP4_MX>(q[0], sb));
+                        v[1] = __builtin_bit_cast(u32x4, fp4_unpack8_bf16<DCR_FP4_MX>(q[1], sb));
+                    } else {
+                        const uint16_t* xr = static_cast<const uint16_t*>(a.x) + (rt.begin + row) * a.x_stride + c;
+                        if (a.x_vec && c + 16 <= red) {
+                            v[0] = reinterpret_cast<const u32x4*>(xr)[0];
+                            v[1] = reinterpret_cast<const u32x4*>(xr)[1];
+                        } else {
+#pragma unroll
+                            for (uint32_t i = 0; i < 16; ++i)
+                                if (c + i < red) v[i / 8][(i / 2) & 3] |= uint32_t(xr[i]) << (16 * (i & 1));
+                        }
+                    }
+                }
+                *reinterpret_cast<u32x4*>(&xt[row][(t & 3u) * 16]) = v[0];
+                *reinterpret_cast<u32x4*>(&xt[row][(t & 3u) * 16 + 8]) = v[1];
+            }
+            {   // w: thread = 16 elements of a row of w
+                const uint32_t row = t >> 2, c16 = (t & 3u) * 16;
+                const uint32_t j = (GRAD ? r0 : o0) + row, c = (GRAD ? o0 : r0) + c16;
+                bf16x8 v[2] = {};
+                if (j < a.n && c < a.k) {
+                    const u32x2 q = codes16(a.wc + (w0 + j) * a.wc_stride, c, a.k, a.w_vec);
+                    const uint32_t sb = a.ws[(w0 + j) * a.ws_stride + c / fp4_block(WF)];
+                    v[0] = fp4_unpack8_bf16<WF>(q[0], sb);
+                    v[1] = fp4_unpack8_bf16<WF>(q[1], sb);
+                }
+                if constexpr (GRAD) {
+                    const u32x4 h[2] = {__builtin_bit_cast(u32x4, v[0]), __builtin_bit_cast(u32x4, v[1])};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        wt[c16 + i][row] = uint16_t(h[i / 8][(i / 2) & 3] >> (16 * (i & 1)));
+                } else {
+                    *reinterpret_cast<bf16x8*>(&wt[row][c16]) = v[0];
+                    *reinterpret_cast<bf16x8*>(&wt[row][c16 + 8]) = v[1];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (uint32_t kk = 0; kk < kGT; kk += 32) {
+                bf16x8 xa[2], wb[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t r = i * 16 + (lane & 15u), c = kk + (lane >> 4) * 8;
+                    xa[i] = *reinterpret_cast<const bf16x8*>(&xt[(wave & 1u) * 32 + r][c]);
+                    wb[i] = *reinterpret_cast<const bf16x8*>(&wt[(wave >> 1) * 32 + r][c]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], xa[i], acc[i][j], 0, 0, 0);
+            }
+        }
+        // a lane holds four neighbouring results of one row
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t row = rt.begin + (wave & 1u) * 32 + i * 16 + (lane & 15u);
+            if (row >= rt.end) continue;
+            OUT* out = static_cast<OUT*>(a.y) + row * a.y_stride;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t c = o0 + (wave >> 1) * 32 + j * 16 + (lane >> 4) * 4;
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r)
+                    if (c + r < outs) store_out(out + c + r, acc[i][j][r] * s);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr uint32_t kMaxGrid = 1u << 20;   // workgroups of the general kernel; more tiles are walked
+
+int32_t check_rows(const void* p, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t elem, const char* what) {
+    const std::string w = what;
+    if (!rows || !cols) return DCR_OK;
+    if (!p) return fp4_fail(DCR_E_INVAL, w + ": NULL");
+    if (reinterpret_cast<uintptr_t>(p) & (elem - 1)) return fp4_fail(DCR_E_INVAL, w + ": not aligned to its elements");
+    if (rows > 1 && stride < cols) return fp4_fail(DCR_E_INVAL, w + ": row stride smaller than a row");
+    if (stride >= (uint64_t(1) << 40)) return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^40 elements or more");
+    return DCR_OK;
+}
+
+template <bool GRAD, bool XQ, uint32_t WF>
+void launch_general(const MArgs& a, bool f32, uint32_t grid, hipStream_t st) {
+    if (f32)
+        hipLaunchKernelGGL((fp4_mm_general_kernel<GRAD, XQ, WF, float>), dim3(grid), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((fp4_mm_general_kernel<GRAD, XQ, WF, uint16_t>), dim3(grid), dim3(256), 0, st, a);
+}
+
+// Shared host path of the three products; xq: 4-bit x, else bf16 rows.
+int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, uint64_t x_stride,
+                const dcr_fp4_tensor* w, const int32_t* offsets, uint32_t n_groups, void* y, uint32_t y_type,
+                uint64_t y_stride, void* ws, uint64_t ws_bytes, hipStream_t st) {
+    int32_t rc = fp4_check(w, "weights");
+    if (rc) return rc;
+    if (xq) {
+        if ((rc = fp4_check(xq, "x"))) return rc;
+        if (xq->format != DCR_FP4_MX || w->format != DCR_FP4_MX)
+            return fp4_fail(DCR_E_INVAL, "a product of two 4-bit operands takes the MX format");
+        if (xq->cols != w->cols) return fp4_fail(DCR_E_INVAL, "x and the weights differ in columns");
+        m = xq->rows;
+    }
+    if (!n_groups || w->rows % n_groups) return fp4_fail(DCR_E_INVAL, "n_groups does not divide the weights' rows");
+    if (n_groups > 1 && !offsets) return fp4_fail(DCR_E_INVAL, "offsets is NULL");
+    if (n_groups > 65536) return fp4_fail(DCR_E_INVAL, "more than 65536 groups");
+    if (reinterpret_cast<uintptr_t>(offsets) & 3u) return fp4_fail(DCR_E_INVAL, "offsets not 4-byte aligned");
+    if (y_type != DCR_F32 && y_type != DCR_BF16) return fp4_fail(DCR_E_INVAL, "result type is neither fp32 nor bf16");
+    const uint64_t n = w->rows / n_groups, k = w->cols;
+    if (m >= (uint64_t(1) << 31) || n >= (uint64_t(1) << 31))
+        return fp4_fail(DCR_E_INVAL, "2^31 or more rows of x or of a group");
+    const uint64_t outs = grad ? k : n, red = grad ? n : k;
+    if (!xq && (rc = check_rows(x, m, red, x_stride, 2, grad ? "dy" : "x"))) return rc;
+    if ((rc = check_rows(y, m, outs, y_stride, y_type == DCR_F32 ? 4 : 2, grad ? "dx" : "y"))) return rc;
+    if (!ws || !al16(ws)) return fp4_fail(DCR_E_INVAL, "workspace is NULL or not 16-byte aligned");
+    if (ws_bytes < DCR_FP4_WORKSPACE_BYTES) return fp4_fail(DCR_E_CAPACITY, "workspace too small");
+    if (!m || !outs) return DCR_OK;
+    MArgs a{};
+    a.x = xq ? xq->codes : x;
+    a.m = m;
+    a.x_stride = m > 1 ? (xq ? xq->code_stride : x_stride) : 0;
+    if (xq) {
+        a.xs = static_cast<const uint8_t*>(xq->scales);
+        a.xs_stride = m > 1 ? xq->scale_stride : 0;
+    }
+    a.wc = static_cast<const uint8_t*>(w->codes);
+    a.ws = static_cast<const uint8_t*>(w->scales);
+    a.wc_stride = w->rows > 1 ? w->code_stride : 0;
+    a.ws_stride = w->rows > 1 ? w->scale_stride : 0;
+    a.tensor_scale = w->tensor_scale;
+    a.offsets = offsets;
+    a.y = y;
+    a.y_stride = m > 1 ? y_stride : 0;
+    a.n = uint32_t(n);
+    a.k = uint32_t(k);
+    a.groups = n_groups;
+    a.x_vec = al16(a.x) && (a.x_stride * (xq ? 1 : 2)) % 16 == 0;
+    a.w_vec = a.wc_stride % 16 == 0;
+    const bool f32 = y_type == DCR_F32, mx = w->format == DCR_FP4_MX;
+    // tiles of a grouped product: at most one short one for each group
+    a.row_tiles = uint32_t((m + kGT - 1) / kGT + (offsets ? n_groups : 0));
+    a.col_tiles = uint32_t((outs + kGT - 1) / kGT);
+    const uint64_t tiles = uint64_t(a.row_tiles) * a.col_tiles;
+    const uint32_t grid = uint32_t(tiles < kMaxGrid ? tiles : kMaxGrid);
+    if (xq)
+        launch_general<false, true, DCR_FP4_MX>(a, f32, grid, st);
+    else if (grad)
+        mx ? launch_general<true, false, DCR_FP4_MX>(a, f32, grid, st)
+           : launch_general<true, false, DCR_FP4_NV>(a, f32, grid, st);
+    else
+        mx ? launch_general<false, false, DCR_FP4_MX>(a, f32, grid, st)
+           : launch_general<false, false, DCR_FP4_NV>(a, f32, grid, st);
+    return fp4_launched();
+}
+
+}  // namespace
+}  // namespace dcr
+
+extern "C" {
+
+int32_t dcr_fp4_matmul(const void* x, uint64_t m, uint64_t x_stride, const dcr_fp4_tensor* w, const int32_t* offsets,
+                       uint32_t n_groups, void* y, uint32_t y_type, uint64_t y_stride, void* workspace_dev,
+                       uint64_t ws_bytes, void* stream) try {
+    dcr::set_error("");
+    return dcr::product(false, nullptr, x, m, x_stride, w, offsets, n_groups, y, y_type, y_stride, workspace_dev,
+                        ws_bytes, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_fp4_matmul_q(const dcr_fp4_tensor* x, const dcr_fp4_tensor* w, const int32_t* offsets, uint32_t n_groups,
+                         void* y, uint32_t y_type, uint64_t y_stride, void* workspace_dev, uint64_t ws_bytes,
+                         void* stream) try {
+    dcr::set_error("");
+    if (!x) return dcr::fp4_fail(DCR_E_INVAL, "x: NULL description");
+    return dcr::product(false, x, nullptr, 0, 0, w, offsets, n_groups, y, y_type, y_stride, workspace_dev, ws_bytes,
+                        static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_fp4_matmul_grad(const void* dy, uint64_t m, uint64_t dy_stride, const dcr_fp4_tensor* w,
+                            const int32_t* offsets, uint32_t n_groups, void* dx, uint32_t dx_type,
+                            uint64_t dx_stride, void* workspace_dev, uint64_t ws_bytes, void* stream) try {
+    dcr::set_error("");
+    return dcr::product(true, nullptr, dy, m, dy_stride, w, offsets, n_groups, dx, dx_type, dx_stride, workspace_dev,
+                        ws_bytes, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+}  // extern "C"

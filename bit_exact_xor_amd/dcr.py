@@ -7,8 +7,9 @@ device pointers and the current torch stream into a hipStream_t, and raises
 
 The names follow the C-ABI: ``dcr_plan_build``, ``dcr_encode``,
 ``dcr_encode_retry_partial``, ``dcr_encode_retry_from_delta``, ``dcr_apply``,
-``dcr_apply_overwrite_retry``, ``dcr_apply_sharded``, ``dcr_apply_overwrite_retry_sharded`` (plus the small
-helpers around them).
+``dcr_apply_overwrite_retry``, ``dcr_apply_sharded``, ``dcr_apply_overwrite_retry_sharded``, and for weights in 4
+bits ``dcr_fp4_quantize``, ``dcr_fp4_dequantize``, ``dcr_fp4_matmul``, ``dcr_fp4_matmul_q``,
+``dcr_fp4_matmul_grad`` (plus the small helpers around them).
 """
 from __future__ import annotations
 
@@ -102,6 +103,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.dcr_apply_overwrite_retry_sharded.argtypes = [P, P, P, P, P, U64, P, P, U64, P]
     lib.dcr_apply_overwrite_retry.restype = I32
     lib.dcr_apply_overwrite_retry.argtypes = [P, P, P, P, P, U64, P, P, U64, P]
+    lib.dcr_fp4_quantize.restype = I32
+    lib.dcr_fp4_quantize.argtypes = [P, U32, U64, P, U32, P, U64, P]
+    lib.dcr_fp4_dequantize.restype = I32
+    lib.dcr_fp4_dequantize.argtypes = [P, P, U32, U64, P]
+    for fn in (lib.dcr_fp4_matmul, lib.dcr_fp4_matmul_grad):
+        fn.restype = I32
+        fn.argtypes = [P, U64, U64, P, P, U32, P, U32, U64, P, U64, P]
+    lib.dcr_fp4_matmul_q.restype = I32
+    lib.dcr_fp4_matmul_q.argtypes = [P, P, P, U32, P, U32, U64, P, U64, P]
     lib.dcr_last_error.restype = ctypes.c_char_p
     lib.dcr_last_error.argtypes = []
     lib.dcr_set_kernel_events.restype = None
@@ -363,6 +373,190 @@ def dcr_apply_overwrite_retry_sharded(plan: Plan, shards, header: np.ndarray, di
         plan.handle, _ptrs(shards), hdr.ctypes.data, _dptr(dir_buf), _dptr(payload),
         expected_base_version, _dptr(result), _dptr(workspace), _nbytes(workspace), _stream(stream))
     _check(rc, "dcr_apply_overwrite_retry_sharded")
+
+
+# ------------------------------------------------------------ 4-bit weights
+
+FP4_MX, FP4_NV = 0, 1              # DCR_FP4_*: blocks of 32 with 2^n scales / of 16 with e4m3 scales
+F32, BF16 = 0, 1                   # DCR_F32, DCR_BF16
+FP4_CALIBRATE = 1                  # DCR_FP4_CALIBRATE
+FP4_WORKSPACE_BYTES = 64 << 20     # DCR_FP4_WORKSPACE_BYTES
+
+
+class Fp4Desc(ctypes.Structure):
+    """dcr_fp4_tensor."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("code_stride", ctypes.c_uint64),
+                ("scale_stride", ctypes.c_uint64), ("format", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+def fp4_blocks(cols: int, fmt: int) -> int:
+    """Scale blocks of a row."""
+    b = 32 if fmt == FP4_MX else 16
+    return -(-int(cols) // b)
+
+
+class Fp4Tensor:
+    """A 4-bit tensor of `rows` x `cols` elements in device memory: `codes`
+    (uint8, [rows, stride], rows padded to 16 bytes where made here),
+    `scales` (uint8, [rows, blocks]) and, in the NV format, `tensor_scale`
+    (fp32, one element).  Buffers that are passed in are used as they are
+    (any row stride); they may be canonical tensors a refit patches."""
+
+    def __init__(self, rows, cols, fmt=FP4_MX, device="cuda", codes=None, scales=None, tensor_scale=None):
+        import torch
+        rows, cols = int(rows), int(cols)
+        if fmt not in (FP4_MX, FP4_NV):
+            raise ValueError("fmt is FP4_MX or FP4_NV")
+        width, blocks = (cols + 1) // 2, fp4_blocks(cols, fmt)
+        if codes is None:
+            codes = torch.zeros(rows, -(-width // 16) * 16, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.zeros(rows, blocks, dtype=torch.uint8, device=codes.device)
+        if fmt == FP4_NV and tensor_scale is None:
+            tensor_scale = torch.ones(1, dtype=torch.float32, device=codes.device)
+        for name, t, w in (("codes", codes, width), ("scales", scales, blocks)):
+            if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < w or \
+                    (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name}: uint8 [{rows}, >= {w}] with contiguous rows expected")
+        if fmt == FP4_NV and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1):
+            raise ValueError("tensor_scale: one fp32 element expected")
+        _one_device(codes, scales, tensor_scale if fmt == FP4_NV else None)
+        self.rows, self.cols, self.fmt = rows, cols, fmt
+        self.codes, self.scales = codes, scales
+        self.tensor_scale = tensor_scale if fmt == FP4_NV else None
+        self.device = codes.device
+        self.desc = Fp4Desc(codes.data_ptr(), scales.data_ptr(),
+                            tensor_scale.data_ptr() if fmt == FP4_NV else None, rows, cols,
+                            codes.stride(0), scales.stride(0), fmt, 0)
+        self._ref = ctypes.addressof(self.desc)
+
+
+def fp4_workspace(device="cuda"):
+    """Workspace of the 4-bit calls (one call at a time; captured graphs that
+    may run together need one each)."""
+    import torch
+    return torch.empty(FP4_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _one_device(*tensors):
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError("4-bit calls take tensors in GPU memory")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+
+
+def _wide(t, rows, cols, name):
+    """(pointer, type, row stride) of a BF16 or fp32 matrix."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        ty = BF16
+    elif t.dtype == torch.float32:
+        ty = F32
+    else:
+        raise ValueError(f"{name}: bfloat16 or float32 expected, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols or \
+            (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: [{'m' if rows is None else rows}, {cols}] with contiguous rows expected, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), ty, t.stride(0)
+
+
+def _fp4_call(fn, what, device, stream, *args):
+    """Call `fn` with the device of its tensors current, on `stream` or that
+    device's current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc:
+        _check(rc, what)
+
+
+def dcr_fp4_quantize(x, q: Fp4Tensor, options=0, workspace=None, stream=None) -> None:
+    """Enqueue the quantisation of x (BF16 or fp32, [rows, cols]) into q;
+    FP4_CALIBRATE (NV) first takes q's tensor scale from x, and needs a
+    workspace."""
+    p, ty, stride = _wide(x, q.rows, q.cols, "x")
+    _one_device(x, q.codes, workspace)
+    _fp4_call(load_library().dcr_fp4_quantize, "dcr_fp4_quantize", q.device, stream, p, ty, stride, q._ref, options,
+              workspace.data_ptr() if workspace is not None else None,
+              _nbytes(workspace) if workspace is not None else 0)
+
+
+def dcr_fp4_dequantize(q: Fp4Tensor, y, stream=None) -> None:
+    """Enqueue reading q back into y (BF16 or fp32, [rows, cols])."""
+    p, ty, stride = _wide(y, q.rows, q.cols, "y")
+    _one_device(y, q.codes)
+    _fp4_call(load_library().dcr_fp4_dequantize, "dcr_fp4_dequantize", q.device, stream, q._ref, p, ty, stride)
+
+
+def _groups(w, offsets):
+    """(offsets pointer, groups, rows of a group) of a product with w."""
+    import torch
+    if offsets is None:
+        return None, 1, w.rows
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets: contiguous int32 [groups + 1] expected")
+    g = offsets.numel() - 1
+    if w.rows % g:
+        raise ValueError(f"{g} groups do not divide {w.rows} rows of weights")
+    return offsets.data_ptr(), g, w.rows // g
+
+
+def _product(fn, what, x, w, y, offsets, workspace, stream, x_cols, y_cols):
+    import torch
+    off, g, _n = _groups(w, offsets)
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: bfloat16 rows expected, got {x.dtype}")
+    xp, _ty, xs = _wide(x, None, x_cols, "x")
+    yp, ty, ys = _wide(y, x.shape[0], y_cols, "y")
+    _one_device(x, w.codes, y, offsets, workspace)
+    _fp4_call(fn, what, w.device, stream, xp, x.shape[0], xs, w._ref, off, g, yp, ty, ys, workspace.data_ptr(),
+              _nbytes(workspace))
+
+
+def dcr_fp4_matmul(x, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:
+    """Enqueue y = x w^T: x BF16 [m, cols], w [n, cols] in 4 bits, y BF16 or
+    fp32 [m, n].  With `offsets` (int32 [groups + 1], device) w holds `groups`
+    weights stacked along its rows and rows offsets[g] .. offsets[g + 1] of x
+    take weight g; the other rows of y are left as they are."""
+    _product(load_library().dcr_fp4_matmul, "dcr_fp4_matmul", x, w, y, offsets, _need(workspace, w), stream, w.cols,
+             _groups(w, offsets)[2])
+
+
+def dcr_fp4_matmul_q(x: Fp4Tensor, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:
+    """Enqueue y = x w^T with both operands in 4 bits (FP4_MX); else as
+    dcr_fp4_matmul."""
+    off, g, n = _groups(w, offsets)
+    ws = _need(workspace, w)
+    yp, ty, ys = _wide(y, x.rows, n, "y")
+    _one_device(x.codes, w.codes, y, offsets, ws)
+    _fp4_call(load_library().dcr_fp4_matmul_q, "dcr_fp4_matmul_q", w.device, stream, x._ref, w._ref, off, g, yp, ty,
+              ys, ws.data_ptr(), _nbytes(ws))
+
+
+def dcr_fp4_matmul_grad(dy, w: Fp4Tensor, dx, offsets=None, workspace=None, stream=None) -> None:
+    """Enqueue dx = dy w, the gradient of dcr_fp4_matmul with respect to x:
+    dy BF16 [m, n], dx BF16 or fp32 [m, cols]."""
+    _product(load_library().dcr_fp4_matmul_grad, "dcr_fp4_matmul_grad", dy, w, dx, offsets, _need(workspace, w),
+             stream, _groups(w, offsets)[2], w.cols)
+
+
+def _need(workspace, w):
+    if workspace is None:
+        raise ValueError("workspace: pass one made by fp4_workspace()")
+    return workspace
 
 
 def dcr_set_kernel_events(start=None, stop=None) -> None:

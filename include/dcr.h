@@ -553,6 +553,112 @@ int32_t dcr_stream_unpack(const dcr_plan* plan, const dcr_stream_header* header,
                           dcr_encode_result* result_dev,
                           void* workspace_dev, uint64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------ 4-bit weights
+ *
+ * A refit's canonical tensors may hold 4-bit weights (the humansand "weight
+ * teleportation" page refits NVFP4 checkpoints).  The calls below make such
+ * tensors from BF16 or fp32 ones, read them back, and multiply with them in
+ * the layout they are stored and patched in: a receiver multiplies with what
+ * dcr_apply has just written, no weight is laid out again.  Codes, scales and
+ * tensor scale are plain byte / fp32 regions to the encoder (elem_bytes 1, 1
+ * and 4). */
+enum { DCR_FP4_MX = 0, DCR_FP4_NV = 1 };
+enum { DCR_F32 = 0, DCR_BF16 = 1 };
+/* dcr_fp4_quantize option: take the tensor scale from the data */
+enum { DCR_FP4_CALIBRATE = 1 };
+
+/* A 4-bit tensor of `rows` rows of `cols` elements.  64 bytes.
+ *   codes         e2m1 codes (bit 3 the sign; 0 .5 1 1.5 2 3 4 6), element 2i
+ *                 of a row in the low nibble of its byte i; (cols + 1) / 2
+ *                 bytes a row, rows code_stride bytes apart
+ *   scales        one byte for each block of a row, the last block possibly
+ *                 short; rows scale_stride bytes apart
+ *                   DCR_FP4_MX  blocks of 32, value = code * 2^(byte - 127),
+ *                               255 is NaN
+ *                   DCR_FP4_NV  blocks of 16, value = code * e4m3(byte) *
+ *                               *tensor_scale, 127 is NaN
+ *   tensor_scale  DCR_FP4_NV: one fp32 in device memory (4-byte aligned),
+ *                 from 2^-100 to 2^117; DCR_FP4_MX: not looked at
+ *   reserved      0
+ * codes and scales are 16-byte aligned; any strides of at least a row are
+ * taken (of a tensor with one row they are not looked at).  Fewer than 2^31
+ * columns, 2^40 rows. */
+typedef struct {
+    void* codes;
+    void* scales;
+    float* tensor_scale;
+    uint64_t rows, cols;
+    uint64_t code_stride, scale_stride;
+    uint32_t format, reserved;
+} dcr_fp4_tensor;
+
+/* Quantise x (rows x cols of `q`, x_type DCR_F32 or DCR_BF16, rows x_stride
+ * elements apart, any alignment of whole elements) into q's codes and scales.
+ * The decisions are those of exact arithmetic, so the same weights give the
+ * same bytes on every call:
+ *   DCR_FP4_MX  byte = max(exponent bits of the fp32 max|x| - 2, 0)
+ *   DCR_FP4_NV  byte = e4m3 nearest max|x| / (6 * *tensor_scale), at most 448
+ *   code = e2m1 nearest x / scale, a tie to the even code, past 6 to 6, with
+ *   x's sign (also on zeros); magnitude 0 in a block whose scale is 0.
+ * A block holding a NaN or an infinity, and every block under a tensor scale
+ * outside its range, gets the NaN scale and codes 0.  Bytes between rows are
+ * left as they are; the unused nibble of an odd row is 0.
+ *   options  0, or DCR_FP4_CALIBRATE (DCR_FP4_NV): *tensor_scale is written
+ *            first, max|x| over the finite elements / 2688, held to its
+ *            range, 1 if x is all zeros
+ *   workspace_dev  DCR_FP4_CALIBRATE: 16-byte aligned, at least 2048 bytes
+ *                  (DCR_E_CAPACITY); else not looked at */
+int32_t dcr_fp4_quantize(const void* x, uint32_t x_type, uint64_t x_stride, const dcr_fp4_tensor* q,
+                         uint32_t options, void* workspace_dev, uint64_t ws_bytes, void* stream);
+
+/* Read q back into y (y_type DCR_F32 or DCR_BF16, rows y_stride elements
+ * apart), each value rounded once to y's type (fp32 first for DCR_FP4_NV with
+ * bf16 results).  Elements between rows are left as they are. */
+int32_t dcr_fp4_dequantize(const dcr_fp4_tensor* q, void* y, uint32_t y_type, uint64_t y_stride, void* stream);
+
+/* Product with 4-bit weights: y[i, :] = sum over k of x[i, k] * w[:, k].
+ *   x          m rows of w->cols bf16 elements, x_stride elements apart
+ *   w          the weights.  n_groups of them (experts) stacked along the
+ *              rows: group g is rows [g * n, (g + 1) * n), n = w->rows /
+ *              n_groups (which has to divide)
+ *   offsets    n_groups = 1: may be NULL (every row of x takes part).  Else
+ *              n_groups + 1 int32 in device memory, not descending: rows
+ *              [offsets[g], offsets[g + 1]) of x are multiplied with group
+ *              g, an empty range is fine; entries are held to 0 .. m.  Rows
+ *              of y outside [offsets[0], offsets[n_groups]) are left as they
+ *              are
+ *   y          m rows of n elements (y_type DCR_F32 or DCR_BF16), y_stride
+ *              elements apart; may not overlap x or w
+ *   workspace_dev, ws_bytes  scratch for products that split the sum; at
+ *              least DCR_FP4_WORKSPACE_BYTES (DCR_E_CAPACITY), 16-byte
+ *              aligned, one call at a time
+ * Products of the operands are exact, sums are held in fp32, and each result
+ * is rounded once to y's type after the tensor scale.  The order of a sum
+ * depends on the sizes alone, so equal calls give equal bits.
+ * A NaN scale makes the results of its row NaN.  x and y may have any
+ * alignment of whole elements; rows that start on 16-byte borders are faster. */
+#define DCR_FP4_WORKSPACE_BYTES (64u << 20)
+int32_t dcr_fp4_matmul(const void* x, uint64_t m, uint64_t x_stride, const dcr_fp4_tensor* w,
+                       const int32_t* offsets, uint32_t n_groups, void* y, uint32_t y_type, uint64_t y_stride,
+                       void* workspace_dev, uint64_t ws_bytes, void* stream);
+
+/* The same with x in 4 bits as well: x->rows rows of w->cols elements.  Both
+ * operands DCR_FP4_MX (the matrix instructions scale by powers of two only;
+ * DCR_E_INVAL otherwise). */
+int32_t dcr_fp4_matmul_q(const dcr_fp4_tensor* x, const dcr_fp4_tensor* w, const int32_t* offsets,
+                         uint32_t n_groups, void* y, uint32_t y_type, uint64_t y_stride, void* workspace_dev,
+                         uint64_t ws_bytes, void* stream);
+
+/* Gradient of dcr_fp4_matmul with respect to x: dx[i, :] = sum over the rows
+ * j of row i's group of dy[i, j] * w[j, :].  dy holds m rows of n bf16
+ * elements, dx m rows of w->cols (dx_type DCR_F32 or DCR_BF16); the remaining
+ * arguments and guarantees as there.  (The gradient of weights that are
+ * quantised with a straight-through estimate is the plain product of dy
+ * transposed and x: no operand of it is in 4 bits.) */
+int32_t dcr_fp4_matmul_grad(const void* dy, uint64_t m, uint64_t dy_stride, const dcr_fp4_tensor* w,
+                            const int32_t* offsets, uint32_t n_groups, void* dx, uint32_t dx_type,
+                            uint64_t dx_stride, void* workspace_dev, uint64_t ws_bytes, void* stream);
+
 /* Benchmark hook.  While set (both non-NULL), every encode, apply or retry
  * call made on this host thread records `start` on its stream just before its
  * main kernel (the encode tile kernels, or the apply kernel) and `stop` just
