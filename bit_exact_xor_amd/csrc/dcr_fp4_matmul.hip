@@ -6,92 +6,10 @@
 // A 4-bit value times its block's scale has at most six significant bits, so
 // it is exact as bf16 and the matrix instructions take it as an operand with
 // no loss; the tensor scale of the NV format multiplies the finished sum.
-#include "dcr_fp4.h"
+#include "dcr_fp4_mm.h"
 
 namespace dcr {
 namespace {
-
-struct MArgs {
-    const void* x;              // bf16 rows, or the codes of 4-bit ones
-    const uint8_t* xs;          // scales of 4-bit rows
-    const uint8_t* wc;          // codes of the weights
-    const uint8_t* ws;          // their scales
-    const float* tensor_scale;  // NV
-    const int32_t* offsets;
-    void* y;
-    uint64_t m, x_stride, xs_stride, wc_stride, ws_stride, y_stride;
-    uint32_t n, k, groups;      // of one group; k = w->cols
-    uint32_t x_vec, w_vec;      // rows of x / w start on 16-byte borders
-    uint32_t row_tiles, col_tiles;   // upper bounds of the grid
-};
-
-struct RowTile {
-    uint32_t group;
-    uint64_t begin, end;        // rows of the tile; begin = end: past the last
-};
-
-// Tile `t` of BM rows, counted through the groups in order (a tile never
-// spans two groups).  Every wave looks through the offsets, 64 groups at a
-// time: tiles of each by its lane, their running sum by lane exchange.
-template <uint32_t BM>
-__device__ __forceinline__ RowTile row_tile(const MArgs& a, uint64_t t) {
-    if (!a.offsets) {
-        const uint64_t b = t * BM;
-        return {0, min(b, a.m), min(b + BM, a.m)};
-    }
-    const uint32_t lane = threadIdx.x & 63u;
-    const int64_t top = int64_t(a.m);
-    for (uint32_t g0 = 0; g0 < a.groups; g0 += 64) {
-        const uint32_t g = g0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (g < a.groups) {
-            lo = min(max(int64_t(a.offsets[g]), int64_t(0)), top);
-            hi = min(max(int64_t(a.offsets[g + 1]), lo), top);
-        }
-        const uint32_t tiles = uint32_t((uint64_t(hi - lo) + BM - 1) / BM);
-        uint32_t sum = tiles;
-#pragma unroll
-        for (uint32_t d = 1; d < 64; d <<= 1) {
-            const uint32_t o = uint32_t(__shfl_up(int(sum), d, 64));
-            if (lane >= d) sum += o;
-        }
-        const uint32_t all = uint32_t(__shfl(int(sum), 63, 64));
-        if (t < all) {
-            const uint64_t hit = __ballot(t < sum);
-            const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-            const uint32_t before = uint32_t(__shfl(int(sum - tiles), l, 64));
-            const uint64_t first = uint32_t(__shfl(int(lo), l, 64)), last = uint32_t(__shfl(int(hi), l, 64));
-            const uint64_t b = first + (t - before) * BM;
-            return {g0 + uint32_t(l), b, min(b + BM, last)};
-        }
-        t -= all;
-    }
-    return {0, 0, 0};
-}
-
-// 16 codes of a row from element c0 (a multiple of 16); zeros from `cols` on
-__device__ __forceinline__ u32x2 codes16(const uint8_t* row, uint32_t c0, uint32_t cols, bool vec) {
-    u32x2 r = {0u, 0u};
-    if (c0 + 16 <= cols) {
-        if (vec) return *reinterpret_cast<const u32x2*>(row + c0 / 2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i / 4] |= uint32_t(row[c0 / 2 + i]) << (8 * (i & 3));
-        return r;
-    }
-    if (c0 >= cols) return r;
-    const uint32_t n = cols - c0;       // 1 .. 15
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-        if (2 * i >= n) break;
-        uint32_t b = row[c0 / 2 + i];
-        if (2 * i + 1 == n) b &= 15u;
-        r[i / 4] |= b << (8 * (i & 3));
-    }
-    return r;
-}
-
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // ------------------------------------------------------------ general tile
 //
@@ -266,6 +184,8 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     a.x_vec = al16(a.x) && (a.x_stride * (xq ? 1 : 2)) % 16 == 0;
     a.w_vec = a.wc_stride % 16 == 0;
     const bool f32 = y_type == DCR_F32, mx = w->format == DCR_FP4_MX;
+    a.y_vec = (reinterpret_cast<uintptr_t>(y) % (f32 ? 16 : 8) == 0) && a.y_stride % 4 == 0;
+    if (!xq && !grad && m > 64 && fp4_mm_tile(a, w->format, f32, st)) return fp4_launched();
     // tiles of a grouped product: at most one short one for each group
     a.row_tiles = uint32_t((m + kGT - 1) / kGT + (offsets ? n_groups : 0));
     a.col_tiles = uint32_t((outs + kGT - 1) / kGT);

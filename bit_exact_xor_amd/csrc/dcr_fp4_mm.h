@@ -1,0 +1,101 @@
+// dcr_fp4_mm.h -- what the kernels of the 4-bit products share: their
+// arguments, the walk through grouped rows, and loads and stores at any
+// alignment.
+#pragma once
+#include "dcr_fp4.h"
+
+namespace dcr {
+
+struct MArgs {
+    const void* x;              // bf16 rows, or the codes of 4-bit ones
+    const uint8_t* xs;          // scales of 4-bit rows
+    const uint8_t* wc;          // codes of the weights
+    const uint8_t* ws;          // their scales
+    const float* tensor_scale;  // NV
+    const int32_t* offsets;
+    void* y;
+    uint64_t m, x_stride, xs_stride, wc_stride, ws_stride, y_stride;
+    uint32_t n, k, groups;      // of one group; k = w->cols
+    uint32_t x_vec, w_vec;      // rows of x / codes of w start on 16-byte borders
+    uint32_t y_vec;             // four results in a row may be stored at once
+    uint32_t row_tiles, col_tiles;   // upper bounds of the grid
+};
+
+struct RowTile {
+    uint32_t group;
+    uint64_t begin, end;        // rows of the tile; begin = end: past the last
+};
+
+// Tile `t` of BM rows, counted through the groups in order (a tile never
+// spans two groups).  Every wave looks through the offsets, 64 groups at a
+// time: tiles of each by its lane, their running sum by lane exchange.
+template <uint32_t BM>
+__device__ __forceinline__ RowTile row_tile(const MArgs& a, uint64_t t) {
+    if (!a.offsets) {
+        const uint64_t b = t * BM;
+        return {0, min(b, a.m), min(b + BM, a.m)};
+    }
+    const uint32_t lane = threadIdx.x & 63u;
+    const int64_t top = int64_t(a.m);
+    for (uint32_t g0 = 0; g0 < a.groups; g0 += 64) {
+        const uint32_t g = g0 + lane;
+        int64_t lo = 0, hi = 0;
+        if (g < a.groups) {
+            lo = min(max(int64_t(a.offsets[g]), int64_t(0)), top);
+            hi = min(max(int64_t(a.offsets[g + 1]), lo), top);
+        }
+        const uint32_t tiles = uint32_t((uint64_t(hi - lo) + BM - 1) / BM);
+        uint32_t sum = tiles;
+#pragma unroll
+        for (uint32_t d = 1; d < 64; d <<= 1) {
+            const uint32_t o = uint32_t(__shfl_up(int(sum), d, 64));
+            if (lane >= d) sum += o;
+        }
+        const uint32_t all = uint32_t(__builtin_amdgcn_readlane(int(sum), 63));
+        if (t < all) {
+            const uint64_t hit = __ballot(t < sum);
+            const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+            // the same in every lane: kept in scalar registers
+            auto of_lane = [&](uint32_t v) { return uint32_t(__builtin_amdgcn_readlane(int(v), l)); };
+            const uint32_t before = of_lane(sum - tiles);
+            const uint64_t first = of_lane(uint32_t(lo)), last = of_lane(uint32_t(hi));
+            const uint64_t b = first + (t - before) * BM;
+            return {g0 + uint32_t(l), b, min(b + BM, last)};
+        }
+        t -= all;
+    }
+    return {0, 0, 0};
+}
+
+// 16 codes of a row from element c0 (a multiple of 16); zeros from `cols` on
+__device__ __forceinline__ u32x2 codes16(const uint8_t* row, uint32_t c0, uint32_t cols, bool vec) {
+    u32x2 r = {0u, 0u};
+    if (c0 + 16 <= cols) {
+        if (vec) return *reinterpret_cast<const u32x2*>(row + c0 / 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i / 4] |= uint32_t(row[c0 / 2 + i]) << (8 * (i & 3));
+        return r;
+    }
+    if (c0 >= cols) return r;
+    const uint32_t n = cols - c0;       // 1 .. 15
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+        if (2 * i >= n) break;
+        uint32_t b = row[c0 / 2 + i];
+        if (2 * i + 1 == n) b &= 15u;
+        r[i / 4] |= b << (8 * (i & 3));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+
+// kernels for parts of the range (false: not for these arguments)
+bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
+
+}  // namespace dcr

@@ -1,0 +1,250 @@
+// dcr_fp4_tile.hip -- bf16 rows times 4-bit weights in large tiles (gfx950).
+#include "dcr_fp4_mm.h"
+
+namespace dcr {
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void glb_void;
+
+constexpr uint32_t kBK = 128;          // elements of the sum a step takes
+constexpr uint32_t kRowB = kBK * 2;    // bytes of a row of x in LDS
+
+// 32 codes of a row from element k; zeros from `cols` on
+__device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_t cols, bool vec) {
+    if (vec && k + 32 <= cols) return *reinterpret_cast<const u32x4*>(row + k / 2);
+    const u32x2 a = codes16(row, k, cols, false), b = codes16(row, k + 16, cols, false);
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool ALIGNED>
+__global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
+    constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16, DMA = BM / 4 / W;
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[BM * kRowB], buf1[BM * kRowB];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r16 = lane & 15u, quad = lane >> 4;
+    const uint32_t wm = wave % WM, wn = wave / WM;
+
+    // eight compute dies take workgroups in turn: give each a run of tiles,
+    // walked four row tiles at a time so that its L2 serves a block of both
+    // operands
+    const uint32_t total = a.row_tiles * a.col_tiles;
+    uint32_t id = blockIdx.x;
+    const uint32_t per = total / 8;
+    if (id < per * 8) id = (id & 7u) * per + (id >> 3);
+    constexpr uint32_t SM = 4;
+    const uint32_t strip = id / (SM * a.col_tiles), in = id - strip * SM * a.col_tiles;
+    const uint32_t sm = min(SM, a.row_tiles - strip * SM);
+    const uint32_t rt_i = strip * SM + in % sm, ct = in / sm;
+
+    const RowTile rt = row_tile<BM>(a, rt_i);
+    if (rt.begin == rt.end) return;
+    const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = ct * BN;
+
+    // x: a row of LDS is 16 pieces of 16 bytes, piece c of row r at place
+    // c ^ (r & 15), so that 16 rows read at one c touch every bank once
+    const uint8_t* xb = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2;
+    const uint32_t xrow0 = wave * 4 + quad, xstep = uint32_t(a.x_stride) * 2;
+    // w: lane (r16, quad) holds row r16 of a subtile, elements [32 quad, +32)
+    // of a step: one MX block
+    const uint8_t* wb = a.wc + (uint64_t(rt.group) * a.n + n0) * a.wc_stride;
+    const uint8_t* sb = a.ws + (uint64_t(rt.group) * a.n + n0) * a.ws_stride;
+    uint32_t wo[NI], so[NI];
+#pragma unroll
+    for (uint32_t i = 0; i < NI; ++i) {
+        const uint32_t r = min(wn * (BN / WN) + i * 16 + r16, a.n - 1 - n0);
+        wo[i] = r * uint32_t(a.wc_stride) + quad * 16;
+        so[i] = r * uint32_t(a.ws_stride) + quad * (WF == DCR_FP4_MX ? 1 : 2);
+    }
+
+    // buffer descriptors: scalar base and step, 32-bit lane offsets
+    const auto xr = rsrc(xb, ((rows - 1) * uint32_t(a.x_stride) + a.k) * 2);
+    const uint32_t wrows = min(BN, a.n - n0);
+    const auto wr = rsrc(wb, (wrows - 1) * uint32_t(a.wc_stride) + (a.k + 1) / 2);
+    const auto sr = rsrc(sb, (wrows - 1) * uint32_t(a.ws_stride) + (a.k + fp4_block(WF) - 1) / fp4_block(WF));
+
+    f32x4 acc[NI][MI] = {};
+    u32x4 wq[2][NI];
+    uint32_t wsc[2][NI];
+
+    const uint32_t steps = (a.k + kBK - 1) / kBK, whole = a.k / kBK;
+
+    // a whole step, rows on 16-byte borders
+    auto load_w = [&](auto slot, uint32_t step) {
+        constexpr int S = decltype(slot)::value;
+        const uint32_t wk = step * (kBK / 2), sk = step * (kBK / fp4_block(WF));
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            wq[S][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], wk, 0));
+            if (WF == DCR_FP4_MX)
+                wsc[S][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], sk, 0);
+            else
+                wsc[S][i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], sk, 0);
+        }
+    };
+    auto load_x = [&](uint8_t* buf, uint32_t step) {
+        uint32_t r0 = xrow0;
+        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
+#pragma unroll
+        for (uint32_t i = 0; i < DMA; ++i) {
+            const uint32_t r = r0 + i * W * 4;
+            const uint32_t off = __umul24(min(r, rows - 1), xstep) + ((r16 ^ (r & 15u)) * 16);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16, off, step * kRowB, 0, 0);
+        }
+    };
+    // any step, any alignment: x through registers, zeros past the row's end
+    auto load_any = [&](uint8_t* buf, uint32_t step) {
+        const uint32_t kw = step * kBK + quad * 32;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            wq[0][i] = u32x4{0, 0, 0, 0};
+            wsc[0][i] = 0;
+            if (kw < a.k) {
+                wq[0][i] = codes32(wb + wo[i] - quad * 16, kw, a.k, a.w_vec);
+                const uint8_t* s = sb + step * (kBK / fp4_block(WF)) + so[i];
+                wsc[0][i] = s[0];
+                if (WF == DCR_FP4_NV && kw + 16 < a.k) wsc[0][i] |= uint32_t(s[1]) << 8;
+            }
+        }
+#pragma unroll 1
+        for (uint32_t i = 0; i < DMA; ++i) {
+            const uint32_t r = (i * W + wave) * 4 + quad;
+            const uint32_t k = step * kBK + (r16 ^ (r & 15u)) * 8;
+            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride + k;
+            u32x4 v = {0, 0, 0, 0};
+            if (k + 8 <= a.k) {
+                __builtin_memcpy(&v, p, 16);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    if (k + e < a.k) v[e / 2] |= uint32_t(p[e]) << (16 * (e & 1));
+            }
+            *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = v;
+        }
+    };
+    // a step's products, two row subtiles at a time: the next two are read
+    // from LDS while these multiply
+    auto compute = [&](const uint8_t* buf, auto slot) {
+        constexpr int S = decltype(slot)::value;
+        constexpr uint32_t H = 2, P = MI / H;
+        const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
+        bf16x8 x[2][H], w[NI];
+        auto read = [&](uint32_t ph) {
+#pragma unroll
+            for (uint32_t m = 0; m < H; ++m)
+                x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
+                                                                (((quad * 4 + ph / P) ^ r16) * 16));
+        };
+        read(0);
+#pragma unroll
+        for (uint32_t ph = 0; ph < 4 * P; ++ph) {
+            if (ph + 1 < 4 * P) read(ph + 1);
+            const uint32_t j = ph / P;
+            if (ph % P == 0)
+#pragma unroll
+                for (uint32_t i = 0; i < NI; ++i)
+                    w[i] = fp4_unpack8_bf16<WF>(wq[S][i][j], WF == DCR_FP4_MX ? wsc[S][i] : (wsc[S][i] >> (j / 2 * 8)) & 255u);
+#pragma unroll
+            for (uint32_t m = 0; m < H; ++m)
+#pragma unroll
+                for (uint32_t i = 0; i < NI; ++i)
+                    acc[i][(ph % P) * H + m] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    std::integral_constant<int, 0> c0;
+    std::integral_constant<int, 1> c1;
+
+    uint32_t t = 0;
+    if constexpr (ALIGNED) {
+        if (whole) {
+            load_x(buf0, 0);
+            load_w(c0, 0);
+        }
+        for (; t + 2 <= whole; t += 2) {
+            __syncthreads();
+            load_x(buf1, t + 1);
+            load_w(c1, t + 1);
+            compute(buf0, c0);
+            __syncthreads();
+            if (t + 2 < whole) {
+                load_x(buf0, t + 2);
+                load_w(c0, t + 2);
+            }
+            compute(buf1, c1);
+        }
+        if (t < whole) {
+            __syncthreads();
+            compute(buf0, c0);
+            ++t;
+        }
+    }
+#pragma unroll 1
+    for (; t < steps; ++t) {
+        __syncthreads();
+        load_any(buf0, t);
+        __syncthreads();
+        compute(buf0, c0);
+    }
+
+    const float s = WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f;
+#pragma unroll
+    for (uint32_t m = 0; m < MI; ++m) {
+        const uint32_t r = wm * (BM / WM) + m * 16 + r16;
+        if (r >= rows) continue;
+        OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            const uint32_t c = n0 + wn * (BN / WN) + i * 16 + quad * 4;
+            const f32x4 v = acc[i][m] * s;
+            if (a.y_vec && c + 4 <= a.n) {
+                store4(out + c, v);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (c + e < a.n) store_out(out + c + e, v[e]);
+            }
+        }
+    }
+}
+
+template <uint32_t WF, typename OUT, bool ALIGNED>
+void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+    if (bm == 256)
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
+    else
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 2, 2, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
+}
+template <uint32_t WF, typename OUT>
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+    a.x_vec && a.w_vec ? launch_tile<WF, OUT, true>(a, st, bm, grid) : launch_tile<WF, OUT, false>(a, st, bm, grid);
+}
+
+}  // namespace
+
+bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
+    // offsets inside a tile are 32 bits
+    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
+    uint32_t bm = 0;
+    for (uint32_t b : {256u, 128u}) {
+        const uint64_t rows = (a.m + b - 1) / b + (a.offsets ? a.groups : 0), cols = (uint64_t(a.n) + b - 1) / b;
+        if (rows * cols >= (1u << 22)) return false;
+        a.row_tiles = uint32_t(rows);
+        a.col_tiles = uint32_t(cols);
+        bm = b;
+        if (!a.offsets && rows * cols >= 192) break;
+    }
+    const uint32_t grid = a.row_tiles * a.col_tiles;
+    if (fmt == DCR_FP4_MX)
+        f32 ? launch<DCR_FP4_MX, float>(a, st, bm, grid) : launch<DCR_FP4_MX, uint16_t>(a, st, bm, grid);
+    else
+        f32 ? launch<DCR_FP4_NV, float>(a, st, bm, grid) : launch<DCR_FP4_NV, uint16_t>(a, st, bm, grid);
+    return true;
+}
+
+}  // namespace dcr
