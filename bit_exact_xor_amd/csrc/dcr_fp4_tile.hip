@@ -7,8 +7,17 @@ namespace {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void glb_void;
 
+constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
 constexpr uint32_t kBK = 128;          // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK * 2;    // bytes of a row of x in LDS
+
+// x in LDS: a row is 16 pieces of 16 bytes, piece c of row r at place
+// c ^ swizzle(r).  A 128-bit read serves 16 lanes at a time, half of them of
+// the next quad (rows 0-3 and 12-15 with rows 4-11 of the quad beside), whose
+// pieces differ in bit 2: those halves go to different halves of the row.
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
+    return (r & 3u) | ((r >> 1) & 4u) | (((r >> 3) ^ (r >> 2)) & 1u) << 3;
+}
 
 // 32 codes of a row from element k; zeros from `cols` on
 __device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_t cols, bool vec) {
@@ -21,7 +30,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t b
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
 
-template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool ALIGNED>
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool W2, bool ALIGNED>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16, DMA = BM / 4 / W;
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[BM * kRowB], buf1[BM * kRowB];
@@ -45,8 +54,6 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = ct * BN;
 
-    // x: a row of LDS is 16 pieces of 16 bytes, piece c of row r at place
-    // c ^ (r & 15), so that 16 rows read at one c touch every bank once
     const uint8_t* xb = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2;
     const uint32_t xrow0 = wave * 4 + quad, xstep = uint32_t(a.x_stride) * 2;
     // w: lane (r16, quad) holds row r16 of a subtile, elements [32 quad, +32)
@@ -68,22 +75,24 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const auto sr = rsrc(sb, (wrows - 1) * uint32_t(a.ws_stride) + (a.k + fp4_block(WF) - 1) / fp4_block(WF));
 
     f32x4 acc[NI][MI] = {};
-    u32x4 wq[2][NI];
-    uint32_t wsc[2][NI];
+    u32x4 wq[NI];
+    uint32_t wsc[NI];
+    bf16x8 w[W2 ? 2 : 1][NI];
 
-    const uint32_t steps = (a.k + kBK - 1) / kBK, whole = a.k / kBK;
+    const uint32_t steps = (a.k + kBK - 1) / kBK;
 
-    // a whole step, rows on 16-byte borders
-    auto load_w = [&](auto slot, uint32_t step) {
-        constexpr int S = decltype(slot)::value;
+    // A step of aligned rows.  Lanes past the end of the sum (a multiple of 32)
+    // read behind the descriptors' range, which gives zeros.
+    auto load_w = [&](uint32_t step) {
         const uint32_t wk = step * (kBK / 2), sk = step * (kBK / fp4_block(WF));
+        const uint32_t out = step * kBK + quad * 32 < a.k ? 0u : kOutside;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
-            wq[S][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], wk, 0));
+            wq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i] | out, wk, 0));
             if (WF == DCR_FP4_MX)
-                wsc[S][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], sk, 0);
+                wsc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i] | out, sk, 0);
             else
-                wsc[S][i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], sk, 0);
+                wsc[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i] | out, sk, 0);
         }
     };
     auto load_x = [&](uint8_t* buf, uint32_t step) {
@@ -91,9 +100,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
 #pragma unroll
         for (uint32_t i = 0; i < DMA; ++i) {
-            const uint32_t r = r0 + i * W * 4;
-            const uint32_t off = __umul24(min(r, rows - 1), xstep) + ((r16 ^ (r & 15u)) * 16);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16, off, step * kRowB, 0, 0);
+            const uint32_t r = r0 + i * W * 4, c = r16 ^ swizzle(r);
+            const uint32_t off = __umul24(min(r, rows - 1), xstep) + c * 16;
+            const uint32_t out = step * kBK + c * 8 < a.k ? 0u : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16, off | out, step * kRowB, 0, 0);
         }
     };
     // any step, any alignment: x through registers, zeros past the row's end
@@ -101,19 +111,19 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         const uint32_t kw = step * kBK + quad * 32;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
-            wq[0][i] = u32x4{0, 0, 0, 0};
-            wsc[0][i] = 0;
+            wq[i] = u32x4{0, 0, 0, 0};
+            wsc[i] = 0;
             if (kw < a.k) {
-                wq[0][i] = codes32(wb + wo[i] - quad * 16, kw, a.k, a.w_vec);
+                wq[i] = codes32(wb + wo[i] - quad * 16, kw, a.k, a.w_vec);
                 const uint8_t* s = sb + step * (kBK / fp4_block(WF)) + so[i];
-                wsc[0][i] = s[0];
-                if (WF == DCR_FP4_NV && kw + 16 < a.k) wsc[0][i] |= uint32_t(s[1]) << 8;
+                wsc[i] = s[0];
+                if (WF == DCR_FP4_NV && kw + 16 < a.k) wsc[i] |= uint32_t(s[1]) << 8;
             }
         }
 #pragma unroll 1
         for (uint32_t i = 0; i < DMA; ++i) {
             const uint32_t r = (i * W + wave) * 4 + quad;
-            const uint32_t k = step * kBK + (r16 ^ (r & 15u)) * 8;
+            const uint32_t k = step * kBK + (r16 ^ swizzle(r)) * 8;
             const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride + k;
             u32x4 v = {0, 0, 0, 0};
             if (k + 8 <= a.k) {
@@ -126,70 +136,69 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = v;
         }
     };
-    // a step's products, two row subtiles at a time: the next two are read
-    // from LDS while these multiply
-    auto compute = [&](const uint8_t* buf, auto slot) {
-        constexpr int S = decltype(slot)::value;
-        constexpr uint32_t H = 2, P = MI / H;
+    auto convert = [&](uint32_t j, uint32_t i) {
+        w[W2 ? j & 1 : 0][i] =
+            fp4_unpack8_bf16<WF>(wq[i][j], WF == DCR_FP4_MX ? wsc[i] : (wsc[i] >> (j / 2 * 8)) & 255u);
+    };
+    // A step's products, two row subtiles at a time.  While these multiply,
+    // the next two are read from LDS (and, with registers for it, part of the
+    // next quarter's codes converted).  The codes' registers are free once the
+    // last quarter is converted, and take the next step's then.
+    auto compute = [&](const uint8_t* buf, uint32_t next) {
+        constexpr uint32_t H = 2, P = MI / H, C = NI / P;
         const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
-        bf16x8 x[2][H], w[NI];
+        bf16x8 x[2][H];
         auto read = [&](uint32_t ph) {
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
                 x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
-                                                                (((quad * 4 + ph / P) ^ r16) * 16));
+                                                                (((quad * 4 + ph / P) ^ swizzle(r16)) * 16));
         };
         read(0);
 #pragma unroll
         for (uint32_t ph = 0; ph < 4 * P; ++ph) {
-            if (ph + 1 < 4 * P) read(ph + 1);
             const uint32_t j = ph / P;
-            if (ph % P == 0)
+            if (ph + 1 < 4 * P) read(ph + 1);
+            if (!W2 ? ph % P == 0 : ph == 0)
 #pragma unroll
-                for (uint32_t i = 0; i < NI; ++i)
-                    w[i] = fp4_unpack8_bf16<WF>(wq[S][i][j], WF == DCR_FP4_MX ? wsc[S][i] : (wsc[S][i] >> (j / 2 * 8)) & 255u);
+                for (uint32_t i = 0; i < NI; ++i) convert(j, i);
+            if (W2 && j < 3)
+#pragma unroll
+                for (uint32_t i = 0; i < C; ++i) convert(j + 1, (ph % P) * C + i);
+            if (ALIGNED && ph == 3 * P) load_w(next);
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i)
-                    acc[i][(ph % P) * H + m] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
+                    acc[i][(ph % P) * H + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        w[W2 ? j & 1 : 0][i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    std::integral_constant<int, 0> c0;
-    std::integral_constant<int, 1> c1;
 
-    uint32_t t = 0;
     if constexpr (ALIGNED) {
-        if (whole) {
+        if (steps) {
             load_x(buf0, 0);
-            load_w(c0, 0);
+            load_w(0);
         }
-        for (; t + 2 <= whole; t += 2) {
+        // two steps a turn (one loop exit keeps the sums in their registers);
+        // a step past the last is all zeros
+        for (uint32_t t = 0; t < steps; t += 2) {
             __syncthreads();
             load_x(buf1, t + 1);
-            load_w(c1, t + 1);
-            compute(buf0, c0);
+            compute(buf0, t + 1);
             __syncthreads();
-            if (t + 2 < whole) {
-                load_x(buf0, t + 2);
-                load_w(c0, t + 2);
-            }
-            compute(buf1, c1);
+            load_x(buf0, t + 2);
+            compute(buf1, t + 2);
         }
-        if (t < whole) {
-            __syncthreads();
-            compute(buf0, c0);
-            ++t;
-        }
-    }
+    } else {
 #pragma unroll 1
-    for (; t < steps; ++t) {
-        __syncthreads();
-        load_any(buf0, t);
-        __syncthreads();
-        compute(buf0, c0);
+        for (uint32_t t = 0; t < steps; ++t) {
+            __syncthreads();
+            load_any(buf0, t);
+            __syncthreads();
+            compute(buf0, 0);
+        }
     }
 
     const float s = WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f;
@@ -216,19 +225,19 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 template <uint32_t WF, typename OUT, bool ALIGNED>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, false, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 2, 2, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 2, 2, true, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
-    a.x_vec && a.w_vec ? launch_tile<WF, OUT, true>(a, st, bm, grid) : launch_tile<WF, OUT, false>(a, st, bm, grid);
+    a.x_vec && a.w_vec && a.k % 32 == 0 ? launch_tile<WF, OUT, true>(a, st, bm, grid) : launch_tile<WF, OUT, false>(a, st, bm, grid);
 }
 
 }  // namespace
 
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
-    // offsets inside a tile are 32 bits
+    // offsets inside a tile are 31 bits
     if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
     uint32_t bm = 0;
     for (uint32_t b : {256u, 128u}) {
