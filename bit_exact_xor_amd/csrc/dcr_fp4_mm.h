@@ -17,6 +17,7 @@ struct MArgs {
     uint64_t m, x_stride, xs_stride, wc_stride, ws_stride, y_stride;
     uint32_t n, k, groups;      // of one group; k = w->cols
     uint32_t x_vec, w_vec;      // rows of x / codes of w start on 16-byte borders
+    uint32_t s_vec;             // rows of scales start on 8-byte borders
     uint32_t y_vec;             // four results in a row may be stored at once
     uint32_t row_tiles, col_tiles;   // upper bounds of the grid
 };
@@ -95,7 +96,74 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
 }
 
+// Row and column tile of a workgroup.  The eight compute dies take workgroups
+// in turn: each gets a run of tiles, walked four row tiles at a time, so that
+// its L2 serves a block of both operands.
+struct TilePlace {
+    uint32_t row, col;
+};
+__device__ __forceinline__ TilePlace tile_place(const MArgs& a, uint32_t id) {
+    const uint32_t per = a.row_tiles * a.col_tiles / 8;
+    if (id < per * 8) id = (id & 7u) * per + (id >> 3);
+    constexpr uint32_t SM = 4;
+    const uint32_t strip = id / (SM * a.col_tiles), in = id - strip * SM * a.col_tiles;
+    const uint32_t sm = min(SM, a.row_tiles - strip * SM);
+    return {strip * SM + in % sm, in / sm};
+}
+
+// loop over compile-time indices
+template <uint32_t N, uint32_t I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<uint32_t, I>{});
+        static_for<N, I + 1>(f);
+    }
+}
+
+// The sums of a wave (a lane holds four neighbouring results of one row in
+// each 16 x 16 subtile), times s, rounded once.
+template <typename OUT, uint32_t MI, uint32_t NI>
+__device__ __forceinline__ void store_tile(const MArgs& a, const f32x4 (&acc)[NI][MI], float s, const RowTile& rt,
+                                           uint32_t rows, uint32_t row0, uint32_t col0, uint32_t outs) {
+    const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+    for (uint32_t m = 0; m < MI; ++m) {
+        const uint32_t r = row0 + m * 16 + (lane & 15u);
+        if (r >= rows) continue;
+        OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            const uint32_t c = col0 + i * 16 + (lane >> 4) * 4;
+            const f32x4 v = acc[i][m] * s;
+            if (a.y_vec && c + 4 <= outs) {
+                store4(out + c, v);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    if (c + e < outs) store_out(out + c + e, v[e]);
+            }
+        }
+    }
+}
+
+// Tile size (256 or 128) and grid of a product with `outs` columns of
+// results; 0 if there would be too many tiles.
+inline uint32_t tile_grid(MArgs* a, uint32_t outs, uint32_t* grid) {
+    uint32_t bm = 0;
+    for (uint32_t b : {256u, 128u}) {
+        const uint64_t rows = (a->m + b - 1) / b + (a->offsets ? a->groups : 0), cols = (uint64_t(outs) + b - 1) / b;
+        if (rows * cols >= (1u << 22)) return 0;
+        a->row_tiles = uint32_t(rows);
+        a->col_tiles = uint32_t(cols);
+        *grid = uint32_t(rows * cols);
+        bm = b;
+        if (!a->offsets && rows * cols >= 192) break;
+    }
+    return bm;
+}
+
 // kernels for parts of the range (false: not for these arguments)
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
+bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st);
 
 }  // namespace dcr

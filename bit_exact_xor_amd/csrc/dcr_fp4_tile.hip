@@ -38,21 +38,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
 
-    // eight compute dies take workgroups in turn: give each a run of tiles,
-    // walked four row tiles at a time so that its L2 serves a block of both
-    // operands
-    const uint32_t total = a.row_tiles * a.col_tiles;
-    uint32_t id = blockIdx.x;
-    const uint32_t per = total / 8;
-    if (id < per * 8) id = (id & 7u) * per + (id >> 3);
-    constexpr uint32_t SM = 4;
-    const uint32_t strip = id / (SM * a.col_tiles), in = id - strip * SM * a.col_tiles;
-    const uint32_t sm = min(SM, a.row_tiles - strip * SM);
-    const uint32_t rt_i = strip * SM + in % sm, ct = in / sm;
-
-    const RowTile rt = row_tile<BM>(a, rt_i);
+    const TilePlace at = tile_place(a, blockIdx.x);
+    const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
-    const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = ct * BN;
+    const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN;
 
     const uint8_t* xb = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2;
     const uint32_t xrow0 = wave * 4 + quad, xstep = uint32_t(a.x_stride) * 2;
@@ -201,31 +190,14 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     }
 
-    const float s = WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f;
-#pragma unroll
-    for (uint32_t m = 0; m < MI; ++m) {
-        const uint32_t r = wm * (BM / WM) + m * 16 + r16;
-        if (r >= rows) continue;
-        OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride;
-#pragma unroll
-        for (uint32_t i = 0; i < NI; ++i) {
-            const uint32_t c = n0 + wn * (BN / WN) + i * 16 + quad * 4;
-            const f32x4 v = acc[i][m] * s;
-            if (a.y_vec && c + 4 <= a.n) {
-                store4(out + c, v);
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < 4; ++e)
-                    if (c + e < a.n) store_out(out + c + e, v[e]);
-            }
-        }
-    }
+    store_tile<OUT, MI, NI>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
+                            n0 + wn * (BN / WN), a.n);
 }
 
 template <uint32_t WF, typename OUT, bool ALIGNED>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, false, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, WF == DCR_FP4_MX, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
     else
         hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 2, 2, true, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
 }
@@ -239,16 +211,9 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
     // offsets inside a tile are 31 bits
     if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
-    uint32_t bm = 0;
-    for (uint32_t b : {256u, 128u}) {
-        const uint64_t rows = (a.m + b - 1) / b + (a.offsets ? a.groups : 0), cols = (uint64_t(a.n) + b - 1) / b;
-        if (rows * cols >= (1u << 22)) return false;
-        a.row_tiles = uint32_t(rows);
-        a.col_tiles = uint32_t(cols);
-        bm = b;
-        if (!a.offsets && rows * cols >= 192) break;
-    }
-    const uint32_t grid = a.row_tiles * a.col_tiles;
+    uint32_t grid = 0;
+    const uint32_t bm = tile_grid(&a, a.n, &grid);
+    if (!bm) return false;
     if (fmt == DCR_FP4_MX)
         f32 ? launch<DCR_FP4_MX, float>(a, st, bm, grid) : launch<DCR_FP4_MX, uint16_t>(a, st, bm, grid);
     else

@@ -1,0 +1,191 @@
+// dcr_fp4_tile4.hip -- products of two 4-bit operands in large tiles (gfx950).
+//
+// The scaled matrix instruction multiplies 128 codes of a row with 128 of a
+// column, each run of 32 with its own power of two: a lane's operand is one
+// MX block and one scale byte, and nothing is converted.
+#include "dcr_fp4_mm.h"
+
+namespace dcr {
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
+constexpr uint32_t kBK = 256;                // elements of the sum a step takes
+constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
+
+// Codes in LDS: a row is 8 pieces of 16 bytes, piece c of row r at place
+// c ^ swizzle(r).  A 128-bit read serves 16 lanes at a time: rows 0-3 and
+// 12-15 of one quad with rows 4-11 of the quad beside, whose pieces differ in
+// bit 0; two rows fill the banks once.
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
+    return ((r >> 1) & 1u) | ((r >> 1) & 2u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+
+template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN>
+__global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) {
+    constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
+    constexpr uint32_t XD = BM / 8 / W, WD = BN / 8 / W;   // 1 KiB loads of a wave and step
+    static_assert(W * 64 == BM + BN, "a thread stages the scales of one row");
+    constexpr uint32_t kCodes = (BM + BN) * kRowB, kScales = (BM + BN) * (kBK / 32);
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kCodes + kScales], buf1[kCodes + kScales];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r16 = lane & 15u, quad = lane >> 4;
+    const uint32_t wm = wave % WM, wn = wave / WM;
+    const TilePlace at = tile_place(a, blockIdx.x);
+    const RowTile rt = row_tile<BM>(a, at.row);
+    if (rt.begin == rt.end) return;
+    const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN, cols = min(BN, a.n - n0);
+
+    const uint8_t* wb = a.wc + (uint64_t(rt.group) * a.n + n0) * a.wc_stride;
+    const uint8_t* sb = a.ws + (uint64_t(rt.group) * a.n + n0) * a.ws_stride;
+    const uint32_t xstep = uint32_t(a.x_stride), wstep = uint32_t(a.wc_stride);
+    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride, (rows - 1) * xstep + a.k / 2);
+    const auto wr = rsrc(wb, (cols - 1) * wstep + a.k / 2);
+
+    // the row whose scales this thread stages (x's, then w's), and where they
+    // go: [quarter of the step][quad][row of a subtile][subtile], so that a
+    // lane reads the bytes of its subtiles at once
+    const bool xside = threadIdx.x < BM;
+    const uint32_t srow = xside ? threadIdx.x : threadIdx.x - BM;
+    const uint8_t* sp = xside ? a.xs + (rt.begin + min(srow, rows - 1)) * a.xs_stride
+                              : sb + min(srow, cols - 1) * a.ws_stride;
+    const uint32_t subs = xside ? BM / 16 : BN / 16;
+    const uint32_t sdst = kCodes + (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
+    const uint32_t blocks = a.k / 32;
+
+    f32x4 acc[NI][MI] = {};
+    const uint32_t steps = (a.k + kBK - 1) / kBK;
+
+    // codes of a step by loads straight to LDS; pieces past the sum's end read
+    // behind the descriptors' range, which gives zeros
+    auto load = [&](uint8_t* buf, uint32_t step) {
+        uint32_t r0 = wave * 8 + (lane >> 3);
+        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i) {
+            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
+            const uint32_t out = step * kBK + c * 32 < a.k ? 0u : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16,
+                                                     (__umul24(min(r, rows - 1), xstep) + c * 16) | out, step * kRowB, 0, 0);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < WD; ++i) {
+            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
+            const uint32_t out = step * kBK + c * 32 < a.k ? 0u : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void*)(buf + BM * kRowB + (i * W + wave) * 1024), 16,
+                                                     (__umul24(min(r, cols - 1), wstep) + c * 16) | out, step * kRowB, 0, 0);
+        }
+    };
+    // the eight scale bytes of a step of this thread's row; zeros past the end
+    auto load_scales = [&](uint32_t step) -> uint64_t {
+        const uint32_t b = step * (kBK / 32);
+        if (b >= blocks) return 0;
+        if (a.s_vec && b + 8 <= blocks) {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(sp + b);
+            return v[0] | uint64_t(v[1]) << 32;
+        }
+        uint64_t v = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+            if (b + i < blocks) v |= uint64_t(sp[b + i]) << (8 * i);
+        return v;
+    };
+    auto store_scales = [&](uint8_t* buf, uint64_t v) {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) buf[sdst + i * 16 * subs] = uint8_t(v >> (8 * i));
+    };
+    auto compute = [&](const uint8_t* buf) {
+        constexpr uint32_t H = 2, P = MI / H;
+        const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
+        const uint8_t* wl = buf + BM * kRowB + (wn * (BN / WN) + r16) * kRowB;
+        u32x4 x[2][H], w[NI];
+        uint32_t xs[MI / 4], ws[NI / 4];
+        auto read = [&](uint32_t ph) {
+#pragma unroll
+            for (uint32_t m = 0; m < H; ++m)
+                x[ph & 1][m] = *reinterpret_cast<const u32x4*>(xl + ((ph % P) * H + m) * 16 * kRowB +
+                                                               (((ph / P * 4 + quad) ^ swizzle(r16)) * 16));
+        };
+        read(0);
+#pragma unroll
+        for (uint32_t ph = 0; ph < 2 * P; ++ph) {
+            const uint32_t j = ph / P;
+            if (ph % P == 0) {
+                const uint8_t* s = buf + kCodes + (j * 4 + quad) * 16 * (BM / 16) + r16 * (BM / 16) + wm * MI;
+                const uint8_t* t = buf + kCodes + BM * (kBK / 32) + (j * 4 + quad) * 16 * (BN / 16) + r16 * (BN / 16) + wn * NI;
+#pragma unroll
+                for (uint32_t i = 0; i < MI / 4; ++i) xs[i] = *reinterpret_cast<const uint32_t*>(s + i * 4);
+#pragma unroll
+                for (uint32_t i = 0; i < NI / 4; ++i) ws[i] = *reinterpret_cast<const uint32_t*>(t + i * 4);
+#pragma unroll
+                for (uint32_t i = 0; i < NI; ++i)
+                    w[i] = *reinterpret_cast<const u32x4*>(wl + i * 16 * kRowB + (((j * 4 + quad) ^ swizzle(r16)) * 16));
+            }
+            if (ph + 1 < 2 * P) read(ph + 1);
+            const auto mul = [&](auto mc, auto ic) {
+                constexpr uint32_t m = decltype(mc)::value, i = decltype(ic)::value;
+                const uint32_t mi = (ph % P) * H + m;
+                const u32x4 p = w[i], q = x[ph & 1][m];
+                const i32x8 pa = {int(p[0]), int(p[1]), int(p[2]), int(p[3]), 0, 0, 0, 0};
+                const i32x8 qa = {int(q[0]), int(q[1]), int(q[2]), int(q[3]), 0, 0, 0, 0};
+                if ((mi & 3) == m)
+                    acc[i][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pa, qa, acc[i][mi], 4, 4, i & 3, int(ws[i / 4]),
+                                                                                  m & 3, int(xs[mi / 4]));
+                else
+                    acc[i][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pa, qa, acc[i][mi], 4, 4, i & 3, int(ws[i / 4]),
+                                                                                  (m + H) & 3, int(xs[mi / 4]));
+            };
+            static_for<H>([&](auto m) { static_for<NI>([&](auto i) { mul(m, i); }); });
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    if (steps) {
+        load(buf0, 0);
+        store_scales(buf0, load_scales(0));
+    }
+    // two steps a turn (one loop exit keeps the sums in their registers); a
+    // step past the last is all zeros
+    for (uint32_t t = 0; t < steps; t += 2) {
+        __syncthreads();
+        load(buf1, t + 1);
+        const uint64_t s1 = load_scales(t + 1);
+        compute(buf0);
+        store_scales(buf1, s1);
+        __syncthreads();
+        load(buf0, t + 2);
+        const uint64_t s2 = load_scales(t + 2);
+        compute(buf1);
+        store_scales(buf0, s2);
+    }
+    store_tile<OUT, MI, NI>(a, acc, 1.0f, rt, rows, wm * (BM / WM), n0 + wn * (BN / WN), a.n);
+}
+
+template <typename OUT>
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+    if (bm == 256)
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, a);
+    else
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st) {
+    // pieces are whole blocks, offsets inside a tile 31 bits
+    if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22)) return false;
+    a.s_vec = a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0;
+    uint32_t grid = 0;
+    const uint32_t bm = tile_grid(&a, a.n, &grid);
+    if (!bm) return false;
+    f32 ? launch<float>(a, st, bm, grid) : launch<uint16_t>(a, st, bm, grid);
+    return true;
+}
+
+}  // namespace dcr
