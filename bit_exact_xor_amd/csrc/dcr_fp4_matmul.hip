@@ -184,7 +184,7 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     a.x_vec = al16(a.x) && (a.x_stride * (xq ? 1 : 2)) % 16 == 0;
     a.w_vec = a.wc_stride % 16 == 0;
     const bool f32 = y_type == DCR_F32, mx = w->format == DCR_FP4_MX;
-    a.y_vec = (reinterpret_cast<uintptr_t>(y) % (f32 ? 16 : 8) == 0) && a.y_stride % 4 == 0;
+    a.y_vec = al16(y) && (a.y_stride * (f32 ? 4 : 2)) % 16 == 0;
     if (!xq && !grad && m > 64 && fp4_mm_tile(a, w->format, f32, st)) return fp4_launched();
     if (xq && m > 32 && fp4_mm_tile4(a, f32, st)) return fp4_launched();
     // tiles of a grouped product: at most one short one for each group

@@ -17,8 +17,7 @@ struct MArgs {
     uint64_t m, x_stride, xs_stride, wc_stride, ws_stride, y_stride;
     uint32_t n, k, groups;      // of one group; k = w->cols
     uint32_t x_vec, w_vec;      // rows of x / codes of w start on 16-byte borders
-    uint32_t s_vec;             // rows of scales start on 8-byte borders
-    uint32_t y_vec;             // four results in a row may be stored at once
+    uint32_t y_vec;             // rows of y start on 16-byte borders
     uint32_t row_tiles, col_tiles;   // upper bounds of the grid
 };
 
@@ -100,7 +99,7 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 // in turn: each gets a run of tiles, walked four row tiles at a time, so that
 // its L2 serves a block of both operands.
 struct TilePlace {
-    uint32_t row, col;
+    uint32_t row, col, id;
 };
 __device__ __forceinline__ TilePlace tile_place(const MArgs& a, uint32_t id) {
     const uint32_t per = a.row_tiles * a.col_tiles / 8;
@@ -108,7 +107,7 @@ __device__ __forceinline__ TilePlace tile_place(const MArgs& a, uint32_t id) {
     constexpr uint32_t SM = 4;
     const uint32_t strip = id / (SM * a.col_tiles), in = id - strip * SM * a.col_tiles;
     const uint32_t sm = min(SM, a.row_tiles - strip * SM);
-    return {strip * SM + in % sm, in / sm};
+    return {strip * SM + in % sm, in / sm, id};
 }
 
 // loop over compile-time indices
@@ -120,29 +119,58 @@ __device__ __forceinline__ void static_for(F&& f) {
     }
 }
 
-// The sums of a wave (a lane holds four neighbouring results of one row in
-// each 16 x 16 subtile), times s, rounded once.
-template <typename OUT, uint32_t MI, uint32_t NI>
+// The sums of a wave, times s, rounded once.  A lane holds four neighbouring
+// results of one row in each 16 x 16 subtile: written as they are they make
+// 32-byte pieces of lines, which costs as much time as the product itself.
+// They go through LDS (`lds`: LB bytes of this wave alone) and leave as whole
+// rows of the wave's tile, 128 or 256 bytes each.  16-byte pieces of a row sit
+// at place p ^ row, which spreads both directions over the banks.
+template <typename OUT, uint32_t MI, uint32_t NI, uint32_t LB>
 __device__ __forceinline__ void store_tile(const MArgs& a, const f32x4 (&acc)[NI][MI], float s, const RowTile& rt,
-                                           uint32_t rows, uint32_t row0, uint32_t col0, uint32_t outs) {
-    const uint32_t lane = threadIdx.x & 63u;
+                                           uint32_t rows, uint32_t row0, uint32_t col0, uint32_t outs, uint8_t* lds) {
+    constexpr uint32_t E = 16 / sizeof(OUT), PR = NI * 16 / E, RB = PR * 16;     // elements of a piece, pieces, bytes of a row
+    constexpr uint32_t MP = LB / RB / 16 < MI ? LB / RB / 16 : MI, RI = 64 / PR; // row subtiles of a pass, rows of a store
+    static_assert(MP && MI % MP == 0 && 64 % PR == 0, "store_tile");
+    const uint32_t lane = threadIdx.x & 63u, r16 = lane & 15u, quad = lane >> 4;
+    const uint32_t piece = lane % PR, col = col0 + piece * E;
 #pragma unroll
-    for (uint32_t m = 0; m < MI; ++m) {
-        const uint32_t r = row0 + m * 16 + (lane & 15u);
-        if (r >= rows) continue;
-        OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride;
+    for (uint32_t p = 0; p < MI / MP; ++p) {
 #pragma unroll
-        for (uint32_t i = 0; i < NI; ++i) {
-            const uint32_t c = col0 + i * 16 + (lane >> 4) * 4;
-            const f32x4 v = acc[i][m] * s;
-            if (a.y_vec && c + 4 <= outs) {
-                store4(out + c, v);
+        for (uint32_t m = 0; m < MP; ++m)
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) {
+                const f32x4 v = acc[i][p * MP + m] * s;
+                uint8_t* row = lds + (m * 16 + r16) * RB;
+                if constexpr (sizeof(OUT) == 4)
+                    store4(reinterpret_cast<float*>(row + ((i * 4 + quad) ^ (r16 & (PR - 1))) * 16), v);
+                else
+                    store4(reinterpret_cast<uint16_t*>(row + ((i * 2 + quad / 2) ^ (r16 & (PR - 1))) * 16 + (quad & 1u) * 8), v);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (uint32_t i = 0; i < MP * 16 / RI; ++i) {
+            const uint32_t lr = i * RI + lane / PR, r = row0 + p * MP * 16 + lr;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(lds + lr * RB + (piece ^ (lr & (PR - 1))) * 16);
+            if (r >= rows) continue;
+            OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride + col;
+            if (a.y_vec && col + E <= outs) {
+                *reinterpret_cast<u32x4*>(out) = v;
             } else {
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e)
-                    if (c + e < outs) store_out(out + c + e, v[e]);
+                for (uint32_t e = 0; e < E; ++e)
+                    if (col + e < outs) {
+                        if constexpr (sizeof(OUT) == 4)
+                            out[e] = __uint_as_float(v[e]);
+                        else
+                            out[e] = uint16_t(v[e / 2] >> (16 * (e & 1)));
+                    }
             }
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
 }
 

@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     }
 
-    store_tile<OUT, MI, NI>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
-                            n0 + wn * (BN / WN), a.n);
+    __syncthreads();
+    constexpr uint32_t LB = BM * kRowB / W;   // one buffer: the variant for any alignment has no second
+    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
+                                n0 + wn * (BN / WN), a.n, buf0 + wave * LB);
 }
 
 template <uint32_t WF, typename OUT, bool ALIGNED>

@@ -27,7 +27,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t b
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
 
-template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN>
+template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool SV>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) {
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
     constexpr uint32_t XD = BM / 8 / W, WD = BN / 8 / W;   // 1 KiB loads of a wave and step
@@ -51,13 +51,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     // the row whose scales this thread stages (x's, then w's), and where they
     // go: [quarter of the step][quad][row of a subtile][subtile], so that a
     // lane reads the bytes of its subtiles at once
-    const bool xside = threadIdx.x < BM;
-    const uint32_t srow = xside ? threadIdx.x : threadIdx.x - BM;
-    const uint8_t* sp = xside ? a.xs + (rt.begin + min(srow, rows - 1)) * a.xs_stride
-                              : sb + min(srow, cols - 1) * a.ws_stride;
+    const bool xside = wave < BM / 64;      // whole waves: the descriptor stays scalar
+    const uint32_t srow = threadIdx.x - (xside ? 0 : BM), last = (xside ? rows : cols) - 1;
+    const uint32_t sstep = uint32_t(xside ? a.xs_stride : a.ws_stride), blocks = a.k / 32;
+    const auto sr = rsrc(xside ? a.xs + rt.begin * a.xs_stride : sb, last * sstep + blocks);
+    const uint32_t soff = min(srow, last) * sstep;
     const uint32_t subs = xside ? BM / 16 : BN / 16;
     const uint32_t sdst = kCodes + (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
-    const uint32_t blocks = a.k / 32;
 
     f32x4 acc[NI][MI] = {};
     const uint32_t steps = (a.k + kBK - 1) / kBK;
@@ -83,22 +83,24 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         }
     };
     // the eight scale bytes of a step of this thread's row; zeros past the end
-    auto load_scales = [&](uint32_t step) -> uint64_t {
+    auto load_scales = [&](uint32_t step) -> u32x2 {
         const uint32_t b = step * (kBK / 32);
-        if (b >= blocks) return 0;
-        if (a.s_vec && b + 8 <= blocks) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(sp + b);
-            return v[0] | uint64_t(v[1]) << 32;
-        }
-        uint64_t v = 0;
+        u32x2 v = {0, 0};
+        if constexpr (SV) {
+            const auto q = __builtin_amdgcn_raw_buffer_load_b64(sr, soff | (b < blocks ? 0u : kOutside), b, 0);
+            v = __builtin_bit_cast(u32x2, q);
+        } else {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i)
-            if (b + i < blocks) v |= uint64_t(sp[b + i]) << (8 * i);
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint32_t out = b + i < blocks ? 0u : kOutside;
+                v[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, (soff + i) | out, b, 0)) << (8 * (i & 3));
+            }
+        }
         return v;
     };
-    auto store_scales = [&](uint8_t* buf, uint64_t v) {
+    auto store_scales = [&](uint8_t* buf, u32x2 v) {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) buf[sdst + i * 16 * subs] = uint8_t(v >> (8 * i));
+        for (uint32_t i = 0; i < 8; ++i) buf[sdst + i * 16 * subs] = uint8_t(v[i / 4] >> (8 * (i & 3)));
     };
     auto compute = [&](const uint8_t* buf) {
         constexpr uint32_t H = 2, P = MI / H;
@@ -155,36 +157,45 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     for (uint32_t t = 0; t < steps; t += 2) {
         __syncthreads();
         load(buf1, t + 1);
-        const uint64_t s1 = load_scales(t + 1);
+        const u32x2 s1 = load_scales(t + 1);
         compute(buf0);
         store_scales(buf1, s1);
         __syncthreads();
         load(buf0, t + 2);
-        const uint64_t s2 = load_scales(t + 2);
+        const u32x2 s2 = load_scales(t + 2);
         compute(buf1);
         store_scales(buf0, s2);
     }
-    store_tile<OUT, MI, NI>(a, acc, 1.0f, rt, rows, wm * (BM / WM), n0 + wn * (BN / WN), a.n);
+    __syncthreads();
+    constexpr uint32_t LB = (BM + BN) * kRowB * 2 / W;
+    uint8_t* mine = wave < W / 2 ? buf0 + wave * LB : buf1 + (wave - W / 2) * LB;
+    store_tile<OUT, MI, NI, LB>(a, acc, 1.0f, rt, rows, wm * (BM / WM), n0 + wn * (BN / WN), a.n, mine);
 }
 
-template <typename OUT>
+template <typename OUT, bool SV>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, SV>), dim3(grid), dim3(512), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2, SV>), dim3(grid), dim3(256), 0, st, a);
 }
 
 }  // namespace
 
 bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st) {
     // pieces are whole blocks, offsets inside a tile 31 bits
-    if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22)) return false;
-    a.s_vec = a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0;
+    if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) ||
+        a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
+        return false;
+    // whole steps of scales at 8-byte borders: one load each
+    const bool sv = a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0;
     uint32_t grid = 0;
     const uint32_t bm = tile_grid(&a, a.n, &grid);
     if (!bm) return false;
-    f32 ? launch<float>(a, st, bm, grid) : launch<uint16_t>(a, st, bm, grid);
+    if (sv)
+        f32 ? launch<float, true>(a, st, bm, grid) : launch<uint16_t, true>(a, st, bm, grid);
+    else
+        f32 ? launch<float, false>(a, st, bm, grid) : launch<uint16_t, false>(a, st, bm, grid);
     return true;
 }
 
