@@ -1,0 +1,180 @@
+// dcr_fp4_grad.hip -- gradient of a 4-bit product with respect to x, in large
+// tiles (gfx950): dx[i, k] = sum_j dy[i, j] w[j, k].
+//
+// The sum runs over the rows of w, along which neither the codes nor their
+// scales are contiguous, while a matrix operand wants eight neighbours of the
+// sum in a lane.  So a step's codes (64 rows of the tile's columns) are
+// converted once for the workgroup, written to LDS as bf16 rows, and read
+// back by the transposing LDS load, four rows of a column at a time.
+#include "dcr_fp4_mm.h"
+
+namespace dcr {
+namespace {
+
+constexpr uint32_t kBJ = 64;             // rows of w (elements of the sum) a step takes
+constexpr uint32_t kRowB = kBJ * 2;      // bytes of a row of dy in LDS
+
+// dy in LDS: piece c (16 bytes) of row r at place c ^ swizzle(r); see the
+// 4-bit tiles, whose rows have the same 128 bytes
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
+    return ((r >> 1) & 1u) | ((r >> 1) & 2u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
+}
+// w in LDS: block b (16 columns, 32 bytes) of row j at place b ^ turn(j): the
+// eight rows that half a wave reads at once, 0-3 and 8-11 of each 16, fall on
+// different banks
+__device__ __forceinline__ uint32_t turn(uint32_t j) { return (j & 3u) | ((j >> 1) & 4u); }
+
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BO, uint32_t WM, uint32_t WN>
+__global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
+    constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BO / WN / 16;
+    constexpr uint32_t XD = BM / 8 / W;          // 1 KiB loads of dy of a wave and step
+    constexpr uint32_t NB = BO / 16, PP = NB / W;   // blocks of a row of w; of a thread and step
+    constexpr uint32_t RP = W * 64 / NB;         // rows of w between a thread's blocks
+    constexpr uint32_t kX = BM * kRowB, kW = kBJ * BO * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kX + kW], buf1[kX + kW];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r16 = lane & 15u, quad = lane >> 4;
+    const uint32_t wm = wave % WM, wn = wave / WM;
+    const TilePlace at = tile_place(a, blockIdx.x);
+    const RowTile rt = row_tile<BM>(a, at.row);
+    if (rt.begin == rt.end) return;
+    const uint32_t rows = uint32_t(rt.end - rt.begin), o0 = at.col * BO;
+
+    const uint32_t xstep = uint32_t(a.x_stride) * 2, wstep = uint32_t(a.wc_stride), sstep = uint32_t(a.ws_stride);
+    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2, (rows - 1) * xstep + a.n * 2);
+    const uint8_t* wb = a.wc + uint64_t(rt.group) * a.n * a.wc_stride + o0 / 2;
+    const uint8_t* sb = a.ws + uint64_t(rt.group) * a.n * a.ws_stride + o0 / fp4_block(WF);
+    // (a row's last eight bytes are read whole: they start on an 8-byte border)
+    const uint32_t wlast = ((a.k + 1) / 2 - o0 / 2 + 7) & ~7u, slast = (a.k + fp4_block(WF) - 1) / fp4_block(WF) - o0 / fp4_block(WF);
+
+    const uint32_t blk = threadIdx.x % NB, row0 = threadIdx.x / NB;
+    const uint32_t wdst = kX + row0 * BO * 2;
+    u32x2 q[PP];
+    uint32_t sc[PP];
+    f32x4 acc[NI][MI] = {};
+    const uint32_t steps = (a.n + kBJ - 1) / kBJ;
+
+    // dy by loads straight to LDS; past the sum's end (a multiple of 8) behind
+    // the descriptor's range, which gives zeros
+    auto load_x = [&](uint8_t* buf, uint32_t step) {
+        uint32_t r0 = wave * 8 + (lane >> 3);
+        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i) {
+            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
+            const uint32_t out = step * kBJ + c * 8 < a.n ? 0u : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16,
+                                                     (__umul24(min(r, rows - 1), xstep) + c * 16) | out, step * kRowB, 0, 0);
+        }
+    };
+    // 16 codes and their scale; rows past the sum's end and columns past the
+    // row's are zeros.  The rows of a step get a descriptor of their own, so
+    // that lane offsets stay small in a weight of any size.
+    auto load_w = [&](uint32_t step) {
+        const uint32_t j0 = min(step * kBJ, a.n - 1), nrow = min(kBJ, a.n - j0);
+        const auto wr = rsrc(wb + uint64_t(j0) * wstep, (nrow - 1) * wstep + wlast);
+        const auto sr = rsrc(sb + uint64_t(j0) * sstep, (nrow - 1) * sstep + slast);
+        const uint32_t in_row = blk * 16 + o0 < a.k ? 0u : kOutside;
+#pragma unroll
+        for (uint32_t i = 0; i < PP; ++i) {
+            const uint32_t r = row0 + i * RP, out = (step * kBJ + r < a.n ? 0u : kOutside) | in_row;
+            q[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, (__umul24(r, wstep) + blk * 8) | out, 0, 0));
+            sc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (__umul24(r, sstep) + blk * 16 / fp4_block(WF)) | out, 0, 0);
+        }
+    };
+    auto convert = [&](uint8_t* buf) {
+#pragma unroll
+        for (uint32_t i = 0; i < PP; ++i) {
+            const uint32_t r = row0 + i * RP;
+            uint8_t* dst = buf + wdst + i * RP * BO * 2 + (blk ^ turn(r)) * 32;
+            *reinterpret_cast<bf16x8*>(dst) = fp4_unpack8_bf16<WF>(q[i][0], sc[i]);
+            *reinterpret_cast<bf16x8*>(dst + 16) = fp4_unpack8_bf16<WF>(q[i][1], sc[i]);
+        }
+    };
+    auto compute = [&](const uint8_t* buf) {
+        constexpr uint32_t H = 2, P = MI / H;
+        const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
+        // a lane names four columns of a row and gets four rows of a column
+        const uint32_t jr = quad * 8 + (r16 >> 2);
+        const uint8_t* wl = buf + kX + jr * BO * 2 + (r16 & 3u) * 8;
+        bf16x8 x[2][H], w[NI];
+        auto read = [&](uint32_t ph) {
+#pragma unroll
+            for (uint32_t m = 0; m < H; ++m)
+                x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
+                                                                (((ph / P * 4 + quad) ^ swizzle(r16)) * 16));
+        };
+        read(0);
+#pragma unroll
+        for (uint32_t ph = 0; ph < 2 * P; ++ph) {
+            if (ph % P == 0)
+#pragma unroll
+                for (uint32_t i = 0; i < NI; ++i) {
+                    const uint8_t* p = wl + ph / P * 32 * BO * 2 + ((wn * NI + i) ^ turn(jr)) * 32;
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * BO * 2));
+                    w[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+            if (ph + 1 < 2 * P) read(ph + 1);
+#pragma unroll
+            for (uint32_t m = 0; m < H; ++m)
+#pragma unroll
+                for (uint32_t i = 0; i < NI; ++i)
+                    acc[i][(ph % P) * H + m] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    if (steps) {
+        load_x(buf0, 0);
+        load_w(0);
+        convert(buf0);
+        load_w(1);
+    }
+    // two steps a turn (one loop exit keeps the sums in their registers); a
+    // step past the last is all zeros
+    for (uint32_t t = 0; t < steps; t += 2) {
+        __syncthreads();
+        load_x(buf1, t + 1);
+        convert(buf1);
+        load_w(t + 2);
+        compute(buf0);
+        __syncthreads();
+        load_x(buf0, t + 2);
+        convert(buf0);
+        load_w(t + 3);
+        compute(buf1);
+    }
+    __syncthreads();
+    constexpr uint32_t LB = (kX + kW) * 2 / W;
+    uint8_t* mine = wave < W / 2 ? buf0 + wave * LB : buf1 + (wave - W / 2) * LB;
+    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
+                                o0 + wn * (BO / WN), a.k, mine);
+}
+
+template <uint32_t WF, typename OUT>
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+    if (bm == 256)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, a);
+    else
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
+    // pieces of dy are eight elements, offsets inside a tile 31 bits
+    if (!a.x_vec || !a.w_vec || a.n % 8 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24))
+        return false;
+    uint32_t grid = 0;
+    const uint32_t bm = tile_grid(&a, a.k, &grid);
+    if (!bm) return false;
+    if (fmt == DCR_FP4_MX)
+        f32 ? launch<DCR_FP4_MX, float>(a, st, bm, grid) : launch<DCR_FP4_MX, uint16_t>(a, st, bm, grid);
+    else
+        f32 ? launch<DCR_FP4_NV, float>(a, st, bm, grid) : launch<DCR_FP4_NV, uint16_t>(a, st, bm, grid);
+    return true;
+}
+
+}  // namespace dcr

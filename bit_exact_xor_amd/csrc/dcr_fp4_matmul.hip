@@ -185,8 +185,10 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     a.w_vec = a.wc_stride % 16 == 0;
     const bool f32 = y_type == DCR_F32, mx = w->format == DCR_FP4_MX;
     a.y_vec = al16(y) && (a.y_stride * (f32 ? 4 : 2)) % 16 == 0;
+    if (!grad && fp4_mm_rows(a, xq != nullptr, w->format, f32, st)) return fp4_launched();
     if (!xq && !grad && m > 64 && fp4_mm_tile(a, w->format, f32, st)) return fp4_launched();
-    if (xq && m > 32 && fp4_mm_tile4(a, f32, st)) return fp4_launched();
+    if (xq && m > 64 && fp4_mm_tile4(a, f32, st)) return fp4_launched();
+    if (grad && n && m > 32 && fp4_mm_grad(a, w->format, f32, st)) return fp4_launched();
     // tiles of a grouped product: at most one short one for each group
     a.row_tiles = uint32_t((m + kGT - 1) / kGT + (offsets ? n_groups : 0));
     a.col_tiles = uint32_t((outs + kGT - 1) / kGT);

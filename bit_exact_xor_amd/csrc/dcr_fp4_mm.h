@@ -6,6 +6,10 @@
 
 namespace dcr {
 
+typedef __attribute__((address_space(3))) void lds_void;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
 struct MArgs {
     const void* x;              // bf16 rows, or the codes of 4-bit ones
     const uint8_t* xs;          // scales of 4-bit rows
@@ -93,6 +97,23 @@ __device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+
+// Buffer descriptor: loads take a scalar base and step and a 32-bit lane
+// offset, and give zeros at offsets of `bytes` or more.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
+
+// 16 x 16 products of 128 codes each way, every lane's 32 codes with the power
+// of two in byte WB / XB of its scale words.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <uint32_t WB, uint32_t XB>
+__device__ __forceinline__ f32x4 mfma_fp4(u32x4 w, u32x4 x, f32x4 c, uint32_t ws, uint32_t xs) {
+    const i32x8 p = {int(w[0]), int(w[1]), int(w[2]), int(w[3]), 0, 0, 0, 0};
+    const i32x8 q = {int(x[0]), int(x[1]), int(x[2]), int(x[3]), 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, 4, 4, WB, int(ws), XB, int(xs));
 }
 
 // Row and column tile of a workgroup.  The eight compute dies take workgroups
@@ -192,6 +213,8 @@ inline uint32_t tile_grid(MArgs* a, uint32_t outs, uint32_t* grid) {
 
 // kernels for parts of the range (false: not for these arguments)
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
+bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st);
 bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st);
+bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
 
 }  // namespace dcr

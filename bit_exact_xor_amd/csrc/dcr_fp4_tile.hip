@@ -4,10 +4,7 @@
 namespace dcr {
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void glb_void;
 
-constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
 constexpr uint32_t kBK = 128;          // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK * 2;    // bytes of a row of x in LDS
 
@@ -24,10 +21,6 @@ __device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_
     if (vec && k + 32 <= cols) return *reinterpret_cast<const u32x4*>(row + k / 2);
     const u32x2 a = codes16(row, k, cols, false), b = codes16(row, k + 16, cols, false);
     return u32x4{a[0], a[1], b[0], b[1]};
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
 
 template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool W2, bool ALIGNED>

@@ -8,10 +8,7 @@
 namespace dcr {
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kOutside = 0x80000000u;   // a lane offset past every descriptor's range
 constexpr uint32_t kBK = 256;                // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
 
@@ -21,10 +18,6 @@ constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
 // bit 0; two rows fill the banks once.
 __device__ __forceinline__ uint32_t swizzle(uint32_t r) {
     return ((r >> 1) & 1u) | ((r >> 1) & 2u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
 
 template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool SV>
@@ -130,18 +123,12 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
                     w[i] = *reinterpret_cast<const u32x4*>(wl + i * 16 * kRowB + (((j * 4 + quad) ^ swizzle(r16)) * 16));
             }
             if (ph + 1 < 2 * P) read(ph + 1);
+            // byte of a subtile in its scale word: the subtile's index mod 4
             const auto mul = [&](auto mc, auto ic) {
                 constexpr uint32_t m = decltype(mc)::value, i = decltype(ic)::value;
                 const uint32_t mi = (ph % P) * H + m;
-                const u32x4 p = w[i], q = x[ph & 1][m];
-                const i32x8 pa = {int(p[0]), int(p[1]), int(p[2]), int(p[3]), 0, 0, 0, 0};
-                const i32x8 qa = {int(q[0]), int(q[1]), int(q[2]), int(q[3]), 0, 0, 0, 0};
-                if ((mi & 3) == m)
-                    acc[i][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pa, qa, acc[i][mi], 4, 4, i & 3, int(ws[i / 4]),
-                                                                                  m & 3, int(xs[mi / 4]));
-                else
-                    acc[i][mi] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pa, qa, acc[i][mi], 4, 4, i & 3, int(ws[i / 4]),
-                                                                                  (m + H) & 3, int(xs[mi / 4]));
+                acc[i][mi] = (mi & 3u) == m ? mfma_fp4<i & 3, m>(w[i], x[ph & 1][m], acc[i][mi], ws[i / 4], xs[mi / 4])
+                                            : mfma_fp4<i & 3, m + H>(w[i], x[ph & 1][m], acc[i][mi], ws[i / 4], xs[mi / 4]);
             };
             static_for<H>([&](auto m) { static_for<NI>([&](auto i) { mul(m, i); }); });
             __builtin_amdgcn_sched_barrier(0);

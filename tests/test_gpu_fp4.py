@@ -213,7 +213,8 @@ def check_product(op, fmt, m, n, k, dtype, data, groups=1, off=None, seed=0, x_p
 OPS = [("matmul", R.MX), ("matmul", R.NV), ("matmul_q", R.MX), ("grad", R.MX), ("grad", R.NV)]
 SIZES = [(1, 1, 1), (1, 16, 32), (1, 4096, 4096), (2, 100, 2048), (3, 7, 33), (5, 768, 2050), (16, 512, 256), (17, 130, 96),
          (24, 1030, 1024), (33, 64, 4096), (64, 256, 160), (65, 129, 257), (100, 1000, 2080), (128, 128, 128),
-         (200, 320, 448), (255, 513, 515), (256, 768, 2048), (300, 2048, 768), (512, 1024, 512), (1030, 300, 288)]
+         (200, 320, 448), (255, 513, 515), (256, 768, 2048), (300, 2048, 768), (512, 1024, 512), (1030, 300, 288),
+         (130, 64, 75), (70, 72, 33), (40, 8, 1), (300, 256, 31)]
 
 
 @pytest.mark.parametrize("op,fmt", OPS)
