@@ -14,11 +14,6 @@ namespace {
 constexpr uint32_t kBJ = 64;             // rows of w (elements of the sum) a step takes
 constexpr uint32_t kRowB = kBJ * 2;      // bytes of a row of dy in LDS
 
-// dy in LDS: piece c (16 bytes) of row r at place c ^ swizzle(r); see the
-// 4-bit tiles, whose rows have the same 128 bytes
-__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
-    return ((r >> 1) & 1u) | ((r >> 1) & 2u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
-}
 // w in LDS: block b (16 columns, 32 bytes) of row j at place b ^ turn(j): the
 // eight rows that half a wave reads at once, 0-3 and 8-11 of each 16, fall on
 // different banks
@@ -54,32 +49,48 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     f32x4 acc[NI][MI] = {};
     const uint32_t steps = (a.n + kBJ - 1) / kBJ;
 
-    // dy by loads straight to LDS; past the sum's end (a multiple of 8) behind
-    // the descriptor's range, which gives zeros
-    auto load_x = [&](uint8_t* buf, uint32_t step) {
-        uint32_t r0 = wave * 8 + (lane >> 3);
-        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
+    // dy by loads straight to LDS.  From the step on in which the sum ends (at a
+    // multiple of 8) lanes past the end read behind the descriptor's range,
+    // which gives zeros; a lane once past it stays there, so its offset is
+    // changed for good and the other steps spend nothing on it.
+    const uint32_t lr = wave * 8 + (lane >> 3), lc = (lane & 7u) ^ swizzle8(lr);
+    uint32_t xo[XD];
 #pragma unroll
-        for (uint32_t i = 0; i < XD; ++i) {
-            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
-            const uint32_t out = step * kBJ + c * 8 < a.n ? 0u : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16,
-                                                     (__umul24(min(r, rows - 1), xstep) + c * 16) | out, step * kRowB, 0, 0);
+    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(lr + i * W * 8, rows - 1) * xstep + lc * 16;
+    auto load_x = [&](uint8_t* buf, uint32_t step) {
+        if ((step + 1) * kBJ > a.n) {
+            const uint32_t out = step * kBJ + lc * 8 < a.n ? 0u : kOutside;
+#pragma unroll
+            for (uint32_t i = 0; i < XD; ++i) xo[i] |= out;
         }
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i) load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
     };
     // 16 codes and their scale; rows past the sum's end and columns past the
     // row's are zeros.  The rows of a step get a descriptor of their own, so
     // that lane offsets stay small in a weight of any size.
+    uint32_t wo[PP], so[PP];
+#pragma unroll
+    for (uint32_t i = 0; i < PP; ++i) {
+        const uint32_t in_row = blk * 16 + o0 < a.k ? 0u : kOutside;
+        wo[i] = ((row0 + i * RP) * wstep + blk * 8) | in_row;
+        so[i] = ((row0 + i * RP) * sstep + blk * 16 / fp4_block(WF)) | in_row;
+    }
     auto load_w = [&](uint32_t step) {
         const uint32_t j0 = min(step * kBJ, a.n - 1), nrow = min(kBJ, a.n - j0);
         const auto wr = rsrc(wb + uint64_t(j0) * wstep, (nrow - 1) * wstep + wlast);
         const auto sr = rsrc(sb + uint64_t(j0) * sstep, (nrow - 1) * sstep + slast);
-        const uint32_t in_row = blk * 16 + o0 < a.k ? 0u : kOutside;
+        if ((step + 1) * kBJ > a.n) {
+#pragma unroll
+            for (uint32_t i = 0; i < PP; ++i) {
+                const uint32_t out = step * kBJ + row0 + i * RP < a.n ? 0u : kOutside;
+                wo[i] |= out, so[i] |= out;
+            }
+        }
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
-            const uint32_t r = row0 + i * RP, out = (step * kBJ + r < a.n ? 0u : kOutside) | in_row;
-            q[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, (__umul24(r, wstep) + blk * 8) | out, 0, 0));
-            sc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, (__umul24(r, sstep) + blk * 16 / fp4_block(WF)) | out, 0, 0);
+            q[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, wo[i], 0, 0));
+            sc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], 0, 0);
         }
     };
     auto convert = [&](uint8_t* buf) {
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
                 x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
-                                                                (((ph / P * 4 + quad) ^ swizzle(r16)) * 16));
+                                                                (((ph / P * 4 + quad) ^ swizzle8(r16)) * 16));
         };
         read(0);
 #pragma unroll
@@ -124,6 +135,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (uint32_t m = 0; m < MI; ++m)
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
     if (steps) {

@@ -116,6 +116,38 @@ __device__ __forceinline__ f32x4 mfma_fp4(u32x4 w, u32x4 x, f32x4 c, uint32_t ws
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, 4, 4, WB, int(ws), XB, int(xs));
 }
 
+// Rows of 128 bytes in LDS: piece c (16 bytes) of row r at place
+// c ^ swizzle8(r).  A 128-bit read serves 16 lanes at a time: rows 0-3 and
+// 12-15 of one quad with rows 4-11 of the quad beside, whose pieces differ in
+// one of the low two bits; each half gets half of the places, and two rows
+// fill the banks once (no conflicts counted).
+__device__ __forceinline__ uint32_t swizzle8(uint32_t r) {
+    return ((r >> 1) & 3u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
+}
+
+// Waits until at most N of this wave's loads are in flight and its LDS reads
+// are done, then for the other waves of the workgroup.
+template <uint32_t N>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes a lane from memory straight to LDS: lane i's at lds + 16 i (`lds`
+// the same in every lane).
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t lane_off, uint32_t off) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_off, off, 0, 0);
+#endif
+}
+
+// Makes the compiler have `v` in its register here: products whose sums are
+// held stay in front of the branches and barriers that follow.
+__device__ __forceinline__ void held(f32x4& v) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+v"(v));
+#endif
+}
+
 // Row and column tile of a workgroup.  The eight compute dies take workgroups
 // in turn: each gets a run of tiles, walked four row tiles at a time, so that
 // its L2 serves a block of both operands.

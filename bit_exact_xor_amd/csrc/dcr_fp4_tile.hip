@@ -1,4 +1,13 @@
 // dcr_fp4_tile.hip -- bf16 rows times 4-bit weights in large tiles (gfx950).
+//
+// Bound by the matrix unit, with the conversion of the codes next to it: an
+// MX code pair is one instruction, an NV one four.  So a wave takes all the
+// tile's rows of x and columns of its own: every code is converted once a
+// tile, in the wave that multiplies with it, and never sees LDS.  x goes
+// there by direct loads and is read by every wave (a quarter of what LDS
+// gives).  Against 2 x 4 waves of 128 x 64, which convert twice, 8 waves of
+// 256 x 32 take 8192 x 14336 x 4096 from 670 to 658 us (MX) and from 778 to
+// 712 us (NV).
 #include "dcr_fp4_mm.h"
 
 namespace dcr {
@@ -23,13 +32,12 @@ __device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_
     return u32x4{a[0], a[1], b[0], b[1]};
 }
 
-template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool W2, bool ALIGNED>
-__global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
-    constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16, DMA = BM / 4 / W;
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t W, bool ALIGNED>
+__global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
+    constexpr uint32_t MI = BM / 16, NI = BN / W / 16, DMA = BM / 4 / W;
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[BM * kRowB], buf1[BM * kRowB];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
-    const uint32_t wm = wave % WM, wn = wave / WM;
 
     const TilePlace at = tile_place(a, blockIdx.x);
     const RowTile rt = row_tile<BM>(a, at.row);
@@ -37,7 +45,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN;
 
     const uint8_t* xb = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2;
-    const uint32_t xrow0 = wave * 4 + quad, xstep = uint32_t(a.x_stride) * 2;
+    const uint32_t xstep = uint32_t(a.x_stride) * 2;
+    uint32_t xo[DMA];
+#pragma unroll
+    for (uint32_t i = 0; i < DMA; ++i) {
+        const uint32_t r = (i * W + wave) * 4 + quad;
+        xo[i] = min(r, rows - 1) * xstep + (r16 ^ swizzle(r)) * 16;
+    }
     // w: lane (r16, quad) holds row r16 of a subtile, elements [32 quad, +32)
     // of a step: one MX block
     const uint8_t* wb = a.wc + (uint64_t(rt.group) * a.n + n0) * a.wc_stride;
@@ -45,7 +59,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     uint32_t wo[NI], so[NI];
 #pragma unroll
     for (uint32_t i = 0; i < NI; ++i) {
-        const uint32_t r = min(wn * (BN / WN) + i * 16 + r16, a.n - 1 - n0);
+        const uint32_t r = min(wave * (BN / W) + i * 16 + r16, a.n - 1 - n0);
         wo[i] = r * uint32_t(a.wc_stride) + quad * 16;
         so[i] = r * uint32_t(a.ws_stride) + quad * (WF == DCR_FP4_MX ? 1 : 2);
     }
@@ -59,34 +73,37 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     f32x4 acc[NI][MI] = {};
     u32x4 wq[NI];
     uint32_t wsc[NI];
-    bf16x8 w[W2 ? 2 : 1][NI];
+    bf16x8 w[2][NI];
 
     const uint32_t steps = (a.k + kBK - 1) / kBK;
 
-    // A step of aligned rows.  Lanes past the end of the sum (a multiple of 32)
-    // read behind the descriptors' range, which gives zeros.
+    // Loads of a step of aligned rows.  From the step on in which the sum ends
+    // (at a multiple of 32), lanes past the end read behind the descriptors'
+    // range, which gives zeros; a lane once past it stays there, so its offset
+    // is changed for good and the other steps spend nothing on it.
+    auto past_end = [&](uint32_t step) {
+        if ((step + 1) * kBK <= a.k) return;
+        const uint32_t xout = step * kBK + (r16 ^ swizzle(wave * 4 + quad)) * 8 < a.k ? 0u : kOutside;
+        const uint32_t wout = step * kBK + quad * 32 < a.k ? 0u : kOutside;
+#pragma unroll
+        for (uint32_t i = 0; i < DMA; ++i) xo[i] |= xout;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) wo[i] |= wout, so[i] |= wout;
+    };
     auto load_w = [&](uint32_t step) {
-        const uint32_t wk = step * (kBK / 2), sk = step * (kBK / fp4_block(WF));
-        const uint32_t out = step * kBK + quad * 32 < a.k ? 0u : kOutside;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
-            wq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i] | out, wk, 0));
+            wq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], step * (kBK / 2), 0));
             if (WF == DCR_FP4_MX)
-                wsc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i] | out, sk, 0);
+                wsc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], step * (kBK / 32), 0);
             else
-                wsc[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i] | out, sk, 0);
+                wsc[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], step * (kBK / 16), 0);
         }
     };
     auto load_x = [&](uint8_t* buf, uint32_t step) {
-        uint32_t r0 = xrow0;
-        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
 #pragma unroll
-        for (uint32_t i = 0; i < DMA; ++i) {
-            const uint32_t r = r0 + i * W * 4, c = r16 ^ swizzle(r);
-            const uint32_t off = __umul24(min(r, rows - 1), xstep) + c * 16;
-            const uint32_t out = step * kBK + c * 8 < a.k ? 0u : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16, off | out, step * kRowB, 0, 0);
-        }
+        for (uint32_t i = 0; i < DMA; ++i)
+            load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
     };
     // any step, any alignment: x through registers, zeros past the row's end
     auto load_any = [&](uint8_t* buf, uint32_t step) {
@@ -119,16 +136,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     };
     auto convert = [&](uint32_t j, uint32_t i) {
-        w[W2 ? j & 1 : 0][i] =
+        w[j & 1][i] =
             fp4_unpack8_bf16<WF>(wq[i][j], WF == DCR_FP4_MX ? wsc[i] : (wsc[i] >> (j / 2 * 8)) & 255u);
     };
-    // A step's products, two row subtiles at a time.  While these multiply,
-    // the next two are read from LDS (and, with registers for it, part of the
-    // next quarter's codes converted).  The codes' registers are free once the
+    // A step's products, four row subtiles at a time.  While these multiply,
+    // the next four are read from LDS and part of the
+    // next quarter's codes is converted.  The codes' registers are free once the
     // last quarter is converted, and take the next step's then.
     auto compute = [&](const uint8_t* buf, uint32_t next) {
-        constexpr uint32_t H = 2, P = MI / H, C = NI / P;
-        const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
+        constexpr uint32_t H = 4, P = MI / H;
+        static_assert(P % NI == 0, "a subtile's codes are converted every P / NI phases");
+        const uint8_t* xl = buf + r16 * kRowB;
         bf16x8 x[2][H];
         auto read = [&](uint32_t ph) {
 #pragma unroll
@@ -141,25 +159,29 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         for (uint32_t ph = 0; ph < 4 * P; ++ph) {
             const uint32_t j = ph / P;
             if (ph + 1 < 4 * P) read(ph + 1);
-            if (!W2 ? ph % P == 0 : ph == 0)
+            if (ph == 0)
 #pragma unroll
-                for (uint32_t i = 0; i < NI; ++i) convert(j, i);
-            if (W2 && j < 3)
-#pragma unroll
-                for (uint32_t i = 0; i < C; ++i) convert(j + 1, (ph % P) * C + i);
+                for (uint32_t i = 0; i < NI; ++i) convert(0, i);
             if (ALIGNED && ph == 3 * P) load_w(next);
+            if (j < 3 && ph % P % (P / NI) == 0) convert(j + 1, ph % P / (P / NI));
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i)
                     acc[i][(ph % P) * H + m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        w[W2 ? j & 1 : 0][i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
+                        w[j & 1][i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (uint32_t m = 0; m < MI; ++m)
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
+
 
     if constexpr (ALIGNED) {
         if (steps) {
+            past_end(0);
             load_x(buf0, 0);
             load_w(0);
         }
@@ -167,9 +189,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         // a step past the last is all zeros
         for (uint32_t t = 0; t < steps; t += 2) {
             __syncthreads();
+            past_end(t + 1);
             load_x(buf1, t + 1);
             compute(buf0, t + 1);
             __syncthreads();
+            past_end(t + 2);
             load_x(buf0, t + 2);
             compute(buf1, t + 2);
         }
@@ -185,16 +209,16 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 
     __syncthreads();
     constexpr uint32_t LB = BM * kRowB / W;   // one buffer: the variant for any alignment has no second
-    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
-                                n0 + wn * (BN / WN), a.n, buf0 + wave * LB);
+    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, 0,
+                                n0 + wave * (BN / W), a.n, buf0 + wave * LB);
 }
 
 template <uint32_t WF, typename OUT, bool ALIGNED>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 2, 4, WF == DCR_FP4_MX, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 2, 2, true, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {

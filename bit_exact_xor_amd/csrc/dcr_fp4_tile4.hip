@@ -12,14 +12,6 @@ namespace {
 constexpr uint32_t kBK = 256;                // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
 
-// Codes in LDS: a row is 8 pieces of 16 bytes, piece c of row r at place
-// c ^ swizzle(r).  A 128-bit read serves 16 lanes at a time: rows 0-3 and
-// 12-15 of one quad with rows 4-11 of the quad beside, whose pieces differ in
-// bit 0; two rows fill the banks once.
-__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
-    return ((r >> 1) & 1u) | ((r >> 1) & 2u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
-}
-
 template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool SV>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) {
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
@@ -55,25 +47,28 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     f32x4 acc[NI][MI] = {};
     const uint32_t steps = (a.k + kBK - 1) / kBK;
 
-    // codes of a step by loads straight to LDS; pieces past the sum's end read
-    // behind the descriptors' range, which gives zeros
+    // Codes of a step by loads straight to LDS.  From the step on in which the
+    // sum ends (at a whole block) lanes past the end read behind the
+    // descriptors' range, which gives zeros; a lane once past it stays there,
+    // so its offset is changed for good and the other steps spend nothing on it.
+    const uint32_t lr = wave * 8 + (lane >> 3), lc = (lane & 7u) ^ swizzle8(lr);
+    uint32_t xo[XD], wo[WD];
+#pragma unroll
+    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(lr + i * W * 8, rows - 1) * xstep + lc * 16;
+#pragma unroll
+    for (uint32_t i = 0; i < WD; ++i) wo[i] = min(lr + i * W * 8, cols - 1) * wstep + lc * 16;
     auto load = [&](uint8_t* buf, uint32_t step) {
-        uint32_t r0 = wave * 8 + (lane >> 3);
-        asm volatile("" : "+v"(r0));   // the rows' offsets are cheaper made again than held
+        if ((step + 1) * kBK > a.k) {
+            const uint32_t out = step * kBK + lc * 32 < a.k ? 0u : kOutside;
 #pragma unroll
-        for (uint32_t i = 0; i < XD; ++i) {
-            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
-            const uint32_t out = step * kBK + c * 32 < a.k ? 0u : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(buf + (i * W + wave) * 1024), 16,
-                                                     (__umul24(min(r, rows - 1), xstep) + c * 16) | out, step * kRowB, 0, 0);
+            for (uint32_t i = 0; i < XD; ++i) xo[i] |= out;
+#pragma unroll
+            for (uint32_t i = 0; i < WD; ++i) wo[i] |= out;
         }
 #pragma unroll
-        for (uint32_t i = 0; i < WD; ++i) {
-            const uint32_t r = r0 + i * W * 8, c = (lane & 7u) ^ swizzle(r & 15u);
-            const uint32_t out = step * kBK + c * 32 < a.k ? 0u : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void*)(buf + BM * kRowB + (i * W + wave) * 1024), 16,
-                                                     (__umul24(min(r, cols - 1), wstep) + c * 16) | out, step * kRowB, 0, 0);
-        }
+        for (uint32_t i = 0; i < XD; ++i) load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
+#pragma unroll
+        for (uint32_t i = 0; i < WD; ++i) load_lds16(wr, buf + BM * kRowB + (i * W + wave) * 1024, wo[i], step * kRowB);
     };
     // the eight scale bytes of a step of this thread's row; zeros past the end
     auto load_scales = [&](uint32_t step) -> u32x2 {
@@ -105,7 +100,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
                 x[ph & 1][m] = *reinterpret_cast<const u32x4*>(xl + ((ph % P) * H + m) * 16 * kRowB +
-                                                               (((ph / P * 4 + quad) ^ swizzle(r16)) * 16));
+                                                               (((ph / P * 4 + quad) ^ swizzle8(r16)) * 16));
         };
         read(0);
 #pragma unroll
@@ -120,7 +115,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
                 for (uint32_t i = 0; i < NI / 4; ++i) ws[i] = *reinterpret_cast<const uint32_t*>(t + i * 4);
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i)
-                    w[i] = *reinterpret_cast<const u32x4*>(wl + i * 16 * kRowB + (((j * 4 + quad) ^ swizzle(r16)) * 16));
+                    w[i] = *reinterpret_cast<const u32x4*>(wl + i * 16 * kRowB + (((j * 4 + quad) ^ swizzle8(r16)) * 16));
             }
             if (ph + 1 < 2 * P) read(ph + 1);
             // byte of a subtile in its scale word: the subtile's index mod 4
@@ -133,6 +128,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
             static_for<H>([&](auto m) { static_for<NI>([&](auto i) { mul(m, i); }); });
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (uint32_t m = 0; m < MI; ++m)
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
     if (steps) {
