@@ -439,46 +439,47 @@ def fp4_workspace(device="cuda"):
     return torch.empty(FP4_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
-def _one_device(*tensors):
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError("4-bit calls take tensors in GPU memory")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+def _one_device(first, *others):
+    """Index of the GPU that all of the tensors (None: left out) are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("4-bit calls take tensors in GPU memory")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return dev
 
 
 def _wide(t, rows, cols, name):
     """(pointer, type, row stride) of a BF16 or fp32 matrix."""
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         ty = BF16
-    elif t.dtype == torch.float32:
+    elif t.dtype is torch.float32:
         ty = F32
     else:
         raise ValueError(f"{name}: bfloat16 or float32 expected, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols or \
-            (cols > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or shape[1] != cols or \
+            (cols > 1 and strides[1] != 1):
         raise ValueError(f"{name}: [{'m' if rows is None else rows}, {cols}] with contiguous rows expected, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
-    if t.shape[0] > 1 and t.stride(0) < cols:
+                         f"got {tuple(shape)} with strides {strides}")
+    if shape[0] > 1 and strides[0] < cols:
         raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), ty, t.stride(0)
+    return t.data_ptr(), ty, strides[0]
 
 
 def _fp4_call(fn, what, device, stream, *args):
-    """Call `fn` with the device of its tensors current, on `stream` or that
-    device's current stream."""
+    """Call `fn` with GPU `device`, the one of its tensors, current, on
+    `stream` or that GPU's current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _stream(stream))
+    # (torch.cuda.current_stream() costs as much as the rest of a small call)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
+            rc = fn(*args, raw)
     if rc:
         _check(rc, what)
 
@@ -488,8 +489,8 @@ def dcr_fp4_quantize(x, q: Fp4Tensor, options=0, workspace=None, stream=None) ->
     FP4_CALIBRATE (NV) first takes q's tensor scale from x, and needs a
     workspace."""
     p, ty, stride = _wide(x, q.rows, q.cols, "x")
-    _one_device(x, q.codes, workspace)
-    _fp4_call(load_library().dcr_fp4_quantize, "dcr_fp4_quantize", q.device, stream, p, ty, stride, q._ref, options,
+    dev = _one_device(x, q.codes, workspace)
+    _fp4_call(load_library().dcr_fp4_quantize, "dcr_fp4_quantize", dev, stream, p, ty, stride, q._ref, options,
               workspace.data_ptr() if workspace is not None else None,
               _nbytes(workspace) if workspace is not None else 0)
 
@@ -497,15 +498,15 @@ def dcr_fp4_quantize(x, q: Fp4Tensor, options=0, workspace=None, stream=None) ->
 def dcr_fp4_dequantize(q: Fp4Tensor, y, stream=None) -> None:
     """Enqueue reading q back into y (BF16 or fp32, [rows, cols])."""
     p, ty, stride = _wide(y, q.rows, q.cols, "y")
-    _one_device(y, q.codes)
-    _fp4_call(load_library().dcr_fp4_dequantize, "dcr_fp4_dequantize", q.device, stream, q._ref, p, ty, stride)
+    dev = _one_device(y, q.codes)
+    _fp4_call(load_library().dcr_fp4_dequantize, "dcr_fp4_dequantize", dev, stream, q._ref, p, ty, stride)
 
 
 def _groups(w, offsets):
     """(offsets pointer, groups, rows of a group) of a product with w."""
-    import torch
     if offsets is None:
         return None, 1, w.rows
+    import torch
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
         raise ValueError("offsets: contiguous int32 [groups + 1] expected")
     g = offsets.numel() - 1
@@ -514,16 +515,22 @@ def _groups(w, offsets):
     return offsets.data_ptr(), g, w.rows // g
 
 
-def _product(fn, what, x, w, y, offsets, workspace, stream, x_cols, y_cols):
+def _product(fn, what, x, w, y, offsets, workspace, stream, grad):
     import torch
-    off, g, _n = _groups(w, offsets)
-    if x.dtype != torch.bfloat16:
+    if workspace is None:
+        raise ValueError("workspace: pass one made by fp4_workspace()")
+    off, g, n = _groups(w, offsets)
+    yp, ty, ys = _wide(y, x.rows if isinstance(x, Fp4Tensor) else x.shape[0], w.cols if grad else n, "dx" if grad else "y")
+    tail = (w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if isinstance(x, Fp4Tensor):
+        dev = _one_device(w.codes, x.codes, y, offsets, workspace)
+        _fp4_call(fn, what, dev, stream, x._ref, *tail)
+        return
+    if x.dtype is not torch.bfloat16:
         raise ValueError(f"{what}: bfloat16 rows expected, got {x.dtype}")
-    xp, _ty, xs = _wide(x, None, x_cols, "x")
-    yp, ty, ys = _wide(y, x.shape[0], y_cols, "y")
-    _one_device(x, w.codes, y, offsets, workspace)
-    _fp4_call(fn, what, w.device, stream, xp, x.shape[0], xs, w._ref, off, g, yp, ty, ys, workspace.data_ptr(),
-              _nbytes(workspace))
+    xp, _ty, xs = _wide(x, None, n if grad else w.cols, "dy" if grad else "x")
+    dev = _one_device(w.codes, x, y, offsets, workspace)
+    _fp4_call(fn, what, dev, stream, xp, x.shape[0], xs, *tail)
 
 
 def dcr_fp4_matmul(x, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:
@@ -531,32 +538,21 @@ def dcr_fp4_matmul(x, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None
     fp32 [m, n].  With `offsets` (int32 [groups + 1], device) w holds `groups`
     weights stacked along its rows and rows offsets[g] .. offsets[g + 1] of x
     take weight g; the other rows of y are left as they are."""
-    _product(load_library().dcr_fp4_matmul, "dcr_fp4_matmul", x, w, y, offsets, _need(workspace, w), stream, w.cols,
-             _groups(w, offsets)[2])
+    _product(load_library().dcr_fp4_matmul, "dcr_fp4_matmul", x, w, y, offsets, workspace, stream, False)
 
 
 def dcr_fp4_matmul_q(x: Fp4Tensor, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:
     """Enqueue y = x w^T with both operands in 4 bits (FP4_MX); else as
     dcr_fp4_matmul."""
-    off, g, n = _groups(w, offsets)
-    ws = _need(workspace, w)
-    yp, ty, ys = _wide(y, x.rows, n, "y")
-    _one_device(x.codes, w.codes, y, offsets, ws)
-    _fp4_call(load_library().dcr_fp4_matmul_q, "dcr_fp4_matmul_q", w.device, stream, x._ref, w._ref, off, g, yp, ty,
-              ys, ws.data_ptr(), _nbytes(ws))
+    if not isinstance(x, Fp4Tensor):
+        raise ValueError("x: an Fp4Tensor expected")
+    _product(load_library().dcr_fp4_matmul_q, "dcr_fp4_matmul_q", x, w, y, offsets, workspace, stream, False)
 
 
 def dcr_fp4_matmul_grad(dy, w: Fp4Tensor, dx, offsets=None, workspace=None, stream=None) -> None:
     """Enqueue dx = dy w, the gradient of dcr_fp4_matmul with respect to x:
     dy BF16 [m, n], dx BF16 or fp32 [m, cols]."""
-    _product(load_library().dcr_fp4_matmul_grad, "dcr_fp4_matmul_grad", dy, w, dx, offsets, _need(workspace, w),
-             stream, _groups(w, offsets)[2], w.cols)
-
-
-def _need(workspace, w):
-    if workspace is None:
-        raise ValueError("workspace: pass one made by fp4_workspace()")
-    return workspace
+    _product(load_library().dcr_fp4_matmul_grad, "dcr_fp4_matmul_grad", dy, w, dx, offsets, workspace, stream, True)
 
 
 def dcr_set_kernel_events(start=None, stop=None) -> None:
