@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
-    const TilePlace at = tile_place(a, blockIdx.x);
+    const TilePlace at = tile_place(a);
     const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), o0 = at.col * BO;
@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     u32x2 q[PP];
     uint32_t sc[PP];
     f32x4 acc[NI][MI] = {};
-    const uint32_t steps = (a.n + kBJ - 1) / kBJ;
+    // this workgroup's steps: from `first` on, up to `steps`
+    const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.n + kBJ - 1) / kBJ);
 
     // dy by loads straight to LDS.  From the step on in which the sum ends (at a
     // multiple of 8) lanes past the end read behind the descriptor's range,
@@ -141,15 +142,15 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    if (steps) {
-        load_x(buf0, 0);
-        load_w(0);
+    if (first < steps) {
+        load_x(buf0, first);
+        load_w(first);
         convert(buf0);
-        load_w(1);
+        load_w(first + 1);
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
-    for (uint32_t t = 0; t < steps; t += 2) {
+    for (uint32_t t = first; t < steps; t += 2) {
         __syncthreads();
         load_x(buf1, t + 1);
         convert(buf1);
@@ -161,34 +162,39 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         load_w(t + 3);
         compute(buf1);
     }
-    __syncthreads();
-    constexpr uint32_t LB = (kX + kW) * 2 / W;
-    uint8_t* mine = wave < W / 2 ? buf0 + wave * LB : buf1 + (wave - W / 2) * LB;
-    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, wm * (BM / WM),
-                                o0 + wn * (BO / WN), a.k, mine);
+    store_block<OUT, BM, BO, W, WM, kX + kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
+                                             wn * (BO / WN), a.k, buf0, buf1);
 }
 
 template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
+    const dim3 g(a.row_tiles * a.col_tiles * a.splits);
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4>), g, dim3(512), 0, st, a);
+    else if (bm == 128)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2>), g, dim3(256), 0, st, a);
+    else if (bm == 64)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 64, 128, 1, 4>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4>), g, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
+bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
+    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600};
     // pieces of dy are eight elements, offsets inside a tile 31 bits
     if (!a.x_vec || !a.w_vec || a.n % 8 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24))
         return false;
-    uint32_t grid = 0;
-    const uint32_t bm = tile_grid(&a, a.k, &grid);
+    const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, kCost);
     if (!bm) return false;
+    const MArgs p = fp4_mm_parts(a, a.k, ws);
+    const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        f32 ? launch<DCR_FP4_MX, float>(a, st, bm, grid) : launch<DCR_FP4_MX, uint16_t>(a, st, bm, grid);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm) : launch<DCR_FP4_MX, uint16_t>(p, st, bm);
     else
-        f32 ? launch<DCR_FP4_NV, float>(a, st, bm, grid) : launch<DCR_FP4_NV, uint16_t>(a, st, bm, grid);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm) : launch<DCR_FP4_NV, uint16_t>(p, st, bm);
+    fp4_mm_join(a, a.k, fmt, f32, ws, st);
     return true;
 }
 

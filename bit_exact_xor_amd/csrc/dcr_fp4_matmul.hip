@@ -6,6 +6,8 @@
 // A 4-bit value times its block's scale has at most six significant bits, so
 // it is exact as bf16 and the matrix instructions take it as an operand with
 // no loss; the tensor scale of the NV format multiplies the finished sum.
+#include <algorithm>
+
 #include "dcr_fp4_mm.h"
 
 namespace dcr {
@@ -113,6 +115,30 @@ __global__ void __launch_bounds__(256) fp4_mm_general_kernel(MArgs a) {
     }
 }
 
+// ------------------------------------------------------------ joined parts
+//
+// Parts of a sum in fp32, [split][row][column]: added in order, four results a
+// thread, times the tensor scale, rounded once.
+template <uint32_t WF, typename OUT>
+__global__ void __launch_bounds__(256) fp4_mm_join_kernel(MArgs a, const float* part, uint32_t outs, uint32_t stride) {
+    const uint32_t quads = stride / 4, id = blockIdx.x * 256 + threadIdx.x;
+    const uint32_t row = id / quads, c = (id - row * quads) * 4;
+    if (row >= a.m) return;
+    if (a.offsets && (int64_t(row) < int64_t(a.offsets[0]) || int64_t(row) >= int64_t(a.offsets[a.groups]))) return;
+    const float* p = part + uint64_t(row) * stride + c;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    for (uint32_t i = 1; i < a.splits; ++i) v += *reinterpret_cast<const f32x4*>(p + i * a.split_elems);
+    if (WF == DCR_FP4_NV) v *= *a.tensor_scale;
+    OUT* out = static_cast<OUT*>(a.y) + uint64_t(row) * a.y_stride + c;
+    if (a.y_vec && c + 4 <= outs) {
+        store4(out, v);
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (c + e < outs) store_out(out + e, v[e]);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 
 constexpr uint32_t kMaxGrid = 1u << 20;   // workgroups of the general kernel; more tiles are walked
@@ -186,9 +212,9 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     const bool f32 = y_type == DCR_F32, mx = w->format == DCR_FP4_MX;
     a.y_vec = al16(y) && (a.y_stride * (f32 ? 4 : 2)) % 16 == 0;
     if (!grad && fp4_mm_rows(a, xq != nullptr, w->format, f32, st)) return fp4_launched();
-    if (!xq && !grad && m > 64 && fp4_mm_tile(a, w->format, f32, st)) return fp4_launched();
-    if (xq && m > 64 && fp4_mm_tile4(a, f32, st)) return fp4_launched();
-    if (grad && n && m > 32 && fp4_mm_grad(a, w->format, f32, st)) return fp4_launched();
+    if (!xq && !grad && fp4_mm_tile(a, w->format, f32, ws, st)) return fp4_launched();
+    if (xq && fp4_mm_tile4(a, f32, ws, st)) return fp4_launched();
+    if (grad && n && fp4_mm_grad(a, w->format, f32, ws, st)) return fp4_launched();
     // tiles of a grouped product: at most one short one for each group
     a.row_tiles = uint32_t((m + kGT - 1) / kGT + (offsets ? n_groups : 0));
     a.col_tiles = uint32_t((outs + kGT - 1) / kGT);
@@ -206,6 +232,64 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
 }
 
 }  // namespace
+
+uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]) {
+    // Time of a candidate: rounds of workgroups over 256 compute units, each
+    // its steps and a fixed start and end; for parts of the sum the launch
+    // that joins them and its traffic, at the cycles they measure.
+    constexpr uint64_t kBlock = 6000, kJoin = 5000, kJoinBytes = 2500;
+    const uint64_t stride = (uint64_t(outs) + 3) & ~uint64_t(3), pairs = (uint64_t(steps) + 1) / 2;
+    uint64_t best = UINT64_MAX;
+    uint32_t bm = 0;
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t b = 256u >> i, bn = b == 256 ? 256 : 128;
+        const uint64_t cols = (uint64_t(outs) + bn - 1) / bn, bound = (a->m + b - 1) / b + (a->offsets ? a->groups : 0);
+        // row tiles to expect: groups end inside a tile
+        const uint64_t rows = (a->m + b - 1) / b + (a->offsets ? std::min<uint64_t>(a->groups, a->m) / 2 : 0);
+        for (uint32_t s = 1; s <= 16; ++s) {
+            if (s > 1 && (pairs / s < 2 || s * a->m * stride * 4 > DCR_FP4_WORKSPACE_BYTES)) break;
+            if (bound * cols * s >= (1u << 22)) break;
+            const uint64_t each = 2 * ((pairs + s - 1) / s);
+            const uint64_t rounds = (rows * cols * s + 255) / 256;
+            const uint64_t t = rounds * (each * cost[i] + kBlock) + (s > 1 ? kJoin + s * a->m * stride * 8 / kJoinBytes : 0);
+            if (t >= best) continue;
+            best = t;
+            bm = b;
+            a->row_tiles = uint32_t(bound);
+            a->col_tiles = uint32_t(cols);
+            a->splits = s;
+            a->split_steps = uint32_t(each);
+        }
+    }
+    a->split_elems = a->splits > 1 ? a->m * stride : 0;
+    return bm;
+}
+
+MArgs fp4_mm_parts(const MArgs& a, uint32_t outs, void* ws) {
+    MArgs p = a;
+    if (a.splits > 1) {
+        p.y = ws;
+        p.y_stride = (uint64_t(outs) + 3) & ~uint64_t(3);
+        p.y_vec = 1;
+    }
+    return p;
+}
+
+void fp4_mm_join(const MArgs& a, uint32_t outs, uint32_t fmt, bool f32, const void* ws, hipStream_t st) {
+    if (a.splits <= 1) return;
+    const uint32_t stride = (outs + 3) & ~3u, grid = uint32_t((a.m * (stride / 4) + 255) / 256);
+    const float* part = static_cast<const float*>(ws);
+    const bool mx = fmt == DCR_FP4_MX;
+    if (f32 && mx)
+        hipLaunchKernelGGL((fp4_mm_join_kernel<DCR_FP4_MX, float>), dim3(grid), dim3(256), 0, st, a, part, outs, stride);
+    else if (f32)
+        hipLaunchKernelGGL((fp4_mm_join_kernel<DCR_FP4_NV, float>), dim3(grid), dim3(256), 0, st, a, part, outs, stride);
+    else if (mx)
+        hipLaunchKernelGGL((fp4_mm_join_kernel<DCR_FP4_MX, uint16_t>), dim3(grid), dim3(256), 0, st, a, part, outs, stride);
+    else
+        hipLaunchKernelGGL((fp4_mm_join_kernel<DCR_FP4_NV, uint16_t>), dim3(grid), dim3(256), 0, st, a, part, outs, stride);
+}
+
 }  // namespace dcr
 
 extern "C" {

@@ -23,6 +23,8 @@ struct MArgs {
     uint32_t x_vec, w_vec;      // rows of x / codes of w start on 16-byte borders
     uint32_t y_vec;             // rows of y start on 16-byte borders
     uint32_t row_tiles, col_tiles;   // upper bounds of the grid
+    uint32_t splits, split_steps;    // parts of the sum, steps of a part (even)
+    uint64_t split_elems;            // results of a part (y is then fp32 scratch)
 };
 
 struct RowTile {
@@ -148,19 +150,21 @@ __device__ __forceinline__ void held(f32x4& v) {
 #endif
 }
 
-// Row and column tile of a workgroup.  The eight compute dies take workgroups
-// in turn: each gets a run of tiles, walked four row tiles at a time, so that
-// its L2 serves a block of both operands.
+// Row and column tile of a workgroup, and its steps of the sum.  The eight
+// compute dies take workgroups in turn: each gets a run of tiles, walked four
+// row tiles at a time, so that its L2 serves a block of both operands.
 struct TilePlace {
-    uint32_t row, col, id;
+    uint32_t row, col, split;
 };
-__device__ __forceinline__ TilePlace tile_place(const MArgs& a, uint32_t id) {
-    const uint32_t per = a.row_tiles * a.col_tiles / 8;
+__device__ __forceinline__ TilePlace tile_place(const MArgs& a) {
+    uint32_t id = blockIdx.x;
+    const uint32_t all = a.row_tiles * a.col_tiles * a.splits, per = all / 8;
     if (id < per * 8) id = (id & 7u) * per + (id >> 3);
+    const uint32_t tile = id / a.splits, split = id - tile * a.splits;
     constexpr uint32_t SM = 4;
-    const uint32_t strip = id / (SM * a.col_tiles), in = id - strip * SM * a.col_tiles;
+    const uint32_t strip = tile / (SM * a.col_tiles), in = tile - strip * SM * a.col_tiles;
     const uint32_t sm = min(SM, a.row_tiles - strip * SM);
-    return {strip * SM + in % sm, in / sm, id};
+    return {strip * SM + in % sm, in / sm, split};
 }
 
 // loop over compile-time indices
@@ -172,42 +176,52 @@ __device__ __forceinline__ void static_for(F&& f) {
     }
 }
 
-// The sums of a wave, times s, rounded once.  A lane holds four neighbouring
-// results of one row in each 16 x 16 subtile: written as they are they make
-// 32-byte pieces of lines, which costs as much time as the product itself.
-// They go through LDS (`lds`: LB bytes of this wave alone) and leave as whole
-// rows of the wave's tile, 128 or 256 bytes each.  16-byte pieces of a row sit
+// A workgroup's BM x BN sums, times s, rounded once.  A lane holds four
+// neighbouring results of one row in each 16 x 16 subtile: stored as they are
+// they make 32-byte pieces of lines, which cost as much time as the product
+// itself (205 of 457 us at 8192 x 14336 x 4096 in 4 bits).  They go through
+// LDS, half of a pass's rows in `lo` and half in `hi` (HB bytes each, unused
+// by then), and leave as whole rows of the tile.  16-byte pieces of a row sit
 // at place p ^ row, which spreads both directions over the banks.
-template <typename OUT, uint32_t MI, uint32_t NI, uint32_t LB>
-__device__ __forceinline__ void store_tile(const MArgs& a, const f32x4 (&acc)[NI][MI], float s, const RowTile& rt,
-                                           uint32_t rows, uint32_t row0, uint32_t col0, uint32_t outs, uint8_t* lds) {
-    constexpr uint32_t E = 16 / sizeof(OUT), PR = NI * 16 / E, RB = PR * 16;     // elements of a piece, pieces, bytes of a row
-    constexpr uint32_t MP = LB / RB / 16 < MI ? LB / RB / 16 : MI, RI = 64 / PR; // row subtiles of a pass, rows of a store
-    static_assert(MP && MI % MP == 0 && 64 % PR == 0, "store_tile");
+// WM waves share the rows, `wm` this one's part; its columns start at `wcol`.
+template <typename OUT, uint32_t BM, uint32_t BN, uint32_t W, uint32_t WM, uint32_t HB, uint32_t MI, uint32_t NI>
+__device__ __forceinline__ void store_block(const MArgs& a, const f32x4 (&acc)[NI][MI], float s, const RowTile& rt,
+                                            const TilePlace& at, uint32_t wm, uint32_t wcol, uint32_t outs, uint8_t* lo,
+                                            uint8_t* hi) {
+    constexpr uint32_t E = 16 / sizeof(OUT), RB = BN * sizeof(OUT), PR = RB / 16;   // elements of a piece; bytes, pieces of a row
+    constexpr uint32_t HR = HB / RB < BM / 2 ? HB / RB : BM / 2, RP = 2 * HR;       // rows of a half, of a pass
+    constexpr uint32_t RPW = RP / WM, RI = W * 64 / PR;                             // rows of a wave in a pass; of a store
+    static_assert(HR % 16 == 0 && BM % RP == 0 && HR % RI == 0 && (WM == 1 || RPW == HR), "store_block");
     const uint32_t lane = threadIdx.x & 63u, r16 = lane & 15u, quad = lane >> 4;
-    const uint32_t piece = lane % PR, col = col0 + piece * E;
+    const uint32_t rows = uint32_t(rt.end - rt.begin), piece = threadIdx.x % PR, row_in = threadIdx.x / PR;
+    const uint32_t col = at.col * BN + piece * E;
+    OUT* y = static_cast<OUT*>(a.y) + at.split * a.split_elems;
 #pragma unroll
-    for (uint32_t p = 0; p < MI / MP; ++p) {
+    for (uint32_t p = 0; p < BM / RP; ++p) {
+        __syncthreads();
 #pragma unroll
-        for (uint32_t m = 0; m < MP; ++m)
+        for (uint32_t m = 0; m < RPW / 16; ++m) {
+            const bool up = WM == 1 ? m * 16 >= HR : wm != 0;
+            uint8_t* row = (up ? hi : lo) + ((WM == 1 && up ? m * 16 - HR : m * 16) + r16) * RB;
 #pragma unroll
             for (uint32_t i = 0; i < NI; ++i) {
-                const f32x4 v = acc[i][p * MP + m] * s;
-                uint8_t* row = lds + (m * 16 + r16) * RB;
+                const f32x4 v = acc[i][p * (RPW / 16) + m] * s;
+                const uint32_t c = wcol + i * 16 + quad * 4;
                 if constexpr (sizeof(OUT) == 4)
-                    store4(reinterpret_cast<float*>(row + ((i * 4 + quad) ^ (r16 & (PR - 1))) * 16), v);
+                    store4(reinterpret_cast<float*>(row + ((c / 4) ^ r16) * 16), v);
                 else
-                    store4(reinterpret_cast<uint16_t*>(row + ((i * 2 + quad / 2) ^ (r16 & (PR - 1))) * 16 + (quad & 1u) * 8), v);
+                    store4(reinterpret_cast<uint16_t*>(row + ((c / 8) ^ r16) * 16 + (quad & 1u) * 8), v);
             }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+        __syncthreads();
 #pragma unroll
-        for (uint32_t i = 0; i < MP * 16 / RI; ++i) {
-            const uint32_t lr = i * RI + lane / PR, r = row0 + p * MP * 16 + lr;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(lds + lr * RB + (piece ^ (lr & (PR - 1))) * 16);
+        for (uint32_t i = 0; i < RP / RI; ++i) {
+            const bool up = i * RI >= HR;
+            const uint32_t lr = (up ? i * RI - HR : i * RI) + row_in;      // in its half
+            const u32x4 v = *reinterpret_cast<const u32x4*>((up ? hi : lo) + lr * RB + (piece ^ (lr & 15u)) * 16);
+            const uint32_t r = WM == 1 ? p * RP + i * RI + row_in : (up ? BM / 2 : 0) + p * RPW + lr;
             if (r >= rows) continue;
-            OUT* out = static_cast<OUT*>(a.y) + (rt.begin + r) * a.y_stride + col;
+            OUT* out = y + (rt.begin + r) * a.y_stride + col;
             if (a.y_vec && col + E <= outs) {
                 *reinterpret_cast<u32x4*>(out) = v;
             } else {
@@ -221,32 +235,20 @@ __device__ __forceinline__ void store_tile(const MArgs& a, const f32x4 (&acc)[NI
                     }
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-}
-
-// Tile size (256 or 128) and grid of a product with `outs` columns of
-// results; 0 if there would be too many tiles.
-inline uint32_t tile_grid(MArgs* a, uint32_t outs, uint32_t* grid) {
-    uint32_t bm = 0;
-    for (uint32_t b : {256u, 128u}) {
-        const uint64_t rows = (a->m + b - 1) / b + (a->offsets ? a->groups : 0), cols = (uint64_t(outs) + b - 1) / b;
-        if (rows * cols >= (1u << 22)) return 0;
-        a->row_tiles = uint32_t(rows);
-        a->col_tiles = uint32_t(cols);
-        *grid = uint32_t(rows * cols);
-        bm = b;
-        if (!a->offsets && rows * cols >= 192) break;
-    }
-    return bm;
 }
 
 // kernels for parts of the range (false: not for these arguments)
-bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
+bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
 bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st);
-bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st);
-bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, hipStream_t st);
+bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st);
+bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
+// Chooses the tiling of a product with `outs` columns of results and `steps`
+// steps of the sum, and fills in the grid; steps' costs in cycles of a compute
+// unit by rows of a tile (256, 128, 64, 32).  Returns bm, 0 if no grid fits.
+uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]);
+// With a->splits > 1: points a copy's y at the scratch, and joins the parts.
+MArgs fp4_mm_parts(const MArgs& a, uint32_t outs, void* ws);
+void fp4_mm_join(const MArgs& a, uint32_t outs, uint32_t fmt, bool f32, const void* ws, hipStream_t st);
 
 }  // namespace dcr

@@ -121,14 +121,9 @@ __global__ void __launch_bounds__(kWaves * 64, 4) fp4_mm_rows_kernel(MArgs a) {
 }
 
 template <bool XQ, uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t mt, uint32_t grid) {
+void launch(const MArgs& a, hipStream_t st, uint32_t grid) {
     const dim3 g(grid), t(kWaves * 64);
-    if (mt == 1)
-        hipLaunchKernelGGL((fp4_mm_rows_kernel<XQ, WF, OUT, 1, 1>), g, t, 0, st, a);
-    else if (mt == 2)
-        hipLaunchKernelGGL((fp4_mm_rows_kernel<XQ, WF, OUT, 2, 2>), g, t, 0, st, a);
-    else
-        hipLaunchKernelGGL((fp4_mm_rows_kernel<XQ, WF, OUT, 4, 2>), g, t, 0, st, a);
+    hipLaunchKernelGGL((fp4_mm_rows_kernel<XQ, WF, OUT, 1, 1>), g, t, 0, st, a);
 }
 
 }  // namespace
@@ -138,20 +133,18 @@ bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st) {
         a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
     // rows of a group, as far as the host can tell
-    const uint64_t each = (a.m + a.groups - 1) / a.groups;
-    if (each > 64) return false;
-    const uint32_t mt = each <= 16 ? 1 : each <= 32 ? 2 : 4, nt = mt == 1 ? 1 : 2;
-    const uint64_t rt = (a.m + 16 * mt - 1) / (16 * mt) + (a.offsets ? a.groups : 0), ct = (uint64_t(a.n) + 16 * nt - 1) / (16 * nt);
+    if ((a.m + a.groups - 1) / a.groups > 16) return false;
+    const uint64_t rt = (a.m + 15) / 16 + (a.offsets ? a.groups : 0), ct = (uint64_t(a.n) + 15) / 16;
     if (rt * ct >= (1u << 22)) return false;
     a.row_tiles = uint32_t(rt);
     a.col_tiles = uint32_t(ct);
     const uint32_t grid = uint32_t(rt * ct);
     if (xq)
-        f32 ? launch<true, DCR_FP4_MX, float>(a, st, mt, grid) : launch<true, DCR_FP4_MX, uint16_t>(a, st, mt, grid);
+        f32 ? launch<true, DCR_FP4_MX, float>(a, st, grid) : launch<true, DCR_FP4_MX, uint16_t>(a, st, grid);
     else if (fmt == DCR_FP4_MX)
-        f32 ? launch<false, DCR_FP4_MX, float>(a, st, mt, grid) : launch<false, DCR_FP4_MX, uint16_t>(a, st, mt, grid);
+        f32 ? launch<false, DCR_FP4_MX, float>(a, st, grid) : launch<false, DCR_FP4_MX, uint16_t>(a, st, grid);
     else
-        f32 ? launch<false, DCR_FP4_NV, float>(a, st, mt, grid) : launch<false, DCR_FP4_NV, uint16_t>(a, st, mt, grid);
+        f32 ? launch<false, DCR_FP4_NV, float>(a, st, grid) : launch<false, DCR_FP4_NV, uint16_t>(a, st, grid);
     return true;
 }
 

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
 
-    const TilePlace at = tile_place(a, blockIdx.x);
+    const TilePlace at = tile_place(a);
     const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN;
@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     uint32_t wsc[NI];
     bf16x8 w[2][NI];
 
-    const uint32_t steps = (a.k + kBK - 1) / kBK;
+    // this workgroup's steps: from `first` on, up to `steps`
+    const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.k + kBK - 1) / kBK);
 
     // Loads of a step of aligned rows.  From the step on in which the sum ends
     // (at a multiple of 32), lanes past the end read behind the descriptors'
@@ -144,8 +145,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     // next quarter's codes is converted.  The codes' registers are free once the
     // last quarter is converted, and take the next step's then.
     auto compute = [&](const uint8_t* buf, uint32_t next) {
-        constexpr uint32_t H = 4, P = MI / H;
-        static_assert(P % NI == 0, "a subtile's codes are converted every P / NI phases");
+        constexpr uint32_t H = MI < 4 ? MI : 4, P = MI / H, C = (NI + P - 1) / P;   // C subtiles of codes a phase
         const uint8_t* xl = buf + r16 * kRowB;
         bf16x8 x[2][H];
         auto read = [&](uint32_t ph) {
@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i) convert(0, i);
             if (ALIGNED && ph == 3 * P) load_w(next);
-            if (j < 3 && ph % P % (P / NI) == 0) convert(j + 1, ph % P / (P / NI));
+            if (j < 3)
+#pragma unroll
+                for (uint32_t i = ph % P * C; i < (ph % P + 1) * C && i < NI; ++i) convert(j + 1, i);
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
 #pragma unroll
@@ -180,14 +182,14 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 
 
     if constexpr (ALIGNED) {
-        if (steps) {
-            past_end(0);
-            load_x(buf0, 0);
-            load_w(0);
+        if (first < steps) {
+            past_end(first);
+            load_x(buf0, first);
+            load_w(first);
         }
         // two steps a turn (one loop exit keeps the sums in their registers);
         // a step past the last is all zeros
-        for (uint32_t t = 0; t < steps; t += 2) {
+        for (uint32_t t = first; t < steps; t += 2) {
             __syncthreads();
             past_end(t + 1);
             load_x(buf1, t + 1);
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     } else {
 #pragma unroll 1
-        for (uint32_t t = 0; t < steps; ++t) {
+        for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
             load_any(buf0, t);
             __syncthreads();
@@ -207,36 +209,42 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     }
 
-    __syncthreads();
-    constexpr uint32_t LB = BM * kRowB / W;   // one buffer: the variant for any alignment has no second
-    store_tile<OUT, MI, NI, LB>(a, acc, WF == DCR_FP4_NV ? *a.tensor_scale : 1.0f, rt, rows, 0,
-                                n0 + wave * (BN / W), a.n, buf0 + wave * LB);
+    store_block<OUT, BM, BN, W, 1, BM * kRowB>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, 0,
+                                               wave * (BN / W), a.n, buf0, buf1);
 }
 
 template <uint32_t WF, typename OUT, bool ALIGNED>
-void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
+    const dim3 g(a.row_tiles * a.col_tiles * a.splits);
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ALIGNED>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ALIGNED>), g, dim3(512), 0, st, a);
+    else if (bm == 128)
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
+    else if (bm == 64)
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 64, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ALIGNED>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 32, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
-    a.x_vec && a.w_vec && a.k % 32 == 0 ? launch_tile<WF, OUT, true>(a, st, bm, grid) : launch_tile<WF, OUT, false>(a, st, bm, grid);
+void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
+    a.x_vec && a.w_vec && a.k % 32 == 0 ? launch_tile<WF, OUT, true>(a, st, bm) : launch_tile<WF, OUT, false>(a, st, bm);
 }
 
 }  // namespace
 
-bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, hipStream_t st) {
+bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
+    constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800};
     // offsets inside a tile are 31 bits
     if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
-    uint32_t grid = 0;
-    const uint32_t bm = tile_grid(&a, a.n, &grid);
+    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, kCost);
     if (!bm) return false;
+    const MArgs p = fp4_mm_parts(a, a.n, ws);
+    const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        f32 ? launch<DCR_FP4_MX, float>(a, st, bm, grid) : launch<DCR_FP4_MX, uint16_t>(a, st, bm, grid);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm) : launch<DCR_FP4_MX, uint16_t>(p, st, bm);
     else
-        f32 ? launch<DCR_FP4_NV, float>(a, st, bm, grid) : launch<DCR_FP4_NV, uint16_t>(a, st, bm, grid);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm) : launch<DCR_FP4_NV, uint16_t>(p, st, bm);
+    fp4_mm_join(a, a.n, fmt, f32, ws, st);
     return true;
 }
 

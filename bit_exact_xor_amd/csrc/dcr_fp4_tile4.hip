@@ -16,13 +16,14 @@ template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) {
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
     constexpr uint32_t XD = BM / 8 / W, WD = BN / 8 / W;   // 1 KiB loads of a wave and step
-    static_assert(W * 64 == BM + BN, "a thread stages the scales of one row");
+    static_assert(W * 64 >= BM + BN && BM % 64 == 0, "a thread stages the scales of one row, a wave those of one operand");
+    static_assert(MI % 4 == 0 && (NI % 4 == 0 || NI == 2), "a subtile's scale byte is its index mod 4");
     constexpr uint32_t kCodes = (BM + BN) * kRowB, kScales = (BM + BN) * (kBK / 32);
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[kCodes + kScales], buf1[kCodes + kScales];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
-    const TilePlace at = tile_place(a, blockIdx.x);
+    const TilePlace at = tile_place(a);
     const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN, cols = min(BN, a.n - n0);
@@ -37,7 +38,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     // go: [quarter of the step][quad][row of a subtile][subtile], so that a
     // lane reads the bytes of its subtiles at once
     const bool xside = wave < BM / 64;      // whole waves: the descriptor stays scalar
-    const uint32_t srow = threadIdx.x - (xside ? 0 : BM), last = (xside ? rows : cols) - 1;
+    const uint32_t srow = xside ? threadIdx.x : (threadIdx.x - BM) % BN;   // (spare threads do one over)
+    const uint32_t last = (xside ? rows : cols) - 1;
     const uint32_t sstep = uint32_t(xside ? a.xs_stride : a.ws_stride), blocks = a.k / 32;
     const auto sr = rsrc(xside ? a.xs + rt.begin * a.xs_stride : sb, last * sstep + blocks);
     const uint32_t soff = min(srow, last) * sstep;
@@ -45,7 +47,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint32_t sdst = kCodes + (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
 
     f32x4 acc[NI][MI] = {};
-    const uint32_t steps = (a.k + kBK - 1) / kBK;
+    // this workgroup's steps: from `first` on, up to `steps`
+    const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.k + kBK - 1) / kBK);
 
     // Codes of a step by loads straight to LDS.  From the step on in which the
     // sum ends (at a whole block) lanes past the end read behind the
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
         const uint8_t* wl = buf + BM * kRowB + (wn * (BN / WN) + r16) * kRowB;
         u32x4 x[2][H], w[NI];
-        uint32_t xs[MI / 4], ws[NI / 4];
+        uint32_t xs[MI / 4], ws[(NI + 3) / 4];
         auto read = [&](uint32_t ph) {
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
@@ -111,8 +114,12 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
                 const uint8_t* t = buf + kCodes + BM * (kBK / 32) + (j * 4 + quad) * 16 * (BN / 16) + r16 * (BN / 16) + wn * NI;
 #pragma unroll
                 for (uint32_t i = 0; i < MI / 4; ++i) xs[i] = *reinterpret_cast<const uint32_t*>(s + i * 4);
+                if constexpr (NI % 4 == 0) {
 #pragma unroll
-                for (uint32_t i = 0; i < NI / 4; ++i) ws[i] = *reinterpret_cast<const uint32_t*>(t + i * 4);
+                    for (uint32_t i = 0; i < NI / 4; ++i) ws[i] = *reinterpret_cast<const uint32_t*>(t + i * 4);
+                } else {
+                    ws[0] = *reinterpret_cast<const uint16_t*>(t);
+                }
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i)
                     w[i] = *reinterpret_cast<const u32x4*>(wl + i * 16 * kRowB + (((j * 4 + quad) ^ swizzle8(r16)) * 16));
@@ -134,13 +141,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    if (steps) {
-        load(buf0, 0);
-        store_scales(buf0, load_scales(0));
+    if (first < steps) {
+        load(buf0, first);
+        store_scales(buf0, load_scales(first));
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
-    for (uint32_t t = 0; t < steps; t += 2) {
+    for (uint32_t t = first; t < steps; t += 2) {
         __syncthreads();
         load(buf1, t + 1);
         const u32x2 s1 = load_scales(t + 1);
@@ -152,36 +159,39 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         compute(buf1);
         store_scales(buf0, s2);
     }
-    __syncthreads();
-    constexpr uint32_t LB = (BM + BN) * kRowB * 2 / W;
-    uint8_t* mine = wave < W / 2 ? buf0 + wave * LB : buf1 + (wave - W / 2) * LB;
-    store_tile<OUT, MI, NI, LB>(a, acc, 1.0f, rt, rows, wm * (BM / WM), n0 + wn * (BN / WN), a.n, mine);
+    store_block<OUT, BM, BN, W, WM, kCodes>(a, acc, 1.0f, rt, at, wm, wn * (BN / WN), a.n, buf0, buf1);
 }
 
 template <typename OUT, bool SV>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm, uint32_t grid) {
+void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
+    const dim3 g(a.row_tiles * a.col_tiles * a.splits);
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, SV>), dim3(grid), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, SV>), g, dim3(512), 0, st, a);
+    else if (bm == 128)
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2, SV>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2, SV>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 64, 128, 1, 4, SV>), g, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-bool fp4_mm_tile4(MArgs a, bool f32, hipStream_t st) {
+bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
+    constexpr uint32_t kCost[4] = {4800, 1600, 1000, UINT32_MAX};
     // pieces are whole blocks, offsets inside a tile 31 bits
     if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) ||
         a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
     // whole steps of scales at 8-byte borders: one load each
     const bool sv = a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0;
-    uint32_t grid = 0;
-    const uint32_t bm = tile_grid(&a, a.n, &grid);
+    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, kCost);
     if (!bm) return false;
+    const MArgs p = fp4_mm_parts(a, a.n, ws);
+    const bool wide = f32 || a.splits > 1;
     if (sv)
-        f32 ? launch<float, true>(a, st, bm, grid) : launch<uint16_t, true>(a, st, bm, grid);
+        wide ? launch<float, true>(p, st, bm) : launch<uint16_t, true>(p, st, bm);
     else
-        f32 ? launch<float, false>(a, st, bm, grid) : launch<uint16_t, false>(a, st, bm, grid);
+        wide ? launch<float, false>(p, st, bm) : launch<uint16_t, false>(p, st, bm);
+    fp4_mm_join(a, a.n, DCR_FP4_MX, f32, ws, st);
     return true;
 }
 
