@@ -32,8 +32,15 @@ __device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_
     return u32x4{a[0], a[1], b[0], b[1]};
 }
 
-template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t W, bool ALIGNED>
+// What is known of the rows: nothing; x and codes on 16-byte borders and a sum
+// of whole MX blocks; and scales of two steps at a time on borders of their
+// own (then one load for 16 rows brings two steps' scales: a load costs as
+// much for a byte of each row as for the 16 bytes of codes).
+enum class Rows { kAny, kAligned, kPaired };
+
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t W, Rows ROWS>
 __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
+    constexpr bool ALIGNED = ROWS != Rows::kAny, PAIRED = ROWS == Rows::kPaired;
     constexpr uint32_t MI = BM / 16, NI = BN / W / 16, DMA = BM / 4 / W;
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[BM * kRowB], buf1[BM * kRowB];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -61,7 +68,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     for (uint32_t i = 0; i < NI; ++i) {
         const uint32_t r = min(wave * (BN / W) + i * 16 + r16, a.n - 1 - n0);
         wo[i] = r * uint32_t(a.wc_stride) + quad * 16;
-        so[i] = r * uint32_t(a.ws_stride) + quad * (WF == DCR_FP4_MX ? 1 : 2);
+        so[i] = r * uint32_t(a.ws_stride) + (PAIRED ? 0 : quad * (WF == DCR_FP4_MX ? 1 : 2));
     }
 
     // buffer descriptors: scalar base and step, 32-bit lane offsets
@@ -73,6 +80,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     f32x4 acc[NI][MI] = {};
     u32x4 wq[NI];
     uint32_t wsc[NI];
+    typename std::conditional<WF == DCR_FP4_MX, u32x2, u32x4>::type pair[NI];   // scales of two steps of a row
     bf16x8 w[2][NI];
 
     // this workgroup's steps: from `first` on, up to `steps`
@@ -95,10 +103,36 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
             wq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], step * (kBK / 2), 0));
-            if (WF == DCR_FP4_MX)
+            if constexpr (PAIRED)
+                continue;
+            else if constexpr (WF == DCR_FP4_MX)
                 wsc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], step * (kBK / 32), 0);
             else
                 wsc[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], step * (kBK / 16), 0);
+        }
+    };
+    auto load_pair = [&](uint32_t step) {
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            if constexpr (!PAIRED)
+                continue;
+            else if constexpr (WF == DCR_FP4_MX)
+                pair[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(sr, so[i], step * (kBK / 32), 0));
+            else
+                pair[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sr, so[i], step * (kBK / 16), 0));
+        }
+    };
+    // this lane's scales of step `odd` of the pair
+    auto from_pair = [&](auto odd) {
+        constexpr uint32_t o = decltype(odd)::value;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) {
+            if constexpr (!PAIRED)
+                continue;
+            else if constexpr (WF == DCR_FP4_MX)
+                wsc[i] = (pair[i][o] >> (8 * quad)) & 255u;
+            else
+                wsc[i] = (quad & 2u ? pair[i][2 * o + 1] : pair[i][2 * o]) >> (16 * (quad & 1u));
         }
     };
     auto load_x = [&](uint8_t* buf, uint32_t step) {
@@ -144,7 +178,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     // the next four are read from LDS and part of the
     // next quarter's codes is converted.  The codes' registers are free once the
     // last quarter is converted, and take the next step's then.
-    auto compute = [&](const uint8_t* buf, uint32_t next) {
+    auto compute = [&](const uint8_t* buf, uint32_t next, auto odd) {
         constexpr uint32_t H = MI < 4 ? MI : 4, P = MI / H, C = (NI + P - 1) / P;   // C subtiles of codes a phase
         const uint8_t* xl = buf + r16 * kRowB;
         bf16x8 x[2][H];
@@ -154,6 +188,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
                 x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
                                                                 (((quad * 4 + ph / P) ^ swizzle(r16)) * 16));
         };
+        from_pair(odd);
         read(0);
 #pragma unroll
         for (uint32_t ph = 0; ph < 4 * P; ++ph) {
@@ -162,7 +197,10 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             if (ph == 0)
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i) convert(0, i);
-            if (ALIGNED && ph == 3 * P) load_w(next);
+            if (ALIGNED && ph == 3 * P) {
+                load_w(next);
+                if (decltype(odd)::value) load_pair(next);
+            }
             if (j < 3)
 #pragma unroll
                 for (uint32_t i = ph % P * C; i < (ph % P + 1) * C && i < NI; ++i) convert(j + 1, i);
@@ -181,11 +219,14 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     };
 
 
+    const std::integral_constant<uint32_t, 0> even;
+    const std::integral_constant<uint32_t, 1> odd;
     if constexpr (ALIGNED) {
         if (first < steps) {
             past_end(first);
             load_x(buf0, first);
             load_w(first);
+            load_pair(first);
         }
         // two steps a turn (one loop exit keeps the sums in their registers);
         // a step past the last is all zeros
@@ -193,11 +234,11 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             __syncthreads();
             past_end(t + 1);
             load_x(buf1, t + 1);
-            compute(buf0, t + 1);
+            compute(buf0, t + 1, even);
             __syncthreads();
             past_end(t + 2);
             load_x(buf0, t + 2);
-            compute(buf1, t + 2);
+            compute(buf1, t + 2, odd);
         }
     } else {
 #pragma unroll 1
@@ -205,7 +246,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             __syncthreads();
             load_any(buf0, t);
             __syncthreads();
-            compute(buf0, 0);
+            compute(buf0, 0, even);
         }
     }
 
@@ -213,21 +254,26 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
                                                wave * (BN / W), a.n, buf0, buf1);
 }
 
-template <uint32_t WF, typename OUT, bool ALIGNED>
+template <uint32_t WF, typename OUT, Rows ROWS>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
     const dim3 g(a.row_tiles * a.col_tiles * a.splits);
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ALIGNED>), g, dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ROWS>), g, dim3(512), 0, st, a);
     else if (bm == 128)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ROWS>), g, dim3(256), 0, st, a);
     else if (bm == 64)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 64, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 64, 128, 4, ROWS>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 32, 128, 4, ALIGNED>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 32, 128, 4, ROWS>), g, dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
-    a.x_vec && a.w_vec && a.k % 32 == 0 ? launch_tile<WF, OUT, true>(a, st, bm) : launch_tile<WF, OUT, false>(a, st, bm);
+    if (!a.x_vec || !a.w_vec || a.k % 32)
+        launch_tile<WF, OUT, Rows::kAny>(a, st, bm);
+    else if (a.k % 256 == 0 && a.ws_stride % (256 / fp4_block(WF)) == 0)
+        launch_tile<WF, OUT, Rows::kPaired>(a, st, bm);
+    else
+        launch_tile<WF, OUT, Rows::kAligned>(a, st, bm);
 }
 
 }  // namespace
