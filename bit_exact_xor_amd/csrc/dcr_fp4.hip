@@ -21,7 +21,7 @@ namespace {
 
 constexpr uint32_t kQT = 256;      // threads of a workgroup
 constexpr uint32_t kQU = 4;        // 16-byte pieces a lane has in flight
-constexpr uint32_t kParts = 512;   // workgroups (and partial maxima) of a calibration
+constexpr uint32_t kParts = 1024;  // workgroups (and partial maxima) of a calibration
 
 struct QArgs {
     const void* x;            // wide side (read by quantise, written by dequantise)
@@ -34,9 +34,16 @@ struct QArgs {
     uint32_t cols, per_row;   // per_row: lane pieces of a row, whole blocks
 };
 
-template <typename T> struct Wide;
-template <> struct Wide<uint16_t> { static constexpr uint32_t E = 8; };
-template <> struct Wide<float> { static constexpr uint32_t E = 4; };
+// 16 bytes of the wide side at its elements' alignment, and the codes of as
+// many elements at any: one access each on gfx950
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
+typedef uint16_t __attribute__((aligned(1))) u16_any;
+
+// elements of a lane's piece: 16 bytes of the wide side; 32 where an NV scale
+// is to be found for fp32 values, which costs a lane as much as eight codes
+template <typename T, bool NV_SCALES = false>
+constexpr uint32_t kPiece = sizeof(T) == 2 ? 8 : NV_SCALES ? 8 : 4;
 
 // row and column of a lane's piece: the workgroup's first piece is divided
 // once in 64 bits, the rest is a 32-bit step from there
@@ -82,27 +89,17 @@ __device__ __forceinline__ float e4m3_val(uint32_t i) {
 }
 
 // Index of the e4m3 value nearest amax / (6 s), ties to even, at most 448.
-// The quotient in fp32 may land on the wrong side of a border, by one index
-// at most; 6 * border has seven significant bits, so the sign of
-// fma(-6 border, s, amax) is exact and settles it.
-__device__ __forceinline__ uint32_t nv_scale(float amax, float s) {
-    const float v = amax * __frcp_rn(6.0f * s);
-    uint32_t i;
-    if (v < 0x1p-6f) {
-        i = uint32_t(__float2int_rn(v * 512.0f));
-    } else {
-        const uint32_t b = __float_as_uint(fminf(v, 1024.0f));
-        i = min(((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - (120u << 3), 126u);
-    }
-    if (i < 126) {
-        const float d = __fmaf_rn(-6.0f * (e4m3_val(i) + 0.5f * e4m3_gap(i)), s, amax);
-        if (d > 0.0f || (d == 0.0f && (i & 1u))) return i + 1;
-    }
-    if (i > 0) {
-        const float d = __fmaf_rn(-6.0f * (e4m3_val(i - 1) + 0.5f * e4m3_gap(i - 1)), s, amax);
-        if (d < 0.0f || (d == 0.0f && (i & 1u))) return i - 1;
-    }
-    return i;
+// The conversion instruction rounds the quotient computed in fp32, off by less
+// than 2^-21 of itself: moved that far down and up it gives the same index, or
+// the borders decide.  6 * border has seven significant bits, so the sign of
+// fma(-6 border, s, amax) is exact.
+__device__ __forceinline__ uint32_t nv_scale(float amax, float s, float inv6s) {
+    const float lo = fminf(amax * (inv6s * (1.0f - 0x1p-20f)), 448.0f), hi = fminf(amax * (inv6s * (1.0f + 0x1p-20f)), 448.0f);
+    const uint32_t pk = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, 0, false));
+    const uint32_t i = pk & 255u;
+    if (i == ((pk >> 8) & 255u)) return i;
+    const float d = __fmaf_rn(-6.0f * (e4m3_val(i) + 0.5f * e4m3_gap(i)), s, amax);
+    return i + ((d > 0.0f || (d == 0.0f && (i & 1u))) ? 1u : 0u);
 }
 
 // code of x at block scale b, tensor scale s, by exact comparison with the
@@ -119,41 +116,33 @@ __device__ __forceinline__ uint32_t nv_code_exact(float x, float b, float s) {
     return c | ((__float_as_uint(x) >> 31) << 3);
 }
 
-// E codes (4 bits each) of v at scales b and s.  The conversion instruction
-// rounds x / (b s) computed in fp32, off by less than 2^-21 of itself: moved
-// that far down and up it gives the same code, or the exact comparison decides.
-template <uint32_t E>
+// Eight codes (4 bits each) of v at scales b and s: found like the scale.
 __device__ __forceinline__ uint32_t nv_codes(const float* v, float b, float s) {
-    const float r = __builtin_amdgcn_rcpf(b * s);
+    const float r = __builtin_amdgcn_rcpf(b * s), dn = r * (1.0f - 0x1p-20f), up = r * (1.0f + 0x1p-20f);
     uint32_t lo = 0, hi = 0;
-    float y[E];
-#pragma unroll
-    for (uint32_t i = 0; i < E; ++i) y[i] = v[i] * r;
-    constexpr float dn = 1.0f - 0x1p-20f, up = 1.0f + 0x1p-20f;
-    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, y[0] * dn, y[1] * dn, 1.0f, 0);
-    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, y[0] * up, y[1] * up, 1.0f, 0);
-    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, y[2] * dn, y[3] * dn, 1.0f, 1);
-    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, y[2] * up, y[3] * up, 1.0f, 1);
-    if constexpr (E == 8) {
-        lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, y[4] * dn, y[5] * dn, 1.0f, 2);
-        hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, y[4] * up, y[5] * up, 1.0f, 2);
-        lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, y[6] * dn, y[7] * dn, 1.0f, 3);
-        hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, y[6] * up, y[7] * up, 1.0f, 3);
-    }
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[0] * dn, v[1] * dn, 1.0f, 0);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[0] * up, v[1] * up, 1.0f, 0);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[2] * dn, v[3] * dn, 1.0f, 1);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[2] * up, v[3] * up, 1.0f, 1);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[4] * dn, v[5] * dn, 1.0f, 2);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[4] * up, v[5] * up, 1.0f, 2);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, v[6] * dn, v[7] * dn, 1.0f, 3);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, v[6] * up, v[7] * up, 1.0f, 3);
     if (lo != hi) {
         lo = 0;
 #pragma unroll
-        for (uint32_t i = 0; i < E; ++i) lo |= nv_code_exact(v[i], b, s) << (4 * i);
+        for (uint32_t i = 0; i < 8; ++i) lo |= nv_code_exact(v[i], b, s) << (4 * i);
     }
     return lo;
 }
 
 // a lane's E elements as fp32 (zeros past the row's end) and max |bits|
-template <typename T, bool VEC>
+// (LAST: not read again by this call)
+template <typename T, uint32_t E, bool LAST>
 __device__ __forceinline__ void load_piece(const T* row, uint32_t c0, uint32_t cols, float* v) {
-    constexpr uint32_t E = Wide<T>::E;
-    if (VEC && c0 + E <= cols) {
-        const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + c0));
+    if (c0 + E <= cols) {
+        const auto* from = reinterpret_cast<const u32x4_any*>(row + c0);
+        const u32x4 q = LAST ? u32x4(__builtin_nontemporal_load(from)) : u32x4(*from);
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -163,6 +152,11 @@ __device__ __forceinline__ void load_piece(const T* row, uint32_t c0, uint32_t c
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(q[i]);
+            if constexpr (E == 8) {
+                const u32x4 p = LAST ? u32x4(__builtin_nontemporal_load(from + 1)) : u32x4(from[1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 + i] = __uint_as_float(p[i]);
+            }
         }
     } else {
 #pragma unroll
@@ -179,9 +173,9 @@ __device__ __forceinline__ void load_piece(const T* row, uint32_t c0, uint32_t c
     }
 }
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kQT) fp4_amax_kernel(QArgs a, uint32_t* parts) {
-    constexpr uint32_t E = Wide<T>::E;
+    constexpr uint32_t E = kPiece<T, true>;
     __shared__ uint32_t lds[kQT / 64];
     uint32_t m = 0;
     const uint64_t step = uint64_t(gridDim.x) * kQT * kQU;
@@ -194,7 +188,7 @@ __global__ void __launch_bounds__(kQT) fp4_amax_kernel(QArgs a, uint32_t* parts)
             if (base + off >= a.items) continue;
             const Place p = place(row0, piece0, off, a.per_row);
             float v[E];
-            load_piece<T, VEC>(static_cast<const T*>(a.x) + p.row * a.x_stride, p.piece * E, a.cols, v);
+            load_piece<T, E, false>(static_cast<const T*>(a.x) + p.row * a.x_stride, p.piece * E, a.cols, v);
 #pragma unroll
             for (uint32_t i = 0; i < E; ++i) {
                 const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
@@ -206,9 +200,9 @@ __global__ void __launch_bounds__(kQT) fp4_amax_kernel(QArgs a, uint32_t* parts)
     if (threadIdx.x == 0) parts[blockIdx.x] = m;
 }
 
-template <typename T, uint32_t FMT, bool VEC>
+template <typename T, uint32_t FMT>
 __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
-    constexpr uint32_t E = Wide<T>::E, LANES = fp4_block(FMT) / E;
+    constexpr uint32_t E = kPiece<T, FMT == DCR_FP4_NV>, LANES = fp4_block(FMT) / E;
     float s = 1.0f;
     if constexpr (FMT == DCR_FP4_NV) {
         if (a.parts) {
@@ -221,6 +215,7 @@ __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
             s = *a.tensor_scale;
         }
     }
+    const float inv6s = FMT == DCR_FP4_NV ? __frcp_rn(6.0f * s) : 0.0f;
     const bool usable = FMT == DCR_FP4_MX || (s >= kFp4MinScale && s <= kFp4MaxScale);
     const uint64_t base = uint64_t(blockIdx.x) * kQT * kQU;
     const uint64_t row0 = base / a.per_row;
@@ -232,7 +227,7 @@ __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
         const uint32_t off = u * kQT + threadIdx.x;
         p[u] = place(row0, piece0, off, a.per_row);
         if (base + off < a.items) {
-            load_piece<T, VEC>(static_cast<const T*>(a.x) + p[u].row * a.x_stride, p[u].piece * E, a.cols, v[u]);
+            load_piece<T, E, true>(static_cast<const T*>(a.x) + p[u].row * a.x_stride, p[u].piece * E, a.cols, v[u]);
         } else {
 #pragma unroll
             for (uint32_t i = 0; i < E; ++i) v[u][i] = 0.0f;
@@ -256,9 +251,9 @@ __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
                 c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[u][6], v[u][7], unit, 3);
             }
         } else {
-            sbyte = finite ? nv_scale(__uint_as_float(m), s) : 127u;
+            sbyte = finite ? nv_scale(__uint_as_float(m), s, inv6s) : 127u;
             if (finite && sbyte) {
-                c = nv_codes<E>(v[u], e4m3_val(sbyte), s);
+                c = nv_codes(v[u], e4m3_f32(sbyte), s);
             } else {
 #pragma unroll
                 for (uint32_t i = 0; i < E; ++i) c |= (__float_as_uint(v[u][i]) >> 31) << (4 * i + 3);
@@ -269,11 +264,11 @@ __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
         const uint32_t c0 = p[u].piece * E;
         if (c0 >= a.cols) continue;     // a lane behind the row's end, in its last block
         uint8_t* out = a.codes + p[u].row * a.code_stride + c0 / 2;
-        if (VEC && c0 + E <= a.cols) {
+        if (c0 + E <= a.cols) {
             if constexpr (E == 8)
-                *reinterpret_cast<uint32_t*>(out) = c;
+                *reinterpret_cast<u32_any*>(out) = c;
             else
-                *reinterpret_cast<uint16_t*>(out) = uint16_t(c);
+                *reinterpret_cast<u16_any*>(out) = uint16_t(c);
         } else {
             const uint32_t n = min(E, a.cols - c0);
             if (n < 8) c &= (1u << (4 * n)) - 1u;
@@ -283,9 +278,9 @@ __global__ void __launch_bounds__(kQT) fp4_quantize_kernel(QArgs a) {
     }
 }
 
-template <typename T, uint32_t FMT, bool VEC>
+template <typename T, uint32_t FMT>
 __global__ void __launch_bounds__(kQT) fp4_dequantize_kernel(QArgs a) {
-    constexpr uint32_t E = Wide<T>::E, LANES = fp4_block(FMT) / E;
+    constexpr uint32_t E = kPiece<T>, LANES = fp4_block(FMT) / E;
     const float s = FMT == DCR_FP4_NV ? *a.tensor_scale : 1.0f;
     const uint64_t base = uint64_t(blockIdx.x) * kQT * kQU;
     const uint64_t row0 = base / a.per_row;
@@ -302,11 +297,11 @@ __global__ void __launch_bounds__(kQT) fp4_dequantize_kernel(QArgs a) {
         c[u] = sb[u] = 0;
         if (!live[u]) continue;
         const uint8_t* in = a.codes + p[u].row * a.code_stride + c0 / 2;
-        if (VEC && c0 + E <= a.cols) {
+        if (c0 + E <= a.cols) {
             if constexpr (E == 8)
-                c[u] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(in));
+                c[u] = *reinterpret_cast<const u32_any*>(in);
             else
-                c[u] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(in));
+                c[u] = *reinterpret_cast<const u16_any*>(in);
         } else {
             const uint32_t n = min(E, a.cols - c0);
             for (uint32_t i = 0; i < (n + 1) / 2; ++i) c[u] |= uint32_t(in[i]) << (8 * i);
@@ -328,18 +323,18 @@ __global__ void __launch_bounds__(kQT) fp4_dequantize_kernel(QArgs a) {
             uint16_t h[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-            if (VEC && c0 + E <= a.cols) {
+            if (c0 + E <= a.cols) {
                 u32x4 q;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) q[i] = h[2 * i] | (uint32_t(h[2 * i + 1]) << 16);
-                __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(out));
+                __builtin_nontemporal_store(q, reinterpret_cast<u32x4_any*>(out));
             } else {
                 for (uint32_t i = 0; i < min(E, a.cols - c0); ++i) out[i] = h[i];
             }
         } else {
-            if (VEC && c0 + E <= a.cols) {
+            if (c0 + E <= a.cols) {
                 const f32x4 q = {v[0], v[1], v[2], v[3]};
-                __builtin_nontemporal_store(q, reinterpret_cast<f32x4*>(out));
+                __builtin_nontemporal_store(__builtin_bit_cast(u32x4, q), reinterpret_cast<u32x4_any*>(out));
             } else {
                 for (uint32_t i = 0; i < min(E, a.cols - c0); ++i) out[i] = v[i];
             }
@@ -347,11 +342,11 @@ __global__ void __launch_bounds__(kQT) fp4_dequantize_kernel(QArgs a) {
     }
 }
 
-// the kernels' arguments for a tensor and its wide side; false if there is
+// the kernels' arguments for a tensor and its wide side, E elements a piece; false if there is
 // nothing to do
-bool plan_pieces(const dcr_fp4_tensor& t, const void* x, uint32_t elem, uint64_t x_stride, QArgs* a, bool* vec) {
+bool plan_pieces(const dcr_fp4_tensor& t, const void* x, uint32_t E, uint64_t x_stride, QArgs* a) {
     if (!t.rows || !t.cols) return false;
-    const uint32_t B = fp4_block(t.format), E = 16 / elem;
+    const uint32_t B = fp4_block(t.format);
     QArgs r{};
     r.x = x;
     r.codes = static_cast<uint8_t*>(t.codes);
@@ -372,9 +367,6 @@ bool plan_pieces(const dcr_fp4_tensor& t, const void* x, uint32_t elem, uint64_t
     r.cols = uint32_t(cols);
     r.per_row = uint32_t((cols + B - 1) / B) * (B / E);
     r.items = r.rows * r.per_row;
-    // 16-byte accesses on the wide side need every row to start on such a
-    // border, the codes' 4- or 2-byte ones theirs
-    *vec = al16(x) && (r.rows == 1 || (r.x_stride * elem % 16 == 0 && r.code_stride % (E / 2) == 0));
     *a = r;
     return true;
 }
@@ -391,24 +383,16 @@ int32_t check_wide(const void* x, uint32_t type, uint64_t stride, const dcr_fp4_
     return DCR_OK;
 }
 
-template <template <typename, uint32_t, bool> class L>
-void dispatch(uint32_t type, uint32_t fmt, bool vec, const QArgs& a, uint32_t grid, hipStream_t st) {
-    const bool b = type == DCR_BF16, mx = fmt == DCR_FP4_MX;
-    if (b && mx) vec ? L<uint16_t, DCR_FP4_MX, true>::go(a, grid, st) : L<uint16_t, DCR_FP4_MX, false>::go(a, grid, st);
-    if (b && !mx) vec ? L<uint16_t, DCR_FP4_NV, true>::go(a, grid, st) : L<uint16_t, DCR_FP4_NV, false>::go(a, grid, st);
-    if (!b && mx) vec ? L<float, DCR_FP4_MX, true>::go(a, grid, st) : L<float, DCR_FP4_MX, false>::go(a, grid, st);
-    if (!b && !mx) vec ? L<float, DCR_FP4_NV, true>::go(a, grid, st) : L<float, DCR_FP4_NV, false>::go(a, grid, st);
+// f(element type, format) with the types and formats as compile-time values
+template <typename F>
+void dispatch(uint32_t type, uint32_t fmt, F&& f) {
+    const std::integral_constant<uint32_t, DCR_FP4_MX> mx;
+    const std::integral_constant<uint32_t, DCR_FP4_NV> nv;
+    if (type == DCR_BF16)
+        fmt == DCR_FP4_MX ? f(uint16_t(), mx) : f(uint16_t(), nv);
+    else
+        fmt == DCR_FP4_MX ? f(float(), mx) : f(float(), nv);
 }
-template <typename T, uint32_t FMT, bool VEC> struct Quantize {
-    static void go(const QArgs& a, uint32_t grid, hipStream_t st) {
-        hipLaunchKernelGGL((fp4_quantize_kernel<T, FMT, VEC>), dim3(grid), dim3(kQT), 0, st, a);
-    }
-};
-template <typename T, uint32_t FMT, bool VEC> struct Dequantize {
-    static void go(const QArgs& a, uint32_t grid, hipStream_t st) {
-        hipLaunchKernelGGL((fp4_dequantize_kernel<T, FMT, VEC>), dim3(grid), dim3(kQT), 0, st, a);
-    }
-};
 
 int32_t quantize(const void* x, uint32_t x_type, uint64_t x_stride, const dcr_fp4_tensor* q, uint32_t options,
                  void* ws, uint64_t ws_bytes, hipStream_t st) {
@@ -419,26 +403,22 @@ int32_t quantize(const void* x, uint32_t x_type, uint64_t x_stride, const dcr_fp
     if (calibrate && q->format != DCR_FP4_NV) return fp4_fail(DCR_E_INVAL, "only the NV format has a tensor scale to calibrate");
     if ((rc = check_wide(x, x_type, x_stride, *q, "source"))) return rc;
     QArgs a;
-    bool vec;
-    if (!plan_pieces(*q, x, x_type == DCR_F32 ? 4 : 2, x_stride, &a, &vec)) return DCR_OK;
+    if (!plan_pieces(*q, x, x_type == DCR_F32 && q->format == DCR_FP4_MX ? 4 : 8, x_stride, &a)) return DCR_OK;
     const uint64_t grid = (a.items + kQT * kQU - 1) / (kQT * kQU);
     if (grid >= (uint64_t(1) << 32) / kQT) return fp4_fail(DCR_E_INVAL, "tensor too large for one launch");
     if (calibrate) {
         if (!ws || !al16(ws)) return fp4_fail(DCR_E_INVAL, "workspace is NULL or not 16-byte aligned");
         if (ws_bytes < kParts * sizeof(uint32_t)) return fp4_fail(DCR_E_CAPACITY, "workspace too small");
         uint32_t* parts = static_cast<uint32_t*>(ws);
-        const dim3 g(kParts), t(kQT);
-        if (x_type == DCR_BF16 && vec)
-            hipLaunchKernelGGL((fp4_amax_kernel<uint16_t, true>), g, t, 0, st, a, parts);
-        else if (x_type == DCR_BF16)
-            hipLaunchKernelGGL((fp4_amax_kernel<uint16_t, false>), g, t, 0, st, a, parts);
-        else if (vec)
-            hipLaunchKernelGGL((fp4_amax_kernel<float, true>), g, t, 0, st, a, parts);
+        if (x_type == DCR_BF16)
+            hipLaunchKernelGGL((fp4_amax_kernel<uint16_t>), dim3(kParts), dim3(kQT), 0, st, a, parts);
         else
-            hipLaunchKernelGGL((fp4_amax_kernel<float, false>), g, t, 0, st, a, parts);
+            hipLaunchKernelGGL((fp4_amax_kernel<float>), dim3(kParts), dim3(kQT), 0, st, a, parts);
         a.parts = parts;
     }
-    dispatch<Quantize>(x_type, q->format, vec, a, uint32_t(grid), st);
+    dispatch(x_type, q->format, [&](auto elem, auto fmt) {
+        hipLaunchKernelGGL((fp4_quantize_kernel<decltype(elem), decltype(fmt)::value>), dim3(uint32_t(grid)), dim3(kQT), 0, st, a);
+    });
     return fp4_launched();
 }
 
@@ -447,11 +427,12 @@ int32_t dequantize(const dcr_fp4_tensor* q, void* y, uint32_t y_type, uint64_t y
     if (rc) return rc;
     if ((rc = check_wide(y, y_type, y_stride, *q, "destination"))) return rc;
     QArgs a;
-    bool vec;
-    if (!plan_pieces(*q, y, y_type == DCR_F32 ? 4 : 2, y_stride, &a, &vec)) return DCR_OK;
+    if (!plan_pieces(*q, y, y_type == DCR_F32 ? 4 : 8, y_stride, &a)) return DCR_OK;
     const uint64_t grid = (a.items + kQT * kQU - 1) / (kQT * kQU);
     if (grid >= (uint64_t(1) << 32) / kQT) return fp4_fail(DCR_E_INVAL, "tensor too large for one launch");
-    dispatch<Dequantize>(y_type, q->format, vec, a, uint32_t(grid), st);
+    dispatch(y_type, q->format, [&](auto elem, auto fmt) {
+        hipLaunchKernelGGL((fp4_dequantize_kernel<decltype(elem), decltype(fmt)::value>), dim3(uint32_t(grid)), dim3(kQT), 0, st, a);
+    });
     return fp4_launched();
 }
 

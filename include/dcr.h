@@ -606,7 +606,7 @@ typedef struct {
  *   options  0, or DCR_FP4_CALIBRATE (DCR_FP4_NV): *tensor_scale is written
  *            first, max|x| over the finite elements / 2688, held to its
  *            range, 1 if x is all zeros
- *   workspace_dev  DCR_FP4_CALIBRATE: 16-byte aligned, at least 2048 bytes
+ *   workspace_dev  DCR_FP4_CALIBRATE: 16-byte aligned, at least 4096 bytes
  *                  (DCR_E_CAPACITY); else not looked at */
 int32_t dcr_fp4_quantize(const void* x, uint32_t x_type, uint64_t x_stride, const dcr_fp4_tensor* q,
                          uint32_t options, void* workspace_dev, uint64_t ws_bytes, void* stream);

@@ -56,7 +56,7 @@ def test_bad_quantize_arguments():
     for kw in (dict(x=None), dict(x=AT + 2), dict(x=AT + 1, ty=1), dict(ty=2), dict(stride=63), dict(stride=1 << 40),
                dict(opt=2), dict(opt=1), dict(d=nv, opt=1), dict(d=nv, opt=1, ws=AT + 8, n=4096)):
         assert quantize(**kw) == dcr.DCR_E_INVAL, kw
-    assert quantize(nv, opt=1, ws=AT, n=2047) == dcr.DCR_E_CAPACITY
+    assert quantize(nv, opt=1, ws=AT, n=4095) == dcr.DCR_E_CAPACITY
     for kw in (dict(y=None), dict(y=AT + 2), dict(ty=7), dict(stride=10)):
         assert dequantize(**kw) == dcr.DCR_E_INVAL, kw
 
