@@ -14,6 +14,10 @@ kernel works on the other).
 
 Only copies (the copy engines) and library calls are issued here; every
 step of the method runs in libdcr's kernels.
+
+Fp4Refit is the same path for weights that the receiver serves in 4 bits:
+the trainer's BF16 or fp32 weights are quantised, the bytes that changed
+travel, and the receiver multiplies with the tensors the apply has patched.
 """
 import numpy as np
 
@@ -155,3 +159,92 @@ class HostLoopback:
         h = self.send_serial(old_shards, new_shards, mode, base_version, new_version, sb, workspace)
         self.d2h.synchronize()
         return self.receive_serial(h, canon, flags, apply_workspace, base_version)
+
+
+class Fp4Refit:
+    """A refit of 4-bit weights over a HostLoopback.
+
+    `shapes` lists the weights' (rows, cols).  The sender holds two versions of
+    each as `Fp4Tensor`s, the committed one (`sent`) and the next; the receiver
+    holds one (`held`), in memory of its own.  Codes and scale bytes are
+    canonical tensors of one-byte elements carried as XOR masks, an NV tensor
+    scale is one fp32 element carried as an overwrite.  The first refit takes
+    the NV tensor scales from the weights and sends everything; later ones keep
+    them (so that few bytes change) unless `calibrate` is passed."""
+
+    def __init__(self, shapes, fmt=dcr.FP4_NV, device="cuda", n_slices=4):
+        import torch
+        self.fmt, self.device, self.n_slices = fmt, device, n_slices
+        self.version = 0
+        self.sent, self.next, self.held = ([dcr.Fp4Tensor(r, c, fmt, device) for r, c in shapes] for _ in range(3))
+        for side in (self.sent, self.next, self.held):
+            for t in side:
+                if t.tensor_scale is not None:
+                    t.tensor_scale.zero_()
+        sizes = []                       # (elements, bytes an element, route) of each canonical tensor
+        for t in self.held:
+            sizes += [(t.codes.numel(), 1, dcr.ROUTE_AFFINE_XOR), (t.scales.numel(), 1, dcr.ROUTE_AFFINE_XOR)]
+            if fmt == dcr.FP4_NV:
+                sizes.append((1, 4, dcr.ROUTE_OVERWRITE))
+        tensors = np.zeros(len(sizes), dtype=dcr.TENSOR_DESC)
+        segments = np.zeros(sum(n > 0 for n, _w, _r in sizes), dtype=dcr.SEGMENT)
+        s = 0
+        for i, (n, w, route) in enumerate(sizes):
+            tensors[i] = (n, w, route, -1, 0)
+            if n:                        # each tensor is its own shard, whole and in order
+                segments[s] = (i, i, 1, 0, 0, 0, [n, 1, 1, 1], [1, 0, 0, 0], [1, 0, 0, 0])
+                s += 1
+        self.plan = dcr.dcr_plan_build(tensors, [n * w for n, w, _r in sizes], segments)
+        dcr.dcr_plan_upload(self.plan, device)
+        info = self.plan.info
+        self.link = HostLoopback(self.plan, info.max_dir_bytes, info.max_payload_bytes, device)
+        self.stream = dcr.StreamBuffers(self.plan, device)
+        self.flags = torch.empty(max(1, info.max_dir_bytes // 32), dtype=torch.uint8, device=device)
+        self.encode_workspace = dcr.workspace(self.plan, device, info.max_payload_bytes)
+        self.apply_workspace = dcr.workspace(self.plan, device)
+        self.fp4_workspace = dcr.fp4_workspace(device)
+
+    def _buffers(self, side):
+        out = []
+        for t in side:
+            out += [t.codes, t.scales]
+            if t.tensor_scale is not None:
+                out.append(t.tensor_scale)
+        return out
+
+    def refit(self, weights, calibrate=False):
+        """Quantise the trainer's `weights` (BF16 or fp32, one for each shape),
+        send what changed and patch `held`; returns the payload bytes sent.
+        The work runs on the current stream and the link's; `held` is patched
+        when the call returns."""
+        import torch
+        if len(weights) != len(self.next):
+            raise ValueError(f"{len(self.next)} weights expected, got {len(weights)}")
+        calibrate = self.fmt == dcr.FP4_NV and (calibrate or self.version == 0)
+        for w, q, old in zip(weights, self.next, self.sent):
+            if q.tensor_scale is not None and not calibrate:
+                q.tensor_scale.copy_(old.tensor_scale)
+            dcr.dcr_fp4_quantize(w, q, dcr.FP4_CALIBRATE if calibrate else 0, self.fp4_workspace)
+        self.flags.zero_()
+        # the receiver's streams wait for the flags and for earlier products
+        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
+        heads, results = self.link.run(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_DELTA,
+                                       self.version, self.version + 1, self.stream, self.encode_workspace,
+                                       self.n_slices, self._buffers(self.held), self.flags, self.apply_workspace)
+        self.link.apply_stream.synchronize()
+        for r in results:
+            bad = dcr.apply_result(r)
+            if int(bad["n_invalid"]):
+                raise dcr.DcrError(dcr.DCR_E_FORMAT, "Fp4Refit.refit", f"{int(bad['n_invalid'])} records refused")
+        self.sent, self.next = self.next, self.sent
+        self.version += 1
+        return _u64(heads[-1], 48)
+
+    def matmul(self, i, x, out_dtype=None, offsets=None):
+        """x w^T with the receiver's weight i (see dcr_fp4_matmul)."""
+        import torch
+        w = self.held[i]
+        n = w.rows if offsets is None else w.rows // (offsets.numel() - 1)
+        y = torch.empty(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
+        dcr.dcr_fp4_matmul(x, w, y, offsets, self.fp4_workspace)
+        return y

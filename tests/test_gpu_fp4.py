@@ -417,3 +417,66 @@ def test_far_offsets():
     w = R.unit_values(c, b, cols, R.NV)
     ref, size = R.product(f64(x), w)
     assert (np.abs(f64(y) - ref * .01) <= bound(size * .01, ref * .01, cols, "fp32") + np.abs(ref) * 1e-9).all()
+
+
+# -------------------------------------------------------------- refit in 4 bits
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_refit_then_product(fmt):
+    """Quantise, encode, transfer, apply in place, multiply: after every refit
+    the receiver holds the sender's bytes and its products are the sender's."""
+    from bit_exact_xor_amd import pipeline
+    rng = np.random.default_rng(9)
+    shapes = [(768, 2048), (130, 96), (33, 70), (512, 512)]
+    link = pipeline.Fp4Refit(shapes, fmt)
+    w = [up((0.02 * rng.standard_normal(s)).astype(np.float32)) for s in shapes]
+    sent = []
+    for step in range(4):
+        if step:
+            for t in w:      # a small update of some of the weights, as a training step makes
+                t += up((rng.random(t.shape) < 0.02) * rng.choice([-1, 1], t.shape) * 2e-3).float()
+        sent.append(link.refit([w[0].bfloat16()] + w[1:], calibrate=step == 3))
+        assert link.version == step + 1
+        for i, (t, s) in enumerate(zip(w, shapes)):
+            src = (w[0].bfloat16() if i == 0 else t).float().cpu().numpy()
+            sc = 1.0 if fmt == R.MX else float(link.held[i].tensor_scale)
+            if fmt == R.NV and step in (0, 3):
+                assert sc == float(R.calibrate(src))
+            c, b = R.quantize(src, fmt, sc)
+            assert np.array_equal(link.held[i].codes.cpu().numpy()[:, :c.shape[1]], c)
+            assert np.array_equal(link.held[i].scales.cpu().numpy(), b)
+            assert torch.equal(link.held[i].codes, link.sent[i].codes)
+            x = up(rng.integers(-2, 3, (5, s[1]))).bfloat16()
+            y = torch.empty(5, s[0], device="cuda")
+            dcr.dcr_fp4_matmul(x, link.sent[i], y, None, link.fp4_workspace)
+            assert torch.equal(link.matmul(i, x, torch.float32), y)
+            ref, size = R.product(f64(x), R.unit_values(c, b, s[1], fmt))
+            assert (np.abs(f64(y) - ref * sc) <= bound(size * sc, ref * sc, s[1], "fp32")).all()
+    assert sent[1] < sent[0] / 4 and sent[2] < sent[0] / 4      # 2 % of elements moved: few bytes travel
+    with pytest.raises(ValueError):
+        link.refit(w[:2])
+
+
+def test_refit_of_unchanged_weights_sends_nothing():
+    from bit_exact_xor_amd import pipeline
+    link = pipeline.Fp4Refit([(64, 96)], R.NV)
+    w = [torch.ones(64, 96, device="cuda")]
+    assert link.refit(w) > 0
+    assert link.refit(w) == 0 and link.refit(w) == 0
+
+
+def test_refit_of_experts():
+    """A stack of experts, refitted and multiplied by groups."""
+    from bit_exact_xor_amd import pipeline
+    rng = np.random.default_rng(11)
+    link = pipeline.Fp4Refit([(8 * 48, 64)], R.MX)
+    w = up(rng.standard_normal((8 * 48, 64)).astype(np.float32))
+    off = [0, 3, 3, 10, 11, 40, 41, 60, 64]
+    x = up(rng.integers(-2, 3, (64, 64))).bfloat16()
+    for _ in range(2):
+        link.refit([w])
+        c, b = R.quantize(w.cpu().numpy(), R.MX)
+        y = link.matmul(0, x, torch.float32, torch.tensor(off, dtype=torch.int32, device="cuda"))
+        ref, size = R.product(f64(x), R.unit_values(c, b, 64, R.MX), off)
+        assert (np.abs(f64(y) - ref) <= bound(size, ref, 64, "fp32")).all()
+        w = w * 1.01
