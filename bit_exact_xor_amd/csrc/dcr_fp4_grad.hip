@@ -19,7 +19,8 @@ constexpr uint32_t kRowB = kBJ * 2;      // bytes of a row of dy in LDS
 // different banks
 __device__ __forceinline__ uint32_t turn(uint32_t j) { return (j & 3u) | ((j >> 1) & 4u); }
 
-template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BO, uint32_t WM, uint32_t WN>
+// ALIGNED: rows of dy and codes on 16-byte borders, a sum of a multiple of 8
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BO, uint32_t WM, uint32_t WN, bool ALIGNED>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BO / WN / 16;
     constexpr uint32_t XD = BM / 8 / W;          // 1 KiB loads of dy of a wave and step
@@ -142,7 +143,36 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    if (first < steps) {
+    // a step of any rows: through registers, with bounds
+    auto load_any = [&](uint8_t* buf, uint32_t step) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < XD; ++i) {
+            const uint32_t r = lr + i * W * 8;
+            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride;
+            *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = bf16x8_any(p, step * kBJ + lc * 8, a.n);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < PP; ++i) {
+            const uint32_t j = step * kBJ + row0 + i * RP, c = blk * 16;   // (columns from o0 on)
+            q[i] = u32x2{0, 0};
+            sc[i] = 0;
+            if (j < a.n && o0 + c < a.k) {
+                q[i] = codes16(wb + uint64_t(j) * wstep, c, a.k - o0, a.w_vec);
+                sc[i] = sb[uint64_t(j) * sstep + c / fp4_block(WF)];
+            }
+        }
+    };
+    if constexpr (!ALIGNED) {
+#pragma unroll 1
+        for (uint32_t t = first; t < steps; ++t) {
+            __syncthreads();
+            load_any(buf0, t);
+            convert(buf0);
+            __syncthreads();
+            compute(buf0);
+        }
+    }
+    if (ALIGNED && first < steps) {
         load_x(buf0, first);
         load_w(first);
         convert(buf0);
@@ -150,7 +180,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
-    for (uint32_t t = first; t < steps; t += 2) {
+    for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
         __syncthreads();
         load_x(buf1, t + 1);
         convert(buf1);
@@ -167,33 +197,37 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
 }
 
 template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
     const dim3 g(a.row_tiles * a.col_tiles * a.splits);
     if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4>), g, dim3(512), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4, true>), g, dim3(512), 0, st, a);
+    else if (bm == 128 && aligned)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2, true>), g, dim3(256), 0, st, a);
+    else if (bm == 64 && aligned)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 64, 128, 1, 4, true>), g, dim3(256), 0, st, a);
+    else if (bm == 32 && aligned)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4, true>), g, dim3(256), 0, st, a);
     else if (bm == 128)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2>), g, dim3(256), 0, st, a);
-    else if (bm == 64)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 64, 128, 1, 4>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2, false>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4, false>), g, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
-    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600};
-    // pieces of dy are eight elements, offsets inside a tile 31 bits
-    if (!a.x_vec || !a.w_vec || a.n % 8 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24))
-        return false;
-    const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, kCost);
+    // offsets inside a tile, and inside the rows of w of a step, are 31 bits
+    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
+    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 5000, 0, 1800};
+    const bool aligned = a.x_vec && a.w_vec && a.n % 8 == 0;
+    const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, aligned ? kCost : kCostAny);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.k, ws);
     const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        wide ? launch<DCR_FP4_MX, float>(p, st, bm) : launch<DCR_FP4_MX, uint16_t>(p, st, bm);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm, aligned) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, aligned);
     else
-        wide ? launch<DCR_FP4_NV, float>(p, st, bm) : launch<DCR_FP4_NV, uint16_t>(p, st, bm);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm, aligned) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, aligned);
     fp4_mm_join(a, a.k, fmt, f32, ws, st);
     return true;
 }

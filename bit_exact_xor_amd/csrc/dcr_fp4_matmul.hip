@@ -242,6 +242,7 @@ uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&c
     uint64_t best = UINT64_MAX;
     uint32_t bm = 0;
     for (uint32_t i = 0; i < 4; ++i) {
+        if (!cost[i]) continue;
         const uint32_t b = 256u >> i, bn = b == 256 ? 256 : 128;
         const uint64_t cols = (uint64_t(outs) + bn - 1) / bn, bound = (a->m + b - 1) / b + (a->offsets ? a->groups : 0);
         // row tiles to expect: groups end inside a tile

@@ -94,6 +94,26 @@ __device__ __forceinline__ u32x2 codes16(const uint8_t* row, uint32_t c0, uint32
     return r;
 }
 
+// 32 codes of a row from element k; zeros from `cols` on
+__device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_t cols, bool vec) {
+    if (vec && k + 32 <= cols) return *reinterpret_cast<const u32x4*>(row + k / 2);
+    const u32x2 a = codes16(row, k, cols, false), b = codes16(row, k + 16, cols, false);
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// eight bf16 of a row from element k, at any alignment; zeros from `cols` on
+__device__ __forceinline__ u32x4 bf16x8_any(const uint16_t* row, uint32_t k, uint32_t cols) {
+    u32x4 v = {0, 0, 0, 0};
+    if (k + 8 <= cols) {
+        __builtin_memcpy(&v, row + k, 16);
+    } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+            if (k + e < cols) v[e / 2] |= uint32_t(row[k + e]) << (16 * (e & 1));
+    }
+    return v;
+}
+
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
@@ -246,7 +266,7 @@ bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
 // Chooses the tiling of a product with `outs` columns of results and `steps`
 // steps of the sum, and fills in the grid; steps' costs in cycles of a compute
 // unit by rows of a tile (256, 128, 64, 32).  Returns bm, 0 if no grid fits.
-uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]);
+uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]);   // (0: not that one)
 // With a->splits > 1: points a copy's y at the scratch, and joins the parts.
 MArgs fp4_mm_parts(const MArgs& a, uint32_t outs, void* ws);
 void fp4_mm_join(const MArgs& a, uint32_t outs, uint32_t fmt, bool f32, const void* ws, hipStream_t st);

@@ -25,13 +25,6 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t r) {
     return (r & 3u) | ((r >> 1) & 4u) | (((r >> 3) ^ (r >> 2)) & 1u) << 3;
 }
 
-// 32 codes of a row from element k; zeros from `cols` on
-__device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_t cols, bool vec) {
-    if (vec && k + 32 <= cols) return *reinterpret_cast<const u32x4*>(row + k / 2);
-    const u32x2 a = codes16(row, k, cols, false), b = codes16(row, k + 16, cols, false);
-    return u32x4{a[0], a[1], b[0], b[1]};
-}
-
 // What is known of the rows: nothing; x and codes on 16-byte borders and a sum
 // of whole MX blocks; and scales of two steps at a time on borders of their
 // own (then one load for 16 rows brings two steps' scales: a load costs as
@@ -158,15 +151,8 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         for (uint32_t i = 0; i < DMA; ++i) {
             const uint32_t r = (i * W + wave) * 4 + quad;
             const uint32_t k = step * kBK + (r16 ^ swizzle(r)) * 8;
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride + k;
-            u32x4 v = {0, 0, 0, 0};
-            if (k + 8 <= a.k) {
-                __builtin_memcpy(&v, p, 16);
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    if (k + e < a.k) v[e / 2] |= uint32_t(p[e]) << (16 * (e & 1));
-            }
+            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride;
+            const u32x4 v = bf16x8_any(p, k, a.k);
             *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = v;
         }
     };

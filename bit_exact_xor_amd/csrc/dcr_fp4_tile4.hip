@@ -12,8 +12,13 @@ namespace {
 constexpr uint32_t kBK = 256;                // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
 
-template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool SV>
+// What is known of the rows: nothing; codes on 16-byte borders and a sum of
+// whole blocks; and eight scales at a time on 8-byte borders.
+enum class Rows { kAny, kAligned, kScales };
+
+template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, Rows ROWS>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) {
+    constexpr bool SV = ROWS == Rows::kScales;
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
     constexpr uint32_t XD = BM / 8 / W, WD = BN / 8 / W;   // 1 KiB loads of a wave and step
     static_assert(W * 64 >= BM + BN && BM % 64 == 0, "a thread stages the scales of one row, a wave those of one operand");
@@ -31,8 +36,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint8_t* wb = a.wc + (uint64_t(rt.group) * a.n + n0) * a.wc_stride;
     const uint8_t* sb = a.ws + (uint64_t(rt.group) * a.n + n0) * a.ws_stride;
     const uint32_t xstep = uint32_t(a.x_stride), wstep = uint32_t(a.wc_stride);
-    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride, (rows - 1) * xstep + a.k / 2);
-    const auto wr = rsrc(wb, (cols - 1) * wstep + a.k / 2);
+    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride, (rows - 1) * xstep + (a.k + 1) / 2);
+    const auto wr = rsrc(wb, (cols - 1) * wstep + (a.k + 1) / 2);
 
     // the row whose scales this thread stages (x's, then w's), and where they
     // go: [quarter of the step][quad][row of a subtile][subtile], so that a
@@ -40,7 +45,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const bool xside = wave < BM / 64;      // whole waves: the descriptor stays scalar
     const uint32_t srow = xside ? threadIdx.x : (threadIdx.x - BM) % BN;   // (spare threads do one over)
     const uint32_t last = (xside ? rows : cols) - 1;
-    const uint32_t sstep = uint32_t(xside ? a.xs_stride : a.ws_stride), blocks = a.k / 32;
+    const uint32_t sstep = uint32_t(xside ? a.xs_stride : a.ws_stride), blocks = (a.k + 31) / 32;
     const auto sr = rsrc(xside ? a.xs + rt.begin * a.xs_stride : sb, last * sstep + blocks);
     const uint32_t soff = min(srow, last) * sstep;
     const uint32_t subs = xside ? BM / 16 : BN / 16;
@@ -61,6 +66,20 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
     for (uint32_t i = 0; i < WD; ++i) wo[i] = min(lr + i * W * 8, cols - 1) * wstep + lc * 16;
     auto load = [&](uint8_t* buf, uint32_t step) {
+        if constexpr (ROWS == Rows::kAny) {
+            // any rows: through registers, zeros past the row's end
+            const uint32_t k = step * kBK + lc * 32;
+            const uint8_t* x = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride;
+#pragma unroll 1
+            for (uint32_t i = 0; i < XD; ++i)
+                *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) =
+                    codes32(x + uint64_t(min(lr + i * W * 8, rows - 1)) * xstep, k, a.k, a.x_vec);
+#pragma unroll 1
+            for (uint32_t i = 0; i < WD; ++i)
+                *reinterpret_cast<u32x4*>(buf + BM * kRowB + (i * W + wave) * 1024 + lane * 16) =
+                    codes32(wb + uint64_t(min(lr + i * W * 8, cols - 1)) * wstep, k, a.k, a.w_vec);
+            return;
+        }
         if ((step + 1) * kBK > a.k) {
             const uint32_t out = step * kBK + lc * 32 < a.k ? 0u : kOutside;
 #pragma unroll
@@ -141,13 +160,23 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    if (first < steps) {
+    if constexpr (ROWS == Rows::kAny) {
+#pragma unroll 1
+        for (uint32_t t = first; t < steps; ++t) {
+            __syncthreads();
+            load(buf0, t);
+            store_scales(buf0, load_scales(t));
+            __syncthreads();
+            compute(buf0);
+        }
+    }
+    if (ROWS != Rows::kAny && first < steps) {
         load(buf0, first);
         store_scales(buf0, load_scales(first));
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
-    for (uint32_t t = first; t < steps; t += 2) {
+    for (uint32_t t = first; ROWS != Rows::kAny && t < steps; t += 2) {
         __syncthreads();
         load(buf1, t + 1);
         const u32x2 s1 = load_scales(t + 1);
@@ -162,35 +191,40 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     store_block<OUT, BM, BN, W, WM, kCodes>(a, acc, 1.0f, rt, at, wm, wn * (BN / WN), a.n, buf0, buf1);
 }
 
-template <typename OUT, bool SV>
+template <typename OUT, Rows ROWS>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
     const dim3 g(a.row_tiles * a.col_tiles * a.splits);
-    if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, SV>), g, dim3(512), 0, st, a);
+    if (ROWS != Rows::kAny && bm == 256)
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, ROWS == Rows::kAny ? Rows::kAligned : ROWS>), g, dim3(512), 0, st, a);
     else if (bm == 128)
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2, SV>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 128, 128, 2, 2, ROWS>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 64, 128, 1, 4, SV>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 64, 128, 1, 4, ROWS>), g, dim3(256), 0, st, a);
+}
+template <typename OUT>
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
+    if (rows == Rows::kAny)
+        launch<OUT, Rows::kAny>(a, st, bm);
+    else if (rows == Rows::kAligned)
+        launch<OUT, Rows::kAligned>(a, st, bm);
+    else
+        launch<OUT, Rows::kScales>(a, st, bm);
 }
 
 }  // namespace
 
 bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
-    constexpr uint32_t kCost[4] = {4800, 1600, 1000, UINT32_MAX};
-    // pieces are whole blocks, offsets inside a tile 31 bits
-    if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) ||
-        a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
+    // offsets inside a tile are 31 bits
+    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
-    // whole steps of scales at 8-byte borders: one load each
-    const bool sv = a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0;
-    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, kCost);
+    const Rows rows = !a.x_vec || !a.w_vec || a.k % 32                                        ? Rows::kAny
+                      : a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0 ? Rows::kScales
+                                                                                               : Rows::kAligned;
+    constexpr uint32_t kCost[4] = {4800, 1600, 1000, 0}, kCostAny[4] = {0, 6000, 3500, 0};
+    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, rows == Rows::kAny ? kCostAny : kCost);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);
-    const bool wide = f32 || a.splits > 1;
-    if (sv)
-        wide ? launch<float, true>(p, st, bm) : launch<uint16_t, true>(p, st, bm);
-    else
-        wide ? launch<float, false>(p, st, bm) : launch<uint16_t, false>(p, st, bm);
+    f32 || a.splits > 1 ? launch<float>(p, st, bm, rows) : launch<uint16_t>(p, st, bm, rows);
     fp4_mm_join(a, a.n, DCR_FP4_MX, f32, ws, st);
     return true;
 }
