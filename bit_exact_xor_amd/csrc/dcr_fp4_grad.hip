@@ -143,13 +143,14 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    // a step of any rows: through registers, with bounds
-    auto load_any = [&](uint8_t* buf, uint32_t step) {
-#pragma unroll 1
+    // Any step, any alignment: into registers while the step before multiplies
+    // (zeros past the ends), then to LDS.
+    u32x4 xn[XD];
+    auto fetch = [&](uint32_t step) {
+#pragma unroll
         for (uint32_t i = 0; i < XD; ++i) {
-            const uint32_t r = lr + i * W * 8;
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride;
-            *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = bf16x8_any(p, step * kBJ + lc * 8, a.n);
+            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(lr + i * W * 8, rows - 1)) * a.x_stride;
+            xn[i] = bf16x8_any(p, step * kBJ + lc * 8, a.n);
         }
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
@@ -163,12 +164,15 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         }
     };
     if constexpr (!ALIGNED) {
+        fetch(first);
 #pragma unroll 1
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
-            load_any(buf0, t);
+#pragma unroll
+            for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(buf0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
             convert(buf0);
             __syncthreads();
+            fetch(t + 1);   // (past the last: zeros)
             compute(buf0);
         }
     }
@@ -218,7 +222,7 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile, and inside the rows of w of a step, are 31 bits
     if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
-    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 5000, 0, 1800};
+    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 2000, 0, 900};
     const bool aligned = a.x_vec && a.w_vec && a.n % 8 == 0;
     const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, aligned ? kCost : kCostAny);
     if (!bm) return false;

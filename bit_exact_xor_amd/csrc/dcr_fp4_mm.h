@@ -242,8 +242,8 @@ __device__ __forceinline__ void store_block(const MArgs& a, const f32x4 (&acc)[N
             const uint32_t r = WM == 1 ? p * RP + i * RI + row_in : (up ? BM / 2 : 0) + p * RPW + lr;
             if (r >= rows) continue;
             OUT* out = y + (rt.begin + r) * a.y_stride + col;
-            if (a.y_vec && col + E <= outs) {
-                *reinterpret_cast<u32x4*>(out) = v;
+            if (col + E <= outs) {
+                __builtin_memcpy(out, &v, 16);   // (at any alignment)
             } else {
 #pragma unroll
                 for (uint32_t e = 0; e < E; ++e)

@@ -133,28 +133,35 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         for (uint32_t i = 0; i < DMA; ++i)
             load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
     };
-    // any step, any alignment: x through registers, zeros past the row's end
-    auto load_any = [&](uint8_t* buf, uint32_t step) {
+    // Any step, any alignment: into registers while the step before multiplies
+    // (zeros past the row's end), then to LDS.
+    u32x4 xn[DMA], wn[NI];
+    uint32_t sn[NI];
+    auto fetch = [&](uint32_t step) {
         const uint32_t kw = step * kBK + quad * 32;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
-            wq[i] = u32x4{0, 0, 0, 0};
-            wsc[i] = 0;
+            wn[i] = u32x4{0, 0, 0, 0};
+            sn[i] = 0;
             if (kw < a.k) {
-                wq[i] = codes32(wb + wo[i] - quad * 16, kw, a.k, a.w_vec);
+                wn[i] = codes32(wb + wo[i] - quad * 16, kw, a.k, a.w_vec);
                 const uint8_t* s = sb + step * (kBK / fp4_block(WF)) + so[i];
-                wsc[i] = s[0];
-                if (WF == DCR_FP4_NV && kw + 16 < a.k) wsc[i] |= uint32_t(s[1]) << 8;
+                sn[i] = s[0];
+                if (WF == DCR_FP4_NV && kw + 16 < a.k) sn[i] |= uint32_t(s[1]) << 8;
             }
         }
-#pragma unroll 1
+#pragma unroll
         for (uint32_t i = 0; i < DMA; ++i) {
             const uint32_t r = (i * W + wave) * 4 + quad;
-            const uint32_t k = step * kBK + (r16 ^ swizzle(r)) * 8;
             const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride;
-            const u32x4 v = bf16x8_any(p, k, a.k);
-            *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = v;
+            xn[i] = bf16x8_any(p, step * kBK + (r16 ^ swizzle(r)) * 8, a.k);
         }
+    };
+    auto put = [&](uint8_t* buf) {
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) wq[i] = wn[i], wsc[i] = sn[i];
+#pragma unroll
+        for (uint32_t i = 0; i < DMA; ++i) *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = xn[i];
     };
     auto convert = [&](uint32_t j, uint32_t i) {
         w[j & 1][i] =
@@ -227,11 +234,13 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             compute(buf1, t + 2, odd);
         }
     } else {
+        fetch(first);
 #pragma unroll 1
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
-            load_any(buf0, t);
+            put(buf0);
             __syncthreads();
+            fetch(t + 1);   // (past the last: zeros)
             compute(buf0, 0, even);
         }
     }
@@ -243,8 +252,8 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 template <uint32_t WF, typename OUT, Rows ROWS>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
     const dim3 g(a.row_tiles * a.col_tiles * a.splits);
-    if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ROWS>), g, dim3(512), 0, st, a);
+    if (ROWS != Rows::kAny && bm == 256)
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ROWS == Rows::kAny ? Rows::kAligned : ROWS>), g, dim3(512), 0, st, a);
     else if (bm == 128)
         hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ROWS>), g, dim3(256), 0, st, a);
     else if (bm == 64)
@@ -253,8 +262,8 @@ void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
         hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 32, 128, 4, ROWS>), g, dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
-    if (!a.x_vec || !a.w_vec || a.k % 32)
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
+    if (!aligned)
         launch_tile<WF, OUT, Rows::kAny>(a, st, bm);
     else if (a.k % 256 == 0 && a.ws_stride % (256 / fp4_block(WF)) == 0)
         launch_tile<WF, OUT, Rows::kPaired>(a, st, bm);
@@ -265,17 +274,18 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
 }  // namespace
 
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
-    constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800};
+    constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostAny[4] = {0, 2800, 1700, 1100};
+    const bool aligned = a.x_vec && a.w_vec && a.k % 32 == 0;
     // offsets inside a tile are 31 bits
     if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
-    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, kCost);
+    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, aligned ? kCost : kCostAny);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);
     const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        wide ? launch<DCR_FP4_MX, float>(p, st, bm) : launch<DCR_FP4_MX, uint16_t>(p, st, bm);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm, aligned) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, aligned);
     else
-        wide ? launch<DCR_FP4_NV, float>(p, st, bm) : launch<DCR_FP4_NV, uint16_t>(p, st, bm);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm, aligned) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, aligned);
     fp4_mm_join(a, a.n, fmt, f32, ws, st);
     return true;
 }

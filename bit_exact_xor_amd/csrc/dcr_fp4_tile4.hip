@@ -66,20 +66,6 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
     for (uint32_t i = 0; i < WD; ++i) wo[i] = min(lr + i * W * 8, cols - 1) * wstep + lc * 16;
     auto load = [&](uint8_t* buf, uint32_t step) {
-        if constexpr (ROWS == Rows::kAny) {
-            // any rows: through registers, zeros past the row's end
-            const uint32_t k = step * kBK + lc * 32;
-            const uint8_t* x = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride;
-#pragma unroll 1
-            for (uint32_t i = 0; i < XD; ++i)
-                *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) =
-                    codes32(x + uint64_t(min(lr + i * W * 8, rows - 1)) * xstep, k, a.k, a.x_vec);
-#pragma unroll 1
-            for (uint32_t i = 0; i < WD; ++i)
-                *reinterpret_cast<u32x4*>(buf + BM * kRowB + (i * W + wave) * 1024 + lane * 16) =
-                    codes32(wb + uint64_t(min(lr + i * W * 8, cols - 1)) * wstep, k, a.k, a.w_vec);
-            return;
-        }
         if ((step + 1) * kBK > a.k) {
             const uint32_t out = step * kBK + lc * 32 < a.k ? 0u : kOutside;
 #pragma unroll
@@ -160,13 +146,32 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
+    // Any step, any alignment: into registers while the step before multiplies
+    // (zeros past the rows' ends), then to LDS.
+    u32x4 xnext[XD], wnext[WD];
+    u32x2 sn;
+    auto fetch = [&](uint32_t step) {
+        const uint32_t k = step * kBK + lc * 32;
+        const uint8_t* x = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride;
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i) xnext[i] = codes32(x + uint64_t(min(lr + i * W * 8, rows - 1)) * xstep, k, a.k, a.x_vec);
+#pragma unroll
+        for (uint32_t i = 0; i < WD; ++i) wnext[i] = codes32(wb + uint64_t(min(lr + i * W * 8, cols - 1)) * wstep, k, a.k, a.w_vec);
+        sn = load_scales(step);
+    };
     if constexpr (ROWS == Rows::kAny) {
+        fetch(first);
 #pragma unroll 1
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
-            load(buf0, t);
-            store_scales(buf0, load_scales(t));
+#pragma unroll
+            for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(buf0 + (i * W + wave) * 1024 + lane * 16) = xnext[i];
+#pragma unroll
+            for (uint32_t i = 0; i < WD; ++i)
+                *reinterpret_cast<u32x4*>(buf0 + BM * kRowB + (i * W + wave) * 1024 + lane * 16) = wnext[i];
+            store_scales(buf0, sn);
             __syncthreads();
+            fetch(t + 1);   // (past the last: zeros)
             compute(buf0);
         }
     }
@@ -220,7 +225,7 @@ bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
     const Rows rows = !a.x_vec || !a.w_vec || a.k % 32                                        ? Rows::kAny
                       : a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0 ? Rows::kScales
                                                                                                : Rows::kAligned;
-    constexpr uint32_t kCost[4] = {4800, 1600, 1000, 0}, kCostAny[4] = {0, 6000, 3500, 0};
+    constexpr uint32_t kCost[4] = {4800, 1600, 1000, 0}, kCostAny[4] = {0, 3000, 1800, 0};
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, rows == Rows::kAny ? kCostAny : kCost);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);
