@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
     const TilePlace at = tile_place(a);
+    if (at.row >= a.row_tiles) return;
     const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), o0 = at.col * BO;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
 
 template <uint32_t WF, typename OUT>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
-    const dim3 g(a.row_tiles * a.col_tiles * a.splits);
+    const dim3 g(a.grid);
     if (bm == 256)
         hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4, true>), g, dim3(512), 0, st, a);
     else if (bm == 128 && aligned)

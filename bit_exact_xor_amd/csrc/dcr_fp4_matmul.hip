@@ -262,6 +262,13 @@ uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&c
             a->split_steps = uint32_t(each);
         }
     }
+    if (!bm) return 0;
+    // Without groups an eighth of the tiles a die.  A grid for groups has spare
+    // row tiles at its end: dies take strips of four row tiles in turn, which
+    // spreads them.
+    const uint32_t all = a->row_tiles * a->col_tiles * a->splits;
+    a->chunk = a->offsets && a->row_tiles >= 64 ? 4 * a->col_tiles * a->splits : a->offsets ? a->splits : (all + 7) / 8;
+    a->grid = (all + 8 * a->chunk - 1) / (8 * a->chunk) * 8 * a->chunk;
     a->split_elems = a->splits > 1 ? a->m * stride : 0;
     return bm;
 }

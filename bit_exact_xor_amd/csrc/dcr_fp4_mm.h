@@ -23,6 +23,7 @@ struct MArgs {
     uint32_t x_vec, w_vec;      // rows of x / codes of w start on 16-byte borders
     uint32_t y_vec;             // rows of y start on 16-byte borders
     uint32_t row_tiles, col_tiles;   // upper bounds of the grid
+    uint32_t chunk, grid;            // neighbouring workgroups of one compute die; workgroups
     uint32_t splits, split_steps;    // parts of the sum, steps of a part (even)
     uint64_t split_elems;            // results of a part (y is then fp32 scratch)
 };
@@ -170,20 +171,22 @@ __device__ __forceinline__ void held(f32x4& v) {
 #endif
 }
 
-// Row and column tile of a workgroup, and its steps of the sum.  The eight
-// compute dies take workgroups in turn: each gets a run of tiles, walked four
-// row tiles at a time, so that its L2 serves a block of both operands.
+// Row and column tile of a workgroup, and its part of the sum.  The eight
+// compute dies take workgroups in turn: each gets runs of `chunk` neighbouring
+// tiles, walked four row tiles at a time, so that its L2 serves a block of
+// both operands.
 struct TilePlace {
     uint32_t row, col, split;
 };
 __device__ __forceinline__ TilePlace tile_place(const MArgs& a) {
-    uint32_t id = blockIdx.x;
-    const uint32_t all = a.row_tiles * a.col_tiles * a.splits, per = all / 8;
-    if (id < per * 8) id = (id & 7u) * per + (id >> 3);
+    const uint32_t die = blockIdx.x & 7u, local = blockIdx.x >> 3, turn = local / a.chunk;
+    const uint32_t id = (turn * 8 + die) * a.chunk + (local - turn * a.chunk);
     const uint32_t tile = id / a.splits, split = id - tile * a.splits;
     constexpr uint32_t SM = 4;
     const uint32_t strip = tile / (SM * a.col_tiles), in = tile - strip * SM * a.col_tiles;
+    if (strip * SM >= a.row_tiles) return {a.row_tiles, 0, 0};     // (the grid is whole chunks)
     const uint32_t sm = min(SM, a.row_tiles - strip * SM);
+    if (in >= sm * a.col_tiles) return {a.row_tiles, 0, 0};
     return {strip * SM + in % sm, in / sm, split};
 }
 

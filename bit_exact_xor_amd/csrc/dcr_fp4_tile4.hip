@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
     const TilePlace at = tile_place(a);
+    if (at.row >= a.row_tiles) return;
     const RowTile rt = row_tile<BM>(a, at.row);
     if (rt.begin == rt.end) return;
     const uint32_t rows = uint32_t(rt.end - rt.begin), n0 = at.col * BN, cols = min(BN, a.n - n0);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 
 template <typename OUT, Rows ROWS>
 void launch(const MArgs& a, hipStream_t st, uint32_t bm) {
-    const dim3 g(a.row_tiles * a.col_tiles * a.splits);
+    const dim3 g(a.grid);
     if (ROWS != Rows::kAny && bm == 256)
         hipLaunchKernelGGL((fp4_mm_tile4_kernel<OUT, 256, 256, 2, 4, ROWS == Rows::kAny ? Rows::kAligned : ROWS>), g, dim3(512), 0, st, a);
     else if (bm == 128)
