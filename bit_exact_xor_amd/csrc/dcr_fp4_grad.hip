@@ -185,18 +185,21 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
+    // (the codes are converted before the next loads are issued: a wait for them
+    // would be a wait for those too)
     for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
-        __syncthreads();
-        load_x(buf1, t + 1);
+        step_barrier<2 * PP>();   // dy is older than the last loads of codes and scales
         convert(buf1);
+        load_x(buf1, t + 1);
         load_w(t + 2);
         compute(buf0);
-        __syncthreads();
-        load_x(buf0, t + 2);
+        step_barrier<2 * PP>();
         convert(buf0);
+        load_x(buf0, t + 2);
         load_w(t + 3);
         compute(buf1);
     }
+    step_barrier<0>();
     store_block<OUT, BM, BO, W, WM, kX + kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
                                              wn * (BO / WN), a.k, buf0, buf1);
 }

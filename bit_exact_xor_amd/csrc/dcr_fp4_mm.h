@@ -148,8 +148,10 @@ __device__ __forceinline__ uint32_t swizzle8(uint32_t r) {
     return ((r >> 1) & 3u) | (((r >> 3) ^ (r >> 2)) & 1u) << 2;
 }
 
-// Waits until at most N of this wave's loads are in flight and its LDS reads
-// are done, then for the other waves of the workgroup.
+// Waits until at most N of this wave's loads are in flight (they finish in
+// order) and its LDS accesses are done, then for the other waves of the
+// workgroup.  Loads to LDS are waited for here and nowhere else: a plain
+// workgroup barrier does not cover them.
 template <uint32_t N>
 __device__ __forceinline__ void step_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");

@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const auto sr = rsrc(sb, (wrows - 1) * uint32_t(a.ws_stride) + (a.k + fp4_block(WF) - 1) / fp4_block(WF));
 
     f32x4 acc[NI][MI] = {};
-    u32x4 wq[NI];
-    uint32_t wsc[NI];
+    u32x4 wq[2][NI];
+    uint32_t wsc[2][NI];
     typename std::conditional<WF == DCR_FP4_MX, u32x2, u32x4>::type pair[NI];   // scales of two steps of a row
     bf16x8 w[2][NI];
 
@@ -84,25 +84,29 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     // (at a multiple of 32), lanes past the end read behind the descriptors'
     // range, which gives zeros; a lane once past it stays there, so its offset
     // is changed for good and the other steps spend nothing on it.
-    auto past_end = [&](uint32_t step) {
+    auto x_past_end = [&](uint32_t step) {
         if ((step + 1) * kBK <= a.k) return;
-        const uint32_t xout = step * kBK + (r16 ^ swizzle(wave * 4 + quad)) * 8 < a.k ? 0u : kOutside;
-        const uint32_t wout = step * kBK + quad * 32 < a.k ? 0u : kOutside;
+        const uint32_t out = step * kBK + (r16 ^ swizzle(wave * 4 + quad)) * 8 < a.k ? 0u : kOutside;
 #pragma unroll
-        for (uint32_t i = 0; i < DMA; ++i) xo[i] |= xout;
-#pragma unroll
-        for (uint32_t i = 0; i < NI; ++i) wo[i] |= wout, so[i] |= wout;
+        for (uint32_t i = 0; i < DMA; ++i) xo[i] |= out;
     };
-    auto load_w = [&](uint32_t step) {
+    auto w_past_end = [&](uint32_t step) {
+        if ((step + 1) * kBK <= a.k) return;
+        const uint32_t out = step * kBK + quad * 32 < a.k ? 0u : kOutside;
+#pragma unroll
+        for (uint32_t i = 0; i < NI; ++i) wo[i] |= out, so[i] |= out;
+    };
+    auto load_w = [&](uint32_t step, auto odd) {
+        constexpr uint32_t o = decltype(odd)::value;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
-            wq[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], step * (kBK / 2), 0));
+            wq[o][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, wo[i], step * (kBK / 2), 0));
             if constexpr (PAIRED)
                 continue;
             else if constexpr (WF == DCR_FP4_MX)
-                wsc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], step * (kBK / 32), 0);
+                wsc[o][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], step * (kBK / 32), 0);
             else
-                wsc[i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], step * (kBK / 16), 0);
+                wsc[o][i] = __builtin_amdgcn_raw_buffer_load_b16(sr, so[i], step * (kBK / 16), 0);
         }
     };
     auto load_pair = [&](uint32_t step) {
@@ -124,9 +128,9 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             if constexpr (!PAIRED)
                 continue;
             else if constexpr (WF == DCR_FP4_MX)
-                wsc[i] = (pair[i][o] >> (8 * quad)) & 255u;
+                wsc[o][i] = (pair[i][o] >> (8 * quad)) & 255u;
             else
-                wsc[i] = (quad & 2u ? pair[i][2 * o + 1] : pair[i][2 * o]) >> (16 * (quad & 1u));
+                wsc[o][i] = (quad & 2u ? pair[i][2 * o + 1] : pair[i][2 * o]) >> (16 * (quad & 1u));
         }
     };
     auto load_x = [&](uint8_t* buf, uint32_t step) {
@@ -160,18 +164,19 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     };
     auto put = [&](uint8_t* buf) {
 #pragma unroll
-        for (uint32_t i = 0; i < NI; ++i) wq[i] = wn[i], wsc[i] = sn[i];
+        for (uint32_t i = 0; i < NI; ++i) wq[0][i] = wn[i], wsc[0][i] = sn[i];
 #pragma unroll
         for (uint32_t i = 0; i < DMA; ++i) *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = xn[i];
     };
-    auto convert = [&](uint32_t j, uint32_t i) {
-        w[j & 1][i] =
-            fp4_unpack8_bf16<WF>(wq[i][j], WF == DCR_FP4_MX ? wsc[i] : (wsc[i] >> (j / 2 * 8)) & 255u);
+    auto convert = [&](auto odd, uint32_t j, uint32_t i) {
+        constexpr uint32_t o = decltype(odd)::value;
+        w[j & 1][i] = fp4_unpack8_bf16<WF>(wq[o][i][j], WF == DCR_FP4_MX ? wsc[o][i] : (wsc[o][i] >> (j / 2 * 8)) & 255u);
     };
     // A step's products, four row subtiles at a time.  While these multiply,
     // the next four are read from LDS and part of the
     // next quarter's codes is converted.  The codes' registers are free once the
-    // last quarter is converted, and take the next step's then.
+    // last quarter is converted, and take those of the step after the next then:
+    // they may come from HBM.
     auto compute = [&](const uint8_t* buf, uint32_t next, auto odd) {
         constexpr uint32_t H = MI < 4 ? MI : 4, P = MI / H, C = (NI + P - 1) / P;   // C subtiles of codes a phase
         const uint8_t* xl = buf + r16 * kRowB;
@@ -183,6 +188,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
                                                                 (((quad * 4 + ph / P) ^ swizzle(r16)) * 16));
         };
         from_pair(odd);
+        if (decltype(odd)::value) load_pair(next);
         read(0);
 #pragma unroll
         for (uint32_t ph = 0; ph < 4 * P; ++ph) {
@@ -190,14 +196,13 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             if (ph + 1 < 4 * P) read(ph + 1);
             if (ph == 0)
 #pragma unroll
-                for (uint32_t i = 0; i < NI; ++i) convert(0, i);
+                for (uint32_t i = 0; i < NI; ++i) convert(odd, 0, i);
             if (ALIGNED && ph == 3 * P) {
-                load_w(next);
-                if (decltype(odd)::value) load_pair(next);
+                load_w(next + 1, odd);
             }
             if (j < 3)
 #pragma unroll
-                for (uint32_t i = ph % P * C; i < (ph % P + 1) * C && i < NI; ++i) convert(j + 1, i);
+                for (uint32_t i = ph % P * C; i < (ph % P + 1) * C && i < NI; ++i) convert(odd, j + 1, i);
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
 #pragma unroll
@@ -217,21 +222,26 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const std::integral_constant<uint32_t, 1> odd;
     if constexpr (ALIGNED) {
         if (first < steps) {
-            past_end(first);
+            x_past_end(first);
             load_x(buf0, first);
-            load_w(first);
+            w_past_end(first);
+            load_w(first, even);
             load_pair(first);
+            w_past_end(first + 1);
+            load_w(first + 1, odd);
         }
         // two steps a turn (one loop exit keeps the sums in their registers);
         // a step past the last is all zeros
         for (uint32_t t = first; t < steps; t += 2) {
-            __syncthreads();
-            past_end(t + 1);
+            step_barrier<2 * NI>();   // x is older than the last loads of codes and scales
+            x_past_end(t + 1);
             load_x(buf1, t + 1);
+            w_past_end(t + 2);
             compute(buf0, t + 1, even);
-            __syncthreads();
-            past_end(t + 2);
+            step_barrier<PAIRED ? NI : 2 * NI>();
+            x_past_end(t + 2);
             load_x(buf0, t + 2);
+            w_past_end(t + 3);
             compute(buf1, t + 2, odd);
         }
     } else {
@@ -246,6 +256,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         }
     }
 
+    step_barrier<0>();
     store_block<OUT, BM, BN, W, 1, BM * kRowB>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, 0,
                                                wave * (BN / W), a.n, buf0, buf1);
 }

@@ -183,17 +183,18 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
     for (uint32_t t = first; ROWS != Rows::kAny && t < steps; t += 2) {
-        __syncthreads();
+        step_barrier<0>();
         load(buf1, t + 1);
         const u32x2 s1 = load_scales(t + 1);
         compute(buf0);
         store_scales(buf1, s1);
-        __syncthreads();
+        step_barrier<0>();
         load(buf0, t + 2);
         const u32x2 s2 = load_scales(t + 2);
         compute(buf1);
         store_scales(buf0, s2);
     }
+    step_barrier<0>();
     store_block<OUT, BM, BN, W, WM, kCodes>(a, acc, 1.0f, rt, at, wm, wn * (BN / WN), a.n, buf0, buf1);
 }
 
