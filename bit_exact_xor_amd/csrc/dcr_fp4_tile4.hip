@@ -24,7 +24,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     static_assert(W * 64 >= BM + BN && BM % 64 == 0, "a thread stages the scales of one row, a wave those of one operand");
     static_assert(MI % 4 == 0 && (NI % 4 == 0 || NI == 2), "a subtile's scale byte is its index mod 4");
     constexpr uint32_t kCodes = (BM + BN) * kRowB, kScales = (BM + BN) * (kBK / 32);
-    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kCodes + kScales], buf1[kCodes + kScales];
+    // (scales apart from what loads to LDS write: the compiler takes a read of
+    // the same array for one of what is still on its way, and waits)
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kCodes], buf1[kCodes];
+    __shared__ __attribute__((aligned(16))) uint8_t sc0[kScales], sc1[kScales];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
@@ -50,7 +53,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const auto sr = rsrc(xside ? a.xs + rt.begin * a.xs_stride : sb, last * sstep + blocks);
     const uint32_t soff = min(srow, last) * sstep;
     const uint32_t subs = xside ? BM / 16 : BN / 16;
-    const uint32_t sdst = kCodes + (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
+    const uint32_t sdst = (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
 
     f32x4 acc[NI][MI] = {};
     // this workgroup's steps: from `first` on, up to `steps`
@@ -95,11 +98,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         }
         return v;
     };
-    auto store_scales = [&](uint8_t* buf, u32x2 v) {
+    auto store_scales = [&](uint8_t* sc, u32x2 v) {
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) buf[sdst + i * 16 * subs] = uint8_t(v[i / 4] >> (8 * (i & 3)));
+        for (uint32_t i = 0; i < 8; ++i) sc[sdst + i * 16 * subs] = uint8_t(v[i / 4] >> (8 * (i & 3)));
     };
-    auto compute = [&](const uint8_t* buf) {
+    auto compute = [&](const uint8_t* buf, const uint8_t* sc) {
         constexpr uint32_t H = 2, P = MI / H;
         const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
         const uint8_t* wl = buf + BM * kRowB + (wn * (BN / WN) + r16) * kRowB;
@@ -116,8 +119,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         for (uint32_t ph = 0; ph < 2 * P; ++ph) {
             const uint32_t j = ph / P;
             if (ph % P == 0) {
-                const uint8_t* s = buf + kCodes + (j * 4 + quad) * 16 * (BM / 16) + r16 * (BM / 16) + wm * MI;
-                const uint8_t* t = buf + kCodes + BM * (kBK / 32) + (j * 4 + quad) * 16 * (BN / 16) + r16 * (BN / 16) + wn * NI;
+                const uint8_t* s = sc + (j * 4 + quad) * 16 * (BM / 16) + r16 * (BM / 16) + wm * MI;
+                const uint8_t* t = sc + BM * (kBK / 32) + (j * 4 + quad) * 16 * (BN / 16) + r16 * (BN / 16) + wn * NI;
 #pragma unroll
                 for (uint32_t i = 0; i < MI / 4; ++i) xs[i] = *reinterpret_cast<const uint32_t*>(s + i * 4);
                 if constexpr (NI % 4 == 0) {
@@ -170,15 +173,15 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
             for (uint32_t i = 0; i < WD; ++i)
                 *reinterpret_cast<u32x4*>(buf0 + BM * kRowB + (i * W + wave) * 1024 + lane * 16) = wnext[i];
-            store_scales(buf0, sn);
+            store_scales(sc0, sn);
             __syncthreads();
             fetch(t + 1);   // (past the last: zeros)
-            compute(buf0);
+            compute(buf0, sc0);
         }
     }
     if (ROWS != Rows::kAny && first < steps) {
         load(buf0, first);
-        store_scales(buf0, load_scales(first));
+        store_scales(sc0, load_scales(first));
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
@@ -186,13 +189,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         step_barrier<0>();
         load(buf1, t + 1);
         const u32x2 s1 = load_scales(t + 1);
-        compute(buf0);
-        store_scales(buf1, s1);
+        compute(buf0, sc0);
+        store_scales(sc1, s1);
         step_barrier<0>();
         load(buf0, t + 2);
         const u32x2 s2 = load_scales(t + 2);
-        compute(buf1);
-        store_scales(buf0, s2);
+        compute(buf1, sc1);
+        store_scales(sc0, s2);
     }
     step_barrier<0>();
     store_block<OUT, BM, BN, W, WM, kCodes>(a, acc, 1.0f, rt, at, wm, wn * (BN / WN), a.n, buf0, buf1);
