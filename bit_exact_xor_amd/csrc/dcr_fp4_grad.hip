@@ -27,7 +27,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     constexpr uint32_t NB = BO / 16, PP = NB / W;   // blocks of a row of w; of a thread and step
     constexpr uint32_t RP = W * 64 / NB;         // rows of w between a thread's blocks
     constexpr uint32_t kX = BM * kRowB, kW = kBJ * BO * 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kX + kW], buf1[kX + kW];
+    // (w apart from what loads to LDS write: the compiler takes a read of the
+    // same array for one of what is still on its way, and waits)
+    __shared__ __attribute__((aligned(1024))) uint8_t x0[kX], x1[kX], w0[kW], w1[kW];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r16 = lane & 15u, quad = lane >> 4;
     const uint32_t wm = wave % WM, wn = wave / WM;
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     const uint32_t wlast = ((a.k + 1) / 2 - o0 / 2 + 7) & ~7u, slast = (a.k + fp4_block(WF) - 1) / fp4_block(WF) - o0 / fp4_block(WF);
 
     const uint32_t blk = threadIdx.x % NB, row0 = threadIdx.x / NB;
-    const uint32_t wdst = kX + row0 * BO * 2;
+    const uint32_t wdst = row0 * BO * 2;
     u32x2 q[PP];
     uint32_t sc[PP];
     f32x4 acc[NI][MI] = {};
@@ -96,21 +98,21 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             sc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], 0, 0);
         }
     };
-    auto convert = [&](uint8_t* buf) {
+    auto convert = [&](uint8_t* wl) {
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
             const uint32_t r = row0 + i * RP;
-            uint8_t* dst = buf + wdst + i * RP * BO * 2 + (blk ^ turn(r)) * 32;
+            uint8_t* dst = wl + wdst + i * RP * BO * 2 + (blk ^ turn(r)) * 32;
             *reinterpret_cast<bf16x8*>(dst) = fp4_unpack8_bf16<WF>(q[i][0], sc[i]);
             *reinterpret_cast<bf16x8*>(dst + 16) = fp4_unpack8_bf16<WF>(q[i][1], sc[i]);
         }
     };
-    auto compute = [&](const uint8_t* buf) {
+    auto compute = [&](const uint8_t* xbuf, const uint8_t* wbuf) {
         constexpr uint32_t H = 2, P = MI / H;
-        const uint8_t* xl = buf + (wm * (BM / WM) + r16) * kRowB;
+        const uint8_t* xl = xbuf + (wm * (BM / WM) + r16) * kRowB;
         // a lane names four columns of a row and gets four rows of a column
         const uint32_t jr = quad * 8 + (r16 >> 2);
-        const uint8_t* wl = buf + kX + jr * BO * 2 + (r16 & 3u) * 8;
+        const uint8_t* wl = wbuf + jr * BO * 2 + (r16 & 3u) * 8;
         bf16x8 x[2][H], w[NI];
         auto read = [&](uint32_t ph) {
 #pragma unroll
@@ -170,17 +172,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
 #pragma unroll
-            for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(buf0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
-            convert(buf0);
+            for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(x0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
+            convert(w0);
             __syncthreads();
             fetch(t + 1);   // (past the last: zeros)
-            compute(buf0);
+            compute(x0, w0);
         }
     }
     if (ALIGNED && first < steps) {
-        load_x(buf0, first);
+        load_x(x0, first);
         load_w(first);
-        convert(buf0);
+        convert(w0);
         load_w(first + 1);
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
@@ -189,19 +191,19 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     // would be a wait for those too)
     for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
         step_barrier<2 * PP>();   // dy is older than the last loads of codes and scales
-        convert(buf1);
-        load_x(buf1, t + 1);
+        convert(w1);
+        load_x(x1, t + 1);
         load_w(t + 2);
-        compute(buf0);
+        compute(x0, w0);
         step_barrier<2 * PP>();
-        convert(buf0);
-        load_x(buf0, t + 2);
+        convert(w0);
+        load_x(x0, t + 2);
         load_w(t + 3);
-        compute(buf1);
+        compute(x1, w1);
     }
     step_barrier<0>();
-    store_block<OUT, BM, BO, W, WM, kX + kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
-                                             wn * (BO / WN), a.k, buf0, buf1);
+    store_block<OUT, BM, BO, W, WM, kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
+                                             wn * (BO / WN), a.k, w0, w1);
 }
 
 template <uint32_t WF, typename OUT>
