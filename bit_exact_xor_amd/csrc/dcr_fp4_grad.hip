@@ -107,37 +107,54 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             *reinterpret_cast<bf16x8*>(dst + 16) = fp4_unpack8_bf16<WF>(q[i][1], sc[i]);
         }
     };
-    auto compute = [&](const uint8_t* xbuf, const uint8_t* wbuf) {
+    // `issue` starts the next loads.  The compiler takes a transposing read for
+    // one of what loads to LDS are writing, and waits for them.  In the largest
+    // tile, alone on its compute unit, all of a step's come before (390 -> 372
+    // us at 4096 x 4096 x 14336); the others wait in the shade of their
+    // neighbours and lose by the longer start (48 -> 53 us at 1024 x 4096 x 4096).
+    auto compute = [&](const uint8_t* xbuf, const uint8_t* wbuf, auto&& issue) {
         constexpr uint32_t H = 2, P = MI / H;
         const uint8_t* xl = xbuf + (wm * (BM / WM) + r16) * kRowB;
         // a lane names four columns of a row and gets four rows of a column
         const uint32_t jr = quad * 8 + (r16 >> 2);
         const uint8_t* wl = wbuf + jr * BO * 2 + (r16 & 3u) * 8;
-        bf16x8 x[2][H], w[NI];
+        constexpr bool FIRST = BM == 256;
+        bf16x8 x[2][H], w[FIRST ? 2 : 1][NI];
         auto read = [&](uint32_t ph) {
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
                 x[ph & 1][m] = *reinterpret_cast<const bf16x8*>(xl + ((ph % P) * H + m) * 16 * kRowB +
                                                                 (((ph / P * 4 + quad) ^ swizzle8(r16)) * 16));
         };
-        read(0);
+        auto read_w = [&](uint32_t h) {
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) {
+                const uint8_t* p = wl + h * 32 * BO * 2 + ((wn * NI + i) ^ turn(jr)) * 32;
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * BO * 2));
+                w[FIRST ? h : 0][i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+        };
+        if constexpr (FIRST) {
+            read_w(0);
+            read_w(1);
+            read(0);
+            __builtin_amdgcn_sched_barrier(0);
+            issue();
+        } else {
+            issue();
+            read(0);
+        }
 #pragma unroll
         for (uint32_t ph = 0; ph < 2 * P; ++ph) {
-            if (ph % P == 0)
-#pragma unroll
-                for (uint32_t i = 0; i < NI; ++i) {
-                    const uint8_t* p = wl + ph / P * 32 * BO * 2 + ((wn * NI + i) ^ turn(jr)) * 32;
-                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * BO * 2));
-                    w[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                }
+            if (!FIRST && ph % P == 0) read_w(ph / P);
             if (ph + 1 < 2 * P) read(ph + 1);
 #pragma unroll
             for (uint32_t m = 0; m < H; ++m)
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i)
                     acc[i][(ph % P) * H + m] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[FIRST ? ph / P : 0][i], x[ph & 1][m], acc[i][(ph % P) * H + m], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -175,8 +192,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(x0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
             convert(w0);
             __syncthreads();
-            fetch(t + 1);   // (past the last: zeros)
-            compute(x0, w0);
+            compute(x0, w0, [&] { fetch(t + 1); });   // (past the last: zeros)
         }
     }
     if (ALIGNED && first < steps) {
@@ -192,14 +208,16 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
         step_barrier<2 * PP>();   // dy is older than the last loads of codes and scales
         convert(w1);
-        load_x(x1, t + 1);
-        load_w(t + 2);
-        compute(x0, w0);
+        compute(x0, w0, [&] {
+            load_x(x1, t + 1);
+            load_w(t + 2);
+        });
         step_barrier<2 * PP>();
         convert(w0);
-        load_x(x0, t + 2);
-        load_w(t + 3);
-        compute(x1, w1);
+        compute(x1, w1, [&] {
+            load_x(x0, t + 2);
+            load_w(t + 3);
+        });
     }
     step_barrier<0>();
     store_block<OUT, BM, BO, W, WM, kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
