@@ -187,13 +187,13 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     // step past the last is all zeros
     for (uint32_t t = first; ROWS != Rows::kAny && t < steps; t += 2) {
         step_barrier<0>();
-        load(buf1, t + 1);
         const u32x2 s1 = load_scales(t + 1);
+        load(buf1, t + 1);
         compute(buf0, sc0);
         store_scales(sc1, s1);
         step_barrier<0>();
-        load(buf0, t + 2);
         const u32x2 s2 = load_scales(t + 2);
+        load(buf0, t + 2);
         compute(buf1, sc1);
         store_scales(sc0, s2);
     }
