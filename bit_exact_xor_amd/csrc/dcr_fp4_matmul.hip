@@ -215,8 +215,7 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     if (!xq && !grad && fp4_mm_tile(a, w->format, f32, ws, st)) return fp4_launched();
     if (xq && fp4_mm_tile4(a, f32, ws, st)) return fp4_launched();
     if (grad && n && fp4_mm_grad(a, w->format, f32, ws, st)) return fp4_launched();
-    // tiles of a grouped product: at most one short one for each group
-    a.row_tiles = uint32_t((m + kGT - 1) / kGT + (offsets ? n_groups : 0));
+    a.row_tiles = uint32_t(row_tile_bound(a, kGT));
     a.col_tiles = uint32_t((outs + kGT - 1) / kGT);
     const uint64_t tiles = uint64_t(a.row_tiles) * a.col_tiles;
     const uint32_t grid = uint32_t(tiles < kMaxGrid ? tiles : kMaxGrid);
@@ -244,9 +243,9 @@ uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&c
     for (uint32_t i = 0; i < 4; ++i) {
         if (!cost[i]) continue;
         const uint32_t b = 256u >> i, bn = b == 256 ? 256 : 128;
-        const uint64_t cols = (uint64_t(outs) + bn - 1) / bn, bound = (a->m + b - 1) / b + (a->offsets ? a->groups : 0);
+        const uint64_t cols = (uint64_t(outs) + bn - 1) / bn, bound = row_tile_bound(*a, b);
         // row tiles to expect: groups end inside a tile
-        const uint64_t rows = (a->m + b - 1) / b + (a->offsets ? std::min<uint64_t>(a->groups, a->m) / 2 : 0);
+        const uint64_t rows = a->offsets ? std::min(bound, (a->m + b - 1) / b + a->groups / 2) : bound;
         for (uint32_t s = 1; s <= 16; ++s) {
             if (s > 1 && (pairs / s < 2 || s * a->m * stride * 4 > DCR_FP4_WORKSPACE_BYTES)) break;
             if (bound * cols * s >= (1u << 22)) break;

@@ -263,6 +263,14 @@ __device__ __forceinline__ void store_block(const MArgs& a, const f32x4 (&acc)[N
     }
 }
 
+// Most row tiles of b rows that offsets over m rows can make: a group that is
+// not empty ends in one short tile at most.
+inline uint64_t row_tile_bound(const MArgs& a, uint64_t b) {
+    if (!a.offsets) return (a.m + b - 1) / b;
+    const uint64_t g = a.m < a.groups ? a.m : a.groups;
+    return g + (a.m - g) / b;
+}
+
 // kernels for parts of the range (false: not for these arguments)
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
 bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st);
@@ -270,8 +278,9 @@ bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st);
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
 // Chooses the tiling of a product with `outs` columns of results and `steps`
 // steps of the sum, and fills in the grid; steps' costs in cycles of a compute
-// unit by rows of a tile (256, 128, 64, 32).  Returns bm, 0 if no grid fits.
-uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]);   // (0: not that one)
+// unit by rows of a tile (256, 128, 64, 32; 0: there is none).  Returns the rows of a
+// tile, 0 if no grid fits.
+uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]);
 // With a->splits > 1: points a copy's y at the scratch, and joins the parts.
 MArgs fp4_mm_parts(const MArgs& a, uint32_t outs, void* ws);
 void fp4_mm_join(const MArgs& a, uint32_t outs, uint32_t fmt, bool f32, const void* ws, hipStream_t st);
