@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         }
 #pragma unroll
         for (uint32_t i = 0; i < XD; ++i) load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
+        __builtin_amdgcn_sched_barrier(0);   // (the step's wait counts the loads after these)
     };
     // 16 codes and their scale; rows past the sum's end and columns past the
     // row's are zeros.  The rows of a step get a descriptor of their own, so
@@ -244,8 +245,8 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 }  // namespace
 
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
-    // offsets inside a tile, and inside the rows of w of a step, are 31 bits
-    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
+    // offsets inside a tile, and inside the rows of w of a step, are 30 bits
+    if (a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
     constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 2000, 0, 900};
     const bool aligned = a.x_vec && a.w_vec && a.n % 8 == 0;
     const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, aligned ? kCost : kCostAny);

@@ -13,7 +13,6 @@
 namespace dcr {
 namespace {
 
-
 constexpr uint32_t kBK = 128;          // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK * 2;    // bytes of a row of x in LDS
 
@@ -137,6 +136,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 #pragma unroll
         for (uint32_t i = 0; i < DMA; ++i)
             load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
+        __builtin_amdgcn_sched_barrier(0);   // (the step's wait counts the loads after these)
     };
     // Any step, any alignment: into registers while the step before multiplies
     // (zeros past the row's end), then to LDS.
@@ -173,10 +173,10 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         w[j & 1][i] = fp4_unpack8_bf16<WF>(wq[o][i][j], WF == DCR_FP4_MX ? wsc[o][i] : (wsc[o][i] >> (j / 2 * 8)) & 255u);
     };
     // A step's products, four row subtiles at a time.  While these multiply,
-    // the next four are read from LDS and part of the
-    // next quarter's codes is converted.  The codes' registers are free once the
-    // last quarter is converted, and take those of the step after the next then:
-    // they may come from HBM.
+    // the next four are read from LDS and part of the next quarter's codes is
+    // converted.  The codes' registers are free once the last quarter is
+    // converted, and take those of the step after the next then: they may come
+    // from HBM.
     auto compute = [&](const uint8_t* buf, uint32_t next, auto odd) {
         constexpr uint32_t H = MI < 4 ? MI : 4, P = MI / H, C = (NI + P - 1) / P;   // C subtiles of codes a phase
         const uint8_t* xl = buf + r16 * kRowB;
@@ -288,8 +288,8 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostAny[4] = {0, 2800, 1700, 1100};
     const bool aligned = a.x_vec && a.w_vec && a.k % 32 == 0;
-    // offsets inside a tile are 31 bits
-    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
+    // offsets inside a tile are 30 bits
+    if (a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, aligned ? kCost : kCostAny);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);
