@@ -48,8 +48,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
 
     const uint32_t blk = threadIdx.x % NB, row0 = threadIdx.x / NB;
     const uint32_t wdst = row0 * BO * 2;
-    u32x2 q[PP];
-    uint32_t sc[PP];
+    // Codes and scales are read AHEAD + 1 steps before they multiply: small
+    // tiles are bound by reading them.
+    constexpr uint32_t AHEAD = BM == 256 ? 1 : 2;
+    u32x2 q[AHEAD][PP];
+    uint32_t sc[AHEAD][PP];
     f32x4 acc[NI][MI] = {};
     // this workgroup's steps: from `first` on, up to `steps`
     const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.n + kBJ - 1) / kBJ);
@@ -82,7 +85,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         wo[i] = ((row0 + i * RP) * wstep + blk * 8) | in_row;
         so[i] = ((row0 + i * RP) * sstep + blk * 16 / fp4_block(WF)) | in_row;
     }
-    auto load_w = [&](uint32_t step) {
+    auto load_w = [&](uint32_t step, auto odd) {
+        constexpr uint32_t o = decltype(odd)::value % AHEAD;
         const uint32_t j0 = min(step * kBJ, a.n - 1), nrow = min(kBJ, a.n - j0);
         const auto wr = rsrc(wb + uint64_t(j0) * wstep, (nrow - 1) * wstep + wlast);
         const auto sr = rsrc(sb + uint64_t(j0) * sstep, (nrow - 1) * sstep + slast);
@@ -95,17 +99,18 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
         }
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
-            q[i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, wo[i], 0, 0));
-            sc[i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], 0, 0);
+            q[o][i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wr, wo[i], 0, 0));
+            sc[o][i] = __builtin_amdgcn_raw_buffer_load_b8(sr, so[i], 0, 0);
         }
     };
-    auto convert = [&](uint8_t* wl) {
+    auto convert = [&](uint8_t* wl, auto odd) {
+        constexpr uint32_t o = decltype(odd)::value % AHEAD;
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
             const uint32_t r = row0 + i * RP;
             uint8_t* dst = wl + wdst + i * RP * BO * 2 + (blk ^ turn(r)) * 32;
-            *reinterpret_cast<bf16x8*>(dst) = fp4_unpack8_bf16<WF>(q[i][0], sc[i]);
-            *reinterpret_cast<bf16x8*>(dst + 16) = fp4_unpack8_bf16<WF>(q[i][1], sc[i]);
+            *reinterpret_cast<bf16x8*>(dst) = fp4_unpack8_bf16<WF>(q[o][i][0], sc[o][i]);
+            *reinterpret_cast<bf16x8*>(dst + 16) = fp4_unpack8_bf16<WF>(q[o][i][1], sc[o][i]);
         }
     };
     // `issue` starts the next loads.  The compiler takes a transposing read for
@@ -176,14 +181,16 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
             const uint32_t j = step * kBJ + row0 + i * RP, c = blk * 16;   // (columns from o0 on)
-            q[i] = u32x2{0, 0};
-            sc[i] = 0;
+            q[0][i] = u32x2{0, 0};
+            sc[0][i] = 0;
             if (j < a.n && o0 + c < a.k) {
-                q[i] = codes16(wb + uint64_t(j) * wstep, c, a.k - o0, a.w_vec);
-                sc[i] = sb[uint64_t(j) * sstep + c / fp4_block(WF)];
+                q[0][i] = codes16(wb + uint64_t(j) * wstep, c, a.k - o0, a.w_vec);
+                sc[0][i] = sb[uint64_t(j) * sstep + c / fp4_block(WF)];
             }
         }
     };
+    const std::integral_constant<uint32_t, 0> even;
+    const std::integral_constant<uint32_t, 1> odd;
     if constexpr (!ALIGNED) {
         fetch(first);
 #pragma unroll 1
@@ -191,16 +198,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             __syncthreads();
 #pragma unroll
             for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(x0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
-            convert(w0);
+            convert(w0, even);
             __syncthreads();
             compute(x0, w0, [&] { fetch(t + 1); });   // (past the last: zeros)
         }
     }
     if (ALIGNED && first < steps) {
         load_x(x0, first);
-        load_w(first);
-        convert(w0);
-        load_w(first + 1);
+        load_w(first, even);
+        if (AHEAD == 2) load_w(first + 1, odd);
+        convert(w0, even);
+        load_w(first + AHEAD, even);
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
@@ -208,16 +216,16 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     // would be a wait for those too)
     for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
         step_barrier<2 * PP>();   // dy is older than the last loads of codes and scales
-        convert(w1);
+        convert(w1, odd);
         compute(x0, w0, [&] {
             load_x(x1, t + 1);
-            load_w(t + 2);
+            load_w(t + 1 + AHEAD, odd);
         });
         step_barrier<2 * PP>();
-        convert(w0);
+        convert(w0, even);
         compute(x1, w1, [&] {
             load_x(x0, t + 2);
-            load_w(t + 3);
+            load_w(t + 2 + AHEAD, even);
         });
     }
     step_barrier<0>();
