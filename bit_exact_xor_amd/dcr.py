@@ -401,7 +401,8 @@ class Fp4Tensor:
     (uint8, [rows, stride], rows padded to 16 bytes where made here),
     `scales` (uint8, [rows, blocks]) and, in the NV format, `tensor_scale`
     (fp32, one element).  Buffers that are passed in are used as they are
-    (any row stride); they may be canonical tensors a refit patches."""
+    (any row stride); they may be canonical tensors a refit patches.  The
+    tensor keeps them: new contents are copied into them."""
 
     def __init__(self, rows, cols, fmt=FP4_MX, device="cuda", codes=None, scales=None, tensor_scale=None):
         import torch
@@ -421,7 +422,7 @@ class Fp4Tensor:
                 raise ValueError(f"{name}: uint8 [{rows}, >= {w}] with contiguous rows expected")
         if fmt == FP4_NV and (tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1):
             raise ValueError("tensor_scale: one fp32 element expected")
-        _one_device(codes, scales, tensor_scale if fmt == FP4_NV else None)
+        self.index = _one_device(codes, scales, tensor_scale if fmt == FP4_NV else None)
         self.rows, self.cols, self.fmt = rows, cols, fmt
         self.codes, self.scales = codes, scales
         self.tensor_scale = tensor_scale if fmt == FP4_NV else None
@@ -430,6 +431,12 @@ class Fp4Tensor:
                             tensor_scale.data_ptr() if fmt == FP4_NV else None, rows, cols,
                             codes.stride(0), scales.stride(0), fmt, 0)
         self._ref = ctypes.addressof(self.desc)
+
+    def __setattr__(self, name, value):
+        # (a new buffer would leave the description with the old one's address)
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{name}: an Fp4Tensor keeps its buffers; copy into them or make another")
+        super().__setattr__(name, value)
 
 
 def fp4_workspace(device="cuda"):
@@ -441,12 +448,12 @@ def fp4_workspace(device="cuda"):
 
 def _one_device(first, *others):
     """Index of the GPU that all of the tensors (None: left out) are on."""
-    dev = first.get_device()
+    dev = first.get_device() if not isinstance(first, Fp4Tensor) else first.index
     if dev < 0:
         raise ValueError("4-bit calls take tensors in GPU memory")
     for t in others:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+            raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
     return dev
 
 
@@ -469,10 +476,9 @@ def _wide(t, rows, cols, name):
     return t.data_ptr(), ty, strides[0]
 
 
-def _fp4_call(fn, what, device, stream, *args):
+def _fp4_call(torch, fn, what, device, stream, *args):
     """Call `fn` with GPU `device`, the one of its tensors, current, on
     `stream` or that GPU's current stream."""
-    import torch
     # (torch.cuda.current_stream() costs as much as the rest of a small call)
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
     if torch.cuda.current_device() == device:
@@ -488,18 +494,20 @@ def dcr_fp4_quantize(x, q: Fp4Tensor, options=0, workspace=None, stream=None) ->
     """Enqueue the quantisation of x (BF16 or fp32, [rows, cols]) into q;
     FP4_CALIBRATE (NV) first takes q's tensor scale from x, and needs a
     workspace."""
+    import torch
     p, ty, stride = _wide(x, q.rows, q.cols, "x")
-    dev = _one_device(x, q.codes, workspace)
-    _fp4_call(load_library().dcr_fp4_quantize, "dcr_fp4_quantize", dev, stream, p, ty, stride, q._ref, options,
+    dev = _one_device(q, x, workspace)
+    _fp4_call(torch, load_library().dcr_fp4_quantize, "dcr_fp4_quantize", dev, stream, p, ty, stride, q._ref, options,
               workspace.data_ptr() if workspace is not None else None,
               _nbytes(workspace) if workspace is not None else 0)
 
 
 def dcr_fp4_dequantize(q: Fp4Tensor, y, stream=None) -> None:
     """Enqueue reading q back into y (BF16 or fp32, [rows, cols])."""
+    import torch
     p, ty, stride = _wide(y, q.rows, q.cols, "y")
-    dev = _one_device(y, q.codes)
-    _fp4_call(load_library().dcr_fp4_dequantize, "dcr_fp4_dequantize", dev, stream, q._ref, p, ty, stride)
+    dev = _one_device(q, y)
+    _fp4_call(torch, load_library().dcr_fp4_dequantize, "dcr_fp4_dequantize", dev, stream, q._ref, p, ty, stride)
 
 
 def _groups(w, offsets):
@@ -520,17 +528,18 @@ def _product(fn, what, x, w, y, offsets, workspace, stream, grad):
     if workspace is None:
         raise ValueError("workspace: pass one made by fp4_workspace()")
     off, g, n = _groups(w, offsets)
-    yp, ty, ys = _wide(y, x.rows if isinstance(x, Fp4Tensor) else x.shape[0], w.cols if grad else n, "dx" if grad else "y")
-    tail = (w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    yp, ty, ys = _wide(y, x.rows if isinstance(x, Fp4Tensor) else x.shape[0], w.cols if grad else n,
+                       "dx" if grad else "y")
+    tail = (w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.nbytes)
     if isinstance(x, Fp4Tensor):
-        dev = _one_device(w.codes, x.codes, y, offsets, workspace)
-        _fp4_call(fn, what, dev, stream, x._ref, *tail)
+        dev = _one_device(w, x.codes, y, offsets, workspace)
+        _fp4_call(torch, fn, what, dev, stream, x._ref, *tail)
         return
     if x.dtype is not torch.bfloat16:
         raise ValueError(f"{what}: bfloat16 rows expected, got {x.dtype}")
     xp, _ty, xs = _wide(x, None, n if grad else w.cols, "dy" if grad else "x")
-    dev = _one_device(w.codes, x, y, offsets, workspace)
-    _fp4_call(fn, what, dev, stream, xp, x.shape[0], xs, *tail)
+    dev = _one_device(w, x, y, offsets, workspace)
+    _fp4_call(torch, fn, what, dev, stream, xp, x.shape[0], xs, *tail)
 
 
 def dcr_fp4_matmul(x, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:

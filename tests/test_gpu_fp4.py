@@ -480,3 +480,26 @@ def test_refit_of_experts():
         ref, size = R.product(f64(x), R.unit_values(c, b, 64, R.MX), off)
         assert (np.abs(f64(y) - ref) <= bound(size, ref, 64, "fp32")).all()
         w = w * 1.01
+
+
+@pytest.mark.parametrize("op,fmt", OPS[:3])
+@pytest.mark.parametrize("m,n,k", [(1, 14336, 2304), (16, 12400, 2592), (11, 6500, 4064), (8, 6400, 2304), (4, 1000, 3616),
+                                   (13, 4096, 4096), (16, 16400, 512)])
+def test_product_few_rows(op, fmt, m, n, k):
+    """Wide and narrow weights, sums of several turns of a wave, scales with and without borders of their own."""
+    check_product(op, fmt, m, n, k, "fp32", "whole")
+    check_product(op, fmt, m, n, k, "bf16", "normal")
+
+
+@pytest.mark.parametrize("op,fmt", OPS[:3])
+@pytest.mark.parametrize("n,k", [(1024, 2304), (1650, 2080), (96, 4096), (3000, 512)])
+def test_product_few_rows_of_groups(op, fmt, n, k):
+    check_product(op, fmt, 33, n, k, "fp32", "whole", groups=8, off=[1, 1, 5, 23, 24, 24, 24, 30, 31])
+    check_product(op, fmt, 2, n, k, "fp32", "whole", groups=8, off=[0, 0, 0, 1, 1, 1, 2, 2, 2])
+
+
+def test_tensor_keeps_its_buffers():
+    q = dcr.Fp4Tensor(4, 64)
+    for name in ("codes", "scales", "tensor_scale", "rows"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, None)
