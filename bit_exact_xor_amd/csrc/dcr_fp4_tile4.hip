@@ -3,11 +3,18 @@
 // The scaled matrix instruction multiplies 128 codes of a row with 128 of a
 // column, each run of 32 with its own power of two: a lane's operand is one
 // MX block and one scale byte, and nothing is converted.
+//
+// 8192 x 14336 x 4096 takes 271 us (3.55 PFLOP/s), the matrix unit busy in 46 %
+// of the cycles: reads from LDS and products alone take 161 us; the codes' loads
+// add some 65, the scales' way through LDS 35 and the results' 45.  Tried and
+// not kept: four waves of 128 x 128 (a third less read from LDS, but the
+// compiler moves full accumulation registers about: 415 us), scales eight
+// bytes a row in LDS (285 us), columns' codes of a step's second half read
+// ahead (even), raised priority for half of the waves (even).
 #include "dcr_fp4_mm.h"
 
 namespace dcr {
 namespace {
-
 
 constexpr uint32_t kBK = 256;                // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
