@@ -258,7 +258,7 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile, and inside the rows of w of a step, are 30 bits
-    if (a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
+    if (a.n >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
     constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 2000, 0, 900};
     const bool aligned = a.x_vec && a.w_vec && a.n % 8 == 0;
     const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, aligned ? kCost : kCostAny);

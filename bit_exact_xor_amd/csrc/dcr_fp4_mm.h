@@ -271,6 +271,10 @@ inline uint64_t row_tile_bound(const MArgs& a, uint64_t b) {
     return g + (a.m - g) / b;
 }
 
+// Sums that the kernels below take are shorter: a single row has no stride to
+// limit its length, and past 2^30 elements kOutside would lie inside it.
+constexpr uint32_t kLongest = 1u << 26;
+
 // kernels for parts of the range (false: not for these arguments)
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st);
 bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st);

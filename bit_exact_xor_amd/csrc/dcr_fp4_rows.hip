@@ -198,7 +198,7 @@ void launch(const MArgs& a, hipStream_t st, bool sv, uint32_t nt) {
 }  // namespace
 
 bool fp4_mm_rows(MArgs a, bool xq, uint32_t fmt, bool f32, hipStream_t st) {
-    if (!a.x_vec || !a.w_vec || a.k % 32 || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) ||
+    if (!a.x_vec || !a.w_vec || a.k % 32 || a.k >= kLongest || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) ||
         a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
     // rows of a group, as far as the host can tell

@@ -289,9 +289,10 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostAny[4] = {0, 2800, 1700, 1100};
-    const bool aligned = a.x_vec && a.w_vec && a.k % 32 == 0;
+    // (two NV scales are read at once)
+    const bool aligned = a.x_vec && a.w_vec && a.k % 32 == 0 && (fmt == DCR_FP4_MX || a.ws_stride % 2 == 0);
     // offsets inside a tile are 30 bits
-    if (a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
+    if (a.k >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, aligned ? kCost : kCostAny);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);

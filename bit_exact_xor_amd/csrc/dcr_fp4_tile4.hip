@@ -231,8 +231,8 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
 }  // namespace
 
 bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
-    // offsets inside a tile are 31 bits
-    if (a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
+    // offsets inside a tile are 30 bits
+    if (a.k >= kLongest || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
     const Rows rows = !a.x_vec || !a.w_vec || a.k % 32                                        ? Rows::kAny
                       : a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0 ? Rows::kScales

@@ -503,3 +503,57 @@ def test_tensor_keeps_its_buffers():
     for name in ("codes", "scales", "tensor_scale", "rows"):
         with pytest.raises(AttributeError):
             setattr(q, name, None)
+
+
+def padded(q, code_pad, scale_pad):
+    """q in buffers with longer rows; what lies between its rows must not matter."""
+    rows, w, nb = q.rows, (q.cols + 1) // 2, dcr.fp4_blocks(q.cols, q.fmt)
+    codes = torch.full((rows, w + code_pad), 0x77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, nb + scale_pad), 255 if q.fmt == R.MX else 127, dtype=torch.uint8, device="cuda")
+    codes[:, :w], scales[:, :nb] = q.codes[:, :w], q.scales[:, :nb]
+    if q.cols % 2:
+        codes[:, w - 1] |= 0x70
+    return dcr.Fp4Tensor(rows, q.cols, q.fmt, codes=codes, scales=scales, tensor_scale=q.tensor_scale)
+
+
+@pytest.mark.parametrize("op,fmt", OPS)
+@pytest.mark.parametrize("m", [2, 20, 70, 300])
+def test_product_weight_strides(op, fmt, m):
+    """Rows of codes and scales at any distance, on borders of 8 and 16 bytes among them, NaN scales between them."""
+    rng = np.random.default_rng(m)
+    ws = dcr.fp4_workspace()
+    for n, k in [(100, 96), (130, 384), (300, 640), (257, 289), (64, 4000), (280, 2336)]:
+        q, w = whole_fp4(n, k, fmt, rng)
+        red, outs = (n, k) if op == "grad" else (k, n)
+        if op == "matmul_q":
+            x, xv = random_fp4(m, k, R.MX, rng, 126, 127)
+        else:
+            xv = rng.integers(-2, 3, (m, red)).astype(np.float64)
+            x = up(xv).bfloat16()
+        want = R.product(xv, w, None, op == "grad")[0]
+        nb, cb = dcr.fp4_blocks(k, fmt), (k + 1) // 2
+        for code_pad, scale_pad in [(0, 1), (1, 0), (-cb % 16, 3), (-cb % 16, -nb % 16), (-cb % 16 + 16, -nb % 8 + 8), (8, 5)]:
+            y = torch.full((m, outs), 9.0, device="cuda")
+            v = padded(x, -cb % 16, -nb % 8 + (scale_pad & 8)) if op == "matmul_q" else x
+            run_product(op, v, padded(q, code_pad, scale_pad), y, None, ws)
+            assert np.array_equal(f64(y), want), (n, k, code_pad, scale_pad)
+
+
+@pytest.mark.parametrize("op", ["matmul", "matmul_q", "grad"])
+def test_longest_sums(op):
+    """One row of 2^26 elements, the first length the tiles leave, against one that they take."""
+    for red in (1 << 26, (1 << 26) - 256):
+        rows, cols = (red, 32) if op == "grad" else (1, red)
+        q = dcr.Fp4Tensor(rows, cols, R.MX)
+        q.codes.fill_(0x22), q.scales.fill_(127)           # ones
+        x = torch.zeros(1, red, dtype=torch.bfloat16, device="cuda")
+        x[0, ::1 << 18] = 1.0
+        x[0, red - 1] = 3.0
+        if op == "matmul_q":
+            v = dcr.Fp4Tensor(1, red, R.MX)
+            dcr.dcr_fp4_quantize(x, v)
+            x = v
+        y = torch.full((1, 32 if op == "grad" else 1), 9.0, device="cuda")
+        run_product(op, x, q, y, None, dcr.fp4_workspace())
+        assert (y == 256 + 3).all()
+        del q, x
