@@ -19,8 +19,10 @@ namespace {
 constexpr uint32_t kBK = 256;                // elements of the sum a step takes
 constexpr uint32_t kRowB = kBK / 2;          // bytes of a row of codes in LDS
 
-// What is known of the rows: nothing; codes on 16-byte borders and a sum of
-// whole blocks; and eight scales at a time on 8-byte borders.
+// What is known of the rows: nothing; codes on 16-byte borders (a row's last
+// codes and scales are then read with what shares their 16 or 4 bytes); and
+// scales on 8-byte borders as well, with a sum of whole steps (sums that end
+// anywhere cost 3 % at 8192 x 14336 x 4096).
 enum class Rows { kAny, kAligned, kScales };
 
 template <typename OUT, uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, Rows ROWS>
@@ -47,8 +49,9 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint8_t* wb = a.wc + (uint64_t(rt.group) * a.n + n0) * a.wc_stride;
     const uint8_t* sb = a.ws + (uint64_t(rt.group) * a.n + n0) * a.ws_stride;
     const uint32_t xstep = uint32_t(a.x_stride), wstep = uint32_t(a.wc_stride);
-    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride, (rows - 1) * xstep + (a.k + 1) / 2);
-    const auto wr = rsrc(wb, (cols - 1) * wstep + (a.k + 1) / 2);
+    const uint32_t last_codes = ((a.k + 1) / 2 + 15) & ~15u;
+    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride, (rows - 1) * xstep + last_codes);
+    const auto wr = rsrc(wb, (cols - 1) * wstep + last_codes);
 
     // the row whose scales this thread stages (x's, then w's), and where they
     // go: [quarter of the step][quad][row of a subtile][subtile], so that a
@@ -57,8 +60,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint32_t srow = xside ? threadIdx.x : (threadIdx.x - BM) % BN;   // (spare threads do one over)
     const uint32_t last = (xside ? rows : cols) - 1;
     const uint32_t sstep = uint32_t(xside ? a.xs_stride : a.ws_stride), blocks = (a.k + 31) / 32;
-    const auto sr = rsrc(xside ? a.xs + rt.begin * a.xs_stride : sb, last * sstep + blocks);
-    const uint32_t soff = min(srow, last) * sstep;
+    const uint8_t* srows = xside ? a.xs + rt.begin * a.xs_stride : sb;
+    const uint32_t skew = SV ? 0 : uint32_t(reinterpret_cast<uintptr_t>(srows)) & 3u;
+    const auto sr = rsrc(srows - skew, (skew + last * sstep + blocks + 3) & ~3u);
+    const uint32_t soff = skew + min(srow, last) * sstep;
     const uint32_t subs = xside ? BM / 16 : BN / 16;
     const uint32_t sdst = (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
 
@@ -67,7 +72,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.k + kBK - 1) / kBK);
 
     // Codes of a step by loads straight to LDS.  From the step on in which the
-    // sum ends (at a whole block) lanes past the end read behind the
+    // sum ends lanes whose block is past the end read behind the
     // descriptors' range, which gives zeros; a lane once past it stays there,
     // so its offset is changed for good and the other steps spend nothing on it.
     const uint32_t lr = wave * 8 + (lane >> 3), lc = (lane & 7u) ^ swizzle8(lr);
@@ -89,25 +94,47 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
         for (uint32_t i = 0; i < WD; ++i) load_lds16(wr, buf + BM * kRowB + (i * W + wave) * 1024, wo[i], step * kRowB);
     };
-    // the eight scale bytes of a step of this thread's row; zeros past the end
-    auto load_scales = [&](uint32_t step) -> u32x2 {
-        const uint32_t b = step * (kBK / 32);
-        u32x2 v = {0, 0};
+    // The eight scale bytes of a step of this thread's row, as whole words that
+    // hold them (one load for eight bytes a row costs what one for a byte does).
+    auto load_scales = [&](uint32_t step) -> u32x4 {
+        const uint32_t b = step * (kBK / 32), out = b < blocks ? 0u : kOutside;
         if constexpr (SV) {
-            const auto q = __builtin_amdgcn_raw_buffer_load_b64(sr, soff | (b < blocks ? 0u : kOutside), b, 0);
-            v = __builtin_bit_cast(u32x2, q);
+            const auto q = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(sr, soff | out, b, 0));
+            return u32x4{q[0], q[1], 0, 0};
         } else {
+            u32x4 v = {};
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const uint32_t out = b + i < blocks ? 0u : kOutside;
-                v[i / 4] |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sr, (soff + i) | out, b, 0)) << (8 * (i & 3));
-            }
+            for (uint32_t i = 0; i < 3; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b32(sr, ((soff & ~3u) + b + 4 * i) | out, 0, 0);
+            return v;
         }
-        return v;
     };
-    auto store_scales = [&](uint8_t* sc, u32x2 v) {
+    // ... to LDS, zeros for blocks past the end
+    auto store_scales = [&](uint8_t* sc, u32x4 v, uint32_t step) {
+        const uint32_t n = blocks - min(blocks, step * (kBK / 32));
+        if constexpr (!SV) {
+            v[0] = __builtin_amdgcn_alignbyte(v[1], v[0], soff & 3u);
+            v[1] = __builtin_amdgcn_alignbyte(v[2], v[1], soff & 3u);
+        }
+        if (!SV && n < 8) {
+            v[0] &= n < 4 ? (1u << (8 * n)) - 1u : ~0u;
+            v[1] &= n < 4 ? 0u : (1u << (8 * n - 32)) - 1u;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) sc[sdst + i * 16 * subs] = uint8_t(v[i / 4] >> (8 * (i & 3)));
+    };
+    // A sum that ends inside a block: x's codes past the end (w's are finite,
+    // and the block's scales their own) become zeros in LDS.
+    const uint32_t tail = a.k % 32;
+    auto end_inside = [&](uint8_t* buf, uint32_t step) {
+        if (SV || tail == 0 || step != a.k / kBK) return;
+        if (threadIdx.x < BM) {
+            u32x4* p = reinterpret_cast<u32x4*>(buf + threadIdx.x * kRowB + ((a.k % kBK / 32) ^ swizzle8(threadIdx.x)) * 16);
+            u32x4 v = *p;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) v[i] &= tail >= 8 * i + 8 ? ~0u : tail <= 8 * i ? 0u : (1u << (4 * (tail - 8 * i))) - 1u;
+            *p = v;
+        }
+        __syncthreads();
     };
     auto compute = [&](const uint8_t* buf, const uint8_t* sc) {
         constexpr uint32_t H = 2, P = MI / H;
@@ -160,7 +187,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     // Any step, any alignment: into registers while the step before multiplies
     // (zeros past the rows' ends), then to LDS.
     u32x4 xnext[XD], wnext[WD];
-    u32x2 sn;
+    u32x4 sn;
     auto fetch = [&](uint32_t step) {
         const uint32_t k = step * kBK + lc * 32;
         const uint8_t* x = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride;
@@ -180,7 +207,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
 #pragma unroll
             for (uint32_t i = 0; i < WD; ++i)
                 *reinterpret_cast<u32x4*>(buf0 + BM * kRowB + (i * W + wave) * 1024 + lane * 16) = wnext[i];
-            store_scales(sc0, sn);
+            store_scales(sc0, sn, t);
             __syncthreads();
             fetch(t + 1);   // (past the last: zeros)
             compute(buf0, sc0);
@@ -188,21 +215,23 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     }
     if (ROWS != Rows::kAny && first < steps) {
         load(buf0, first);
-        store_scales(sc0, load_scales(first));
+        store_scales(sc0, load_scales(first), first);
     }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
     for (uint32_t t = first; ROWS != Rows::kAny && t < steps; t += 2) {
         step_barrier<0>();
-        const u32x2 s1 = load_scales(t + 1);
+        end_inside(buf0, t);
+        const u32x4 s1 = load_scales(t + 1);
         load(buf1, t + 1);
         compute(buf0, sc0);
-        store_scales(sc1, s1);
+        store_scales(sc1, s1, t + 1);
         step_barrier<0>();
-        const u32x2 s2 = load_scales(t + 2);
+        end_inside(buf1, t + 1);
+        const u32x4 s2 = load_scales(t + 2);
         load(buf0, t + 2);
         compute(buf1, sc1);
-        store_scales(sc0, s2);
+        store_scales(sc0, s2, t + 2);
     }
     step_barrier<0>();
     store_block<OUT, BM, BN, W, WM, kCodes>(a, acc, 1.0f, rt, at, wm, wn * (BN / WN), a.n, buf0, buf1);
@@ -234,9 +263,9 @@ bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile are 30 bits
     if (a.k >= kLongest || a.x_stride >= (1u << 22) || a.wc_stride >= (1u << 22) || a.xs_stride >= (1u << 22) || a.ws_stride >= (1u << 22))
         return false;
-    const Rows rows = !a.x_vec || !a.w_vec || a.k % 32                                        ? Rows::kAny
+    const Rows rows = !a.x_vec || !a.w_vec                                             ? Rows::kAny
                       : a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0 ? Rows::kScales
-                                                                                               : Rows::kAligned;
+                                                                                       : Rows::kAligned;
     constexpr uint32_t kCost[4] = {4800, 1600, 1000, 0}, kCostAny[4] = {0, 3000, 1800, 0};
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, rows == Rows::kAny ? kCostAny : kCost);
     if (!bm) return false;
