@@ -27,7 +27,8 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t r) {
 }
 
 // What is known of the rows: nothing; x and codes on 16-byte borders and a sum
-// of whole MX blocks; and scales of two steps at a time on borders of their
+// of whole pieces of x (codes behind its end are finite, and multiplied by
+// zeros); and scales of two steps at a time on borders of their
 // own (then one load for 16 rows brings two steps' scales: a load costs as
 // much for a byte of each row as for the 16 bytes of codes).
 enum class Rows { kAny, kAligned, kPaired };
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     // buffer descriptors: scalar base and step, 32-bit lane offsets
     const auto xr = rsrc(xb, ((rows - 1) * uint32_t(a.x_stride) + a.k) * 2);
     const uint32_t wrows = min(BN, a.n - n0);
-    const auto wr = rsrc(wb, (wrows - 1) * uint32_t(a.wc_stride) + (a.k + 1) / 2);
+    const auto wr = rsrc(wb, (wrows - 1) * uint32_t(a.wc_stride) + (((a.k + 1) / 2 + 15) & ~15u));
     const auto sr = rsrc(sb, (wrows - 1) * uint32_t(a.ws_stride) + (a.k + fp4_block(WF) - 1) / fp4_block(WF));
 
     f32x4 acc[NI][MI] = {};
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
     const uint32_t first = at.split * a.split_steps, steps = min(first + a.split_steps, (a.k + kBK - 1) / kBK);
 
     // Loads of a step of aligned rows.  From the step on in which the sum ends
-    // (at a multiple of 32), lanes past the end read behind the descriptors'
+    // (at a multiple of 8), lanes past the end read behind the descriptors'
     // range, which gives zeros; a lane once past it stays there, so its offset
     // is changed for good and the other steps spend nothing on it.
     auto x_past_end = [&](uint32_t step) {
@@ -289,8 +290,9 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostAny[4] = {0, 2800, 1700, 1100};
-    // (two NV scales are read at once)
-    const bool aligned = a.x_vec && a.w_vec && a.k % 32 == 0 && (fmt == DCR_FP4_MX || a.ws_stride % 2 == 0);
+    // (two NV scales are read at once, so both have to be there)
+    const bool aligned = a.x_vec && a.w_vec && a.k % 8 == 0 &&
+                         (fmt == DCR_FP4_MX || (a.ws_stride % 2 == 0 && (a.k - 1) % 32 >= 16));
     // offsets inside a tile are 30 bits
     if (a.k >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, aligned ? kCost : kCostAny);

@@ -557,3 +557,12 @@ def test_longest_sums(op):
         run_product(op, x, q, y, None, dcr.fp4_workspace())
         assert (y == 256 + 3).all()
         del q, x
+
+
+@pytest.mark.parametrize("op,fmt", OPS)
+@pytest.mark.parametrize("k", [8, 1000, 1016, 1048, 1304])
+def test_product_sums_of_whole_pieces(op, fmt, k):
+    """Sums that end inside a block, rows of x on 16-byte borders all the same."""
+    for m, n in [(3, 40), (24, 136), (70, 1000), (280, 264)]:
+        check_product(op, fmt, m, n, k, "fp32", "whole")
+        check_product(op, fmt, m, k, n, "fp32", "whole", x_pad=-k % 8)
