@@ -19,8 +19,8 @@ namespace {
 // 64 x 64 results a workgroup, sums over 64 at a time: both operands go to
 // LDS as bf16 and four waves multiply 32 x 32 each.  Takes every size, stride
 // and alignment, and is left with what the rows and tiles of the other files do
-// not take: row strides from 2^21 elements on, sums from 2^26 on, grids from
-// 2^22 tiles on, and gradients of weights without rows (zeros).
+// not take: row strides from 2^21 elements on, sums below 8 and from 2^26 on,
+// grids from 2^22 tiles on.
 constexpr uint32_t kGT = 64, kGPad = 72;
 
 template <bool GRAD, bool XQ, uint32_t WF, typename OUT>

@@ -26,16 +26,16 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t r) {
     return (r & 3u) | ((r >> 1) & 4u) | (((r >> 3) ^ (r >> 2)) & 1u) << 3;
 }
 
-// What is known of the rows: nothing; x and codes on 16-byte borders and a sum
-// of whole pieces of x (codes behind its end are finite, and multiplied by
-// zeros); and scales of two steps at a time on borders of their
+// What is known of the rows: nothing; codes on 16-byte borders (those behind
+// the sum's end are finite, and multiplied by zeros); x there too, and a sum of
+// whole pieces of x; and scales of two steps at a time on borders of their
 // own (then one load for 16 rows brings two steps' scales: a load costs as
 // much for a byte of each row as for the 16 bytes of codes).
-enum class Rows { kAny, kAligned, kPaired };
+enum class Rows { kAny, kCodes, kAligned, kPaired };
 
 template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BN, uint32_t W, Rows ROWS>
 __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
-    constexpr bool ALIGNED = ROWS != Rows::kAny, PAIRED = ROWS == Rows::kPaired;
+    constexpr bool CODES = ROWS != Rows::kAny, ALIGNED = CODES && ROWS != Rows::kCodes, PAIRED = ROWS == Rows::kPaired;
     constexpr uint32_t MI = BM / 16, NI = BN / W / 16, DMA = BM / 4 / W;
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[BM * kRowB], buf1[BM * kRowB];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -141,11 +141,36 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
         __builtin_amdgcn_sched_barrier(0);   // (the step's wait counts the loads after these)
     };
-    // Any step, any alignment: into registers while the step before multiplies
-    // (zeros past the row's end), then to LDS.
+    // Any alignment: into registers while the step before multiplies, then to
+    // LDS.  A piece of x that the sum's end cuts is read as the row's last eight
+    // elements and moved down.
     u32x4 xn[DMA], wn[NI];
     uint32_t sn[NI];
-    auto fetch = [&](uint32_t step) {
+    auto fetch_x = [&](uint32_t step) {
+        if ((step + 1) * kBK <= a.k) {
+#pragma unroll
+            for (uint32_t i = 0; i < DMA; ++i) __builtin_memcpy(&xn[i], xb + step * kRowB + xo[i], 16);
+            return;
+        }
+        const uint32_t c = step * kBK + (r16 ^ swizzle(wave * 4 + quad)) * 8, past = c - min(c, a.k - 8);
+#pragma unroll
+        for (uint32_t i = 0; i < DMA; ++i) {
+            u32x4 v;
+            __builtin_memcpy(&v, xb + uint64_t(xo[i]) + step * kRowB - past * 2, 16);
+            uint64_t lo = v[0] | uint64_t(v[1]) << 32, hi = v[2] | uint64_t(v[3]) << 32;
+            const uint32_t bits = min(past, 8u) * 16;
+            lo = bits >= 64 ? hi : lo, hi = bits >= 64 ? 0 : hi;
+            const uint32_t n = bits & 63u;
+            lo = n ? lo >> n | hi << (64 - n) : lo, hi >>= n;
+            lo = bits >= 128 ? 0 : lo;
+            xn[i] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+        }
+    };
+    auto put_x = [&](uint8_t* buf) {
+#pragma unroll
+        for (uint32_t i = 0; i < DMA; ++i) *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = xn[i];
+    };
+    auto fetch_w = [&](uint32_t step) {
         const uint32_t kw = step * kBK + quad * 32;
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) {
@@ -158,18 +183,10 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
                 if (WF == DCR_FP4_NV && kw + 16 < a.k) sn[i] |= uint32_t(s[1]) << 8;
             }
         }
-#pragma unroll
-        for (uint32_t i = 0; i < DMA; ++i) {
-            const uint32_t r = (i * W + wave) * 4 + quad;
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(r, rows - 1)) * a.x_stride;
-            xn[i] = bf16x8_any(p, step * kBK + (r16 ^ swizzle(r)) * 8, a.k);
-        }
     };
-    auto put = [&](uint8_t* buf) {
+    auto put_w = [&] {
 #pragma unroll
         for (uint32_t i = 0; i < NI; ++i) wq[0][i] = wn[i], wsc[0][i] = sn[i];
-#pragma unroll
-        for (uint32_t i = 0; i < DMA; ++i) *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = xn[i];
     };
     auto convert = [&](auto odd, uint32_t j, uint32_t i) {
         constexpr uint32_t o = decltype(odd)::value;
@@ -200,7 +217,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             if (ph == 0)
 #pragma unroll
                 for (uint32_t i = 0; i < NI; ++i) convert(odd, 0, i);
-            if (ALIGNED && ph == 3 * P) {
+            if (CODES && ph == 3 * P) {
                 load_w(next + 1, odd);
             }
             if (j < 3)
@@ -223,6 +240,8 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 
     const std::integral_constant<uint32_t, 0> even;
     const std::integral_constant<uint32_t, 1> odd;
+    // two steps a turn (one loop exit keeps the sums in their registers); a step
+    // past the last is all zeros
     if constexpr (ALIGNED) {
         if (first < steps) {
             x_past_end(first);
@@ -233,8 +252,6 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             w_past_end(first + 1);
             load_w(first + 1, odd);
         }
-        // two steps a turn (one loop exit keeps the sums in their registers);
-        // a step past the last is all zeros
         for (uint32_t t = first; t < steps; t += 2) {
             step_barrier<2 * NI>();   // x is older than the last loads of codes and scales
             x_past_end(t + 1);
@@ -247,14 +264,38 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
             w_past_end(t + 3);
             compute(buf1, t + 2, odd);
         }
+    } else if constexpr (CODES) {
+        if (first < steps) {
+            w_past_end(first);
+            load_w(first, even);
+            w_past_end(first + 1);
+            load_w(first + 1, odd);
+            fetch_x(first);
+            put_x(buf0);
+        }
+        for (uint32_t t = first; t < steps; t += 2) {
+            __syncthreads();
+            fetch_x(t + 1);
+            w_past_end(t + 2);
+            compute(buf0, t + 1, even);
+            put_x(buf1);
+            __syncthreads();
+            fetch_x(t + 2);
+            w_past_end(t + 3);
+            compute(buf1, t + 2, odd);
+            put_x(buf0);
+        }
     } else {
-        fetch(first);
+        fetch_w(first);
+        fetch_x(first);
 #pragma unroll 1
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
-            put(buf0);
+            put_w();
+            put_x(buf0);
             __syncthreads();
-            fetch(t + 1);   // (past the last: zeros)
+            fetch_w(t + 1);   // (past the last: zeros)
+            fetch_x(t + 1);
             compute(buf0, 0, even);
         }
     }
@@ -267,8 +308,9 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
 template <uint32_t WF, typename OUT, Rows ROWS>
 void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
     const dim3 g(a.grid);
-    if (ROWS != Rows::kAny && bm == 256)
-        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ROWS == Rows::kAny ? Rows::kAligned : ROWS>), g, dim3(512), 0, st, a);
+    constexpr bool ALIGNED = ROWS == Rows::kAligned || ROWS == Rows::kPaired;
+    if (ALIGNED && bm == 256)
+        hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 256, 256, 8, ALIGNED ? ROWS : Rows::kAligned>), g, dim3(512), 0, st, a);
     else if (bm == 128)
         hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 128, 128, 4, ROWS>), g, dim3(256), 0, st, a);
     else if (bm == 64)
@@ -277,10 +319,12 @@ void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
         hipLaunchKernelGGL((fp4_mm_tile_kernel<WF, OUT, 32, 128, 4, ROWS>), g, dim3(256), 0, st, a);
 }
 template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
-    if (!aligned)
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
+    if (rows == Rows::kAny)
         launch_tile<WF, OUT, Rows::kAny>(a, st, bm);
-    else if (a.k % 256 == 0 && a.ws_stride % (256 / fp4_block(WF)) == 0)
+    else if (rows == Rows::kCodes)
+        launch_tile<WF, OUT, Rows::kCodes>(a, st, bm);
+    else if (rows == Rows::kPaired)
         launch_tile<WF, OUT, Rows::kPaired>(a, st, bm);
     else
         launch_tile<WF, OUT, Rows::kAligned>(a, st, bm);
@@ -289,20 +333,24 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
 }  // namespace
 
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
-    constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostAny[4] = {0, 2800, 1700, 1100};
-    // (two NV scales are read at once, so both have to be there)
-    const bool aligned = a.x_vec && a.w_vec && a.k % 8 == 0 &&
-                         (fmt == DCR_FP4_MX || (a.ws_stride % 2 == 0 && (a.k - 1) % 32 >= 16));
     // offsets inside a tile are 30 bits
-    if (a.k >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
-    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, aligned ? kCost : kCostAny);
+    if (a.k < 8 || a.k >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
+    constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostCodes[4] = {0, 2400, 1500, 900}, kCostAny[4] = {0, 2800, 1700, 1100};
+    // (two NV scales are read at once, so both have to be there)
+    const bool codes = a.w_vec && (fmt == DCR_FP4_MX || (a.ws_stride % 2 == 0 && (a.k - 1) % 32 >= 16));
+    const Rows rows = !codes                                            ? Rows::kAny
+                      : !a.x_vec || a.k % 8                               ? Rows::kCodes
+                      : a.k % 256 || a.ws_stride % (256 / fp4_block(fmt)) ? Rows::kAligned
+                                                                          : Rows::kPaired;
+    const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK,
+                                    rows == Rows::kAny ? kCostAny : rows == Rows::kCodes ? kCostCodes : kCost);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.n, ws);
     const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        wide ? launch<DCR_FP4_MX, float>(p, st, bm, aligned) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, aligned);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm, rows) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, rows);
     else
-        wide ? launch<DCR_FP4_NV, float>(p, st, bm, aligned) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, aligned);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm, rows) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, rows);
     fp4_mm_join(a, a.n, fmt, f32, ws, st);
     return true;
 }
