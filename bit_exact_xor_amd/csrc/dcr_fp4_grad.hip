@@ -23,9 +23,13 @@ constexpr uint32_t kRowB = kBJ * 2;      // bytes of a row of dy in LDS
 // different banks
 __device__ __forceinline__ uint32_t turn(uint32_t j) { return (j & 3u) | ((j >> 1) & 4u); }
 
-// ALIGNED: rows of dy and codes on 16-byte borders, a sum of a multiple of 8
-template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BO, uint32_t WM, uint32_t WN, bool ALIGNED>
+// What is known of the rows: nothing; codes on 16-byte borders; dy there too,
+// and a sum of a multiple of 8.
+enum class Rows { kAny, kCodes, kAligned };
+
+template <uint32_t WF, typename OUT, uint32_t BM, uint32_t BO, uint32_t WM, uint32_t WN, Rows ROWS>
 __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
+    constexpr bool CODES = ROWS != Rows::kAny, ALIGNED = ROWS == Rows::kAligned;
     constexpr uint32_t W = WM * WN, MI = BM / WM / 16, NI = BO / WN / 16;
     constexpr uint32_t XD = BM / 8 / W;          // 1 KiB loads of dy of a wave and step
     constexpr uint32_t NB = BO / 16, PP = NB / W;   // blocks of a row of w; of a thread and step
@@ -44,7 +48,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     const uint32_t rows = uint32_t(rt.end - rt.begin), o0 = at.col * BO;
 
     const uint32_t xstep = uint32_t(a.x_stride) * 2, wstep = uint32_t(a.wc_stride), sstep = uint32_t(a.ws_stride);
-    const auto xr = rsrc(static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2, (rows - 1) * xstep + a.n * 2);
+    const uint8_t* xb = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride * 2;
+    const auto xr = rsrc(xb, (rows - 1) * xstep + a.n * 2);
     const uint8_t* wb = a.wc + uint64_t(rt.group) * a.n * a.wc_stride + o0 / 2;
     const uint8_t* sb = a.ws + uint64_t(rt.group) * a.n * a.ws_stride + o0 / fp4_block(WF);
     // (a row's last eight bytes are read whole: they start on an 8-byte border)
@@ -173,15 +178,26 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             for (uint32_t i = 0; i < NI; ++i) held(acc[i][m]);
     };
 
-    // Any step, any alignment: into registers while the step before multiplies
-    // (zeros past the ends), then to LDS.
+    // Any alignment: into registers while the step before multiplies, then to
+    // LDS.  A piece of dy that the sum's end cuts is read as the row's last
+    // eight elements and moved down.
     u32x4 xn[XD];
-    auto fetch = [&](uint32_t step) {
+    auto fetch_x = [&](uint32_t step) {
+        if ((step + 1) * kBJ <= a.n) {
 #pragma unroll
-        for (uint32_t i = 0; i < XD; ++i) {
-            const uint16_t* p = static_cast<const uint16_t*>(a.x) + (rt.begin + min(lr + i * W * 8, rows - 1)) * a.x_stride;
-            xn[i] = bf16x8_any(p, step * kBJ + lc * 8, a.n);
+            for (uint32_t i = 0; i < XD; ++i) __builtin_memcpy(&xn[i], xb + step * kRowB + xo[i], 16);
+            return;
         }
+        const uint32_t j = step * kBJ + lc * 8, past = j - min(j, a.n - 8);
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i)
+            xn[i] = last_elements(xb + uint64_t(xo[i]) + step * kRowB - past * 2, past);
+    };
+    auto put_x = [&](uint8_t* buf) {
+#pragma unroll
+        for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(buf + (i * W + wave) * 1024 + lane * 16) = xn[i];
+    };
+    auto fetch_w = [&](uint32_t step) {
 #pragma unroll
         for (uint32_t i = 0; i < PP; ++i) {
             const uint32_t j = step * kBJ + row0 + i * RP, c = blk * 16;   // (columns from o0 on)
@@ -195,20 +211,26 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     };
     const std::integral_constant<uint32_t, 0> even;
     const std::integral_constant<uint32_t, 1> odd;
-    if constexpr (!ALIGNED) {
-        fetch(first);
+    if constexpr (!CODES) {
+        fetch_x(first);
+        fetch_w(first);
 #pragma unroll 1
         for (uint32_t t = first; t < steps; ++t) {
             __syncthreads();
-#pragma unroll
-            for (uint32_t i = 0; i < XD; ++i) *reinterpret_cast<u32x4*>(x0 + (i * W + wave) * 1024 + lane * 16) = xn[i];
+            put_x(x0);
             convert(w0, even);
             __syncthreads();
-            compute(x0, w0, [&] { fetch(t + 1); });   // (past the last: zeros)
+            compute(x0, w0, [&] {   // (past the last: zeros)
+                fetch_x(t + 1);
+                fetch_w(t + 1);
+            });
         }
     }
-    if (ALIGNED && first < steps) {
-        load_x(x0, first);
+    if (CODES && first < steps) {
+        if constexpr (ALIGNED)
+            load_x(x0, first);
+        else
+            fetch_x(first), put_x(x0);
         load_w(first, even);
         if (AHEAD == 2) load_w(first + 1, odd);
         convert(w0, even);
@@ -218,57 +240,62 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     // step past the last is all zeros
     // (the codes are converted before the next loads are issued: a wait for them
     // would be a wait for those too)
-    for (uint32_t t = first; ALIGNED && t < steps; t += 2) {
-        step_barrier<2 * PP>();   // dy is older than the last loads of codes and scales
+    for (uint32_t t = first; CODES && t < steps; t += 2) {
+        step_barrier<ALIGNED ? 2 * PP : 63>();   // dy is older than the last loads of codes and scales
         convert(w1, odd);
         compute(x0, w0, [&] {
-            load_x(x1, t + 1);
+            ALIGNED ? load_x(x1, t + 1) : fetch_x(t + 1);
             load_w(t + 1 + AHEAD, odd);
         });
-        step_barrier<2 * PP>();
+        if constexpr (!ALIGNED) put_x(x1);
+        step_barrier<ALIGNED ? 2 * PP : 63>();
         convert(w0, even);
         compute(x1, w1, [&] {
-            load_x(x0, t + 2);
+            ALIGNED ? load_x(x0, t + 2) : fetch_x(t + 2);
             load_w(t + 2 + AHEAD, even);
         });
+        if constexpr (!ALIGNED) put_x(x0);
     }
     step_barrier<0>();
     store_block<OUT, BM, BO, W, WM, kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,
                                              wn * (BO / WN), a.k, w0, w1);
 }
 
-template <uint32_t WF, typename OUT>
-void launch(const MArgs& a, hipStream_t st, uint32_t bm, bool aligned) {
+template <uint32_t WF, typename OUT, Rows ROWS>
+void launch_tile(const MArgs& a, hipStream_t st, uint32_t bm) {
     const dim3 g(a.grid);
-    if (bm == 256)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4, true>), g, dim3(512), 0, st, a);
-    else if (bm == 128 && aligned)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2, true>), g, dim3(256), 0, st, a);
-    else if (bm == 64 && aligned)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 64, 128, 1, 4, true>), g, dim3(256), 0, st, a);
-    else if (bm == 32 && aligned)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4, true>), g, dim3(256), 0, st, a);
+    if (ROWS == Rows::kAligned && bm == 256)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 256, 256, 2, 4, Rows::kAligned>), g, dim3(512), 0, st, a);
     else if (bm == 128)
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2, false>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 128, 128, 2, 2, ROWS>), g, dim3(256), 0, st, a);
+    else if (ROWS != Rows::kAny && bm == 64)
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 64, 128, 1, 4, ROWS == Rows::kAny ? Rows::kCodes : ROWS>), g, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4, false>), g, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fp4_mm_grad_kernel<WF, OUT, 32, 128, 1, 4, ROWS>), g, dim3(256), 0, st, a);
+}
+template <uint32_t WF, typename OUT>
+void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
+    rows == Rows::kAligned ? launch_tile<WF, OUT, Rows::kAligned>(a, st, bm)
+    : rows == Rows::kCodes ? launch_tile<WF, OUT, Rows::kCodes>(a, st, bm)
+                           : launch_tile<WF, OUT, Rows::kAny>(a, st, bm);
 }
 
 }  // namespace
 
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile, and inside the rows of w of a step, are 30 bits
-    if (a.n >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
-    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostAny[4] = {0, 2000, 0, 900};
-    const bool aligned = a.x_vec && a.w_vec && a.n % 8 == 0;
-    const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ, aligned ? kCost : kCostAny);
+    if (a.n < 8 || a.n >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
+    constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostCodes[4] = {0, 1500, 950, 700}, kCostAny[4] = {0, 2000, 0, 900};
+    const Rows rows = !a.w_vec ? Rows::kAny : !a.x_vec || a.n % 8 ? Rows::kCodes : Rows::kAligned;
+    const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ,
+                                    rows == Rows::kAny ? kCostAny : rows == Rows::kCodes ? kCostCodes : kCost);
     if (!bm) return false;
     const MArgs p = fp4_mm_parts(a, a.k, ws);
     const bool wide = f32 || a.splits > 1;
     if (fmt == DCR_FP4_MX)
-        wide ? launch<DCR_FP4_MX, float>(p, st, bm, aligned) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, aligned);
+        wide ? launch<DCR_FP4_MX, float>(p, st, bm, rows) : launch<DCR_FP4_MX, uint16_t>(p, st, bm, rows);
     else
-        wide ? launch<DCR_FP4_NV, float>(p, st, bm, aligned) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, aligned);
+        wide ? launch<DCR_FP4_NV, float>(p, st, bm, rows) : launch<DCR_FP4_NV, uint16_t>(p, st, bm, rows);
     fp4_mm_join(a, a.k, fmt, f32, ws, st);
     return true;
 }

@@ -217,7 +217,7 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     if (!grad && fp4_mm_rows(a, xq != nullptr, w->format, f32, st)) return fp4_launched();
     if (!xq && !grad && fp4_mm_tile(a, w->format, f32, ws, st)) return fp4_launched();
     if (xq && fp4_mm_tile4(a, f32, ws, st)) return fp4_launched();
-    if (grad && n && fp4_mm_grad(a, w->format, f32, ws, st)) return fp4_launched();
+    if (grad && fp4_mm_grad(a, w->format, f32, ws, st)) return fp4_launched();
     a.row_tiles = uint32_t(row_tile_bound(a, kGT));
     a.col_tiles = uint32_t((outs + kGT - 1) / kGT);
     const uint64_t tiles = uint64_t(a.row_tiles) * a.col_tiles;

@@ -102,24 +102,23 @@ __device__ __forceinline__ u32x4 codes32(const uint8_t* row, uint32_t k, uint32_
     return u32x4{a[0], a[1], b[0], b[1]};
 }
 
-// eight bf16 of a row from element k, at any alignment; zeros from `cols` on
-__device__ __forceinline__ u32x4 bf16x8_any(const uint16_t* row, uint32_t k, uint32_t cols) {
-    u32x4 v = {0, 0, 0, 0};
-    if (k + 8 <= cols) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
-#pragma unroll
-        for (uint32_t e = 0; e < 8; ++e)
-            if (k + e < cols) v[e / 2] |= uint32_t(row[k + e]) << (16 * (e & 1));
-    }
-    return v;
-}
-
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<bf16x4*>(p) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+
+// The eight elements at `p`, any alignment, moved down by `past`: zeros move in.
+__device__ __forceinline__ u32x4 last_elements(const uint8_t* p, uint32_t past) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    uint64_t lo = v[0] | uint64_t(v[1]) << 32, hi = v[2] | uint64_t(v[3]) << 32;
+    const uint32_t bits = min(past, 8u) * 16, n = bits & 63u;
+    lo = bits >= 64 ? hi : lo, hi = bits >= 64 ? 0 : hi;
+    lo = n ? lo >> n | hi << (64 - n) : lo, hi >>= n;
+    lo = bits >= 128 ? 0 : lo;
+    return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
 }
 
 // Buffer descriptor: loads take a scalar base and step and a 32-bit lane

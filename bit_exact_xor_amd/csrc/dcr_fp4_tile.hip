@@ -155,15 +155,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         const uint32_t c = step * kBK + (r16 ^ swizzle(wave * 4 + quad)) * 8, past = c - min(c, a.k - 8);
 #pragma unroll
         for (uint32_t i = 0; i < DMA; ++i) {
-            u32x4 v;
-            __builtin_memcpy(&v, xb + uint64_t(xo[i]) + step * kRowB - past * 2, 16);
-            uint64_t lo = v[0] | uint64_t(v[1]) << 32, hi = v[2] | uint64_t(v[3]) << 32;
-            const uint32_t bits = min(past, 8u) * 16;
-            lo = bits >= 64 ? hi : lo, hi = bits >= 64 ? 0 : hi;
-            const uint32_t n = bits & 63u;
-            lo = n ? lo >> n | hi << (64 - n) : lo, hi >>= n;
-            lo = bits >= 128 ? 0 : lo;
-            xn[i] = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+            xn[i] = last_elements(xb + uint64_t(xo[i]) + step * kRowB - past * 2, past);
         }
     };
     auto put_x = [&](uint8_t* buf) {
