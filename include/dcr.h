@@ -634,9 +634,11 @@ int32_t dcr_fp4_dequantize(const dcr_fp4_tensor* q, void* y, uint32_t y_type, ui
  *              aligned, one call at a time
  * Products of the operands are exact, sums are held in fp32, and each result
  * is rounded once to y's type after the tensor scale.  The order of a sum
- * depends on the sizes alone, so equal calls give equal bits.
- * A NaN scale makes the results of its row NaN.  x and y may have any
- * alignment of whole elements; rows that start on 16-byte borders are faster. */
+ * depends on sizes, strides and alignments alone, so equal calls give equal
+ * bits.  A NaN scale makes the results of its row NaN.  x and y may have any
+ * alignment of whole elements; rows that start on 16-byte borders are faster,
+ * and so are rows of codes 16 bytes and of scales 8 (MX) or 16 (NV) bytes
+ * apart or a multiple of that. */
 #define DCR_FP4_WORKSPACE_BYTES (64u << 20)
 int32_t dcr_fp4_matmul(const void* x, uint64_t m, uint64_t x_stride, const dcr_fp4_tensor* w,
                        const int32_t* offsets, uint32_t n_groups, void* y, uint32_t y_type, uint64_t y_stride,
