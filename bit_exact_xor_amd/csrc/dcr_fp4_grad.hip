@@ -73,15 +73,17 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     const uint32_t lr = wave * 8 + (lane >> 3), lc = (lane & 7u) ^ swizzle8(lr);
     uint32_t xo[XD];
 #pragma unroll
-    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(lr + i * W * 8, rows - 1) * xstep + lc * 16;
-    auto load_x = [&](uint8_t* buf, uint32_t step) {
+    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(tile_row<BM, WM>(lr + i * W * 8), rows - 1) * xstep + lc * 16;
+    auto load_x = [&](uint8_t* buf, uint32_t step, auto subtiles) {
         if ((step + 1) * kBJ > a.n) {
             const uint32_t out = step * kBJ + lc * 8 < a.n ? 0u : kOutside;
 #pragma unroll
             for (uint32_t i = 0; i < XD; ++i) xo[i] |= out;
         }
 #pragma unroll
-        for (uint32_t i = 0; i < XD; ++i) load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
+        for (uint32_t i = 0; i < XD; ++i)
+            if (i * W * 8 % (BM / WM) < decltype(subtiles)::value * 16)
+                load_lds16(xr, buf + (i * W + wave) * 1024, xo[i], step * kRowB);
         __builtin_amdgcn_sched_barrier(0);   // (the step's wait counts the loads after these)
     };
     // 16 codes and their scale; rows past the sum's end and columns past the
@@ -127,8 +129,8 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     // tile, alone on its compute unit, all of a step's come before (390 -> 372
     // us at 4096 x 4096 x 14336); the others wait in the shade of their
     // neighbours and lose by the longer start (48 -> 53 us at 1024 x 4096 x 4096).
-    auto compute = [&](const uint8_t* xbuf, const uint8_t* wbuf, auto&& issue) {
-        constexpr uint32_t H = 2, P = MI / H;
+    auto compute = [&](const uint8_t* xbuf, const uint8_t* wbuf, auto subtiles, auto&& issue) {
+        constexpr uint32_t M = decltype(subtiles)::value, H = M < 2 ? M : 2, P = M / H;
         const uint8_t* xl = xbuf + (wm * (BM / WM) + r16) * kRowB;
         // a lane names four columns of a row and gets four rows of a column
         const uint32_t jr = quad * 8 + (r16 >> 2);
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
     };
     const std::integral_constant<uint32_t, 0> even;
     const std::integral_constant<uint32_t, 1> odd;
+    const std::integral_constant<uint32_t, MI> full;
     if constexpr (!CODES) {
         fetch_x(first);
         fetch_w(first);
@@ -220,41 +223,52 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_grad_kernel(MArgs a) {
             put_x(x0);
             convert(w0, even);
             __syncthreads();
-            compute(x0, w0, [&] {   // (past the last: zeros)
+            compute(x0, w0, full, [&] {   // (past the last: zeros)
                 fetch_x(t + 1);
                 fetch_w(t + 1);
             });
         }
     }
-    if (CODES && first < steps) {
-        if constexpr (ALIGNED)
-            load_x(x0, first);
-        else
-            fetch_x(first), put_x(x0);
-        load_w(first, even);
-        if (AHEAD == 2) load_w(first + 1, odd);
-        convert(w0, even);
-        load_w(first + AHEAD, even);
-    }
     // two steps a turn (one loop exit keeps the sums in their registers); a
     // step past the last is all zeros
     // (the codes are converted before the next loads are issued: a wait for them
     // would be a wait for those too)
-    for (uint32_t t = first; CODES && t < steps; t += 2) {
-        step_barrier<ALIGNED ? 2 * PP : 63>();   // dy is older than the last loads of codes and scales
-        convert(w1, odd);
-        compute(x0, w0, [&] {
-            ALIGNED ? load_x(x1, t + 1) : fetch_x(t + 1);
-            load_w(t + 1 + AHEAD, odd);
-        });
-        if constexpr (!ALIGNED) put_x(x1);
-        step_barrier<ALIGNED ? 2 * PP : 63>();
-        convert(w0, even);
-        compute(x1, w1, [&] {
-            ALIGNED ? load_x(x0, t + 2) : fetch_x(t + 2);
-            load_w(t + 2 + AHEAD, even);
-        });
-        if constexpr (!ALIGNED) put_x(x0);
+    auto steps_of = [&](auto subtiles) {
+        if (first < steps) {
+            if constexpr (ALIGNED)
+                load_x(x0, first, subtiles);
+            else
+                fetch_x(first), put_x(x0);
+            load_w(first, even);
+            if (AHEAD == 2) load_w(first + 1, odd);
+            convert(w0, even);
+            load_w(first + AHEAD, even);
+        }
+        for (uint32_t t = first; t < steps; t += 2) {
+            step_barrier<ALIGNED ? 2 * PP : 63>();   // dy is older than the last loads of codes and scales
+            convert(w1, odd);
+            compute(x0, w0, subtiles, [&] {
+                ALIGNED ? load_x(x1, t + 1, subtiles) : fetch_x(t + 1);
+                load_w(t + 1 + AHEAD, odd);
+            });
+            if constexpr (!ALIGNED) put_x(x1);
+            step_barrier<ALIGNED ? 2 * PP : 63>();
+            convert(w0, even);
+            compute(x1, w1, subtiles, [&] {
+                ALIGNED ? load_x(x0, t + 2, subtiles) : fetch_x(t + 2);
+                load_w(t + 2 + AHEAD, even);
+            });
+            if constexpr (!ALIGNED) put_x(x0);
+        }
+    };
+    if constexpr (CODES) {
+        // a group's last tile is often less than half full: 4096 rows of 128
+        // experts through 768 x 2048 59.7 -> 56.4 us
+        constexpr bool HALF = ALIGNED && (BM == 64 || BM == 128);
+        if (HALF && rows <= BM / 2)
+            steps_of(std::integral_constant<uint32_t, HALF ? MI / 2 : MI>());
+        else
+            steps_of(full);
     }
     step_barrier<0>();
     store_block<OUT, BM, BO, W, WM, kW>(a, acc, WF == DCR_FP4_NV && a.splits == 1 ? *a.tensor_scale : 1.0f, rt, at, wm,

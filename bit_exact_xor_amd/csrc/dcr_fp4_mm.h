@@ -200,6 +200,16 @@ __device__ __forceinline__ void static_for(F&& f) {
     }
 }
 
+// Row of a tile that is kept in row `l` of LDS: where WM waves share the rows
+// they take every WM-th 16 of them, so that a tile that is less than half full
+// is half of the work for each (tiles of 256 rows have no such form).
+template <uint32_t BM, uint32_t WM>
+__device__ __forceinline__ uint32_t tile_row(uint32_t l) {
+    if constexpr (WM == 1 || BM == 256) return l;
+    constexpr uint32_t R = BM / WM;
+    return (l % R / 16 * WM + l / R) * 16 + (l & 15u);
+}
+
 // A workgroup's BM x BN sums, times s, rounded once.  A lane holds four
 // neighbouring results of one row in each 16 x 16 subtile: stored as they are
 // they make 32-byte pieces of lines, which cost as much time as the product
@@ -207,7 +217,8 @@ __device__ __forceinline__ void static_for(F&& f) {
 // LDS, half of a pass's rows in `lo` and half in `hi` (HB bytes each, unused
 // by then), and leave as whole rows of the tile.  16-byte pieces of a row sit
 // at place p ^ row, which spreads both directions over the banks.
-// WM waves share the rows, `wm` this one's part; its columns start at `wcol`.
+// WM waves share the rows (see tile_row), `wm` this one's part; its columns
+// start at `wcol`.
 template <typename OUT, uint32_t BM, uint32_t BN, uint32_t W, uint32_t WM, uint32_t HB, uint32_t MI, uint32_t NI>
 __device__ __forceinline__ void store_block(const MArgs& a, const f32x4 (&acc)[NI][MI], float s, const RowTile& rt,
                                             const TilePlace& at, uint32_t wm, uint32_t wcol, uint32_t outs, uint8_t* lo,
@@ -243,7 +254,7 @@ __device__ __forceinline__ void store_block(const MArgs& a, const f32x4 (&acc)[N
             const bool up = i * RI >= HR;
             const uint32_t lr = (up ? i * RI - HR : i * RI) + row_in;      // in its half
             const u32x4 v = *reinterpret_cast<const u32x4*>((up ? hi : lo) + lr * RB + (piece ^ (lr & 15u)) * 16);
-            const uint32_t r = WM == 1 ? p * RP + i * RI + row_in : (up ? BM / 2 : 0) + p * RPW + lr;
+            const uint32_t r = tile_row<BM, WM>(WM == 1 ? p * RP + i * RI + row_in : (up ? BM / 2 : 0) + p * RPW + lr);
             if (r >= rows) continue;
             OUT* out = y + (rt.begin + r) * a.y_stride + col;
             if (col + E <= outs) {

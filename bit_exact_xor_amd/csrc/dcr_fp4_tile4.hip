@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint8_t* srows = xside ? a.xs + rt.begin * a.xs_stride : sb;
     const uint32_t skew = SV ? 0 : uint32_t(reinterpret_cast<uintptr_t>(srows)) & 3u;
     const auto sr = rsrc(srows - skew, (skew + last * sstep + blocks + 3) & ~3u);
-    const uint32_t soff = skew + min(srow, last) * sstep;
+    const uint32_t soff = skew + min(xside ? tile_row<BM, WM>(srow) : srow, last) * sstep;
     const uint32_t subs = xside ? BM / 16 : BN / 16;
     const uint32_t sdst = (xside ? 0 : BM * (kBK / 32)) + (srow & 15u) * subs + (srow >> 4);
 
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
     const uint32_t lr = wave * 8 + (lane >> 3), lc = (lane & 7u) ^ swizzle8(lr);
     uint32_t xo[XD], wo[WD];
 #pragma unroll
-    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(lr + i * W * 8, rows - 1) * xstep + lc * 16;
+    for (uint32_t i = 0; i < XD; ++i) xo[i] = min(tile_row<BM, WM>(lr + i * W * 8), rows - 1) * xstep + lc * 16;
 #pragma unroll
     for (uint32_t i = 0; i < WD; ++i) wo[i] = min(lr + i * W * 8, cols - 1) * wstep + lc * 16;
     auto load = [&](uint8_t* buf, uint32_t step) {
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) fp4_mm_tile4_kernel(MArgs a) 
         const uint32_t k = step * kBK + lc * 32;
         const uint8_t* x = static_cast<const uint8_t*>(a.x) + rt.begin * a.x_stride;
 #pragma unroll
-        for (uint32_t i = 0; i < XD; ++i) xnext[i] = codes32(x + uint64_t(min(lr + i * W * 8, rows - 1)) * xstep, k, a.k, a.x_vec);
+        for (uint32_t i = 0; i < XD; ++i) xnext[i] = codes32(x + uint64_t(min(tile_row<BM, WM>(lr + i * W * 8), rows - 1)) * xstep, k, a.k, a.x_vec);
 #pragma unroll
         for (uint32_t i = 0; i < WD; ++i) wnext[i] = codes32(wb + uint64_t(min(lr + i * W * 8, cols - 1)) * wstep, k, a.k, a.w_vec);
         sn = load_scales(step);
