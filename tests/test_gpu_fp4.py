@@ -566,3 +566,43 @@ def test_product_sums_of_whole_pieces(op, fmt, k):
     for m, n in [(3, 40), (24, 136), (70, 1000), (280, 264)]:
         check_product(op, fmt, m, n, k, "fp32", "whole")
         check_product(op, fmt, m, k, n, "fp32", "whole", x_pad=-k % 8)
+
+
+@pytest.mark.parametrize("m", [6, 150])
+def test_graph_of_groups(m):
+    """Captured products of experts, replayed with other rows and other offsets: the eager bits every time."""
+    rng = np.random.default_rng(m)
+    ws, ws2 = dcr.fp4_workspace(), dcr.fp4_workspace()
+    q, _ = whole_fp4(8 * 320, 448, R.NV, rng)
+    qm, _ = whole_fp4(8 * 320, 448, R.MX, rng)
+    x, off = torch.empty(m, 448, dtype=torch.bfloat16, device="cuda"), torch.zeros(9, dtype=torch.int32, device="cuda")
+    x4 = dcr.Fp4Tensor(m, 448)
+    y, dx, y4 = (torch.empty(m, n, device="cuda") for n in (320, 448, 320))
+
+    def step(work):
+        dcr.dcr_fp4_matmul(x, q, y, off, work)
+        dcr.dcr_fp4_matmul_grad(y.bfloat16(), q, dx, off, work)
+        dcr.dcr_fp4_quantize(x, x4)
+        dcr.dcr_fp4_matmul_q(x4, qm, y4, off, work)
+
+    def fill(i):
+        r = np.random.default_rng(100 * m + i)
+        cuts = np.sort(r.integers(0, m + 1, 7)) if i else np.full(7, m)
+        off.copy_(up(np.concatenate([[0], cuts, [m]]).astype(np.int32)))
+        x.copy_(up(r.standard_normal((m, 448))))
+        y.zero_(), dx.zero_(), y4.zero_()
+
+    fill(0)
+    step(ws2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(ws2)
+    for i in (1, 0, 2, 3, 1):
+        fill(i)
+        step(ws)
+        want = [t.clone() for t in (y, dx, y4)]
+        fill(i)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((y, dx, y4), want)), i
