@@ -39,6 +39,15 @@ inline int32_t fp4_launched() {
     return DCR_OK;
 }
 
+// DCR_OK, or the refusal of a description's tensor scale
+inline int32_t fp4_check_scale(const dcr_fp4_tensor* t, const std::string& w) {
+    if (t->format != DCR_FP4_NV) return DCR_OK;
+    if (!t->tensor_scale) return fp4_fail(DCR_E_INVAL, w + ": NULL tensor scale");
+    if (reinterpret_cast<uintptr_t>(t->tensor_scale) & 3u)
+        return fp4_fail(DCR_E_INVAL, w + ": tensor scale not 4-byte aligned");
+    return DCR_OK;
+}
+
 // DCR_OK, or the refusal of a tensor description
 inline int32_t fp4_check(const dcr_fp4_tensor* t, const char* what) {
     const std::string w = what;
@@ -55,11 +64,7 @@ inline int32_t fp4_check(const dcr_fp4_tensor* t, const char* what) {
             return fp4_fail(DCR_E_INVAL, w + ": a row stride is smaller than a row");
         if (t->code_stride >= (uint64_t(1) << 32) || t->scale_stride >= (uint64_t(1) << 32))
             return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^32 bytes or more");
-        if (t->format == DCR_FP4_NV) {
-            if (!t->tensor_scale) return fp4_fail(DCR_E_INVAL, w + ": NULL tensor scale");
-            if (reinterpret_cast<uintptr_t>(t->tensor_scale) & 3u)
-                return fp4_fail(DCR_E_INVAL, w + ": tensor scale not 4-byte aligned");
-        }
+        return fp4_check_scale(t, w);
     }
     return DCR_OK;
 }

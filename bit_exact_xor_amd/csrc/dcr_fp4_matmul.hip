@@ -191,6 +191,8 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
     if (!ws || !al16(ws)) return fp4_fail(DCR_E_INVAL, "workspace is NULL or not 16-byte aligned");
     if (ws_bytes < DCR_FP4_WORKSPACE_BYTES) return fp4_fail(DCR_E_CAPACITY, "workspace too small");
     if (!m || !outs) return DCR_OK;
+    // (sums of nothing are zeros that the kernels multiply with the scale too)
+    if ((rc = fp4_check_scale(w, "weights"))) return rc;
     MArgs a{};
     a.x = xq ? xq->codes : x;
     a.m = m;

@@ -77,6 +77,20 @@ def test_bad_product_of_two():
     assert matmul_q(n=0) == dcr.DCR_E_CAPACITY
 
 
+@pytest.mark.parametrize("ts", [None, AT + 2])
+def test_bad_scale_of_empty_sums(ts):
+    """Weights without columns (the gradient: without rows) still give results, zeros, and the kernels read the tensor
+    scale for them; with no results nothing is read."""
+    for kw in (dict(d=desc(cols=0, fmt=1, ts=ts)), dict(d=desc(rows=0, fmt=1, ts=ts), grad=True),
+               dict(d=desc(rows=0, fmt=1, ts=ts), grad=True, g=4, off=AT)):
+        assert matmul(**kw) == dcr.DCR_E_INVAL, kw
+        assert b"tensor scale" in dcr.load_library().dcr_last_error()
+        assert matmul(m=0, **kw) == dcr.DCR_OK, kw
+    assert matmul(desc(rows=0, fmt=1, ts=ts)) == dcr.DCR_OK
+    assert matmul(desc(cols=0, fmt=1, ts=ts), grad=True) == dcr.DCR_OK
+    assert quantize(desc(rows=0, fmt=1, ts=ts)) == dcr.DCR_OK and dequantize(desc(cols=0, fmt=1, ts=ts)) == dcr.DCR_OK
+
+
 def test_binding_refuses():
     """Python-side checks: host tensors, shapes and types, before the library is called."""
     with pytest.raises(ValueError):
