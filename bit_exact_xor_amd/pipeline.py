@@ -144,6 +144,24 @@ class HostLoopback:
                           apply_workspace, stream=self.apply_stream)
         return res
 
+    def receive_retry(self, header, canon, apply_workspace, base_version):
+        """The receiver of a RETRY stream in host memory: the whole stream
+        host -> device, then its overwrites, whatever an interrupted apply
+        has already written.  Returns the apply result; the caller
+        synchronises the apply stream."""
+        import torch
+        n, pb = _u64(header, 40), _u64(header, 48)
+        self._fits(n, pb)
+        with torch.cuda.stream(self.h2d):
+            self.rdir[:n * 32].copy_(self.host_dir[:n * 32], non_blocking=True)
+            self.rpayload[:pb].copy_(self.host_payload[:pb], non_blocking=True)
+        self.h2d.synchronize()
+        with torch.cuda.stream(self.apply_stream):
+            res = torch.empty(32, dtype=torch.uint8, device=self.device)
+            dcr.dcr_apply_overwrite_retry(self.plan, canon, header, self.rdir, self.rpayload, base_version, res,
+                                          apply_workspace, stream=self.apply_stream)
+        return res
+
     # ------------------------------------------------- both on one GPU
     def run(self, old_shards, new_shards, mode, base_version, new_version, sb: "dcr.StreamBuffers", workspace,
             n_slices: int, canon, flags, apply_workspace):
@@ -170,12 +188,18 @@ class Fp4Refit:
     canonical tensors of one-byte elements carried as XOR masks, an NV tensor
     scale is one fp32 element carried as an overwrite.  The first refit takes
     the NV tensor scales from the weights and sends everything; later ones keep
-    them (so that few bytes change) unless `calibrate` is passed."""
+    them (so that few bytes change) unless `calibrate` is passed.
+
+    A refit that raises once it has begun to send may have patched part of
+    `held` (`interrupted`): the masks must not be applied again, and products
+    are refused.  recover() finishes it, the same change set as overwrites; so
+    does the next refit before it starts."""
 
     def __init__(self, shapes, fmt=dcr.FP4_NV, device="cuda", n_slices=4):
         import torch
         self.fmt, self.device, self.n_slices = fmt, device, n_slices
         self.version = 0
+        self.interrupted = False
         self.sent, self.next, self.held = ([dcr.Fp4Tensor(r, c, fmt, device) for r, c in shapes] for _ in range(3))
         for side in (self.sent, self.next, self.held):
             for t in side:
@@ -220,6 +244,7 @@ class Fp4Refit:
         import torch
         if len(weights) != len(self.next):
             raise ValueError(f"{len(self.next)} weights expected, got {len(weights)}")
+        self.recover()
         calibrate = self.fmt == dcr.FP4_NV and (calibrate or self.version == 0)
         for w, q, old in zip(weights, self.next, self.sent):
             if q.tensor_scale is not None and not calibrate:
@@ -228,21 +253,47 @@ class Fp4Refit:
         self.flags.zero_()
         # the receiver's streams wait for the flags and for earlier products
         self.link.apply_stream.wait_stream(torch.cuda.current_stream())
-        heads, results = self.link.run(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_DELTA,
-                                       self.version, self.version + 1, self.stream, self.encode_workspace,
-                                       self.n_slices, self._buffers(self.held), self.flags, self.apply_workspace)
+        self.interrupted = True          # until all of it has arrived
+        try:
+            heads, results = self.link.run(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_DELTA,
+                                           self.version, self.version + 1, self.stream, self.encode_workspace,
+                                           self.n_slices, self._buffers(self.held), self.flags, self.apply_workspace)
+            self._arrived(results)
+        except BaseException:
+            # (the next call uses its buffers: nothing may be in flight)
+            for s in (torch.cuda.current_stream(), self.link.d2h, self.link.h2d, self.link.apply_stream):
+                s.synchronize()
+            raise
+        return _u64(heads[-1], 48)
+
+    def recover(self):
+        """Finish an interrupted refit: the bytes that it changes, sent again
+        as overwrites (idempotent, so what its applies have done does not
+        matter).  Nothing is done where none was interrupted."""
+        import torch
+        if not self.interrupted:
+            return
+        header = self.link.send_serial(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_RETRY, self.version,
+                                       self.version + 1, self.stream, self.encode_workspace)
+        self.link.d2h.synchronize()
+        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
+        self._arrived([self.link.receive_retry(header, self._buffers(self.held), self.apply_workspace, self.version)])
+
+    def _arrived(self, results):
+        """Wait for the applies of a stream; with all of it in `held`, the
+        next version is the sent one."""
         self.link.apply_stream.synchronize()
         for r in results:
             bad = dcr.apply_result(r)
             if int(bad["n_invalid"]):
-                raise dcr.DcrError(dcr.DCR_E_FORMAT, "Fp4Refit.refit", f"{int(bad['n_invalid'])} records refused")
-        self.sent, self.next = self.next, self.sent
-        self.version += 1
-        return _u64(heads[-1], 48)
+                raise dcr.DcrError(dcr.DCR_E_FORMAT, "Fp4Refit", f"{int(bad['n_invalid'])} records refused")
+        self.sent, self.next, self.version, self.interrupted = self.next, self.sent, self.version + 1, False
 
     def matmul(self, i, x, out_dtype=None, offsets=None):
         """x w^T with the receiver's weight i (see dcr_fp4_matmul)."""
         import torch
+        if self.interrupted:
+            raise dcr.DcrError(dcr.DCR_E_VERSION, "Fp4Refit.matmul", "the last refit was interrupted: recover() first")
         w = self.held[i]
         n = w.rows if offsets is None else w.rows // (offsets.numel() - 1)
         y = torch.empty(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)

@@ -1,0 +1,94 @@
+"""Refits of 4-bit weights that go wrong, that share a GPU with products on other streams, and products of groups."""
+import numpy as np
+import pytest
+import torch
+
+from bit_exact_xor_amd import dcr, pipeline
+from tests import fp4_ref as R
+from tests.test_gpu_fp4 import bound, f64, up
+
+pytestmark = pytest.mark.gpu
+SHAPES = [(768, 2048), (130, 96), (33, 70)]
+
+
+def weights(seed, shapes=SHAPES):
+    rng = np.random.default_rng(seed)
+    return [up((0.02 * rng.standard_normal(s)).astype(np.float32)) for s in shapes]
+
+
+def check_held(link, fmt, w):
+    """The receiver holds the bytes of w, under the tensor scale that the sender took."""
+    for t, q, sent in zip(w, link.held, link.sent):
+        s = float(q.tensor_scale) if fmt == R.NV else 1.0
+        assert fmt == R.MX or s == float(sent.tensor_scale)
+        c, b = R.quantize(t.cpu().numpy(), fmt, s)
+        assert np.array_equal(q.codes.cpu().numpy()[:, :c.shape[1]], c)
+        assert np.array_equal(q.scales.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("where", ["send", "apply", "refused"])
+@pytest.mark.parametrize("then", ["same", "other", "recover"])
+def test_refit_after_a_failure(fmt, where, then, monkeypatch):
+    """A refit that fails before, within or after its applies leaves weights that no product takes; the next refit, or
+    recover(), ends at the bytes it should have given."""
+    link = pipeline.Fp4Refit(SHAPES, fmt)
+    w0, w1, w2 = weights(0), weights(1), weights(2)
+    link.refit(w0)
+    x = torch.ones(3, 2048, dtype=torch.bfloat16, device="cuda")
+    real = dcr.dcr_apply
+
+    def broken_apply(plan, canon, header, dirs, payload, flags, first, n, *rest, **kw):
+        real(plan, canon, header, dirs, payload, flags, first, max(1, n // 2), *rest, **kw)
+        raise RuntimeError("planted")
+
+    def broken_wait(*_args):
+        raise RuntimeError("planted")
+
+    def refusing_result(t):
+        r = np.zeros(1, dcr.APPLY_RESULT)
+        r["n_invalid"] = 1
+        return r[0]
+
+    with monkeypatch.context() as mp:
+        if where == "apply":
+            mp.setattr(dcr, "dcr_apply", broken_apply)
+        elif where == "send":
+            mp.setattr(dcr, "dcr_ready_wait", broken_wait)
+        else:
+            mp.setattr(dcr, "apply_result", refusing_result)
+        with pytest.raises(RuntimeError):
+            link.refit(w1)
+        assert link.version == 1
+    with pytest.raises(dcr.DcrError):
+        link.matmul(0, x)
+    if then == "recover":
+        link.recover()
+        assert link.version == 2
+        check_held(link, fmt, w1)
+        link.matmul(0, x)
+    w = w2 if then == "other" else w1
+    link.refit(w)
+    assert link.version == 3
+    check_held(link, fmt, w)
+    assert link.refit(w) == 0
+    y = torch.empty(3, 768, device="cuda")
+    dcr.dcr_fp4_matmul(x, link.sent[0], y, None, link.fp4_workspace)
+    assert torch.equal(link.matmul(0, x, torch.float32), y)
+
+
+def test_refit_refused_before_it_sends():
+    """Weights of a wrong shape are refused before anything travels: products and the next refit are as if not called."""
+    link = pipeline.Fp4Refit(SHAPES, R.NV)
+    w0 = weights(0)
+    link.refit(w0)
+    w1 = weights(1)
+    with pytest.raises(ValueError):
+        link.refit([w1[0], w1[1], w1[2][:, 1:]])
+    link.matmul(1, torch.ones(3, 96, dtype=torch.bfloat16, device="cuda"))
+    check_held(link, R.NV, w0)
+    link.refit(w1)
+    assert link.version == 2
+    check_held(link, R.NV, w1)
+    link.recover()
+    assert link.version == 2
