@@ -193,13 +193,19 @@ class Fp4Refit:
     A refit that raises once it has begun to send may have patched part of
     `held` (`interrupted`): the masks must not be applied again, and products
     are refused.  recover() finishes it, the same change set as overwrites; so
-    does the next refit before it starts."""
+    does the next refit before it starts.
+
+    Calls come from one thread at a time, on any streams: a product reads the
+    weights as the calls before it left them, and has scratch memory of its
+    own.  Replays of a captured product are not seen here: a refit is called
+    when they are done."""
 
     def __init__(self, shapes, fmt=dcr.FP4_NV, device="cuda", n_slices=4):
         import torch
         self.fmt, self.device, self.n_slices = fmt, device, n_slices
         self.version = 0
         self.interrupted = False
+        self.products = {}               # stream -> event behind its last product since the last refit
         self.sent, self.next, self.held = ([dcr.Fp4Tensor(r, c, fmt, device) for r, c in shapes] for _ in range(3))
         for side in (self.sent, self.next, self.held):
             for t in side:
@@ -251,8 +257,7 @@ class Fp4Refit:
                 q.tensor_scale.copy_(old.tensor_scale)
             dcr.dcr_fp4_quantize(w, q, dcr.FP4_CALIBRATE if calibrate else 0, self.fp4_workspace)
         self.flags.zero_()
-        # the receiver's streams wait for the flags and for earlier products
-        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
+        self._before_applies()           # (the flags, too)
         self.interrupted = True          # until all of it has arrived
         try:
             heads, results = self.link.run(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_DELTA,
@@ -276,8 +281,16 @@ class Fp4Refit:
         header = self.link.send_serial(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_RETRY, self.version,
                                        self.version + 1, self.stream, self.encode_workspace)
         self.link.d2h.synchronize()
-        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
+        self._before_applies()
         self._arrived([self.link.receive_retry(header, self._buffers(self.held), self.apply_workspace, self.version)])
+
+    def _before_applies(self):
+        """The receiver's streams wait for what the current one holds and for
+        the products of all."""
+        import torch
+        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
+        for event in self.products.values():
+            self.link.apply_stream.wait_event(event)
 
     def _arrived(self, results):
         """Wait for the applies of a stream; with all of it in `held`, the
@@ -288,6 +301,7 @@ class Fp4Refit:
             if int(bad["n_invalid"]):
                 raise dcr.DcrError(dcr.DCR_E_FORMAT, "Fp4Refit", f"{int(bad['n_invalid'])} records refused")
         self.sent, self.next, self.version, self.interrupted = self.next, self.sent, self.version + 1, False
+        self.products.clear()
 
     def matmul(self, i, x, out_dtype=None, offsets=None):
         """x w^T with the receiver's weight i (see dcr_fp4_matmul)."""
@@ -297,5 +311,12 @@ class Fp4Refit:
         w = self.held[i]
         n = w.rows if offsets is None else w.rows // (offsets.numel() - 1)
         y = torch.empty(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
-        dcr.dcr_fp4_matmul(x, w, y, offsets, self.fp4_workspace)
+        # (torch hands memory that is free again to the same stream only, and
+        # to a capture its graph's own)
+        dcr.dcr_fp4_matmul(x, w, y, offsets, dcr.fp4_workspace(self.device))
+        if not torch.cuda.is_current_stream_capturing():
+            stream = torch.cuda.current_stream()
+            if stream.cuda_stream not in self.products:
+                self.products[stream.cuda_stream] = torch.cuda.Event()
+            self.products[stream.cuda_stream].record(stream)
         return y

@@ -92,3 +92,77 @@ def test_refit_refused_before_it_sends():
     check_held(link, R.NV, w1)
     link.recover()
     assert link.version == 2
+
+
+def test_refit_waits_for_products_on_other_streams():
+    """A product enqueued on a side stream before a refit reads the weights from before it."""
+    link = pipeline.Fp4Refit(SHAPES, R.MX)
+    link.refit(weights(0))
+    x = up(np.random.default_rng(5).standard_normal((40, 2048))).bfloat16()
+    old = link.matmul(0, x, torch.float32)
+    busy, sides = torch.zeros(1 << 26, device="cuda"), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for side in sides:
+        with torch.cuda.stream(side):
+            for _ in range(500):          # keeps the stream from its product for some time
+                busy.add_(1)
+            got.append(link.matmul(0, x, torch.float32))
+    assert not any(s.query() for s in sides)
+    link.refit(weights(1))
+    new = link.matmul(0, x, torch.float32)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, old) for y in got)
+    assert not torch.equal(new, old)
+
+
+def test_products_on_two_streams_at_once():
+    """Products that split their sums, on two streams together with a refit that takes tensor scales: the results of
+    one after the other."""
+    shape = (136, 4096)
+    link = pipeline.Fp4Refit([shape], R.NV)
+    w = weights(0, [shape])
+    link.refit(w)
+    rng = np.random.default_rng(6)
+    xs = [up(rng.standard_normal((700, 4096))).bfloat16() for _ in range(2)]
+    want = [link.matmul(0, x, torch.float32) for x in xs]
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(40):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(link.matmul(0, xs[i], torch.float32))
+    link.refit(w, calibrate=True)
+    torch.cuda.synchronize()
+    for ys, t in zip(got, want):
+        assert all(torch.equal(y, t) for y in ys)
+    check_held(link, R.NV, w)
+
+
+def test_captured_product():
+    """A product captured into a graph, replayed beside eager ones on another stream and after a refit."""
+    shape = (136, 4096)
+    link = pipeline.Fp4Refit([shape], R.NV)
+    rng = np.random.default_rng(7)
+    x, z = (up(rng.standard_normal((700, 4096))).bfloat16() for _ in range(2))
+    link.refit(weights(0, [shape]))
+    want_z = link.matmul(0, z, torch.float32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = link.matmul(0, x, torch.float32)
+    side = torch.cuda.Stream()
+    for seed in (0, 1, 2):
+        if seed:
+            link.refit(weights(seed, [shape]))
+            want_z = link.matmul(0, z, torch.float32)
+        want = link.matmul(0, x, torch.float32)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            y.zero_()
+            with torch.cuda.stream(side):
+                others = [link.matmul(0, z, torch.float32) for _ in range(4)]
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+            assert all(torch.equal(o, want_z) for o in others)
