@@ -19,6 +19,8 @@ Fp4Refit is the same path for weights that the receiver serves in 4 bits:
 the trainer's BF16 or fp32 weights are quantised, the bytes that changed
 travel, and the receiver multiplies with the tensors the apply has patched.
 """
+import contextlib
+
 import numpy as np
 
 from . import dcr
@@ -247,42 +249,49 @@ class Fp4Refit:
         send what changed and patch `held`; returns the payload bytes sent.
         The work runs on the current stream and the link's; `held` is patched
         when the call returns."""
-        import torch
         if len(weights) != len(self.next):
             raise ValueError(f"{len(self.next)} weights expected, got {len(weights)}")
         self.recover()
         calibrate = self.fmt == dcr.FP4_NV and (calibrate or self.version == 0)
-        for w, q, old in zip(weights, self.next, self.sent):
-            if q.tensor_scale is not None and not calibrate:
-                q.tensor_scale.copy_(old.tensor_scale)
-            dcr.dcr_fp4_quantize(w, q, dcr.FP4_CALIBRATE if calibrate else 0, self.fp4_workspace)
-        self.flags.zero_()
-        self._before_applies()           # (the flags, too)
-        self.interrupted = True          # until all of it has arrived
-        try:
+        with self._drained():
+            for w, q, old in zip(weights, self.next, self.sent):
+                if q.tensor_scale is not None and not calibrate:
+                    q.tensor_scale.copy_(old.tensor_scale)
+                dcr.dcr_fp4_quantize(w, q, dcr.FP4_CALIBRATE if calibrate else 0, self.fp4_workspace)
+            self.flags.zero_()
+            self._before_applies()           # (the flags, too)
+            self.interrupted = True          # until all of it has arrived
             heads, results = self.link.run(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_DELTA,
                                            self.version, self.version + 1, self.stream, self.encode_workspace,
                                            self.n_slices, self._buffers(self.held), self.flags, self.apply_workspace)
             self._arrived(results)
-        except BaseException:
-            # (the next call uses its buffers: nothing may be in flight)
-            for s in (torch.cuda.current_stream(), self.link.d2h, self.link.h2d, self.link.apply_stream):
-                s.synchronize()
-            raise
         return _u64(heads[-1], 48)
 
     def recover(self):
         """Finish an interrupted refit: the bytes that it changes, sent again
         as overwrites (idempotent, so what its applies have done does not
         matter).  Nothing is done where none was interrupted."""
-        import torch
         if not self.interrupted:
             return
-        header = self.link.send_serial(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_RETRY, self.version,
-                                       self.version + 1, self.stream, self.encode_workspace)
-        self.link.d2h.synchronize()
-        self._before_applies()
-        self._arrived([self.link.receive_retry(header, self._buffers(self.held), self.apply_workspace, self.version)])
+        with self._drained():
+            header = self.link.send_serial(self._buffers(self.sent), self._buffers(self.next), dcr.MODE_RETRY,
+                                           self.version, self.version + 1, self.stream, self.encode_workspace)
+            self.link.d2h.synchronize()
+            self._before_applies()
+            self._arrived([self.link.receive_retry(header, self._buffers(self.held), self.apply_workspace,
+                                                   self.version)])
+
+    @contextlib.contextmanager
+    def _drained(self):
+        """An error leaves when nothing is in flight: the next call, on
+        whatever stream, uses the same buffers."""
+        import torch
+        try:
+            yield
+        except BaseException:
+            for s in (torch.cuda.current_stream(), self.link.d2h, self.link.h2d, self.link.apply_stream):
+                s.synchronize()
+            raise
 
     def _before_applies(self):
         """The receiver's streams wait for what the current one holds and for

@@ -166,3 +166,27 @@ def test_captured_product():
             torch.cuda.synchronize()
             assert torch.equal(y, want)
             assert all(torch.equal(o, want_z) for o in others)
+
+
+def late(stream, busy):
+    """Work that keeps `stream` busy for some time."""
+    with torch.cuda.stream(stream):
+        for _ in range(500):
+            busy.add_(1)
+
+
+def test_refused_on_one_stream_refitted_on_another():
+    """What a refused refit has enqueued on its stream does not reach the next one's weights."""
+    link = pipeline.Fp4Refit(SHAPES, R.MX)
+    w0, w1 = weights(0), weights(1)
+    link.refit(w0)
+    side, busy = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    late(side, busy)
+    with torch.cuda.stream(side), pytest.raises(ValueError):
+        link.refit([w0[0] + 1, w0[1] + 1, w0[2][:, 1:]])
+    link.refit(w1)
+    torch.cuda.synchronize()
+    check_held(link, R.MX, w1)
+    assert all(torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales) for a, b in zip(link.held, link.sent))
+    assert link.refit(w1) == 0
