@@ -197,12 +197,22 @@ class Fp4Refit:
     are refused.  recover() finishes it, the same change set as overwrites; so
     does the next refit before it starts.
 
-    Calls come from one thread at a time, on any streams: a product reads the
-    weights as the calls before it left them, and has scratch memory of its
-    own.  Replays of a captured product are not seen here: a refit is called
-    when they are done."""
+    Calls come from one thread at a time, on any streams of the weights' GPU: a
+    product reads the weights as the calls before it left them, and has scratch
+    memory of its own.  Replays of a captured product are not seen here: a
+    refit is called when they are done."""
 
     def __init__(self, shapes, fmt=dcr.FP4_NV, device="cuda", n_slices=4):
+        import torch
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(device):
+            self._make(shapes, fmt, device, n_slices)
+            # (the first calls may come on other streams)
+            torch.cuda.current_stream().synchronize()
+
+    def _make(self, shapes, fmt, device, n_slices):
         import torch
         self.fmt, self.device, self.n_slices = fmt, device, n_slices
         self.version = 0
@@ -283,15 +293,17 @@ class Fp4Refit:
 
     @contextlib.contextmanager
     def _drained(self):
-        """An error leaves when nothing is in flight: the next call, on
-        whatever stream, uses the same buffers."""
+        """On the weights' GPU and its current stream; an error leaves when
+        nothing is in flight: the next call, on whatever stream, uses the same
+        buffers."""
         import torch
-        try:
-            yield
-        except BaseException:
-            for s in (torch.cuda.current_stream(), self.link.d2h, self.link.h2d, self.link.apply_stream):
-                s.synchronize()
-            raise
+        with torch.cuda.device(self.device):
+            try:
+                yield
+            except BaseException:
+                for s in (torch.cuda.current_stream(), self.link.d2h, self.link.h2d, self.link.apply_stream):
+                    s.synchronize()
+                raise
 
     def _before_applies(self):
         """The receiver's streams wait for what the current one holds and for
@@ -320,12 +332,13 @@ class Fp4Refit:
         w = self.held[i]
         n = w.rows if offsets is None else w.rows // (offsets.numel() - 1)
         y = torch.empty(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
-        # (torch hands memory that is free again to the same stream only, and
-        # to a capture its graph's own)
-        dcr.dcr_fp4_matmul(x, w, y, offsets, dcr.fp4_workspace(self.device))
-        if not torch.cuda.is_current_stream_capturing():
-            stream = torch.cuda.current_stream()
-            if stream.cuda_stream not in self.products:
-                self.products[stream.cuda_stream] = torch.cuda.Event()
-            self.products[stream.cuda_stream].record(stream)
+        with torch.cuda.device(self.device):
+            # (torch hands memory that is free again to the same stream only,
+            # and to a capture its graph's own)
+            dcr.dcr_fp4_matmul(x, w, y, offsets, dcr.fp4_workspace(self.device))
+            if not torch.cuda.is_current_stream_capturing():
+                stream = torch.cuda.current_stream()
+                if stream.cuda_stream not in self.products:
+                    self.products[stream.cuda_stream] = torch.cuda.Event()
+                self.products[stream.cuda_stream].record(stream)
         return y

@@ -190,3 +190,40 @@ def test_refused_on_one_stream_refitted_on_another():
     check_held(link, R.MX, w1)
     assert all(torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales) for a, b in zip(link.held, link.sent))
     assert link.refit(w1) == 0
+
+
+def test_made_on_one_stream_used_on_another():
+    """The first refit on another stream than the object was made on: its buffers hold what they should by then."""
+    side, busy = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    torch.cuda.synchronize()
+    late(side, busy)
+    with torch.cuda.stream(side):
+        link = pipeline.Fp4Refit(SHAPES, R.NV)
+    w = weights(0)
+    link.refit(w)
+    torch.cuda.synchronize()
+    check_held(link, R.NV, w)
+    assert link.refit(w) == 0
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_weights_on_another_gpu():
+    """Refit, recovery and product with the weights on a GPU that is not the current one."""
+    link = pipeline.Fp4Refit(SHAPES, R.NV, device="cuda:1")
+    for seed in (0, 1):
+        w = [t.to("cuda:1") for t in weights(seed)]
+        link.refit(w)
+        check_held(link, R.NV, w)
+    link.interrupted = True
+    link.recover()
+    y = link.matmul(0, torch.ones(3, 2048, dtype=torch.bfloat16, device="cuda:1"), torch.float32)
+    v = R.unit_values(link.held[0].codes.cpu().numpy(), link.held[0].scales.cpu().numpy(), 2048, R.NV)
+    s = float(link.held[0].tensor_scale)
+    ref, size = R.product(np.ones((3, 2048)), v)
+    assert torch.cuda.current_device() == 0 and (np.abs(f64(y) - ref * s) <= bound(size * s, ref * s, 2048, "fp32")).all()
+
+
+def test_device_is_the_one_it_was_made_on():
+    assert pipeline.Fp4Refit([(4, 32)], R.MX).device == torch.device("cuda", torch.cuda.current_device())
+    with pytest.raises(ValueError):
+        pipeline.Fp4Refit([(4, 32)], R.MX, device="cpu")
