@@ -325,13 +325,17 @@ class Fp4Refit:
         self.products.clear()
 
     def matmul(self, i, x, out_dtype=None, offsets=None):
-        """x w^T with the receiver's weight i (see dcr_fp4_matmul)."""
+        """x w^T with the receiver's weight i (see dcr_fp4_matmul).  With
+        `offsets`, rows of x in front of the first group and behind the last
+        give zeros."""
         import torch
         if self.interrupted:
             raise dcr.DcrError(dcr.DCR_E_VERSION, "Fp4Refit.matmul", "the last refit was interrupted: recover() first")
         w = self.held[i]
-        n = w.rows if offsets is None else w.rows // (offsets.numel() - 1)
-        y = torch.empty(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
+        _off, _g, n = dcr._groups(w, offsets)
+        # (the product leaves those rows as they are)
+        make = torch.empty if offsets is None else torch.zeros
+        y = make(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
         with torch.cuda.device(self.device):
             # (torch hands memory that is free again to the same stream only,
             # and to a capture its graph's own)

@@ -227,3 +227,29 @@ def test_device_is_the_one_it_was_made_on():
     assert pipeline.Fp4Refit([(4, 32)], R.MX).device == torch.device("cuda", torch.cuda.current_device())
     with pytest.raises(ValueError):
         pipeline.Fp4Refit([(4, 32)], R.MX, device="cpu")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, None])
+def test_product_rows_of_no_group_are_zeros(dtype):
+    """Rows in front of the first group and behind the last one (a padded batch) come back as zeros."""
+    link = pipeline.Fp4Refit([(4 * 48, 64)], R.MX)
+    w = weights(3, [(4 * 48, 64)])
+    link.refit(w)
+    x = up(np.random.default_rng(8).integers(-2, 3, (64, 64))).bfloat16()
+    off = [5, 20, 20, 41, 50]
+    torch.full((64, 48), 99.0, dtype=dtype or torch.bfloat16, device="cuda")    # (freed: what new memory holds)
+    y = f64(link.matmul(0, x, dtype, torch.tensor(off, dtype=torch.int32, device="cuda")))
+    c, b = R.quantize(w[0].cpu().numpy(), R.MX)
+    ref, size = R.product(f64(x), R.unit_values(c, b, 64, R.MX), off)
+    rows = np.isnan(ref).all(1)
+    assert rows.sum() == 19 and (y[rows] == 0).all()
+    assert (np.abs(y - ref) <= bound(size, ref, 64, "fp32" if dtype else "bf16"))[~rows].all()
+
+
+def test_product_refuses_offsets():
+    link = pipeline.Fp4Refit([(4 * 48, 64)], R.MX)
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    for off in (torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                torch.zeros(5, device="cuda"), torch.zeros(6, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            link.matmul(0, x, offsets=off)
