@@ -62,7 +62,7 @@ inline int32_t fp4_check(const dcr_fp4_tensor* t, const char* what) {
         if (t->rows > 1 && (t->code_stride < (t->cols + 1) / 2 ||
                             t->scale_stride < (t->cols + fp4_block(t->format) - 1) / fp4_block(t->format)))
             return fp4_fail(DCR_E_INVAL, w + ": a row stride is smaller than a row");
-        if (t->code_stride >= (uint64_t(1) << 32) || t->scale_stride >= (uint64_t(1) << 32))
+        if (t->rows > 1 && (t->code_stride >= (uint64_t(1) << 32) || t->scale_stride >= (uint64_t(1) << 32)))
             return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^32 bytes or more");
         return fp4_check_scale(t, w);
     }

@@ -382,7 +382,7 @@ int32_t check_wide(const void* x, uint32_t type, uint64_t stride, const dcr_fp4_
     if (reinterpret_cast<uintptr_t>(x) & (type == DCR_F32 ? 3u : 1u))
         return fp4_fail(DCR_E_INVAL, w + ": not aligned to its elements");
     if (t.rows > 1 && stride < t.cols) return fp4_fail(DCR_E_INVAL, w + ": row stride smaller than a row");
-    if (stride >= (uint64_t(1) << 40)) return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^40 elements or more");
+    if (t.rows > 1 && stride >= (uint64_t(1) << 40)) return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^40 elements or more");
     return DCR_OK;
 }
 

@@ -152,7 +152,7 @@ int32_t check_rows(const void* p, uint64_t rows, uint64_t cols, uint64_t stride,
     if (!p) return fp4_fail(DCR_E_INVAL, w + ": NULL");
     if (reinterpret_cast<uintptr_t>(p) & (elem - 1)) return fp4_fail(DCR_E_INVAL, w + ": not aligned to its elements");
     if (rows > 1 && stride < cols) return fp4_fail(DCR_E_INVAL, w + ": row stride smaller than a row");
-    if (stride >= (uint64_t(1) << 40)) return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^40 elements or more");
+    if (rows > 1 && stride >= (uint64_t(1) << 40)) return fp4_fail(DCR_E_INVAL, w + ": row stride of 2^40 elements or more");
     return DCR_OK;
 }
 

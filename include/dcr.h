@@ -580,9 +580,10 @@ enum { DCR_FP4_CALIBRATE = 1 };
  *   tensor_scale  DCR_FP4_NV: one fp32 in device memory (4-byte aligned),
  *                 from 2^-100 to 2^117; DCR_FP4_MX: not looked at
  *   reserved      0
- * codes and scales are 16-byte aligned; any strides of at least a row are
- * taken (of a tensor with one row they are not looked at).  Fewer than 2^31
- * columns, 2^40 rows. */
+ * codes and scales are 16-byte aligned; any strides of at least a row and
+ * below 2^32 bytes are taken.  Fewer than 2^31 columns, 2^40 rows.  Of a
+ * tensor with one row the strides are not looked at; the same goes for the
+ * BF16 and fp32 matrices of the calls below (theirs are below 2^40 elements). */
 typedef struct {
     void* codes;
     void* scales;

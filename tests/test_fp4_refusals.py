@@ -91,6 +91,13 @@ def test_bad_scale_of_empty_sums(ts):
     assert quantize(desc(rows=0, fmt=1, ts=ts)) == dcr.DCR_OK and dequantize(desc(cols=0, fmt=1, ts=ts)) == dcr.DCR_OK
 
 
+def test_strides_of_one_row():
+    """A single row's strides are not looked at; those of two are."""
+    for kw in (dict(cs=1 << 32), dict(ss=1 << 40), dict(cs=0, ss=0)):
+        assert matmul(desc(rows=1, **kw), m=0) == dcr.DCR_OK, kw
+        assert matmul(desc(rows=2, **kw), m=0) == dcr.DCR_E_INVAL, kw
+
+
 def test_binding_refuses():
     """Python-side checks: host tensors, shapes and types, before the library is called."""
     with pytest.raises(ValueError):
