@@ -26,8 +26,9 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t r) {
     return (r & 3u) | ((r >> 1) & 4u) | (((r >> 3) ^ (r >> 2)) & 1u) << 3;
 }
 
-// What is known of the rows: nothing; codes on 16-byte borders (those behind
-// the sum's end are finite, and multiplied by zeros); x there too, and a sum of
+// What is known of the rows: nothing; codes on 16-byte borders (what a row's
+// last 16 bytes hold behind the sum's end is loaded too, and multiplied by
+// zeros, see end_inside); x there too, and a sum of
 // whole pieces of x; and scales of two steps at a time on borders of their
 // own (then one load for 16 rows brings two steps' scales: a load costs as
 // much for a byte of each row as for the 16 bytes of codes).
@@ -184,6 +185,20 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         constexpr uint32_t o = decltype(odd)::value;
         w[j & 1][i] = fp4_unpack8_bf16<WF>(wq[o][i][j], WF == DCR_FP4_MX ? wsc[o][i] : (wsc[o][i] >> (j / 2 * 8)) & 255u);
     };
+    // A sum that ends inside a block: codes behind a row's end become zeros.  (x
+    // is zero there, but the largest MX scales take a code past bf16's range.)
+    const uint32_t end_step = a.k % 32 ? a.k / kBK : ~0u;
+    auto end_inside = [&](uint32_t step, auto odd) {
+        constexpr uint32_t o = decltype(odd)::value;
+        if (__builtin_expect(step != end_step, 1)) return;
+        const uint32_t live = a.k - min(step * kBK + quad * 32, a.k);
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t mask = live >= 8 * j + 8 ? ~0u : live <= 8 * j ? 0u : (1u << (4 * (live - 8 * j))) - 1u;
+#pragma unroll
+            for (uint32_t i = 0; i < NI; ++i) wq[o][i][j] &= mask;
+        }
+    };
     // A step's products, four row subtiles at a time.  While these multiply,
     // the next four are read from LDS and part of the next quarter's codes is
     // converted.  The codes' registers are free once the last quarter is
@@ -202,6 +217,7 @@ __global__ void __launch_bounds__(W * 64, 2) fp4_mm_tile_kernel(MArgs a) {
         from_pair(odd);
         if (decltype(odd)::value) load_pair(next);
         read(0);
+        if constexpr (CODES && !PAIRED && WF == DCR_FP4_MX) end_inside(next - 1, odd);
 #pragma unroll
         for (uint32_t ph = 0; ph < 4 * P; ++ph) {
             const uint32_t j = ph / P;

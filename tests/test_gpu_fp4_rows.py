@@ -5,7 +5,7 @@ import torch
 
 from bit_exact_xor_amd import dcr
 from tests import fp4_ref as R
-from tests.test_gpu_fp4 import bound, f64, up
+from tests.test_gpu_fp4 import bound, f64, padded, random_fp4, run_product, up
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,30 @@ def test_one_row_at_any_stride(fmt):
     dcr.dcr_fp4_matmul(x, q, r, None, dcr.fp4_workspace())
     ref, size = R.product(f64(x), v)
     assert (np.abs(f64(r) - ref * s) <= bound(size * s, ref * s, k, "fp32")).all()
+
+
+# ------------------------------------------------------------- what lies behind a row
+
+@pytest.mark.parametrize("op", ["matmul", "matmul_q", "grad"])
+@pytest.mark.parametrize("byte", [253, 254])
+@pytest.mark.parametrize("m,n,k", [(3, 136, 40), (3, 96, 77), (20, 136, 2088), (70, 300, 1000), (70, 300, 1001), (4100, 136, 40),
+                                   (4100, 136, 335), (8200, 136, 104), (8200, 136, 105), (4100, 1000, 40), (4100, 1000, 296)])
+def test_codes_behind_a_row(op, byte, m, n, k):
+    """Sums that end inside a block of the largest scales: the codes between rows, which such a scale takes past
+    bf16's range, do not matter.  (Codes up to 1.5 in the rows themselves: times 2^127 still finite.)"""
+    rng = np.random.default_rng(byte + m + k)
+    w = (k + 1) // 2
+    pick = np.array([0, 1, 2, 3, 8, 9, 10, 11], dtype=np.uint8)
+    codes = pick[rng.integers(0, 8, (n, w))] | pick[rng.integers(0, 8, (n, w))] << 4
+    scales = np.full((n, dcr.fp4_blocks(k, R.MX)), byte, dtype=np.uint8)
+    values = R.unit_values(codes, scales, k, R.MX)
+    q = padded(dcr.Fp4Tensor(n, k, R.MX, codes=up(codes), scales=up(scales)), -w % 16, -scales.shape[1] % 8 + 8)
+    red, outs = (n, k) if op == "grad" else (k, n)
+    if op == "matmul_q":
+        x, xv = random_fp4(m, k, R.MX, rng, 27, 27)
+    else:
+        xv = rng.integers(-2, 3, (m, red)) * 2.0 ** -100
+        x = up(xv).bfloat16()
+    y = torch.empty(m, outs, device="cuda")
+    run_product(op, x, q, y, None, dcr.fp4_workspace())
+    assert np.array_equal(f64(y), R.product(xv, values, None, op == "grad")[0])
