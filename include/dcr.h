@@ -633,8 +633,12 @@ int32_t dcr_fp4_dequantize(const dcr_fp4_tensor* q, void* y, uint32_t y_type, ui
  *   workspace_dev, ws_bytes  scratch for products that split the sum; at
  *              least DCR_FP4_WORKSPACE_BYTES (DCR_E_CAPACITY), 16-byte
  *              aligned, one call at a time
- * Products of the operands are exact, sums are held in fp32, and each result
- * is rounded once to y's type after the tensor scale.  The order of a sum
+ * A weight is taken as the bf16 value of its code and block scale (without the
+ * tensor scale), which is exact but for MX scale bytes 253 and 254: 2^128 and
+ * more is an infinity there, as in dcr_fp4_dequantize (which never reads such
+ * a byte back from dcr_fp4_quantize: its largest is 252).  Products of the
+ * operands are exact, sums are held in fp32, and each result is rounded once to
+ * y's type after the tensor scale.  The order of a sum
  * depends on sizes, strides and alignments alone, so equal calls give equal
  * bits.  A NaN scale makes the results of its row NaN.  x and y may have any
  * alignment of whole elements; rows that start on 16-byte borders are faster,
@@ -647,7 +651,8 @@ int32_t dcr_fp4_matmul(const void* x, uint64_t m, uint64_t x_stride, const dcr_f
 
 /* The same with x in 4 bits as well: x->rows rows of w->cols elements.  Both
  * operands DCR_FP4_MX (the matrix instructions scale by powers of two only;
- * DCR_E_INVAL otherwise). */
+ * DCR_E_INVAL otherwise).  Codes and scales are multiplied as they are, the
+ * largest scales too: a result is infinite only where its sum is. */
 int32_t dcr_fp4_matmul_q(const dcr_fp4_tensor* x, const dcr_fp4_tensor* w, const int32_t* offsets,
                          uint32_t n_groups, void* y, uint32_t y_type, uint64_t y_stride, void* workspace_dev,
                          uint64_t ws_bytes, void* stream);

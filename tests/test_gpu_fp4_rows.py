@@ -58,3 +58,32 @@ def test_codes_behind_a_row(op, byte, m, n, k):
     y = torch.empty(m, outs, device="cuda")
     run_product(op, x, q, y, None, dcr.fp4_workspace())
     assert np.array_equal(f64(y), R.product(xv, values, None, op == "grad")[0])
+
+
+@pytest.mark.parametrize("op", ["matmul", "matmul_q", "grad"])
+@pytest.mark.parametrize("m", [2, 70, 300])
+@pytest.mark.parametrize("byte,code", [(252, 7), (253, 5), (253, 6), (254, 3), (254, 4), (254, 7),
+                                       (0, 1), (0, 3), (0, 7), (1, 1), (1, 2), (2, 1)])
+def test_weights_at_the_ends_of_the_range(op, m, byte, code):
+    """Scale bytes 253 and 254: values from 2^128 on are infinities to the products that take weights as bf16, as they
+    are when read back; the product of two 4-bit operands scales exactly.  Bytes 0 to 2: values below the normal
+    numbers, down to 2^-128, are kept."""
+    n = k = 96
+    codes = np.zeros((n, k // 2), dtype=np.uint8)
+    codes[np.arange(n), np.arange(n) // 2] = code << 4 * (np.arange(n) % 2)      # one in each row and column
+    scales = np.full((n, 3), byte, dtype=np.uint8)
+    q = dcr.Fp4Tensor(n, k, R.MX, codes=up(codes), scales=up(scales))
+    back = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    dcr.dcr_fp4_dequantize(q, back)
+    v, e = R.GRID[code] * 2.0 ** (byte - 127), -100 if byte > 127 else 100
+    assert (f64(back).diagonal() == (v if v < 2.0 ** 128 else np.inf)).all()
+    if op == "matmul_q":
+        ones = np.full((m, k // 2), 0x22, dtype=np.uint8)
+        x = dcr.Fp4Tensor(m, k, R.MX, codes=up(ones), scales=up(np.full((m, 3), 127 + e, dtype=np.uint8)))
+        want = v * 2.0 ** e
+    else:
+        x = torch.full((m, k), 2.0 ** e, dtype=torch.bfloat16, device="cuda")
+        want = v * 2.0 ** e if v < 2.0 ** 128 else np.inf
+    y = torch.empty(m, n, device="cuda")
+    run_product(op, x, q, y, None, dcr.fp4_workspace())
+    assert (f64(y) == want).all()
