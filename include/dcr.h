@@ -580,6 +580,11 @@ enum { DCR_FP4_CALIBRATE = 1 };
  *   tensor_scale  DCR_FP4_NV: one fp32 in device memory (4-byte aligned),
  *                 from 2^-100 to 2^117; DCR_FP4_MX: not looked at
  *   reserved      0
+ * The calls write the bytes of rows named here and no others.  The products
+ * read rows of codes that start on 16-byte borders in whole pieces of 16
+ * bytes, and scales in whole words of 4: up to the next such border behind a
+ * row's end, the last row's too (never across it, so never into another page
+ * of memory).  What lies there does not matter to a result.
  * codes and scales are 16-byte aligned; any strides of at least a row and
  * below 2^32 bytes are taken.  Fewer than 2^31 columns, 2^40 rows.  Of a
  * tensor with one row the strides are not looked at; the same goes for the
