@@ -476,6 +476,12 @@ def _wide(t, rows, cols, name):
     return t.data_ptr(), ty, strides[0]
 
 
+def _whole(workspace):
+    """Refuse a workspace with gaps: the library takes an address and a size."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous memory expected")
+
+
 def _fp4_call(torch, fn, what, device, stream, *args):
     """Call `fn` with GPU `device`, the one of its tensors, current, on
     `stream` or that GPU's current stream."""
@@ -496,6 +502,8 @@ def dcr_fp4_quantize(x, q: Fp4Tensor, options=0, workspace=None, stream=None) ->
     workspace."""
     import torch
     p, ty, stride = _wide(x, q.rows, q.cols, "x")
+    if workspace is not None:
+        _whole(workspace)
     dev = _one_device(q, x, workspace)
     _fp4_call(torch, load_library().dcr_fp4_quantize, "dcr_fp4_quantize", dev, stream, p, ty, stride, q._ref, options,
               workspace.data_ptr() if workspace is not None else None,
@@ -527,19 +535,23 @@ def _product(fn, what, x, w, y, offsets, workspace, stream, grad):
     import torch
     if workspace is None:
         raise ValueError("workspace: pass one made by fp4_workspace()")
+    _whole(workspace)
     off, g, n = _groups(w, offsets)
-    yp, ty, ys = _wide(y, x.rows if isinstance(x, Fp4Tensor) else x.shape[0], w.cols if grad else n,
-                       "dx" if grad else "y")
-    tail = (w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.nbytes)
+    yn = "dx" if grad else "y"
     if isinstance(x, Fp4Tensor):
+        if fn is not load_library().dcr_fp4_matmul_q:
+            raise ValueError(f"{what}: bfloat16 rows expected, got an Fp4Tensor")
+        yp, ty, ys = _wide(y, x.rows, n, yn)
         dev = _one_device(w, x.codes, y, offsets, workspace)
-        _fp4_call(torch, fn, what, dev, stream, x._ref, *tail)
+        _fp4_call(torch, fn, what, dev, stream, x._ref, w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.nbytes)
         return
     if x.dtype is not torch.bfloat16:
         raise ValueError(f"{what}: bfloat16 rows expected, got {x.dtype}")
     xp, _ty, xs = _wide(x, None, n if grad else w.cols, "dy" if grad else "x")
+    m = x.shape[0]
+    yp, ty, ys = _wide(y, m, w.cols if grad else n, yn)
     dev = _one_device(w, x, y, offsets, workspace)
-    _fp4_call(torch, fn, what, dev, stream, xp, x.shape[0], xs, *tail)
+    _fp4_call(torch, fn, what, dev, stream, xp, m, xs, w._ref, off, g, yp, ty, ys, workspace.data_ptr(), workspace.nbytes)
 
 
 def dcr_fp4_matmul(x, w: Fp4Tensor, y, offsets=None, workspace=None, stream=None) -> None:

@@ -87,3 +87,22 @@ def test_weights_at_the_ends_of_the_range(op, m, byte, code):
     y = torch.empty(m, n, device="cuda")
     run_product(op, x, q, y, None, dcr.fp4_workspace())
     assert (f64(y) == want).all()
+
+
+def test_calls_of_the_wrong_kind():
+    """4-bit rows for a call that takes bf16 ones, matrices of other dimensions, workspaces with gaps: refused."""
+    q, ws = dcr.Fp4Tensor(64, 96), dcr.fp4_workspace()
+    x = dcr.Fp4Tensor(8, 96)
+    with pytest.raises(ValueError):
+        dcr.dcr_fp4_matmul(x, q, torch.empty(8, 64, device="cuda"), None, ws)
+    with pytest.raises(ValueError):
+        dcr.dcr_fp4_matmul_grad(dcr.Fp4Tensor(8, 64), q, torch.empty(8, 96, device="cuda"), None, ws)
+    for bad in (torch.zeros((), dtype=torch.bfloat16, device="cuda"), torch.zeros(96, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(2, 8, 96, dtype=torch.bfloat16, device="cuda")):
+        with pytest.raises(ValueError):
+            dcr.dcr_fp4_matmul(bad, q, torch.empty(8, 64, device="cuda"), None, ws)
+    gaps = torch.empty(2 * dcr.FP4_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")[::2]
+    with pytest.raises(ValueError):
+        dcr.dcr_fp4_matmul(torch.zeros(8, 96, dtype=torch.bfloat16, device="cuda"), q, torch.empty(8, 64, device="cuda"), None, gaps)
+    with pytest.raises(ValueError):
+        dcr.dcr_fp4_quantize(torch.zeros(8, 96, device="cuda"), dcr.Fp4Tensor(8, 96, R.NV), dcr.FP4_CALIBRATE, gaps)
