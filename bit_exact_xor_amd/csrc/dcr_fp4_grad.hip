@@ -299,6 +299,8 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
 bool fp4_mm_grad(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile, and inside the rows of w of a step, are 30 bits
     if (a.n < 8 || a.n >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 24) || a.ws_stride >= (1u << 24)) return false;
+    // A step measures 1466, 471, 296 and 218 ns (MX; NV 1578 to 246), with rows
+    // of dy anywhere 562, 335 and 227, with codes anywhere 561 and 260.
     constexpr uint32_t kCost[4] = {3800, 1300, 800, 600}, kCostCodes[4] = {0, 1500, 950, 700}, kCostAny[4] = {0, 2000, 0, 900};
     const Rows rows = !a.w_vec ? Rows::kAny : !a.x_vec || a.n % 8 ? Rows::kCodes : Rows::kAligned;
     const uint32_t bm = fp4_mm_plan(&a, a.k, (a.n + kBJ - 1) / kBJ,

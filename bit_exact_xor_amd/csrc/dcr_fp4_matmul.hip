@@ -240,12 +240,20 @@ int32_t product(bool grad, const dcr_fp4_tensor* xq, const void* x, uint64_t m, 
 uint32_t fp4_mm_plan(MArgs* a, uint32_t outs, uint32_t steps, const uint32_t (&cost)[4]) {
     // Time of a candidate: rounds of workgroups over 256 compute units, each
     // its steps and a fixed start and end; for parts of the sum the launch
-    // that joins them and its traffic, at the cycles they measure.  Groups make
-    // the start longer (offsets, weights that no neighbour has read), which
-    // shows where a workgroup is alone on its compute unit.  Over 114 products
-    // and gradients of 8 to 256 experts the tile so chosen takes 3.8 % more than
-    // the best one, without that 4.3 % (16384 rows of 128 experts through
-    // 2048 x 768: 123 us in tiles of 256 rows, 103 of 128).
+    // that joins them and its traffic.  A step's cost (see each kernel's) is
+    // what 4096 x 4096 results take more for a sum of 4096 than for one of
+    // 1024, a round and step, with the tile forced, in units of 0.4 to 0.5 ns
+    // (proportions decide).  Start and end are what is left, 10 us a round in
+    // tiles of 256 rows, 3 of 128 and 1 of 64: kBlock, between them, is for all.
+    // kJoin is the launch that joins, kJoinBytes what it moves a unit.  Over 100
+    // products and gradients drawn at random (17 to 8192 rows) the choice takes
+    // 1.7 % more than the best tile and number of parts, 52 % at worst (2551 x
+    // 2432 x 384 in 4 bits: 13.1 us as chosen, 8.6 in tiles of 64 rows).
+    // Groups make the start longer (offsets, weights that no neighbour has
+    // read), which shows where a workgroup is alone on its compute unit: over
+    // 100 of 8 to 256 experts the choice takes 2.7 % more than the best, without
+    // that 4.5 % (16384 rows of 128 experts through 2048 x 768: 123 us in tiles
+    // of 256 rows, 103 of 128).
     constexpr uint64_t kBlock = 6000, kGroupBlock = 12000, kJoin = 5000, kJoinBytes = 2500;
     const uint64_t stride = (uint64_t(outs) + 3) & ~uint64_t(3), pairs = (uint64_t(steps) + 1) / 2;
     uint64_t best = UINT64_MAX;

@@ -355,8 +355,14 @@ void launch(const MArgs& a, hipStream_t st, uint32_t bm, Rows rows) {
 bool fp4_mm_tile(MArgs a, uint32_t fmt, bool f32, void* ws, hipStream_t st) {
     // offsets inside a tile are 30 bits
     if (a.k < 8 || a.k >= kLongest || a.x_stride >= (1u << 21) || a.wc_stride >= (1u << 22) || a.ws_stride >= (1u << 22)) return false;
+    // A step measures 2762, 850, 551 and 431 ns (MX; NV 3070 to 417), with rows
+    // of x anywhere 1124, 714 and 569, with codes anywhere 1782, 1390 and 1218
+    // (the costs of these lean to small tiles more than that).
     constexpr uint32_t kCost[4] = {6100, 2000, 1200, 800}, kCostCodes[4] = {0, 2400, 1500, 900}, kCostAny[4] = {0, 2800, 1700, 1100};
-    // (two NV scales are read at once, so both have to be there)
+    // (two NV scales are read at once, so both have to be there.  Sums that end
+    // in the first half of a block of 32 read their codes byte by byte
+    // therefore: 4096 x 4096 x 4072 takes 164 us and 4088 110, 24 rows through
+    // 4096 x 4072 14.0 and through 4088 11.4)
     const bool codes = a.w_vec && (fmt == DCR_FP4_MX || (a.ws_stride % 2 == 0 && (a.k - 1) % 32 >= 16));
     const Rows rows = !codes                                            ? Rows::kAny
                       : !a.x_vec || a.k % 8                               ? Rows::kCodes

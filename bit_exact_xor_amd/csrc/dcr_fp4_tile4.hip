@@ -266,6 +266,7 @@ bool fp4_mm_tile4(MArgs a, bool f32, void* ws, hipStream_t st) {
     const Rows rows = !a.x_vec || !a.w_vec                                             ? Rows::kAny
                       : a.k % kBK == 0 && a.xs_stride % 8 == 0 && a.ws_stride % 8 == 0 ? Rows::kScales
                                                                                        : Rows::kAligned;
+    // A step measures 2055, 670 and 480 ns, with rows anywhere 1264 and 983.
     constexpr uint32_t kCost[4] = {4800, 1600, 1000, 0}, kCostAny[4] = {0, 3000, 1800, 0};
     const uint32_t bm = fp4_mm_plan(&a, a.n, (a.k + kBK - 1) / kBK, rows == Rows::kAny ? kCostAny : kCost);
     if (!bm) return false;
