@@ -199,8 +199,10 @@ class Fp4Refit:
 
     Calls come from one thread at a time, on any streams of the weights' GPU: a
     product reads the weights as the calls before it left them, and has scratch
-    memory of its own.  Replays of a captured product are not seen here: a
-    refit is called when they are done."""
+    memory of its stream's own.  A refit waits for the streams that products
+    were put on since the last one (which have to be there still).  Replays of
+    a captured product are not seen here: a refit is called when they are
+    done."""
 
     def __init__(self, shapes, fmt=dcr.FP4_NV, device="cuda", n_slices=4):
         import torch
@@ -217,7 +219,7 @@ class Fp4Refit:
         self.fmt, self.device, self.n_slices = fmt, device, n_slices
         self.version = 0
         self.interrupted = False
-        self.products = {}               # stream -> event behind its last product since the last refit
+        self.products = {}               # streams with products since the last refit: (stream, scratch memory)
         self.sent, self.next, self.held = ([dcr.Fp4Tensor(r, c, fmt, device) for r, c in shapes] for _ in range(3))
         for side in (self.sent, self.next, self.held):
             for t in side:
@@ -309,9 +311,8 @@ class Fp4Refit:
         """The receiver's streams wait for what the current one holds and for
         the products of all."""
         import torch
-        self.link.apply_stream.wait_stream(torch.cuda.current_stream())
-        for event in self.products.values():
-            self.link.apply_stream.wait_event(event)
+        for stream in (torch.cuda.current_stream(), *(s for s, _workspace in self.products.values())):
+            self.link.apply_stream.wait_stream(stream)
 
     def _arrived(self, results):
         """Wait for the applies of a stream; with all of it in `held`, the
@@ -324,25 +325,28 @@ class Fp4Refit:
         self.sent, self.next, self.version, self.interrupted = self.next, self.sent, self.version + 1, False
         self.products.clear()
 
-    def matmul(self, i, x, out_dtype=None, offsets=None):
-        """x w^T with the receiver's weight i (see dcr_fp4_matmul).  With
-        `offsets`, rows of x in front of the first group and behind the last
-        give zeros."""
+    def matmul(self, i, x, out_dtype=None, offsets=None, y=None):
+        """x w^T with the receiver's weight i (see dcr_fp4_matmul), in a new
+        tensor or in `y`.  With `offsets`, rows of x in front of the first
+        group and behind the last give zeros, and leave those of `y` as they
+        are."""
         import torch
         if self.interrupted:
             raise dcr.DcrError(dcr.DCR_E_VERSION, "Fp4Refit.matmul", "the last refit was interrupted: recover() first")
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.matmul(i, x, out_dtype, offsets, y)
         w = self.held[i]
-        _off, _g, n = dcr._groups(w, offsets)
-        # (the product leaves those rows as they are)
-        make = torch.empty if offsets is None else torch.zeros
-        y = make(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
-        with torch.cuda.device(self.device):
-            # (torch hands memory that is free again to the same stream only,
-            # and to a capture its graph's own)
-            dcr.dcr_fp4_matmul(x, w, y, offsets, dcr.fp4_workspace(self.device))
-            if not torch.cuda.is_current_stream_capturing():
-                stream = torch.cuda.current_stream()
-                if stream.cuda_stream not in self.products:
-                    self.products[stream.cuda_stream] = torch.cuda.Event()
-                self.products[stream.cuda_stream].record(stream)
+        if y is None:
+            _off, _g, n = dcr._groups(w, offsets)
+            make = torch.empty if offsets is None else torch.zeros
+            y = make(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
+        if torch.cuda.is_current_stream_capturing():
+            workspace = dcr.fp4_workspace(self.device)       # (of the graph's memory)
+        else:
+            raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+            if raw not in self.products:
+                self.products[raw] = (torch.cuda.current_stream(), dcr.fp4_workspace(self.device))
+            workspace = self.products[raw][1]
+        dcr.dcr_fp4_matmul(x, w, y, offsets, workspace)
         return y

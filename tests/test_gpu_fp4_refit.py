@@ -246,6 +246,20 @@ def test_product_rows_of_no_group_are_zeros(dtype):
     assert (np.abs(y - ref) <= bound(size, ref, 64, "fp32" if dtype else "bf16"))[~rows].all()
 
 
+def test_product_into_a_tensor():
+    """Results in the caller's tensor: rows of no group as they were."""
+    link = pipeline.Fp4Refit([(4 * 48, 64)], R.MX)
+    link.refit(weights(3, [(4 * 48, 64)]))
+    x = up(np.random.default_rng(8).integers(-2, 3, (64, 64))).bfloat16()
+    off = torch.tensor([5, 20, 20, 41, 50], dtype=torch.int32, device="cuda")
+    want = link.matmul(0, x, torch.float32, off)
+    y = torch.full((64, 48), 99.0, device="cuda")
+    assert link.matmul(0, x, offsets=off, y=y) is y
+    assert torch.equal(y[5:50], want[5:50]) and (y[:5] == 99.0).all() and (y[50:] == 99.0).all()
+    with pytest.raises(ValueError):
+        link.matmul(0, x, offsets=off, y=y[:, 1:])
+
+
 def test_product_refuses_offsets():
     link = pipeline.Fp4Refit([(4 * 48, 64)], R.MX)
     x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
