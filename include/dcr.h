@@ -611,7 +611,8 @@ typedef struct {
  * left as they are; the unused nibble of an odd row is 0.
  *   options  0, or DCR_FP4_CALIBRATE (DCR_FP4_NV): *tensor_scale is written
  *            first, max|x| over the finite elements / 2688, held to its
- *            range, 1 if x is all zeros
+ *            range, 1 if x is all zeros (of a tensor without elements nothing
+ *            is written)
  *   workspace_dev  DCR_FP4_CALIBRATE: 16-byte aligned, at least 4096 bytes
  *                  (DCR_E_CAPACITY); else not looked at */
 int32_t dcr_fp4_quantize(const void* x, uint32_t x_type, uint64_t x_stride, const dcr_fp4_tensor* q,
