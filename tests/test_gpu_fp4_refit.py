@@ -267,3 +267,43 @@ def test_product_refuses_offsets():
                 torch.zeros(5, device="cuda"), torch.zeros(6, dtype=torch.int32, device="cuda")):
         with pytest.raises(ValueError):
             link.matmul(0, x, offsets=off)
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+def test_recovery_with_nothing_to_send(fmt, monkeypatch):
+    """A refit of unchanged weights that is interrupted: recover() has no records to apply."""
+    link = pipeline.Fp4Refit(SHAPES, fmt)
+    w = weights(0)
+    link.refit(w)
+
+    def broken_wait(*_args):
+        raise RuntimeError("planted")
+
+    for _ in range(2):
+        with monkeypatch.context() as mp:
+            mp.setattr(dcr, "dcr_ready_wait", broken_wait)
+            with pytest.raises(RuntimeError):
+                link.refit(w)
+        link.recover()
+    assert link.version == 3 and link.refit(w) == 0
+    check_held(link, fmt, w)
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+def test_first_refit_interrupted(fmt, monkeypatch):
+    """The first refit, which takes the NV tensor scales, finished by the second."""
+    link = pipeline.Fp4Refit(SHAPES, fmt)
+    real = dcr.dcr_apply
+
+    def broken_apply(plan, canon, header, dirs, payload, flags, first, n, *rest, **kw):
+        real(plan, canon, header, dirs, payload, flags, first, max(1, n // 2), *rest, **kw)
+        raise RuntimeError("planted")
+
+    with monkeypatch.context() as mp:
+        mp.setattr(dcr, "dcr_apply", broken_apply)
+        with pytest.raises(RuntimeError):
+            link.refit(weights(0))
+    w = weights(1)
+    link.refit(w)
+    assert link.version == 2
+    check_held(link, fmt, w)
