@@ -278,6 +278,8 @@ def _with_handles(s):
         c = s["case"]
         if c["kind"] in ("select", "logprobs"):
             s["workspace"] = dcr.step_workspace()
+        if c["kind"] == "select_grad":
+            s["ids"] = s["ids"].int()            # as dcr_experts_select gives them
         if c["kind"] == "adamw":
             at, sizes = _starts(c), _numels(c)
 
