@@ -1,7 +1,7 @@
 """Build the gfx950 libraries in-tree with hipcc.
 
-  libdcr.so        the delta encode / apply library and its 4-bit weight calls
-                   (C-ABI in include/dcr.h)
+  libdcr.so        the delta encode / apply library, its 4-bit weight calls and
+                   those of a training turn (C-ABI in include/dcr.h)
   libdcr_synth.so  the seeded synthetic input generator (test / bench inputs)
 
 Run ``python -m bit_exact_xor_amd.build`` (or ``__graft_entry__.build()``).
@@ -31,7 +31,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-Wall", "-I", INCLUDE, "-I", CSRC]
 
 DCR_SOURCES = ["dcr_plan.cpp", "dcr_kernels.hip", "dcr_transcode.hip", "dcr_pack.hip", "dcr_fp4.hip",
-               "dcr_fp4_matmul.hip", "dcr_fp4_rows.hip", "dcr_fp4_tile.hip", "dcr_fp4_tile4.hip", "dcr_fp4_grad.hip"]
+               "dcr_fp4_matmul.hip", "dcr_fp4_rows.hip", "dcr_fp4_tile.hip", "dcr_fp4_tile4.hip", "dcr_fp4_grad.hip",
+               "dcr_experts.hip", "dcr_rows.hip", "dcr_logprobs.hip", "dcr_adamw.hip"]
 
 
 def _compile(out: str, sources: list[str], extra: list[str] | None = None) -> None:

@@ -1,0 +1,458 @@
+// dcr_adamw.hip -- an AdamW step over many tensors in one launch (one for each
+// combination of types that occurs).
+//
+//   g' = grad_scale g
+//   m  = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
+//   p  = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//
+// Bound by memory: everything is read once and written once, 30 bytes an
+// element with fp32 states, bf16 gradients and a bf16 copy, 16.1 with states in
+// 8 bits.  A workgroup takes 4096 consecutive elements of a tensor, so small
+// tensors cost a workgroup each and no launch.
+//
+// States in 8 bits: blocks of 32 elements under one power of two (an e8m0
+// byte), e4m3 codes; of the second moment the square root is held, whose range
+// is half as wide in powers of two.  A power of two as the scale makes both
+// conversions exact but for the one rounding of a code.  With only three bits
+// behind the leading one a moment that is rounded to nearest would stop
+// following: v moves by a twentieth of itself or less, half a step is a
+// sixteenth.  So a code is rounded up with the probability of the remainder
+// (the dither); the random numbers are a function of the seed, the step and
+// the element's index, so equal calls give equal bits, whatever the shards.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "dcr_step.h"
+
+namespace dcr {
+namespace {
+
+constexpr uint32_t kAT = 256;                 // threads of a workgroup
+constexpr uint32_t kAChunk = 4096;            // elements of a workgroup
+constexpr uint32_t kStateBlock = DCR_ADAMW_BLOCK;
+
+// what the steps of a call share
+struct AdamArgs {
+    float grad_scale, beta1, new1, beta2, new2;   // new: 1 - beta
+    float rate, root, eps, keep;                  // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), eps, 1 - lr decay
+    uint32_t key, dither;
+};
+
+struct DevAdam {
+    uint8_t *param, *m, *v, *m_scales, *v_scales;
+    const uint8_t* grad;
+    uint16_t* copy;
+    uint64_t numel, first;
+    uint32_t no_decay, pad;
+};
+static_assert(sizeof(DevAdam) == 80, "DevAdam");
+struct DevAdamChunk {
+    uint32_t tensor, at;                      // at: in units of kAChunk
+};
+
+// Odd numbers of the fractions of square roots of 2, 3, 5 and of the golden
+// ratio, which spreads consecutive numbers evenly.
+constexpr uint32_t kGolden = 0x9E3779B1u, kRoot2 = 0x6A09E667u, kRoot3 = 0xBB67AE85u, kRoot5 = 0x3C6EF373u;
+
+// two 16-bit random numbers of element i: low half for m, high half for v
+__device__ __forceinline__ uint32_t dither_of(uint64_t i, uint32_t key) {
+    uint32_t x = uint32_t(i) * kGolden + uint32_t(i >> 32) * kRoot3 + key;
+    x = (x ^ (x >> 16)) * kRoot2;
+    x = (x ^ (x >> 15)) * kRoot5;
+    return x ^ (x >> 16);
+}
+
+// Four elements of a state at fp32 or bf16.
+__device__ __forceinline__ void load4(const float* p, float* v) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(q[i]);
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
+    const u32x2 q = *reinterpret_cast<const u32x2*>(p);
+    unpack2(q[0], v);
+    unpack2(q[1], v + 2);
+}
+__device__ __forceinline__ void save4(float* p, const float* v) { *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ void save4(uint16_t* p, const float* v) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+}
+template <typename T>
+__device__ __forceinline__ void load4_some(const T* p, float* v, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? wide(p[i]) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void save4_some(T* p, const float* v, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) narrow(v[i], p + i);
+}
+
+__device__ __forceinline__ void codes4(uint32_t q, uint32_t byte, float* v) {
+    const float unit = byte == 255 ? NAN : ldexpf(1.0f, int(byte) - 127);
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(q), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(int(q), true);
+    v[0] = a[0] * unit, v[1] = a[1] * unit, v[2] = b[0] * unit, v[3] = b[1] * unit;
+}
+
+// the scale byte of a block whose largest magnitude has these bits: the least
+// power of two that brings it to 448 or below
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    if (top >= 0x7F800000u) return 255;
+    const int e = int(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return uint32_t(max(e, 0));
+}
+
+// e4m3 code of magnitude y (at most 448): down to the code below where the rest
+// is less than 1 - r / 65536 of the code's step.  Above 2^-6 the codes are the
+// leading bits of the number itself, below they are multiples of 2^-9.
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t r) {
+    const uint32_t b = __float_as_uint(y);
+    if (b >= 0x3C800000u) return ((b + (r << 4)) >> 20) - (120u << 3);
+    return uint32_t(floorf(__fmaf_rn(y, 512.0f, float(r) * 0x1p-16f)));
+}
+
+// largest of the eight lanes of a block
+__device__ __forceinline__ uint32_t block_top(const float* v) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) t = max(t, uint32_t(__shfl_xor(int(t), d, 64)));
+    return t;
+}
+
+template <typename TP, typename TG, uint32_t BITS>
+__global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* tensors, const DevAdamChunk* chunks, AdamArgs args,
+                                                    const AdamArgs* live) {
+    const DevAdamChunk c = chunks[blockIdx.x];
+    const DevAdam t = tensors[c.tensor];
+    const AdamArgs a = live ? *live : args;
+    const float keep = t.no_decay ? 1.0f : a.keep;
+    const uint64_t from = uint64_t(c.at) * kAChunk;
+#pragma unroll 2
+    for (uint32_t u = 0; u < kAChunk / (4 * kAT); ++u) {
+        const uint64_t i = from + (u * kAT + threadIdx.x) * 4;
+        const int n = i < t.numel ? int(min(uint64_t(4), t.numel - i)) : 0;
+        TP* pp = reinterpret_cast<TP*>(t.param) + i;
+        const TG* gp = reinterpret_cast<const TG*>(t.grad) + i;
+        float p[4], g[4], m[4], v[4], w[4];
+        if (n == 4) {
+            load4(pp, p);
+            load4(gp, g);
+        } else {
+            load4_some(pp, p, n);
+            load4_some(gp, g, n);
+        }
+        if (BITS == 32) {
+            float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
+            if (n == 4) {
+                load4(mp, m);
+                load4(vp, v);
+            } else {
+                load4_some(mp, m, n);
+                load4_some(vp, v, n);
+            }
+        } else {
+            uint32_t mq = 0, vq = 0, mb = 0, vb = 0;
+            if (n) {
+                if (n == 4) {
+                    mq = *reinterpret_cast<const uint32_t*>(t.m + i);
+                    vq = *reinterpret_cast<const uint32_t*>(t.v + i);
+                } else {
+                    for (int j = 0; j < n; ++j) {
+                        mq |= uint32_t(t.m[i + j]) << (8 * j);
+                        vq |= uint32_t(t.v[i + j]) << (8 * j);
+                    }
+                }
+                mb = t.m_scales[i / kStateBlock];
+                vb = t.v_scales[i / kStateBlock];
+            }
+            codes4(mq, mb, m);
+            codes4(vq, vb, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float s = g[j] * a.grad_scale;
+            m[j] = __fmaf_rn(m[j], a.beta1, s * a.new1);
+            v[j] = __fmaf_rn(v[j], a.beta2, s * s * a.new2);
+            w[j] = sqrtf(v[j]);
+            p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] / __fmaf_rn(w[j], a.root, a.eps)));
+        }
+        if (n == 4)
+            save4(pp, p);
+        else
+            save4_some(pp, p, n);
+        if (t.copy) n == 4 ? save4(t.copy + i, p) : save4_some(t.copy + i, p, n);
+        if (BITS == 32) {
+            float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
+            if (n == 4) {
+                save4(mp, m);
+                save4(vp, v);
+            } else {
+                save4_some(mp, m, n);
+                save4_some(vp, v, n);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j >= n) m[j] = w[j] = 0.0f;      // (behind the end)
+            const uint32_t mb = scale_byte(block_top(m)), wb = scale_byte(block_top(w));
+            uint32_t mq = 0, wq = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t rm = 0x8000u, rw = 0x8000u;
+                if (a.dither) {
+                    const uint32_t r = dither_of(t.first + i + j, a.key);
+                    rm = r & 0xFFFFu, rw = r >> 16;
+                }
+                const uint32_t cm = code_of(fabsf(ldexpf(m[j], 127 - int(mb))), rm);
+                uint32_t cw = code_of(ldexpf(w[j], 127 - int(wb)), rw);
+                cw = max(cw, w[j] > 0.0f ? 1u : 0u); // (0 would make the next update one of eps)
+                mq |= (mb == 255 ? 0u : cm | (__float_as_uint(m[j]) >> 31) << 7) << (8 * j);
+                wq |= (wb == 255 ? 0u : cw) << (8 * j);
+            }
+            if (n == 4) {
+                *reinterpret_cast<uint32_t*>(t.m + i) = mq;
+                *reinterpret_cast<uint32_t*>(t.v + i) = wq;
+            } else {
+                for (int j = 0; j < n; ++j) {
+                    t.m[i + j] = uint8_t(mq >> (8 * j));
+                    t.v[i + j] = uint8_t(wq >> (8 * j));
+                }
+            }
+            if (n && i % kStateBlock == 0) {
+                t.m_scales[i / kStateBlock] = uint8_t(mb);
+                t.v_scales[i / kStateBlock] = uint8_t(wb);
+            }
+        }
+    }
+}
+
+// x^n by squaring, alike on the host and the GPU
+__host__ __device__ inline double power(double x, uint64_t n) {
+    double r = 1.0;
+    for (; n; n >>= 1, x *= x)
+        if (n & 1) r *= x;
+    return r;
+}
+
+__host__ __device__ inline AdamArgs adam_args(const dcr_adamw_args& h, double step, double lr, double grad_scale) {
+    AdamArgs a{};
+    const uint64_t t = uint64_t(step);
+    a.grad_scale = float(grad_scale);
+    a.beta1 = float(h.beta1), a.new1 = float(1.0 - h.beta1), a.beta2 = float(h.beta2), a.new2 = float(1.0 - h.beta2);
+    a.rate = float(lr / (1.0 - power(h.beta1, t)));
+    a.root = float(1.0 / sqrt(1.0 - power(h.beta2, t)));
+    a.eps = float(h.eps), a.keep = float(1.0 - lr * h.weight_decay);
+    a.key = uint32_t(h.dither_seed) * kGolden + uint32_t(t) * kRoot2, a.dither = h.dither_seed ? 1 : 0;
+    return a;
+}
+
+// the step's arguments from device memory: step, lr, grad_scale
+__global__ void adamw_live_kernel(dcr_adamw_args h, AdamArgs* out) {
+    *out = adam_args(h, h.live[0], h.live[1], h.live[2]);
+}
+
+constexpr uint32_t kVariants = 8;             // param type | gradient type | bits
+
+}  // namespace
+}  // namespace dcr
+
+struct dcr_adamw_plan {
+    std::vector<uint8_t> blob;                // AdamArgs of a live step | tensors | chunks, by variant
+    uint64_t off_tensors = 0, off_chunks = 0;
+    uint64_t chunk_first[dcr::kVariants + 1] = {};
+    uint8_t* dev = nullptr;
+};
+
+namespace dcr {
+namespace {
+
+int32_t check_adam(const dcr_adamw_tensor& t, uint64_t at) {
+    const std::string w = "tensor " + std::to_string(at);
+    if (t.param_type > DCR_BF16 || t.grad_type > DCR_BF16) return step_fail(DCR_E_INVAL, w + ": type is neither fp32 nor bf16");
+    if (t.state_bits != 8 && t.state_bits != 32) return step_fail(DCR_E_INVAL, w + ": state_bits is neither 8 nor 32");
+    if (t.flags & ~uint32_t(DCR_ADAMW_NO_DECAY)) return step_fail(DCR_E_INVAL, w + ": unknown flag");
+    if (t.numel > (uint64_t(1) << 40)) return step_fail(DCR_E_INVAL, w + ": more than 2^40 elements");
+    if (!t.numel) return DCR_OK;
+    if (!t.param || !t.grad || !t.m || !t.v) return step_fail(DCR_E_INVAL, w + ": NULL");
+    if (!al16(t.param) || !al16(t.grad) || !al16(t.m) || !al16(t.v) || !al16(t.copy))
+        return step_fail(DCR_E_INVAL, w + ": a buffer is not 16-byte aligned");
+    if (t.state_bits == 8 && (!t.m_scales || !t.v_scales)) return step_fail(DCR_E_INVAL, w + ": NULL scales");
+    if (t.copy && t.param_type != DCR_F32) return step_fail(DCR_E_INVAL, w + ": a bf16 copy is of fp32 parameters");
+    return DCR_OK;
+}
+
+// whether memory that the step writes is written or read through another tensor too
+bool overlaps(const dcr_adamw_tensor* tensors, uint64_t n) {
+    struct Range {
+        uintptr_t from, to;
+        bool written;
+    };
+    std::vector<Range> r;
+    const auto add = [&](const void* at, uint64_t bytes, bool written) {
+        if (at && bytes) r.push_back({reinterpret_cast<uintptr_t>(at), reinterpret_cast<uintptr_t>(at) + bytes, written});
+    };
+    for (uint64_t i = 0; i < n; ++i) {
+        const dcr_adamw_tensor& t = tensors[i];
+        const uint64_t state = t.numel * (t.state_bits / 8), scales = t.state_bits == 8 ? (t.numel + kStateBlock - 1) / kStateBlock : 0;
+        add(t.param, t.numel * type_bytes(t.param_type), true);
+        add(t.grad, t.numel * type_bytes(t.grad_type), false);
+        add(t.m, state, true), add(t.v, state, true);
+        add(t.m_scales, scales, true), add(t.v_scales, scales, true);
+        add(t.copy, t.numel * 2, true);
+    }
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+    uintptr_t any = 0, written = 0;
+    for (const Range& x : r) {
+        if (x.from < (x.written ? any : written)) return true;
+        any = std::max(any, x.to);
+        if (x.written) written = std::max(written, x.to);
+    }
+    return false;
+}
+
+int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan& p) {
+    std::vector<DevAdam> dev(n);
+    std::vector<DevAdamChunk> by[kVariants];
+    uint64_t chunks = 0;
+    for (uint64_t i = 0; i < n; ++i) {
+        const dcr_adamw_tensor& t = tensors[i];
+        if (int32_t rc = check_adam(t, i)) return rc;
+        chunks += (t.numel + kAChunk - 1) / kAChunk;
+        if (chunks >= (uint64_t(1) << 32) / kAT) return step_fail(DCR_E_INVAL, "more elements than one launch takes");
+        DevAdam d{};
+        d.param = static_cast<uint8_t*>(t.param), d.grad = static_cast<const uint8_t*>(t.grad);
+        d.m = static_cast<uint8_t*>(t.m), d.v = static_cast<uint8_t*>(t.v);
+        d.m_scales = static_cast<uint8_t*>(t.m_scales), d.v_scales = static_cast<uint8_t*>(t.v_scales);
+        d.copy = static_cast<uint16_t*>(t.copy), d.numel = t.numel, d.first = t.first;
+        d.no_decay = t.flags & DCR_ADAMW_NO_DECAY;
+        dev[i] = d;
+        std::vector<DevAdamChunk>& to = by[t.param_type | t.grad_type << 1 | (t.state_bits == 8 ? 4u : 0u)];
+        for (uint64_t c = 0; c * kAChunk < t.numel; ++c) to.push_back({uint32_t(i), uint32_t(c)});
+    }
+    if (overlaps(tensors, n)) return step_fail(DCR_E_INVAL, "buffers of the tensors overlap");
+    p.off_tensors = (sizeof(AdamArgs) + 15) / 16 * 16;
+    p.off_chunks = p.off_tensors + n * sizeof(DevAdam);
+    p.blob.resize(p.off_chunks + chunks * sizeof(DevAdamChunk));
+    if (n) memcpy(p.blob.data() + p.off_tensors, dev.data(), n * sizeof(DevAdam));
+    for (uint32_t k = 0; k < kVariants; ++k) {
+        p.chunk_first[k + 1] = p.chunk_first[k] + by[k].size();
+        if (!by[k].empty())
+            memcpy(p.blob.data() + p.off_chunks + p.chunk_first[k] * sizeof(DevAdamChunk), by[k].data(),
+                   by[k].size() * sizeof(DevAdamChunk));
+    }
+    return DCR_OK;
+}
+
+bool fraction(double x) { return x >= 0.0 && x < 1.0; }
+
+int32_t adamw_step(const dcr_adamw_plan* p, const dcr_adamw_args* h, hipStream_t st) {
+    if (!p || !h) return step_fail(DCR_E_INVAL, "NULL argument");
+    if (!p->dev) return step_fail(DCR_E_INVAL, "plan not uploaded");
+    if (h->reserved) return step_fail(DCR_E_INVAL, "reserved field not 0");
+    if (!fraction(h->beta1) || !fraction(h->beta2)) return step_fail(DCR_E_INVAL, "beta1 or beta2 is not in [0, 1)");
+    if (!(h->eps >= 0x1p-100 && h->eps < INFINITY)) return step_fail(DCR_E_INVAL, "eps is below 2^-100 or not finite");
+    if (!std::isfinite(h->weight_decay)) return step_fail(DCR_E_INVAL, "weight_decay is not finite");
+    if (!h->live && (!h->step || h->step > (uint64_t(1) << 53))) return step_fail(DCR_E_INVAL, "step is not 1 .. 2^53");
+    if (!h->live && (!std::isfinite(h->lr) || !std::isfinite(h->grad_scale)))
+        return step_fail(DCR_E_INVAL, "lr or grad_scale is not finite");
+    if (reinterpret_cast<uintptr_t>(h->live) & 7u) return step_fail(DCR_E_INVAL, "live is not 8-byte aligned");
+    AdamArgs a{};
+    AdamArgs* live = nullptr;
+    if (h->live) {
+        live = reinterpret_cast<AdamArgs*>(p->dev);
+        hipLaunchKernelGGL(adamw_live_kernel, dim3(1), dim3(1), 0, st, *h, live);
+    } else {
+        a = adam_args(*h, double(h->step), h->lr, h->grad_scale);
+    }
+    const DevAdam* tensors = reinterpret_cast<const DevAdam*>(p->dev + p->off_tensors);
+    const DevAdamChunk* chunks = reinterpret_cast<const DevAdamChunk*>(p->dev + p->off_chunks);
+    for (uint32_t k = 0; k < kVariants; ++k) {
+        const uint32_t n = uint32_t(p->chunk_first[k + 1] - p->chunk_first[k]);
+        if (!n) continue;
+        with_type(k & 1, [&](auto tp) {
+            with_type(k >> 1 & 1, [&](auto tg) {
+                typedef decltype(tp) TP;
+                typedef decltype(tg) TG;
+                if (k & 4)
+                    hipLaunchKernelGGL((adamw_kernel<TP, TG, 8>), dim3(n), dim3(kAT), 0, st, tensors, chunks + p->chunk_first[k], a, live);
+                else
+                    hipLaunchKernelGGL((adamw_kernel<TP, TG, 32>), dim3(n), dim3(kAT), 0, st, tensors, chunks + p->chunk_first[k], a, live);
+            });
+        });
+    }
+    return step_launched();
+}
+
+}  // namespace
+}  // namespace dcr
+
+extern "C" {
+
+int32_t dcr_adamw_plan_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan** out) try {
+    using namespace dcr;
+    set_error("");
+    if (!out) return step_fail(DCR_E_INVAL, "out is NULL");
+    *out = nullptr;
+    if (n && !tensors) return step_fail(DCR_E_INVAL, "tensors: NULL");
+    if (n >= (uint64_t(1) << 31)) return step_fail(DCR_E_INVAL, "2^31 tensors or more");
+    dcr_adamw_plan* p = new (std::nothrow) dcr_adamw_plan();
+    if (!p) return step_fail(DCR_E_NOMEM, "out of host memory");
+    int32_t rc;
+    try {
+        rc = adamw_build(tensors, n, *p);
+    } catch (const std::bad_alloc&) {
+        rc = step_fail(DCR_E_NOMEM, "out of host memory");
+    }
+    if (rc) {
+        delete p;
+        return rc;
+    }
+    *out = p;
+    return DCR_OK;
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_adamw_plan_bytes(const dcr_adamw_plan* plan, uint64_t* bytes) try {
+    using namespace dcr;
+    set_error("");
+    if (!plan || !bytes) return step_fail(DCR_E_INVAL, "NULL argument");
+    *bytes = plan->blob.size();
+    return DCR_OK;
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_adamw_plan_upload(dcr_adamw_plan* plan, void* table_dev, uint64_t bytes, void* stream) try {
+    using namespace dcr;
+    set_error("");
+    if (!plan || !table_dev) return step_fail(DCR_E_INVAL, "NULL argument");
+    if (!al16(table_dev)) return step_fail(DCR_E_INVAL, "table not 16-byte aligned");
+    if (bytes < plan->blob.size()) return step_fail(DCR_E_CAPACITY, "table too small");
+    const hipError_t e = hipMemcpyAsync(table_dev, plan->blob.data(), plan->blob.size(), hipMemcpyHostToDevice,
+                                        static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return step_fail(DCR_E_HIP, std::string("plan upload: ") + hipGetErrorString(e));
+    plan->dev = static_cast<uint8_t*>(table_dev);
+    return DCR_OK;
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+void dcr_adamw_plan_destroy(dcr_adamw_plan* plan) { delete plan; }
+
+int32_t dcr_adamw_step(const dcr_adamw_plan* plan, const dcr_adamw_args* args, void* stream) try {
+    dcr::set_error("");
+    return dcr::adamw_step(plan, args, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+}  // extern "C"

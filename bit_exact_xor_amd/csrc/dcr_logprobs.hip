@@ -1,0 +1,405 @@
+// dcr_logprobs.hip -- log probabilities of given tokens, the entropy of their
+// distribution and the most probable tokens; and the gradient.
+//
+// With z_j = scale x_j, m = max z, S = sum exp(z - m), T = sum exp(z - m) (z - m):
+//   lse = m + log S,   log p_t = z_t - lse,   entropy = log S - T / S.
+// (m, S, T) of two parts of a row join to those of both, so the logits are read
+// once: every thread holds a running triple, in powers of two.  The entropy from
+// log S and T, not from lse and a sum of z: where one token takes nearly all,
+// log S and T / S are small themselves and nothing cancels.
+//
+// Bound by memory: one read of the logits.  A row is split over workgroups
+// where there are few rows; a second launch joins the parts.
+#include <algorithm>
+
+#include "dcr_step.h"
+
+namespace dcr {
+namespace {
+
+constexpr uint32_t kLT = 256;                // threads of a workgroup
+constexpr uint32_t kLWaves = kLT / 64;
+constexpr uint32_t kPiece = 16;              // logits of a thread in a step
+constexpr uint32_t kMostParts = 2048;        // parts of all rows, where rows are split
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+struct LpArgs {
+    const void* logits;
+    const void* targets;
+    float *logp, *lse, *entropy, *top_values;
+    int32_t* top_ids;
+    uint64_t stride;
+    uint32_t rows, vocab, top, wide_ids, parts, part_len;   // part_len: a multiple of 8
+    float scale;
+    f32x4* sums;                             // [rows][parts]: m, S, T in base 2
+    uint64_t* keys;                          // [rows][parts][top]
+};
+
+// m: the largest logit, not scaled; differences d of logits to it are scaled
+// (so the lowest finite numbers, as masks have them, stay finite), and s and t
+// are sums of 2^d and 2^d d
+struct Sums {
+    float m, s, t;
+};
+__device__ __forceinline__ Sums join(Sums a, Sums b, float unit) {
+    const float m = fmaxf(a.m, b.m);
+    // (2^-160 is 0; -infinity, which a difference may overflow to, times that is not)
+    const float da = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * unit, -160.0f);
+    const float db = b.m == -INFINITY ? 0.0f : fmaxf((b.m - m) * unit, -160.0f);
+    const float fa = exp2f(da), fb = exp2f(db);
+    return {m, __fmaf_rn(a.s, fa, b.s * fb), fa * __fmaf_rn(a.s, da, a.t) + fb * __fmaf_rn(b.s, db, b.t)};
+}
+
+// order of logits as that of unsigned integers, -0 as 0, NaN below all
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return x != x ? 0u : b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_order(uint32_t u) {
+    return u == 0 ? NAN : __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+// a logit and its index as one number, no two alike; 0 stands for none
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t at) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - at); }
+
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+    return (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32) |
+           uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), lane));
+}
+
+// A wave's best keys, one a lane, the largest in lane 0.
+struct TopList {
+    uint64_t mine, least;                    // least: the key of lane top - 1, which a new one has to pass
+    __device__ __forceinline__ void insert(uint64_t key, uint32_t top) {
+        const int at = __popcll(__ballot(mine > key));
+        const uint64_t above = uint64_t(__shfl_up((unsigned long long)mine, 1, 64));
+        const int lane = int(threadIdx.x & 63u);
+        mine = lane < at ? mine : lane == at ? key : above;
+        least = lane_value(mine, int(top) - 1);
+    }
+};
+
+// the keys of a workgroup's waves (LDS, n of them, none twice) in order: the best `top` to `put(rank, key)`
+template <typename F>
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, uint32_t n, uint32_t top, F&& put) {
+    for (uint32_t i = threadIdx.x; i < n; i += kLT) {
+        const uint64_t k = keys[i];
+        if (!k) continue;
+        uint32_t r = 0;
+        for (uint32_t j = 0; j < n; ++j) r += keys[j] > k ? 1u : 0u;
+        if (r < top) put(r, k);
+    }
+}
+
+__device__ __forceinline__ int64_t target_of(const LpArgs& a, uint32_t row) {
+    return a.wide_ids ? static_cast<const int64_t*>(a.targets)[row] : int64_t(static_cast<const int32_t*>(a.targets)[row]);
+}
+
+// what turns a logit into its log probability
+struct RowOf {
+    float m, log_s;
+    __device__ __forceinline__ float logp(float x, float scale) const {
+        return m == -INFINITY && log_s == log_s ? -INFINITY : (x - m) * scale - log_s;
+    }
+};
+
+// what a row's sums give; by one thread
+template <typename T>
+__device__ __forceinline__ RowOf finish_row(const LpArgs& a, uint32_t row, Sums s) {
+    const bool none = s.m == -INFINITY && s.s == s.s;        // an empty row
+    const RowOf of = {s.m, none ? 0.0f : logf(s.s)};
+    if (a.lse) a.lse[row] = none ? -INFINITY : __fmaf_rn(s.m, a.scale, of.log_s);
+    if (a.entropy) a.entropy[row] = none ? 0.0f : of.log_s - kLn2 * s.t / s.s;
+    if (a.logp) {
+        const int64_t t = target_of(a, row);
+        float lp = t < 0 ? 0.0f : NAN;
+        if (t >= 0 && t < int64_t(a.vocab))
+            lp = of.logp(wide(static_cast<const T*>(a.logits)[uint64_t(row) * a.stride + uint64_t(t)]), a.scale);
+        a.logp[row] = lp;
+    }
+    return of;
+}
+
+__device__ __forceinline__ void put_top(const LpArgs& a, uint32_t row, uint32_t r, uint64_t key, RowOf of) {
+    const uint64_t to = uint64_t(row) * a.top + r;
+    a.top_ids[to] = int32_t(0xFFFFFFFFu - uint32_t(key));
+    a.top_values[to] = of.logp(of_order(uint32_t(key >> 32)), a.scale);
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
+    __shared__ Sums of_wave[kLWaves];
+    __shared__ uint64_t keys[TOP ? kLT : 1], sorted[TOP ? DCR_LOGPROBS_MAX_TOP : 1];
+    __shared__ RowOf row_of;
+    const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
+    const uint32_t from = part * a.part_len, to = min(a.vocab, from + a.part_len);
+    const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
+    const float unit = a.scale * kLog2e;
+    Sums sum = {-INFINITY, 0.0f, 0.0f};
+    TopList best = {0, 0};
+    // wave by wave through the part: 64 lanes of two times eight logits
+    for (uint32_t c0 = from + wave * 64 * kPiece; c0 < to; c0 += kLT * kPiece) {
+        float v[kPiece];
+        uint32_t at[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            at[h] = c0 + (h * 64 + lane) * 8;
+            Raw8<T> raw;
+            const int n = at[h] < to ? int(min(8u, to - at[h])) : 0;
+            if (n == 8)
+                raw.load(x + at[h]);
+            else
+                raw.load_some(x + at[h], n, kBf16MinusInf);
+            raw.get(v + 8 * h);
+        }
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < int(kPiece); ++i) top = fmaxf(top, v[i]);
+        const float m = fmaxf(sum.m, top);
+        const float base = m == -INFINITY ? 0.0f : m;
+        const float d = sum.m == -INFINITY ? 0.0f : fmaxf((sum.m - m) * unit, -160.0f), f = exp2f(d);
+        float s = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < int(kPiece); ++i) {
+            const float e = (v[i] - base) * unit, p = __builtin_amdgcn_exp2f(e);
+            s += p;
+            t = __fmaf_rn(p, fmaxf(e, -160.0f), t);
+        }
+        sum.t = __fmaf_rn(f, __fmaf_rn(sum.s, d, sum.t), t);
+        sum.s = __fmaf_rn(sum.s, f, s);
+        sum.m = m;
+        if (TOP) {
+            // each lane's best key that the wave's list does not hold yet, until none passes the least
+            uint64_t below = ~uint64_t(0);
+            const uint32_t bound = order_of(top);
+            while (true) {
+                uint64_t cand = 0;
+                if (bound >= uint32_t(best.least >> 32) || best.least == 0) {
+#pragma unroll
+                    for (int i = 0; i < int(kPiece); ++i) {
+                        const uint32_t j = at[i / 8] + i % 8;
+                        const uint64_t k = j < to ? key_of(v[i], j) : 0;
+                        cand = k < below && k > cand ? k : cand;
+                    }
+                }
+                uint64_t who = __ballot(cand > best.least);
+                if (!who) break;
+                while (who) {
+                    const int l = __ffsll((unsigned long long)who) - 1;
+                    who &= who - 1;
+                    const uint64_t k = lane_value(cand, l);
+                    if (k > best.least) best.insert(k, a.top);
+                }
+                below = cand;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
+    if (lane == 0) of_wave[wave] = sum;
+    if (TOP) keys[threadIdx.x] = lane < a.top ? best.mine : 0;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint32_t w = 1; w < kLWaves; ++w) sum = join(sum, of_wave[w], unit);
+        if (a.parts == 1)
+            row_of = finish_row<T>(a, row, sum);
+        else
+            a.sums[blockIdx.x] = f32x4{sum.m, sum.s, sum.t, 0.0f};
+    }
+    if (!TOP) return;
+    __syncthreads();
+    if (a.parts == 1) {
+        rank_keys(keys, kLT, a.top, [&](uint32_t r, uint64_t k) { put_top(a, row, r, k, row_of); });
+    } else {
+        if (threadIdx.x < a.top) sorted[threadIdx.x] = 0;
+        __syncthreads();
+        rank_keys(keys, kLT, a.top, [&](uint32_t r, uint64_t k) { sorted[r] = k; });
+        __syncthreads();
+        if (threadIdx.x < a.top) a.keys[uint64_t(blockIdx.x) * a.top + threadIdx.x] = sorted[threadIdx.x];
+    }
+}
+
+// the parts of a row; a workgroup a row
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
+    __shared__ uint64_t keys[TOP ? kMostParts : 1];
+    __shared__ RowOf row_of;
+    const uint32_t row = blockIdx.x;
+    const float unit = a.scale * kLog2e;
+    if (threadIdx.x < 64) {
+        Sums sum = {-INFINITY, 0.0f, 0.0f};
+        for (uint32_t p = threadIdx.x; p < a.parts; p += 64) {
+            const f32x4 q = a.sums[uint64_t(row) * a.parts + p];
+            sum = join(sum, Sums{q[0], q[1], q[2]}, unit);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
+        if (threadIdx.x == 0) row_of = finish_row<T>(a, row, sum);
+    }
+    if (!TOP) return;
+    const uint32_t n = a.parts * a.top;
+    for (uint32_t i = threadIdx.x; i < n; i += kLT) keys[i] = a.keys[uint64_t(row) * n + i];
+    __syncthreads();
+    rank_keys(keys, n, a.top, [&](uint32_t r, uint64_t k) { put_top(a, row, r, k, row_of); });
+}
+
+struct LpGradArgs {
+    const void* logits;
+    const void* targets;
+    const float *lse, *dlogp, *entropy, *dentropy;
+    void* dlogits;
+    uint64_t stride, d_stride;
+    uint32_t rows, vocab, wide_ids, pieces;      // pieces: workgroups of a row
+    float scale;
+};
+
+constexpr uint32_t kGU = 2;                      // eights of a thread
+
+// dx_j = scale (dlogp (1[j = t] - p_j) - dentropy p_j (log p_j + entropy))
+template <typename T>
+__global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
+    const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
+    const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
+    T* y = static_cast<T*>(a.dlogits) + uint64_t(row) * a.d_stride;
+    const int64_t target = a.wide_ids ? static_cast<const int64_t*>(a.targets)[row]
+                                      : int64_t(static_cast<const int32_t*>(a.targets)[row]);
+    const float lse = a.lse[row];
+    float up = target < 0 ? 0.0f : a.dlogp[row];
+    if (target >= int64_t(a.vocab)) up = NAN;
+    const float b = a.dentropy ? a.dentropy[row] : 0.0f;
+    const float c = a.dentropy ? __fmaf_rn(b, a.entropy[row], up) : up;
+    const bool none = lse == -INFINITY;          // an empty row
+    Raw8<T> raw[kGU];
+    uint32_t at[kGU];
+    int n[kGU];
+#pragma unroll
+    for (uint32_t u = 0; u < kGU; ++u) {
+        at[u] = ((piece * kGU + u) * kLT + threadIdx.x) * 8;
+        n[u] = at[u] < a.vocab ? int(min(8u, a.vocab - at[u])) : 0;
+        n[u] == 8 ? raw[u].load(x + at[u]) : raw[u].load_some(x + at[u], n[u], kBf16MinusInf);
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kGU; ++u) {
+        float v[8];
+        raw[u].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float l = __fmaf_rn(v[i], a.scale, -lse);
+            const float p = __builtin_amdgcn_exp2f(l * kLog2e);
+            // p (up + b (log p + entropy)); p = 0 where log p is -infinity
+            const float g = -p * __fmaf_rn(b, fmaxf(l, -110.0f), c);
+            v[i] = none ? 0.0f : g * a.scale;
+        }
+        const int64_t hot = target - int64_t(at[u]);
+        if (hot >= 0 && hot < 8 && !none) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i == int(hot)) v[i] = __fmaf_rn(up, a.scale, v[i]);
+        }
+        n[u] == 8 ? store8(y + at[u], v) : store_some(y + at[u], v, n[u]);
+    }
+}
+
+int32_t check_logits(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
+                     uint32_t targets_bytes, float scale) {
+    int32_t rc;
+    if (rows >= (uint64_t(1) << 31)) return step_fail(DCR_E_INVAL, "2^31 rows or more");
+    if (!vocab || vocab >= (uint64_t(1) << 31) - kLT * kPiece) return step_fail(DCR_E_INVAL, "vocabulary of 0 or about 2^31 tokens or more");
+    if (!(scale > 0.0f && scale < INFINITY)) return step_fail(DCR_E_INVAL, "scale is not positive and finite");
+    if ((rc = check_matrix(logits, type, rows, vocab, stride, "logits"))) return rc;
+    if (targets_bytes != 4 && targets_bytes != 8) return step_fail(DCR_E_INVAL, "targets are neither int32 nor int64");
+    return targets ? check_array(targets, "targets", targets_bytes) : DCR_OK;
+}
+
+int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
+                 uint32_t targets_bytes, float scale, float* logp, float* lse, float* entropy, uint32_t top, int32_t* top_ids,
+                 float* top_values, void* ws, uint64_t ws_bytes, hipStream_t st) {
+    int32_t rc;
+    if ((rc = check_logits(logits, type, stride, rows, vocab, targets, targets_bytes, scale))) return rc;
+    if (top > DCR_LOGPROBS_MAX_TOP || top > vocab) return step_fail(DCR_E_INVAL, "top is more than 64 or than the vocabulary");
+    if (!rows) return DCR_OK;
+    if (logp && !targets) return step_fail(DCR_E_INVAL, "targets: NULL");
+    if ((logp && (rc = check_array(logp, "logp"))) || (lse && (rc = check_array(lse, "lse"))) ||
+        (entropy && (rc = check_array(entropy, "entropy"))) ||
+        (top && ((rc = check_array(top_ids, "top_ids")) || (rc = check_array(top_values, "top_values")))) ||
+        (rc = check_step_workspace(ws, ws_bytes)))
+        return rc;
+    LpArgs a{};
+    a.logits = logits, a.targets = targets, a.logp = logp, a.lse = lse, a.entropy = entropy;
+    a.top_values = top_values, a.top_ids = top_ids, a.stride = rows > 1 ? stride : 0;
+    a.rows = uint32_t(rows), a.vocab = uint32_t(vocab), a.top = top, a.wide_ids = targets_bytes == 8, a.scale = scale;
+    // parts so that about 1024 workgroups run, none shorter than a step
+    uint64_t parts = rows >= 512 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>(1024 / rows, (vocab + kLT * kPiece - 1) / (kLT * kPiece)));
+    if (top) parts = std::min<uint64_t>(parts, kMostParts / top);
+    uint64_t len = ((vocab + parts - 1) / parts + 7) / 8 * 8;
+    parts = (vocab + len - 1) / len;
+    a.parts = uint32_t(parts), a.part_len = uint32_t(len);
+    a.sums = static_cast<f32x4*>(ws);
+    a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kMostParts * sizeof(f32x4));
+    const uint64_t grid = rows * parts;
+    if (grid * kLT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many rows for one launch");
+    with_type(type, [&](auto t) {
+        auto go = [&](auto some) {
+            constexpr bool TOP = decltype(some)::value;
+            hipLaunchKernelGGL((logprobs_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
+            if (parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<decltype(t), TOP>), dim3(a.rows), dim3(kLT), 0, st, a);
+        };
+        top ? go(std::true_type()) : go(std::false_type());
+    });
+    return step_launched();
+}
+
+int32_t logprobs_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
+                      uint32_t targets_bytes, float scale, const float* lse, const float* dlogp, const float* entropy,
+                      const float* dentropy, void* dlogits, uint64_t d_stride, hipStream_t st) {
+    int32_t rc;
+    if ((rc = check_logits(logits, type, stride, rows, vocab, targets, targets_bytes, scale)) ||
+        (rc = check_matrix(dlogits, type, rows, vocab, d_stride, "dlogits")))
+        return rc;
+    if (!rows) return DCR_OK;
+    if (!targets) return step_fail(DCR_E_INVAL, "targets: NULL");
+    if ((rc = check_array(lse, "lse")) || (rc = check_array(dlogp, "dlogp")) ||
+        (dentropy && ((rc = check_array(dentropy, "dentropy")) || (rc = check_array(entropy, "entropy")))))
+        return rc;
+    LpGradArgs a{};
+    a.logits = logits, a.targets = targets, a.lse = lse, a.dlogp = dlogp, a.entropy = entropy, a.dentropy = dentropy;
+    a.dlogits = dlogits, a.stride = stride, a.d_stride = d_stride, a.rows = uint32_t(rows), a.vocab = uint32_t(vocab);
+    a.wide_ids = targets_bytes == 8, a.scale = scale;
+    a.pieces = uint32_t((vocab + kLT * 8 * kGU - 1) / (kLT * 8 * kGU));
+    const uint64_t grid = rows * a.pieces;
+    if (grid * kLT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many logits for one launch");
+    with_type(type, [&](auto t) {
+        hipLaunchKernelGGL((logprobs_grad_kernel<decltype(t)>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
+    });
+    return step_launched();
+}
+
+}  // namespace
+}  // namespace dcr
+
+extern "C" {
+
+int32_t dcr_logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
+                     uint32_t targets_bytes, float scale, float* logp, float* lse, float* entropy, uint32_t top,
+                     int32_t* top_ids, float* top_values, void* workspace_dev, uint64_t ws_bytes, void* stream) try {
+    dcr::set_error("");
+    return dcr::logprobs(logits, type, stride, rows, vocab, targets, targets_bytes, scale, logp, lse, entropy, top, top_ids,
+                         top_values, workspace_dev, ws_bytes, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_logprobs_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab,
+                          const void* targets, uint32_t targets_bytes, float scale, const float* lse, const float* dlogp,
+                          const float* entropy, const float* dentropy, void* dlogits, uint64_t dlogits_stride,
+                          void* stream) try {
+    dcr::set_error("");
+    return dcr::logprobs_grad(logits, type, stride, rows, vocab, targets, targets_bytes, scale, lse, dlogp, entropy, dentropy,
+                              dlogits, dlogits_stride, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+}  // extern "C"

@@ -1,0 +1,250 @@
+// dcr_rows.hip -- rows of tokens to the slots of their experts and back.
+//
+//   dispatch      y[slot[t, j]] = x[t]
+//   combine       y[t] = sum over j of w[t, j] x[slot[t, j]]   (w absent: 1)
+//   combine_grad  dx[slot[t, j]] = w[t, j] dy[t],  dw[t, j] = <dy[t], x[slot[t, j]]>
+//
+// All are bound by memory: the rows of slots are read or written once, the
+// tokens' rows once.  So the work goes by token, never by slot (which would
+// read each token k times), and no row is moved in between.
+#include "dcr_step.h"
+
+namespace dcr {
+namespace {
+
+constexpr uint32_t kRT = 256;              // threads of a workgroup
+
+struct RowArgs {
+    const void* a;         // dispatch, combine: x; gradient: dy
+    const void* b;         // gradient: x
+    void* y;               // dispatch, combine: y; gradient: dx
+    const int32_t* slots;
+    const float* weights;
+    float* dweights;
+    uint64_t a_stride, b_stride, y_stride;
+    uint32_t tokens, width, k, n_slots;
+    uint32_t lanes_log2;   // lanes that share a token
+};
+
+// One thread holds eight columns of a token and takes them to every slot.
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(kRT) rows_dispatch_kernel(RowArgs a) {
+    const uint32_t at = blockIdx.x * (kRT >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+    if (at >= a.tokens) return;
+    const uint32_t step = 8u << a.lanes_log2;
+    const int32_t* slots = a.slots + uint64_t(at) * a.k;
+    const TX* x = static_cast<const TX*>(a.a) + uint64_t(at) * a.a_stride;
+    for (uint32_t c = (threadIdx.x & ((1u << a.lanes_log2) - 1)) * 8; c < a.width; c += step) {
+        const int n = int(min(8u, a.width - c));
+        Raw8<TX> r;
+        float v[8];
+        n == 8 ? r.load(x + c) : r.load_some(x + c, n, 0);
+        r.get(v);
+        for (uint32_t j = 0; j < a.k; ++j) {
+            const uint32_t s = uint32_t(slots[j]);
+            if (s >= a.n_slots) continue;
+            TY* y = static_cast<TY*>(a.y) + uint64_t(s) * a.y_stride + c;
+            n == 8 ? store8(y, v) : store_some(y, v, n);
+        }
+    }
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(kRT) rows_combine_kernel(RowArgs a) {
+    const uint32_t at = blockIdx.x * (kRT >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
+    if (at >= a.tokens) return;
+    const uint32_t step = 8u << a.lanes_log2;
+    const int32_t* slots = a.slots + uint64_t(at) * a.k;
+    const float* weights = a.weights + uint64_t(at) * a.k;
+    TY* y = static_cast<TY*>(a.y) + uint64_t(at) * a.y_stride;
+    for (uint32_t c = (threadIdx.x & ((1u << a.lanes_log2) - 1)) * 8; c < a.width; c += step) {
+        const int n = int(min(8u, a.width - c));
+        float sum[8] = {};
+        for (uint32_t j = 0; j < a.k; ++j) {
+            const uint32_t s = uint32_t(slots[j]);
+            if (s >= a.n_slots) continue;
+            const float w = a.weights ? weights[j] : 1.0f;
+            const TX* x = static_cast<const TX*>(a.a) + uint64_t(s) * a.a_stride + c;
+            Raw8<TX> r;
+            float v[8];
+            n == 8 ? r.load(x) : r.load_some(x, n, 0);
+            r.get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(w, v[i], sum[i]);
+        }
+        n == 8 ? store8(y + c, sum) : store_some(y + c, sum, n);
+    }
+}
+
+// A wave for each token; a lane's columns lie 512 apart.
+template <typename TD, typename TX, typename TG>
+__global__ void __launch_bounds__(kRT) rows_combine_grad_kernel(RowArgs a) {
+    const uint32_t at = blockIdx.x * (kRT / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63u;
+    if (at >= a.tokens) return;
+    const TD* dy = static_cast<const TD*>(a.a) + uint64_t(at) * a.a_stride;
+    for (uint32_t j = 0; j < a.k; ++j) {
+        const uint64_t pair = uint64_t(at) * a.k + j;
+        const uint32_t s = uint32_t(a.slots[pair]);
+        float dot = 0.0f;
+        if (s < a.n_slots) {
+            const float w = a.weights[pair];
+            const TX* x = static_cast<const TX*>(a.b) + uint64_t(s) * a.b_stride;
+            TG* dx = static_cast<TG*>(a.y) + uint64_t(s) * a.y_stride;
+            for (uint32_t c = lane * 8; c < a.width; c += 512) {
+                const int n = int(min(8u, a.width - c));
+                Raw8<TD> rd;
+                Raw8<TX> rx;
+                float d[8], v[8];
+                if (n == 8) {
+                    rd.load(dy + c);
+                    rx.load(x + c);
+                } else {
+                    rd.load_some(dy + c, n, 0);
+                    rx.load_some(x + c, n, 0);
+                }
+                rd.get(d);
+                rx.get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot = __fmaf_rn(d[i], v[i], dot);
+                    d[i] *= w;
+                }
+                n == 8 ? store8(dx + c, d) : store_some(dx + c, d, n);
+            }
+        }
+        dot = lanes_sum<64>(dot);
+        if (lane == 0) a.dweights[pair] = dot;
+    }
+}
+
+int32_t check_rows(uint64_t tokens, uint64_t width, uint32_t k, uint64_t n_slots, const int32_t* slots) {
+    if (tokens >= (uint64_t(1) << 31) || n_slots >= (uint64_t(1) << 31) || width >= (uint64_t(1) << 31))
+        return step_fail(DCR_E_INVAL, "2^31 rows, slots or columns or more");
+    if (!k || k > DCR_EXPERTS_MAX_K) return step_fail(DCR_E_INVAL, "k is not 1 .. 64");
+    if (tokens && width) return check_array(slots, "slots");
+    return DCR_OK;
+}
+
+// the least power of two of lanes that holds a row in one step, at most a workgroup
+uint32_t row_lanes_log2(uint64_t width) {
+    uint32_t l = 0;
+    while (l < 8 && (uint64_t(8) << l) < width) ++l;
+    return l;
+}
+
+int32_t row_grid(uint64_t tokens, uint32_t per_group, uint32_t* grid) {
+    const uint64_t g = (tokens + per_group - 1) / per_group;
+    if (g * kRT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many rows for one launch");
+    *grid = uint32_t(g);
+    return DCR_OK;
+}
+
+int32_t dispatch_rows(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t tokens, uint64_t width, const int32_t* slots,
+                      uint32_t k, void* y, uint32_t y_type, uint64_t y_stride, uint64_t n_slots, hipStream_t st) {
+    int32_t rc;
+    if ((rc = check_rows(tokens, width, k, n_slots, slots)) || (rc = check_matrix(x, x_type, tokens, width, x_stride, "x")) ||
+        (rc = check_matrix(y, y_type, n_slots, width, y_stride, "y")))
+        return rc;
+    if (!tokens || !width || !n_slots) return DCR_OK;
+    RowArgs a{};
+    a.a = x, a.y = y, a.slots = slots, a.a_stride = x_stride, a.y_stride = n_slots > 1 ? y_stride : 0;
+    a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
+    a.lanes_log2 = row_lanes_log2(width);
+    uint32_t grid;
+    if ((rc = row_grid(tokens, kRT >> a.lanes_log2, &grid))) return rc;
+    with_type(x_type, [&](auto tx) {
+        with_type(y_type, [&](auto ty) {
+            hipLaunchKernelGGL((rows_dispatch_kernel<decltype(tx), decltype(ty)>), dim3(grid), dim3(kRT), 0, st, a);
+        });
+    });
+    return step_launched();
+}
+
+int32_t combine_rows(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots,
+                     const float* weights, uint64_t tokens, uint64_t width, uint32_t k, void* y, uint32_t y_type,
+                     uint64_t y_stride, hipStream_t st) {
+    int32_t rc;
+    if ((rc = check_rows(tokens, width, k, n_slots, slots)) || (rc = check_matrix(x, x_type, n_slots, width, x_stride, "x")) ||
+        (rc = check_matrix(y, y_type, tokens, width, y_stride, "y")))
+        return rc;
+    if (!tokens || !width) return DCR_OK;
+    if (weights && (rc = check_array(weights, "weights"))) return rc;
+    RowArgs a{};
+    a.a = x, a.y = y, a.slots = slots, a.weights = weights, a.a_stride = n_slots > 1 ? x_stride : 0, a.y_stride = y_stride;
+    a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
+    a.lanes_log2 = row_lanes_log2(width);
+    uint32_t grid;
+    if ((rc = row_grid(tokens, kRT >> a.lanes_log2, &grid))) return rc;
+    with_type(x_type, [&](auto tx) {
+        with_type(y_type, [&](auto ty) {
+            hipLaunchKernelGGL((rows_combine_kernel<decltype(tx), decltype(ty)>), dim3(grid), dim3(kRT), 0, st, a);
+        });
+    });
+    return step_launched();
+}
+
+int32_t combine_rows_grad(const void* dy, uint32_t dy_type, uint64_t dy_stride, uint64_t tokens, uint64_t width, const void* x,
+                          uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots, const float* weights,
+                          uint32_t k, void* dx, uint32_t dx_type, uint64_t dx_stride, float* dweights, hipStream_t st) {
+    int32_t rc;
+    if ((rc = check_rows(tokens, width, k, n_slots, slots)) || (rc = check_matrix(dy, dy_type, tokens, width, dy_stride, "dy")) ||
+        (rc = check_matrix(x, x_type, n_slots, width, x_stride, "x")) ||
+        (rc = check_matrix(dx, dx_type, n_slots, width, dx_stride, "dx")))
+        return rc;
+    if (!tokens) return DCR_OK;
+    if ((rc = check_array(slots, "slots")) || (rc = check_array(weights, "weights")) || (rc = check_array(dweights, "dweights")))
+        return rc;
+    RowArgs a{};
+    a.a = dy, a.b = x, a.y = dx, a.slots = slots, a.weights = weights, a.dweights = dweights;
+    a.a_stride = dy_stride, a.b_stride = n_slots > 1 ? x_stride : 0, a.y_stride = n_slots > 1 ? dx_stride : 0;
+    a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
+    uint32_t grid;
+    if ((rc = row_grid(tokens, kRT / 64, &grid))) return rc;
+    with_type(dy_type, [&](auto td) {
+        with_type(x_type, [&](auto tx) {
+            with_type(dx_type, [&](auto tg) {
+                hipLaunchKernelGGL((rows_combine_grad_kernel<decltype(td), decltype(tx), decltype(tg)>), dim3(grid), dim3(kRT), 0,
+                                   st, a);
+            });
+        });
+    });
+    return step_launched();
+}
+
+}  // namespace
+}  // namespace dcr
+
+extern "C" {
+
+int32_t dcr_experts_dispatch(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t tokens, uint64_t width,
+                             const int32_t* slots, uint32_t k, void* y, uint32_t y_type, uint64_t y_stride, uint64_t n_slots,
+                             void* stream) try {
+    dcr::set_error("");
+    return dcr::dispatch_rows(x, x_type, x_stride, tokens, width, slots, k, y, y_type, y_stride, n_slots,
+                              static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_experts_combine(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots,
+                            const float* weights, uint64_t tokens, uint64_t width, uint32_t k, void* y, uint32_t y_type,
+                            uint64_t y_stride, void* stream) try {
+    dcr::set_error("");
+    return dcr::combine_rows(x, x_type, x_stride, n_slots, slots, weights, tokens, width, k, y, y_type, y_stride,
+                             static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+int32_t dcr_experts_combine_grad(const void* dy, uint32_t dy_type, uint64_t dy_stride, uint64_t tokens, uint64_t width,
+                                 const void* x, uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots,
+                                 const float* weights, uint32_t k, void* dx, uint32_t dx_type, uint64_t dx_stride,
+                                 float* dweights, void* stream) try {
+    dcr::set_error("");
+    return dcr::combine_rows_grad(dy, dy_type, dy_stride, tokens, width, x, x_type, x_stride, n_slots, slots, weights, k, dx,
+                                  dx_type, dx_stride, dweights, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return DCR_E_NOMEM;
+}
+
+}  // extern "C"

@@ -1,0 +1,138 @@
+// dcr_step.h -- what the calls of a training turn share (choice of experts,
+// rows to experts, log probabilities, AdamW): checks of matrices, accesses of
+// eight or four elements at any alignment, sums over lanes.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <string>
+#include <type_traits>
+
+#include "dcr_fp4.h"
+
+namespace dcr {
+
+// 16, 8 and 4 bytes at any alignment of whole elements (the hardware takes them)
+typedef u32x4 u32x4_el __attribute__((aligned(2)));
+typedef u32x2 u32x2_el __attribute__((aligned(2)));
+typedef uint32_t u32_el __attribute__((aligned(2)));
+
+// ---------------------------------------------------------------- host side
+
+inline int32_t step_fail(int32_t rc, const std::string& m) { return fp4_fail(rc, m); }
+inline int32_t step_launched() { return fp4_launched(); }
+
+inline uint32_t type_bytes(uint32_t type) { return type == DCR_F32 ? 4 : 2; }
+
+// DCR_OK, or the refusal of a matrix of fp32 or bf16
+inline int32_t check_matrix(const void* x, uint32_t type, uint64_t rows, uint64_t cols, uint64_t stride, const char* what) {
+    const std::string w = what;
+    if (type != DCR_F32 && type != DCR_BF16) return step_fail(DCR_E_INVAL, w + ": type is neither fp32 nor bf16");
+    if (!rows || !cols) return DCR_OK;
+    if (!x) return step_fail(DCR_E_INVAL, w + ": NULL");
+    if (reinterpret_cast<uintptr_t>(x) & (type_bytes(type) - 1)) return step_fail(DCR_E_INVAL, w + ": not aligned to its elements");
+    if (rows > 1 && stride < cols) return step_fail(DCR_E_INVAL, w + ": row stride smaller than a row");
+    if (rows > 1 && stride >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, w + ": row stride of 2^32 elements or more");
+    return DCR_OK;
+}
+
+// DCR_OK, or the refusal of a contiguous array of 4-byte (or `bytes`-byte) elements
+inline int32_t check_array(const void* x, const char* what, uint32_t bytes = 4) {
+    if (!x) return step_fail(DCR_E_INVAL, std::string(what) + ": NULL");
+    if (reinterpret_cast<uintptr_t>(x) & (bytes - 1)) return step_fail(DCR_E_INVAL, std::string(what) + ": not aligned to its elements");
+    return DCR_OK;
+}
+
+inline int32_t check_step_workspace(const void* ws, uint64_t bytes) {
+    if (!ws || !al16(ws)) return step_fail(DCR_E_INVAL, "workspace is NULL or not 16-byte aligned");
+    if (bytes < DCR_STEP_WORKSPACE_BYTES) return step_fail(DCR_E_CAPACITY, "workspace too small");
+    return DCR_OK;
+}
+
+// f(element) with the type's element (uint16_t: bf16)
+template <typename F>
+void with_type(uint32_t type, F&& f) {
+    type == DCR_BF16 ? f(uint16_t()) : f(float());
+}
+
+// -------------------------------------------------------------- device side
+
+__device__ __forceinline__ float wide(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
+__device__ __forceinline__ float wide(float x) { return x; }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ void narrow(float x, uint16_t* p) { *p = __builtin_bit_cast(uint16_t, (__bf16)x); }
+__device__ __forceinline__ void narrow(float x, float* p) { *p = x; }
+
+__device__ __forceinline__ void unpack2(uint32_t w, float* v) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+
+// Eight elements as they lie in memory: held apart from their values so that
+// loads can be on their way while others are used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    u32x4 q;
+    __device__ __forceinline__ void load(const uint16_t* p) { q = *reinterpret_cast<const u32x4_el*>(p); }
+    // n of them (0 .. 8), the others `rest`
+    __device__ __forceinline__ void load_some(const uint16_t* p, int n, uint32_t rest) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = (2 * i < n ? uint32_t(p[2 * i]) : rest) | ((2 * i + 1 < n ? uint32_t(p[2 * i + 1]) : rest) << 16);
+    }
+    __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack2(q[i], v + 2 * i);
+    }
+};
+template <>
+struct Raw8<float> {
+    u32x4 q[2];
+    __device__ __forceinline__ void load(const float* p) {
+        q[0] = *reinterpret_cast<const u32x4_el*>(p);
+        q[1] = *reinterpret_cast<const u32x4_el*>(p + 4);
+    }
+    __device__ __forceinline__ void load_some(const float* p, int n, uint32_t rest) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i >> 2][i & 3] = i < n ? __float_as_uint(p[i]) : rest << 16;
+    }
+    __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(q[i >> 2][i & 3]);
+    }
+};
+constexpr uint32_t kBf16MinusInf = 0xFF80u;   // `rest` of load_some: -infinity in either type
+
+__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pack2(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<u32x4_el*>(p) = q;
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 q = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        *reinterpret_cast<u32x4_el*>(p + 4 * h) = __builtin_bit_cast(u32x4, q);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, const float* v, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) narrow(v[i], p + i);
+}
+
+template <int LANES, typename T>
+__device__ __forceinline__ T lanes_sum(T v) {
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+}  // namespace dcr

@@ -9,7 +9,10 @@ The names follow the C-ABI: ``dcr_plan_build``, ``dcr_encode``,
 ``dcr_encode_retry_partial``, ``dcr_encode_retry_from_delta``, ``dcr_apply``,
 ``dcr_apply_overwrite_retry``, ``dcr_apply_sharded``, ``dcr_apply_overwrite_retry_sharded``, and for weights in 4
 bits ``dcr_fp4_quantize``, ``dcr_fp4_dequantize``, ``dcr_fp4_matmul``, ``dcr_fp4_matmul_q``,
-``dcr_fp4_matmul_grad`` (plus the small helpers around them).
+``dcr_fp4_matmul_grad`` (plus the small helpers around them).  One turn of training round a refit:
+``dcr_experts_select``, ``dcr_experts_select_grad``, ``dcr_experts_order``, ``dcr_experts_dispatch``,
+``dcr_experts_combine``, ``dcr_experts_combine_grad``, ``dcr_logprobs``, ``dcr_logprobs_grad`` and ``dcr_adamw_step`` (on
+``AdamWTensors``).
 """
 from __future__ import annotations
 
@@ -112,6 +115,22 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         fn.argtypes = [P, U64, U64, P, P, U32, P, U32, U64, P, U64, P]
     lib.dcr_fp4_matmul_q.restype = I32
     lib.dcr_fp4_matmul_q.argtypes = [P, P, P, U32, P, U32, U64, P, U64, P]
+    FLT = ctypes.c_float
+    for name, args in (
+            ("dcr_experts_select", [P, U32, U64, U64, U32, P, U32, U32, U32, U32, FLT, U32, P, P, P]),
+            ("dcr_experts_select_grad", [P, U32, U64, U64, U32, P, P, U32, U32, U32, FLT, P, U64, P]),
+            ("dcr_experts_order", [P, U64, U32, P, P, P, U64, P]),
+            ("dcr_experts_dispatch", [P, U32, U64, U64, U64, P, U32, P, U32, U64, U64, P]),
+            ("dcr_experts_combine", [P, U32, U64, U64, P, P, U64, U64, U32, P, U32, U64, P]),
+            ("dcr_experts_combine_grad", [P, U32, U64, U64, U64, P, U32, U64, U64, P, P, U32, P, U32, U64, P, P]),
+            ("dcr_logprobs", [P, U32, U64, U64, U64, P, U32, FLT, P, P, P, U32, P, P, P, U64, P]),
+            ("dcr_logprobs_grad", [P, U32, U64, U64, U64, P, U32, FLT, P, P, P, P, P, U64, P]),
+            ("dcr_adamw_plan_build", [P, U64, ctypes.POINTER(P)]), ("dcr_adamw_plan_bytes", [P, ctypes.POINTER(U64)]),
+            ("dcr_adamw_plan_upload", [P, P, U64, P]), ("dcr_adamw_step", [P, P, P])):
+        getattr(lib, name).restype = I32
+        getattr(lib, name).argtypes = args
+    lib.dcr_adamw_plan_destroy.restype = None
+    lib.dcr_adamw_plan_destroy.argtypes = [P]
     lib.dcr_last_error.restype = ctypes.c_char_p
     lib.dcr_last_error.argtypes = []
     lib.dcr_set_kernel_events.restype = None
@@ -574,6 +593,306 @@ def dcr_fp4_matmul_grad(dy, w: Fp4Tensor, dx, offsets=None, workspace=None, stre
     """Enqueue dx = dy w, the gradient of dcr_fp4_matmul with respect to x:
     dy BF16 [m, n], dx BF16 or fp32 [m, cols]."""
     _product(load_library().dcr_fp4_matmul_grad, "dcr_fp4_matmul_grad", dy, w, dx, offsets, workspace, stream, True)
+
+
+# ------------------------------------------- one turn of training round a refit
+
+STEP_WORKSPACE_BYTES = 4 << 20     # DCR_STEP_WORKSPACE_BYTES
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1   # DCR_SCORE_*
+EXPERTS_RENORMALIZE = 1            # DCR_EXPERTS_RENORMALIZE
+ADAMW_BLOCK = 32                   # DCR_ADAMW_BLOCK
+ADAMW_NO_DECAY = 1                 # DCR_ADAMW_NO_DECAY
+
+
+def step_workspace(device="cuda"):
+    """Workspace of dcr_experts_order and dcr_logprobs (one call at a time;
+    captured graphs that may run together need one each)."""
+    import torch
+    return torch.empty(STEP_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _array(t, dtype, shape, name):
+    """Address of a contiguous tensor of one type and shape, None of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} expected, got {t.dtype} {list(t.shape)} with strides "
+                         f"{t.stride()}")
+    return t.data_ptr()
+
+
+def _need(t, name):
+    if t is None:
+        raise ValueError(f"{name}: a tensor expected")
+    return t
+
+
+def _step_space(workspace):
+    if workspace is None:
+        raise ValueError("workspace: pass one made by step_workspace()")
+    _whole(workspace)
+
+
+def dcr_experts_select(logits, ids, weights, bias=None, score=SCORE_SOFTMAX, groups=1, top_groups=1, renormalize=False,
+                       scale=1.0, stream=None) -> None:
+    """Enqueue the choice of the k best experts of each row: logits BF16 or
+    fp32 [rows, experts], ids int32 [rows, k] (-1: none left), weights fp32
+    [rows, k]; `bias` (fp32 [experts]) is seen by the choice alone, which is
+    among the experts of the `top_groups` best of `groups` groups."""
+    import torch
+    rows, k = ids.shape
+    p, ty, stride = _wide(logits, rows, logits.shape[-1], "logits")
+    experts = logits.shape[1]
+    i, w = _array(ids, torch.int32, (rows, k), "ids"), _array(weights, torch.float32, (rows, k), "weights")
+    b = _array(bias, torch.float32, (experts,), "bias")
+    dev = _one_device(logits, ids, weights, bias)
+    _fp4_call(torch, load_library().dcr_experts_select, "dcr_experts_select", dev, stream, p, ty, stride, rows, experts, b,
+              score, groups, top_groups, EXPERTS_RENORMALIZE if renormalize else 0, scale, k, i, w)
+
+
+def dcr_experts_select_grad(logits, ids, dweights, dlogits, score=SCORE_SOFTMAX, renormalize=False, scale=1.0,
+                            stream=None) -> None:
+    """Enqueue the gradient of dcr_experts_select's weights with respect to the
+    logits; dlogits has the logits' type and may be the logits."""
+    import torch
+    rows, k = ids.shape
+    experts = logits.shape[-1]
+    p, ty, stride = _wide(logits, rows, experts, "logits")
+    d, dty, d_stride = _wide(dlogits, rows, experts, "dlogits")
+    if dty != ty:
+        raise ValueError(f"dlogits: {logits.dtype} expected, got {dlogits.dtype}")
+    i, w = _array(ids, torch.int32, (rows, k), "ids"), _array(dweights, torch.float32, (rows, k), "dweights")
+    dev = _one_device(logits, ids, dweights, dlogits)
+    _fp4_call(torch, load_library().dcr_experts_select_grad, "dcr_experts_select_grad", dev, stream, p, ty, stride, rows,
+              experts, i, w, k, score, EXPERTS_RENORMALIZE if renormalize else 0, scale, d, d_stride)
+
+
+def dcr_experts_order(ids, offsets, slots, workspace, stream=None) -> None:
+    """Enqueue the slots of the pairs sorted by expert (int32, like ids; -1
+    without one) and the experts' offsets (int32 [experts + 1])."""
+    import torch
+    _step_space(workspace)
+    i, s = _array(ids, torch.int32, ids.shape, "ids"), _array(slots, torch.int32, ids.shape, "slots")
+    o = _array(offsets, torch.int32, offsets.shape, "offsets")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: [experts + 1] expected")
+    dev = _one_device(ids, offsets, slots, workspace)
+    _fp4_call(torch, load_library().dcr_experts_order, "dcr_experts_order", dev, stream, i, ids.numel(), offsets.numel() - 1,
+              o, s, workspace.data_ptr(), workspace.nbytes)
+
+
+def dcr_experts_dispatch(x, slots, y, stream=None) -> None:
+    """Enqueue y[slots[t, j]] = x[t]: x [tokens, width], slots int32 [tokens, k],
+    y [slots, width], each BF16 or fp32; other rows of y stay as they are."""
+    import torch
+    tokens, k = slots.shape
+    width = x.shape[-1]
+    xp, xt, xs = _wide(x, tokens, width, "x")
+    yp, yt, ys = _wide(y, None, width, "y")
+    s = _array(slots, torch.int32, (tokens, k), "slots")
+    dev = _one_device(x, slots, y)
+    _fp4_call(torch, load_library().dcr_experts_dispatch, "dcr_experts_dispatch", dev, stream, xp, xt, xs, tokens, width, s,
+              k, yp, yt, ys, y.shape[0])
+
+
+def dcr_experts_combine(x, slots, weights, y, stream=None) -> None:
+    """Enqueue y[t] = sum over j of weights[t, j] x[slots[t, j]]; `weights`
+    (fp32 [tokens, k]) None: 1, the gradient of dcr_experts_dispatch."""
+    import torch
+    tokens, k = slots.shape
+    width = y.shape[-1]
+    xp, xt, xs = _wide(x, None, width, "x")
+    yp, yt, ys = _wide(y, tokens, width, "y")
+    s, w = _array(slots, torch.int32, (tokens, k), "slots"), _array(weights, torch.float32, (tokens, k), "weights")
+    dev = _one_device(x, slots, weights, y)
+    _fp4_call(torch, load_library().dcr_experts_combine, "dcr_experts_combine", dev, stream, xp, xt, xs, x.shape[0], s, w,
+              tokens, width, k, yp, yt, ys)
+
+
+def dcr_experts_combine_grad(dy, x, slots, weights, dx, dweights, stream=None) -> None:
+    """Enqueue dx[slots[t, j]] = weights[t, j] dy[t] (other rows stay as they
+    are) and dweights[t, j] = <dy[t], x[slots[t, j]]>."""
+    import torch
+    tokens, k = slots.shape
+    width = dy.shape[-1]
+    dp, dt, ds = _wide(dy, tokens, width, "dy")
+    xp, xt, xs = _wide(x, None, width, "x")
+    n = x.shape[0]
+    gp, gt, gs = _wide(dx, n, width, "dx")
+    s, w = _array(slots, torch.int32, (tokens, k), "slots"), _array(_need(weights, "weights"), torch.float32, (tokens, k), "weights")
+    dw = _array(dweights, torch.float32, (tokens, k), "dweights")
+    dev = _one_device(dy, x, slots, weights, dx, dweights)
+    _fp4_call(torch, load_library().dcr_experts_combine_grad, "dcr_experts_combine_grad", dev, stream, dp, dt, ds, tokens,
+              width, xp, xt, xs, n, s, w, k, gp, gt, gs, dw)
+
+
+def _targets(t, rows):
+    """(address, bytes of an element) of target tokens."""
+    import torch
+    if t is None:
+        return None, 4
+    if t.dtype is not torch.int32 and t.dtype is not torch.int64:
+        raise ValueError(f"targets: int32 or int64 expected, got {t.dtype}")
+    return _array(t, t.dtype, (rows,), "targets"), t.element_size()
+
+
+def dcr_logprobs(logits, targets, logp=None, lse=None, entropy=None, top_ids=None, top_values=None, scale=1.0,
+                 workspace=None, stream=None) -> None:
+    """Enqueue the log probabilities of `targets` (int32 or int64 [rows],
+    negative: none; None without logp) under softmax(scale * logits), logits
+    BF16 or fp32 [rows, vocab]; `lse` and `entropy` fp32 [rows], and the most
+    probable tokens: top_ids int32, top_values fp32 [rows, top]."""
+    import torch
+    rows, vocab = logits.shape
+    p, ty, stride = _wide(logits, rows, vocab, "logits")
+    if logp is not None:
+        _need(targets, "targets")
+    t, tb = _targets(targets, rows)
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    if (top_ids is None) != (top_values is None):
+        raise ValueError("top_ids and top_values go together")
+    a, b, c = (_array(v, torch.float32, (rows,), n) for v, n in ((logp, "logp"), (lse, "lse"), (entropy, "entropy")))
+    i, v = _array(top_ids, torch.int32, (rows, top), "top_ids"), _array(top_values, torch.float32, (rows, top), "top_values")
+    _step_space(workspace)
+    dev = _one_device(logits, targets, logp, lse, entropy, top_ids, top_values, workspace)
+    _fp4_call(torch, load_library().dcr_logprobs, "dcr_logprobs", dev, stream, p, ty, stride, rows, vocab, t, tb, scale, a, b,
+              c, top, i, v, workspace.data_ptr(), workspace.nbytes)
+
+
+def dcr_logprobs_grad(logits, targets, lse, dlogp, dlogits, entropy=None, dentropy=None, scale=1.0, stream=None) -> None:
+    """Enqueue the gradient of dcr_logprobs's logp (and, with `dentropy`, its
+    entropy) with respect to the logits; dlogits has the logits' type and may
+    be the logits."""
+    import torch
+    rows, vocab = logits.shape
+    p, ty, stride = _wide(logits, rows, vocab, "logits")
+    d, dty, d_stride = _wide(dlogits, rows, vocab, "dlogits")
+    if dty != ty:
+        raise ValueError(f"dlogits: {logits.dtype} expected, got {dlogits.dtype}")
+    if dentropy is not None:
+        _need(entropy, "entropy")
+    t, tb = _targets(_need(targets, "targets"), rows)
+    a, b, c, e = (_array(v, torch.float32, (rows,), n) for v, n in
+                  ((_need(lse, "lse"), "lse"), (_need(dlogp, "dlogp"), "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")))
+    dev = _one_device(logits, targets, lse, dlogp, dlogits, entropy, dentropy)
+    _fp4_call(torch, load_library().dcr_logprobs_grad, "dcr_logprobs_grad", dev, stream, p, ty, stride, rows, vocab, t, tb,
+              scale, a, b, c, e, d, d_stride)
+
+
+class AdamWDesc(ctypes.Structure):
+    """dcr_adamw_tensor."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scales", "v_scales", "copy")] + \
+        [("numel", ctypes.c_uint64), ("first", ctypes.c_uint64)] + \
+        [(n, ctypes.c_uint32) for n in ("param_type", "grad_type", "state_bits", "flags")]
+
+
+class AdamWArgs(ctypes.Structure):
+    """dcr_adamw_args."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + \
+        [("step", ctypes.c_uint64), ("live", ctypes.c_void_p), ("dither_seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class AdamWTensors:
+    """The tensors that dcr_adamw_step updates, with their moments, and the
+    plan of the step over them: addresses laid out once in device memory.
+
+    `params` and `grads` are lists of contiguous BF16 or fp32 tensors (any
+    shape).  `bits` 32: moments `m`, `v` in fp32; 8: float8_e4m3fn codes with
+    uint8 `m_scales`, `v_scales` (one for each ADAMW_BLOCK elements), v by its
+    square root.  Moments that are not given are made, zero.  `copies` (bf16,
+    of fp32 parameters) receive the rounded parameters: the shards or canonical
+    tensors that a refit compares.  `decay`: one truth value a tensor (default:
+    all); `first`: the index of a tensor's first element to the dither, so
+    that a shard is rounded as the whole tensor would be (default: one tensor
+    behind the other).
+
+    The buffers are kept; gradients are written into the same tensors step
+    after step.  The step may follow on any stream."""
+
+    def __init__(self, params, grads, bits=32, copies=None, m=None, v=None, m_scales=None, v_scales=None, decay=None,
+                 first=None):
+        import torch
+        if bits not in (8, 32):
+            raise ValueError("bits is 8 or 32")
+        n = len(params)
+        if n == 0:
+            raise ValueError("no tensors")
+        types = {torch.float32: F32, torch.bfloat16: BF16}
+        state = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        make = lambda t, ty, per: torch.zeros(-(-t.numel() // per), dtype=ty, device=t.device)  # noqa: E731
+        self.bits, self.params, self.grads = bits, list(params), list(grads)
+        self.copies = [None] * n if copies is None else list(copies)
+        self.m = [make(p, state, 1) for p in params] if m is None else list(m)
+        self.v = [make(p, state, 1) for p in params] if v is None else list(v)
+        self.m_scales = self.v_scales = [None] * n
+        if bits == 8:
+            self.m_scales = [make(p, torch.uint8, ADAMW_BLOCK) for p in params] if m_scales is None else list(m_scales)
+            self.v_scales = [make(p, torch.uint8, ADAMW_BLOCK) for p in params] if v_scales is None else list(v_scales)
+        decay = [True] * n if decay is None else list(decay)
+        if first is None:
+            first = [0]
+            for p in params:
+                first.append(first[-1] + -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK)
+            first = first[:-1]
+        columns = (self.params, self.grads, self.m, self.v, self.m_scales, self.v_scales, self.copies, decay, first)
+        if any(len(c) != n for c in columns):
+            raise ValueError(f"{n} tensors: lists of that length expected")
+        self.index = _one_device(self.params[0])
+        descs = (AdamWDesc * n)()
+        for i, (p, g, a, b, sa, sb, c, d, f) in enumerate(zip(*columns)):
+            count = p.numel()
+            for name, t, ty, size in (("params", p, None, count), ("grads", g, None, count), ("m", a, state, count),
+                                      ("v", b, state, count), ("m_scales", sa, torch.uint8, -(-count // ADAMW_BLOCK)),
+                                      ("v_scales", sb, torch.uint8, -(-count // ADAMW_BLOCK)),
+                                      ("copies", c, torch.bfloat16, count)):
+                if t is None and (name == "copies" or (bits == 32 and name.endswith("scales"))):
+                    continue
+                if t.numel() != size or not t.is_contiguous() or (t.dtype not in types if ty is None else t.dtype is not ty):
+                    raise ValueError(f"{name}[{i}]: {size} contiguous elements of {ty or 'float32 or bfloat16'} expected, got "
+                                     f"{t.dtype} {list(t.shape)}")
+                if t.get_device() != self.index:
+                    raise ValueError(f"tensors on different devices: cuda:{self.index} and {t.device}")
+            at = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()  # noqa: E731
+            descs[i] = AdamWDesc(at(p), at(g), at(a), at(b), at(sa), at(sb), at(c), count, int(f), types[p.dtype],
+                                 types[g.dtype], bits, 0 if d else ADAMW_NO_DECAY)
+        lib = load_library()
+        handle = ctypes.c_void_p()
+        _check(lib.dcr_adamw_plan_build(ctypes.addressof(descs), n, ctypes.byref(handle)), "dcr_adamw_plan_build")
+        self.handle = handle.value
+        size = ctypes.c_uint64()
+        _check(lib.dcr_adamw_plan_bytes(self.handle, ctypes.byref(size)), "dcr_adamw_plan_bytes")
+        with torch.cuda.device(self.index):
+            self.table = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+            _check(lib.dcr_adamw_plan_upload(self.handle, self.table.data_ptr(), size.value, _stream(None)),
+                   "dcr_adamw_plan_upload")
+            # (the first step may come on another stream)
+            torch.cuda.current_stream().synchronize()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:
+            _lib.dcr_adamw_plan_destroy(h)
+
+
+def dcr_adamw_step(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0,
+                   dither=0, live=None, stream=None) -> None:
+    """Enqueue step number `step` (1 upwards) of AdamW on all tensors.  `dither`:
+    seed of the rounding of 8-bit moments (0: to nearest).  `live`: float64 [3]
+    in device memory, the step number, lr and grad_scale that the GPU reads in
+    place of those passed (for captured graphs)."""
+    import torch
+    if not 0 <= dither < 1 << 32:
+        raise ValueError("dither: a seed below 2^32 expected")
+    if live is None and not 1 <= step <= 1 << 53:
+        raise ValueError("step: 1 upwards expected")
+    if live is not None:
+        _one_device(tensors.table, live)
+        _array(live, torch.float64, (3,), "live")
+        tensors.live = live
+    args = AdamWArgs(lr, beta1, beta2, eps, weight_decay, grad_scale, 0 if live is not None else int(step),
+                     None if live is None else live.data_ptr(), dither, 0)
+    _fp4_call(torch, load_library().dcr_adamw_step, "dcr_adamw_step", tensors.index, stream, tensors.handle,
+              ctypes.addressof(args))
 
 
 def dcr_set_kernel_events(start=None, stop=None) -> None:

@@ -673,6 +673,193 @@ int32_t dcr_fp4_matmul_grad(const void* dy, uint64_t m, uint64_t dy_stride, cons
                             const int32_t* offsets, uint32_t n_groups, void* dx, uint32_t dx_type,
                             uint64_t dx_stride, void* workspace_dev, uint64_t ws_bytes, void* stream);
 
+/* --------------------------------------- one turn of training round a refit
+ *
+ * The calls below stand on both sides of a refit: the router of a mixture of
+ * experts and the rows of its grouped products (dcr_fp4_matmul with offsets),
+ * the log probabilities that a policy is trained on and that tell trainer and
+ * receiver apart after a refit, with their gradient, and the optimizer step
+ * that makes the weights which dcr_encode and dcr_fp4_quantize take.
+ *
+ * Matrices have rows of consecutive elements, a row stride in elements (at
+ * least a row, below 2^32; not looked at where there is one row) and any
+ * alignment of whole elements; rows on 16-byte borders are faster.  Arrays
+ * named "[n]" or "[rows, k]" are contiguous and aligned to their elements.
+ * Results may not overlap what a call reads unless that is said.  Sums are held
+ * in fp32 or more and their order depends on sizes and arguments alone: equal
+ * calls give equal bits. */
+#define DCR_STEP_WORKSPACE_BYTES (4u << 20)
+enum { DCR_SCORE_SOFTMAX = 0, DCR_SCORE_SIGMOID = 1 };
+/* dcr_experts_select option: the chosen weights are divided by their sum */
+enum { DCR_EXPERTS_RENORMALIZE = 1 };
+#define DCR_EXPERTS_MAX 1024
+#define DCR_EXPERTS_MAX_K 64
+#define DCR_EXPERTS_MAX_GROUPS 64
+
+/* The k best experts of each row of a router's logits, and their weights.
+ *   logits      rows x experts (DCR_F32 or DCR_BF16), 1 .. 1024 experts; an
+ *               expert at -infinity is shut: it has score 0 and is not chosen
+ *   bias        NULL, or [experts] fp32, added to the scores for the choice
+ *               alone (it balances the experts' load, the weights do not see it)
+ *   score       s = softmax over the row's experts, or sigmoid of each logit
+ *   groups, top_groups  experts lie in `groups` groups of consecutive ones (a
+ *               divisor of the experts, at most 64); only those of the
+ *               top_groups best groups are chosen from, a group's value being
+ *               the sum of its two largest s + bias.  1, 1: all
+ *   options     0 or DCR_EXPERTS_RENORMALIZE
+ *   scale       factor of the weights
+ *   ids         [rows, k] int32: the chosen ones, the largest s + bias first,
+ *               the lowest index of equals first; -1 where fewer than k are open
+ *   weights     [rows, k] fp32: scale * s, over the sum of the row's chosen s
+ *               where renormalised; 0 where the id is -1
+ * 1 <= k <= min(64, experts).  The choice is that of 64-bit arithmetic; without
+ * a bias experts are compared by their logits.  A NaN among the values compared
+ * counts as the largest, and makes weights NaN. */
+int32_t dcr_experts_select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint32_t experts,
+                           const float* bias, uint32_t score, uint32_t groups, uint32_t top_groups, uint32_t options,
+                           float scale, uint32_t k, int32_t* ids, float* weights, void* stream);
+
+/* Gradient of the weights of dcr_experts_select with respect to the logits, at
+ * the choice `ids` (constant; an id outside 0 .. experts - 1 has no part; one
+ * that occurs twice counts twice).  dlogits has the logits' type and may be the
+ * logits.  The remaining arguments as there. */
+int32_t dcr_experts_select_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint32_t experts,
+                                const int32_t* ids, const float* dweights, uint32_t k, uint32_t score, uint32_t options,
+                                float scale, void* dlogits, uint64_t dlogits_stride, void* stream);
+
+/* Where the chosen pairs go: the pairs sorted by expert, those of an expert in
+ * their own order.
+ *   ids        [n] int32 (the ids of dcr_experts_select, rows * k of them); one
+ *              outside 0 .. experts - 1 goes nowhere
+ *   offsets    [experts + 1] int32: expert e has slots offsets[e] ..
+ *              offsets[e + 1] - 1, as the grouped products take them
+ *   slots      [n] int32: the slot of each pair, -1 of one that goes nowhere;
+ *              may be the ids
+ *   workspace_dev  at least DCR_STEP_WORKSPACE_BYTES (DCR_E_CAPACITY), 16-byte
+ *              aligned, one call at a time */
+int32_t dcr_experts_order(const int32_t* ids, uint64_t n, uint32_t experts, int32_t* offsets, int32_t* slots,
+                          void* workspace_dev, uint64_t ws_bytes, void* stream);
+
+/* y[slots[t, j], :] = x[t, :] for every token t and j < k.  Slots outside 0 ..
+ * n_slots - 1 are left out; rows of y that no pair has are left as they are.  A
+ * slot named twice gets one of its rows, element by element.  x and y may have
+ * different types. */
+int32_t dcr_experts_dispatch(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t tokens, uint64_t width,
+                             const int32_t* slots, uint32_t k, void* y, uint32_t y_type, uint64_t y_stride, uint64_t n_slots,
+                             void* stream);
+
+/* y[t, :] = sum over j of weights[t, j] * x[slots[t, j], :], in the order of j,
+ * over the slots in 0 .. n_slots - 1 (zeros where there is none).  weights NULL:
+ * 1, which is the gradient of dcr_experts_dispatch with respect to x. */
+int32_t dcr_experts_combine(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots,
+                            const float* weights, uint64_t tokens, uint64_t width, uint32_t k, void* y, uint32_t y_type,
+                            uint64_t y_stride, void* stream);
+
+/* Gradient of dcr_experts_combine:
+ *   dx[slots[t, j], :] = weights[t, j] * dy[t, :]   (other rows are left as they are)
+ *   dweights[t, j] = sum of dy[t, :] * x[slots[t, j], :]   (0 without a slot)
+ * with slots that differ from one another. */
+int32_t dcr_experts_combine_grad(const void* dy, uint32_t dy_type, uint64_t dy_stride, uint64_t tokens, uint64_t width,
+                                 const void* x, uint32_t x_type, uint64_t x_stride, uint64_t n_slots, const int32_t* slots,
+                                 const float* weights, uint32_t k, void* dx, uint32_t dx_type, uint64_t dx_stride,
+                                 float* dweights, void* stream);
+
+#define DCR_LOGPROBS_MAX_TOP 64
+
+/* Log probabilities of given tokens under softmax(scale * logits).
+ *   logits     rows x vocab (DCR_F32 or DCR_BF16); -infinity masks a token
+ *   targets    [rows] int32 or int64 (targets_bytes 4 or 8); a negative one
+ *              stands for none (log probability 0), one past the vocabulary
+ *              gives NaN.  May be NULL with logp
+ *   scale      1 / temperature, positive and finite
+ *   logp       NULL or [rows] fp32: scale * x_t - lse
+ *   lse        NULL or [rows] fp32: log of the sum of exp(scale * x)
+ *   entropy    NULL or [rows] fp32: - sum of p log p
+ *   top        0 .. min(64, vocab): top_ids ([rows, top] int32) and top_values
+ *              ([rows, top] fp32, log probabilities) are the largest logits, the
+ *              lowest index of equals first; not looked at where top is 0
+ *   workspace_dev  as for dcr_experts_order
+ * A row with every token masked has lse and log probabilities of -infinity and
+ * entropy 0.  A row that holds a NaN or +infinity has NaN in all its floating
+ * results (NaN ranks below all numbers in top_ids).  Masks of the lowest finite
+ * number are numbers as all others: a row of nothing else is uniform. */
+int32_t dcr_logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
+                     uint32_t targets_bytes, float scale, float* logp, float* lse, float* entropy, uint32_t top,
+                     int32_t* top_ids, float* top_values, void* workspace_dev, uint64_t ws_bytes, void* stream);
+
+/* Gradient of logp and entropy with respect to the logits:
+ *   dlogits[j] = scale * (dlogp * ([j = target] - p_j) - dentropy * p_j * (log p_j + entropy)),
+ * log p_j = scale * x_j - lse, with the lse and entropy of dcr_logprobs.  dlogp:
+ * [rows] fp32 (counts as 0 without a target); dentropy NULL (entropy is then not
+ * looked at) or [rows] fp32.  dlogits has the logits' type and may be the
+ * logits.  A row whose lse is -infinity gives zeros. */
+int32_t dcr_logprobs_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab,
+                          const void* targets, uint32_t targets_bytes, float scale, const float* lse, const float* dlogp,
+                          const float* entropy, const float* dentropy, void* dlogits, uint64_t dlogits_stride, void* stream);
+
+/* A tensor of an AdamW step.  88 bytes.
+ *   param       fp32 or bf16 (param_type), updated in place
+ *   grad        fp32 or bf16 (grad_type), read
+ *   m, v        the moments.  state_bits 32: fp32.  8: e4m3 codes in blocks of
+ *               DCR_ADAMW_BLOCK elements, of v's square root in place of v
+ *   m_scales, v_scales  state_bits 8: an e8m0 byte for each block, value = code
+ *               * 2^(byte - 127), 255 is NaN.  All zeros: moments of zero
+ *   copy        NULL, or bf16: fp32 parameters are written here too, rounded (the
+ *               weights that dcr_encode compares)
+ *   numel       elements, 0 upwards
+ *   first       index of the first element to the dither: a shard takes that of
+ *               its first element in the whole tensor
+ *   flags       0 or DCR_ADAMW_NO_DECAY
+ * All buffers but the scales are 16-byte aligned; none that is written may
+ * overlap another. */
+#define DCR_ADAMW_BLOCK 32
+enum { DCR_ADAMW_NO_DECAY = 1 };
+typedef struct {
+    void* param;
+    const void* grad;
+    void *m, *v, *m_scales, *v_scales;
+    void* copy;
+    uint64_t numel, first;
+    uint32_t param_type, grad_type, state_bits, flags;
+} dcr_adamw_tensor;
+
+/* Arguments of a step.  72 bytes.
+ *   step         1 upwards: t of the bias corrections
+ *   grad_scale   factor of the gradients (1 / loss scale, clipping)
+ *   dither_seed  8-bit states: 0 rounds codes to nearest (ties up); else codes
+ *                are rounded up with the probability of the remainder, by numbers
+ *                that depend on the seed, the step and the element alone
+ *   live         NULL, or 3 doubles in device memory read when the stream gets
+ *                there: step, lr and grad_scale in place of those above (for
+ *                captured graphs) */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    uint64_t step;
+    const double* live;
+    uint32_t dither_seed, reserved;
+} dcr_adamw_args;
+
+typedef struct dcr_adamw_plan dcr_adamw_plan; /* opaque; host-owned */
+
+/* A plan over a list of tensors: their addresses and the work of a step, laid
+ * out once.  Build, upload into a table the caller owns (at least the plan's
+ * bytes, 16-byte aligned; used until the plan is destroyed), step any number of
+ * times.  A step that follows on another stream waits for the upload as for any
+ * work; steps of one plan run one after the other. */
+int32_t dcr_adamw_plan_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan** out);
+int32_t dcr_adamw_plan_bytes(const dcr_adamw_plan* plan, uint64_t* bytes);
+int32_t dcr_adamw_plan_upload(dcr_adamw_plan* plan, void* table_dev, uint64_t bytes, void* stream);
+void dcr_adamw_plan_destroy(dcr_adamw_plan* plan);
+
+/* One step on every tensor of a plan, with g = grad_scale * grad:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32 (DCR_ADAMW_NO_DECAY: without weight_decay); the update takes the moments before they are rounded
+ * to 8 bits.  A block of an 8-bit state that holds a NaN or an infinity becomes
+ * NaN; a nonzero second moment never becomes 0.  0 <= beta < 1, eps at least
+ * 2^-100. */
+int32_t dcr_adamw_step(const dcr_adamw_plan* plan, const dcr_adamw_args* args, void* stream);
+
 /* Benchmark hook.  While set (both non-NULL), every encode, apply or retry
  * call made on this host thread records `start` on its stream just before its
  * main kernel (the encode tile kernels, or the apply kernel) and `stop` just

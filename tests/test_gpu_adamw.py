@@ -1,0 +1,250 @@
+"""AdamW steps on the GPU against a plain 64-bit implementation."""
+import numpy as np
+import pytest
+import torch
+
+from bit_exact_xor_amd import dcr
+from tests import step_ref as R
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+E = 2.0 ** -24
+SIZES = [0, 1, 3, 31, 32, 33, 64, 255, 1000, 4095, 4096, 4097, 20001]
+
+
+def up(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def formula(p, g, m, v, t, lr, b1, b2, eps, wd, gs):
+    g = g * gs
+    m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+    den = np.sqrt(v / (1 - b2 ** t)) + eps
+    return p * (1 - lr * wd) - lr / (1 - b1 ** t) * m / den, m, v, den
+
+
+def tolerances(p, g, m, v, t, lr, b1, b2, eps, wd, gs):
+    """m: both products' factors and themselves are rounded (4 roundings); v: a square more; p: the decayed weight's two,
+    the update's from m's error and about 8 of its own."""
+    g = g * gs
+    tm = 4 * E * (np.abs(b1 * m) + np.abs((1 - b1) * g))
+    tv = 7 * E * (b2 * v + (1 - b2) * g * g)
+    p1, m1, v1, den = formula(p, g / gs, m, v, t, lr, b1, b2, eps, wd, gs)
+    rate = lr / (1 - b1 ** t)
+    return 3 * E * np.abs(p) + rate / den * (tm + 12 * E * np.abs(m1)) + 2.0 ** -140, tm + 2.0 ** -149, tv + 2.0 ** -140
+
+
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, grad_scale=0.37)
+
+
+def tensors_of(sizes, pt, gt, bits, rng, copy=False, **kw):
+    params = [up(rng.standard_normal(n).astype(np.float32)).to(TYPES[pt]) for n in sizes]
+    grads = [up((rng.standard_normal(n) * 10.0 ** rng.integers(-6, 2, n)).astype(np.float32)).to(TYPES[gt]) for n in sizes]
+    for g in grads:
+        g[::7] = 0
+    copies = [torch.full((n,), 7.0, dtype=torch.bfloat16, device="cuda") for n in sizes] if copy else None
+    return dcr.AdamWTensors(params, grads, bits=bits, copies=copies, **kw)
+
+
+@pytest.mark.parametrize("pt,gt", [("fp32", "fp32"), ("fp32", "bf16"), ("bf16", "bf16"), ("bf16", "fp32")])
+def test_wide_states(pt, gt):
+    """Three steps, each from the state that the one before left; tensors of all sizes in one call."""
+    rng = np.random.default_rng(1)
+    decay = [i % 3 != 1 for i in range(len(SIZES))]
+    T = tensors_of(SIZES, pt, gt, 32, rng, copy=pt == "fp32", decay=decay)
+    for t in (1, 2, 50):
+        before = [[f64(x) for x in row] for row in zip(T.params, T.grads, T.m, T.v)]
+        dcr.dcr_adamw_step(T, t, **HYPER)
+        for i, (p, g, m, v) in enumerate(before):
+            h = [HYPER["lr"], 0.9, 0.95, 1e-8, 0.1 if decay[i] else 0.0, 0.37]
+            want = formula(p, g, m, v, t, *h)
+            tp, tm, tv = tolerances(p, g, m, v, t, *h)
+            assert (np.abs(f64(T.params[i]) - want[0]) <= tp + HALF[pt] * (np.abs(want[0]) + tp)).all()
+            assert (np.abs(f64(T.m[i]) - want[1]) <= tm).all() and (np.abs(f64(T.v[i]) - want[2]) <= tv).all()
+            if pt == "fp32":
+                assert torch.equal(T.copies[i], T.params[i].bfloat16())
+
+
+@pytest.mark.parametrize("pt,gt", [("fp32", "bf16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("seed", [0, 77])
+def test_narrow_states(pt, gt, seed):
+    """Codes and scales in 8 bits: with betas that are sums of few powers of two, and gradients and moments of few bits,
+    every product is exact in 32 bits, so a moment is the exact one rounded once and its codes are the reference's; the
+    parameters take the moments before they are rounded."""
+    rng = np.random.default_rng(2)
+    T = tensors_of(SIZES, pt, gt, 8, rng)
+    h = dict(lr=1e-2, beta1=0.5, beta2=0.75, eps=1e-6, weight_decay=0.0, grad_scale=2.0)
+    for i, n in enumerate(SIZES):
+        # gradients: 1 or 3 times a power of two; moments: few codes under any scale
+        T.grads[i].copy_(up((rng.choice([0.0, 1.0, -1.0, 3.0], n) * 2.0 ** rng.integers(-9, 9, n)).astype(np.float32)))
+        T.m[i].copy_(up(rng.choice([0.0, 1.0, -1.5, 2.0, 448.0, 2.0 ** -9], n).astype(np.float32)).to(torch.float8_e4m3fn))
+        T.v[i].copy_(up(rng.choice([0.0, 1.0, 2.0, 256.0], n).astype(np.float32)).to(torch.float8_e4m3fn))
+        T.m_scales[i].copy_(up(rng.integers(120, 134, -(-n // 32)).astype(np.uint8)))
+        T.v_scales[i].copy_(up(rng.integers(120, 134, -(-n // 32)).astype(np.uint8)))
+    at = 0
+    first = []
+    for n in SIZES:
+        first.append(at)
+        at += -(-n // 32) * 32
+    before = [(f64(p), f64(g), R.from8(m.view(torch.uint8).cpu().numpy(), ms.cpu().numpy()),
+               R.from8(v.view(torch.uint8).cpu().numpy(), vs.cpu().numpy()) ** 2)
+              for p, g, m, v, ms, vs in zip(T.params, T.grads, T.m, T.v, T.m_scales, T.v_scales)]
+    dcr.dcr_adamw_step(T, 9, dither=seed, **h)
+    for i, (p, g, m, v) in enumerate(before):
+        want = formula(p, g, m, v, 9, *h.values())
+        tp, _tm, _tv = tolerances(p, g, m, v, 9, *h.values())
+        assert (np.abs(f64(T.params[i]) - want[0]) <= tp + HALF[pt] * (np.abs(want[0]) + tp)).all()
+        m32 = want[1].astype(np.float32).astype(np.float64)
+        u = np.sqrt(want[2].astype(np.float32)).astype(np.float64)        # (correctly rounded on both sides)
+        rm, rv = R.dither(np.arange(SIZES[i], dtype=np.uint64) + np.uint64(first[i]), seed, 9) if seed else (0.5, 0.5)
+        for name, x, r, keep in (("m", m32, rm, False), ("v", u, rv, True)):
+            codes, byte = R.to8(x, r, keep)
+            got = getattr(T, name)[i].view(torch.uint8).cpu().numpy()
+            assert np.array_equal(getattr(T, name + "_scales")[i].cpu().numpy(), byte), (SIZES[i], name)
+            assert np.array_equal(got, codes), (SIZES[i], name, np.nonzero(got != codes)[0][:5])
+
+
+def test_narrow_states_follow():
+    """With the dither the held moments follow small changes: over many steps with one gradient the second moment's root
+    comes near |g| although a step changes it by less than half a code (a standard deviation of the mean of 4096
+    elements' codes, each within an eighth: 2^-3 / 64 / sqrt(3) of the value, five of them and the moment's own
+    1 - 0.99^400 = 0.982)."""
+    n = 4096
+    T = dcr.AdamWTensors([torch.zeros(n, device="cuda")], [torch.full((n,), 0.37, device="cuda")], bits=8)
+    for t in range(1, 401):
+        dcr.dcr_adamw_step(T, t, lr=0.0, beta1=0.99, beta2=0.99, dither=5)
+    for codes, scales, want in ((T.m[0], T.m_scales[0], 0.37 * (1 - .99 ** 400)), (T.v[0], T.v_scales[0], 0.37 * (1 - .99 ** 400) ** .5)):
+        held = R.from8(codes.view(torch.uint8).cpu().numpy(), scales.cpu().numpy())
+        assert abs(held.mean() / want - 1) < 0.03, held.mean() / want
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_extremes(bits):
+    """Zero, tiny and huge gradients, infinities and NaN: only the element (8 bits: its block's states) is touched by them,
+    nothing else becomes other than finite, and a second moment that is not zero stays so."""
+    n = 320
+    g = torch.zeros(n, device="cuda")
+    g[0], g[33], g[70], g[100], g[130], g[200] = 1e-30, 1e18, float("nan"), float("inf"), -3e38, 1e-3
+    T = dcr.AdamWTensors([torch.ones(n, device="cuda")], [g], bits=bits)
+    for t in (1, 2):
+        dcr.dcr_adamw_step(T, t, lr=1e-3)
+    p = T.params[0]
+    bad = ~torch.isfinite(p)
+    allowed = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for i in (70, 100, 130):                    # (the square of 3e38 is infinite)
+        block = slice(i, i + 1) if bits == 32 else slice(i // 32 * 32, i // 32 * 32 + 32)
+        allowed[block] = True
+    assert not (bad & ~allowed).any() and bad[70]
+    assert (p[1:32] == 1).all() and p[33] < 1 and p[200] < 1
+    if bits == 8:
+        assert T.m_scales[0][70 // 32] == 255 and T.v_scales[0][100 // 32] == 255 and T.v_scales[0][130 // 32] == 255
+        v = T.v[0].view(torch.uint8)
+        assert v[200] > 0 and v[33] > 0 and (v[1:32] == 0).all()
+        codes = T.m[0].view(torch.uint8)
+        assert (codes[64:96] == 0).all()
+
+
+def test_smallest_second_moment_stays():
+    """A second moment far below its block's largest keeps the smallest code, not zero."""
+    g = torch.full((32,), 1e-8, device="cuda")
+    g[3] = 1.0
+    for seed in (0, 1, 2, 3):
+        T = dcr.AdamWTensors([torch.zeros(32, device="cuda")], [g], bits=8)
+        dcr.dcr_adamw_step(T, 1, dither=seed)
+        assert (T.v[0].view(torch.uint8) >= 1).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_shards_are_rounded_as_the_whole(bits):
+    """A tensor in three shards, with `first`, gives the bits of the whole tensor."""
+    rng = np.random.default_rng(3)
+    n = 3 * 1024 + 512
+    p, g = rng.standard_normal(n).astype(np.float32), rng.standard_normal(n).astype(np.float32)
+    base = (1 << 32) - 1024                        # the index passes 32 bits on the way
+    whole = dcr.AdamWTensors([up(p)], [up(g)], bits=bits, first=[base])
+    cuts = [0, 1024, 2080, n]
+    parts = dcr.AdamWTensors([up(p[a:b]) for a, b in zip(cuts, cuts[1:])], [up(g[a:b]) for a, b in zip(cuts, cuts[1:])], bits=bits,
+                             first=[base + a for a in cuts[:-1]])
+    for t in (1, 2, 3):
+        dcr.dcr_adamw_step(whole, t, dither=11)
+        dcr.dcr_adamw_step(parts, t, dither=11)
+    assert torch.equal(whole.params[0], torch.cat(parts.params))
+    for a, b in ((whole.m, parts.m), (whole.v, parts.v)):
+        assert torch.equal(a[0].view(torch.uint8), torch.cat([x.view(torch.uint8) for x in b]))
+
+
+def test_live_arguments_and_graphs():
+    """A captured step reads its number, rate and scale from device memory: replays give the bits of eager steps, with
+    eager work in between."""
+    rng = np.random.default_rng(4)
+    for bits in (8, 32):
+        mk = lambda: tensors_of([1000, 5000], "fp32", "bf16", bits, np.random.default_rng(4), copy=True)  # noqa: E731
+        A, B = mk(), mk()
+        live = torch.tensor([1.0, 1e-3, 0.5], dtype=torch.float64, device="cuda")
+        s = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            dcr.dcr_adamw_step(A, 1, live=live, beta2=0.95, weight_decay=0.01, dither=3)
+            live[0] += 1
+        for t in range(1, 6):
+            lr = 1e-3 / t
+            live[1] = lr
+            graph.replay()
+            dcr.dcr_adamw_step(B, t, lr=lr, beta2=0.95, weight_decay=0.01, grad_scale=0.5, dither=3)
+            for g, h in zip(A.grads, B.grads):
+                new = up(rng.standard_normal(g.numel()).astype(np.float32)).bfloat16()
+                torch.cuda.synchronize()
+                for x, y in ((A, B),):
+                    for a, b in zip(x.params + x.m + x.v + x.copies, y.params + y.m + y.v + y.copies):
+                        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (bits, t)
+                g.copy_(new)
+                h.copy_(new)
+
+
+def test_streams_and_lifetime():
+    """Steps on a stream of the caller's; a plan that goes away leaves its tensors."""
+    rng = np.random.default_rng(5)
+    T = tensors_of([3000], "fp32", "fp32", 32, rng)
+    U = tensors_of([3000], "fp32", "fp32", 32, np.random.default_rng(5))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for t in (1, 2, 3):
+        dcr.dcr_adamw_step(T, t, stream=s)
+        dcr.dcr_adamw_step(U, t)
+    torch.cuda.synchronize()
+    assert torch.equal(T.params[0], U.params[0])
+    p = T.params[0]
+    del T
+    assert torch.equal(p, U.params[0])
+
+
+def test_refusals_of_tensors():
+    z = lambda n, **k: torch.zeros(n, device="cuda", **k)  # noqa: E731
+    a = z(64)
+    for bad in (lambda: dcr.AdamWTensors([a], [z(63)]), lambda: dcr.AdamWTensors([a], [z(64, dtype=torch.float16)]),
+                lambda: dcr.AdamWTensors([a], [torch.zeros(64)]), lambda: dcr.AdamWTensors([a], [z(64)], m=[z(64, dtype=torch.bfloat16)]),
+                lambda: dcr.AdamWTensors([a], [z(64)], bits=8, m_scales=[z(3, dtype=torch.uint8)]),
+                lambda: dcr.AdamWTensors([a], [z(64)], copies=[z(64)]), lambda: dcr.AdamWTensors([a], [z(64), z(64)]),
+                lambda: dcr.AdamWTensors([z(128)[::2]], [z(64)]), lambda: dcr.AdamWTensors([a], [z(64)], decay=[])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: dcr.AdamWTensors([a], [a]), lambda: dcr.AdamWTensors([a, a], [z(64), z(64)]),
+                lambda: dcr.AdamWTensors([z(65)[1:]], [z(64)]),
+                lambda: dcr.AdamWTensors([z(64, dtype=torch.bfloat16)], [z(64)], copies=[z(64, dtype=torch.bfloat16)])):
+        with pytest.raises(dcr.DcrError):
+            bad()
+    T = dcr.AdamWTensors([a], [z(64)])
+    for kw in (dict(beta1=1.0), dict(beta2=-0.1), dict(eps=0.0), dict(eps=float("nan")), dict(lr=float("inf")),
+               dict(weight_decay=float("nan")), dict(grad_scale=float("nan")), dict(beta1=float("nan"))):
+        with pytest.raises(dcr.DcrError):
+            dcr.dcr_adamw_step(T, 1, **kw)
+    for kw in (dict(live=torch.zeros(3, dtype=torch.float64)), dict(live=z(3)), dict(live=z(2, dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            dcr.dcr_adamw_step(T, 1, **kw)
+    assert (a == 0).all()

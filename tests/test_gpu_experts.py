@@ -1,0 +1,335 @@
+"""The choice of experts, the order of pairs and their rows on the GPU against a plain 64-bit implementation."""
+import numpy as np
+import pytest
+import torch
+
+from bit_exact_xor_amd import dcr
+from tests import step_ref as R
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}       # half a step of a rounding, relative to the value
+SOFTMAX, SIGMOID = dcr.SCORE_SOFTMAX, dcr.SCORE_SIGMOID
+
+
+def up(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def logits_of(kind, rows, e, rng):
+    x = rng.standard_normal((rows, e)) * 2
+    if kind == "ties":               # few values: equal logits side by side, zeros of both signs
+        x = rng.integers(-2, 3, (rows, e)) * rng.choice([-1.0, 1.0], (rows, e))
+    elif kind == "masked":           # shut experts, rows with few and with no open ones
+        x[rng.random((rows, e)) < 0.4] = -np.inf
+        x[::3] = -np.inf
+        x[1::6, : max(1, e // 7)] = 0.25
+    elif kind == "lowest":           # masks of the lowest finite number
+        x[rng.random((rows, e)) < 0.5] = np.finfo(np.float32).min if e % 2 else -3.3895e38
+        x[:1] = -3.3895e38
+    elif kind == "far":              # scores far below the largest, and sigmoids at 1
+        x = np.exp(rng.uniform(0, 6, (rows, e))) * rng.choice([-1.0, 1.0], (rows, e))
+    return x
+
+
+KINDS = ["normal", "ties", "masked", "lowest", "far"]
+
+
+def run_select(x, k, bias=None, score=SOFTMAX, groups=1, top_groups=1, renormalize=False, scale=1.0):
+    ids = torch.full((x.shape[0], k), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((x.shape[0], k), float("nan"), device="cuda")
+    dcr.dcr_experts_select(x, ids, w, bias=bias, score=score, groups=groups, top_groups=top_groups, renormalize=renormalize,
+                           scale=scale)
+    return ids, w
+
+
+# (rows, experts, k): one token to many, odd numbers of experts, every layout of a row in lanes
+SIZES = [(1, 1, 1), (1, 128, 8), (3, 7, 7), (33, 60, 6), (65, 64, 1), (5, 65, 64), (130, 128, 8), (17, 160, 12), (9, 255, 3),
+         (12, 384, 8), (7, 513, 10), (4, 1024, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_select(kind, dtype):
+    """Ids are the reference's; a weight is rounded once (64-bit scores, off by about 1e-14 of themselves where the argument
+    of an exponential is rounded: up to 710 * 2^-53)."""
+    rng = np.random.default_rng(KINDS.index(kind))
+    for n, (rows, e, k) in enumerate(SIZES):
+        x = up(logits_of(kind, rows, e, rng).astype(np.float32)).to(TYPES[dtype])
+        host = f64(x)
+        for score in (SOFTMAX, SIGMOID):
+            for bias in (None, (0.2 * rng.standard_normal(e)).astype(np.float32)):
+                renorm, scale = bool((n + score) % 2), (1.0, 2.5)[n % 2]
+                ids, w = run_select(x, k, None if bias is None else up(bias), score, renormalize=renorm, scale=scale)
+                want_ids, want = R.select(host, bias, k, score == SIGMOID, renormalize=renorm, scale=scale)
+                assert np.array_equal(ids.cpu().numpy(), want_ids), (rows, e, k, score, bias is None)
+                assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all(), (rows, e, k)
+
+
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("groups,top_groups", [(2, 1), (4, 2), (8, 4), (8, 7), (16, 3), (64, 5)])
+def test_select_groups(score, groups, top_groups):
+    rng = np.random.default_rng(groups)
+    for rows, size, k in ((1, 1, 1), (19, 5, 3), (40, 16, 4), (6, 128 // groups * 2, 2)):
+        e = groups * size
+        if e > 1024:
+            continue
+        k = min(k, e)
+        for kind in ("normal", "ties", "masked"):
+            x = up(logits_of(kind, rows, e, rng).astype(np.float32))
+            for bias in (None, (0.1 * rng.standard_normal(e)).astype(np.float32)):
+                ids, w = run_select(x, k, None if bias is None else up(bias), score, groups, top_groups, renormalize=True)
+                want_ids, want = R.select(f64(x), bias, k, score == SIGMOID, groups, top_groups, True)
+                assert np.array_equal(ids.cpu().numpy(), want_ids), (rows, e, k, kind, bias is None)
+                assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all()
+
+
+def test_select_close_to_a_border():
+    """Sums of score and bias that 32 bits cannot tell apart: the bias undoes the scores' differences but for 2^-30."""
+    rng = np.random.default_rng(8)
+    for score in (SOFTMAX, SIGMOID):
+        x = rng.standard_normal((1, 96)).astype(np.float32)
+        s = R.scores(x.astype(np.float64), score == SIGMOID)[0]
+        bias = (0.5 - s + rng.integers(-3, 4, 96) * 2.0 ** -30).astype(np.float32)
+        for groups, top_groups in ((1, 1), (8, 3)):
+            ids, _w = run_select(up(x), 16, up(bias), score, groups, top_groups)
+            want, _ = R.select(x, bias, 16, score == SIGMOID, groups, top_groups)
+            assert np.array_equal(ids.cpu().numpy(), want)
+
+
+def test_select_nan_is_seen():
+    """A NaN counts as the largest and its weight is NaN; other rows do not change."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((6, 40)).astype(np.float32)
+    good, _ = R.select(x, None, 4, True)
+    x[2, 33] = np.nan
+    for groups in ((1, 1), (4, 2)):
+        ids, w = run_select(up(x), 4, None, SIGMOID, *groups)
+        assert int(ids[2, 0]) == 33 and torch.isnan(w[2, 0]) and not torch.isnan(w[[0, 1, 3, 4, 5]]).any()
+    assert np.array_equal(np.delete(run_select(up(x), 4, None, SIGMOID)[0].cpu().numpy(), 2, 0), np.delete(good, 2, 0))
+    _ids, w = run_select(up(x), 4)
+    assert torch.isnan(w[2]).all() and not torch.isnan(w[[0, 1, 3, 4, 5]]).any()
+
+
+def test_select_strided_logits():
+    rng = np.random.default_rng(2)
+    big = up(rng.standard_normal((20, 300)).astype(np.float32))
+    for dtype in (torch.float32, torch.bfloat16):
+        b = big.to(dtype)
+        for view in (b[:, 3:131], b[::2, 8:136], b[1:2, 5:], b[:, 1:8]):
+            ids, _ = run_select(view, 5)
+            assert np.array_equal(ids.cpu().numpy(), R.select(f64(view), None, 5, False)[0])
+            d = torch.full((20, 400), 5.0, dtype=dtype, device="cuda")
+            out = d[: view.shape[0], 7: 7 + view.shape[1]]
+            dw = torch.ones(view.shape[0], 5, device="cuda") * torch.arange(5, device="cuda")
+            dcr.dcr_experts_select_grad(view, ids, dw, out)
+            assert (d[:, :7] == 5).all() and (d[:, 7 + view.shape[1]:] == 5).all() and (d[view.shape[0]:] == 5).all()
+            want, most = R.select_grad(f64(view), ids.cpu().numpy(), f64(dw), False, False)
+            assert (np.abs(f64(out) - want) <= most * 2.0 ** -18 + np.abs(want) * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_select_grad(dtype, score, renormalize):
+    """Scores in 32 bits are off by the rounding of the exponential's argument (below 32 here: 2^-19) and some roundings
+    of 2^-24: 2^-18 of the sum of the terms' magnitudes, then the rounding of the result."""
+    rng = np.random.default_rng(3)
+    for rows, e, k in SIZES:
+        for kind in ("normal", "masked"):
+            x = up(logits_of(kind, rows, e, rng).astype(np.float32)).to(TYPES[dtype])
+            ids, _ = run_select(x, k, score=score)
+            dw = up(rng.standard_normal((rows, k)).astype(np.float32))
+            d = torch.full(x.shape, float("nan"), dtype=x.dtype, device="cuda")
+            dcr.dcr_experts_select_grad(x, ids, dw, d, score=score, renormalize=renormalize, scale=1.5)
+            want, most = R.select_grad(f64(x), ids.cpu().numpy(), f64(dw), score == SIGMOID, renormalize, 1.5)
+            err = np.abs(f64(d) - want)
+            assert (err <= most * 2.0 ** -18 + np.abs(want) * HALF[dtype] + 2.0 ** -140).all(), (rows, e, k, kind, err.max())
+            if k == 1 and renormalize:
+                assert (d == 0).all()                  # a single weight is 1 whatever the logits are
+            dcr.dcr_experts_select_grad(x, ids, dw, x, score=score, renormalize=renormalize, scale=1.5)   # in place
+            assert torch.equal(x, d)
+
+
+def test_select_grad_against_differences():
+    """The reference's gradient is the limit of its weights' differences, in 64 bits: central differences at h = 1e-5 are
+    off by h^2 times third derivatives (below 2 here) and 2^-52 / h."""
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((3, 9))
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            ids, _ = R.select(x, None, 4, sigmoid)
+            dw = rng.standard_normal((3, 4))
+
+            def value(y):
+                s = np.take_along_axis(R.scores(y, sigmoid), ids.astype(np.int64), 1)
+                return (dw * (s / s.sum(1, keepdims=True) if renorm else s) * 0.7).sum()
+            want, _ = R.select_grad(x, ids, dw, sigmoid, renorm, 0.7)
+            for r in range(3):
+                for c in range(9):
+                    y, z = x.copy(), x.copy()
+                    y[r, c] += 1e-5
+                    z[r, c] -= 1e-5
+                    assert abs((value(y) - value(z)) / 2e-5 - want[r, c]) < 1e-9
+
+
+def test_select_grad_of_odd_ids():
+    """Ids out of range have no part, one that is there twice counts twice."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((4, 20)).astype(np.float32)
+    ids = np.array([[3, -1, 5, 20], [7, 7, 2, 2], [-5, 1 << 30, -(1 << 31), 19], [-1, -1, -1, -1]], np.int32)
+    dw = rng.standard_normal((4, 4)).astype(np.float32)
+    for renorm in (False, True):
+        for score in (SOFTMAX, SIGMOID):
+            d = torch.empty(4, 20, device="cuda")
+            dcr.dcr_experts_select_grad(up(x), up(ids), up(dw), d, score=score, renormalize=renorm)
+            want, most = R.select_grad(x, ids, dw, score == SIGMOID, renorm)
+            assert (np.abs(f64(d) - want) <= most * 2.0 ** -18 + np.abs(want) * 2.0 ** -24).all()
+            assert (d[3] == 0).all()
+
+
+# ------------------------------------------------------------------- order
+
+def run_order(ids, experts, slots=None):
+    offsets = torch.full((experts + 1,), 99, dtype=torch.int32, device="cuda")
+    slots = torch.full(ids.shape, 99, dtype=torch.int32, device="cuda") if slots is None else slots
+    dcr.dcr_experts_order(ids, offsets, slots, dcr.step_workspace())
+    return offsets, slots
+
+
+@pytest.mark.parametrize("n,experts", [(0, 4), (1, 1), (8, 128), (63, 3), (64, 64), (65, 1000), (2048, 7), (2049, 128), (4096, 256),
+                                       (12345, 60), (100003, 513), (131072, 128), (300001, 1024)])
+def test_order(n, experts):
+    rng = np.random.default_rng(n)
+    for kind in ("even", "skewed", "holes", "one"):
+        ids = rng.integers(0, experts, n)
+        if kind == "skewed":
+            ids = (experts * rng.random(n) ** 4).astype(np.int64)
+        elif kind == "holes":
+            bad = rng.random(n) < 0.3
+            ids[bad] = rng.choice([-1, -7, experts, 1 << 30, -(1 << 31)], bad.sum())
+        elif kind == "one":
+            ids[:] = experts - 1
+        ids = ids.astype(np.int32)
+        offsets, slots = run_order(up(ids), experts)
+        want_offsets, want = R.order(ids, experts)
+        assert np.array_equal(offsets.cpu().numpy(), want_offsets), kind
+        assert np.array_equal(slots.cpu().numpy(), want), kind
+        t = up(ids)
+        offsets, slots = run_order(t, experts, t)                    # in place
+        assert np.array_equal(offsets.cpu().numpy(), want_offsets) and np.array_equal(slots.cpu().numpy(), want), kind
+
+
+# -------------------------------------------------------------------- rows
+
+def some_slots(tokens, k, experts, rng, holes=0.1):
+    ids = np.argsort(rng.random((tokens, max(k, experts))), 1)[:, :k].astype(np.int32)
+    ids[rng.random((tokens, k)) < holes] = -1
+    ids[: tokens // 5] = -1                                          # padding
+    return R.order(ids, max(k, experts))[1]
+
+
+ROWS = [(1, 1, 1, 4), (3, 7, 2, 4), (5, 8, 1, 3), (24, 2048, 8, 128), (33, 100, 6, 16), (70, 768, 8, 60), (9, 4096, 4, 8),
+        (6, 8192, 12, 16), (130, 24, 3, 7), (11, 2055, 5, 9), (4, 16390, 64, 70)]
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp32"])
+@pytest.mark.parametrize("yt", ["bf16", "fp32"])
+def test_rows(xt, yt):
+    """Dispatched rows are copies (or one conversion); a combined value is k + 1 roundings of 2^-24 of the sum of magnitudes
+    off and rounded once; rows without a pair stay as they were."""
+    rng = np.random.default_rng(7)
+    for tokens, width, k, e in ROWS:
+        slots = some_slots(tokens, k, e, rng)
+        n = tokens * k + 3
+        for gap, shift in ((0, 0), (5, 1), (16, 8)):
+            x = up(rng.standard_normal((tokens, width + gap + shift)).astype(np.float32)).to(TYPES[xt])[:, shift: shift + width]
+            y = torch.full((n, width + gap), 3.0, dtype=TYPES[yt], device="cuda")
+            dcr.dcr_experts_dispatch(x, up(slots), y[:, :width])
+            want = torch.full_like(y, 3.0)
+            at, has = up(slots.reshape(-1)).long(), up(slots.reshape(-1) >= 0)
+            want[:, :width][at[has]] = x.repeat_interleave(k, 0)[has].to(y.dtype)
+            assert torch.equal(y, want), (tokens, width, gap)
+            w = up(rng.standard_normal((tokens, k)).astype(np.float32))
+            z = up(rng.standard_normal((n, width + gap + shift)).astype(np.float32)).to(TYPES[xt])[:, shift: shift + width]
+            for weights in (w, None):
+                out = torch.full((tokens, width + gap), 3.0, dtype=TYPES[yt], device="cuda")
+                dcr.dcr_experts_combine(z, up(slots), weights, out[:, :width])
+                zz = f64(z)[np.maximum(slots, 0)] * (slots >= 0)[..., None]
+                ww = np.ones((tokens, k)) if weights is None else f64(w)
+                exact, most = (zz * ww[..., None]).sum(1), (np.abs(zz) * np.abs(ww)[..., None]).sum(1)
+                err = np.abs(f64(out[:, :width]) - exact)
+                assert (err <= (k + 1) * 2.0 ** -24 * most + HALF[yt] * (np.abs(exact) + (k + 1) * 2.0 ** -24 * most)).all()
+                assert (out[:, width:] == 3).all()
+
+
+@pytest.mark.parametrize("dt,xt,gt", [("bf16", "bf16", "bf16"), ("fp32", "bf16", "bf16"), ("bf16", "fp32", "bf16"),
+                                      ("fp32", "fp32", "fp32"), ("bf16", "bf16", "fp32"), ("fp32", "bf16", "fp32"),
+                                      ("bf16", "fp32", "fp32"), ("fp32", "fp32", "bf16")])
+def test_combine_grad(dt, xt, gt):
+    """dx is one product, rounded to 32 bits and to its type; a lane of dw adds up an eighth of its eighths of a row at
+    most (width / 64 + 8 terms), 64 lanes by six more sums: (width / 64 + 16) 2^-24 of the sum of magnitudes."""
+    rng = np.random.default_rng(9)
+    for tokens, width, k, e in ROWS:
+        slots = some_slots(tokens, k, e, rng)
+        n = tokens * k + 2
+        for gap, shift in ((0, 0), (3, 1)):
+            def some(rows, t):
+                return up(rng.standard_normal((rows, width + gap + shift)).astype(np.float32)).to(TYPES[t])[:, shift: shift + width]
+            dy, x, w = some(tokens, dt), some(n, xt), up(rng.standard_normal((tokens, k)).astype(np.float32))
+            dx = torch.full((n, width + gap), 3.0, dtype=TYPES[gt], device="cuda")
+            dw = torch.full((tokens, k), float("nan"), device="cuda")
+            dcr.dcr_experts_combine_grad(dy, x, up(slots), w, dx[:, :width], dw)
+            want = np.full((n, width), 3.0)
+            has = slots >= 0
+            each = f64(w)[..., None] * f64(dy)[:, None, :]
+            want[slots[has]] = each[has]
+            got = f64(dx)
+            assert (np.abs(got[:, :width] - want) <= np.abs(want) * (HALF[gt] + 2.0 ** -23)).all()
+            untouched = np.ones(n, bool)
+            untouched[slots[has]] = False
+            assert (got[untouched] == 3).all() and (got[:, width:] == 3).all()
+            terms = f64(dy)[:, None, :] * f64(x)[np.maximum(slots, 0)] * has[..., None]
+            assert (np.abs(f64(dw) - terms.sum(2)) <= (width / 64 + 16) * 2.0 ** -24 * np.abs(terms).sum(2)).all()
+            assert (f64(dw)[~has] == 0).all()
+
+
+def test_rows_of_foreign_slots():
+    """Slots out of range are left out, one that is named twice gets one of its rows."""
+    x = torch.arange(1, 4, device="cuda", dtype=torch.float32)[:, None].expand(3, 40).contiguous()
+    slots = up(np.array([[0, 5], [-3, 1 << 30], [2, 2]], np.int32))
+    y = torch.zeros(5, 40, device="cuda")
+    dcr.dcr_experts_dispatch(x, slots, y)
+    assert torch.equal(y[:, 0].cpu(), torch.tensor([1., 0, 3, 0, 0])) and (y == y[:, :1]).all()
+    out = torch.full((3, 40), 9.0, device="cuda")
+    dcr.dcr_experts_combine(y, slots, torch.full((3, 2), 2.0, device="cuda"), out)
+    assert torch.equal(out[:, 0].cpu(), torch.tensor([2., 0, 12])) and (out == out[:, :1]).all()
+    dw, dx = torch.full((3, 2), 9.0, device="cuda"), torch.zeros(5, 40, device="cuda")
+    dcr.dcr_experts_combine_grad(x, y, slots, torch.full((3, 2), 2.0, device="cuda"), dx, dw)
+    assert torch.equal(dw.cpu(), torch.tensor([[40., 0], [0, 0], [360, 360]]))
+    empty = torch.zeros(0, 40, device="cuda")
+    dcr.dcr_experts_dispatch(x, slots, empty)
+    dcr.dcr_experts_combine(empty, slots, None, out)
+    assert (out == 0).all()
+    dcr.dcr_experts_combine_grad(x, empty, slots, torch.ones(3, 2, device="cuda"), empty, dw)
+    assert (dw == 0).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows that begin more than 2^32 elements into their matrix (strides, so that little memory is needed)."""
+    pool = torch.zeros((1 << 32) + (1 << 12), dtype=torch.bfloat16, device="cuda")
+    stride = 1 << 31
+    x = torch.as_strided(pool, (3, 64), (stride, 1))
+    x.copy_(torch.arange(1, 4, device="cuda")[:, None].expand(3, 64))
+    slots = up(np.array([[2, 0], [1, 2]], np.int32))
+    y = torch.empty(2, 64, device="cuda")
+    dcr.dcr_experts_combine(x, slots, None, y)
+    assert torch.equal(y[:, 0].cpu(), torch.tensor([4., 5.])) and (y == y[:, :1]).all()
+    dcr.dcr_experts_dispatch(y[:1] * 2, up(np.array([[2]], np.int32)), x)
+    assert (x[2] == 8).all() and (x[1] == 2).all()
+    ids, w = run_select(x, 3)
+    assert torch.equal(ids.cpu(), torch.tensor([[0, 1, 2]] * 3, dtype=torch.int32)) and (w == 1 / 64).all()

@@ -1,0 +1,238 @@
+"""Log probabilities and their gradient on the GPU against a plain 64-bit implementation."""
+import numpy as np
+import pytest
+import torch
+
+from bit_exact_xor_amd import dcr
+from tests import step_ref as R
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+INF = float("inf")
+
+
+def up(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def logits_of(kind, rows, vocab, dtype, rng, gap=0, shift=0):
+    x = rng.standard_normal((rows, vocab)) * 3
+    if kind == "peaked":
+        x[np.arange(rows), rng.integers(0, vocab, rows)] = 25
+    elif kind == "masked":
+        x[rng.random((rows, vocab)) < 0.5] = -np.inf
+        x[::3] = -np.inf
+        x[1::6, vocab // 2] = -2.0
+    elif kind == "lowest":
+        x[rng.random((rows, vocab)) < 0.5] = -3.3895e38
+        x[::3] = -3.3895e38
+    elif kind == "ties":
+        x = rng.integers(-1, 2, (rows, vocab)) * rng.choice([-1.0, 1.0], (rows, vocab))
+    elif kind == "rising":
+        x = np.sort(x, 1)
+    elif kind == "shifted":
+        x += 1000
+    t = torch.empty(rows, vocab + gap + shift, dtype=TYPES[dtype], device="cuda")[:, shift: shift + vocab]
+    return t.copy_(up(x.astype(np.float32)))
+
+
+KINDS = ["normal", "peaked", "masked", "lowest", "ties", "rising", "shifted"]
+SIZES = [(1, 1), (2, 3), (5, 64), (3, 1000), (2, 4096), (1, 4097), (9, 50257), (2, 151936), (520, 300), (513, 5001)]
+
+
+def order_of(x):
+    """Indices by value, the lowest of equals first."""
+    return np.lexsort((np.arange(x.shape[1])[None].repeat(len(x), 0), -(x + 0.0)), axis=1)
+
+
+def close(got, want, tol):
+    both = np.isneginf(want)
+    assert (np.isneginf(got) == both).all()
+    with np.errstate(invalid="ignore"):
+        err = np.abs(np.where(both, 0, got - np.where(both, 0, want)))
+    assert (err <= tol).all(), (err.max(), np.max(err - tol))
+
+
+def tolerances(x, scale):
+    """(of lse, of log p without its own difference, of the entropy).  An exponential 2^d takes a difference rounded
+    twice (2^-23 |d|, d up to 160 before it vanishes: but p |d| is below 0.54) and is 2^-23 off: 2^-21 of S in all.  A
+    thread adds at most vocab / 256 + 16 terms and its sums are rescaled as often as it takes 16 terms, then 20 joins:
+    (vocab / 256 + 40) 2^-24 of S and, with |T| / S for the entropy, of T.  log S below 2^5: 2^-20 with its own rounding."""
+    rows, vocab = x.shape
+    lp, lse, ent, p = R.logprobs(x, scale)
+    grow = (vocab / 256 + 40) * 2.0 ** -24 + 2.0 ** -21
+    with np.errstate(invalid="ignore"):
+        d = np.where(p > 0, (x - x.max(1, keepdims=True)) * scale, 0)
+    t = -(p * d).sum(1)
+    big = np.abs(np.where(np.isneginf(lse), 0, lse))
+    return grow + 2.0 ** -20 + 2.0 ** -23 * big, grow + 2.0 ** -20, 2 * grow * (1 + t) + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_logprobs(kind, dtype):
+    rng = np.random.default_rng(KINDS.index(kind))
+    ws = dcr.step_workspace()
+    ws.fill_(0xFF)
+    for n, (rows, vocab) in enumerate(SIZES):
+        gap, shift = ((0, 0), (5, 1), (8, 8))[n % 3]
+        scale = float(np.float32((1.0, 0.7, 1.0)[n % 3]))
+        logits = logits_of(kind, rows, vocab, dtype, rng, gap, shift)
+        x = f64(logits)
+        targets = rng.integers(0, vocab, rows)
+        targets[1::4] = -1
+        t = up(targets.astype(np.int64 if n % 2 else np.int32))
+        lp, lse, ent, p = R.logprobs(x, scale)
+        at_lse, at_lp, at_ent = tolerances(x, scale)
+        order = order_of(x)
+        for top in sorted({0, 1, min(5, vocab), min(20, vocab), min(64, vocab)}):
+            out = [torch.full((rows,), 77.0, device="cuda") for _ in range(3)]
+            ids = torch.full((rows, top), -5, dtype=torch.int32, device="cuda") if top else None
+            vals = torch.full((rows, top), 77.0, device="cuda") if top else None
+            dcr.dcr_logprobs(logits, t, *out, ids, vals, scale=scale, workspace=ws)
+            at = np.maximum(targets, 0)
+            mine = np.take_along_axis(lp, at[:, None], 1)[:, 0]
+            with np.errstate(invalid="ignore"):
+                far = 2.0 ** -22 * np.abs(np.nan_to_num((x[np.arange(rows), at] - x.max(1)) * scale, nan=0, posinf=0, neginf=0))
+            close(f64(out[0]), np.where(targets < 0, 0, mine), at_lp + far)
+            close(f64(out[1]), lse, at_lse)
+            close(f64(out[2]), ent, at_ent)
+            if top:
+                assert np.array_equal(ids.cpu().numpy(), order[:, :top]), (rows, vocab, top)
+                best = np.take_along_axis(lp, order[:, :top], 1)
+                with np.errstate(invalid="ignore"):
+                    d = np.nan_to_num((np.take_along_axis(x, order[:, :top], 1) - x.max(1, keepdims=True)) * scale, nan=0, neginf=0)
+                close(f64(vals), best, at_lp + 2.0 ** -22 * np.abs(d))
+
+
+def test_logprobs_of_odd_targets():
+    """None, the ends, past the vocabulary; outputs that are not asked for."""
+    x = torch.randn(6, 1003, device="cuda")
+    ws = dcr.step_workspace()
+    t = torch.tensor([-100, 0, 1002, 1003, 1 << 40, -(1 << 40)], device="cuda")
+    lp = torch.empty(6, device="cuda")
+    dcr.dcr_logprobs(x, t, lp, workspace=ws)
+    want = torch.log_softmax(x.double(), 1)
+    assert lp[0] == 0 and lp[5] == 0 and torch.isnan(lp[3:5]).all()
+    assert abs(float(lp[1] - want[1, 0])) < 1e-5 and abs(float(lp[2] - want[2, 1002])) < 1e-5
+    lse = torch.empty(6, device="cuda")
+    dcr.dcr_logprobs(x, None, lse=lse, workspace=ws)
+    assert torch.allclose(lse.double(), torch.logsumexp(x.double(), 1), atol=1e-5)
+    dcr.dcr_logprobs(x[:0], t[:0], lp[:0], workspace=ws)
+
+
+@pytest.mark.parametrize("rows", [3, 600])
+def test_nan_and_infinity_stay_in_their_row(rows):
+    x = torch.randn(rows, 5000, device="cuda")
+    x[1, 4321], x[2, 17] = float("nan"), INF
+    out = [torch.empty(rows, device="cuda") for _ in range(3)]
+    ids, vals = torch.empty(rows, 4, dtype=torch.int32, device="cuda"), torch.empty(rows, 4, device="cuda")
+    dcr.dcr_logprobs(x, torch.zeros(rows, dtype=torch.int32, device="cuda"), *out, ids, vals, workspace=dcr.step_workspace())
+    for v in (*out, vals[:, 0]):
+        assert torch.isnan(v[1:3]).all() and not torch.isnan(v[0]) and not torch.isnan(v[3:]).any()
+    assert ids[2, 0] == 17 and (ids[1] >= 0).all() and len(set(ids[1].tolist())) == 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["normal", "peaked", "masked", "ties"])
+def test_logprobs_grad(kind, dtype):
+    """With l = log p rounded once and multiplied (|l| 2^-22 in the exponent) and an exponential 2^-23 off, a term's factors
+    are off by (3 |l| + 8) 2^-23 of themselves; the one-hot term is one rounding; then the result's."""
+    rng = np.random.default_rng(11)
+    for n, (rows, vocab) in enumerate(SIZES):
+        gap, shift = ((0, 0), (5, 1), (8, 8))[n % 3]
+        scale = float(np.float32((1.0, 0.7, 1.3)[n % 3]))       # the call takes the scale in 32 bits
+        logits = logits_of(kind, rows, vocab, dtype, rng, gap, shift)
+        x = f64(logits)
+        targets = rng.integers(0, vocab, rows)
+        targets[2::4] = -1
+        t = up(targets.astype(np.int32 if n % 2 else np.int64))
+        _lp, lse, ent, _p = R.logprobs(x, scale)
+        lse, ent = up(lse.astype(np.float32)), up(ent.astype(np.float32))
+        dlogp, dent = up(rng.standard_normal(rows).astype(np.float32)), up(rng.standard_normal(rows).astype(np.float32))
+        for b in (None, dent):
+            d = torch.full((rows, vocab + 3), 9.0, dtype=TYPES[dtype], device="cuda")
+            dcr.dcr_logprobs_grad(logits, t, lse, dlogp, d[:, :vocab], entropy=ent if b is not None else None, dentropy=b,
+                                  scale=scale)
+            a = np.where(targets < 0, 0, f64(dlogp))[:, None]
+            be, h = (np.zeros((rows, 1)), 0) if b is None else (f64(b)[:, None], f64(ent)[:, None])
+            low = f64(lse)[:, None]
+            empty = np.isneginf(low)
+            with np.errstate(invalid="ignore"):
+                l = np.where(empty, -np.inf, x * scale - low)
+            p = np.exp(l)
+            ll = np.where(p > 0, l, 0)
+            hot = np.zeros_like(x)
+            hot[np.arange(rows), np.maximum(targets, 0)] = 1
+            want = scale * (a * (hot - p) - be * p * (ll + h)) * ~empty
+            most = scale * p * (np.abs(a) + np.abs(be) * (np.abs(ll) + np.abs(h)))
+            tol = most * (3 * np.abs(ll) + 8) * 2.0 ** -23 + 2.0 ** -23 * scale * hot * np.abs(a)
+            err = np.abs(f64(d[:, :vocab]) - want)
+            assert (err <= tol + HALF[dtype] * (np.abs(want) + tol) + 2.0 ** -126).all(), (rows, vocab, (err - tol).max())
+            assert (d[:, vocab:] == 9).all()
+        copy = logits.clone()
+        dcr.dcr_logprobs_grad(copy, t, lse, dlogp, copy, entropy=ent, dentropy=dent, scale=scale)     # in place
+        assert torch.equal(copy, d[:, :vocab])
+
+
+def test_grad_against_differences():
+    """logp and entropy as the calls give them, their derivative along a direction against central differences of the
+    64-bit reference (h = 1e-4: off by h^2 and 2^-52 / h; the gradient itself by 2^-20 of its terms)."""
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((4, 50)) * 2
+    t = np.array([3, -1, 49, 0])
+    a, b = rng.standard_normal(4), rng.standard_normal(4)
+    scale = float(np.float32(0.8))
+    logits = up(x.astype(np.float32))
+    x = f64(logits)
+    lse, ent = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    targets = up(t)
+    dcr.dcr_logprobs(logits, targets, None, lse, ent, scale=scale, workspace=dcr.step_workspace())
+    d = torch.empty_like(logits)
+    dcr.dcr_logprobs_grad(logits, targets, lse, up(a.astype(np.float32)), d, entropy=ent, dentropy=up(b.astype(np.float32)),
+                          scale=scale)
+
+    def value(y):
+        lp, _lse, h, _p = R.logprobs(y, scale)
+        return sum(a[r] * lp[r, t[r]] for r in range(4) if t[r] >= 0) + (b * h).sum()
+    for _ in range(20):
+        u = rng.standard_normal(x.shape)
+        got = (f64(d) * u).sum()
+        want = (value(x + 1e-4 * u) - value(x - 1e-4 * u)) / 2e-4
+        assert abs(got - want) < 2e-5 * max(1, np.abs(f64(d) * u).sum())
+
+
+def test_grad_of_odd_targets():
+    x = torch.randn(4, 100, device="cuda")
+    lse = torch.logsumexp(x, 1)
+    d = torch.empty_like(x)
+    one = torch.ones(4, device="cuda")
+    dcr.dcr_logprobs_grad(x, torch.tensor([-1, 100, 1 << 35, 5], device="cuda"), lse, one, d)
+    assert (d[0] == 0).all() and torch.isnan(d[1:3]).all() and not torch.isnan(d[3]).any()
+    lse[0], lse[3] = -INF, float("nan")
+    dcr.dcr_logprobs_grad(x, torch.tensor([7, 7, 7, 5], device="cuda"), lse, one, d)
+    assert (d[0] == 0).all() and torch.isnan(d[3]).all() and not torch.isnan(d[1:3]).any()
+
+
+def test_rows_past_32_bits():
+    """A row that begins more than 2^32 elements into its matrix."""
+    pool = torch.zeros((1 << 32) + (1 << 13), dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(pool, (3, 4100), (1 << 31, 1))
+    x[2, 4099] = 3.0
+    lp = torch.empty(3, device="cuda")
+    ids, vals = torch.empty(3, 2, dtype=torch.int32, device="cuda"), torch.empty(3, 2, device="cuda")
+    lse = torch.empty(3, device="cuda")
+    t = torch.tensor([5, 5, 4099], device="cuda")
+    dcr.dcr_logprobs(x, t, lp, lse, top_ids=ids, top_values=vals, workspace=dcr.step_workspace())
+    assert ids.tolist() == [[0, 1], [0, 1], [4099, 0]]
+    want = torch.log_softmax(x.double(), 1)
+    assert torch.allclose(lp.double(), want[torch.arange(3), t.cpu()], atol=1e-5)
+    one = torch.ones(3, device="cuda")
+    dcr.dcr_logprobs_grad(x, t, lse, one, x)
+    got = 1 - torch.exp(want[2, 4099])
+    assert abs(float(x[2, 4099]) - float(got)) < 2.0 ** -8 and float(x[2, 0]) < 0
