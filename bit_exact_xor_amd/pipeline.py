@@ -17,7 +17,9 @@ step of the method runs in libdcr's kernels.
 
 Fp4Refit is the same path for weights that the receiver serves in 4 bits:
 the trainer's BF16 or fp32 weights are quantised, the bytes that changed
-travel, and the receiver multiplies with the tensors the apply has patched.
+travel, and the receiver multiplies with the tensors the apply has patched:
+single weights, the experts of a layer, a head whose log probabilities are
+asked for.
 """
 import contextlib
 
@@ -325,14 +327,87 @@ class Fp4Refit:
         self.sent, self.next, self.version, self.interrupted = self.next, self.sent, self.version + 1, False
         self.products.clear()
 
+    def step(self, tensors, number, calibrate=False, **hyper):
+        """AdamW step `number` (see dcr_adamw_step) on the trainer's weights,
+        the parameters of `tensors` (a dcr.AdamWTensors, one for each shape),
+        and a refit with them; returns the payload bytes sent.  Where the refit
+        raises, the step has been taken: recover() finishes it."""
+        import torch
+        if [p.numel() for p in tensors.params] != [t.rows * t.cols for t in self.next]:
+            raise ValueError("step: one parameter of each weight's size expected")
+        self.recover()
+        with torch.cuda.device(self.device):
+            dcr.dcr_adamw_step(tensors, number, **hyper)
+        return self.refit([p.view(t.rows, t.cols) for p, t in zip(tensors.params, self.next)], calibrate)
+
+    def _ready(self, what):
+        if self.interrupted:
+            raise dcr.DcrError(dcr.DCR_E_VERSION, f"Fp4Refit.{what}", "the last refit was interrupted: recover() first")
+
+    def _scratch(self):
+        """Scratch memory of the current stream (also what the other calls need
+        between products), or of the graph that it is captured into."""
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            return dcr.fp4_workspace(self.device)
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if raw not in self.products:
+            self.products[raw] = (torch.cuda.current_stream(), dcr.fp4_workspace(self.device))
+        return self.products[raw][1]
+
+    def experts(self, up, down, x, logits, k, activation, out_dtype=None, bias=None, score=dcr.SCORE_SOFTMAX, groups=1,
+                top_groups=1, renormalize=True, scale=1.0):
+        """A layer of experts with the receiver's weights: for each row of x
+        (BF16), of the k experts that the router's `logits` choose (see
+        dcr_experts_select), the sum of weight * down(activation(up x)).
+        Weights `up` and `down` hold as many experts as the logits have columns
+        and as many columns as x and activation's result (BF16) have;
+        `activation` takes and gives rows, and is called with zeros in rows
+        that no pair has."""
+        import torch
+        self._ready("experts")
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.experts(up, down, x, logits, k, activation, out_dtype, bias, score, groups, top_groups, renormalize,
+                                    scale)
+        tokens, count = logits.shape
+        make = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        ids, weights = make(tokens, k), make(tokens, k, dtype=torch.float32)
+        offsets, slots = make(count + 1), make(tokens, k)
+        dcr.dcr_experts_select(logits, ids, weights, bias, score, groups, top_groups, renormalize, scale)
+        dcr.dcr_experts_order(ids, offsets, slots, self._scratch())
+        rows = make(tokens * k, x.shape[-1], dtype=torch.bfloat16)
+        dcr.dcr_experts_dispatch(x, slots, rows)
+        rows = self.matmul(down, activation(self.matmul(up, rows, offsets=offsets)), offsets=offsets)
+        y = make(tokens, rows.shape[1], dtype=out_dtype or x.dtype)
+        dcr.dcr_experts_combine(rows, slots, weights, y)
+        return y
+
+    def logprobs(self, i, x, targets, scale=1.0, top=0):
+        """(log probabilities of `targets`, entropy) of the rows of x (BF16)
+        through the receiver's weight i, a head with a row for each token of
+        the vocabulary, and with `top` the most probable tokens and their log
+        probabilities as well (see dcr_logprobs)."""
+        import torch
+        self._ready("logprobs")
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self.logprobs(i, x, targets, scale, top)
+        logits = self.matmul(i, x, torch.float32)
+        make = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        rows = x.shape[0]
+        logp, entropy = make(rows), make(rows)
+        best = (make(rows, top, dtype=torch.int32), make(rows, top)) if top else (None, None)
+        dcr.dcr_logprobs(logits, targets, logp, None, entropy, *best, scale=scale, workspace=self._scratch())
+        return (logp, entropy, *best) if top else (logp, entropy)
+
     def matmul(self, i, x, out_dtype=None, offsets=None, y=None):
         """x w^T with the receiver's weight i (see dcr_fp4_matmul), in a new
         tensor or in `y`.  With `offsets`, rows of x in front of the first
         group and behind the last give zeros, and leave those of `y` as they
         are."""
         import torch
-        if self.interrupted:
-            raise dcr.DcrError(dcr.DCR_E_VERSION, "Fp4Refit.matmul", "the last refit was interrupted: recover() first")
+        self._ready("matmul")
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 return self.matmul(i, x, out_dtype, offsets, y)
@@ -341,12 +416,5 @@ class Fp4Refit:
             _off, _g, n = dcr._groups(w, offsets)
             make = torch.empty if offsets is None else torch.zeros
             y = make(x.shape[0], n, dtype=out_dtype or x.dtype, device=x.device)
-        if torch.cuda.is_current_stream_capturing():
-            workspace = dcr.fp4_workspace(self.device)       # (of the graph's memory)
-        else:
-            raw = torch._C._cuda_getCurrentRawStream(self.device.index)
-            if raw not in self.products:
-                self.products[raw] = (torch.cuda.current_stream(), dcr.fp4_workspace(self.device))
-            workspace = self.products[raw][1]
-        dcr.dcr_fp4_matmul(x, w, y, offsets, workspace)
+        dcr.dcr_fp4_matmul(x, w, y, offsets, self._scratch())
         return y
