@@ -61,33 +61,79 @@ __device__ __forceinline__ float of_order(uint32_t u) {
 // a logit and its index as one number, no two alike; 0 stands for none
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t at) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - at); }
 
-__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
-    return (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32) |
-           uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), lane));
+// The best `top` keys that a workgroup has met, in order, in LDS.  Each round
+// the threads bring some more, at most `per` each.  Only keys above the last
+// one held come in question; where more than kDirect threads have such keys, a
+// bound is taken first: the top-th largest of the threads' best keys.  At most
+// `top` threads reach it, so what is gathered is bounded whatever the order of
+// the logits, and with logits in no order it is little more than `top`.  Ranks
+// are counted (no two keys are alike), so nothing depends on the order in which
+// threads arrive.
+constexpr uint32_t kDirect = 32, kMostPer = 16;
+struct TopLds {
+    uint64_t held[DCR_LOGPROBS_MAX_TOP];
+    uint64_t best[kLT];
+    uint64_t more[DCR_LOGPROBS_MAX_TOP * kMostPer + DCR_LOGPROBS_MAX_TOP];
+    uint64_t bound;
+    uint32_t n;
+};
+static_assert(kDirect <= DCR_LOGPROBS_MAX_TOP, "room for what few threads bring");
+
+// how many of the n keys at `keys` (LDS) are larger
+__device__ __forceinline__ uint32_t larger(const uint64_t* keys, uint32_t n, uint64_t key) {
+    uint32_t r = 0;
+#pragma unroll 8
+    for (uint32_t j = 0; j < n; ++j) r += keys[j] > key ? 1u : 0u;
+    return r;
 }
 
-// A wave's best keys, one a lane, the largest in lane 0.
-struct TopList {
-    uint64_t mine, least;                    // least: the key of lane top - 1, which a new one has to pass
-    __device__ __forceinline__ void insert(uint64_t key, uint32_t top) {
-        const int at = __popcll(__ballot(mine > key));
-        const uint64_t above = uint64_t(__shfl_up((unsigned long long)mine, 1, 64));
-        const int lane = int(threadIdx.x & 63u);
-        mine = lane < at ? mine : lane == at ? key : above;
-        least = lane_value(mine, int(top) - 1);
-    }
-};
+__device__ __forceinline__ void top_begin(TopLds& l) {
+    if (threadIdx.x < DCR_LOGPROBS_MAX_TOP) l.held[threadIdx.x] = 0;
+    if (threadIdx.x == 0) l.n = 0;
+    __syncthreads();
+}
 
-// the keys of a workgroup's waves (LDS, n of them, none twice) in order: the best `top` to `put(rank, key)`
-template <typename F>
-__device__ __forceinline__ void rank_keys(const uint64_t* keys, uint32_t n, uint32_t top, F&& put) {
-    for (uint32_t i = threadIdx.x; i < n; i += kLT) {
-        const uint64_t k = keys[i];
-        if (!k) continue;
-        uint32_t r = 0;
-        for (uint32_t j = 0; j < n; ++j) r += keys[j] > k ? 1u : 0u;
-        if (r < top) put(r, k);
+// A round, of all threads: `passes` tells (it may be too often true) whether
+// one of the thread's keys is above `least`, `best` gives its largest key, `each`
+// calls a function with every key.  Returns the last key held.
+template <typename B, typename E>
+__device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t least, bool passes, B&& best, E&& each) {
+    const uint32_t some = uint32_t(__syncthreads_count(passes));
+    if (!some) return least;
+    uint64_t from = least;
+    if (some > kDirect && top < kLT) {
+        const uint64_t mine = best();
+        l.best[threadIdx.x] = mine;
+        if (threadIdx.x == 0) l.bound = 0;
+        __syncthreads();
+        if (mine && larger(l.best, kLT, mine) == top - 1) l.bound = mine - 1;
+        __syncthreads();
+        from = max(from, l.bound);
     }
+    if (passes) {
+        each([&](uint64_t k) {
+            if (k > from) l.more[atomicAdd(&l.n, 1u)] = k;
+        });
+    }
+    __syncthreads();
+    // (held keys first: there is room behind them for all that came)
+    const uint32_t n = l.n;
+    uint64_t mine[(DCR_LOGPROBS_MAX_TOP * (kMostPer + 1) + kLT - 1) / kLT];
+    uint32_t at[sizeof(mine) / sizeof(mine[0])];
+#pragma unroll
+    for (uint32_t u = 0; u < sizeof(mine) / sizeof(mine[0]); ++u) {
+        const uint32_t i = u * kLT + threadIdx.x;
+        mine[u] = i < n ? l.more[i] : i - n < top ? l.held[i - n] : 0;
+        at[u] = top;
+        if (u * kLT < n + top && mine[u]) at[u] = larger(l.more, n, mine[u]) + larger(l.held, top, mine[u]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t u = 0; u < sizeof(mine) / sizeof(mine[0]); ++u)
+        if (at[u] < top) l.held[at[u]] = mine[u];
+    if (threadIdx.x == 0) l.n = 0;
+    __syncthreads();
+    return l.held[top - 1];
 }
 
 __device__ __forceinline__ int64_t target_of(const LpArgs& a, uint32_t row) {
@@ -125,10 +171,25 @@ __device__ __forceinline__ void put_top(const LpArgs& a, uint32_t row, uint32_t 
     a.top_values[to] = of.logp(of_order(uint32_t(key >> 32)), a.scale);
 }
 
+// a thread's logits of a step: twice eight, 8 kLT apart, so that a wave reads
+// whole lines
+template <typename T>
+__device__ __forceinline__ void load_step(const T* x, uint32_t c0, uint32_t to, Raw8<T>* raw) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t at = c0 + (h * kLT + threadIdx.x) * 8;
+        const int n = at < to ? int(min(8u, to - at)) : 0;
+        if (n == 8)
+            raw[h].load(x + at);
+        else
+            raw[h].load_some(x + at, n, kBf16MinusInf);
+    }
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
     __shared__ Sums of_wave[kLWaves];
-    __shared__ uint64_t keys[TOP ? kLT : 1], sorted[TOP ? DCR_LOGPROBS_MAX_TOP : 1];
+    __shared__ std::conditional_t<TOP, TopLds, uint32_t> lds;
     __shared__ RowOf row_of;
     const uint32_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
@@ -136,22 +197,15 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
     const float unit = a.scale * kLog2e;
     Sums sum = {-INFINITY, 0.0f, 0.0f};
-    TopList best = {0, 0};
-    // wave by wave through the part: 64 lanes of two times eight logits
-    for (uint32_t c0 = from + wave * 64 * kPiece; c0 < to; c0 += kLT * kPiece) {
+    uint64_t least = 0;
+    if constexpr (TOP) top_begin(lds);
+    Raw8<T> raw[2];
+    load_step(x, from, to, raw);
+    for (uint32_t c0 = from; c0 < to; c0 += kLT * kPiece) {
         float v[kPiece];
-        uint32_t at[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            at[h] = c0 + (h * 64 + lane) * 8;
-            Raw8<T> raw;
-            const int n = at[h] < to ? int(min(8u, to - at[h])) : 0;
-            if (n == 8)
-                raw.load(x + at[h]);
-            else
-                raw.load_some(x + at[h], n, kBf16MinusInf);
-            raw.get(v + 8 * h);
-        }
+        raw[0].get(v);
+        raw[1].get(v + 8);
+        if (c0 + kLT * kPiece < to) load_step(x, c0 + kLT * kPiece, to, raw);
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < int(kPiece); ++i) top = fmaxf(top, v[i]);
@@ -168,37 +222,31 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
         sum.t = __fmaf_rn(f, __fmaf_rn(sum.s, d, sum.t), t);
         sum.s = __fmaf_rn(sum.s, f, s);
         sum.m = m;
-        if (TOP) {
-            // each lane's best key that the wave's list does not hold yet, until none passes the least
-            uint64_t below = ~uint64_t(0);
-            const uint32_t bound = order_of(top);
-            while (true) {
-                uint64_t cand = 0;
-                if (bound >= uint32_t(best.least >> 32) || best.least == 0) {
+        if constexpr (TOP) {
+            const auto key = [&](int i) {
+                const uint32_t j = c0 + ((i / 8) * kLT + threadIdx.x) * 8 + i % 8;
+                return j < to ? key_of(v[i], j) : 0;
+            };
+            // (without `top` keys every thread with logits comes in question, NaN too)
+            const bool passes = least == 0 ? c0 + threadIdx.x * 8 < to : order_of(top) >= uint32_t(least >> 32);
+            least = top_round(
+                lds, a.top, least, passes,
+                [&] {
+                    uint64_t b = 0;
 #pragma unroll
-                    for (int i = 0; i < int(kPiece); ++i) {
-                        const uint32_t j = at[i / 8] + i % 8;
-                        const uint64_t k = j < to ? key_of(v[i], j) : 0;
-                        cand = k < below && k > cand ? k : cand;
-                    }
-                }
-                uint64_t who = __ballot(cand > best.least);
-                if (!who) break;
-                while (who) {
-                    const int l = __ffsll((unsigned long long)who) - 1;
-                    who &= who - 1;
-                    const uint64_t k = lane_value(cand, l);
-                    if (k > best.least) best.insert(k, a.top);
-                }
-                below = cand;
-            }
+                    for (int i = 0; i < int(kPiece); ++i) b = max(b, key(i));
+                    return b;
+                },
+                [&](auto&& put) {
+#pragma unroll
+                    for (int i = 0; i < int(kPiece); ++i) put(key(i));
+                });
         }
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1)
         sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
     if (lane == 0) of_wave[wave] = sum;
-    if (TOP) keys[threadIdx.x] = lane < a.top ? best.mine : 0;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (uint32_t w = 1; w < kLWaves; ++w) sum = join(sum, of_wave[w], unit);
@@ -207,26 +255,35 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
         else
             a.sums[blockIdx.x] = f32x4{sum.m, sum.s, sum.t, 0.0f};
     }
-    if (!TOP) return;
-    __syncthreads();
-    if (a.parts == 1) {
-        rank_keys(keys, kLT, a.top, [&](uint32_t r, uint64_t k) { put_top(a, row, r, k, row_of); });
-    } else {
-        if (threadIdx.x < a.top) sorted[threadIdx.x] = 0;
+    if constexpr (TOP) {
         __syncthreads();
-        rank_keys(keys, kLT, a.top, [&](uint32_t r, uint64_t k) { sorted[r] = k; });
-        __syncthreads();
-        if (threadIdx.x < a.top) a.keys[uint64_t(blockIdx.x) * a.top + threadIdx.x] = sorted[threadIdx.x];
+        if (threadIdx.x < a.top) {
+            if (a.parts == 1)
+                put_top(a, row, threadIdx.x, lds.held[threadIdx.x], row_of);
+            else
+                a.keys[uint64_t(blockIdx.x) * a.top + threadIdx.x] = lds.held[threadIdx.x];
+        }
     }
 }
 
 // the parts of a row; a workgroup a row
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
-    __shared__ uint64_t keys[TOP ? kMostParts : 1];
+    __shared__ std::conditional_t<TOP, TopLds, uint32_t> lds;
     __shared__ RowOf row_of;
     const uint32_t row = blockIdx.x;
     const float unit = a.scale * kLog2e;
+    const uint32_t n = a.parts * a.top;
+    constexpr uint32_t MOST = kMostParts / kLT;
+    uint64_t keys[TOP ? MOST : 1];
+    if constexpr (TOP) {
+#pragma unroll
+        for (uint32_t u = 0; u < MOST; ++u) {
+            const uint32_t i = u * kLT + threadIdx.x;
+            keys[u] = i < n ? a.keys[uint64_t(row) * n + i] : 0;
+        }
+        top_begin(lds);
+    }
     if (threadIdx.x < 64) {
         Sums sum = {-INFINITY, 0.0f, 0.0f};
         for (uint32_t p = threadIdx.x; p < a.parts; p += 64) {
@@ -238,11 +295,21 @@ __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
             sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
         if (threadIdx.x == 0) row_of = finish_row<T>(a, row, sum);
     }
-    if (!TOP) return;
-    const uint32_t n = a.parts * a.top;
-    for (uint32_t i = threadIdx.x; i < n; i += kLT) keys[i] = a.keys[uint64_t(row) * n + i];
-    __syncthreads();
-    rank_keys(keys, n, a.top, [&](uint32_t r, uint64_t k) { put_top(a, row, r, k, row_of); });
+    if constexpr (TOP) {
+        top_round(
+            lds, a.top, 0, true,
+            [&] {
+                uint64_t b = 0;
+#pragma unroll
+                for (uint32_t u = 0; u < MOST; ++u) b = max(b, keys[u]);
+                return b;
+            },
+            [&](auto&& put) {
+#pragma unroll
+                for (uint32_t u = 0; u < MOST; ++u) put(keys[u]);
+            });
+        if (threadIdx.x < a.top) put_top(a, row, threadIdx.x, lds.held[threadIdx.x], row_of);
+    }
 }
 
 struct LpGradArgs {

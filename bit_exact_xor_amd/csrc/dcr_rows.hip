@@ -13,6 +13,7 @@ namespace dcr {
 namespace {
 
 constexpr uint32_t kRT = 256;              // threads of a workgroup
+constexpr uint32_t kRows = 4;              // rows that a thread has on their way
 
 struct RowArgs {
     const void* a;         // dispatch, combine: x; gradient: dy
@@ -60,17 +61,28 @@ __global__ void __launch_bounds__(kRT) rows_combine_kernel(RowArgs a) {
     for (uint32_t c = (threadIdx.x & ((1u << a.lanes_log2) - 1)) * 8; c < a.width; c += step) {
         const int n = int(min(8u, a.width - c));
         float sum[8] = {};
-        for (uint32_t j = 0; j < a.k; ++j) {
-            const uint32_t s = uint32_t(slots[j]);
-            if (s >= a.n_slots) continue;
-            const float w = a.weights ? weights[j] : 1.0f;
-            const TX* x = static_cast<const TX*>(a.a) + uint64_t(s) * a.a_stride + c;
-            Raw8<TX> r;
-            float v[8];
-            n == 8 ? r.load(x) : r.load_some(x, n, 0);
-            r.get(v);
+        // four rows on their way together
+        for (uint32_t j0 = 0; j0 < a.k; j0 += kRows) {
+            Raw8<TX> r[kRows];
+            float w[kRows];
+            bool has[kRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(w, v[i], sum[i]);
+            for (uint32_t u = 0; u < kRows; ++u) {
+                const uint32_t s = j0 + u < a.k ? uint32_t(slots[j0 + u]) : ~0u;
+                has[u] = s < a.n_slots;
+                if (!has[u]) continue;
+                w[u] = a.weights ? weights[j0 + u] : 1.0f;
+                const TX* x = static_cast<const TX*>(a.a) + uint64_t(s) * a.a_stride + c;
+                n == 8 ? r[u].load(x) : r[u].load_some(x, n, 0);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kRows; ++u) {
+                if (!has[u]) continue;
+                float v[8];
+                r[u].get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(w[u], v[i], sum[i]);
+            }
         }
         n == 8 ? store8(y + c, sum) : store_some(y + c, sum, n);
     }

@@ -128,11 +128,52 @@ __device__ __forceinline__ void store_some(T* p, const float* v, int n) {
         if (i < n) narrow(v[i], p + i);
 }
 
+// What f makes of the values of LANES neighbouring lanes, in all of them; f
+// commutes.  Registers only: permutations inside rows of 16 lanes, then swaps of
+// rows and of halves (through LDS a step takes some 100 cycles, here about 8).
+template <int STEP>
+__device__ __forceinline__ void partners(uint32_t v, uint32_t* a, uint32_t* b) {
+    if constexpr (STEP == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        *a = p[0], *b = p[1];
+    } else if constexpr (STEP == 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        *a = p[0], *b = p[1];
+    } else {
+        // neighbour; pair of a quad; the other quad of eight, the other eight (mirrored: within them all are alike by now)
+        constexpr int CTRL = STEP == 1 ? 0xB1 : STEP == 2 ? 0x4E : STEP == 4 ? 0x141 : 0x140;
+        *a = v, *b = uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xF, 0xF, true));
+    }
+}
+template <int STEP, typename T>
+__device__ __forceinline__ void partners_of(T v, T* a, T* b) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t x, y;
+        partners<STEP>(__builtin_bit_cast(uint32_t, v), &x, &y);
+        *a = __builtin_bit_cast(T, x), *b = __builtin_bit_cast(T, y);
+    } else {
+        const u32x2 q = __builtin_bit_cast(u32x2, v);
+        u32x2 x, y;
+        uint32_t lo[2], hi[2];
+        partners<STEP>(q[0], &lo[0], &lo[1]);
+        partners<STEP>(q[1], &hi[0], &hi[1]);
+        x = u32x2{lo[0], hi[0]}, y = u32x2{lo[1], hi[1]};
+        *a = __builtin_bit_cast(T, x), *b = __builtin_bit_cast(T, y);
+    }
+}
+template <int LANES, int STEP = 1, typename T, typename F>
+__device__ __forceinline__ T lanes_all(T v, F&& f) {
+    if constexpr (STEP < LANES) {
+        T a, b;
+        partners_of<STEP>(v, &a, &b);
+        return lanes_all<LANES, 2 * STEP>(f(a, b), f);
+    } else {
+        return v;
+    }
+}
 template <int LANES, typename T>
 __device__ __forceinline__ T lanes_sum(T v) {
-#pragma unroll
-    for (int d = LANES / 2; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    return lanes_all<LANES>(v, [](T a, T b) { return a + b; });
 }
 
 }  // namespace dcr
