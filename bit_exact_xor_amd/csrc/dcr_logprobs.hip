@@ -20,7 +20,8 @@ namespace {
 constexpr uint32_t kLT = 256;                // threads of a workgroup
 constexpr uint32_t kLWaves = kLT / 64;
 constexpr uint32_t kPiece = 16;              // logits of a thread in a step
-constexpr uint32_t kMostParts = 2048;        // parts of all rows, where rows are split
+constexpr uint32_t kMostParts = 1 << 13;     // parts of all rows, where rows are split
+constexpr uint32_t kMostKeys = 2048;         // keys of the parts of a row
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct LpArgs {
@@ -62,52 +63,68 @@ __device__ __forceinline__ float of_order(uint32_t u) {
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t at) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - at); }
 
 // The best `top` keys that a workgroup has met, in order, in LDS.  Each round
-// the threads bring some more, at most `per` each.  Only keys above the last
+// the threads bring some more, at most kMostPer each.  Only keys above the last
 // one held come in question; where more than kDirect threads have such keys, a
-// bound is taken first: the top-th largest of the threads' best keys.  At most
-// `top` threads reach it, so what is gathered is bounded whatever the order of
-// the logits, and with logits in no order it is little more than `top`.  Ranks
-// are counted (no two keys are alike), so nothing depends on the order in which
-// threads arrive.
-constexpr uint32_t kDirect = 32, kMostPer = 16;
+// bound is taken first: the top-th largest of the best keys of 64 quads of
+// threads (128 pairs, 256 threads where `top` is larger).  Only `top` of them
+// reach it, so what is gathered is bounded whatever the order of the logits, and
+// with logits in no order it is little more than `top`.  Ranks are counted (no
+// two keys are alike), so nothing depends on the order in which threads arrive.
+constexpr uint32_t kDirect = 32, kMostPer = 16, kQuads = 20, kPairs = 32;
+constexpr uint32_t kGathered = kQuads * 4 * kMostPer;
+static_assert(kGathered >= kPairs * 2 * kMostPer && kGathered >= DCR_LOGPROBS_MAX_TOP * kMostPer && kGathered >= kDirect * kMostPer,
+              "room for what may pass the bound");
 struct TopLds {
     uint64_t held[DCR_LOGPROBS_MAX_TOP];
     uint64_t best[kLT];
-    uint64_t more[DCR_LOGPROBS_MAX_TOP * kMostPer + DCR_LOGPROBS_MAX_TOP];
+    uint64_t more[kGathered];
     uint64_t bound;
     uint32_t n;
 };
-static_assert(kDirect <= DCR_LOGPROBS_MAX_TOP, "room for what few threads bring");
 
-// how many of the n keys at `keys` (LDS) are larger
-__device__ __forceinline__ uint32_t larger(const uint64_t* keys, uint32_t n, uint64_t key) {
+// how many of the keys first, first + step, ... of n at `keys` (LDS) are larger
+__device__ __forceinline__ uint32_t larger(const uint64_t* keys, uint32_t first, uint32_t n, uint32_t step, uint64_t key) {
     uint32_t r = 0;
 #pragma unroll 8
-    for (uint32_t j = 0; j < n; ++j) r += keys[j] > key ? 1u : 0u;
+    for (uint32_t j = first; j < n; j += step) r += keys[j] > key ? 1u : 0u;
     return r;
 }
 
 __device__ __forceinline__ void top_begin(TopLds& l) {
-    if (threadIdx.x < DCR_LOGPROBS_MAX_TOP) l.held[threadIdx.x] = 0;
     if (threadIdx.x == 0) l.n = 0;
+    __syncthreads();
+}
+
+// LANES threads share a key in the search for the bound
+template <uint32_t LANES>
+__device__ __forceinline__ void find_bound(TopLds& l, uint32_t top, uint64_t best) {
+    const uint64_t mine = lanes_all<LANES>(best, [](uint64_t a, uint64_t b) { return max(a, b); });
+    const uint32_t sub = threadIdx.x % LANES;
+    if (sub == 0) l.best[threadIdx.x / LANES] = mine;
+    if (threadIdx.x == 0) l.bound = 0;
+    __syncthreads();
+    const uint32_t above = lanes_sum<LANES>(larger(l.best, sub, kLT / LANES, LANES, mine));
+    if (sub == 0 && mine && above == top - 1) l.bound = mine - 1;
     __syncthreads();
 }
 
 // A round, of all threads: `passes` tells (it may be too often true) whether
 // one of the thread's keys is above `least`, `best` gives its largest key, `each`
-// calls a function with every key.  Returns the last key held.
+// calls a function with every key.  Returns the last key held, 0 (nothing is)
+// before the first round.
 template <typename B, typename E>
-__device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t least, bool passes, B&& best, E&& each) {
+__device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t least, bool first, bool passes, B&& best, E&& each) {
     const uint32_t some = uint32_t(__syncthreads_count(passes));
-    if (!some) return least;
+    if (!some && !first) return least;
     uint64_t from = least;
-    if (some > kDirect && top < kLT) {
+    if (some > kDirect) {
         const uint64_t mine = best();
-        l.best[threadIdx.x] = mine;
-        if (threadIdx.x == 0) l.bound = 0;
-        __syncthreads();
-        if (mine && larger(l.best, kLT, mine) == top - 1) l.bound = mine - 1;
-        __syncthreads();
+        if (top <= kQuads)
+            find_bound<4>(l, top, mine);
+        else if (top <= kPairs)
+            find_bound<2>(l, top, mine);
+        else
+            find_bound<1>(l, top, mine);
         from = max(from, l.bound);
     }
     if (passes) {
@@ -116,24 +133,33 @@ __device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t 
         });
     }
     __syncthreads();
-    // (held keys first: there is room behind them for all that came)
-    const uint32_t n = l.n;
-    uint64_t mine[(DCR_LOGPROBS_MAX_TOP * (kMostPer + 1) + kLT - 1) / kLT];
-    uint32_t at[sizeof(mine) / sizeof(mine[0])];
+    const uint32_t n = l.n, held = first ? 0 : top;
+    constexpr uint32_t U = (kGathered + DCR_LOGPROBS_MAX_TOP + kLT - 1) / kLT;
+    uint64_t mine[U];
+    uint32_t at[U];
 #pragma unroll
-    for (uint32_t u = 0; u < sizeof(mine) / sizeof(mine[0]); ++u) {
+    for (uint32_t u = 0; u < U; ++u) {
+        mine[u] = 0, at[u] = top;
+        if (u * kLT >= n + held) continue;
         const uint32_t i = u * kLT + threadIdx.x;
-        mine[u] = i < n ? l.more[i] : i - n < top ? l.held[i - n] : 0;
-        at[u] = top;
-        if (u * kLT < n + top && mine[u]) at[u] = larger(l.more, n, mine[u]) + larger(l.held, top, mine[u]);
+        mine[u] = i < n ? l.more[i] : i - n < held ? l.held[i - n] : 0;
+        if (mine[u]) at[u] = larger(l.more, 0, n, 1, mine[u]) + larger(l.held, 0, held, 1, mine[u]);
     }
     __syncthreads();
-#pragma unroll
-    for (uint32_t u = 0; u < sizeof(mine) / sizeof(mine[0]); ++u)
-        if (at[u] < top) l.held[at[u]] = mine[u];
+    if (threadIdx.x < top && threadIdx.x >= n + held) l.held[threadIdx.x] = 0;      // (fewer keys than `top` so far)
     if (threadIdx.x == 0) l.n = 0;
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u)
+        if (at[u] < top) l.held[at[u]] = mine[u];
     __syncthreads();
     return l.held[top - 1];
+}
+
+// The sums of the lanes of a wave: the largest first, then each lane's by it.
+__device__ __forceinline__ Sums join_wave(Sums a, float unit) {
+    const float m = lanes_all<64>(a.m, [](float x, float y) { return fmaxf(x, y); });
+    const float d = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * unit, -160.0f), f = exp2f(d);
+    return {m, lanes_sum<64>(a.s * f), lanes_sum<64>(f * __fmaf_rn(a.s, d, a.t))};
 }
 
 __device__ __forceinline__ int64_t target_of(const LpArgs& a, uint32_t row) {
@@ -180,7 +206,7 @@ __device__ __forceinline__ void load_step(const T* x, uint32_t c0, uint32_t to, 
         const uint32_t at = c0 + (h * kLT + threadIdx.x) * 8;
         const int n = at < to ? int(min(8u, to - at)) : 0;
         if (n == 8)
-            raw[h].load(x + at);
+            raw[h].load_once(x + at);
         else
             raw[h].load_some(x + at, n, kBf16MinusInf);
     }
@@ -198,9 +224,9 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
     const float unit = a.scale * kLog2e;
     Sums sum = {-INFINITY, 0.0f, 0.0f};
     uint64_t least = 0;
-    if constexpr (TOP) top_begin(lds);
     Raw8<T> raw[2];
     load_step(x, from, to, raw);
+    if constexpr (TOP) top_begin(lds);
     for (uint32_t c0 = from; c0 < to; c0 += kLT * kPiece) {
         float v[kPiece];
         raw[0].get(v);
@@ -230,7 +256,7 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
             // (without `top` keys every thread with logits comes in question, NaN too)
             const bool passes = least == 0 ? c0 + threadIdx.x * 8 < to : order_of(top) >= uint32_t(least >> 32);
             least = top_round(
-                lds, a.top, least, passes,
+                lds, a.top, least, c0 == from, passes,
                 [&] {
                     uint64_t b = 0;
 #pragma unroll
@@ -243,9 +269,7 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
                 });
         }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
+    sum = join_wave(sum, unit);
     if (lane == 0) of_wave[wave] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -274,7 +298,7 @@ __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
     const uint32_t row = blockIdx.x;
     const float unit = a.scale * kLog2e;
     const uint32_t n = a.parts * a.top;
-    constexpr uint32_t MOST = kMostParts / kLT;
+    constexpr uint32_t MOST = kMostKeys / kLT;
     uint64_t keys[TOP ? MOST : 1];
     if constexpr (TOP) {
 #pragma unroll
@@ -290,14 +314,12 @@ __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
             const f32x4 q = a.sums[uint64_t(row) * a.parts + p];
             sum = join(sum, Sums{q[0], q[1], q[2]}, unit);
         }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            sum = join(sum, Sums{__shfl_xor(sum.m, d, 64), __shfl_xor(sum.s, d, 64), __shfl_xor(sum.t, d, 64)}, unit);
+        sum = join_wave(sum, unit);
         if (threadIdx.x == 0) row_of = finish_row<T>(a, row, sum);
     }
     if constexpr (TOP) {
         top_round(
-            lds, a.top, 0, true,
+            lds, a.top, 0, true, true,
             [&] {
                 uint64_t b = 0;
 #pragma unroll
@@ -345,7 +367,7 @@ __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
     for (uint32_t u = 0; u < kGU; ++u) {
         at[u] = ((piece * kGU + u) * kLT + threadIdx.x) * 8;
         n[u] = at[u] < a.vocab ? int(min(8u, a.vocab - at[u])) : 0;
-        n[u] == 8 ? raw[u].load(x + at[u]) : raw[u].load_some(x + at[u], n[u], kBf16MinusInf);
+        n[u] == 8 ? raw[u].load_once(x + at[u]) : raw[u].load_some(x + at[u], n[u], kBf16MinusInf);
     }
 #pragma unroll
     for (uint32_t u = 0; u < kGU; ++u) {
@@ -365,7 +387,7 @@ __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
             for (int i = 0; i < 8; ++i)
                 if (i == int(hot)) v[i] = __fmaf_rn(up, a.scale, v[i]);
         }
-        n[u] == 8 ? store8(y + at[u], v) : store_some(y + at[u], v, n[u]);
+        n[u] == 8 ? store8<true>(y + at[u], v) : store_some(y + at[u], v, n[u]);
     }
 }
 
@@ -397,9 +419,14 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
     a.logits = logits, a.targets = targets, a.logp = logp, a.lse = lse, a.entropy = entropy;
     a.top_values = top_values, a.top_ids = top_ids, a.stride = rows > 1 ? stride : 0;
     a.rows = uint32_t(rows), a.vocab = uint32_t(vocab), a.top = top, a.wide_ids = targets_bytes == 8, a.scale = scale;
-    // parts so that about 1024 workgroups run, none shorter than a step
-    uint64_t parts = rows >= 512 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>(1024 / rows, (vocab + kLT * kPiece - 1) / (kLT * kPiece)));
-    if (top) parts = std::min<uint64_t>(parts, kMostParts / top);
+    // Parts so that at least 1024 workgroups run, none shorter than a step (8 x
+    // 151936: 6.5 us in 38 parts, 8.2 in 10; 256 rows 21.1 us, in 512 workgroups
+    // 24.2).  Between one and two times the 2048 that run at once a second part
+    // fills the last round (2500 rows 124 us, whole 139; with `top`, which a part
+    // costs more than that, 187 whole and 209).
+    const uint64_t target = rows > 2048 && rows < 4096 && !top ? 4096 : 1024, step = kLT * kPiece;
+    uint64_t parts = std::max<uint64_t>(1, std::min<uint64_t>((target + rows - 1) / rows, (vocab + step - 1) / step));
+    if (top) parts = std::min<uint64_t>(parts, kMostKeys / top);
     uint64_t len = ((vocab + parts - 1) / parts + 7) / 8 * 8;
     parts = (vocab + len - 1) / len;
     a.parts = uint32_t(parts), a.part_len = uint32_t(len);

@@ -506,7 +506,7 @@ def _fp4_call(torch, fn, what, device, stream, *args):
     `stream` or that GPU's current stream."""
     # (torch.cuda.current_stream() costs as much as the rest of a small call)
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -751,8 +751,9 @@ def dcr_logprobs(logits, targets, logp=None, lse=None, entropy=None, top_ids=Non
     top = 0 if top_ids is None else top_ids.shape[-1]
     if (top_ids is None) != (top_values is None):
         raise ValueError("top_ids and top_values go together")
-    a, b, c = (_array(v, torch.float32, (rows,), n) for v, n in ((logp, "logp"), (lse, "lse"), (entropy, "entropy")))
-    i, v = _array(top_ids, torch.int32, (rows, top), "top_ids"), _array(top_values, torch.float32, (rows, top), "top_values")
+    f32, shape = torch.float32, (rows,)
+    a, b, c = _array(logp, f32, shape, "logp"), _array(lse, f32, shape, "lse"), _array(entropy, f32, shape, "entropy")
+    i, v = _array(top_ids, torch.int32, (rows, top), "top_ids"), _array(top_values, f32, (rows, top), "top_values")
     _step_space(workspace)
     dev = _one_device(logits, targets, logp, lse, entropy, top_ids, top_values, workspace)
     _fp4_call(torch, load_library().dcr_logprobs, "dcr_logprobs", dev, stream, p, ty, stride, rows, vocab, t, tb, scale, a, b,
@@ -772,8 +773,9 @@ def dcr_logprobs_grad(logits, targets, lse, dlogp, dlogits, entropy=None, dentro
     if dentropy is not None:
         _need(entropy, "entropy")
     t, tb = _targets(_need(targets, "targets"), rows)
-    a, b, c, e = (_array(v, torch.float32, (rows,), n) for v, n in
-                  ((_need(lse, "lse"), "lse"), (_need(dlogp, "dlogp"), "dlogp"), (entropy, "entropy"), (dentropy, "dentropy")))
+    f32, shape = torch.float32, (rows,)
+    a, b = _array(_need(lse, "lse"), f32, shape, "lse"), _array(_need(dlogp, "dlogp"), f32, shape, "dlogp")
+    c, e = _array(entropy, f32, shape, "entropy"), _array(dentropy, f32, shape, "dentropy")
     dev = _one_device(logits, targets, lse, dlogp, dlogits, entropy, dentropy)
     _fp4_call(torch, load_library().dcr_logprobs_grad, "dcr_logprobs_grad", dev, stream, p, ty, stride, rows, vocab, t, tb,
               scale, a, b, c, e, d, d_stride)
