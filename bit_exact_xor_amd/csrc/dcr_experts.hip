@@ -3,10 +3,16 @@
 //
 // A row of logits lies in the registers of 8 to 64 lanes of a wave, eight
 // consecutive ones (or twice eight) a lane, so several rows share a wave and
-// nothing of a row leaves it but what is written.  The choice is made as in 64
-// bits: the scores of experts next to one another often differ by less than
-// the rounding of 32, and a choice that depended on it would differ from one
-// program to the next.
+// nothing of a row leaves it but what is written.
+//
+// The choice is that of 64 bits: the values of experts next to one another often
+// differ by less than the rounding of 32, and a choice that depended on it would
+// differ from one program to the next.  32 bits decide what they can: a bound
+// that the k best values surely reach (the k-th of the lanes' largest) leaves
+// little more than k candidates a row, and those alone, one a lane, are computed
+// and ranked in 64.  (All experts in 64 bits took 20 us for 16384 rows of 256
+// where this takes 12; 32 bits with a second look at close rows 13 to 18, since a
+// launch waits for its few second looks.)
 #include <algorithm>
 
 #include "dcr_step.h"
@@ -15,6 +21,8 @@ namespace dcr {
 namespace {
 
 constexpr uint32_t kET = 256;                     // threads of a workgroup
+constexpr uint32_t kAnyGroups = 31;
+constexpr uint32_t kFewGroups = 8;                // groups of any size that are compared in 32 bits first
 
 struct SelectArgs {
     const void* logits;
@@ -25,29 +33,27 @@ struct SelectArgs {
     void* dlogits;
     uint64_t stride, d_stride;
     uint32_t rows, experts, k, groups, top_groups, sigmoid, renormalize;
-    uint32_t wide, group_log2;      // the choice in 64 bits at once; else a group is 8 << group_log2 experts
+    uint32_t group_log2;      // a group is 8 << group_log2 experts, or (kAnyGroups) any number
     float scale;
 };
 
-// order of numbers as that of unsigned integers; NaN in front of all, and
-// 0 for what may not be chosen
+// order of numbers as that of unsigned integers, NaN in front of all; above 0
 __device__ __forceinline__ uint64_t rank_of(double c) {
     if (c != c) return ~uint64_t(0);
     const uint64_t b = uint64_t(__double_as_longlong(c + 0.0));
     return b ^ (uint64_t(int64_t(b) >> 63) | (uint64_t(1) << 63));
 }
-__device__ __forceinline__ uint32_t rank_of(float c) {
-    if (c != c) return ~0u;
+__device__ __forceinline__ uint64_t rank_of(float c) {
+    if (c != c) return ~uint64_t(0);
     const uint32_t b = __float_as_uint(c + 0.0f);
-    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+    return uint64_t(b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u)) << 32;
 }
-__device__ __forceinline__ float of_rank(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
-
-// LDS of one wave: its accesses are in order, the compiler has to keep them so
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
+// A rank with an index in its last ten bits, the lowest index first: no two
+// alike, so one comparison decides.  (Of a sum in 64 bits that leaves 42 bits
+// behind the leading one.)
+static_assert(DCR_EXPERTS_MAX <= 1024 && DCR_EXPERTS_MAX_GROUPS <= 64, "ten bits of a key, 64 bits of groups");
+__device__ __forceinline__ uint64_t key_of(uint64_t rank, uint32_t at) { return (rank | 1023u) - at; }
+__device__ __forceinline__ uint32_t index_of(uint64_t key) { return 1023u - uint32_t(key & 1023u); }
 
 template <int LANES, typename T>
 __device__ __forceinline__ T lanes_max(T v) {
@@ -77,161 +83,285 @@ __device__ __forceinline__ uint32_t expert_of(uint32_t lane, int i) {
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-// The k largest ranks of a row, one after the other, 0 taking no part; a lane
-// keeps every LANES-th.  `seen` gets each round's rank, then that of what would
-// come next.
-template <int LANES, int N, typename U, typename F>
-__device__ __forceinline__ void take_best(U* rank, uint32_t lane, uint32_t k, int32_t* id, F&& seen) {
-    constexpr int KEEP = DCR_EXPERTS_MAX_K / LANES;
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) id[q] = -1;
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) {
-        for (uint32_t j = q * LANES; j < min(k, uint32_t(q + 1) * LANES); ++j) {
-            U mine = rank[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) mine = max(mine, rank[i]);
-            const U best = lanes_all<LANES>(mine, [](U a, U b) { return max(a, b); });
-            seen(best);
-            uint32_t at = ~0u;
-#pragma unroll
-            for (int i = N - 1; i >= 0; --i) at = rank[i] == best ? expert_of<LANES>(lane, i) : at;
-            at = lanes_all<LANES>(at, [](uint32_t a, uint32_t b) { return min(a, b); });
-#pragma unroll
-            for (int i = 0; i < N; ++i) rank[i] = expert_of<LANES>(lane, i) == at ? U(0) : rank[i];
-            if (j - q * LANES == lane) id[q] = best ? int32_t(at) : -1;
-        }
-    }
-    U mine = rank[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mine = max(mine, rank[i]);
-    seen(lanes_all<LANES>(mine, [](U a, U b) { return max(a, b); }));
+// e^x for the comparisons, 2^-51 off: x as a multiple of log 2 and a rest below
+// 0.35, of which the power series to the 12th power.  Held to +-700, where
+// everything is 0 or 1 beside a bias.
+__device__ __forceinline__ double exp_near(double x) {
+    x = fmin(fmax(x, -700.0), 700.0);
+    const double n = rint(x * 1.44269504088896340736);
+    const double r = __fma_rn(n, -2.3190468138462996e-17, __fma_rn(n, -0.69314718055994530942, x));
+    double p = 1.0 / 479001600;
+    p = __fma_rn(p, r, 1.0 / 39916800), p = __fma_rn(p, r, 1.0 / 3628800), p = __fma_rn(p, r, 1.0 / 362880);
+    p = __fma_rn(p, r, 1.0 / 40320), p = __fma_rn(p, r, 1.0 / 5040), p = __fma_rn(p, r, 1.0 / 720);
+    p = __fma_rn(p, r, 1.0 / 120), p = __fma_rn(p, r, 1.0 / 24), p = __fma_rn(p, r, 1.0 / 6);
+    p = __fma_rn(p, r, 0.5), p = __fma_rn(p, r, 1.0), p = __fma_rn(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, int(n));
+}
+// 1 / x: the hardware's estimate and two steps of Newton's iteration
+__device__ __forceinline__ double inverse_near(double x) {
+    double y = __builtin_amdgcn_rcp(x);
+    y = __fma_rn(__fma_rn(-x, y, 1.0), y, y);
+    return __fma_rn(__fma_rn(-x, y, 1.0), y, y);
 }
 
-// The same where each lane first sorts its eight (28 steps of neighbours, which
-// leave equals in their order): a round then is a maximum and a minimum over the
-// heads of the lanes' lists, and the lane that had the best moves up.  About 30
-// instructions a round where searching eight took 79.
-template <int LANES, typename F>
-__device__ __forceinline__ void take_sorted(uint32_t* rank, uint32_t lane, uint32_t k, int32_t* id, F&& seen) {
-    constexpr int KEEP = DCR_EXPERTS_MAX_K / LANES;
-    uint32_t at[8], order = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) at[i] = uint32_t(i);
-#pragma unroll
-    for (int last = 7; last > 0; --last) {
-#pragma unroll
-        for (int i = 0; i < last; ++i) {
-            const bool swap = rank[i] < rank[i + 1];
-            const uint32_t x = rank[i], y = at[i];
-            rank[i] = max(x, rank[i + 1]);
-            rank[i + 1] = min(x, rank[i + 1]);
-            at[i] = swap ? at[i + 1] : y;
-            at[i + 1] = swap ? y : at[i + 1];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) order |= at[i] << (4 * i);
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) id[q] = -1;
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) {
-        for (uint32_t j = q * LANES; j < min(k, uint32_t(q + 1) * LANES); ++j) {
-            const uint32_t best = lanes_all<LANES>(rank[0], [](uint32_t a, uint32_t b) { return max(a, b); });
-            seen(best);
-            const uint32_t mine = 8 * lane + (order & 7u);
-            const uint32_t e = lanes_all<LANES>(rank[0] == best ? mine : ~0u, [](uint32_t a, uint32_t b) { return min(a, b); });
-            const bool won = e == mine;
-#pragma unroll
-            for (int i = 0; i < 7; ++i) rank[i] = won ? rank[i + 1] : rank[i];
-            rank[7] = won ? 0 : rank[7];
-            order = won ? order >> 4 : order;
-            if (j - q * LANES == lane) id[q] = best ? int32_t(e) : -1;
-        }
-    }
-    seen(lanes_all<LANES>(rank[0], [](uint32_t a, uint32_t b) { return max(a, b); }));
+// LDS of one wave: its accesses are in order, the compiler has to keep them so
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// The choice in 64 bits, through LDS where there are groups (the row's values
-// and its groups' ranks).
+// order of 32-bit values as that of unsigned integers, NaN in front of all;
+// above 0
+__device__ __forceinline__ uint32_t rank32(float c) { return uint32_t(rank_of(c) >> 32); }
+__device__ __forceinline__ float of_rank32(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u); }
+
+// sum over the lanes of a row up to and with this one
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_upto(uint32_t v, uint32_t lane) {
+    const auto add = [&](auto shift) {
+        constexpr int D = decltype(shift)::value;
+        const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x110 + D, 0xF, 0xF, true));   // D lanes up in a row of 16
+        v += (LANES >= 16 || lane >= D) ? o : 0;
+    };
+    add(std::integral_constant<int, 1>()), add(std::integral_constant<int, 2>()), add(std::integral_constant<int, 4>());
+    if constexpr (LANES >= 16) add(std::integral_constant<int, 8>());
+    if constexpr (LANES >= 32) v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));  // row 0 to 1, 2 to 3
+    if constexpr (LANES >= 64) v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));  // half to half
+    return v;
+}
+
+// The two largest values of a lane's part of a group, and over STEP lanes more.
+struct Two {
+    double first, second;
+    __device__ __forceinline__ void meet(double f, double s) {
+        second = fmax(fmin(first, f), fmax(second, s));
+        first = fmax(first, f);
+    }
+    template <int STEP, int LANES>
+    __device__ __forceinline__ void fold(uint32_t lanes) {
+        if constexpr (STEP < LANES) {
+            if (lanes > STEP) {
+                double f[2], s[2];
+                partners_of<STEP>(first, &f[0], &f[1]);
+                partners_of<STEP>(second, &s[0], &s[1]);
+                first = f[0], second = s[0];
+                meet(f[1], s[1]);
+            }
+            fold<2 * STEP, LANES>(lanes);
+        }
+    }
+    // 0 where the group has nothing open
+    __device__ __forceinline__ uint64_t key(uint32_t group) const {
+        return first == -INFINITY ? 0 : key_of(rank_of(second == -INFINITY ? first : first + second), group);
+    }
+};
+
+// The groups' choice in 32 bits: `off` bounds a value's error, so sums of two
+// that lie 5 `off` apart (relative to them, above 1) are in order.  Shuts experts
+// (ranks to 0) and returns whether what decides was that far apart.
 template <int LANES, int N>
-__device__ __forceinline__ void choose64(const SelectArgs& a, const float* v, const float* bias, float top, double* lds,
-                                         uint32_t lane, int32_t* id) {
-    const bool grouped = a.top_groups < a.groups;
-    double sum = 1.0;
-    if (!a.sigmoid) {
-        double z = 0.0;
+__device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, uint32_t* rank) {
+    struct {
+        float first, second;
+        __device__ __forceinline__ void meet(float f, float s) {
+            second = fmaxf(fminf(first, f), fmaxf(second, s));
+            first = fmaxf(first, f);
+        }
+    } two;
+    const auto fold = [&](auto step, uint32_t lanes) {
+        constexpr int S = decltype(step)::value;
+        if constexpr (S < LANES) {
+            if (lanes > S) {
+                float f[2], s[2];
+                partners_of<S>(two.first, &f[0], &f[1]);
+                partners_of<S>(two.second, &s[0], &s[1]);
+                two.first = f[0], two.second = s[0];
+                two.meet(f[1], s[1]);
+            }
+        }
+    };
+    const auto value = [&](uint32_t lanes) {       // of the group that lies in so many lanes
+        fold(std::integral_constant<int, 1>(), lanes), fold(std::integral_constant<int, 2>(), lanes);
+        fold(std::integral_constant<int, 4>(), lanes), fold(std::integral_constant<int, 8>(), lanes);
+        fold(std::integral_constant<int, 16>(), lanes), fold(std::integral_constant<int, 32>(), lanes);
+        return two.first == -INFINITY ? 0 : rank32(two.second == -INFINITY ? two.first : two.first + two.second);
+    };
+    bool odd = false;
 #pragma unroll
-        for (int i = 0; i < N; ++i) z += exp(double(v[i]) - double(top));
-        sum = lanes_sum<LANES>(z);
-        if (sum == 0.0) sum = 1.0;
+    for (int i = 0; i < N; ++i) odd |= c[i] != c[i];
+    two.first = two.second = -INFINITY;
+    uint32_t least, most = 0;                      // of the groups taken, of the others
+    if (a.group_log2 < kAnyGroups) {
+        // groups of whole lanes, a power of two of them: all groups at once
+#pragma unroll
+        for (int i = 0; i < N; ++i) two.meet(c[i], -INFINITY);
+        const uint32_t of = value(1u << a.group_log2);
+        const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
+        uint32_t ahead = 0;
+        for (uint32_t g = 0; g < a.groups; ++g) {
+            const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.group_log2)), 64));
+            ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
+        }
+        const bool in = ahead < a.top_groups;      // (lanes behind the last group are shut, and last)
+        least = lanes_all<LANES>(in && mine < a.groups ? of : ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
+        most = lanes_all<LANES>(in ? 0u : of, [](uint32_t x, uint32_t y) { return max(x, y); });
+#pragma unroll
+        for (int i = 0; i < N; ++i) rank[i] = in ? rank[i] : 0;
+    } else {
+        // up to kFewGroups groups of any size: one after the other over all lanes
+        const uint32_t size = a.experts / a.groups;
+        uint32_t of[kFewGroups], in = 0;           // in, bit g: group g is taken
+#pragma unroll
+        for (uint32_t g = 0; g < kFewGroups; ++g) {
+            of[g] = 0;
+            if (g >= a.groups) continue;
+            two.first = two.second = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) two.meet(expert_of<LANES>(lane, i) - g * size < size ? c[i] : -INFINITY, -INFINITY);
+            of[g] = value(LANES);
+        }
+        least = ~0u;
+#pragma unroll
+        for (uint32_t g = 0; g < kFewGroups; ++g) {
+            if (g >= a.groups) continue;
+            uint32_t ahead = 0;
+#pragma unroll
+            for (uint32_t o = 0; o < kFewGroups; ++o) ahead += (of[o] > of[g] || (of[o] == of[g] && o < g)) ? 1u : 0u;
+            if (ahead < a.top_groups)
+                in |= 1u << g, least = min(least, of[g]);
+            else
+                most = max(most, of[g]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            bool open = false;
+#pragma unroll
+            for (uint32_t g = 0; g < kFewGroups; ++g) open |= (in >> g & 1u) && expert_of<LANES>(lane, i) - g * size < size;
+            rank[i] = open ? rank[i] : 0;
+        }
     }
-    uint64_t rank[N];
+    const float x = of_rank32(least), y = of_rank32(most);
+    return !odd && (most == 0 || x - y > 5 * off * fmaxf(1.0f, fabsf(x)));
+}
+
+// The same in 64 bits, groups of any number and size.  c: the lane's s + bias,
+// -infinity where shut.
+template <int LANES, int N>
+__device__ __forceinline__ void take_groups(const SelectArgs& a, const double* c, uint32_t lane, uint32_t* rank) {
+    const uint32_t size = a.experts / a.groups;
+    bool odd = false;                              // a NaN in the lane's part: its group goes first
+    if (a.group_log2 < kAnyGroups) {
+        // groups of whole lanes, a power of two of them: all groups at once
+        Two two = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < N; ++i) two.meet(c[i], -INFINITY), odd |= c[i] != c[i];
+        two.template fold<1, LANES>(1u << a.group_log2);
+        const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
+        const uint64_t odds = __ballot(odd) >> (base + (mine << a.group_log2));
+        uint64_t of = two.key(mine);
+        if (odds & ((uint64_t(2) << ((1u << a.group_log2) - 1)) - 1)) of = key_of(~uint64_t(0), mine);
+        uint32_t ahead = 0;
+        for (uint32_t g = 0; g < a.groups; ++g)
+            ahead += uint64_t(__shfl((unsigned long long)of, int(base + (g << a.group_log2)), 64)) > of ? 1u : 0u;
+        if (!of || ahead >= a.top_groups) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) rank[i] = 0;
+        }
+        return;
+    }
+    // groups of any size, one after the other over all lanes; a lane keeps the
+    // groups lane, lane + LANES, ... in mind
+    constexpr int KEEP = DCR_EXPERTS_MAX_GROUPS / LANES;
+    uint64_t of[KEEP];
+#pragma unroll
+    for (int q = 0; q < KEEP; ++q) of[q] = 0;
+    for (uint32_t g = 0; g < a.groups; ++g) {
+        Two two = {-INFINITY, -INFINITY};
+        odd = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool in = expert_of<LANES>(lane, i) - g * size < size;
+            two.meet(in ? c[i] : -INFINITY, -INFINITY);
+            odd |= in && c[i] != c[i];
+        }
+        two.template fold<1, LANES>(LANES);
+        const uint32_t odds = lanes_all<LANES>(odd ? 1u : 0u, [](uint32_t x, uint32_t y) { return x | y; });
+#pragma unroll
+        for (int q = 0; q < KEEP; ++q)
+            if (g == lane + q * LANES) of[q] = odds ? key_of(~uint64_t(0), g) : two.key(g);
+    }
+    // the top_groups largest, as bits
+    uint64_t in = 0;
+    for (uint32_t n = 0; n < a.top_groups; ++n) {
+        uint64_t mine = of[0];
+#pragma unroll
+        for (int q = 1; q < KEEP; ++q) mine = mine > of[q] ? mine : of[q];
+        const uint64_t best = lanes_all<LANES>(mine, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+        if (best) in |= uint64_t(1) << index_of(best);
+#pragma unroll
+        for (int q = 0; q < KEEP; ++q) of[q] = of[q] == best ? 0 : of[q];
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const uint32_t e = expert_of<LANES>(lane, i);
-        double c = double(v[i]);               // without a bias the logits have the order of the scores
-        if (a.bias || grouped) {
-            c = a.sigmoid ? sigmoid64(c) : exp(c - double(top)) / sum;
-            c += double(bias[i]);
-            if (grouped && e < a.experts) lds[e] = v[i] == -INFINITY ? -INFINITY : c;
-            if (!a.bias) c = double(v[i]);
-        }
-        rank[i] = v[i] == -INFINITY ? 0 : rank_of(c);
+        if (e >= a.experts || !(in >> (e / size) & 1)) rank[i] = 0;
     }
-    if (grouped) {
-        uint64_t* of_group = reinterpret_cast<uint64_t*>(lds + a.experts);
-        const uint32_t size = a.experts / a.groups;
-        wave_sync();
-        for (uint32_t g = lane; g < a.groups; g += LANES) {
-            double first = -INFINITY, second = -INFINITY;
-            bool odd = false;
-            for (uint32_t i = 0; i < size; ++i) {
-                const double c = lds[g * size + i];
-                odd |= c != c;
-                second = c > first ? first : c > second ? c : second;
-                first = c > first ? c : first;
-            }
-            of_group[g] = odd ? ~uint64_t(0) : first == -INFINITY ? 0 : rank_of(second == -INFINITY ? first : first + second);
-        }
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t e = expert_of<LANES>(lane, i);
-            if (e >= a.experts) continue;
-            const uint32_t mine = e / size;
-            const uint64_t r = of_group[mine];
-            uint32_t ahead = 0;
-            for (uint32_t g = 0; g < a.groups; ++g) ahead += (of_group[g] > r || (of_group[g] == r && g < mine)) ? 1u : 0u;
-            if (ahead >= a.top_groups) rank[i] = 0;
-        }
-    }
-    take_best<LANES, N>(rank, lane, a.k, id, [](uint64_t) {});
 }
 
-// The same in 32 bits, for groups of a power of two of lanes; false where two
-// values that decide are closer than they are certain.  A sigmoid by the
-// hardware's exponential and reciprocal (one step off each) is off by less than
-// 2.3 * 2^-23 and a sum with the bias by 2^-24 of itself; a softmax's sum of up
-// to 1024 terms adds less than 2^-20 of a score.  So `off` bounds a value's error,
-// and two values 2 `off` apart (groups: sums of two, 5 `off`) are in order.
+// scores of a row in 64 bits for the comparisons
 template <int LANES, int N>
-__device__ __forceinline__ bool choose32(const SelectArgs& a, const float* v, const float* bias, float top, uint32_t lane,
-                                         int32_t* id) {
-    constexpr float kLog2e = 1.44269504088896340736f;
-    const bool grouped = a.top_groups < a.groups;
-    float c[N];
-    uint32_t rank[N];
-    bool odd = false;
+__device__ __forceinline__ double softmax_inverse(const float* v, float top) {
+    double z = 0.0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) odd |= v[i] != v[i];
+    for (int i = 0; i < N; ++i) z += v[i] == -INFINITY ? 0.0 : exp_near(double(v[i]) - double(top));
+    z = lanes_sum<LANES>(z);
+    return z == 0.0 ? 0.0 : 1.0 / z;
+}
+
+// LDS of a row: its candidates (logit and index), their keys, the chosen ones
+__host__ __device__ inline uint32_t select_lds(uint32_t experts, uint32_t k) { return 16 * experts + 16 * k; }
+
+template <typename T, int LANES, int R>
+__global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
+    constexpr int N = 8 * R, ROWS = kET / LANES;
+    constexpr float kLog2e = 1.44269504088896340736f;
+    extern __shared__ uint64_t lds[];
+    const uint32_t lane = threadIdx.x % LANES, in_wg = threadIdx.x / LANES;
+    uint64_t* found = lds + in_wg * (select_lds(a.experts, a.k) / 8);
+    uint64_t* keys = found + a.experts;
+    double* weights = reinterpret_cast<double*>(keys + a.experts);
+    int32_t* ids = reinterpret_cast<int32_t*>(weights + a.k);
+    const uint32_t at = blockIdx.x * ROWS + in_wg;
+    const bool live = at < a.rows;
+    const T* row = static_cast<const T*>(a.logits) + uint64_t(live ? at : 0) * a.stride;
+    const bool grouped = a.top_groups < a.groups;
+    float v[N], bias[N];
+    load_row<T, LANES, R>(row, lane, a.experts, v);
+    if (a.bias) {
+        load_row<float, LANES, R>(a.bias, lane, a.experts, bias);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) bias[i] = 0.0f;
+    }
+    for (uint32_t j = lane; j < a.k; j += LANES) ids[j] = -1, weights[j] = 0.0;
+    float top = 0.0f;
+    if (!a.sigmoid) {
+        top = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) top = (v[i] > top || v[i] != v[i]) ? v[i] : top;
+        top = lanes_max<LANES>(top);
+        if (top == -INFINITY) top = 0.0f;      // every expert is shut
+    }
+    // Ranks in 32 bits.  A sigmoid by the hardware's exponential and reciprocal
+    // (one step off each) is off by less than 2.3 * 2^-23 and a sum with the bias
+    // by 2^-24 of itself; a softmax's sum of up to 1024 terms adds less than 2^-20
+    // of a score.  Without a bias the logits themselves have the scores' order.
     const float off = a.sigmoid ? 0x1p-21f : 0x1p-20f;
-    const auto apart = [](uint32_t hi, uint32_t lo, float by) {
-        const float x = of_rank(hi), y = of_rank(lo);
-        return lo == 0 || x - y > by * fmaxf(1.0f, fabsf(x));
-    };
+    uint32_t rank[N];
+    double inverse = 1.0;                      // of the softmax's sum
+    if (!a.sigmoid && (a.bias || !a.renormalize)) inverse = softmax_inverse<LANES, N>(v, top);
     if (a.bias || grouped) {
-        float inv = 1.0f;
+        float c[N], inv = 1.0f;
         if (a.sigmoid) {
 #pragma unroll
             for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v[i]));
@@ -245,115 +375,97 @@ __device__ __forceinline__ bool choose32(const SelectArgs& a, const float* v, co
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             c[i] = v[i] == -INFINITY ? -INFINITY : __fmaf_rn(c[i], inv, bias[i]);
-            odd |= c[i] != c[i];
+            rank[i] = v[i] == -INFINITY ? 0 : rank32(a.bias ? c[i] : v[i]);
         }
-    }
+        if (grouped) {
+            uint32_t all[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) rank[i] = v[i] == -INFINITY ? 0 : rank_of(a.bias ? c[i] : v[i]);
-    if (grouped) {
-        float first = -INFINITY, second = -INFINITY;
-        const auto meet = [&](float f, float s) {
-            second = fmaxf(fminf(first, f), fmaxf(second, s));
-            first = fmaxf(first, f);
-        };
+            for (int i = 0; i < N; ++i) all[i] = rank[i];
+            const bool few = a.group_log2 < kAnyGroups || a.groups <= kFewGroups;
+            if (!few || __any(!take_groups32<LANES, N>(a, c, lane, off, rank))) {
+                double d[N];
+                double z = inverse;
+                if (!a.sigmoid && !a.bias && a.renormalize) z = softmax_inverse<LANES, N>(v, top);
 #pragma unroll
-        for (int i = 0; i < N; ++i) meet(c[i], -INFINITY);
-        const auto fold = [&](auto step) {
-            constexpr int S = decltype(step)::value;
-            if constexpr (S < LANES) {
-                if ((1u << a.group_log2) > S) {
-                    float f[2], s[2];
-                    partners_of<S>(first, &f[0], &f[1]);
-                    partners_of<S>(second, &s[0], &s[1]);
-                    first = f[0], second = s[0];
-                    meet(f[1], s[1]);
+                for (int i = 0; i < N; ++i) {
+                    rank[i] = all[i];
+                    d[i] = a.sigmoid ? inverse_near(1.0 + exp_near(-double(v[i]))) : exp_near(double(v[i]) - double(top)) * z;
+                    d[i] = v[i] == -INFINITY ? -INFINITY : (v[i] != v[i] || top != top) ? NAN : d[i] + double(bias[i]);
                 }
+                take_groups<LANES, N>(a, d, lane, rank);
             }
-        };
-        fold(std::integral_constant<int, 1>()), fold(std::integral_constant<int, 2>()), fold(std::integral_constant<int, 4>());
-        fold(std::integral_constant<int, 8>()), fold(std::integral_constant<int, 16>()), fold(std::integral_constant<int, 32>());
-        const uint32_t of = first == -INFINITY ? 0 : rank_of(second == -INFINITY ? first : first + second);
-        const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
-        uint32_t ahead = 0;
-        for (uint32_t g = 0; g < a.groups; ++g) {
-            const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.group_log2)), 64));
-            ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
         }
-        const bool in = ahead < a.top_groups;      // (lanes behind the last group are shut, and last)
-        const uint32_t least = lanes_all<LANES>(in && mine < a.groups ? of : ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
-        const uint32_t most = lanes_all<LANES>(in ? 0u : of, [](uint32_t x, uint32_t y) { return max(x, y); });
-        odd |= !apart(least, most, 5 * off);
-#pragma unroll
-        for (int i = 0; i < N; ++i) rank[i] = in ? rank[i] : 0;
-    }
-    uint32_t before = 0;
-    bool sure = true;
-    const auto seen = [&](uint32_t best) {
-        if (a.bias && before) sure &= apart(before, best, 2 * off);
-        before = best;
-    };
-    if constexpr (N == 8)
-        take_sorted<LANES>(rank, lane, a.k, id, seen);
-    else
-        take_best<LANES, N>(rank, lane, a.k, id, seen);
-    return sure && !odd;
-}
-
-template <typename T, int LANES, int R>
-__global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
-    constexpr int N = 8 * R, ROWS = kET / LANES, KEEP = DCR_EXPERTS_MAX_K / LANES;
-    extern __shared__ double values[];         // with groups: a row's values, then its groups' ranks
-    const uint32_t lane = threadIdx.x % LANES, in_wg = threadIdx.x / LANES;
-    const uint32_t at = blockIdx.x * ROWS + in_wg;
-    const bool live = at < a.rows;
-    const T* row = static_cast<const T*>(a.logits) + uint64_t(live ? at : 0) * a.stride;
-    float v[N], bias[N];
-    load_row<T, LANES, R>(row, lane, a.experts, v);
-    if (a.bias) {
-        load_row<float, LANES, R>(a.bias, lane, a.experts, bias);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) bias[i] = 0.0f;
+        for (int i = 0; i < N; ++i) rank[i] = v[i] == -INFINITY ? 0 : rank32(v[i]);
     }
-    float top = v[0];
+    // the k-th largest of the lanes' largest ranks (or, with equals among them,
+    // one below): at least k experts reach it
+    uint32_t bound = 0;
+    if (a.k <= LANES) {
+        uint32_t mine = rank[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = (v[i] > top || v[i] != v[i]) ? v[i] : top;
-    top = lanes_max<LANES>(top);
-    if (top == -INFINITY) top = 0.0f;          // every expert is shut
-    int32_t id[KEEP];
-    const bool sure = !a.wide && choose32<LANES, N>(a, v, bias, top, lane, id);
-    if (__any(!sure)) choose64<LANES, N>(a, v, bias, top, values + in_wg * (a.experts + a.groups), lane, id);
-
-    // the weights in 64 bits: a few exponentials a row
-    double sum = 1.0;
-    if (!a.sigmoid && !a.renormalize) {
-        double z = 0.0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) z += exp(double(v[i]) - double(top));
-        sum = lanes_sum<LANES>(z);
-        if (sum == 0.0) sum = 1.0;
-    }
-    double w[KEEP], all = 0.0;
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) {
-        w[q] = 0.0;
-        if (id[q] >= 0) {
-            const double l = double(wide(row[id[q]]));
-            w[q] = a.sigmoid ? sigmoid64(l) : exp(l - double(top));
+        for (int i = 1; i < N; ++i) mine = max(mine, rank[i]);
+        for (uint32_t j = 0; j < a.k; ++j) {
+            bound = lanes_all<LANES>(mine, [](uint32_t x, uint32_t y) { return max(x, y); });
+            mine = mine == bound ? 0 : mine;
         }
-        all += w[q];
+        if (a.bias && bound && bound != ~0u) {     // and in 64 bits at least this
+            const float x = of_rank32(bound);
+            bound = rank32(x - 2 * off * fmaxf(1.0f, fabsf(x)));
+        }
     }
+    bound = max(bound, 1u);
+    // the candidates, one behind the other
+    uint32_t count = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) count += rank[i] >= bound ? 1u : 0u;
+    const uint32_t upto = lanes_upto<LANES>(count, lane);
+    const uint32_t n = uint32_t(__shfl(int(upto), int((threadIdx.x & 63u) | (LANES - 1)), 64));
+    uint32_t to = upto - count;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (rank[i] >= bound) found[to] = uint64_t(__float_as_uint(v[i])) << 32 | expert_of<LANES>(lane, i);
+        to += rank[i] >= bound ? 1u : 0u;
+    }
+    wave_sync();
+    for (uint32_t i = lane; i < n; i += LANES) {
+        const uint32_t e = uint32_t(found[i]);
+        const float l = __uint_as_float(uint32_t(found[i] >> 32));
+        uint64_t key;
+        if (a.bias) {
+            double c = a.sigmoid ? inverse_near(1.0 + exp_near(-double(l))) : exp_near(double(l) - double(top)) * inverse;
+            if (l != l || top != top) c = NAN;
+            key = rank_of(c + double(a.bias[e]));
+        } else {
+            key = rank_of(l);
+        }
+        keys[i] = key_of(key, e);
+    }
+    wave_sync();
+    for (uint32_t i = lane; i < n; i += LANES) {
+        const uint64_t mine = keys[i];
+        uint32_t ahead = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < n; ++j) ahead += keys[j] > mine ? 1u : 0u;
+        if (ahead < a.k) {
+            const double l = double(__uint_as_float(uint32_t(found[i] >> 32)));
+            ids[ahead] = int32_t(uint32_t(found[i]));
+            weights[ahead] = a.sigmoid ? sigmoid64(l) : exp(l - double(top)) * (a.renormalize ? 1.0 : inverse);
+        }
+    }
+    wave_sync();
+    double all = 1.0;
     if (a.renormalize) {
-        sum = lanes_sum<LANES>(all);
-        if (sum == 0.0) sum = 1.0;
+        double sum = 0.0;
+        for (uint32_t j = lane; j < a.k; j += LANES) sum += weights[j];
+        sum = lanes_sum<LANES>(sum);
+        if (sum != 0.0) all = sum;
     }
     if (!live) return;
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) {
-        const uint32_t j = q * LANES + lane;
-        if (j >= a.k) continue;
-        a.ids[uint64_t(at) * a.k + j] = id[q];
-        a.weights[uint64_t(at) * a.k + j] = float(w[q] / sum * double(a.scale));
+    for (uint32_t j = lane; j < a.k; j += LANES) {
+        a.ids[uint64_t(at) * a.k + j] = ids[j];
+        a.weights[uint64_t(at) * a.k + j] = float(weights[j] / all * double(a.scale));
     }
 }
 
@@ -622,14 +734,14 @@ int32_t select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows
     if (top_groups < groups) {
         const uint32_t size = experts / groups;
         while ((8u << a.group_log2) < size) ++a.group_log2;
-        a.wide = experts > 512 || (8u << a.group_log2) != size;
+        if (experts > 512 || (8u << a.group_log2) != size) a.group_log2 = kAnyGroups;
     }
     with_type(type, [&](auto t) {
         with_lanes(experts, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
-            const uint32_t lds = top_groups < groups ? ROWS * (experts + groups) * 8 : 0;
             const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);
-            hipLaunchKernelGGL((experts_select_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET), lds, st, a);
+            hipLaunchKernelGGL((experts_select_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET),
+                               ROWS * select_lds(experts, k), st, a);
         });
     });
     return step_launched();
