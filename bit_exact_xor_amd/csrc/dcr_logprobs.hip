@@ -84,9 +84,15 @@ struct TopLds {
 
 // how many of the keys first, first + step, ... of n at `keys` (LDS) are larger
 __device__ __forceinline__ uint32_t larger(const uint64_t* keys, uint32_t first, uint32_t n, uint32_t step, uint64_t key) {
-    uint32_t r = 0;
-#pragma unroll 8
-    for (uint32_t j = first; j < n; j += step) r += keys[j] > key ? 1u : 0u;
+    uint32_t r = 0, j = first;
+    for (; j + 7 * step < n; j += 8 * step) {      // eight on their way together
+        uint64_t k[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) k[u] = keys[j + u * step];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) r += k[u] > key ? 1u : 0u;
+    }
+    for (; j < n; j += step) r += keys[j] > key ? 1u : 0u;
     return r;
 }
 
@@ -110,7 +116,7 @@ __device__ __forceinline__ void find_bound(TopLds& l, uint32_t top, uint64_t bes
 
 // A round, of all threads: `passes` tells (it may be too often true) whether
 // one of the thread's keys is above `least`, `best` gives its largest key, `each`
-// calls a function with every key.  Returns the last key held, 0 (nothing is)
+// calls a function with every key above its argument, or more.  Returns the last key held, 0 (nothing is)
 // before the first round.
 template <typename B, typename E>
 __device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t least, bool first, bool passes, B&& best, E&& each) {
@@ -128,7 +134,7 @@ __device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t 
         from = max(from, l.bound);
     }
     if (passes) {
-        each([&](uint64_t k) {
+        each(from, [&](uint64_t k) {
             if (k > from) l.more[atomicAdd(&l.n, 1u)] = k;
         });
     }
@@ -174,11 +180,14 @@ struct RowOf {
     }
 };
 
+__device__ __forceinline__ bool none_open(Sums s) { return s.m == -INFINITY && s.s == s.s; }     // an empty row
+__device__ __forceinline__ RowOf row_of_sums(Sums s) { return {s.m, none_open(s) ? 0.0f : logf(s.s)}; }
+
 // what a row's sums give; by one thread
 template <typename T>
 __device__ __forceinline__ RowOf finish_row(const LpArgs& a, uint32_t row, Sums s) {
-    const bool none = s.m == -INFINITY && s.s == s.s;        // an empty row
-    const RowOf of = {s.m, none ? 0.0f : logf(s.s)};
+    const bool none = none_open(s);
+    const RowOf of = row_of_sums(s);
     if (a.lse) a.lse[row] = none ? -INFINITY : __fmaf_rn(s.m, a.scale, of.log_s);
     if (a.entropy) a.entropy[row] = none ? 0.0f : of.log_s - kLn2 * s.t / s.s;
     if (a.logp) {
@@ -197,19 +206,40 @@ __device__ __forceinline__ void put_top(const LpArgs& a, uint32_t row, uint32_t 
     a.top_values[to] = of.logp(of_order(uint32_t(key >> 32)), a.scale);
 }
 
-// a thread's logits of a step: twice eight, 8 kLT apart, so that a wave reads
-// whole lines
-template <typename T>
+// a thread's logits of a step of THREADS: twice eight, 8 THREADS apart, so that a
+// wave reads whole lines
+template <uint32_t THREADS, typename T>
 __device__ __forceinline__ void load_step(const T* x, uint32_t c0, uint32_t to, Raw8<T>* raw) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint32_t at = c0 + (h * kLT + threadIdx.x) * 8;
+        const uint32_t at = c0 + (h * THREADS + threadIdx.x % THREADS) * 8;
         const int n = at < to ? int(min(8u, to - at)) : 0;
         if (n == 8)
             raw[h].load_once(x + at);
         else
             raw[h].load_some(x + at, n, kBf16MinusInf);
     }
+}
+
+// a step's logits into a thread's sums; returns the largest of them
+__device__ __forceinline__ float add_step(const float* v, float unit, Sums& sum) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < int(kPiece); ++i) top = fmaxf(top, v[i]);
+    const float m = fmaxf(sum.m, top);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const float d = sum.m == -INFINITY ? 0.0f : fmaxf((sum.m - m) * unit, -160.0f), f = exp2f(d);
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < int(kPiece); ++i) {
+        const float e = (v[i] - base) * unit, p = __builtin_amdgcn_exp2f(e);
+        s += p;
+        t = __fmaf_rn(p, fmaxf(e, -160.0f), t);
+    }
+    sum.t = __fmaf_rn(f, __fmaf_rn(sum.s, d, sum.t), t);
+    sum.s = __fmaf_rn(sum.s, f, s);
+    sum.m = m;
+    return top;
 }
 
 template <typename T, bool TOP>
@@ -225,29 +255,14 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
     Sums sum = {-INFINITY, 0.0f, 0.0f};
     uint64_t least = 0;
     Raw8<T> raw[2];
-    load_step(x, from, to, raw);
+    load_step<kLT>(x, from, to, raw);
     if constexpr (TOP) top_begin(lds);
     for (uint32_t c0 = from; c0 < to; c0 += kLT * kPiece) {
         float v[kPiece];
         raw[0].get(v);
         raw[1].get(v + 8);
-        if (c0 + kLT * kPiece < to) load_step(x, c0 + kLT * kPiece, to, raw);
-        float top = v[0];
-#pragma unroll
-        for (int i = 1; i < int(kPiece); ++i) top = fmaxf(top, v[i]);
-        const float m = fmaxf(sum.m, top);
-        const float base = m == -INFINITY ? 0.0f : m;
-        const float d = sum.m == -INFINITY ? 0.0f : fmaxf((sum.m - m) * unit, -160.0f), f = exp2f(d);
-        float s = 0.0f, t = 0.0f;
-#pragma unroll
-        for (int i = 0; i < int(kPiece); ++i) {
-            const float e = (v[i] - base) * unit, p = __builtin_amdgcn_exp2f(e);
-            s += p;
-            t = __fmaf_rn(p, fmaxf(e, -160.0f), t);
-        }
-        sum.t = __fmaf_rn(f, __fmaf_rn(sum.s, d, sum.t), t);
-        sum.s = __fmaf_rn(sum.s, f, s);
-        sum.m = m;
+        if (c0 + kLT * kPiece < to) load_step<kLT>(x, c0 + kLT * kPiece, to, raw);
+        [[maybe_unused]] const float top = add_step(v, unit, sum);
         if constexpr (TOP) {
             const auto key = [&](int i) {
                 const uint32_t j = c0 + ((i / 8) * kLT + threadIdx.x) * 8 + i % 8;
@@ -263,9 +278,11 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
                     for (int i = 0; i < int(kPiece); ++i) b = max(b, key(i));
                     return b;
                 },
-                [&](auto&& put) {
+                [&](uint64_t above, auto&& put) {
+                    const float low = of_order(uint32_t(above >> 32));      // (NaN of 0: nothing is below)
 #pragma unroll
-                    for (int i = 0; i < int(kPiece); ++i) put(key(i));
+                    for (int i = 0; i < int(kPiece); ++i)
+                        if (!(v[i] < low)) put(key(i));
                 });
         }
     }
@@ -286,6 +303,142 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
                 put_top(a, row, threadIdx.x, lds.held[threadIdx.x], row_of);
             else
                 a.keys[uint64_t(blockIdx.x) * a.top + threadIdx.x] = lds.held[threadIdx.x];
+        }
+    }
+}
+
+// The best `top` keys that a wave has met, one a lane, the largest in lane 0.  What
+// few lanes bring is put in one after the other: ranked by a ballot, the lanes
+// behind move up.  Where many lanes pass, as TopLds without barriers: the bound
+// is the top-th largest of the 64 lanes' best keys.  LDS of a wave: the keys held
+// before and after, the lanes' best, what was gathered.
+constexpr uint32_t kFewLanes = 6;
+constexpr uint32_t wave_keys(uint32_t top) { return 2 * DCR_LOGPROBS_MAX_TOP + 64 + top * kMostPer; }
+
+__device__ __forceinline__ void wave_sync() {      // LDS of one wave is in order, the compiler has to keep it so
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+    return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32 |
+           uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), lane));
+}
+
+struct TopWave {
+    uint64_t* lds;
+    uint64_t mine, least;                    // the lane's key; that of lane top - 1
+    uint32_t have;                           // keys held, 0 or `top`
+
+    __device__ __forceinline__ explicit TopWave(uint64_t* at) : lds(at), mine(0), least(0), have(0) {}
+
+    __device__ __forceinline__ void insert(uint64_t key, uint32_t top) {
+        const uint32_t lane = threadIdx.x & 63u, at = uint32_t(__popcll(__ballot(mine > key)));
+        // (the lane in front's: a shift of the whole wave)
+        const uint64_t front = uint64_t(uint32_t(__builtin_amdgcn_update_dpp(0, int(mine >> 32), 0x138, 0xF, 0xF, false))) << 32 |
+                               uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(mine)), 0x138, 0xF, 0xF, false));
+        mine = lane < at ? mine : lane == at ? key : front;
+        least = lane_value(mine, int(top) - 1);
+    }
+
+    template <typename K>
+    __device__ __forceinline__ void round(uint32_t top, bool passes, const float* v, K&& key) {
+        const uint32_t lane = threadIdx.x & 63u;
+        const uint32_t some = uint32_t(__popcll(__ballot(passes)));
+        if (!some && have) return;
+        if (some <= kFewLanes && have) {
+            float low = of_order(uint32_t(least >> 32));       // (NaN of 0: nothing is below)
+#pragma unroll
+            for (int i = 0; i < int(kPiece); ++i) {
+                uint64_t who = __ballot(passes && !(v[i] < low));
+                if (!who) continue;
+                const uint64_t k = key(i);
+                for (; who; who &= who - 1) {
+                    const uint64_t one = lane_value(k, __ffsll((unsigned long long)who) - 1);
+                    if (one > least) insert(one, top);
+                }
+                low = of_order(uint32_t(least >> 32));
+            }
+            return;
+        }
+        uint64_t *held = lds, *other = lds + DCR_LOGPROBS_MAX_TOP, *best = other + DCR_LOGPROBS_MAX_TOP, *more = best + 64;
+        uint64_t from = least;
+        if (some > top) {
+            uint64_t b = 0;
+#pragma unroll
+            for (int i = 0; i < int(kPiece); ++i) b = max(b, key(i));
+            best[lane] = b;
+            wave_sync();
+            const uint64_t who = __ballot(b && larger(best, 0, 64, 1, b) == top - 1);
+            if (who) from = max(from, lane_value(b, __ffsll((unsigned long long)who) - 1) - 1);
+        }
+        uint32_t n = 0;
+        const float low = of_order(uint32_t(from >> 32));
+#pragma unroll
+        for (int i = 0; i < int(kPiece); ++i) {
+            if (!__ballot(passes && !(v[i] < low))) continue;
+            const uint64_t k = key(i);
+            const bool in = passes && k > from;
+            const uint64_t who = __ballot(in);
+            if (in) more[n + uint32_t(__popcll(who & ((uint64_t(1) << lane) - 1)))] = k;
+            n += uint32_t(__popcll(who));
+        }
+        if (lane < have) held[lane] = mine;
+        if (lane < top) other[lane] = 0;                       // (fewer keys than `top` so far)
+        wave_sync();
+        for (uint32_t i = lane; i < n + have; i += 64) {
+            const uint64_t k = i < n ? more[i] : held[i - n];
+            if (!k) continue;
+            const uint32_t at = larger(more, 0, n, 1, k) + larger(held, 0, have, 1, k);
+            if (at < top) other[at] = k;
+        }
+        wave_sync();
+        mine = lane < top ? other[lane] : 0;
+        wave_sync();
+        have = top;
+        least = lane_value(mine, int(top) - 1);
+    }
+};
+
+// A wave a part: no barriers.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLT) logprobs_wave_kernel(LpArgs a) {
+    extern __shared__ uint64_t wave_lds[];
+    const uint32_t unit_of = __builtin_amdgcn_readfirstlane(blockIdx.x * kLWaves + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
+    const uint32_t row = unit_of / a.parts, part = unit_of % a.parts;
+    if (row >= a.rows) return;
+    const uint32_t from = part * a.part_len, to = min(a.vocab, from + a.part_len);
+    const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
+    const float unit = a.scale * kLog2e;
+    constexpr uint32_t STEP = 64 * kPiece;
+    Sums sum = {-INFINITY, 0.0f, 0.0f};
+    TopWave best(wave_lds + (threadIdx.x >> 6) * wave_keys(a.top));
+    Raw8<T> raw[2];
+    load_step<64>(x, from, to, raw);
+    for (uint32_t c0 = from; c0 < to; c0 += STEP) {
+        float v[kPiece];
+        raw[0].get(v);
+        raw[1].get(v + 8);
+        if (c0 + STEP < to) load_step<64>(x, c0 + STEP, to, raw);
+        [[maybe_unused]] const float top = add_step(v, unit, sum);
+        if constexpr (TOP) {
+            const bool passes = best.least == 0 ? c0 + lane * 8 < to : order_of(top) >= uint32_t(best.least >> 32);
+            best.round(a.top, passes, v, [&](int i) {
+                const uint32_t j = c0 + ((i / 8) * 64 + lane) * 8 + i % 8;
+                return j < to ? key_of(v[i], j) : 0;
+            });
+        }
+    }
+    sum = join_wave(sum, unit);
+    if (a.parts == 1) {
+        if (lane == 0) finish_row<T>(a, row, sum);
+        if constexpr (TOP) {
+            if (lane < a.top) put_top(a, row, lane, best.mine, row_of_sums(sum));
+        }
+    } else {
+        if (lane == 0) a.sums[unit_of] = f32x4{sum.m, sum.s, sum.t, 0.0f};
+        if constexpr (TOP) {
+            if (lane < a.top) a.keys[uint64_t(unit_of) * a.top + lane] = best.mine;
         }
     }
 }
@@ -326,7 +479,7 @@ __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
                 for (uint32_t u = 0; u < MOST; ++u) b = max(b, keys[u]);
                 return b;
             },
-            [&](auto&& put) {
+            [&](uint64_t, auto&& put) {
 #pragma unroll
                 for (uint32_t u = 0; u < MOST; ++u) put(keys[u]);
             });
@@ -419,25 +572,38 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
     a.logits = logits, a.targets = targets, a.logp = logp, a.lse = lse, a.entropy = entropy;
     a.top_values = top_values, a.top_ids = top_ids, a.stride = rows > 1 ? stride : 0;
     a.rows = uint32_t(rows), a.vocab = uint32_t(vocab), a.top = top, a.wide_ids = targets_bytes == 8, a.scale = scale;
-    // Parts so that at least 1024 workgroups run, none shorter than a step (8 x
-    // 151936: 6.5 us in 38 parts, 8.2 in 10; 256 rows 21.1 us, in 512 workgroups
-    // 24.2).  Between one and two times the 2048 that run at once a second part
-    // fills the last round (2500 rows 124 us, whole 139; with `top`, which a part
-    // costs more than that, 187 whole and 209).
-    const uint64_t target = rows > 2048 && rows < 4096 && !top ? 4096 : 1024, step = kLT * kPiece;
-    uint64_t parts = std::max<uint64_t>(1, std::min<uint64_t>((target + rows - 1) / rows, (vocab + step - 1) / step));
+    // Who takes a row (us; `top` 0 and 20).  A wave, where a row is one step of
+    // it (16384 x 1000: 12 and 29, a workgroup 33 and 95) or rows fill the GPU
+    // (4096 x 16384: 28 and 57, a workgroup 29 and 67; of longest rows only with
+    // `top`: 4096 x 151936 214 and 273, a workgroup 205 and 373); several, so that
+    // 4096 run, where fewer rows are long (1024 x 151936: 57 and 107, workgroups
+    // 61 and 131; but 1024 x 32000 18 and 48, workgroups 16 and 40).  Else at
+    // least 1024 workgroups, each with a step or more (8 x 151936: 6.5 and 14 in
+    // 38 parts, 8.2 and 27 in 10; 256 rows 21, in 512 workgroups 24).
+    const bool is_long = vocab >= 65536;
+    bool by_wave = vocab <= 64 * kPiece;
+    uint64_t parts = 1;
+    if (!by_wave) {
+        by_wave = rows >= 4096 ? top || !is_long : rows >= 1024 && is_long;
+        const uint64_t target = by_wave ? 4096 : 1024, step = kLT * kPiece;
+        parts = std::max<uint64_t>(1, std::min<uint64_t>((target + rows - 1) / rows, (vocab + step - 1) / step));
+    }
     if (top) parts = std::min<uint64_t>(parts, kMostKeys / top);
-    uint64_t len = ((vocab + parts - 1) / parts + 7) / 8 * 8;
+    const uint64_t len = ((vocab + parts - 1) / parts + 7) / 8 * 8;
     parts = (vocab + len - 1) / len;
     a.parts = uint32_t(parts), a.part_len = uint32_t(len);
     a.sums = static_cast<f32x4*>(ws);
     a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kMostParts * sizeof(f32x4));
-    const uint64_t grid = rows * parts;
+    const uint64_t grid = by_wave ? (rows * parts + kLWaves - 1) / kLWaves : rows * parts;
     if (grid * kLT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many rows for one launch");
     with_type(type, [&](auto t) {
         auto go = [&](auto some) {
             constexpr bool TOP = decltype(some)::value;
-            hipLaunchKernelGGL((logprobs_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
+            if (by_wave)
+                hipLaunchKernelGGL((logprobs_wave_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT),
+                                   TOP ? kLWaves * wave_keys(top) * 8 : 0, st, a);
+            else
+                hipLaunchKernelGGL((logprobs_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
             if (parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<decltype(t), TOP>), dim3(a.rows), dim3(kLT), 0, st, a);
         };
         top ? go(std::true_type()) : go(std::false_type());

@@ -88,7 +88,37 @@ __global__ void __launch_bounds__(kRT) rows_combine_kernel(RowArgs a) {
     }
 }
 
-// A wave for each token; a lane's columns lie 512 apart.
+// Part of a pair's row: WAVES waves of a workgroup have columns 8 (lane + 64
+// wave), the next lie 512 WAVES further.  Returns the lane's share of dw.
+template <typename TD, typename TX, typename TG, bool FAR, uint32_t WAVES>
+__device__ __forceinline__ float pair_grad(const RowArgs& a, const TD* dy, const TX* x, TG* dx, float w, uint32_t first) {
+    float dot = 0.0f;
+#pragma unroll 2
+    for (uint32_t c = first; c < a.width; c += 512 * WAVES) {
+        const int n = int(min(8u, a.width - c));
+        Raw8<TD> rd;
+        Raw8<TX> rx;
+        float d[8], v[8];
+        if (n == 8) {
+            rd.load(dy + c);
+            rx.load_once(x + c);
+        } else {
+            rd.load_some(dy + c, n, 0);
+            rx.load_some(x + c, n, 0);
+        }
+        rd.get(d);
+        rx.get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dot = __fmaf_rn(d[i], v[i], dot);
+            d[i] *= w;
+        }
+        n == 8 ? store8<FAR>(dx + c, d) : store_some(dx + c, d, n);
+    }
+    return dot;
+}
+
+// A wave for each token, which reads dy once (from then on the cache has it).
 template <typename TD, typename TX, typename TG, bool FAR>
 __global__ void __launch_bounds__(kRT) rows_combine_grad_kernel(RowArgs a) {
     const uint32_t at = blockIdx.x * (kRT / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63u;
@@ -98,34 +128,77 @@ __global__ void __launch_bounds__(kRT) rows_combine_grad_kernel(RowArgs a) {
         const uint64_t pair = uint64_t(at) * a.k + j;
         const uint32_t s = uint32_t(a.slots[pair]);
         float dot = 0.0f;
-        if (s < a.n_slots) {
-            const float w = a.weights[pair];
-            const TX* x = static_cast<const TX*>(a.b) + uint64_t(s) * a.b_stride;
-            TG* dx = static_cast<TG*>(a.y) + uint64_t(s) * a.y_stride;
-            for (uint32_t c = lane * 8; c < a.width; c += 512) {
-                const int n = int(min(8u, a.width - c));
-                Raw8<TD> rd;
-                Raw8<TX> rx;
-                float d[8], v[8];
-                if (n == 8) {
-                    rd.load(dy + c);
-                    rx.load_once(x + c);
-                } else {
-                    rd.load_some(dy + c, n, 0);
-                    rx.load_some(x + c, n, 0);
-                }
-                rd.get(d);
-                rx.get(v);
+        if (s < a.n_slots)
+            dot = pair_grad<TD, TX, TG, FAR, 1>(a, dy, static_cast<const TX*>(a.b) + uint64_t(s) * a.b_stride,
+                                                static_cast<TG*>(a.y) + uint64_t(s) * a.y_stride, a.weights[pair], lane * 8);
+        dot = lanes_sum<64>(dot);
+        if (lane == 0) a.dweights[pair] = dot;
+    }
+}
+
+// Narrow rows: LANES lanes hold a token's row of dy, several tokens share a wave,
+// and kRows rows of x are on their way together.
+template <typename TD, typename TX, typename TG, int LANES>
+__global__ void __launch_bounds__(kRT) rows_combine_grad_narrow_kernel(RowArgs a) {
+    const uint32_t at = blockIdx.x * (kRT / LANES) + threadIdx.x / LANES, c = threadIdx.x % LANES * 8;
+    const bool live = at < a.tokens;
+    const uint64_t safe = live ? at : 0;
+    const int n = c < a.width ? int(min(8u, a.width - c)) : 0;
+    Raw8<TD> rd;
+    float d[8];
+    const TD* dy = static_cast<const TD*>(a.a) + safe * a.a_stride + c;
+    n == 8 ? rd.load_once(dy) : rd.load_some(dy, n, 0);
+    rd.get(d);
+    for (uint32_t j0 = 0; j0 < a.k; j0 += kRows) {
+        Raw8<TX> rx[kRows];
+        uint32_t s[kRows];
+#pragma unroll
+        for (uint32_t u = 0; u < kRows; ++u) {
+            s[u] = live && j0 + u < a.k ? uint32_t(a.slots[safe * a.k + j0 + u]) : ~0u;
+            if (s[u] >= a.n_slots) continue;
+            const TX* x = static_cast<const TX*>(a.b) + uint64_t(s[u]) * a.b_stride + c;
+            n == 8 ? rx[u].load_once(x) : rx[u].load_some(x, n, 0);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kRows; ++u) {
+            if (j0 + u >= a.k) break;
+            const uint64_t pair = safe * a.k + j0 + u;
+            float dot = 0.0f;
+            if (s[u] < a.n_slots) {
+                const float w = a.weights[pair];
+                float v[8], g[8];
+                rx[u].get(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     dot = __fmaf_rn(d[i], v[i], dot);
-                    d[i] *= w;
+                    g[i] = d[i] * w;
                 }
-                n == 8 ? store8<FAR>(dx + c, d) : store_some(dx + c, d, n);
+                TG* dx = static_cast<TG*>(a.y) + uint64_t(s[u]) * a.y_stride + c;
+                n == 8 ? store8(dx, g) : store_some(dx, g, n);
             }
+            dot = lanes_sum<LANES>(dot);
+            if (c == 0 && live) a.dweights[pair] = dot;
         }
-        dot = lanes_sum<64>(dot);
-        if (lane == 0) a.dweights[pair] = dot;
+    }
+}
+
+// A workgroup for each pair, where tokens alone do not fill the GPU.
+template <typename TD, typename TX, typename TG>
+__global__ void __launch_bounds__(kRT) rows_combine_grad_pair_kernel(RowArgs a) {
+    __shared__ float of_wave[kRT / 64];
+    const uint32_t pair = blockIdx.x;
+    const uint32_t s = uint32_t(a.slots[pair]);
+    float dot = 0.0f;
+    if (s < a.n_slots)
+        dot = pair_grad<TD, TX, TG, false, kRT / 64>(a, static_cast<const TD*>(a.a) + uint64_t(pair / a.k) * a.a_stride,
+                                                   static_cast<const TX*>(a.b) + uint64_t(s) * a.b_stride,
+                                                   static_cast<TG*>(a.y) + uint64_t(s) * a.y_stride, a.weights[pair], threadIdx.x * 8);
+    dot = lanes_sum<64>(dot);
+    if ((threadIdx.x & 63u) == 0) of_wave[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (uint32_t w = 1; w < kRT / 64; ++w) dot += of_wave[w];
+        a.dweights[pair] = dot;
     }
 }
 
@@ -222,14 +295,30 @@ int32_t combine_rows_grad(const void* dy, uint32_t dy_type, uint64_t dy_stride, 
     a.a_stride = dy_stride, a.b_stride = n_slots > 1 ? x_stride : 0, a.y_stride = n_slots > 1 ? dx_stride : 0;
     a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
     uint32_t grid;
-    if ((rc = row_grid(tokens, kRT / 64, &grid))) return rc;
+    // Wide rows of few tokens by pair (256 tokens, 8 pairs of 2048 bf16: 5.6 us, a
+    // wave a token 20; 2048 tokens, 8 pairs: even; 16384: 239 and 235).
+    const bool narrow = width <= 512, by_pair = !narrow && tokens < 2048;
+    uint32_t lanes = 8;
+    while (narrow && lanes * 8 < width) lanes *= 2;
+    if ((rc = by_pair ? row_grid(tokens * k, 1, &grid) : row_grid(tokens, narrow ? kRT / lanes : kRT / 64, &grid))) return rc;
     with_type(dy_type, [&](auto td) {
         with_type(x_type, [&](auto tx) {
             with_type(dx_type, [&](auto tg) {
-                with_far(uint64_t(n_slots) * width * sizeof(tg), [&](auto far) {
-                    hipLaunchKernelGGL((rows_combine_grad_kernel<decltype(td), decltype(tx), decltype(tg), decltype(far)::value>),
-                                       dim3(grid), dim3(kRT), 0, st, a);
-                });
+                typedef decltype(td) TD;
+                typedef decltype(tx) TX;
+                typedef decltype(tg) TG;
+                const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kRT), 0, st, a); };
+                if (narrow) {
+                    lanes == 8    ? go(rows_combine_grad_narrow_kernel<TD, TX, TG, 8>)
+                    : lanes == 16 ? go(rows_combine_grad_narrow_kernel<TD, TX, TG, 16>)
+                    : lanes == 32 ? go(rows_combine_grad_narrow_kernel<TD, TX, TG, 32>)
+                                  : go(rows_combine_grad_narrow_kernel<TD, TX, TG, 64>);
+                } else if (by_pair) {
+                    go(rows_combine_grad_pair_kernel<TD, TX, TG>);
+                } else {
+                    with_far(uint64_t(n_slots) * width * sizeof(tg),
+                             [&](auto far) { go(rows_combine_grad_kernel<TD, TX, TG, decltype(far)::value>); });
+                }
             });
         });
     });
