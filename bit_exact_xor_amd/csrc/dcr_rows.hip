@@ -24,68 +24,72 @@ struct RowArgs {
     float* dweights;
     uint64_t a_stride, b_stride, y_stride;
     uint32_t tokens, width, k, n_slots;
-    uint32_t lanes_log2;   // lanes that share a token
+    uint32_t pieces;       // of eight columns, of a row
 };
+
+// The thread's token and the first of its eight columns; false behind the end.
+// Threads are dealt to pieces of eight columns one after the other, whatever the
+// width, so none is without work in the middle of a row.
+__device__ __forceinline__ bool piece_of(const RowArgs& a, uint32_t* at, uint32_t* c) {
+    const uint32_t i = blockIdx.x * kRT + threadIdx.x;
+    *at = i / a.pieces;
+    *c = (i - *at * a.pieces) * 8;
+    return *at < a.tokens;
+}
 
 // One thread holds eight columns of a token and takes them to every slot.
 template <typename TX, typename TY, bool FAR>
 __global__ void __launch_bounds__(kRT) rows_dispatch_kernel(RowArgs a) {
-    const uint32_t at = blockIdx.x * (kRT >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-    if (at >= a.tokens) return;
-    const uint32_t step = 8u << a.lanes_log2;
+    uint32_t at, c;
+    if (!piece_of(a, &at, &c)) return;
     const int32_t* slots = a.slots + uint64_t(at) * a.k;
-    const TX* x = static_cast<const TX*>(a.a) + uint64_t(at) * a.a_stride;
-    for (uint32_t c = (threadIdx.x & ((1u << a.lanes_log2) - 1)) * 8; c < a.width; c += step) {
-        const int n = int(min(8u, a.width - c));
-        Raw8<TX> r;
-        float v[8];
-        n == 8 ? r.load_once(x + c) : r.load_some(x + c, n, 0);
-        r.get(v);
-        for (uint32_t j = 0; j < a.k; ++j) {
-            const uint32_t s = uint32_t(slots[j]);
-            if (s >= a.n_slots) continue;
-            TY* y = static_cast<TY*>(a.y) + uint64_t(s) * a.y_stride + c;
-            n == 8 ? store8<FAR>(y, v) : store_some(y, v, n);
-        }
+    const TX* x = static_cast<const TX*>(a.a) + uint64_t(at) * a.a_stride + c;
+    const int n = int(min(8u, a.width - c));
+    Raw8<TX> r;
+    float v[8];
+    n == 8 ? r.load_once(x) : r.load_some(x, n, 0);
+    r.get(v);
+    for (uint32_t j = 0; j < a.k; ++j) {
+        const uint32_t s = uint32_t(slots[j]);
+        if (s >= a.n_slots) continue;
+        TY* y = static_cast<TY*>(a.y) + uint64_t(s) * a.y_stride + c;
+        n == 8 ? store8<FAR>(y, v) : store_some(y, v, n);
     }
 }
 
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kRT) rows_combine_kernel(RowArgs a) {
-    const uint32_t at = blockIdx.x * (kRT >> a.lanes_log2) + (threadIdx.x >> a.lanes_log2);
-    if (at >= a.tokens) return;
-    const uint32_t step = 8u << a.lanes_log2;
+    uint32_t at, c;
+    if (!piece_of(a, &at, &c)) return;
     const int32_t* slots = a.slots + uint64_t(at) * a.k;
     const float* weights = a.weights + uint64_t(at) * a.k;
-    TY* y = static_cast<TY*>(a.y) + uint64_t(at) * a.y_stride;
-    for (uint32_t c = (threadIdx.x & ((1u << a.lanes_log2) - 1)) * 8; c < a.width; c += step) {
-        const int n = int(min(8u, a.width - c));
-        float sum[8] = {};
-        // four rows on their way together
-        for (uint32_t j0 = 0; j0 < a.k; j0 += kRows) {
-            Raw8<TX> r[kRows];
-            float w[kRows];
-            bool has[kRows];
+    const int n = int(min(8u, a.width - c));
+    float sum[8] = {};
+    // kRows rows on their way together
+    for (uint32_t j0 = 0; j0 < a.k; j0 += kRows) {
+        Raw8<TX> r[kRows];
+        float w[kRows];
+        bool has[kRows];
 #pragma unroll
-            for (uint32_t u = 0; u < kRows; ++u) {
-                const uint32_t s = j0 + u < a.k ? uint32_t(slots[j0 + u]) : ~0u;
-                has[u] = s < a.n_slots;
-                if (!has[u]) continue;
-                w[u] = a.weights ? weights[j0 + u] : 1.0f;
-                const TX* x = static_cast<const TX*>(a.a) + uint64_t(s) * a.a_stride + c;
-                n == 8 ? r[u].load_once(x) : r[u].load_some(x, n, 0);
-            }
-#pragma unroll
-            for (uint32_t u = 0; u < kRows; ++u) {
-                if (!has[u]) continue;
-                float v[8];
-                r[u].get(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(w[u], v[i], sum[i]);
-            }
+        for (uint32_t u = 0; u < kRows; ++u) {
+            const uint32_t s = j0 + u < a.k ? uint32_t(slots[j0 + u]) : ~0u;
+            has[u] = s < a.n_slots;
+            if (!has[u]) continue;
+            w[u] = a.weights ? weights[j0 + u] : 1.0f;
+            const TX* x = static_cast<const TX*>(a.a) + uint64_t(s) * a.a_stride + c;
+            n == 8 ? r[u].load_once(x) : r[u].load_some(x, n, 0);
         }
-        n == 8 ? store8(y + c, sum) : store_some(y + c, sum, n);
+#pragma unroll
+        for (uint32_t u = 0; u < kRows; ++u) {
+            if (!has[u]) continue;
+            float v[8];
+            r[u].get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(w[u], v[i], sum[i]);
+        }
     }
+    TY* y = static_cast<TY*>(a.y) + uint64_t(at) * a.y_stride + c;
+    n == 8 ? store8(y, sum) : store_some(y, sum, n);
 }
 
 // Part of a pair's row: WAVES waves of a workgroup have columns 8 (lane + 64
@@ -210,23 +214,17 @@ int32_t check_rows(uint64_t tokens, uint64_t width, uint32_t k, uint64_t n_slots
     return DCR_OK;
 }
 
-// the least power of two of lanes that holds a row in one step, at most a workgroup
-uint32_t row_lanes_log2(uint64_t width) {
-    uint32_t l = 0;
-    while (l < 8 && (uint64_t(8) << l) < width) ++l;
-    return l;
-}
-
-// f(whether so many bytes of results go past the caches).  Written past them the
-// rows of 131072 slots of 2048 bf16 take 85 us, else 96; rows that fit are left
-// to the product that reads them next.
+// f(whether so many bytes of results go past the caches: more than the last of
+// them, 256 MiB, holds).  16384 tokens there and back with 8 rows of 2048 bf16
+// 220 us, else 237; their gradient 234 and 246.  Below it they stay for the
+// product that reads them next (4096 tokens' gradient 52 us, past the caches 63).
 template <typename F>
 void with_far(uint64_t bytes, F&& f) {
-    bytes > (uint64_t(64) << 20) ? f(std::true_type()) : f(std::false_type());
+    bytes > (uint64_t(256) << 20) ? f(std::true_type()) : f(std::false_type());
 }
 
-int32_t row_grid(uint64_t tokens, uint32_t per_group, uint32_t* grid) {
-    const uint64_t g = (tokens + per_group - 1) / per_group;
+int32_t row_grid(uint64_t units, uint32_t per_group, uint32_t* grid) {
+    const uint64_t g = (units + per_group - 1) / per_group;
     if (g * kRT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many rows for one launch");
     *grid = uint32_t(g);
     return DCR_OK;
@@ -242,9 +240,9 @@ int32_t dispatch_rows(const void* x, uint32_t x_type, uint64_t x_stride, uint64_
     RowArgs a{};
     a.a = x, a.y = y, a.slots = slots, a.a_stride = x_stride, a.y_stride = n_slots > 1 ? y_stride : 0;
     a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
-    a.lanes_log2 = row_lanes_log2(width);
+    a.pieces = uint32_t((width + 7) / 8);
     uint32_t grid;
-    if ((rc = row_grid(tokens, kRT >> a.lanes_log2, &grid))) return rc;
+    if ((rc = row_grid(tokens * a.pieces, kRT, &grid))) return rc;
     with_type(x_type, [&](auto tx) {
         with_type(y_type, [&](auto ty) {
             with_far(uint64_t(n_slots) * width * sizeof(ty), [&](auto far) {
@@ -268,9 +266,9 @@ int32_t combine_rows(const void* x, uint32_t x_type, uint64_t x_stride, uint64_t
     RowArgs a{};
     a.a = x, a.y = y, a.slots = slots, a.weights = weights, a.a_stride = n_slots > 1 ? x_stride : 0, a.y_stride = y_stride;
     a.tokens = uint32_t(tokens), a.width = uint32_t(width), a.k = k, a.n_slots = uint32_t(n_slots);
-    a.lanes_log2 = row_lanes_log2(width);
+    a.pieces = uint32_t((width + 7) / 8);
     uint32_t grid;
-    if ((rc = row_grid(tokens, kRT >> a.lanes_log2, &grid))) return rc;
+    if ((rc = row_grid(tokens * a.pieces, kRT, &grid))) return rc;
     with_type(x_type, [&](auto tx) {
         with_type(y_type, [&](auto ty) {
             hipLaunchKernelGGL((rows_combine_kernel<decltype(tx), decltype(ty)>), dim3(grid), dim3(kRT), 0, st, a);
