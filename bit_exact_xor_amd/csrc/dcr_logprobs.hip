@@ -20,7 +20,8 @@ namespace {
 constexpr uint32_t kLT = 256;                // threads of a workgroup
 constexpr uint32_t kLWaves = kLT / 64;
 constexpr uint32_t kPiece = 16;              // logits of a thread in a step
-constexpr uint32_t kMostParts = 1 << 13;     // parts of all rows, where rows are split
+constexpr uint32_t kMostParts = 4096;        // parts of all rows, where rows are split
+static_assert(kMostParts * (16 + 8 * DCR_LOGPROBS_MAX_TOP) <= DCR_STEP_WORKSPACE_BYTES, "sums and keys of all parts");
 constexpr uint32_t kMostKeys = 2048;         // keys of the parts of a row
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -585,10 +586,11 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
     uint64_t parts = 1;
     if (!by_wave) {
         by_wave = rows >= 4096 ? top || !is_long : rows >= 1024 && is_long;
-        const uint64_t target = by_wave ? 4096 : 1024, step = kLT * kPiece;
-        parts = std::max<uint64_t>(1, std::min<uint64_t>((target + rows - 1) / rows, (vocab + step - 1) / step));
+        const uint64_t step = kLT * kPiece;
+        parts = std::min<uint64_t>(by_wave ? 4096 / rows : (1024 + rows - 1) / rows, (vocab + step - 1) / step);
+        if (top) parts = std::min<uint64_t>(parts, kMostKeys / top);
+        parts = std::max<uint64_t>(1, std::min<uint64_t>(parts, kMostParts / rows));
     }
-    if (top) parts = std::min<uint64_t>(parts, kMostKeys / top);
     const uint64_t len = ((vocab + parts - 1) / parts + 7) / 8 * 8;
     parts = (vocab + len - 1) / len;
     a.parts = uint32_t(parts), a.part_len = uint32_t(len);

@@ -236,3 +236,52 @@ def test_rows_past_32_bits():
     dcr.dcr_logprobs_grad(x, t, lse, one, x)
     got = 1 - torch.exp(want[2, 4099])
     assert abs(float(x[2, 4099]) - float(got)) < 2.0 ** -8 and float(x[2, 0]) < 0
+
+
+# rows and vocabulary so that a row goes to one wave, to several, to one workgroup, to several
+SPLITS = [(4100, 1500), (4097, 66000), (1100, 65600), (2048, 65536), (2100, 65544), (4095, 65537), (1500, 9001), (1023, 70000)]
+
+
+@pytest.mark.parametrize("rows,vocab", SPLITS)
+def test_every_split(rows, vocab):
+    """Against 64-bit arithmetic on the GPU, with the workspace at the end of a larger buffer: nothing is written behind it.
+    (Tolerances as above, with log p and the entropy below 2^5.)"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    x = torch.empty(rows, vocab + 8, dtype=torch.bfloat16, device="cuda")[:, :vocab]
+    for part in x.split(512):
+        part.copy_(torch.randn(part.shape, device="cuda", generator=g) * 3)
+    x[3] = -INF
+    x[5, : vocab // 2] = -INF
+    x[7] = x[7].sort().values                     # rising
+    x[9] = 1.0                                    # all alike
+    t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    buffer = torch.full((dcr.STEP_WORKSPACE_BYTES + (1 << 20),), 0xAB, dtype=torch.uint8, device="cuda")
+    ws = buffer[: dcr.STEP_WORKSPACE_BYTES]
+    for top in (0, 20, 64):
+        out = [torch.full((rows,), 77.0, device="cuda") for _ in range(3)]
+        ids = torch.full((rows, top), -5, dtype=torch.int32, device="cuda") if top else None
+        vals = torch.full((rows, top), 77.0, device="cuda") if top else None
+        dcr.dcr_logprobs(x, t, *out, ids, vals, workspace=ws)
+        assert (buffer[dcr.STEP_WORKSPACE_BYTES:] == 0xAB).all()
+        for i in range(0, rows, 256):
+            y = x[i:i + 256].double()
+            lse = torch.logsumexp(y, 1)
+            lp = torch.where(torch.isneginf(lse)[:, None], -INF, y - lse[:, None])
+            ent = -(lp.exp() * torch.where(lp.exp() > 0, lp, 0.0)).sum(1)
+            tol = (vocab / 256 + 40) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -21
+            mine = lp.gather(1, t[i:i + 256, None])[:, 0]
+            for got, want, wide in ((out[0], mine, 2.0 ** -17), (out[1], lse, 2.0 ** -18), (out[2], ent, 64 * tol)):
+                got = got[i:i + 256].double()
+                none = torch.isneginf(want)
+                assert torch.equal(torch.isneginf(got), none)
+                assert ((got - want)[~none].abs() <= tol + wide).all()
+            if top:
+                # logits first, then indices: the lowest of equals (both exact in 64 bits)
+                key = torch.where(torch.isneginf(y), -1e9, y * 2.0 ** 24) * 2.0 ** 20 - torch.arange(vocab, device="cuda", dtype=torch.float64)
+                best = key.topk(top, 1).indices
+                assert torch.equal(ids[i:i + 256].long(), best), (i, top)
+                want = lp.gather(1, best)
+                none = torch.isneginf(want)
+                got = vals[i:i + 256].double()
+                assert torch.equal(torch.isneginf(got), none) and ((got - want)[~none].abs() <= tol + 2.0 ** -17).all()
