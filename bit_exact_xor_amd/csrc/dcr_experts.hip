@@ -705,7 +705,8 @@ void with_lanes(uint32_t n, F&& f) {
 }
 
 int32_t check_select(uint64_t rows, uint32_t experts, uint32_t k, uint32_t score, uint32_t options, float scale) {
-    if (rows >= (uint64_t(1) << 31) || rows * k >= (uint64_t(1) << 31)) return step_fail(DCR_E_INVAL, "2^31 rows or pairs or more");
+    // (a launch takes 2^32 threads, a row at most 64 of them)
+    if (rows >= (uint64_t(1) << 26) || rows * k >= (uint64_t(1) << 31)) return step_fail(DCR_E_INVAL, "2^26 rows, 2^31 pairs or more");
     if (!experts || experts > DCR_EXPERTS_MAX) return step_fail(DCR_E_INVAL, "experts are not 1 .. 1024");
     if (!k || k > DCR_EXPERTS_MAX_K || k > experts) return step_fail(DCR_E_INVAL, "k is not 1 .. 64 and at most the experts");
     if (score != DCR_SCORE_SOFTMAX && score != DCR_SCORE_SIGMOID) return step_fail(DCR_E_INVAL, "unknown score");
@@ -739,7 +740,7 @@ int32_t select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows
     with_type(type, [&](auto t) {
         with_lanes(experts, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
-            const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);
+            const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
             hipLaunchKernelGGL((experts_select_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET),
                                ROWS * select_lds(experts, k), st, a);
         });
@@ -764,7 +765,7 @@ int32_t select_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t
     with_type(type, [&](auto t) {
         with_lanes(experts, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
-            const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);
+            const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
             hipLaunchKernelGGL((experts_select_grad_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET), 0, st, a);
         });
     });

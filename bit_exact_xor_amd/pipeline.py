@@ -335,6 +335,8 @@ class Fp4Refit:
         import torch
         if [p.numel() for p in tensors.params] != [t.rows * t.cols for t in self.next]:
             raise ValueError("step: one parameter of each weight's size expected")
+        if tensors.index != self.device.index:
+            raise ValueError(f"step: parameters on cuda:{tensors.index}, weights on {self.device}")
         self.recover()
         with torch.cuda.device(self.device):
             dcr.dcr_adamw_step(tensors, number, **hyper)

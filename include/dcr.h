@@ -697,8 +697,9 @@ enum { DCR_EXPERTS_RENORMALIZE = 1 };
 #define DCR_EXPERTS_MAX_GROUPS 64
 
 /* The k best experts of each row of a router's logits, and their weights.
- *   logits      rows x experts (DCR_F32 or DCR_BF16), 1 .. 1024 experts; an
- *               expert at -infinity is shut: it has score 0 and is not chosen
+ *   logits      rows x experts (DCR_F32 or DCR_BF16), 1 .. 1024 experts, fewer
+ *               than 2^26 rows and (rows * k) 2^31 pairs; an expert at
+ *               -infinity is shut: it has score 0 and is not chosen
  *   bias        NULL, or [experts] fp32, added to the scores for the choice
  *               alone (it balances the experts' load, the weights do not see it)
  *   score       s = softmax over the row's experts, or sigmoid of each logit
@@ -712,8 +713,9 @@ enum { DCR_EXPERTS_RENORMALIZE = 1 };
  *               the lowest index of equals first; -1 where fewer than k are open
  *   weights     [rows, k] fp32: scale * s, over the sum of the row's chosen s
  *               where renormalised; 0 where the id is -1
- * 1 <= k <= min(64, experts).  The choice is that of 64-bit arithmetic; without
- * a bias experts are compared by their logits.  A NaN among the values compared
+ * 1 <= k <= min(64, experts).  The choice is that of 64-bit arithmetic (sums that
+ * differ by less than 2^-42 of themselves count as equal); without a bias experts
+ * are compared by their logits.  A NaN among the values compared
  * counts as the largest, and makes weights NaN. */
 int32_t dcr_experts_select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint32_t experts,
                            const float* bias, uint32_t score, uint32_t groups, uint32_t top_groups, uint32_t options,
@@ -808,7 +810,8 @@ int32_t dcr_logprobs_grad(const void* logits, uint32_t type, uint64_t stride, ui
  *               weights that dcr_encode compares)
  *   numel       elements, 0 upwards
  *   first       index of the first element to the dither: a shard takes that of
- *               its first element in the whole tensor
+ *               its first element in the whole tensor, and shards that are cut
+ *               between blocks give the bits of the whole tensor
  *   flags       0 or DCR_ADAMW_NO_DECAY
  * All buffers but the scales are 16-byte aligned; none that is written may
  * overlap another. */

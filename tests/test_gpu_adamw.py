@@ -248,3 +248,33 @@ def test_refusals_of_tensors():
         with pytest.raises(ValueError):
             dcr.dcr_adamw_step(T, 1, **kw)
     assert (a == 0).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("pt,gt", [("fp32", "bf16"), ("bf16", "fp32")])
+def test_many_elements(bits, pt, gt):
+    """More elements than the caches hold, and more than take short steps: the bits that slices of them by themselves give."""
+    n = 12_000_031 if bits == 32 else 24_000_031
+    g = torch.Generator(device="cuda")
+    g.manual_seed(bits)
+    p = torch.randn(n, device="cuda", generator=g).to(TYPES[pt])
+    grad = (torch.randn(n, device="cuda", generator=g) * 1e-2).to(TYPES[gt])
+    copy = lambda m: [torch.empty(m, dtype=torch.bfloat16, device="cuda")] if pt == "fp32" else None  # noqa: E731
+    cuts = [(0, 5000), (4096 * 1000, 4096 * 1000 + 70000), (n // 32 * 32 - 32000, n)]
+    big = dcr.AdamWTensors([p.clone()], [grad], bits=bits, copies=copy(n))
+    small = [dcr.AdamWTensors([p[a:b].clone()], [grad[a:b].clone()], bits=bits, copies=copy(b - a), first=[a]) for a, b in cuts]
+    for t in (1, 2):
+        dcr.dcr_adamw_step(big, t, dither=9, weight_decay=0.1)
+        for s in small:
+            dcr.dcr_adamw_step(s, t, dither=9, weight_decay=0.1)
+    for s, (a, b) in zip(small, cuts):
+        # (8 bits: a block that a slice cuts has its scale from other elements; whole blocks are compared)
+        whole = bits == 32 or b == n
+        b = b if whole else a + (b - a) // 32 * 32
+        assert torch.equal(big.params[0][a:b], s.params[0][:b - a])
+        if pt == "fp32":
+            assert torch.equal(big.copies[0][a:b], s.copies[0][:b - a])
+        for x, y in ((big.m, s.m), (big.v, s.v)):
+            assert torch.equal(x[0][a:b].view(torch.uint8), y[0][:b - a].view(torch.uint8))
+        if bits == 8:
+            assert torch.equal(big.m_scales[0][a // 32: -(-b // 32)], s.m_scales[0][: -(-(b - a) // 32)])

@@ -333,3 +333,47 @@ def test_offsets_past_32_bits():
     assert (x[2] == 8).all() and (x[1] == 2).all()
     ids, w = run_select(x, 3)
     assert torch.equal(ids.cpu(), torch.tensor([[0, 1, 2]] * 3, dtype=torch.int32)) and (w == 1 / 64).all()
+
+
+@pytest.mark.parametrize("tokens,width,k", [(2100, 520, 2), (2048, 4096, 18), (2047, 513, 3), (4096, 512, 2), (3000, 24, 5)])
+def test_rows_of_many_tokens(tokens, width, k):
+    """The forms for many tokens (a wave a token, narrow rows, results past the caches) against 32-bit torch on the GPU:
+    copies are equal; sums of k products within (k + 2) 2^-24, of `width` within (width / 64 + 16) 2^-24 of the sums of
+    magnitudes on both sides, bf16 results within half a step more."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens)
+    n = tokens * k
+    slots = torch.randperm(n, device="cuda", generator=g).int().view(tokens, k)
+    slots[::50] = -1
+    has = slots >= 0
+    at = slots.clamp(min=0).long()
+    x = torch.randn(tokens, width, device="cuda", generator=g).bfloat16()
+    sent = torch.full((n, width), 3.0, dtype=torch.bfloat16, device="cuda")
+    dcr.dcr_experts_dispatch(x, slots, sent)
+    for j in range(k):
+        assert torch.equal(sent[at[has[:, j], j]], x[has[:, j]])
+    untouched = torch.ones(n, dtype=torch.bool, device="cuda")
+    untouched[at[has]] = False
+    assert (sent[untouched] == 3).all()
+    z = torch.randn(n, width, device="cuda", generator=g).bfloat16()
+    w = torch.randn(tokens, k, device="cuda", generator=g)
+    y = torch.empty_like(x)
+    dcr.dcr_experts_combine(z, slots, w, y)
+    want, most = torch.zeros(tokens, width, device="cuda"), torch.zeros(tokens, width, device="cuda")
+    for j in range(k):
+        term = torch.where(has[:, j, None], w[:, j, None] * z[at[:, j]].float(), 0.0)
+        want += term
+        most += term.abs()
+    tol = 2 * (k + 2) * 2.0 ** -24 * most
+    assert ((y.float() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all()
+    dy = torch.randn(tokens, width, device="cuda", generator=g).bfloat16()
+    dz, dw = torch.full_like(z, 3.0), torch.full((tokens, k), 77.0, device="cuda")
+    dcr.dcr_experts_combine_grad(dy, z, slots, w, dz, dw)
+    assert (dz[untouched] == 3).all()
+    for j in range(k):
+        h = has[:, j]
+        a, b = at[h, j], dy[h].float()
+        assert torch.equal(dz[a], (w[h, j, None] * b).bfloat16())
+        terms = b * z[a].float()
+        assert ((dw[h, j].double() - terms.double().sum(1)).abs() <= (width / 64 + 17) * 2.0 ** -24 * terms.abs().sum(1)).all()
+        assert (dw[~h, j] == 0).all()
