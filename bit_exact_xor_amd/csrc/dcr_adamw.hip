@@ -7,8 +7,10 @@
 //
 // Bound by memory: everything is read once and written once, 30 bytes an
 // element with fp32 states, bf16 gradients and a bf16 copy, 16.1 with states in
-// 8 bits.  A workgroup takes 4096 consecutive elements of a tensor, so small
-// tensors cost a workgroup each and no launch.
+// 8 bits.  A workgroup takes 512 consecutive elements of a tensor and ends, so
+// small tensors cost a workgroup each and no launch, and what runs at once covers
+// a short stretch of every buffer (176 M elements with fp32 states 803 us; 1024
+// elements 820, in two steps 857; 4096 in four 922).
 //
 // States in 8 bits: blocks of 32 elements under one power of two (an e8m0
 // byte), e4m3 codes; of the second moment the square root is held, whose range
@@ -30,12 +32,12 @@
 namespace dcr {
 namespace {
 
-constexpr uint32_t kAT = 256;                 // threads of a workgroup
-constexpr uint32_t kAChunk = 4096;            // elements of a workgroup at most
+constexpr uint32_t kAT = 128;                 // threads of a workgroup
+constexpr uint32_t kAChunk = 4 * kAT;         // elements of a workgroup
+constexpr uint64_t kAMostGroups = (uint64_t(1) << 32) / kAT - 1;      // of a launch
 constexpr uint32_t kStateBlock = DCR_ADAMW_BLOCK;
 // Tensors of more bytes than this (the last cache holds 256 MiB) go past the
-// caches: 176 M elements with fp32 states 930 us, else 943; 151 M with 8-bit
-// states 454 us, else 466.
+// caches (1 to 3 %).
 constexpr uint64_t kFarBytes = uint64_t(256) << 20;
 
 // what the steps of a call share
@@ -152,105 +154,100 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamA
     const DevAdam t = chunks[blockIdx.x];
     const AdamArgs a = live ? *live : args;
     const float keep = t.no_decay ? 1.0f : a.keep;
-    constexpr uint32_t UNROLL = BITS == 32 ? 2 : 1;
-#pragma unroll UNROLL
-    for (uint32_t u = 0; u < kAChunk / (4 * kAT); ++u) {
-        if (u * kAT * 4 >= t.numel) break;
-        const uint32_t i = (u * kAT + threadIdx.x) * 4;
-        const int n = i < t.numel ? int(min(4u, t.numel - i)) : 0;
-        TP* pp = reinterpret_cast<TP*>(t.param) + i;
-        const TG* gp = reinterpret_cast<const TG*>(t.grad) + i;
-        float p[4], g[4], m[4], v[4], w[4];
+    const uint32_t i = threadIdx.x * 4;
+    const int n = i < t.numel ? int(min(4u, t.numel - i)) : 0;
+    TP* pp = reinterpret_cast<TP*>(t.param) + i;
+    const TG* gp = reinterpret_cast<const TG*>(t.grad) + i;
+    float p[4], g[4], m[4], v[4], w[4];
+    if (n == 4) {
+        load4<FAR>(pp, p);
+        load4<FAR>(gp, g);
+    } else {
+        load4_some(pp, p, n);
+        load4_some(gp, g, n);
+    }
+    if (BITS == 32) {
+        float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
         if (n == 4) {
-            load4<FAR>(pp, p);
-            load4<FAR>(gp, g);
+            load4<FAR>(mp, m);
+            load4<FAR>(vp, v);
         } else {
-            load4_some(pp, p, n);
-            load4_some(gp, g, n);
+            load4_some(mp, m, n);
+            load4_some(vp, v, n);
         }
-        if (BITS == 32) {
-            float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
+    } else {
+        uint32_t mq = 0, vq = 0, mb = 0, vb = 0;
+        if (n) {
             if (n == 4) {
-                load4<FAR>(mp, m);
-                load4<FAR>(vp, v);
-            } else {
-                load4_some(mp, m, n);
-                load4_some(vp, v, n);
-            }
-        } else {
-            uint32_t mq = 0, vq = 0, mb = 0, vb = 0;
-            if (n) {
-                if (n == 4) {
-                    mq = fetch<FAR, uint32_t>(t.m + i);
-                    vq = fetch<FAR, uint32_t>(t.v + i);
-                } else {
-                    for (int j = 0; j < n; ++j) {
-                        mq |= uint32_t(t.m[i + j]) << (8 * j);
-                        vq |= uint32_t(t.v[i + j]) << (8 * j);
-                    }
-                }
-                mb = t.m_scales[i / kStateBlock];
-                vb = t.v_scales[i / kStateBlock];
-            }
-            codes4(mq, mb, m);
-            codes4(vq, vb, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] *= v[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float s = g[j] * a.grad_scale;
-            m[j] = __fmaf_rn(m[j], a.beta1, s * a.new1);
-            v[j] = __fmaf_rn(v[j], a.beta2, s * s * a.new2);
-            w[j] = sqrtf(v[j]);
-            p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] / __fmaf_rn(w[j], a.root, a.eps)));
-        }
-        if (n == 4)
-            save4<FAR>(pp, p);
-        else
-            save4_some(pp, p, n);
-        if (t.copy) n == 4 ? save4<FAR>(t.copy + i, p) : save4_some(t.copy + i, p, n);
-        if (BITS == 32) {
-            float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
-            if (n == 4) {
-                save4<FAR>(mp, m);
-                save4<FAR>(vp, v);
-            } else {
-                save4_some(mp, m, n);
-                save4_some(vp, v, n);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j >= n) m[j] = w[j] = 0.0f;      // (behind the end)
-            const uint32_t mb = scale_byte(block_top(m)), wb = scale_byte(block_top(w));
-            uint32_t mq = 0, wq = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t rm = 0x8000u, rw = 0x8000u;
-                if (a.dither) {
-                    const uint32_t r = dither_of(t.first + i + j, a.key);
-                    rm = r & 0xFFFFu, rw = r >> 16;
-                }
-                const uint32_t cm = code_of(fabsf(ldexpf(m[j], 127 - int(mb))), rm);
-                uint32_t cw = code_of(ldexpf(w[j], 127 - int(wb)), rw);
-                cw = max(cw, w[j] > 0.0f ? 1u : 0u); // (0 would make the next update one of eps)
-                mq |= (mb == 255 ? 0u : cm | (__float_as_uint(m[j]) >> 31) << 7) << (8 * j);
-                wq |= (wb == 255 ? 0u : cw) << (8 * j);
-            }
-            if (n == 4) {
-                put<FAR>(mq, t.m + i);
-                put<FAR>(wq, t.v + i);
+                mq = fetch<FAR, uint32_t>(t.m + i);
+                vq = fetch<FAR, uint32_t>(t.v + i);
             } else {
                 for (int j = 0; j < n; ++j) {
-                    t.m[i + j] = uint8_t(mq >> (8 * j));
-                    t.v[i + j] = uint8_t(wq >> (8 * j));
+                    mq |= uint32_t(t.m[i + j]) << (8 * j);
+                    vq |= uint32_t(t.v[i + j]) << (8 * j);
                 }
             }
-            if (n && i % kStateBlock == 0) {
-                t.m_scales[i / kStateBlock] = uint8_t(mb);
-                t.v_scales[i / kStateBlock] = uint8_t(wb);
+            mb = t.m_scales[i / kStateBlock];
+            vb = t.v_scales[i / kStateBlock];
+        }
+        codes4(mq, mb, m);
+        codes4(vq, vb, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= v[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float s = g[j] * a.grad_scale;
+        m[j] = __fmaf_rn(m[j], a.beta1, s * a.new1);
+        v[j] = __fmaf_rn(v[j], a.beta2, s * s * a.new2);
+        w[j] = sqrtf(v[j]);
+        p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] / __fmaf_rn(w[j], a.root, a.eps)));
+    }
+    if (n == 4)
+        save4<FAR>(pp, p);
+    else
+        save4_some(pp, p, n);
+    if (t.copy) n == 4 ? save4<FAR>(t.copy + i, p) : save4_some(t.copy + i, p, n);
+    if (BITS == 32) {
+        float *mp = reinterpret_cast<float*>(t.m) + i, *vp = reinterpret_cast<float*>(t.v) + i;
+        if (n == 4) {
+            save4<FAR>(mp, m);
+            save4<FAR>(vp, v);
+        } else {
+            save4_some(mp, m, n);
+            save4_some(vp, v, n);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j >= n) m[j] = w[j] = 0.0f;      // (behind the end)
+        const uint32_t mb = scale_byte(block_top(m)), wb = scale_byte(block_top(w));
+        uint32_t mq = 0, wq = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t rm = 0x8000u, rw = 0x8000u;
+            if (a.dither) {
+                const uint32_t r = dither_of(t.first + i + j, a.key);
+                rm = r & 0xFFFFu, rw = r >> 16;
             }
+            const uint32_t cm = code_of(fabsf(ldexpf(m[j], 127 - int(mb))), rm);
+            uint32_t cw = code_of(ldexpf(w[j], 127 - int(wb)), rw);
+            cw = max(cw, w[j] > 0.0f ? 1u : 0u); // (0 would make the next update one of eps)
+            mq |= (mb == 255 ? 0u : cm | (__float_as_uint(m[j]) >> 31) << 7) << (8 * j);
+            wq |= (wb == 255 ? 0u : cw) << (8 * j);
+        }
+        if (n == 4) {
+            put<FAR>(mq, t.m + i);
+            put<FAR>(wq, t.v + i);
+        } else {
+            for (int j = 0; j < n; ++j) {
+                t.m[i + j] = uint8_t(mq >> (8 * j));
+                t.v[i + j] = uint8_t(wq >> (8 * j));
+            }
+        }
+        if (n && i % kStateBlock == 0) {
+            t.m_scales[i / kStateBlock] = uint8_t(mb);
+            t.v_scales[i / kStateBlock] = uint8_t(wb);
         }
     }
 }
@@ -342,17 +339,12 @@ bool overlaps(const dcr_adamw_tensor* tensors, uint64_t n) {
 
 int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan& p) {
     std::vector<DevAdam> by[kVariants];
-    // few elements over more workgroups, a step of theirs each (0.5 M elements
-    // 4.6 us, by 4096 7.3)
-    uint64_t all = 0;
-    for (uint64_t i = 0; i < n; ++i) all = std::min(all, uint64_t(1) << 60) + std::min(tensors[i].numel, uint64_t(1) << 60);
-    const uint64_t chunk = all <= (uint64_t(1) << 22) ? kAT * 4 : kAChunk;
     uint64_t chunks = 0, bytes = 0;
     for (uint64_t i = 0; i < n; ++i) {
         const dcr_adamw_tensor& t = tensors[i];
         if (int32_t rc = check_adam(t, i)) return rc;
-        chunks += (t.numel + chunk - 1) / chunk;
-        if (chunks >= (uint64_t(1) << 32) / kAT) return step_fail(DCR_E_INVAL, "more elements than one launch takes");
+        chunks += (t.numel + kAChunk - 1) / kAChunk;
+        if (chunks >= (uint64_t(1) << 28)) return step_fail(DCR_E_INVAL, "2^37 elements or more");
     }
     if (overlaps(tensors, n)) return step_fail(DCR_E_INVAL, "buffers of the tensors overlap");
     for (uint64_t i = 0; i < n; ++i) {
@@ -360,7 +352,7 @@ int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan&
         const uint32_t p_bytes = type_bytes(t.param_type), g_bytes = type_bytes(t.grad_type), s_bytes = t.state_bits / 8;
         bytes += t.numel * (p_bytes + g_bytes + 2 * s_bytes + (t.copy ? 2 : 0));
         std::vector<DevAdam>& to = by[t.param_type | t.grad_type << 1 | (t.state_bits == 8 ? 4u : 0u)];
-        for (uint64_t at = 0; at < t.numel; at += chunk) {
+        for (uint64_t at = 0; at < t.numel; at += kAChunk) {
             DevAdam d{};
             d.param = static_cast<uint8_t*>(t.param) + at * p_bytes, d.grad = static_cast<const uint8_t*>(t.grad) + at * g_bytes;
             d.m = static_cast<uint8_t*>(t.m) + at * s_bytes, d.v = static_cast<uint8_t*>(t.v) + at * s_bytes;
@@ -369,7 +361,7 @@ int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan&
                 d.v_scales = static_cast<uint8_t*>(t.v_scales) + at / kStateBlock;
             }
             if (t.copy) d.copy = static_cast<uint16_t*>(t.copy) + at;
-            d.first = t.first + at, d.numel = uint32_t(std::min<uint64_t>(chunk, t.numel - at));
+            d.first = t.first + at, d.numel = uint32_t(std::min<uint64_t>(kAChunk, t.numel - at));
             d.no_decay = t.flags & DCR_ADAMW_NO_DECAY;
             to.push_back(d);
         }
@@ -408,14 +400,15 @@ int32_t adamw_step(const dcr_adamw_plan* p, const dcr_adamw_args* h, hipStream_t
     }
     const DevAdam* chunks = reinterpret_cast<const DevAdam*>(p->dev + p->off_chunks);
     for (uint32_t k = 0; k < kVariants; ++k) {
-        const uint32_t n = uint32_t(p->chunk_first[k + 1] - p->chunk_first[k]);
-        if (!n) continue;
         with_type(k & 1, [&](auto tp) {
             with_type(k >> 1 & 1, [&](auto tg) {
                 typedef decltype(tp) TP;
                 typedef decltype(tg) TG;
                 const auto go = [&](auto kernel) {
-                    hipLaunchKernelGGL(kernel, dim3(n), dim3(kAT), 0, st, chunks + p->chunk_first[k], a, live);
+                    for (uint64_t c = p->chunk_first[k]; c < p->chunk_first[k + 1]; c += kAMostGroups) {
+                        const uint32_t n = uint32_t(std::min(kAMostGroups, p->chunk_first[k + 1] - c));
+                        hipLaunchKernelGGL(kernel, dim3(n), dim3(kAT), 0, st, chunks + c, a, live);
+                    }
                 };
                 if (k & 4)
                     go(p->far ? adamw_kernel<TP, TG, 8, true> : adamw_kernel<TP, TG, 8, false>);
