@@ -37,17 +37,30 @@ struct LpArgs {
     uint64_t* keys;                          // [rows][parts][top]
 };
 
-// m: the largest logit, not scaled; differences d of logits to it are scaled
-// (so the lowest finite numbers, as masks have them, stay finite), and s and t
-// are sums of 2^d and 2^d d
+// m: the largest logit, not scaled; s and t: sums of 2^d and 2^d d over the
+// differences d to it in base 2.
 struct Sums {
     float m, s, t;
 };
+
+// What d is taken against.  d = x unit - mu by one fused product, mu the rounded
+// m unit (row_of_sums puts its rounding right); of numbers so far out that the
+// products overflow, as the lowest finite one, which masks have, it is
+// (x - m) unit.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > 0x1p100f; }
+__device__ __forceinline__ float times_unit(float m, float unit) {
+#pragma clang fp contract(off)
+    return m * unit;
+}
+// the difference of a largest logit to a larger one; held to -160 (2^-160 is 0,
+// and -infinity times that is not)
+__device__ __forceinline__ float below(float a, float m, float unit) {
+    if (a == -INFINITY) return 0.0f;
+    return fmaxf(is_far(a) || is_far(m) ? (a - m) * unit : times_unit(a, unit) - times_unit(m, unit), -160.0f);
+}
 __device__ __forceinline__ Sums join(Sums a, Sums b, float unit) {
     const float m = fmaxf(a.m, b.m);
-    // (2^-160 is 0; -infinity, which a difference may overflow to, times that is not)
-    const float da = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * unit, -160.0f);
-    const float db = b.m == -INFINITY ? 0.0f : fmaxf((b.m - m) * unit, -160.0f);
+    const float da = below(a.m, m, unit), db = below(b.m, m, unit);
     const float fa = exp2f(da), fb = exp2f(db);
     return {m, __fmaf_rn(a.s, fa, b.s * fb), fa * __fmaf_rn(a.s, da, a.t) + fb * __fmaf_rn(b.s, db, b.t)};
 }
@@ -165,7 +178,7 @@ __device__ __forceinline__ uint64_t top_round(TopLds& l, uint32_t top, uint64_t 
 // The sums of the lanes of a wave: the largest first, then each lane's by it.
 __device__ __forceinline__ Sums join_wave(Sums a, float unit) {
     const float m = lanes_all<64>(a.m, [](float x, float y) { return fmaxf(x, y); });
-    const float d = a.m == -INFINITY ? 0.0f : fmaxf((a.m - m) * unit, -160.0f), f = exp2f(d);
+    const float d = below(a.m, m, unit), f = exp2f(d);
     return {m, lanes_sum<64>(a.s * f), lanes_sum<64>(f * __fmaf_rn(a.s, d, a.t))};
 }
 
@@ -182,15 +195,19 @@ struct RowOf {
 };
 
 __device__ __forceinline__ bool none_open(Sums s) { return s.m == -INFINITY && s.s == s.s; }     // an empty row
-__device__ __forceinline__ RowOf row_of_sums(Sums s) { return {s.m, none_open(s) ? 0.0f : logf(s.s)}; }
+__device__ __forceinline__ RowOf row_of_sums(Sums s, float unit) {
+    if (none_open(s)) return {s.m, 0.0f};
+    const float rounded = is_far(s.m) ? 0.0f : -__fmaf_rn(s.m, unit, -times_unit(s.m, unit));    // mu - m unit
+    return {s.m, __fmaf_rn(rounded, kLn2, logf(s.s))};
+}
 
 // what a row's sums give; by one thread
 template <typename T>
 __device__ __forceinline__ RowOf finish_row(const LpArgs& a, uint32_t row, Sums s) {
     const bool none = none_open(s);
-    const RowOf of = row_of_sums(s);
+    const RowOf of = row_of_sums(s, a.scale * kLog2e);
     if (a.lse) a.lse[row] = none ? -INFINITY : __fmaf_rn(s.m, a.scale, of.log_s);
-    if (a.entropy) a.entropy[row] = none ? 0.0f : of.log_s - kLn2 * s.t / s.s;
+    if (a.entropy) a.entropy[row] = none ? 0.0f : logf(s.s) - kLn2 * s.t / s.s;
     if (a.logp) {
         const int64_t t = target_of(a, row);
         float lp = t < 0 ? 0.0f : NAN;
@@ -222,20 +239,38 @@ __device__ __forceinline__ void load_step(const T* x, uint32_t c0, uint32_t to, 
     }
 }
 
-// a step's logits into a thread's sums; returns the largest of them
-__device__ __forceinline__ float add_step(const float* v, float unit, Sums& sum) {
+// A step's logits into a thread's sums; returns the largest of them.  Masks make
+// 0 times -infinity of a sum of t, which then is taken again with the difference
+// held above that: an instruction of twelve that the others do without, as they
+// do without the second product of numbers far out (4096 x 151936: 197 us, with
+// both everywhere 207).  `cut`: the step ends behind the row, in masks.
+__device__ __forceinline__ float add_step(const float* v, float unit, bool cut, Sums& sum) {
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < int(kPiece); ++i) top = fmaxf(top, v[i]);
     const float m = fmaxf(sum.m, top);
-    const float base = m == -INFINITY ? 0.0f : m;
-    const float d = sum.m == -INFINITY ? 0.0f : fmaxf((sum.m - m) * unit, -160.0f), f = exp2f(d);
+    const float base = m == -INFINITY ? 0.0f : m, mu = times_unit(base, unit);
+    const float d = below(sum.m, m, unit), f = exp2f(d);
+    const bool far = is_far(base);
     float s = 0.0f, t = 0.0f;
+    if (!cut) {
 #pragma unroll
-    for (int i = 0; i < int(kPiece); ++i) {
-        const float e = (v[i] - base) * unit, p = __builtin_amdgcn_exp2f(e);
-        s += p;
-        t = __fmaf_rn(p, fmaxf(e, -160.0f), t);
+        for (int i = 0; i < int(kPiece); ++i) {
+            const float e = __fmaf_rn(v[i], unit, -mu), p = __builtin_amdgcn_exp2f(e);
+            s += p;
+            t = __fmaf_rn(p, e, t);
+        }
+    }
+    if (cut || __any(far || t != t)) {
+        s = t = 0.0f;
+        float again = unit;                  // (so that nothing of the above is held in registers for this)
+        asm("" : "+v"(again));
+#pragma unroll
+        for (int i = 0; i < int(kPiece); ++i) {
+            const float e = far ? (v[i] - base) * again : __fmaf_rn(v[i], again, -mu), p = __builtin_amdgcn_exp2f(e);
+            s += p;
+            t = __fmaf_rn(p, fmaxf(e, -160.0f), t);
+        }
     }
     sum.t = __fmaf_rn(f, __fmaf_rn(sum.s, d, sum.t), t);
     sum.s = __fmaf_rn(sum.s, f, s);
@@ -244,7 +279,7 @@ __device__ __forceinline__ float add_step(const float* v, float unit, Sums& sum)
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
+__global__ void __launch_bounds__(kLT, !TOP ? 8 : sizeof(T) == 2 ? 6 : 5) logprobs_kernel(LpArgs a) {
     __shared__ Sums of_wave[kLWaves];
     __shared__ std::conditional_t<TOP, TopLds, uint32_t> lds;
     __shared__ RowOf row_of;
@@ -263,7 +298,7 @@ __global__ void __launch_bounds__(kLT) logprobs_kernel(LpArgs a) {
         raw[0].get(v);
         raw[1].get(v + 8);
         if (c0 + kLT * kPiece < to) load_step<kLT>(x, c0 + kLT * kPiece, to, raw);
-        [[maybe_unused]] const float top = add_step(v, unit, sum);
+        [[maybe_unused]] const float top = add_step(v, unit, c0 + kLT * kPiece > to, sum);
         if constexpr (TOP) {
             const auto key = [&](int i) {
                 const uint32_t j = c0 + ((i / 8) * kLT + threadIdx.x) * 8 + i % 8;
@@ -403,7 +438,7 @@ struct TopWave {
 
 // A wave a part: no barriers.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLT) logprobs_wave_kernel(LpArgs a) {
+__global__ void __launch_bounds__(kLT, TOP ? 6 : 8) logprobs_wave_kernel(LpArgs a) {
     extern __shared__ uint64_t wave_lds[];
     const uint32_t unit_of = __builtin_amdgcn_readfirstlane(blockIdx.x * kLWaves + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
     const uint32_t row = unit_of / a.parts, part = unit_of % a.parts;
@@ -421,7 +456,7 @@ __global__ void __launch_bounds__(kLT) logprobs_wave_kernel(LpArgs a) {
         raw[0].get(v);
         raw[1].get(v + 8);
         if (c0 + STEP < to) load_step<64>(x, c0 + STEP, to, raw);
-        [[maybe_unused]] const float top = add_step(v, unit, sum);
+        [[maybe_unused]] const float top = add_step(v, unit, c0 + STEP > to, sum);
         if constexpr (TOP) {
             const bool passes = best.least == 0 ? c0 + lane * 8 < to : order_of(top) >= uint32_t(best.least >> 32);
             best.round(a.top, passes, v, [&](int i) {
@@ -434,7 +469,7 @@ __global__ void __launch_bounds__(kLT) logprobs_wave_kernel(LpArgs a) {
     if (a.parts == 1) {
         if (lane == 0) finish_row<T>(a, row, sum);
         if constexpr (TOP) {
-            if (lane < a.top) put_top(a, row, lane, best.mine, row_of_sums(sum));
+            if (lane < a.top) put_top(a, row, lane, best.mine, row_of_sums(sum, unit));
         }
     } else {
         if (lane == 0) a.sums[unit_of] = f32x4{sum.m, sum.s, sum.t, 0.0f};
