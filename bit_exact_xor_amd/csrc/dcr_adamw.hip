@@ -437,7 +437,7 @@ int32_t dcr_adamw_plan_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_ad
     int32_t rc;
     try {
         rc = adamw_build(tensors, n, *p);
-    } catch (const std::bad_alloc&) {
+    } catch (...) {
         rc = step_fail(DCR_E_NOMEM, "out of host memory");
     }
     if (rc) {

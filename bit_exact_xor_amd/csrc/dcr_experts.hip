@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
         }
         if (a.bias && bound && bound != ~0u) {     // and in 64 bits at least this
             const float x = of_rank32(bound);
-            bound = rank32(x - 2 * off * fmaxf(1.0f, fabsf(x)));
+            if (x < INFINITY) bound = rank32(x - 2 * off * fmaxf(1.0f, fabsf(x)));
         }
     }
     bound = max(bound, 1u);

@@ -469,7 +469,7 @@ def _one_device(first, *others):
     """Index of the GPU that all of the tensors (None: left out) are on."""
     dev = first.get_device() if not isinstance(first, Fp4Tensor) else first.index
     if dev < 0:
-        raise ValueError("4-bit calls take tensors in GPU memory")
+        raise ValueError("tensors in GPU memory expected")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on different devices: cuda:{dev} and {t.device}")
@@ -809,7 +809,8 @@ class AdamWTensors:
     behind the other).
 
     The buffers are kept; gradients are written into the same tensors step
-    after step.  The step may follow on any stream."""
+    after step.  Steps may follow on any stream; the object has to be there
+    until they are done (and as long as a graph that has captured one)."""
 
     def __init__(self, params, grads, bits=32, copies=None, m=None, v=None, m_scales=None, v_scales=None, decay=None,
                  first=None):

@@ -701,7 +701,9 @@ enum { DCR_EXPERTS_RENORMALIZE = 1 };
  *               than 2^26 rows and (rows * k) 2^31 pairs; an expert at
  *               -infinity is shut: it has score 0 and is not chosen
  *   bias        NULL, or [experts] fp32, added to the scores for the choice
- *               alone (it balances the experts' load, the weights do not see it)
+ *               alone (it balances the experts' load, the weights do not see
+ *               it); at -infinity the expert comes behind all that are open and
+ *               has no part in its group's value
  *   score       s = softmax over the row's experts, or sigmoid of each logit
  *   groups, top_groups  experts lie in `groups` groups of consecutive ones (a
  *               divisor of the experts, at most 64); only those of the

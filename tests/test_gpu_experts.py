@@ -101,6 +101,21 @@ def test_select_close_to_a_border():
             assert np.array_equal(ids.cpu().numpy(), want)
 
 
+def test_select_infinite_biases():
+    """Experts that a bias puts in front of all or behind all: in the order of their indices there."""
+    rng = np.random.default_rng(12)
+    for e, k, first, last in ((40, 8, 3, 10), (200, 8, 12, 100), (128, 20, 8, 110), (20, 20, 5, 10)):
+        x = rng.standard_normal((9, e)).astype(np.float32)
+        bias = (0.1 * rng.standard_normal(e)).astype(np.float32)
+        at = rng.permutation(e)
+        bias[at[:first]], bias[at[first:first + last]] = np.inf, -np.inf
+        for score in (SOFTMAX, SIGMOID):
+            ids, w = run_select(up(x), k, up(bias), score)
+            want_ids, want = R.select(x, bias, k, score == SIGMOID)
+            assert np.array_equal(ids.cpu().numpy(), want_ids), (e, k, score)
+            assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12)).all()
+
+
 def test_select_nan_is_seen():
     """A NaN counts as the largest and its weight is NaN; other rows do not change."""
     rng = np.random.default_rng(4)
