@@ -610,17 +610,27 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
     uint32_t* sums = base + a.experts;            // [experts]: pairs in all runs
     uint32_t* part = sums + a.experts;            // [kOWaves]
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    for (uint32_t i = threadIdx.x; i < (kOWaves + 2) * a.experts; i += kOT) cnt[i] = 0;
-    __syncthreads();
     const uint64_t from = (uint64_t(blockIdx.x) * kOWaves + wave) * a.per_wave;
     const uint64_t to = min(uint64_t(a.n), from + a.per_wave);
-    for (uint64_t i = from + lane; i < to; i += 64) {
-        const uint32_t e = uint32_t(a.ids[i]);
-        if (e < a.experts) atomicAdd(&cnt[wave * a.experts + e], 1u);
+    // the wave's first pairs, on their way while the runs are added up
+    constexpr int AHEAD = 4;
+    uint32_t ahead[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+        const uint64_t i = from + 64 * u + lane;
+        ahead[u] = i < to ? uint32_t(a.ids[i]) : ~0u;
     }
+    for (uint32_t i = threadIdx.x; i < (kOWaves + 2) * a.experts; i += kOT) cnt[i] = 0;
     __syncthreads();
     // the experts' pairs in all runs and in the runs in front: each wave adds up
     // some of the runs (so that the loads are on their way together)
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        if (ahead[u] < a.experts) atomicAdd(&cnt[wave * a.experts + ahead[u]], 1u);
+    for (uint64_t i = from + 64 * AHEAD + lane; i < to; i += 64) {
+        const uint32_t e = uint32_t(a.ids[i]);
+        if (e < a.experts) atomicAdd(&cnt[wave * a.experts + e], 1u);
+    }
     if (a.runs > 1) {
         for (uint32_t e = lane; e < a.experts; e += 64) {
             uint32_t all = 0, front = 0;
@@ -633,8 +643,8 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
             atomicAdd(&sums[e], all);
             atomicAdd(&base[e], front);
         }
-        __syncthreads();
     }
+    __syncthreads();
     uint32_t all[2] = {}, front[2] = {};          // two experts a thread
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -676,9 +686,7 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
         }
     }
     __syncthreads();
-    for (uint64_t i0 = from; i0 < to; i0 += 64) {
-        const uint64_t i = i0 + lane;
-        const uint32_t e = i < to ? uint32_t(a.ids[i]) : ~0u;
+    const auto place = [&](uint64_t i, uint32_t e) {
         const bool has = e < a.experts;
         const uint64_t peers = same_expert(e, has, a.bits);
         uint32_t* mine = &cnt[wave * a.experts + (has ? e : 0)];
@@ -688,7 +696,11 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
         if (has && rank == 0) *mine = start + uint32_t(__popcll(peers));
         __builtin_amdgcn_wave_barrier();
         if (i < to) a.slots[i] = has ? int32_t(start + rank) : -1;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        if (from + 64 * u < to) place(from + 64 * u + lane, ahead[u]);
+    for (uint64_t i0 = from + 64 * AHEAD; i0 < to; i0 += 64) place(i0 + lane, i0 + lane < to ? uint32_t(a.ids[i0 + lane]) : ~0u);
 }
 
 // -------------------------------------------------------------------- host
