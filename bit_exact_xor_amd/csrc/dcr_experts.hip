@@ -22,7 +22,6 @@ namespace {
 
 constexpr uint32_t kET = 256;                     // threads of a workgroup
 constexpr uint32_t kAnyGroups = 31;
-constexpr uint32_t kFewGroups = 8;                // groups of any size that are compared in 32 bits first
 
 struct SelectArgs {
     const void* logits;
@@ -34,6 +33,7 @@ struct SelectArgs {
     uint64_t stride, d_stride;
     uint32_t rows, experts, k, groups, top_groups, sigmoid, renormalize;
     uint32_t group_log2;      // a group is 8 << group_log2 experts, or (kAnyGroups) any number
+    uint32_t share_log2;      // lanes of a group then
     float scale;
 };
 
@@ -160,7 +160,7 @@ struct Two {
 // that lie 5 `off` apart (relative to them, above 1) are in order.  Shuts experts
 // (ranks to 0) and returns whether what decides was that far apart.
 template <int LANES, int N>
-__device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, uint32_t* rank) {
+__device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, float* lds, uint32_t* rank) {
     struct {
         float first, second;
         __device__ __forceinline__ void meet(float f, float s) {
@@ -208,36 +208,32 @@ __device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* 
 #pragma unroll
         for (int i = 0; i < N; ++i) rank[i] = in ? rank[i] : 0;
     } else {
-        // up to kFewGroups groups of any size: one after the other over all lanes
-        const uint32_t size = a.experts / a.groups;
-        uint32_t of[kFewGroups], in = 0;           // in, bit g: group g is taken
+        // groups of any size, at most one for each lane: through LDS, the lanes
+        // dealt to groups in shares of a power of two
+        const uint32_t size = a.experts / a.groups, share = 1u << a.share_log2;
 #pragma unroll
-        for (uint32_t g = 0; g < kFewGroups; ++g) {
-            of[g] = 0;
-            if (g >= a.groups) continue;
-            two.first = two.second = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < N; ++i) two.meet(expert_of<LANES>(lane, i) - g * size < size ? c[i] : -INFINITY, -INFINITY);
-            of[g] = value(LANES);
+        for (int i = 0; i < N; ++i)
+            if (expert_of<LANES>(lane, i) < a.experts) lds[expert_of<LANES>(lane, i)] = c[i];
+        wave_sync();
+        const uint32_t mine = lane >> a.share_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
+        if (mine < a.groups)
+            for (uint32_t i = lane & (share - 1); i < size; i += share) two.meet(lds[mine * size + i], -INFINITY);
+        wave_sync();
+        const uint32_t of = value(share);
+        uint32_t ahead = 0;
+        for (uint32_t g = 0; g < a.groups; ++g) {
+            const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.share_log2)), 64));
+            ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
         }
-        least = ~0u;
-#pragma unroll
-        for (uint32_t g = 0; g < kFewGroups; ++g) {
-            if (g >= a.groups) continue;
-            uint32_t ahead = 0;
-#pragma unroll
-            for (uint32_t o = 0; o < kFewGroups; ++o) ahead += (of[o] > of[g] || (of[o] == of[g] && o < g)) ? 1u : 0u;
-            if (ahead < a.top_groups)
-                in |= 1u << g, least = min(least, of[g]);
-            else
-                most = max(most, of[g]);
-        }
+        const bool in = mine < a.groups && ahead < a.top_groups;
+        least = lanes_all<LANES>(in ? of : ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
+        most = lanes_all<LANES>(in ? 0u : of, [](uint32_t x, uint32_t y) { return max(x, y); });
+        const uint64_t taken = __ballot(in) >> base;
+        const float inv = 1.0f / float(size);      // ((e + 1/2) / size is at least 1/2 / size from a whole number: far more than its error)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            bool open = false;
-#pragma unroll
-            for (uint32_t g = 0; g < kFewGroups; ++g) open |= (in >> g & 1u) && expert_of<LANES>(lane, i) - g * size < size;
-            rank[i] = open ? rank[i] : 0;
+            const uint32_t e = expert_of<LANES>(lane, i), g = uint32_t((float(e) + 0.5f) * inv);
+            rank[i] = e < a.experts && (taken >> (g << a.share_log2) & 1) ? rank[i] : 0;
         }
     }
     const float x = of_rank32(least), y = of_rank32(most);
@@ -381,8 +377,8 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
             uint32_t all[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) all[i] = rank[i];
-            const bool few = a.group_log2 < kAnyGroups || a.groups <= kFewGroups;
-            if (!few || __any(!take_groups32<LANES, N>(a, c, lane, off, rank))) {
+            const bool few = a.group_log2 < kAnyGroups || a.groups <= LANES;
+            if (!few || __any(!take_groups32<LANES, N>(a, c, lane, off, reinterpret_cast<float*>(keys), rank))) {
                 double d[N];
                 double z = inverse;
                 if (!a.sigmoid && !a.bias && a.renormalize) z = softmax_inverse<LANES, N>(v, top);
@@ -705,15 +701,20 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
 
 // -------------------------------------------------------------------- host
 
-// f(lanes, registers of eight) for a row of n elements
+// f(lanes, registers of eight) for rows of n elements, of which k are taken: the
+// fewest lanes that hold a row, or one for each that is taken while the rows leave
+// lanes without work (24 of 128 for 4000 rows 16 us, with the 16 lanes that hold
+// them 27 us; 16000 rows 39 us with either)
 template <typename F>
-void with_lanes(uint32_t n, F&& f) {
+void with_lanes(uint32_t n, uint32_t k, uint64_t rows, F&& f) {
     const std::integral_constant<int, 1> one;
-    if (n <= 64) f(std::integral_constant<int, 8>(), one);
-    else if (n <= 128) f(std::integral_constant<int, 16>(), one);
-    else if (n <= 256) f(std::integral_constant<int, 32>(), one);
-    else if (n <= 512) f(std::integral_constant<int, 64>(), one);
-    else f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    uint32_t lanes = 8;
+    while (lanes < 64 && (lanes * 8 < n || (lanes < k && rows * lanes * 2 <= 262144))) lanes *= 2;
+    if (n > 512) f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+    else if (lanes == 8) f(std::integral_constant<int, 8>(), one);
+    else if (lanes == 16) f(std::integral_constant<int, 16>(), one);
+    else if (lanes == 32) f(std::integral_constant<int, 32>(), one);
+    else f(std::integral_constant<int, 64>(), one);
 }
 
 int32_t check_select(uint64_t rows, uint32_t experts, uint32_t k, uint32_t score, uint32_t options, float scale) {
@@ -750,8 +751,10 @@ int32_t select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows
         if (experts > 512 || (8u << a.group_log2) != size) a.group_log2 = kAnyGroups;
     }
     with_type(type, [&](auto t) {
-        with_lanes(experts, [&](auto lanes, auto r) {
+        with_lanes(experts, k, rows, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
+            a.share_log2 = 0;
+            while ((2u << a.share_log2) * groups <= uint32_t(L)) ++a.share_log2;
             const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
             hipLaunchKernelGGL((experts_select_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET),
                                ROWS * select_lds(experts, k), st, a);
@@ -775,7 +778,7 @@ int32_t select_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t
     a.stride = stride, a.d_stride = d_stride, a.rows = uint32_t(rows), a.experts = experts, a.k = k;
     a.sigmoid = score == DCR_SCORE_SIGMOID, a.renormalize = options & DCR_EXPERTS_RENORMALIZE, a.scale = scale;
     with_type(type, [&](auto t) {
-        with_lanes(experts, [&](auto lanes, auto r) {
+        with_lanes(experts, 0, rows, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
             const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
             hipLaunchKernelGGL((experts_select_grad_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET), 0, st, a);

@@ -27,6 +27,17 @@ struct RowArgs {
     uint32_t pieces;       // of eight columns, of a row
 };
 
+// Eight columns from c on, of a row of at least eight: a piece that would end
+// behind the row is moved back over the one in front, so all are whole (both then
+// write the same; taken column by column the last piece holds up its whole wave:
+// 32380 tokens' gradient, 10 rows of 198 columns each, 166 us, so 66).  Returns by
+// how much.
+__device__ __forceinline__ uint32_t moved_back(uint32_t width, uint32_t* c) {
+    const uint32_t by = width >= 8 && *c + 8 > width ? *c + 8 - width : 0;
+    *c -= by;
+    return by;
+}
+
 // The thread's token and the first of its eight columns; false behind the end.
 // Threads are dealt to pieces of eight columns one after the other, whatever the
 // width, so none is without work in the middle of a row.
@@ -34,6 +45,7 @@ __device__ __forceinline__ bool piece_of(const RowArgs& a, uint32_t* at, uint32_
     const uint32_t i = blockIdx.x * kRT + threadIdx.x;
     *at = i / a.pieces;
     *c = (i - *at * a.pieces) * 8;
+    moved_back(a.width, c);
     return *at < a.tokens;
 }
 
@@ -98,8 +110,9 @@ template <typename TD, typename TX, typename TG, bool FAR, uint32_t WAVES>
 __device__ __forceinline__ float pair_grad(const RowArgs& a, const TD* dy, const TX* x, TG* dx, float w, uint32_t first) {
     float dot = 0.0f;
 #pragma unroll 2
-    for (uint32_t c = first; c < a.width; c += 512 * WAVES) {
-        const int n = int(min(8u, a.width - c));
+    for (uint32_t c0 = first; c0 < a.width; c0 += 512 * WAVES) {
+        uint32_t c = c0;
+        const int twice = int(moved_back(a.width, &c)), n = int(min(8u, a.width - c));
         Raw8<TD> rd;
         Raw8<TX> rx;
         float d[8], v[8];
@@ -114,7 +127,7 @@ __device__ __forceinline__ float pair_grad(const RowArgs& a, const TD* dy, const
         rx.get(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            dot = __fmaf_rn(d[i], v[i], dot);
+            dot = i < twice ? dot : __fmaf_rn(d[i], v[i], dot);
             d[i] *= w;
         }
         n == 8 ? store8<FAR>(dx + c, d) : store_some(dx + c, d, n);
@@ -144,10 +157,11 @@ __global__ void __launch_bounds__(kRT) rows_combine_grad_kernel(RowArgs a) {
 // and kRows rows of x are on their way together.
 template <typename TD, typename TX, typename TG, int LANES>
 __global__ void __launch_bounds__(kRT) rows_combine_grad_narrow_kernel(RowArgs a) {
-    const uint32_t at = blockIdx.x * (kRT / LANES) + threadIdx.x / LANES, c = threadIdx.x % LANES * 8;
+    const uint32_t at = blockIdx.x * (kRT / LANES) + threadIdx.x / LANES, first = threadIdx.x % LANES * 8;
     const bool live = at < a.tokens;
     const uint64_t safe = live ? at : 0;
-    const int n = c < a.width ? int(min(8u, a.width - c)) : 0;
+    uint32_t c = first < a.width ? first : 0;
+    const int twice = int(moved_back(a.width, &c)), n = first < a.width ? int(min(8u, a.width - c)) : 0;
     Raw8<TD> rd;
     float d[8];
     const TD* dy = static_cast<const TD*>(a.a) + safe * a.a_stride + c;
@@ -174,14 +188,14 @@ __global__ void __launch_bounds__(kRT) rows_combine_grad_narrow_kernel(RowArgs a
                 rx[u].get(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    dot = __fmaf_rn(d[i], v[i], dot);
+                    dot = i < twice ? dot : __fmaf_rn(d[i], v[i], dot);
                     g[i] = d[i] * w;
                 }
                 TG* dx = static_cast<TG*>(a.y) + uint64_t(s[u]) * a.y_stride + c;
                 n == 8 ? store8(dx, g) : store_some(dx, g, n);
             }
             dot = lanes_sum<LANES>(dot);
-            if (c == 0 && live) a.dweights[pair] = dot;
+            if (first == 0 && live) a.dweights[pair] = dot;
         }
     }
 }
@@ -214,13 +228,15 @@ int32_t check_rows(uint64_t tokens, uint64_t width, uint32_t k, uint64_t n_slots
     return DCR_OK;
 }
 
-// f(whether so many bytes of results go past the caches: more than the last of
-// them, 256 MiB, holds).  16384 tokens there and back with 8 rows of 2048 bf16
+// f(whether so many bf16 results go past the caches: more than the last of them,
+// 256 MiB, holds).  16384 tokens there and back with 8 rows of 2048 bf16
 // 220 us, else 237; their gradient 234 and 246.  Below it they stay for the
 // product that reads them next (4096 tokens' gradient 52 us, past the caches 63).
-template <typename F>
-void with_far(uint64_t bytes, F&& f) {
-    bytes > (uint64_t(256) << 20) ? f(std::true_type()) : f(std::false_type());
+template <typename T, typename F>
+void with_far(T, uint64_t elements, F&& f) {
+    if constexpr (sizeof(T) == 2)
+        if (elements * sizeof(T) > (uint64_t(256) << 20)) return f(std::true_type());
+    f(std::false_type());
 }
 
 int32_t row_grid(uint64_t units, uint32_t per_group, uint32_t* grid) {
@@ -245,7 +261,7 @@ int32_t dispatch_rows(const void* x, uint32_t x_type, uint64_t x_stride, uint64_
     if ((rc = row_grid(tokens * a.pieces, kRT, &grid))) return rc;
     with_type(x_type, [&](auto tx) {
         with_type(y_type, [&](auto ty) {
-            with_far(uint64_t(n_slots) * width * sizeof(ty), [&](auto far) {
+            with_far(ty, uint64_t(n_slots) * width, [&](auto far) {
                 hipLaunchKernelGGL((rows_dispatch_kernel<decltype(tx), decltype(ty), decltype(far)::value>), dim3(grid), dim3(kRT),
                                    0, st, a);
             });
@@ -314,7 +330,7 @@ int32_t combine_rows_grad(const void* dy, uint32_t dy_type, uint64_t dy_stride, 
                 } else if (by_pair) {
                     go(rows_combine_grad_pair_kernel<TD, TX, TG>);
                 } else {
-                    with_far(uint64_t(n_slots) * width * sizeof(tg),
+                    with_far(tg, uint64_t(n_slots) * width,
                              [&](auto far) { go(rows_combine_grad_kernel<TD, TX, TG, decltype(far)::value>); });
                 }
             });

@@ -88,6 +88,22 @@ def test_select_groups(score, groups, top_groups):
                 assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("rows,e,k,groups,top_groups", [(50, 456, 10, 8, 3), (33, 322, 7, 2, 1), (9, 1000, 20, 40, 7),
+                                                        (7, 210, 30, 30, 4), (5, 99, 24, 33, 11), (6, 24, 5, 12, 5),
+                                                        (40, 1023, 64, 31, 9), (600, 100, 24, 1, 1), (9000, 100, 24, 4, 2),
+                                                        (2100, 57, 13, 3, 2)])
+def test_select_groups_of_any_size(rows, e, k, groups, top_groups):
+    """Groups that lie across lanes, more groups than lanes, more experts to take than lanes hold a row."""
+    rng = np.random.default_rng(e)
+    for score, kind in ((SOFTMAX, "ties"), (SIGMOID, "normal"), (SIGMOID, "masked")):
+        x = logits_of(kind, rows, e, rng).astype(np.float32)
+        bias = (0.1 * rng.standard_normal(e)).astype(np.float32)
+        ids, w = run_select(up(x), k, up(bias), score, groups, top_groups)
+        want_ids, want = R.select(x, bias, k, score == SIGMOID, groups, top_groups)
+        assert np.array_equal(ids.cpu().numpy(), want_ids), kind
+        assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all()
+
+
 def test_select_close_to_a_border():
     """Sums of score and bias that 32 bits cannot tell apart: the bias undoes the scores' differences but for 2^-30."""
     rng = np.random.default_rng(8)
@@ -350,7 +366,8 @@ def test_offsets_past_32_bits():
     assert torch.equal(ids.cpu(), torch.tensor([[0, 1, 2]] * 3, dtype=torch.int32)) and (w == 1 / 64).all()
 
 
-@pytest.mark.parametrize("tokens,width,k", [(2100, 520, 2), (2048, 4096, 18), (2047, 513, 3), (4096, 512, 2), (3000, 24, 5)])
+@pytest.mark.parametrize("tokens,width,k", [(2100, 520, 2), (2048, 4096, 18), (2047, 513, 3), (4096, 512, 2), (3000, 24, 5),
+                                            (2500, 198, 10), (2500, 51, 11), (2100, 1031, 3), (100, 9, 4)])
 def test_rows_of_many_tokens(tokens, width, k):
     """The forms for many tokens (a wave a token, narrow rows, results past the caches) against 32-bit torch on the GPU:
     copies are equal; sums of k products within (k + 2) 2^-24, of `width` within (width / 64 + 16) 2^-24 of the sums of
