@@ -156,11 +156,16 @@ struct Two {
     }
 };
 
-// The groups' choice in 32 bits: `off` bounds a value's error, so sums of two
-// that lie 5 `off` apart (relative to them, above 1) are in order.  Shuts experts
-// (ranks to 0) and returns whether what decides was that far apart.
+// The groups' choice in 32 bits.  Shuts experts (ranks to 0) and returns whether
+// what decides is certain.  A value is off by `off` and 2^-24 of itself, and so
+// is a sum of two once more: values 4 `off` and 2^-21 of the largest among them
+// apart are in order.  Without a bias also those 2^-16 of themselves apart: a
+// score is off by 2^-17 of itself at most (where its logit is 87 away from the
+// others, by the rounding of its exponent) but for what all have in common, and
+// has fewer bits only near 2^-126.
 template <int LANES, int N>
-__device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, float* lds, uint32_t* rank) {
+__device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, float* lds,
+                                              uint32_t* rank) {
     struct {
         float first, second;
         __device__ __forceinline__ void meet(float f, float s) {
@@ -237,7 +242,10 @@ __device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* 
         }
     }
     const float x = of_rank32(least), y = of_rank32(most);
-    return !odd && (most == 0 || x - y > 5 * off * fmaxf(1.0f, fabsf(x)));
+    const float far = fmaxf(two.first == -INFINITY ? 0.0f : fabsf(two.first), two.second == -INFINITY ? 0.0f : fabsf(two.second));
+    float apart = fmaf(0x1p-20f, lanes_all<LANES>(far, [](float p, float q) { return fmaxf(p, q); }), 5 * off);
+    if (!a.bias) apart = fminf(apart, fmaf(0x1p-15f, x, 0x1p-120f));
+    return !odd && (most == 0 || x - y > apart);
 }
 
 // The same in 64 bits, groups of any number and size.  c: the lane's s + bias,
@@ -314,8 +322,8 @@ __device__ __forceinline__ double softmax_inverse(const float* v, float top) {
     return z == 0.0 ? 0.0 : 1.0 / z;
 }
 
-// LDS of a row: its candidates (logit and index), their keys, the chosen ones
-__host__ __device__ inline uint32_t select_lds(uint32_t experts, uint32_t k) { return 16 * experts + 16 * k; }
+// LDS of a row: its candidates' keys and logits, the chosen ones
+__host__ __device__ inline uint32_t select_lds(uint32_t experts, uint32_t k) { return (12 * (experts + k) + 7) / 8 * 8; }
 
 template <typename T, int LANES, int R>
 __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
@@ -323,10 +331,10 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
     constexpr float kLog2e = 1.44269504088896340736f;
     extern __shared__ uint64_t lds[];
     const uint32_t lane = threadIdx.x % LANES, in_wg = threadIdx.x / LANES;
-    uint64_t* found = lds + in_wg * (select_lds(a.experts, a.k) / 8);
-    uint64_t* keys = found + a.experts;
+    uint64_t* keys = lds + in_wg * (select_lds(a.experts, a.k) / 8);
     double* weights = reinterpret_cast<double*>(keys + a.experts);
-    int32_t* ids = reinterpret_cast<int32_t*>(weights + a.k);
+    float* found = reinterpret_cast<float*>(weights + a.k);
+    int32_t* ids = reinterpret_cast<int32_t*>(found + a.experts);
     const uint32_t at = blockIdx.x * ROWS + in_wg;
     const bool live = at < a.rows;
     const T* row = static_cast<const T*>(a.logits) + uint64_t(live ? at : 0) * a.stride;
@@ -350,9 +358,11 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
     }
     // Ranks in 32 bits.  A sigmoid by the hardware's exponential and reciprocal
     // (one step off each) is off by less than 2.3 * 2^-23 and a sum with the bias
-    // by 2^-24 of itself; a softmax's sum of up to 1024 terms adds less than 2^-20
-    // of a score.  Without a bias the logits themselves have the scores' order.
-    const float off = a.sigmoid ? 0x1p-21f : 0x1p-20f;
+    // by 2^-24 of itself.  A softmax's sum of up to 1024 terms is off by less than
+    // 28 * 2^-24: 14 additions, a term's 2 steps, and its exponent's rounding, 2.3
+    // times its distance from the largest, of which the terms' mean is below 4.5.
+    // Without a bias the logits themselves have the scores' order.
+    float off = 0x1p-21f;
     uint32_t rank[N];
     double inverse = 1.0;                      // of the softmax's sum
     if (!a.sigmoid && (a.bias || !a.renormalize)) inverse = softmax_inverse<LANES, N>(v, top);
@@ -367,6 +377,7 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
             for (int i = 0; i < N; ++i) z += c[i] = __builtin_amdgcn_exp2f((v[i] - top) * kLog2e);
             z = lanes_sum<LANES>(z);
             inv = z == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(z);
+            off = 0x1p-19f * inv;              // (the largest score is inv)
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -408,7 +419,7 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
         }
         if (a.bias && bound && bound != ~0u) {     // and in 64 bits at least this
             const float x = of_rank32(bound);
-            if (x < INFINITY) bound = rank32(x - 2 * off * fmaxf(1.0f, fabsf(x)));
+            if (x < INFINITY) bound = rank32(x - 2 * fmaf(0x1p-22f, fabsf(x), off));
         }
     }
     bound = max(bound, 1u);
@@ -421,13 +432,13 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
     uint32_t to = upto - count;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (rank[i] >= bound) found[to] = uint64_t(__float_as_uint(v[i])) << 32 | expert_of<LANES>(lane, i);
+        if (rank[i] >= bound) found[to] = v[i], keys[to] = expert_of<LANES>(lane, i);
         to += rank[i] >= bound ? 1u : 0u;
     }
     wave_sync();
     for (uint32_t i = lane; i < n; i += LANES) {
-        const uint32_t e = uint32_t(found[i]);
-        const float l = __uint_as_float(uint32_t(found[i] >> 32));
+        const uint32_t e = uint32_t(keys[i]);
+        const float l = found[i];
         uint64_t key;
         if (a.bias) {
             double c = a.sigmoid ? inverse_near(1.0 + exp_near(-double(l))) : exp_near(double(l) - double(top)) * inverse;
@@ -445,8 +456,8 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
 #pragma unroll 4
         for (uint32_t j = 0; j < n; ++j) ahead += keys[j] > mine ? 1u : 0u;
         if (ahead < a.k) {
-            const double l = double(__uint_as_float(uint32_t(found[i] >> 32)));
-            ids[ahead] = int32_t(uint32_t(found[i]));
+            const double l = double(found[i]);
+            ids[ahead] = int32_t(index_of(mine));
             weights[ahead] = a.sigmoid ? sigmoid64(l) : exp(l - double(top)) * (a.renormalize ? 1.0 : inverse);
         }
     }
@@ -628,16 +639,33 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
         if (e < a.experts) atomicAdd(&cnt[wave * a.experts + e], 1u);
     }
     if (a.runs > 1) {
-        for (uint32_t e = lane; e < a.experts; e += 64) {
-            uint32_t all = 0, front = 0;
-#pragma unroll 8
-            for (uint32_t r = wave; r < a.runs; r += kOWaves) {
-                const uint32_t c = a.counts[r * a.experts + e];
-                all += c;
-                front += r < blockIdx.x ? c : 0;
+        // (two experts and eight runs on their way together, as far as there are some)
+        for (uint32_t e0 = lane; e0 < a.experts; e0 += 128) {
+            uint32_t all[2] = {}, front[2] = {};
+            for (uint32_t r0 = wave; r0 < a.runs; r0 += 8 * kOWaves) {
+                uint32_t c[2][8];
+#pragma unroll
+                for (uint32_t u = 0; u < 8; ++u) {
+                    const uint32_t r = r0 + u * kOWaves;
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h)
+                        c[h][u] = r < a.runs && e0 + 64 * h < a.experts ? a.counts[r * a.experts + e0 + 64 * h] : 0;
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < 8; ++u) {
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        all[h] += c[h][u];
+                        front[h] += r0 + u * kOWaves < blockIdx.x ? c[h][u] : 0;
+                    }
+                }
             }
-            atomicAdd(&sums[e], all);
-            atomicAdd(&base[e], front);
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+                if (e0 + 64 * h >= a.experts) continue;
+                atomicAdd(&sums[e0 + 64 * h], all[h]);
+                atomicAdd(&base[e0 + 64 * h], front[h]);
+            }
         }
     }
     __syncthreads();

@@ -117,6 +117,23 @@ def test_select_close_to_a_border():
             assert np.array_equal(ids.cpu().numpy(), want)
 
 
+def test_select_groups_of_far_biases():
+    """Groups whose two best have biases that cancel: what is left decides, 2^-20 of them."""
+    rng = np.random.default_rng(15)
+    for groups, size in ((8, 16), (16, 8), (5, 7)):
+        e = groups * size
+        for score in (SOFTMAX, SIGMOID):
+            x = rng.standard_normal((30, e)).astype(np.float32)
+            bias = np.full((groups, size), -2.0 ** 20, dtype=np.float32)
+            bias[np.arange(groups), rng.integers(0, size, groups)] = 2.0 ** 20
+            bias[:, 0] += (rng.integers(-2, 3, groups) / 16).astype(np.float32)
+            for top_groups in (1, 3):
+                ids, w = run_select(up(x), 3, up(bias.reshape(-1)), score, groups, top_groups)
+                want_ids, want = R.select(x, bias.reshape(-1), 3, score == SIGMOID, groups, top_groups)
+                assert np.array_equal(ids.cpu().numpy(), want_ids), (groups, score, top_groups)
+                assert (np.abs(f64(w) - want) <= np.abs(want) * (2.0 ** -24 + 1e-12)).all()
+
+
 def test_select_infinite_biases():
     """Experts that a bias puts in front of all or behind all: in the order of their indices there."""
     rng = np.random.default_rng(12)
