@@ -529,16 +529,16 @@ struct LpGradArgs {
     const float *lse, *dlogp, *entropy, *dentropy;
     void* dlogits;
     uint64_t stride, d_stride;
-    uint32_t rows, vocab, wide_ids, pieces;      // pieces: workgroups of a row
+    uint32_t rows, vocab, wide_ids, pieces;      // pieces: workgroups, or threads, of a row
     float scale;
 };
 
-constexpr uint32_t kGU = 2;                      // eights of a thread
+constexpr uint32_t kGU = 2;                      // eights of a thread in a row of its workgroup's
 
-// dx_j = scale (dlogp (1[j = t] - p_j) - dentropy p_j (log p_j + entropy))
-template <typename T>
-__global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
-    const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
+// dx_j = scale (dlogp (1[j = t] - p_j) - dentropy p_j (log p_j + entropy)), for
+// the eight logits from `at` on
+template <typename T, int U>
+__device__ __forceinline__ void grad_of(const LpGradArgs& a, uint32_t row, const uint32_t* at) {
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
     T* y = static_cast<T*>(a.dlogits) + uint64_t(row) * a.d_stride;
     const int64_t target = a.wide_ids ? static_cast<const int64_t*>(a.targets)[row]
@@ -549,17 +549,15 @@ __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
     const float b = a.dentropy ? a.dentropy[row] : 0.0f;
     const float c = a.dentropy ? __fmaf_rn(b, a.entropy[row], up) : up;
     const bool none = lse == -INFINITY;          // an empty row
-    Raw8<T> raw[kGU];
-    uint32_t at[kGU];
-    int n[kGU];
+    Raw8<T> raw[U];
+    int n[U];
 #pragma unroll
-    for (uint32_t u = 0; u < kGU; ++u) {
-        at[u] = ((piece * kGU + u) * kLT + threadIdx.x) * 8;
+    for (int u = 0; u < U; ++u) {
         n[u] = at[u] < a.vocab ? int(min(8u, a.vocab - at[u])) : 0;
         n[u] == 8 ? raw[u].load_once(x + at[u]) : raw[u].load_some(x + at[u], n[u], kBf16MinusInf);
     }
 #pragma unroll
-    for (uint32_t u = 0; u < kGU; ++u) {
+    for (int u = 0; u < U; ++u) {
         float v[8];
         raw[u].get(v);
 #pragma unroll
@@ -578,6 +576,23 @@ __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
         }
         n[u] == 8 ? store8<true>(y + at[u], v) : store_some(y + at[u], v, n[u]);
     }
+}
+
+// A workgroup has kGU eights a thread of one row.
+template <typename T>
+__global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
+    const uint32_t row = blockIdx.x / a.pieces, first = (blockIdx.x % a.pieces * kGU * kLT + threadIdx.x) * 8;
+    uint32_t at[kGU];
+#pragma unroll
+    for (uint32_t u = 0; u < kGU; ++u) at[u] = first + u * kLT * 8;
+    grad_of<T, kGU>(a, row, at);
+}
+
+// Short rows: threads have an eight each, dealt over the rows one after the other.
+template <typename T>
+__global__ void __launch_bounds__(kLT) logprobs_grad_short_kernel(LpGradArgs a) {
+    const uint32_t i = blockIdx.x * kLT + threadIdx.x, row = i / a.pieces, at = (i - row * a.pieces) * 8;
+    if (row < a.rows) grad_of<T, 1>(a, row, &at);
 }
 
 int32_t check_logits(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
@@ -664,11 +679,17 @@ int32_t logprobs_grad(const void* logits, uint32_t type, uint64_t stride, uint64
     a.logits = logits, a.targets = targets, a.lse = lse, a.dlogp = dlogp, a.entropy = entropy, a.dentropy = dentropy;
     a.dlogits = dlogits, a.stride = stride, a.d_stride = d_stride, a.rows = uint32_t(rows), a.vocab = uint32_t(vocab);
     a.wide_ids = targets_bytes == 8, a.scale = scale;
-    a.pieces = uint32_t((vocab + kLT * 8 * kGU - 1) / (kLT * 8 * kGU));
-    const uint64_t grid = rows * a.pieces;
+    // 10000 x 512 bf16 19.8 us by row, short 11.2; x 1264 21.1 and 14.7, x 2048 (8000)
+    // 18.5 and 18.0, x 4096 (8000) 25.8 and 31.4
+    const bool by_row = vocab >= 2048;
+    const uint64_t unit = by_row ? kLT * 8 * kGU : 8;
+    a.pieces = uint32_t((vocab + unit - 1) / unit);
+    const uint64_t grid = by_row ? rows * a.pieces : (rows * a.pieces + kLT - 1) / kLT;
     if (grid * kLT >= (uint64_t(1) << 32)) return step_fail(DCR_E_INVAL, "too many logits for one launch");
     with_type(type, [&](auto t) {
-        hipLaunchKernelGGL((logprobs_grad_kernel<decltype(t)>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
+        typedef decltype(t) T;
+        const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(uint32_t(grid)), dim3(kLT), 0, st, a); };
+        by_row ? go(logprobs_grad_kernel<T>) : go(logprobs_grad_short_kernel<T>);
     });
     return step_launched();
 }
