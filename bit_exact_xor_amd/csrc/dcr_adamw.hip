@@ -10,7 +10,9 @@
 // 8 bits.  A workgroup takes 512 consecutive elements of a tensor and ends, so
 // small tensors cost a workgroup each and no launch, and what runs at once covers
 // a short stretch of every buffer (176 M elements with fp32 states 803 us; 1024
-// elements 820, in two steps 857; 4096 in four 922).
+// elements 820, in two steps 857; 4096 in four 922).  With states in 8 bits the
+// arithmetic comes near: about 85 instructions an element, where 151 M take 390 us
+// (with the compiler's division and root and every code's two ways 100, and 413).
 //
 // States in 8 bits: blocks of 32 elements under one power of two (an e8m0
 // byte), e4m3 codes; of the second moment the square root is held, whose range
@@ -47,6 +49,17 @@ struct AdamArgs {
     uint32_t key, dither;
 };
 
+// Square root of a number well inside the range, rounded once: the hardware's
+// estimate of its inverse, a step of Newton's iteration for both and the rest put
+// right.
+__device__ __forceinline__ float root_of(float x) {
+    const float y = __builtin_amdgcn_rsqf(x);
+    float s = x * y, h = 0.5f * y;
+    const float e = __fmaf_rn(-h, s, 0.5f);
+    s = __fmaf_rn(s, e, s), h = __fmaf_rn(h, e, h);
+    return __fmaf_rn(__fmaf_rn(-s, s, x), h, s);
+}
+
 // What a workgroup does: everything of its elements in one entry, so that a small
 // tensor's time is two loads behind one another, not three.
 struct DevAdam {
@@ -62,9 +75,9 @@ static_assert(sizeof(DevAdam) == 80, "DevAdam");
 // ratio, which spreads consecutive numbers evenly.
 constexpr uint32_t kGolden = 0x9E3779B1u, kRoot2 = 0x6A09E667u, kRoot3 = 0xBB67AE85u, kRoot5 = 0x3C6EF373u;
 
-// two 16-bit random numbers of element i: low half for m, high half for v
-__device__ __forceinline__ uint32_t dither_of(uint64_t i, uint32_t key) {
-    uint32_t x = uint32_t(i) * kGolden + uint32_t(i >> 32) * kRoot3 + key;
+// two 16-bit random numbers of an element i: low half for m, high half for v.  x:
+// i's low half times kGolden, its high half times kRoot3 and the key, added up.
+__device__ __forceinline__ uint32_t dither_of(uint32_t x) {
     x = (x ^ (x >> 16)) * kRoot2;
     x = (x ^ (x >> 15)) * kRoot5;
     return x ^ (x >> 16);
@@ -134,11 +147,14 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 
 // e4m3 code of magnitude y (at most 448): down to the code below where the rest
 // is less than 1 - r / 65536 of the code's step.  Above 2^-6 the codes are the
-// leading bits of the number itself, below they are multiples of 2^-9.
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t r) {
-    const uint32_t b = __float_as_uint(y);
-    if (b >= 0x3C800000u) return ((b + (r << 4)) >> 20) - (120u << 3);
-    return uint32_t(floorf(__fmaf_rn(y, 512.0f, float(r) * 0x1p-16f)));
+// leading bits of the number itself, below they are multiples of 2^-9.  `some`:
+// a lane of the wave has one below (else its steps are left out).
+constexpr float kLeastNormal = 0x1p-6f;
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t r, bool some) {
+    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - (120u << 3);
+    if (!some) return normal;
+    asm volatile("");                                // (a branch, not both and a choice)
+    return y >= kLeastNormal ? normal : uint32_t(floorf(__fmaf_rn(y, 512.0f, float(r) * 0x1p-16f)));
 }
 
 // largest of the eight lanes of a block
@@ -195,13 +211,26 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamA
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= v[j];
     }
+    bool odd = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float s = g[j] * a.grad_scale;
         m[j] = __fmaf_rn(m[j], a.beta1, s * a.new1);
         v[j] = __fmaf_rn(v[j], a.beta2, s * s * a.new2);
-        w[j] = sqrtf(v[j]);
-        p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] / __fmaf_rn(w[j], a.root, a.eps)));
+        odd |= !(v[j] >= 0x1p-90f && v[j] <= 0x1p90f);
+    }
+    const bool plain = BITS == 8 && !__any(odd);     // (fp32 states: memory alone bounds the step)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (plain) {
+            asm volatile("");                        // (a branch, not both and a choice)
+            w[j] = root_of(v[j]);
+        } else {
+            asm volatile("");
+            w[j] = sqrtf(v[j]);
+        }
+        // (the hardware's reciprocal, one step off, for the division's half)
+        p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] * __builtin_amdgcn_rcpf(__fmaf_rn(w[j], a.root, a.eps))));
     }
     if (n == 4)
         save4<FAR>(pp, p);
@@ -218,24 +247,39 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamA
             save4_some(vp, v, n);
         }
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j >= n) m[j] = w[j] = 0.0f;      // (behind the end)
+        // (behind the end moments and gradients are 0, as a block of zeros has them)
         const uint32_t mb = scale_byte(block_top(m)), wb = scale_byte(block_top(w));
+        float ym[4], yw[4];
+        float least = INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ym[j] = fabsf(ldexpf(m[j], 127 - int(mb))), yw[j] = ldexpf(w[j], 127 - int(wb));
+            least = fminf(least, fminf(ym[j], yw[j]));
+        }
+        const bool some = __any(least < kLeastNormal);
+        uint32_t x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = uint32_t(t.first), hi = uint32_t(t.first >> 32) * kRoot3 + a.key;
+            x[j] = (lo * kGolden + hi) + i * kGolden + j * kGolden;
+            x[j] += i + j > ~lo ? kRoot3 : 0;    // (i + j carry into the high half)
+        }
         uint32_t mq = 0, wq = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t rm = 0x8000u, rw = 0x8000u;
             if (a.dither) {
-                const uint32_t r = dither_of(t.first + i + j, a.key);
+                const uint32_t r = dither_of(x[j]);
                 rm = r & 0xFFFFu, rw = r >> 16;
             }
-            const uint32_t cm = code_of(fabsf(ldexpf(m[j], 127 - int(mb))), rm);
-            uint32_t cw = code_of(ldexpf(w[j], 127 - int(wb)), rw);
+            const uint32_t cm = code_of(ym[j], rm, some);
+            uint32_t cw = code_of(yw[j], rw, some);
             cw = max(cw, w[j] > 0.0f ? 1u : 0u); // (0 would make the next update one of eps)
-            mq |= (mb == 255 ? 0u : cm | (__float_as_uint(m[j]) >> 31) << 7) << (8 * j);
-            wq |= (wb == 255 ? 0u : cw) << (8 * j);
+            mq |= (cm | (__float_as_uint(m[j]) >> 31) << 7) << (8 * j);
+            wq |= cw << (8 * j);
         }
+        if (mb == 255) mq = 0;
+        if (wb == 255) wq = 0;
         if (n == 4) {
             put<FAR>(mq, t.m + i);
             put<FAR>(wq, t.v + i);

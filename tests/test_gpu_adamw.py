@@ -159,6 +159,30 @@ def test_smallest_second_moment_stays():
         assert (T.v[0].view(torch.uint8) >= 1).all()
 
 
+@pytest.mark.parametrize("spread", [0, 14])
+def test_dither_past_32_bits(spread):
+    """Elements whose index passes 32 bits inside a workgroup's, from an odd one on; codes that are all above the smallest
+    normal one (spread 0) and of all sizes.  Moments are exact in 32 bits but for a last rounding, as above."""
+    rng = np.random.default_rng(spread)
+    n, first = 2053, (1 << 32) - 713
+    h = dict(lr=2.0 ** -6, beta1=0.75, beta2=0.875, eps=2.0 ** -20, weight_decay=0.0, grad_scale=1.0)
+    g = rng.choice([1.0, -1.0, 3.0], n) * 2.0 ** rng.integers(-spread, 1, n)
+    T = dcr.AdamWTensors([up(np.ones(n, np.float32))], [up(g.astype(np.float32))], bits=8, first=[first])
+    T.m[0].copy_(up(rng.choice([1.0, -1.5, 2.0], n).astype(np.float32)).to(torch.float8_e4m3fn))
+    T.v[0].copy_(up(rng.choice([1.0, 2.0, 3.0], n).astype(np.float32)).to(torch.float8_e4m3fn))
+    T.m_scales[0].fill_(127 - spread), T.v_scales[0].fill_(127 - spread)
+    m, v = (R.from8(x.view(torch.uint8).cpu().numpy(), y.cpu().numpy())
+            for x, y in ((T.m[0], T.m_scales[0]), (T.v[0], T.v_scales[0])))
+    dcr.dcr_adamw_step(T, 9, dither=5, **h)
+    _p, m, v, _den = formula(np.ones(n), g, m, v * v, 9, *h.values())
+    rm, rv = R.dither(np.arange(n, dtype=np.uint64) + np.uint64(first), 5, 9)
+    for x, r, keep, codes, scales in ((m.astype(np.float32), rm, False, T.m[0], T.m_scales[0]),
+                                      (np.sqrt(v.astype(np.float32)), rv, True, T.v[0], T.v_scales[0])):
+        want, byte = R.to8(x.astype(np.float64), r, keep)
+        assert np.array_equal(scales.cpu().numpy(), byte)
+        assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("bits", [8, 32])
 def test_shards_are_rounded_as_the_whole(bits):
     """A tensor in three shards, with `first`, gives the bits of the whole tensor."""
