@@ -11,7 +11,7 @@
 // small tensors cost a workgroup each and no launch, and what runs at once covers
 // a short stretch of every buffer (176 M elements with fp32 states 803 us; 1024
 // elements 820, in two steps 857; 4096 in four 922).  With states in 8 bits the
-// arithmetic comes near: about 85 instructions an element, where 151 M take 390 us
+// arithmetic comes near: about 80 instructions an element, where 151 M take 390 us
 // (with the compiler's division and root and every code's two ways 100, and 413).
 //
 // States in 8 bits: blocks of 32 elements under one power of two (an e8m0
