@@ -70,6 +70,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
     return x != x ? 0u : b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
 }
+constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_of(-infinity)
 __device__ __forceinline__ float of_order(uint32_t u) {
     return u == 0 ? NAN : __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
@@ -345,11 +346,19 @@ __global__ void __launch_bounds__(kLT, !TOP ? 8 : sizeof(T) == 2 ? 6 : 5) logpro
 
 // The best `top` keys that a wave has met, one a lane, the largest in lane 0.  What
 // few lanes bring is put in one after the other: ranked by a ballot, the lanes
-// behind move up.  Where many lanes pass, as TopLds without barriers: the bound
-// is the top-th largest of the 64 lanes' best keys.  LDS of a wave: the keys held
-// before and after, the lanes' best, what was gathered.
-constexpr uint32_t kFewLanes = 6;
-constexpr uint32_t wave_keys(uint32_t top) { return 2 * DCR_LOGPROBS_MAX_TOP + 64 + top * kMostPer; }
+// behind move up.  Where many lanes pass a bound is taken first, the top-th
+// largest logit of the bests of the 128 halves of the lanes' sixteens, found bit
+// by bit with ballots; what reaches it goes to LDS with the keys held, and ranks
+// are counted.  LDS of a wave: the keys held, then what was gathered, from `top`
+// halves (some more where logits are equal); up to 32 keys whole sixteens serve.
+// (By ranks of the sixteens' best keys the 64 best of 4096 x 16384 took 649 us,
+// where all of them reach the bound, so 103; the 20 best 54 with either.)
+constexpr uint32_t kFewLanes = 10;
+// halves that may reach the bound, some equals among them
+__host__ __device__ constexpr uint32_t most_halves(uint32_t top) { return (top <= 32 ? 2 * top : top) + 16; }
+constexpr uint32_t wave_keys(uint32_t top) {   // an even number, at least 128 behind the keys held
+    return 2 * DCR_LOGPROBS_MAX_TOP + 8 + most_halves(top) * (kPiece / 2);
+}
 
 __device__ __forceinline__ void wave_sync() {      // LDS of one wave is in order, the compiler has to keep it so
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -363,10 +372,29 @@ __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
 
 struct TopWave {
     uint64_t* lds;
-    uint64_t mine, least;                    // the lane's key; that of lane top - 1
+    uint64_t mine, least;                    // the lane's key; that of lane top - 1, or a larger one that `top` keys of the row reach
     uint32_t have;                           // keys held, 0 or `top`
+    // The waves of a workgroup that have parts of one row tell one another the
+    // logit of their share-th key: `top` logits reach the least of these.  Nobody
+    // waits: what is read too early is smaller.
+    volatile uint32_t* told;
+    uint32_t wave, share;
+    u32x4 not_ours;                          // ones for the waves of other rows
 
-    __device__ __forceinline__ explicit TopWave(uint64_t* at) : lds(at), mine(0), least(0), have(0) {}
+    __device__ __forceinline__ TopWave(uint64_t* at, uint32_t* told_, uint32_t wave_, uint32_t from, uint32_t to, uint32_t top)
+        : lds(at), mine(0), least(0), have(0), told(told_), wave(wave_), share(to - from < 2 ? 0 : (top + to - from - 1) / (to - from)) {
+#pragma unroll
+        for (uint32_t w = 0; w < kLWaves; ++w) not_ours[w] = w >= from && w < to ? 0u : ~0u;
+    }
+
+    __device__ __forceinline__ void hear() {
+        const u32x4 t = *reinterpret_cast<volatile u32x4*>(told) | not_ours;
+        const uint32_t low = __builtin_amdgcn_readfirstlane(min(min(t[0], t[1]), min(t[2], t[3])));
+        if (low) least = max(least, (uint64_t(low) << 32) - 1);
+    }
+    __device__ __forceinline__ void tell() {
+        if (share) told[wave] = uint32_t(__builtin_amdgcn_readlane(int(mine >> 32), int(share) - 1));    // (all lanes the same)
+    }
 
     __device__ __forceinline__ void insert(uint64_t key, uint32_t top) {
         const uint32_t lane = threadIdx.x & 63u, at = uint32_t(__popcll(__ballot(mine > key)));
@@ -374,12 +402,17 @@ struct TopWave {
         const uint64_t front = uint64_t(uint32_t(__builtin_amdgcn_update_dpp(0, int(mine >> 32), 0x138, 0xF, 0xF, false))) << 32 |
                                uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(mine)), 0x138, 0xF, 0xF, false));
         mine = lane < at ? mine : lane == at ? key : front;
-        least = lane_value(mine, int(top) - 1);
+        least = max(least, lane_value(mine, int(top) - 1));
     }
 
-    template <typename K>
-    __device__ __forceinline__ void round(uint32_t top, bool passes, const float* v, K&& key) {
+    // LAST: the last bit of order_of that differs between values of the logits' type
+    template <uint32_t LAST, typename K>
+    __device__ __forceinline__ void round(uint32_t top, bool passes, float largest, const float* v, K&& key) {
         const uint32_t lane = threadIdx.x & 63u;
+        if (share && __any(passes)) {
+            hear();
+            passes = passes && order_of(largest) >= uint32_t(least >> 32);
+        }
         const uint32_t some = uint32_t(__popcll(__ballot(passes)));
         if (!some && have) return;
         if (some <= kFewLanes && have) {
@@ -388,51 +421,94 @@ struct TopWave {
             for (int i = 0; i < int(kPiece); ++i) {
                 uint64_t who = __ballot(passes && !(v[i] < low));
                 if (!who) continue;
-                const uint64_t k = key(i);
+                const uint64_t k = key(v[i], i);
                 for (; who; who &= who - 1) {
                     const uint64_t one = lane_value(k, __ffsll((unsigned long long)who) - 1);
                     if (one > least) insert(one, top);
                 }
                 low = of_order(uint32_t(least >> 32));
             }
+            tell();
             return;
         }
-        uint64_t *held = lds, *other = lds + DCR_LOGPROBS_MAX_TOP, *best = other + DCR_LOGPROBS_MAX_TOP, *more = best + 64;
+        uint64_t *held = lds, *more = lds + DCR_LOGPROBS_MAX_TOP;
         uint64_t from = least;
-        if (some > top) {
-            uint64_t b = 0;
+        if (2 * some > top) {                                  // (else there is room for all)
+            uint32_t bound = 0, reach = 0;
+            const auto search = [&](auto&& reached) {          // by how many a logit's order is reached
+#pragma unroll 1
+                for (uint32_t bit = 1u << 31; bit >= LAST; bit >>= 1) {
+                    const uint32_t n = reached(bound | bit);
+                    if (n >= top) bound |= bit, reach = n;
+                }
+            };
+            if (top <= 32) {
+                const uint32_t order = order_of(largest);
+                search([&](uint32_t b) { return uint32_t(__popcll(__ballot(order >= b))); });
+                reach *= 2;
+            } else {
+                float best[2] = {v[0], v[8]};
 #pragma unroll
-            for (int i = 0; i < int(kPiece); ++i) b = max(b, key(i));
-            best[lane] = b;
-            wave_sync();
-            const uint64_t who = __ballot(b && larger(best, 0, 64, 1, b) == top - 1);
-            if (who) from = max(from, lane_value(b, __ffsll((unsigned long long)who) - 1) - 1);
+                for (int i = 1; i < 8; ++i) best[0] = fmaxf(best[0], v[i]), best[1] = fmaxf(best[1], v[8 + i]);
+                const uint32_t order[2] = {order_of(best[0]), order_of(best[1])};
+                search([&](uint32_t b) {
+                    return uint32_t(__popcll(__ballot(order[0] >= b)) + __popcll(__ballot(order[1] >= b)));
+                });
+            }
+            // (-infinity also stands behind the end of a row)
+            if (bound > kMinusInf && reach <= most_halves(top)) {
+                from = max(from, (uint64_t(bound) << 32) - 1);
+            } else {                                           // many equals, or fewer numbers: by whole keys
+                uint64_t b[2] = {};
+#pragma unroll
+                for (int i = 0; i < int(kPiece); ++i) {
+                    float x = v[i];
+                    asm volatile("" : "+v"(x));                // (not kept for what follows: it would take 32 registers)
+                    b[i / 8] = max(b[i / 8], key(x, i));
+                }
+                more[lane] = b[0], more[64 + lane] = b[1];
+                wave_sync();
+                uint32_t ahead[2] = {};
+#pragma unroll 4
+                for (int j = 0; j < 128; ++j) {
+                    const uint64_t k = more[j];
+                    ahead[0] += k > b[0] ? 1u : 0u, ahead[1] += k > b[1] ? 1u : 0u;
+                }
+                wave_sync();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t who = __ballot(b[h] && ahead[h] == top - 1);
+                    if (who) from = max(from, lane_value(b[h], __ffsll((unsigned long long)who) - 1) - 1);
+                }
+            }
         }
         uint32_t n = 0;
         const float low = of_order(uint32_t(from >> 32));
 #pragma unroll
         for (int i = 0; i < int(kPiece); ++i) {
             if (!__ballot(passes && !(v[i] < low))) continue;
-            const uint64_t k = key(i);
+            const uint64_t k = key(v[i], i);
             const bool in = passes && k > from;
             const uint64_t who = __ballot(in);
             if (in) more[n + uint32_t(__popcll(who & ((uint64_t(1) << lane) - 1)))] = k;
             n += uint32_t(__popcll(who));
         }
-        if (lane < have) held[lane] = mine;
-        if (lane < top) other[lane] = 0;                       // (fewer keys than `top` so far)
+        if (lane < have) more[n + lane] = mine;
+        n += have;
+        if (lane < 8) more[n + lane] = 0;                      // (ranks are counted eight at a time)
+        if (lane < top) held[lane] = 0;                        // (fewer keys than `top` so far)
         wave_sync();
-        for (uint32_t i = lane; i < n + have; i += 64) {
-            const uint64_t k = i < n ? more[i] : held[i - n];
-            if (!k) continue;
-            const uint32_t at = larger(more, 0, n, 1, k) + larger(held, 0, have, 1, k);
-            if (at < top) other[at] = k;
+        for (uint32_t i = lane; i < n; i += 64) {
+            const uint64_t k = more[i];
+            const uint32_t at = larger(more, 0, (n + 7) / 8 * 8, 1, k);
+            if (k && at < top) held[at] = k;
         }
         wave_sync();
-        mine = lane < top ? other[lane] : 0;
+        mine = lane < top ? held[lane] : 0;
         wave_sync();
         have = top;
-        least = lane_value(mine, int(top) - 1);
+        least = max(least, lane_value(mine, int(top) - 1));
+        tell();
     }
 };
 
@@ -442,13 +518,19 @@ __global__ void __launch_bounds__(kLT, TOP ? 6 : 8) logprobs_wave_kernel(LpArgs 
     extern __shared__ uint64_t wave_lds[];
     const uint32_t unit_of = __builtin_amdgcn_readfirstlane(blockIdx.x * kLWaves + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
     const uint32_t row = unit_of / a.parts, part = unit_of % a.parts;
+    uint32_t* told = reinterpret_cast<uint32_t*>(wave_lds + kLWaves * wave_keys(a.top));
+    if constexpr (TOP) {
+        if (threadIdx.x < kLWaves) told[threadIdx.x] = 0;
+        __syncthreads();
+    }
     if (row >= a.rows) return;
     const uint32_t from = part * a.part_len, to = min(a.vocab, from + a.part_len);
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
     const float unit = a.scale * kLog2e;
     constexpr uint32_t STEP = 64 * kPiece;
     Sums sum = {-INFINITY, 0.0f, 0.0f};
-    TopWave best(wave_lds + (threadIdx.x >> 6) * wave_keys(a.top));
+    const uint32_t wave = unit_of % kLWaves;
+    TopWave best(wave_lds + wave * wave_keys(a.top), told, wave, wave - min(wave, part), min(kLWaves, wave + a.parts - part), a.top);
     Raw8<T> raw[2];
     load_step<64>(x, from, to, raw);
     for (uint32_t c0 = from; c0 < to; c0 += STEP) {
@@ -459,9 +541,9 @@ __global__ void __launch_bounds__(kLT, TOP ? 6 : 8) logprobs_wave_kernel(LpArgs 
         [[maybe_unused]] const float top = add_step(v, unit, c0 + STEP > to, sum);
         if constexpr (TOP) {
             const bool passes = best.least == 0 ? c0 + lane * 8 < to : order_of(top) >= uint32_t(best.least >> 32);
-            best.round(a.top, passes, v, [&](int i) {
+            best.template round<sizeof(T) == 2 ? 1u << 16 : 1u>(a.top, passes, top, v, [&](float x, int i) {
                 const uint32_t j = c0 + ((i / 8) * 64 + lane) * 8 + i % 8;
-                return j < to ? key_of(v[i], j) : 0;
+                return j < to ? key_of(x, j) : 0;
             });
         }
     }
@@ -625,18 +707,20 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
     a.rows = uint32_t(rows), a.vocab = uint32_t(vocab), a.top = top, a.wide_ids = targets_bytes == 8, a.scale = scale;
     // Who takes a row (us; `top` 0 and 20).  A wave, where a row is one step of
     // it (16384 x 1000: 12 and 29, a workgroup 33 and 95) or rows fill the GPU
-    // (4096 x 16384: 28 and 57, a workgroup 29 and 67; of longest rows only with
-    // `top`: 4096 x 151936 214 and 273, a workgroup 205 and 373); several, so that
-    // 4096 run, where fewer rows are long (1024 x 151936: 57 and 107, workgroups
-    // 61 and 131; but 1024 x 32000 18 and 48, workgroups 16 and 40).  Else at
-    // least 1024 workgroups, each with a step or more (8 x 151936: 6.5 and 14 in
-    // 38 parts, 8.2 and 27 in 10; 256 rows 21, in 512 workgroups 24).
+    // (4096 x 16384: 26 and 54, a workgroup 29 and 67; of longest rows only with
+    // `top`: 4096 x 151936 214 and 273, a workgroup 197 and 373); several, so that
+    // 4096 run, where fewer rows are long (1024 x 151936: 60 and 91, workgroups
+    // 61 and 131; but 1024 x 32000 18, workgroups 16) and, with `top`, of 256 rows
+    // or more (256 x 151936: 42, workgroups 48; 512 x 32000: 28.6 and 29.5; but 2500
+    // x 20000, a wave each, 55 and 51).  Else at least 1024 workgroups, each with a
+    // step or more (8 x 151936: 6.5 and 14 in 38 parts, 8.2 and 27 in 10; 256 rows
+    // without `top` 21, in 512 workgroups 24).
     const bool is_long = vocab >= 65536;
     bool by_wave = vocab <= 64 * kPiece;
     uint64_t parts = 1;
     if (!by_wave) {
-        by_wave = rows >= 4096 ? top || !is_long : rows >= 1024 && is_long;
-        const uint64_t step = kLT * kPiece;
+        by_wave = rows >= 4096 ? top || !is_long : (rows >= 1024 && is_long) || (top && rows >= 256 && rows <= 1024);
+        const uint64_t step = (by_wave && top ? 64 : kLT) * kPiece;
         parts = std::min<uint64_t>(by_wave ? 4096 / rows : (1024 + rows - 1) / rows, (vocab + step - 1) / step);
         if (top) parts = std::min<uint64_t>(parts, kMostKeys / top);
         parts = std::max<uint64_t>(1, std::min<uint64_t>(parts, kMostParts / rows));
@@ -653,7 +737,7 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
             constexpr bool TOP = decltype(some)::value;
             if (by_wave)
                 hipLaunchKernelGGL((logprobs_wave_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT),
-                                   TOP ? kLWaves * wave_keys(top) * 8 : 0, st, a);
+                                   TOP ? kLWaves * wave_keys(top) * 8 + sizeof(u32x4) : 0, st, a);
             else
                 hipLaunchKernelGGL((logprobs_kernel<decltype(t), TOP>), dim3(uint32_t(grid)), dim3(kLT), 0, st, a);
             if (parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<decltype(t), TOP>), dim3(a.rows), dim3(kLT), 0, st, a);

@@ -219,6 +219,28 @@ def test_grad_of_odd_targets():
     assert (d[0] == 0).all() and torch.isnan(d[3]).all() and not torch.isnan(d[1:3]).any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,vocab", [(4, 700), (300, 5000), (5000, 1100)])
+def test_top_of_rows_with_nan(rows, vocab, dtype):
+    """Numbers first, -infinity behind them, then NaN by their indices; rows of all NaN, of nearly nothing else, with equals
+    at the end of what is asked for."""
+    rng = np.random.default_rng(vocab)
+    x = np.round(rng.standard_normal((rows, vocab)) * 4) / 4
+    x[0] = np.nan
+    x[1] = np.where(rng.random(vocab) < 0.98, np.nan, x[1])
+    x[2, : vocab - 30] = np.nan
+    x[3, 30:] = -np.inf
+    x[3, 40: vocab // 2] = np.nan
+    logits = up(x.astype(np.float32)).to(TYPES[dtype])
+    order = np.lexsort((np.arange(vocab)[None].repeat(rows, 0), -(np.nan_to_num(x, nan=-np.inf) + 0.0), np.isnan(x)), axis=1)
+    for top in (1, 20, 33, 64):
+        ids, vals = torch.empty(rows, top, dtype=torch.int32, device="cuda"), torch.empty(rows, top, device="cuda")
+        dcr.dcr_logprobs(logits, None, top_ids=ids, top_values=vals, workspace=dcr.step_workspace())
+        assert np.array_equal(ids.cpu().numpy(), order[:, :top])
+        nan = torch.isnan(vals)
+        assert nan[:4][[0, 1, 2, 3]].all() and not nan[4:].any()
+
+
 def test_rows_past_32_bits():
     """A row that begins more than 2^32 elements into its matrix."""
     pool = torch.zeros((1 << 32) + (1 << 13), dtype=torch.bfloat16, device="cuda")
@@ -239,7 +261,8 @@ def test_rows_past_32_bits():
 
 
 # rows and vocabulary so that a row goes to one wave, to several, to one workgroup, to several
-SPLITS = [(4100, 1500), (4097, 66000), (1100, 65600), (2048, 65536), (2100, 65544), (4095, 65537), (1500, 9001), (1023, 70000)]
+SPLITS = [(4100, 1500), (4097, 66000), (1100, 65600), (2048, 65536), (2100, 65544), (4095, 65537), (1500, 9001), (1023, 70000),
+          (256, 40001), (341, 33333), (700, 2047), (1024, 1025), (1025, 20000)]
 
 
 @pytest.mark.parametrize("rows,vocab", SPLITS)
