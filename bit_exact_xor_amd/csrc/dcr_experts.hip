@@ -8,10 +8,11 @@
 // The choice is that of 64 bits: the values of experts next to one another often
 // differ by less than the rounding of 32, and a choice that depended on it would
 // differ from one program to the next.  32 bits decide what they can: a bound
-// that the k best values surely reach (the k-th of the lanes' largest) leaves
-// little more than k candidates a row, and those alone, one a lane, are computed
-// and ranked in 64.  (All experts in 64 bits took 20 us for 16384 rows of 256
-// where this takes 12; 32 bits with a second look at close rows 13 to 18, since a
+// that the k best values surely reach (the k-th of the largest of the lanes'
+// halves; of whole lanes' largest 24 of 128 took 39 us for 16000 rows, so 15)
+// leaves little more than k candidates a row, and those alone, one a lane, are
+// computed and ranked in 64.  (All experts in 64 bits took 20 us for 16384 rows of
+// 256 where this takes 11; 32 bits with a second look at close rows 13 to 18, since a
 // launch waits for its few second looks.)
 #include <algorithm>
 
@@ -21,7 +22,6 @@ namespace dcr {
 namespace {
 
 constexpr uint32_t kET = 256;                     // threads of a workgroup
-constexpr uint32_t kAnyGroups = 31;
 
 struct SelectArgs {
     const void* logits;
@@ -32,8 +32,8 @@ struct SelectArgs {
     void* dlogits;
     uint64_t stride, d_stride;
     uint32_t rows, experts, k, groups, top_groups, sigmoid, renormalize;
-    uint32_t group_log2;      // a group is 8 << group_log2 experts, or (kAnyGroups) any number
-    uint32_t share_log2;      // lanes of a group then
+    uint32_t group_log2;      // a group is looked at by 1 << group_log2 lanes
+    uint32_t whole;           // its experts are theirs
     float scale;
 };
 
@@ -131,9 +131,10 @@ __device__ __forceinline__ uint32_t lanes_upto(uint32_t v, uint32_t lane) {
 }
 
 // The two largest values of a lane's part of a group, and over STEP lanes more.
+template <typename V>
 struct Two {
-    double first, second;
-    __device__ __forceinline__ void meet(double f, double s) {
+    V first, second;
+    __device__ __forceinline__ void meet(V f, V s) {
         second = fmax(fmin(first, f), fmax(second, s));
         first = fmax(first, f);
     }
@@ -141,7 +142,7 @@ struct Two {
     __device__ __forceinline__ void fold(uint32_t lanes) {
         if constexpr (STEP < LANES) {
             if (lanes > STEP) {
-                double f[2], s[2];
+                V f[2], s[2];
                 partners_of<STEP>(first, &f[0], &f[1]);
                 partners_of<STEP>(second, &s[0], &s[1]);
                 first = f[0], second = s[0];
@@ -150,11 +151,54 @@ struct Two {
             fold<2 * STEP, LANES>(lanes);
         }
     }
-    // 0 where the group has nothing open
-    __device__ __forceinline__ uint64_t key(uint32_t group) const {
-        return first == -INFINITY ? 0 : key_of(rank_of(second == -INFINITY ? first : first + second), group);
-    }
+    __device__ __forceinline__ bool none() const { return first == -INFINITY; }      // nothing is open
+    __device__ __forceinline__ V value() const { return second == -INFINITY ? first : first + second; }
 };
+
+// The two largest of each group, in all of its lanes, from values c of the lane's
+// experts (-infinity where shut).  Groups that are not whole lanes go through LDS.
+// odd: there is a NaN among what the lane has seen.
+template <int LANES, int N, typename V>
+__device__ __forceinline__ Two<V> two_of_groups(const SelectArgs& a, const V* c, uint32_t lane, V* lds, bool* odd) {
+    Two<V> two = {-INFINITY, -INFINITY};
+    *odd = false;
+    if (a.whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) two.meet(c[i], -INFINITY), *odd |= c[i] != c[i];
+    } else {
+        const uint32_t size = a.experts / a.groups, mine = lane >> a.group_log2, share = 1u << a.group_log2;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (expert_of<LANES>(lane, i) < a.experts) lds[expert_of<LANES>(lane, i)] = c[i];
+        wave_sync();
+        if (mine < a.groups) {
+            for (uint32_t i = lane & (share - 1); i < size; i += share) {
+                const V x = lds[mine * size + i];
+                two.meet(x, -INFINITY), *odd |= x != x;
+            }
+        }
+        wave_sync();
+    }
+    two.template fold<1, LANES>(1u << a.group_log2);
+    return two;
+}
+
+// Ranks to 0 outside the groups that are `in` (a group's lanes say the same).
+template <int LANES, int N>
+__device__ __forceinline__ void shut_groups(const SelectArgs& a, uint32_t lane, bool in, uint32_t* rank) {
+    if (a.whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) rank[i] = in ? rank[i] : 0;
+        return;
+    }
+    const uint64_t taken = __ballot(in) >> (threadIdx.x & 63u & ~uint32_t(LANES - 1));
+    const float inv = 1.0f / float(a.experts / a.groups);      // (e + 1/2 over the size is further from a whole number than its rounding)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t e = expert_of<LANES>(lane, i), g = uint32_t((float(e) + 0.5f) * inv);
+        rank[i] = e < a.experts && (taken >> (g << a.group_log2) & 1) ? rank[i] : 0;
+    }
+}
 
 // The groups' choice in 32 bits.  Shuts experts (ranks to 0) and returns whether
 // what decides is certain.  A value is off by `off` and 2^-24 of itself, and so
@@ -166,150 +210,39 @@ struct Two {
 template <int LANES, int N>
 __device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* c, uint32_t lane, float off, float* lds,
                                               uint32_t* rank) {
-    struct {
-        float first, second;
-        __device__ __forceinline__ void meet(float f, float s) {
-            second = fmaxf(fminf(first, f), fmaxf(second, s));
-            first = fmaxf(first, f);
-        }
-    } two;
-    const auto fold = [&](auto step, uint32_t lanes) {
-        constexpr int S = decltype(step)::value;
-        if constexpr (S < LANES) {
-            if (lanes > S) {
-                float f[2], s[2];
-                partners_of<S>(two.first, &f[0], &f[1]);
-                partners_of<S>(two.second, &s[0], &s[1]);
-                two.first = f[0], two.second = s[0];
-                two.meet(f[1], s[1]);
-            }
-        }
-    };
-    const auto value = [&](uint32_t lanes) {       // of the group that lies in so many lanes
-        fold(std::integral_constant<int, 1>(), lanes), fold(std::integral_constant<int, 2>(), lanes);
-        fold(std::integral_constant<int, 4>(), lanes), fold(std::integral_constant<int, 8>(), lanes);
-        fold(std::integral_constant<int, 16>(), lanes), fold(std::integral_constant<int, 32>(), lanes);
-        return two.first == -INFINITY ? 0 : rank32(two.second == -INFINITY ? two.first : two.first + two.second);
-    };
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) odd |= c[i] != c[i];
-    two.first = two.second = -INFINITY;
-    uint32_t least, most = 0;                      // of the groups taken, of the others
-    if (a.group_log2 < kAnyGroups) {
-        // groups of whole lanes, a power of two of them: all groups at once
-#pragma unroll
-        for (int i = 0; i < N; ++i) two.meet(c[i], -INFINITY);
-        const uint32_t of = value(1u << a.group_log2);
-        const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
-        uint32_t ahead = 0;
-        for (uint32_t g = 0; g < a.groups; ++g) {
-            const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.group_log2)), 64));
-            ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
-        }
-        const bool in = ahead < a.top_groups;      // (lanes behind the last group are shut, and last)
-        least = lanes_all<LANES>(in && mine < a.groups ? of : ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
-        most = lanes_all<LANES>(in ? 0u : of, [](uint32_t x, uint32_t y) { return max(x, y); });
-#pragma unroll
-        for (int i = 0; i < N; ++i) rank[i] = in ? rank[i] : 0;
-    } else {
-        // groups of any size, at most one for each lane: through LDS, the lanes
-        // dealt to groups in shares of a power of two
-        const uint32_t size = a.experts / a.groups, share = 1u << a.share_log2;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (expert_of<LANES>(lane, i) < a.experts) lds[expert_of<LANES>(lane, i)] = c[i];
-        wave_sync();
-        const uint32_t mine = lane >> a.share_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
-        if (mine < a.groups)
-            for (uint32_t i = lane & (share - 1); i < size; i += share) two.meet(lds[mine * size + i], -INFINITY);
-        wave_sync();
-        const uint32_t of = value(share);
-        uint32_t ahead = 0;
-        for (uint32_t g = 0; g < a.groups; ++g) {
-            const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.share_log2)), 64));
-            ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
-        }
-        const bool in = mine < a.groups && ahead < a.top_groups;
-        least = lanes_all<LANES>(in ? of : ~0u, [](uint32_t x, uint32_t y) { return min(x, y); });
-        most = lanes_all<LANES>(in ? 0u : of, [](uint32_t x, uint32_t y) { return max(x, y); });
-        const uint64_t taken = __ballot(in) >> base;
-        const float inv = 1.0f / float(size);      // ((e + 1/2) / size is at least 1/2 / size from a whole number: far more than its error)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t e = expert_of<LANES>(lane, i), g = uint32_t((float(e) + 0.5f) * inv);
-            rank[i] = e < a.experts && (taken >> (g << a.share_log2) & 1) ? rank[i] : 0;
-        }
+    bool odd;
+    const Two<float> two = two_of_groups<LANES, N>(a, c, lane, lds, &odd);
+    const uint32_t of = two.none() ? 0 : rank32(two.value());
+    const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
+    uint32_t ahead = 0;
+    for (uint32_t g = 0; g < a.groups; ++g) {
+        const uint32_t o = uint32_t(__shfl(int(of), int(base + (g << a.group_log2)), 64));
+        ahead += (o > of || (o == of && g < mine)) ? 1u : 0u;
     }
-    const float x = of_rank32(least), y = of_rank32(most);
+    const bool in = mine < a.groups && ahead < a.top_groups;
+    const auto of_lanes = [](auto v, auto f) { return lanes_all<LANES>(v, f); };
+    const float x = of_rank32(of_lanes(in ? of : ~0u, [](uint32_t p, uint32_t q) { return min(p, q); }));      // least taken
+    const uint32_t most = of_lanes(in || mine >= a.groups ? 0u : of, [](uint32_t p, uint32_t q) { return max(p, q); });
     const float far = fmaxf(two.first == -INFINITY ? 0.0f : fabsf(two.first), two.second == -INFINITY ? 0.0f : fabsf(two.second));
-    float apart = fmaf(0x1p-20f, lanes_all<LANES>(far, [](float p, float q) { return fmaxf(p, q); }), 5 * off);
+    float apart = fmaf(0x1p-20f, of_lanes(far, [](float p, float q) { return fmaxf(p, q); }), 5 * off);
     if (!a.bias) apart = fminf(apart, fmaf(0x1p-15f, x, 0x1p-120f));
-    return !odd && (most == 0 || x - y > apart);
+    shut_groups<LANES, N>(a, lane, in, rank);
+    return !odd && (most == 0 || x - of_rank32(most) > apart);
 }
 
-// The same in 64 bits, groups of any number and size.  c: the lane's s + bias,
-// -infinity where shut.
+// The same in 64 bits; a NaN's group goes first.
 template <int LANES, int N>
-__device__ __forceinline__ void take_groups(const SelectArgs& a, const double* c, uint32_t lane, uint32_t* rank) {
-    const uint32_t size = a.experts / a.groups;
-    bool odd = false;                              // a NaN in the lane's part: its group goes first
-    if (a.group_log2 < kAnyGroups) {
-        // groups of whole lanes, a power of two of them: all groups at once
-        Two two = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < N; ++i) two.meet(c[i], -INFINITY), odd |= c[i] != c[i];
-        two.template fold<1, LANES>(1u << a.group_log2);
-        const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
-        const uint64_t odds = __ballot(odd) >> (base + (mine << a.group_log2));
-        uint64_t of = two.key(mine);
-        if (odds & ((uint64_t(2) << ((1u << a.group_log2) - 1)) - 1)) of = key_of(~uint64_t(0), mine);
-        uint32_t ahead = 0;
-        for (uint32_t g = 0; g < a.groups; ++g)
-            ahead += uint64_t(__shfl((unsigned long long)of, int(base + (g << a.group_log2)), 64)) > of ? 1u : 0u;
-        if (!of || ahead >= a.top_groups) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) rank[i] = 0;
-        }
-        return;
-    }
-    // groups of any size, one after the other over all lanes; a lane keeps the
-    // groups lane, lane + LANES, ... in mind
-    constexpr int KEEP = DCR_EXPERTS_MAX_GROUPS / LANES;
-    uint64_t of[KEEP];
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q) of[q] = 0;
-    for (uint32_t g = 0; g < a.groups; ++g) {
-        Two two = {-INFINITY, -INFINITY};
-        odd = false;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const bool in = expert_of<LANES>(lane, i) - g * size < size;
-            two.meet(in ? c[i] : -INFINITY, -INFINITY);
-            odd |= in && c[i] != c[i];
-        }
-        two.template fold<1, LANES>(LANES);
-        const uint32_t odds = lanes_all<LANES>(odd ? 1u : 0u, [](uint32_t x, uint32_t y) { return x | y; });
-#pragma unroll
-        for (int q = 0; q < KEEP; ++q)
-            if (g == lane + q * LANES) of[q] = odds ? key_of(~uint64_t(0), g) : two.key(g);
-    }
-    // the top_groups largest, as bits
-    uint64_t in = 0;
-    for (uint32_t n = 0; n < a.top_groups; ++n) {
-        uint64_t mine = of[0];
-#pragma unroll
-        for (int q = 1; q < KEEP; ++q) mine = mine > of[q] ? mine : of[q];
-        const uint64_t best = lanes_all<LANES>(mine, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
-        if (best) in |= uint64_t(1) << index_of(best);
-#pragma unroll
-        for (int q = 0; q < KEEP; ++q) of[q] = of[q] == best ? 0 : of[q];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint32_t e = expert_of<LANES>(lane, i);
-        if (e >= a.experts || !(in >> (e / size) & 1)) rank[i] = 0;
-    }
+__device__ __forceinline__ void take_groups(const SelectArgs& a, const double* c, uint32_t lane, double* lds, uint32_t* rank) {
+    bool odd;
+    const Two<double> two = two_of_groups<LANES, N>(a, c, lane, lds, &odd);
+    const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
+    uint64_t of = two.none() || mine >= a.groups ? 0 : key_of(rank_of(two.value()), mine);
+    const uint64_t odds = __ballot(odd) >> (base + (mine << a.group_log2));
+    if (odds & ((uint64_t(2) << ((1u << a.group_log2) - 1)) - 1)) of = key_of(~uint64_t(0), mine);
+    uint32_t ahead = 0;
+    for (uint32_t g = 0; g < a.groups; ++g)
+        ahead += uint64_t(__shfl((unsigned long long)of, int(base + (g << a.group_log2)), 64)) > of ? 1u : 0u;
+    shut_groups<LANES, N>(a, lane, of && ahead < a.top_groups, rank);
 }
 
 // scores of a row in 64 bits for the comparisons
@@ -388,8 +321,7 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
             uint32_t all[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) all[i] = rank[i];
-            const bool few = a.group_log2 < kAnyGroups || a.groups <= LANES;
-            if (!few || __any(!take_groups32<LANES, N>(a, c, lane, off, reinterpret_cast<float*>(keys), rank))) {
+            if (__any(!take_groups32<LANES, N>(a, c, lane, off, reinterpret_cast<float*>(keys), rank))) {
                 double d[N];
                 double z = inverse;
                 if (!a.sigmoid && !a.bias && a.renormalize) z = softmax_inverse<LANES, N>(v, top);
@@ -399,23 +331,28 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
                     d[i] = a.sigmoid ? inverse_near(1.0 + exp_near(-double(v[i]))) : exp_near(double(v[i]) - double(top)) * z;
                     d[i] = v[i] == -INFINITY ? -INFINITY : (v[i] != v[i] || top != top) ? NAN : d[i] + double(bias[i]);
                 }
-                take_groups<LANES, N>(a, d, lane, rank);
+                take_groups<LANES, N>(a, d, lane, reinterpret_cast<double*>(keys), rank);
             }
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) rank[i] = v[i] == -INFINITY ? 0 : rank32(v[i]);
     }
-    // the k-th largest of the lanes' largest ranks (or, with equals among them,
-    // one below): at least k experts reach it
+    // the k-th largest of the largest ranks of the lanes' halves (or, with equals
+    // among them, one below): at least k experts reach it
     uint32_t bound = 0;
-    if (a.k <= LANES) {
-        uint32_t mine = rank[0];
+    if (a.k <= 2 * LANES) {
+        uint32_t mine = rank[0], next = rank[N / 2];
 #pragma unroll
-        for (int i = 1; i < N; ++i) mine = max(mine, rank[i]);
+        for (int i = 1; i < N / 2; ++i) mine = max(mine, rank[i]), next = max(next, rank[N / 2 + i]);
+        if (mine < next) {
+            const uint32_t less = mine;
+            mine = next, next = less;
+        }
         for (uint32_t j = 0; j < a.k; ++j) {
             bound = lanes_all<LANES>(mine, [](uint32_t x, uint32_t y) { return max(x, y); });
-            mine = mine == bound ? 0 : mine;
+            const bool out = mine == bound;
+            mine = out ? next : mine, next = out ? 0 : next;
         }
         if (a.bias && bound && bound != ~0u) {     // and in 64 bits at least this
             const float x = of_rank32(bound);
@@ -731,8 +668,8 @@ __global__ void __launch_bounds__(kOT) experts_place_kernel(OrderArgs a) {
 
 // f(lanes, registers of eight) for rows of n elements, of which k are taken: the
 // fewest lanes that hold a row, or one for each that is taken while the rows leave
-// lanes without work (24 of 128 for 4000 rows 16 us, with the 16 lanes that hold
-// them 27 us; 16000 rows 39 us with either)
+// lanes without work (24 of 128 for 1000 rows 7.8 us, with the 16 lanes that hold
+// them 10.5 us; 16000 rows 15 us with either)
 template <typename F>
 void with_lanes(uint32_t n, uint32_t k, uint64_t rows, F&& f) {
     const std::integral_constant<int, 1> one;
@@ -773,16 +710,14 @@ int32_t select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows
     a.logits = logits, a.bias = bias, a.ids = ids, a.weights = weights, a.stride = stride;
     a.rows = uint32_t(rows), a.experts = experts, a.k = k, a.groups = groups, a.top_groups = top_groups;
     a.sigmoid = score == DCR_SCORE_SIGMOID, a.renormalize = options & DCR_EXPERTS_RENORMALIZE, a.scale = scale;
-    if (top_groups < groups) {
-        const uint32_t size = experts / groups;
-        while ((8u << a.group_log2) < size) ++a.group_log2;
-        if (experts > 512 || (8u << a.group_log2) != size) a.group_log2 = kAnyGroups;
-    }
+    const uint32_t size = experts / groups;
+    a.whole = experts <= 512 && size % 8 == 0 && !(size & (size - 1));
     with_type(type, [&](auto t) {
-        with_lanes(experts, k, rows, [&](auto lanes, auto r) {
+        // (at least a lane for each group)
+        with_lanes(std::max(experts, top_groups < groups ? groups * 8 : 0), k, rows, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
-            a.share_log2 = 0;
-            while ((2u << a.share_log2) * groups <= uint32_t(L)) ++a.share_log2;
+            a.group_log2 = 0;
+            while (a.whole ? (8u << a.group_log2) < size : (2u << a.group_log2) * groups <= uint32_t(L)) ++a.group_log2;
             const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
             hipLaunchKernelGGL((experts_select_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET),
                                ROWS * select_lds(experts, k), st, a);
