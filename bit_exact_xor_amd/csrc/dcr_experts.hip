@@ -255,19 +255,21 @@ __device__ __forceinline__ double softmax_inverse(const float* v, float top) {
     return z == 0.0 ? 0.0 : 1.0 / z;
 }
 
-// LDS of a row: its candidates' keys and logits, the chosen ones
-__host__ __device__ inline uint32_t select_lds(uint32_t experts, uint32_t k) { return (12 * (experts + k) + 7) / 8 * 8; }
+// LDS of a row: its candidates, the chosen ones
+__host__ __device__ inline uint32_t select_lds(uint32_t experts, uint32_t k) { return (8 * experts + 12 * k + 7) / 8 * 8; }
 
+// (Held to the registers of eight waves a SIMD: 16384 x 256 in groups 14.0 us, with
+// seven 14.9; 8 bytes of LDS an expert, not 12, so that they fit: 16000 x 1024 20
+// us for 24.)
 template <typename T, int LANES, int R>
-__global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(SelectArgs a) {
     constexpr int N = 8 * R, ROWS = kET / LANES;
     constexpr float kLog2e = 1.44269504088896340736f;
     extern __shared__ uint64_t lds[];
     const uint32_t lane = threadIdx.x % LANES, in_wg = threadIdx.x / LANES;
     uint64_t* keys = lds + in_wg * (select_lds(a.experts, a.k) / 8);
     double* weights = reinterpret_cast<double*>(keys + a.experts);
-    float* found = reinterpret_cast<float*>(weights + a.k);
-    int32_t* ids = reinterpret_cast<int32_t*>(found + a.experts);
+    int32_t* ids = reinterpret_cast<int32_t*>(weights + a.k);
     const uint32_t at = blockIdx.x * ROWS + in_wg;
     const bool live = at < a.rows;
     const T* row = static_cast<const T*>(a.logits) + uint64_t(live ? at : 0) * a.stride;
@@ -369,13 +371,15 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
     uint32_t to = upto - count;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (rank[i] >= bound) found[to] = v[i], keys[to] = expert_of<LANES>(lane, i);
+        if (rank[i] >= bound) keys[to] = uint64_t(__float_as_uint(v[i])) << 32 | expert_of<LANES>(lane, i);
         to += rank[i] >= bound ? 1u : 0u;
     }
     wave_sync();
+    float first = 0.0f;                        // the logit of the lane's first candidate (there are seldom more)
     for (uint32_t i = lane; i < n; i += LANES) {
         const uint32_t e = uint32_t(keys[i]);
-        const float l = found[i];
+        const float l = __uint_as_float(uint32_t(keys[i] >> 32));
+        first = i == lane ? l : first;
         uint64_t key;
         if (a.bias) {
             double c = a.sigmoid ? inverse_near(1.0 + exp_near(-double(l))) : exp_near(double(l) - double(top)) * inverse;
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(kET) experts_select_kernel(SelectArgs a) {
 #pragma unroll 4
         for (uint32_t j = 0; j < n; ++j) ahead += keys[j] > mine ? 1u : 0u;
         if (ahead < a.k) {
-            const double l = double(found[i]);
+            const double l = double(i == lane ? first : wide(row[index_of(mine)]));
             ids[ahead] = int32_t(index_of(mine));
             weights[ahead] = a.sigmoid ? sigmoid64(l) : exp(l - double(top)) * (a.renormalize ? 1.0 : inverse);
         }
