@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
         for (int i = 1; i < N; ++i) top = (v[i] > top || v[i] != v[i]) ? v[i] : top;
         top = lanes_max<LANES>(top);
         if (top == -INFINITY) top = 0.0f;      // every expert is shut
+        if (top == INFINITY) top = NAN;        // infinity less itself: no score of the row is a number, as with a NaN
     }
     // Ranks in 32 bits.  A sigmoid by the hardware's exponential and reciprocal
     // (one step off each) is off by less than 2.3 * 2^-23 and a sum with the bias
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
     if (!live) return;
     for (uint32_t j = lane; j < a.k; j += LANES) {
         a.ids[uint64_t(at) * a.k + j] = ids[j];
-        a.weights[uint64_t(at) * a.k + j] = float(weights[j] / all * double(a.scale));
+        a.weights[uint64_t(at) * a.k + j] = ids[j] < 0 ? 0.0f : float(weights[j] / all * double(a.scale));      // (`all` may be NaN)
     }
 }
 

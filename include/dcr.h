@@ -718,7 +718,9 @@ enum { DCR_EXPERTS_RENORMALIZE = 1 };
  * 1 <= k <= min(64, experts).  The choice is that of 64-bit arithmetic (sums that
  * differ by less than 2^-42 of themselves count as equal); without a bias experts
  * are compared by their logits.  A NaN among the values compared
- * counts as the largest, and makes weights NaN. */
+ * counts as the largest, and makes weights NaN.  A softmax of a row with a NaN or
+ * +infinity is NaN for all of its open experts (with a bias or groups those are
+ * then equals); a sigmoid of +infinity is 1. */
 int32_t dcr_experts_select(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint32_t experts,
                            const float* bias, uint32_t score, uint32_t groups, uint32_t top_groups, uint32_t options,
                            float scale, uint32_t k, int32_t* ids, float* weights, void* stream);

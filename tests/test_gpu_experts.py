@@ -426,3 +426,61 @@ def test_rows_of_many_tokens(tokens, width, k):
         terms = b * z[a].float()
         assert ((dw[h, j].double() - terms.double().sum(1)).abs() <= (width / 64 + 17) * 2.0 ** -24 * terms.abs().sum(1)).all()
         assert (dw[~h, j] == 0).all()
+
+
+def by_definition(x, bias, k, sigmoid, groups=1, top_groups=1, renormalize=False):
+    """As step_ref.select, of rows with infinities and NaN: a NaN counts as the largest of what is compared, the lowest index
+    of equals first, a group's value is the sum of its two largest above -infinity, ids of -1 have weight 0."""
+    first = lambda v, i: (not np.isnan(v), -(0.0 if np.isnan(v) else v), i)  # noqa: E731
+    x = x.astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        s = R.scores(x, sigmoid)
+        value = s + (0 if bias is None else bias.astype(np.float64))
+    rows, e = x.shape
+    size = e // groups
+    ids, w = np.full((rows, k), -1), np.zeros((rows, k))
+    for r in range(rows):
+        taken = range(groups)
+        if top_groups < groups:
+            of = []
+            for g in range(groups):
+                best = sorted((first(value[r, i], i) for i in range(g * size, (g + 1) * size)
+                               if not np.isneginf(x[r, i]) and not np.isneginf(value[r, i])))[:2]
+                of.append(sum(value[r, i] for _n, _v, i in best) if best else -np.inf)
+            taken = sorted(range(groups), key=lambda g: first(of[g], g))[:top_groups]
+        rank = x[r] if bias is None else value[r]
+        best = sorted((first(rank[i], i) for i in range(e) if not np.isneginf(x[r, i]) and i // size in set(taken)))[:k]
+        ids[r, :len(best)] = [i for _n, _v, i in best]
+        w[r, :len(best)] = s[r, ids[r, :len(best)]]
+        if renormalize and w[r].sum() != 0:
+            w[r, :len(best)] /= w[r].sum()
+    return ids, w
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("e,k,groups,top_groups", [(40, 6, 1, 1), (64, 8, 8, 3), (200, 12, 1, 1), (456, 10, 8, 3), (1000, 20, 40, 7)])
+def test_select_of_infinite_and_nan_logits(e, k, groups, top_groups, dtype):
+    """A softmax of a row with +infinity or NaN has no numbers: all weights of its chosen experts are NaN, and where scores
+    are compared (a bias, groups) all are equal.  A sigmoid of +infinity is 1.  (A weight is rounded once, as above.)"""
+    rng = np.random.default_rng(e)
+    x = rng.standard_normal((12, e)) * 2
+    x[1, 5] = np.inf
+    x[2, [7, e - 1]] = np.inf
+    x[3, e // 2] = np.nan
+    x[4, 3], x[4, e - 2] = np.nan, np.inf
+    x[5, : e - 3], x[5, e - 2] = -np.inf, np.inf           # fewer open than are asked for
+    x[6, ::2], x[6, 1] = -np.inf, np.inf
+    x[7] = np.inf
+    logits = up(x.astype(np.float32)).to(TYPES[dtype])
+    host = f64(logits)
+    for score in (SOFTMAX, SIGMOID):
+        for bias in (None, (0.1 * rng.standard_normal(e)).astype(np.float32), np.zeros(e, np.float32)):
+            for renorm in (False, True):
+                ids, w = run_select(logits, k, None if bias is None else up(bias), score, groups, top_groups, renorm)
+                want_ids, want = by_definition(host, bias, k, score == SIGMOID, groups, top_groups, renorm)
+                what = (score, None if bias is None else float(np.abs(bias).max()), renorm)
+                assert np.array_equal(ids.cpu().numpy(), want_ids), what
+                got = f64(w)
+                assert np.array_equal(np.isnan(got), np.isnan(want)), what
+                good = ~np.isnan(want)
+                assert (np.abs(got - want)[good] <= np.abs(want[good]) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all(), what
