@@ -230,19 +230,21 @@ __device__ __forceinline__ bool take_groups32(const SelectArgs& a, const float* 
     return !odd && (most == 0 || x - of_rank32(most) > apart);
 }
 
-// The same in 64 bits; a NaN's group goes first.
+// The same in 64 bits; a NaN's group goes first.  Groups without a value come
+// behind all, the lowest index first, in both: their experts at a bias of
+// -infinity may be taken yet.
 template <int LANES, int N>
 __device__ __forceinline__ void take_groups(const SelectArgs& a, const double* c, uint32_t lane, double* lds, uint32_t* rank) {
     bool odd;
     const Two<double> two = two_of_groups<LANES, N>(a, c, lane, lds, &odd);
     const uint32_t mine = lane >> a.group_log2, base = threadIdx.x & 63u & ~uint32_t(LANES - 1);
-    uint64_t of = two.none() || mine >= a.groups ? 0 : key_of(rank_of(two.value()), mine);
+    uint64_t of = two.none() ? key_of(0, mine) : key_of(rank_of(two.value()), mine);      // (a rank is above 0)
     const uint64_t odds = __ballot(odd) >> (base + (mine << a.group_log2));
     if (odds & ((uint64_t(2) << ((1u << a.group_log2) - 1)) - 1)) of = key_of(~uint64_t(0), mine);
     uint32_t ahead = 0;
     for (uint32_t g = 0; g < a.groups; ++g)
         ahead += uint64_t(__shfl((unsigned long long)of, int(base + (g << a.group_log2)), 64)) > of ? 1u : 0u;
-    shut_groups<LANES, N>(a, lane, of && ahead < a.top_groups, rank);
+    shut_groups<LANES, N>(a, lane, mine < a.groups && ahead < a.top_groups, rank);
 }
 
 // scores of a row in 64 bits for the comparisons

@@ -484,3 +484,21 @@ def test_select_of_infinite_and_nan_logits(e, k, groups, top_groups, dtype):
                 assert np.array_equal(np.isnan(got), np.isnan(want)), what
                 good = ~np.isnan(want)
                 assert (np.abs(got - want)[good] <= np.abs(want[good]) * (2.0 ** -24 + 1e-12) + 2.0 ** -149).all(), what
+
+
+def test_select_groups_do_not_depend_on_other_rows():
+    """Rows in which fewer groups than are taken have a value (the others are behind all by their bias): the rest is taken by
+    index, whether or not a row beside them has to be decided in 64 bits (two equal groups at the border)."""
+    e, groups, k = 64, 8, 12
+    rng = np.random.default_rng(21)
+    bias = np.zeros(e, np.float32)
+    bias[:16] = -np.inf                                    # groups 0 and 1
+    for score in (SOFTMAX, SIGMOID):
+        x = rng.standard_normal((16, e)).astype(np.float32)
+        x[1::2, 16:56] = -np.inf                           # only group 7 has a value
+        alone, _ = run_select(up(x[1::2]), k, up(bias), score, groups, 4)
+        x[0::2, 16:] = np.tile(x[0::2, 16:24], (1, 6))     # six equal groups
+        ids, _ = run_select(up(x), k, up(bias), score, groups, 4)
+        want, _ = by_definition(x, bias, k, score == SIGMOID, groups, 4)
+        assert np.array_equal(alone.cpu().numpy(), want[1::2]), score
+        assert np.array_equal(ids.cpu().numpy(), want), score
