@@ -787,8 +787,9 @@ int32_t dcr_experts_combine_grad(const void* dy, uint32_t dy_type, uint64_t dy_s
  *   workspace_dev  as for dcr_experts_order
  * A row with every token masked has lse and log probabilities of -infinity and
  * entropy 0.  A row that holds a NaN or +infinity has NaN in all its floating
- * results (NaN ranks below all numbers in top_ids).  Masks of the lowest finite
- * number are numbers as all others: a row of nothing else is uniform. */
+ * results (NaN ranks below all numbers in top_ids).  Masks by finite numbers are
+ * numbers as all others, whatever their size: a row of nothing else is uniform.
+ * Log probabilities are 0 at most and entropies 0 at least. */
 int32_t dcr_logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,
                      uint32_t targets_bytes, float scale, float* logp, float* lse, float* entropy, uint32_t top,
                      int32_t* top_ids, float* top_values, void* workspace_dev, uint64_t ws_bytes, void* stream);

@@ -308,3 +308,90 @@ def test_every_split(rows, vocab):
                 none = torch.isneginf(want)
                 got = vals[i:i + 256].double()
                 assert torch.equal(torch.isneginf(got), none) and ((got - want)[~none].abs() <= tol + 2.0 ** -17).all()
+
+
+# (rows, vocabulary): a wave a row, a workgroup a row, parts of both kinds
+FORMS = [(10, 300), (10, 5001), (10, 70000), (1100, 65600), (4100, 1500), (1030, 9001), (300, 30001)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e10, -1e12, -1e20, -1e25, -1e30, -2.0 ** 100, -2e30, -3.3895e38])
+def test_finite_masks_are_numbers(mask, dtype):
+    """Masks by finite numbers of any size, at any scale: of whole rows (uniform then), of a tail and of every second half of
+    what a thread, a wave or a part sees, of all but one token, with both largest in turn.  Against 64 bits on the GPU; the
+    largest's product with the scale is rounded in lse, and a difference twice in log p: 2^-22 of themselves; the sums as
+    in tolerances()."""
+    for n, (rows, vocab) in enumerate(FORMS):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(n)
+        scale = float(np.float32((1.0, 0.7, 2.5, 0.01)[n % 4]))
+        x = torch.empty(rows, vocab, dtype=TYPES[dtype], device="cuda")
+        for part in x.split(256):
+            part.copy_(torch.randn(part.shape, device="cuda", generator=g) * 3)
+        j = torch.arange(vocab, device="cuda")
+        x[0] = mask
+        x[1, vocab // 3:] = mask                           # a padded vocabulary
+        x[2, 1:] = mask                                    # one open token, at the front and at the end
+        x[7, :-1] = mask
+        for r, width in enumerate((8, 128, 1024, 2048)):   # stretches
+            x[r + 3, (j // width) % 2 == 0] = mask
+        x[rows - 1, ::2], x[rows - 1, 1::2] = mask, 2 * mask if abs(mask) < 1e38 else mask
+        t = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+        top = min(7, vocab)
+        ws = dcr.step_workspace()
+        for some in (0, top):
+            out = [torch.full((rows,), 77.0, device="cuda") for _ in range(3)]
+            ids = torch.full((rows, top), -5, dtype=torch.int32, device="cuda") if some else None
+            vals = torch.full((rows, top), 77.0, device="cuda") if some else None
+            dcr.dcr_logprobs(x, t, *out, ids, vals, scale=scale, workspace=ws)
+            grow = (vocab / 256 + 40) * 2.0 ** -24 + 2.0 ** -21
+            for i in range(0, rows, 256):
+                y = x[i:i + 256].double() * scale
+                most = y.amax(1, keepdim=True)
+                d = y - most
+                log_s = d.exp().sum(1, keepdim=True).log()
+                lp = d - log_s
+                ent = -(lp.exp() * lp.clamp(min=-800)).sum(1)
+                mine = lp.gather(1, t[i:i + 256, None])[:, 0]
+                want = [mine, (most + log_s)[:, 0], ent]
+                tol = [grow + 2.0 ** -20 + 2.0 ** -22 * mine.abs(), grow + 2.0 ** -20 + 2.0 ** -23 * want[1].abs(),
+                       2 * grow * (1 + ent) + 2.0 ** -20]
+                for name, a, b, c in zip(("logp", "lse", "entropy"), out, want, tol):
+                    a = a[i:i + 256].double()
+                    low = b < -3.4028e38                   # (beyond the numbers of 32 bits)
+                    assert torch.isfinite(a[~low]).all() and (a[low] <= -3.4028e38).all(), (rows, vocab, some, name)
+                    assert ((a - b).abs() <= c)[~low].all(), (rows, vocab, some, name, (a - b).abs()[~low].max())
+                if some:
+                    best = lp.gather(1, ids[i:i + 256].long())
+                    got = vals[i:i + 256].double()
+                    low = best < -3.4028e38
+                    assert ((got - best).abs() <= grow + 2.0 ** -20 + 2.0 ** -22 * best.abs())[~low].all(), (rows, vocab)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_peaked_rows_have_no_positive_log_probabilities(dtype):
+    """One token far above the others: its log probability is at most 0 and the entropy at least 0, and where all others
+    together weigh less than 2^-26 the sum is 1 and log p is 0 to within their weight.  (The largest term is 1 itself, so no
+    sum is below it, and what is added to 1 is rounded to 1 below 2^-24.)"""
+    rng = np.random.default_rng(51)
+    ws = dcr.step_workspace()
+    for rows, vocab in ((3000, 2000), (700, 900), (64, 20000), (1100, 65600), (4100, 1500)):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(vocab)
+        x = torch.empty(rows, vocab, dtype=TYPES[dtype], device="cuda")
+        for part in x.split(256):
+            part.copy_(torch.randn(part.shape, device="cuda", generator=g))
+        at = torch.randint(0, vocab, (rows, 1), device="cuda", generator=g)
+        x.scatter_(1, at, (25 + 20 * torch.rand(rows, 1, device="cuda", generator=g)).to(x.dtype))
+        for scale in (1.0, float(np.float32(0.7)), float(np.float32(1.3))):
+            lp, lse, ent = (torch.full((rows,), 77.0, device="cuda") for _ in range(3))
+            ids, vals = torch.empty(rows, 2, dtype=torch.int32, device="cuda"), torch.empty(rows, 2, device="cuda")
+            dcr.dcr_logprobs(x, at[:, 0], lp, lse, ent, ids, vals, scale=scale, workspace=ws)
+            assert torch.equal(ids[:, :1].long(), at) and torch.equal(vals[:, 0], lp)
+            assert (lp <= 0).all() and (ent >= 0).all(), (rows, vocab, scale, float(lp.max()), float(ent.min()))
+            for i in range(0, rows, 256):
+                y = x[i:i + 256].double() * scale
+                y -= y.amax(1, keepdim=True)
+                rest = y.exp().sum(1) - 1
+                sharp = rest < 2.0 ** -26
+                assert (lp[i:i + 256].double() + rest)[sharp].abs().max() <= 2.0 ** -26 if sharp.any() else True
