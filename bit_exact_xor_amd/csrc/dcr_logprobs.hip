@@ -193,12 +193,19 @@ struct RowOf {
 __device__ __forceinline__ bool none_open(Sums s) { return s.m == -INFINITY && s.s == s.s; }     // an empty row
 __device__ __forceinline__ RowOf row_of_sums(Sums s) { return {s.m, none_open(s) ? 0.0f : logf(s.s)}; }
 
+// lse of a row that is not empty, a finite number also where it lies beyond those
+// of 32 bits: -infinity stands for an empty row
+__device__ __forceinline__ float lse_of(RowOf of, float scale) {
+    const float l = __fmaf_rn(of.m, scale, of.log_s);
+    return fabsf(l) == INFINITY ? copysignf(0x1.fffffep127f, l) : l;
+}
+
 // what a row's sums give; by one thread
 template <typename T>
 __device__ __forceinline__ RowOf finish_row(const LpArgs& a, uint32_t row, Sums s) {
     const bool none = none_open(s);
     const RowOf of = row_of_sums(s);
-    if (a.lse) a.lse[row] = none ? -INFINITY : __fmaf_rn(s.m, a.scale, of.log_s);
+    if (a.lse) a.lse[row] = none ? -INFINITY : lse_of(of, a.scale);
     if (a.entropy) a.entropy[row] = none ? 0.0f : of.log_s - kLn2 * s.t / s.s;
     if (a.logp) {
         const int64_t t = target_of(a, row);
@@ -606,10 +613,44 @@ struct LpGradArgs {
 
 constexpr uint32_t kGU = 2;                      // eights of a thread in a row of its workgroup's
 
+// Half a step of lse is in every p of its row: 2^-19 of it below 64, but 3e-5 at
+// 1000 and all of it at the lowest finite number, a mask.  From 64 on a row's
+// largest logit and log S are taken apart from one another again, from the logits
+// (log p = scale (x - m) - log S, as the forward call has it), by one workgroup, or
+// wave of short rows, which reads them twice (4096 x 151936 918 us for 399, 10000 x
+// 1264 33 for 13.9, 8 x 151936 87 for 7).  An lse that the logits do not give (of
+// a vocabulary that is held in parts) is taken as it is.
+constexpr float kFarLse = 64.0f, kOwnLse = 0x1p-22f;
+__device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY; }
+
+// log p = scale (x - m) - log_s of a row with such an lse, m 0 and log_s the lse where
+// it is another's; in all threads, from a wave's sums of the row
+__device__ __forceinline__ RowOf row_of_far(Sums s, float lse, float scale) {
+    const RowOf of = row_of_sums(s);
+    return fabsf(lse_of(of, scale) - lse) <= kOwnLse * fabsf(lse) ? of : RowOf{0.0f, lse};
+}
+
+// sums of the row by THREADS threads, a thread's part
+template <uint32_t THREADS, typename T>
+__device__ __forceinline__ Sums part_of_row(const T* x, uint32_t vocab, float unit) {
+    Sums sum = {-INFINITY, 0.0f, 0.0f};
+    for (uint32_t c0 = 0; c0 < vocab; c0 += THREADS * kPiece) {
+        Raw8<T> raw[2];
+        float v[kPiece];
+        load_step<THREADS>(x, c0, vocab, raw);
+        raw[0].get(v);
+        raw[1].get(v + 8);
+        add_step(v, unit, c0 + THREADS * kPiece > vocab, sum);
+    }
+    return sum;
+}
+
 // dx_j = scale (dlogp (1[j = t] - p_j) - dentropy p_j (log p_j + entropy)), for
-// the eight logits from `at` on
-template <typename T, int U>
-__device__ __forceinline__ void grad_of(const LpGradArgs& a, uint32_t row, const uint32_t* at) {
+// the eight logits from `at` on.  Without FAR nothing is done and true returned
+// where the lse is far (which the loads of the logits need not wait for: 10000 x
+// 1264 13.9 us, else 15.0).
+template <typename T, int U, bool FAR = false>
+__device__ __forceinline__ bool grad_of(const LpGradArgs& a, uint32_t row, const uint32_t* at, RowOf of = {}) {
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
     T* y = static_cast<T*>(a.dlogits) + uint64_t(row) * a.d_stride;
     const int64_t target = a.wide_ids ? static_cast<const int64_t*>(a.targets)[row]
@@ -627,13 +668,14 @@ __device__ __forceinline__ void grad_of(const LpGradArgs& a, uint32_t row, const
         n[u] = at[u] < a.vocab ? int(min(8u, a.vocab - at[u])) : 0;
         n[u] == 8 ? raw[u].load_once(x + at[u]) : raw[u].load_some(x + at[u], n[u], kBf16MinusInf);
     }
+    if (!FAR && is_far(lse)) return true;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float v[8];
         raw[u].get(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float l = __fmaf_rn(v[i], a.scale, -lse);
+            const float l = FAR ? __fmaf_rn(v[i] - of.m, a.scale, -of.log_s) : __fmaf_rn(v[i], a.scale, -lse);
             const float p = __builtin_amdgcn_exp2f(l * kLog2e);
             // p (up + b (log p + entropy)); p = 0 where log p is -infinity
             const float g = -p * __fmaf_rn(b, fmaxf(l, -110.0f), c);
@@ -647,23 +689,54 @@ __device__ __forceinline__ void grad_of(const LpGradArgs& a, uint32_t row, const
         }
         n[u] == 8 ? store8<true>(y + at[u], v) : store_some(y + at[u], v, n[u]);
     }
+    return false;
 }
 
-// A workgroup has kGU eights a thread of one row.
+// A workgroup has kGU eights a thread of one row; the first has all of a row with
+// a far lse (the others would read logits that it may have written over).
 template <typename T>
 __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
-    const uint32_t row = blockIdx.x / a.pieces, first = (blockIdx.x % a.pieces * kGU * kLT + threadIdx.x) * 8;
+    const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
     uint32_t at[kGU];
+    const auto place = [&](uint32_t first) {
 #pragma unroll
-    for (uint32_t u = 0; u < kGU; ++u) at[u] = first + u * kLT * 8;
-    grad_of<T, kGU>(a, row, at);
+        for (uint32_t u = 0; u < kGU; ++u) at[u] = first + (u * kLT + threadIdx.x) * 8;
+    };
+    if (!is_far(a.lse[row])) {
+        place(piece * kGU * kLT * 8);
+        grad_of<T, kGU>(a, row, at);
+        return;
+    }
+    if (piece) return;
+    __shared__ Sums of_wave[kLWaves];
+    const float unit = a.scale * kLog2e;
+    Sums sum = part_of_row<kLT>(static_cast<const T*>(a.logits) + uint64_t(row) * a.stride, a.vocab, unit);
+    sum = join_wave(sum, unit);
+    if ((threadIdx.x & 63u) == 0) of_wave[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = of_wave[0];
+    for (uint32_t w = 1; w < kLWaves; ++w) sum = join(sum, of_wave[w], unit);
+    const RowOf of = row_of_far(sum, a.lse[row], a.scale);
+    for (uint32_t c0 = 0; c0 < a.vocab; c0 += kGU * kLT * 8) {
+        place(c0);
+        grad_of<T, kGU, true>(a, row, at, of);
+    }
 }
 
-// Short rows: threads have an eight each, dealt over the rows one after the other.
+// Short rows: threads have an eight each, dealt over the rows one after the other;
+// rows with a far lse go to the waves that have their first eights, one after the
+// other.
 template <typename T>
-__global__ void __launch_bounds__(kLT) logprobs_grad_short_kernel(LpGradArgs a) {
+__global__ void __launch_bounds__(kLT, 8) logprobs_grad_short_kernel(LpGradArgs a) {
     const uint32_t i = blockIdx.x * kLT + threadIdx.x, row = i / a.pieces, at = (i - row * a.pieces) * 8;
-    if (row < a.rows) grad_of<T, 1>(a, row, &at);
+    const bool far = row < a.rows && grad_of<T, 1>(a, row, &at);
+    for (uint64_t some = __ballot(far && at == 0); some; some &= some - 1) {
+        const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(row), __ffsll((unsigned long long)some) - 1));
+        const float unit = a.scale * kLog2e;
+        const Sums sum = part_of_row<64>(static_cast<const T*>(a.logits) + uint64_t(r) * a.stride, a.vocab, unit);
+        const RowOf of = row_of_far(join_wave(sum, unit), a.lse[r], a.scale);
+        for (uint32_t c = (threadIdx.x & 63u) * 8; c < a.vocab; c += 64 * 8) grad_of<T, 1, true>(a, r, &c, of);
+    }
 }
 
 int32_t check_logits(const void* logits, uint32_t type, uint64_t stride, uint64_t rows, uint64_t vocab, const void* targets,

@@ -779,7 +779,8 @@ int32_t dcr_experts_combine_grad(const void* dy, uint32_t dy_type, uint64_t dy_s
  *              gives NaN.  May be NULL with logp
  *   scale      1 / temperature, positive and finite
  *   logp       NULL or [rows] fp32: scale * x_t - lse
- *   lse        NULL or [rows] fp32: log of the sum of exp(scale * x)
+ *   lse        NULL or [rows] fp32: log of the sum of exp(scale * x); where that
+ *              lies beyond the numbers of 32 bits, the last of them
  *   entropy    NULL or [rows] fp32: - sum of p log p
  *   top        0 .. min(64, vocab): top_ids ([rows, top] int32) and top_values
  *              ([rows, top] fp32, log probabilities) are the largest logits, the
@@ -796,7 +797,10 @@ int32_t dcr_logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_
 
 /* Gradient of logp and entropy with respect to the logits:
  *   dlogits[j] = scale * (dlogp * ([j = target] - p_j) - dentropy * p_j * (log p_j + entropy)),
- * log p_j = scale * x_j - lse, with the lse and entropy of dcr_logprobs.  dlogp:
+ * log p_j = scale * x_j - lse, with the lse and entropy of dcr_logprobs.  Where
+ * |lse| is 64 or more its rounding is not in p: the row is read for its own sum,
+ * which counts where lse is within 2^-22 of it (another lse is taken as it is, as of
+ * a vocabulary held in parts).  dlogp:
  * [rows] fp32 (counts as 0 without a target); dentropy NULL (entropy is then not
  * looked at) or [rows] fp32.  dlogits has the logits' type and may be the
  * logits.  A row whose lse is -infinity gives zeros. */

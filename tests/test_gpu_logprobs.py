@@ -395,3 +395,91 @@ def test_peaked_rows_have_no_positive_log_probabilities(dtype):
                 rest = y.exp().sum(1) - 1
                 sharp = rest < 2.0 ** -26
                 assert (lp[i:i + 256].double() + rest)[sharp].abs().max() <= 2.0 ** -26 if sharp.any() else True
+
+
+GRAD_FORMS = [(6, 300), (300, 77), (5, 2047), (5, 5001), (3, 70000), (700, 2500), (40, 32000)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["lowest", "all lowest", "1e10", "1e30", "shifted", "far shifted", "rising", "padded"])
+def test_grad_is_that_of_the_log_probabilities(kind, dtype):
+    """Against the gradient in 64 bits from the logits themselves, with the lse that the forward call gives.  A term p is off
+    by the rounding of log p (3 |log p| + 8) 2^-23, by half a step of lse where that is below 64 (2^-19), else by its own
+    sum's (vocab / 256 + 40) 2^-24 and 2^-20.  A row's terms add up to what the rounding of p leaves of |dlogp|."""
+    rng = np.random.default_rng(61)
+    ws = dcr.step_workspace()
+    for n, (rows, vocab) in enumerate(GRAD_FORMS):
+        gap, shift = ((0, 0), (5, 1), (8, 8))[n % 3]
+        scale = float(np.float32((1.0, 0.7, 1.4)[n % 3]))
+        x = rng.standard_normal((rows, vocab)) * 3
+        some = rng.random((rows, vocab)) < 0.5
+        if kind in ("lowest", "1e10", "1e30"):
+            x[some] = {"lowest": -3.3895e38, "1e10": -1e10, "1e30": -1e30}[kind]
+            x[::3] = {"lowest": -3.3895e38, "1e10": -1e10, "1e30": -1e30}[kind]
+        elif kind == "all lowest":
+            x[:] = -3.3895e38
+        elif kind == "shifted":
+            x += np.where(np.arange(rows) % 2, 1000, -70)[:, None]
+        elif kind == "far shifted":
+            x = np.round(x) * 4096 + 1e5
+        elif kind == "rising":
+            x = np.sort(x, 1) * 8
+        elif kind == "padded":
+            x = x - 90
+            x[:, vocab * 2 // 3:] = -np.inf
+            x[::5] = -np.inf
+        logits = torch.empty(rows, vocab + gap + shift, dtype=TYPES[dtype], device="cuda")[:, shift: shift + vocab]
+        logits.copy_(up(x.astype(np.float32)))
+        x = f64(logits)
+        targets = rng.integers(0, vocab, rows)
+        targets[2::4] = -1
+        t = up(targets)
+        lse = torch.empty(rows, device="cuda")
+        dcr.dcr_logprobs(logits, t, lse=lse, scale=scale, workspace=ws)
+        lp, lse64, ent64, p = R.logprobs(x, scale)
+        ent = up(ent64.astype(np.float32))
+        dlogp, dent = up(rng.standard_normal(rows).astype(np.float32)), up(rng.standard_normal(rows).astype(np.float32))
+        hot = np.zeros_like(x)
+        hot[np.arange(rows), np.maximum(targets, 0)] = 1
+        open_rows = ~np.isneginf(lse64)[:, None]
+        grow = (vocab / 256 + 40) * 2.0 ** -24 + 2.0 ** -20
+        for b in (None, dent):
+            d = torch.full((rows, vocab + 3), 9.0, dtype=TYPES[dtype], device="cuda")
+            dcr.dcr_logprobs_grad(logits, t, lse, dlogp, d[:, :vocab], entropy=ent if b is not None else None, dentropy=b, scale=scale)
+            a = np.where(targets < 0, 0, f64(dlogp))[:, None]
+            be, h = (np.zeros((rows, 1)), 0) if b is None else (f64(b)[:, None], f64(ent)[:, None])
+            ll = np.where(p > 0, lp, 0)
+            want = scale * (a * (hot - p) - be * p * (ll + h)) * open_rows
+            off = (3 * np.abs(ll) + 8) * 2.0 ** -23 + 2.0 ** -19 + grow
+            # (p off by `off` of itself, and log p by the same where the entropy's part multiplies it)
+            most = scale * p * ((np.abs(a) + np.abs(be) * (np.abs(ll) + np.abs(h))) * off + np.abs(be) * off)
+            tol = most + 2.0 ** -23 * scale * hot * np.abs(a)
+            # (an exponential below 2^-126 is 0: p is off by as much, times what it is multiplied with)
+            tol = tol + 2.0 ** -126 * scale * (np.abs(a) + np.abs(be) * (np.abs(ll) + np.abs(h)))
+            err = np.abs(f64(d[:, :vocab]) - want)
+            assert (err <= tol + HALF[dtype] * (np.abs(want) + tol) + 2.0 ** -126).all(), (rows, vocab, b is None, np.max(err - tol))
+            assert (d[:, vocab:] == 9).all()
+            if dtype == "fp32":
+                total = np.abs(f64(d[:, :vocab]).sum(1))
+                assert (total <= (tol + 2.0 ** -24 * np.abs(want)).sum(1) + 2.0 ** -40).all(), (rows, vocab)
+        copy = torch.empty(rows, vocab + gap + shift, dtype=TYPES[dtype], device="cuda")[:, shift: shift + vocab].copy_(logits)
+        dcr.dcr_logprobs_grad(copy, t, lse, dlogp, copy, entropy=ent, dentropy=dent, scale=scale)     # in place
+        assert torch.equal(copy, d[:, :vocab])
+
+
+def test_grad_with_a_foreign_lse():
+    """An lse that is not these logits' own (of a vocabulary that several GPUs share, say) is taken as it is given, near 0 and
+    far from it: p = exp(scale x - lse), rounded as |lse| has it."""
+    rng = np.random.default_rng(62)
+    for rows, vocab in ((9, 300), (9, 6000)):
+        for base in (0.0, 90.0, -500.0):
+            x = (base + rng.standard_normal((rows, vocab))).astype(np.float32)
+            lse = (R.logprobs(x, 1.0)[1] + np.linspace(0.01, 3, rows)).astype(np.float32)
+            d = torch.empty(rows, vocab, device="cuda")
+            one = torch.ones(rows, device="cuda")
+            dcr.dcr_logprobs_grad(up(x), torch.full((rows,), 3, device="cuda"), up(lse), one, d)
+            l = x.astype(np.float64) - lse.astype(np.float64)[:, None]
+            want = -np.exp(l)
+            want[:, 3] += 1
+            tol = np.exp(l) * ((3 * np.abs(l) + 8) * 2.0 ** -23)
+            assert (np.abs(f64(d) - want) <= tol + 2.0 ** -23).all(), (rows, base)
