@@ -420,11 +420,16 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
     }
 }
 
-// The gradient.  With w_j = scale s_j / W (W: the chosen scores' sum, or 1)
-//   ds_j = scale (dw_j - [renormalised] sum dw s / W) / W
-//   dl   = s (1 - s) ds  or, of a softmax, s (ds - sum ds s), a sum that is
-//          zero where the weights are renormalised
+// The gradient, with ds_j = scale dw_j added up over the pairs of an expert:
+//   dl = s (1 - s) ds  or, of a softmax, s (ds - sum ds s)
+// and of renormalised weights, with r_j = s_j over the sum of the chosen scores:
+//   dl = scale r_j (dw_j - sum dw r)  times 1 - s_j for a sigmoid
+// of the chosen experts alone.  There the scores as such do not occur: r is taken
+// from the chosen logits by their largest, so that scores of any size (at -100 all
+// are 0 in 32 bits, the weights are not) give derivatives of the weights' size.
+// Only where the scores of the forward call vanish, in 64 bits, do these.
 // A lane has the pairs j = lane, lane + LANES, ..., whose logits it fetches.
+constexpr float kGoneSigmoid = -709.7828f, kGoneSoftmax = -745.1332f;      // below these e^x overflows, or is 0, in 64 bits
 template <typename T, int LANES, int R>
 __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) {
     constexpr int N = 8 * R, ROWS = kET / LANES, KEEP = DCR_EXPERTS_MAX_K / LANES;
@@ -452,33 +457,59 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
         for (int i = 1; i < N; ++i) top = (v[i] > top || v[i] != v[i]) ? v[i] : top;
         top = lanes_max<LANES>(top);
         if (top == -INFINITY) top = 0.0f;
-        float z = 0.0f;
+        if (top == INFINITY) top = NAN;        // (as in the choice)
+        if (!a.renormalize) {
+            float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) z += d[i] = expf(v[i] - top);
-        z = lanes_sum<LANES>(z);
-        inv = z == 0.0f ? 0.0f : 1.0f / z;
+            for (int i = 0; i < N; ++i) z += d[i] = expf(v[i] - top);
+            z = lanes_sum<LANES>(z);
+            inv = z == 0.0f ? 0.0f : 1.0f / z;
+        }
     }
     // the row's scalars in 64 bits: dw and its mean are often nearly the same
     double all = 0.0, dot = 0.0;
+    float most = -INFINITY, rest[KEEP];        // largest of the chosen logits (a sigmoid's up to 0); 1 - s
+    if (a.renormalize) {
+#pragma unroll
+        for (int q = 0; q < KEEP; ++q) {
+            if (id[q] == ~0u) continue;
+            const float l = a.sigmoid && s[q] > 0.0f ? 0.0f : s[q];
+            most = (l > most || l != l) ? l : most;
+        }
+        most = lanes_max<LANES>(most);
+    }
+    const bool gone = a.sigmoid ? most < kGoneSigmoid : most - top < kGoneSoftmax;
 #pragma unroll
     for (int q = 0; q < KEEP; ++q) {
+        rest[q] = 1.0f;
         if (id[q] == ~0u) continue;
-        s[q] = a.sigmoid ? 1.0f / (1.0f + expf(-s[q])) : expf(s[q] - top) * inv;
+        const float l = s[q];
+        if (!a.renormalize) {
+            s[q] = a.sigmoid ? 1.0f : expf(l - top) * inv;
+        } else if (a.sigmoid) {
+            const float e = expf(-fabsf(l));
+            s[q] = expf((l > 0.0f ? 0.0f : l) - most) / (1.0f + e);
+            rest[q] = (l > 0.0f ? e : 1.0f) / (1.0f + e);
+        } else {
+            s[q] = expf(l - most);
+        }
+        if (a.renormalize && gone) s[q] = 0.0f;
         all += double(s[q]);
         dot += double(dw[q]) * double(s[q]);
     }
     dot = lanes_sum<LANES>(dot);
-    double over = double(a.scale), mean = 0.0;     // scale / W, and what the renormalisation takes off dw
+    double mean = 0.0;                         // what the renormalisation takes off dw
     if (a.renormalize) {
         all = lanes_sum<LANES>(all);
         if (all == 0.0) all = 1.0;
-        over /= all;
         mean = dot / all;
     }
-    const float off = a.sigmoid || a.renormalize ? 0.0f : float(dot * over);
+    const float off = a.sigmoid || a.renormalize ? 0.0f : float(dot * double(a.scale));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (a.sigmoid) {
+        if (a.renormalize) {
+            v[i] = top == top ? 1.0f : NAN;
+        } else if (a.sigmoid) {
             const float q = expf(-fabsf(v[i]));    // s (1 - s) = q / (1 + q)^2
             v[i] = q / ((1.0f + q) * (1.0f + q));
         } else {
@@ -490,7 +521,8 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
 #pragma unroll
     for (int q = 0; q < KEEP; ++q) {
         if (uint32_t(q) * LANES >= a.k) break;
-        const float ds = float((double(dw[q]) - mean) * over);
+        float ds = dw[q] * a.scale;
+        if (a.renormalize) ds = float((double(dw[q]) - mean) * double(a.scale) * (double(s[q]) / all * double(rest[q])));
         for (uint32_t j = 0; j < min(uint32_t(LANES), a.k - q * LANES); ++j) {
             const uint32_t e = uint32_t(__shfl(int(id[q]), base + int(j), 64));
             const float of = __shfl(ds, base + int(j), 64);

@@ -502,3 +502,55 @@ def test_select_groups_do_not_depend_on_other_rows():
         want, _ = by_definition(x, bias, k, score == SIGMOID, groups, 4)
         assert np.array_equal(alone.cpu().numpy(), want[1::2]), score
         assert np.array_equal(ids.cpu().numpy(), want), score
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_select_grad_of_small_scores(score, dtype):
+    """Renormalised weights have derivatives of their own size whatever the chosen scores are: logits near where a score
+    leaves the normal numbers of 32 bits, far below it, and chosen ones far below the row's largest.  An exponential's
+    argument is a difference d rounded once (2^-24 |d| of the term, d as far as the chosen ones lie apart, and what is that
+    far down is as small itself: |d| e^-|d| < 0.37), some 2^-22 more for its own rounding and the sums: 2^-18 of the sum of
+    the terms' magnitudes as above."""
+    rng = np.random.default_rng(31)
+    for e, k in ((60, 6), (128, 8), (384, 12), (1000, 64)):
+        for base in (-60, -86, -87.5, -88, -88.6, -89, -100, -103.5, -110, -300, -600):
+            x = (base + rng.standard_normal((20, e))).astype(np.float32)
+            bias = None
+            if score == SOFTMAX:                           # the bias chooses among experts far below the largest
+                x[:, 0] = 0.5
+                bias = np.zeros(e, np.float32)
+                bias[1::2] = 2.0
+            logits = up(x).to(TYPES[dtype])
+            ids, w = run_select(logits, k, None if bias is None else up(bias), score, renormalize=True)
+            dw = up(rng.standard_normal((20, k)).astype(np.float32))
+            d = torch.full(logits.shape, float("nan"), dtype=logits.dtype, device="cuda")
+            dcr.dcr_experts_select_grad(logits, ids, dw, d, score=score, renormalize=True, scale=1.5)
+            want, most = R.select_grad(f64(logits), ids.cpu().numpy(), f64(dw), score == SIGMOID, True, 1.5)
+            assert np.abs(want).max() > 0.01
+            err = np.abs(f64(d) - want)
+            assert (err <= most * 2.0 ** -18 + np.abs(want) * HALF[dtype] + 2.0 ** -126).all(), (e, k, base, err.max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_select_grad_of_far_logits(score, renormalize, dtype):
+    """The kinds that the choice is tested with: masks of the lowest finite number, logits up to some hundreds.  Where weights
+    are not renormalised a score's exponent is rounded as its distance |d| from the largest (or from 0) has it, 2^-23 |d| of
+    the score; the others as above."""
+    rng = np.random.default_rng(32)
+    for rows, e, k in SIZES:
+        for kind in ("lowest", "far", "ties"):
+            x = up(logits_of(kind, rows, e, rng).astype(np.float32)).to(TYPES[dtype])
+            ids, _ = run_select(x, k, score=score)
+            dw = up(rng.standard_normal((rows, k)).astype(np.float32))
+            d = torch.full(x.shape, float("nan"), dtype=x.dtype, device="cuda")
+            dcr.dcr_experts_select_grad(x, ids, dw, d, score=score, renormalize=renormalize, scale=1.5)
+            host = f64(x)
+            with np.errstate(over="ignore"):
+                want, most = R.select_grad(host, ids.cpu().numpy(), f64(dw), score == SIGMOID, renormalize, 1.5)
+                far = np.abs(host if score == SIGMOID else host - host.max(1, keepdims=True))
+            err = np.abs(f64(d) - want)
+            tol = most * (2.0 ** -18 + 2.0 ** -23 * np.minimum(far, 1e3))
+            assert (err <= tol + np.abs(want) * HALF[dtype] + 2.0 ** -126).all(), (rows, e, k, kind, err.max())
