@@ -296,9 +296,11 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
     }
     // Ranks in 32 bits.  A sigmoid by the hardware's exponential and reciprocal
     // (one step off each) is off by less than 2.3 * 2^-23 and a sum with the bias
-    // by 2^-24 of itself.  A softmax's sum of up to 1024 terms is off by less than
-    // 28 * 2^-24: 14 additions, a term's 2 steps, and its exponent's rounding, 2.3
-    // times its distance from the largest, of which the terms' mean is below 4.5.
+    // by 2^-24 of itself.  A softmax's sum of a lane's 8 terms and 64 lanes' is off by
+    // less than 26 * 2^-24: 13 additions, a term's 2 steps, and its exponent's
+    // rounding, 2.3 times its distance from the largest, of which the terms' mean is
+    // below 4.5 for 1024 of them; of a lane's 16 by 34 * 2^-24, eight additions more.
+    // A score has its reciprocal's 2 and its own term's 2 steps besides: 30 and 38.
     // Without a bias the logits themselves have the scores' order.
     float off = 0x1p-21f;
     uint32_t rank[N];
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
             for (int i = 0; i < N; ++i) z += c[i] = __builtin_amdgcn_exp2f((v[i] - top) * kLog2e);
             z = lanes_sum<LANES>(z);
             inv = z == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(z);
-            off = 0x1p-19f * inv;              // (the largest score is inv)
+            off = (R == 2 ? 0x1p-18f : 0x1p-19f) * inv;      // (the largest score is inv)
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {

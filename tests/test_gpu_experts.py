@@ -554,3 +554,21 @@ def test_select_grad_of_far_logits(score, renormalize, dtype):
             err = np.abs(f64(d) - want)
             tol = most * (2.0 ** -18 + 2.0 ** -23 * np.minimum(far, 1e3))
             assert (err <= tol + np.abs(want) * HALF[dtype] + 2.0 ** -126).all(), (rows, e, k, kind, err.max())
+
+
+def test_select_near_a_border_of_many_experts():
+    """More than 512 experts (16 a lane), whose softmax scores a bias undoes but for a few 2^-20 of the largest: the choice is
+    that of 64 bits however the sum of 32 bits is rounded."""
+    rng = np.random.default_rng(41)
+    for e in (513, 700, 1024):
+        for kind in range(3):
+            x = rng.standard_normal((1, e)).astype(np.float32)
+            if kind:
+                x = np.sort(x)[:, ::-1] if kind == 1 else np.full((1, e), 0.3, np.float32) + rng.standard_normal((1, e)).astype(np.float32) * 2.0 ** -10
+            s = R.scores(x.astype(np.float64), False)[0]
+            bias = (1.0 - s + rng.integers(-4, 5, e) * (2.0 ** -20 * s.max())).astype(np.float32)
+            for k in (1, 7, 64):
+                for groups, top_groups in ((1, 1), (e // (e // 9 if e == 513 else e // 4), 2)):
+                    ids, _w = run_select(up(x), k, up(bias), SOFTMAX, groups, top_groups)
+                    want, _ = R.select(x, bias, k, False, groups, top_groups)
+                    assert np.array_equal(ids.cpu().numpy(), want), (e, kind, k, groups)
