@@ -229,8 +229,11 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamA
             asm volatile("");
             w[j] = sqrtf(v[j]);
         }
-        // (the hardware's reciprocal, one step off, for the division's half)
-        p[j] = __fmaf_rn(p[j], keep, -(a.rate * m[j] * __builtin_amdgcn_rcpf(__fmaf_rn(w[j], a.root, a.eps))));
+        // (8 bits: the hardware's reciprocal, one step off, where instructions are as
+        // near a bound as the memory; with fp32 states the division costs no time)
+        const float den = __fmaf_rn(w[j], a.root, a.eps);
+        const float u = BITS == 8 ? a.rate * m[j] * __builtin_amdgcn_rcpf(den) : a.rate * m[j] / den;
+        p[j] = __fmaf_rn(p[j], keep, -u);
     }
     if (n == 4)
         save4<FAR>(pp, p);

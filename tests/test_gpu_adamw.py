@@ -302,3 +302,16 @@ def test_many_elements(bits, pt, gt):
             assert torch.equal(x[0][a:b].view(torch.uint8), y[0][:b - a].view(torch.uint8))
         if bits == 8:
             assert torch.equal(big.m_scales[0][a // 32: -(-b // 32)], s.m_scales[0][: -(-(b - a) // 32)])
+
+
+def test_updates_are_divided():
+    """Zero parameters, so that the result is the update itself, of numbers whose sums and products are exact (no averages,
+    powers of two as rate, scale and eps, squares of up to twelve bits): it is the quotient rounded once."""
+    rng = np.random.default_rng(71)
+    n = 20000
+    g = (rng.integers(1, 4096, n) * rng.choice([-1.0, 1.0], n)).astype(np.float32)
+    T = dcr.AdamWTensors([torch.zeros(n, device="cuda")], [up(g)])
+    dcr.dcr_adamw_step(T, 1, lr=2.0 ** -7, beta1=0.0, beta2=0.0, eps=3 * 2.0 ** -3)
+    den = np.abs(g).astype(np.float64) + 0.375              # 12 bits and three behind the point
+    want = -(2.0 ** -7 * g.astype(np.float64) / den)
+    assert np.array_equal(f64(T.params[0]), want.astype(np.float32).astype(np.float64))
