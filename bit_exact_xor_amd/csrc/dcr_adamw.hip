@@ -3,7 +3,10 @@
 //
 //   g' = grad_scale g
 //   m  = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
-//   p  = p (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//   p  = p - (lr decay p + lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps))
+//
+// (the decay as a part of p that is taken off: a factor 1 - lr decay comes in steps
+// of 6e-8, and at lr = 1e-6 and decay = 0.1 the decay itself is 1e-7)
 //
 // Bound by memory: everything is read once and written once, 30 bytes an
 // element with fp32 states, bf16 gradients and a bf16 copy, 16.1 with states in
@@ -45,7 +48,7 @@ constexpr uint64_t kFarBytes = uint64_t(256) << 20;
 // what the steps of a call share
 struct AdamArgs {
     float grad_scale, beta1, new1, beta2, new2;   // new: 1 - beta
-    float rate, root, eps, keep;                  // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), eps, 1 - lr decay
+    float rate, root, eps, decay;                 // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t), eps, lr decay
     uint32_t key, dither;
 };
 
@@ -169,7 +172,7 @@ template <typename TP, typename TG, uint32_t BITS, bool FAR>
 __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamArgs args, const AdamArgs* live) {
     const DevAdam t = chunks[blockIdx.x];
     const AdamArgs a = live ? *live : args;
-    const float keep = t.no_decay ? 1.0f : a.keep;
+    const float decay = t.no_decay ? 0.0f : a.decay;
     const uint32_t i = threadIdx.x * 4;
     const int n = i < t.numel ? int(min(4u, t.numel - i)) : 0;
     TP* pp = reinterpret_cast<TP*>(t.param) + i;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamA
         // near a bound as the memory; with fp32 states the division costs no time)
         const float den = __fmaf_rn(w[j], a.root, a.eps);
         const float u = BITS == 8 ? a.rate * m[j] * __builtin_amdgcn_rcpf(den) : a.rate * m[j] / den;
-        p[j] = __fmaf_rn(p[j], keep, -u);
+        p[j] -= __fmaf_rn(p[j], decay, u);
     }
     if (n == 4)
         save4<FAR>(pp, p);
@@ -314,7 +317,7 @@ __host__ __device__ inline AdamArgs adam_args(const dcr_adamw_args& h, double st
     a.beta1 = float(h.beta1), a.new1 = float(1.0 - h.beta1), a.beta2 = float(h.beta2), a.new2 = float(1.0 - h.beta2);
     a.rate = float(lr / (1.0 - power(h.beta1, t)));
     a.root = float(1.0 / sqrt(1.0 - power(h.beta2, t)));
-    a.eps = float(h.eps), a.keep = float(1.0 - lr * h.weight_decay);
+    a.eps = float(h.eps), a.decay = float(lr * h.weight_decay);
     a.key = uint32_t(h.dither_seed) * kGolden + uint32_t(t) * kRoot2, a.dither = h.dither_seed ? 1 : 0;
     return a;
 }

@@ -315,3 +315,18 @@ def test_updates_are_divided():
     den = np.abs(g).astype(np.float64) + 0.375              # 12 bits and three behind the point
     want = -(2.0 ** -7 * g.astype(np.float64) / den)
     assert np.array_equal(f64(T.params[0]), want.astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_small_decays(bits):
+    """A decay far below a step of 1 is taken off what it is of, not rounded as a factor: without gradients the parameter is
+    p (1 - lr decay) within its own rounding and 2^-23 of the decay."""
+    rng = np.random.default_rng(72)
+    n = 20000
+    p = rng.standard_normal(n).astype(np.float32)
+    for lr, decay in ((1e-6, 0.1), (3e-7, 0.1), (1e-6, 0.3), (2e-5, 0.01)):
+        T = dcr.AdamWTensors([up(p)], [torch.zeros(n, device="cuda")], bits=bits)
+        dcr.dcr_adamw_step(T, 1, lr=lr, weight_decay=decay)
+        want = p.astype(np.float64) * (1 - lr * decay)
+        half = np.spacing(np.abs(want).astype(np.float32)).astype(np.float64) / 2
+        assert (np.abs(f64(T.params[0]) - want) <= half * (1 + 2.0 ** -20) + np.abs(p) * lr * decay * 2.0 ** -22).all(), (lr, decay)
