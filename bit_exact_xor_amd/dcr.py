@@ -808,9 +808,10 @@ class AdamWTensors:
     that a shard is rounded as the whole tensor would be (default: one tensor
     behind the other).
 
-    The buffers are kept; gradients are written into the same tensors step
-    after step.  Steps may follow on any stream; the object has to be there
-    until they are done (and as long as a graph that has captured one)."""
+    The buffers are kept, and the `live` tensors of captured steps; gradients are
+    written into the same tensors step after step.  Steps may follow on any
+    stream, one after the other; the object has to be there until they are done
+    (and as long as a graph that has captured one)."""
 
     def __init__(self, params, grads, bits=32, copies=None, m=None, v=None, m_scales=None, v_scales=None, decay=None,
                  first=None):
@@ -824,6 +825,7 @@ class AdamWTensors:
         state = torch.float32 if bits == 32 else torch.float8_e4m3fn
         make = lambda t, ty, per: torch.zeros(-(-t.numel() // per), dtype=ty, device=t.device)  # noqa: E731
         self.bits, self.params, self.grads = bits, list(params), list(grads)
+        self.live = []                   # what captured steps read
         self.copies = [None] * n if copies is None else list(copies)
         self.m = [make(p, state, 1) for p in params] if m is None else list(m)
         self.v = [make(p, state, 1) for p in params] if v is None else list(v)
@@ -877,12 +879,32 @@ class AdamWTensors:
             _lib.dcr_adamw_plan_destroy(h)
 
 
+def _captures(device, stream):
+    """Whether `stream`, or the GPU's current stream, is captured into a graph."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(_as_stream(stream, device)):
+            return torch.cuda.is_current_stream_capturing()
+
+
+def _as_stream(stream, device):
+    """A torch stream of GPU `device` from one or from its handle."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(stream)
+    return torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+
+
 def dcr_adamw_step(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0,
                    dither=0, live=None, stream=None) -> None:
     """Enqueue step number `step` (1 upwards) of AdamW on all tensors.  `dither`:
     seed of the rounding of 8-bit moments (0: to nearest).  `live`: float64 [3]
     in device memory, the step number, lr and grad_scale that the GPU reads in
-    place of those passed (for captured graphs)."""
+    place of those passed (for captured graphs: one that a captured step reads is kept
+    by `tensors`)."""
     import torch
     if not 0 <= dither < 1 << 32:
         raise ValueError("dither: a seed below 2^32 expected")
@@ -891,11 +913,15 @@ def dcr_adamw_step(tensors: AdamWTensors, step, lr=1e-3, beta1=0.9, beta2=0.999,
     if live is not None:
         _one_device(tensors.table, live)
         _array(live, torch.float64, (3,), "live")
-        tensors.live = live
     args = AdamWArgs(lr, beta1, beta2, eps, weight_decay, grad_scale, 0 if live is not None else int(step),
                      None if live is None else live.data_ptr(), dither, 0)
     _fp4_call(torch, load_library().dcr_adamw_step, "dcr_adamw_step", tensors.index, stream, tensors.handle,
               ctypes.addressof(args))
+    if live is not None:
+        if _captures(tensors.index, stream):
+            tensors.live.append(live)
+        elif stream is not None:         # (it may be gone before that stream has read it)
+            live.record_stream(_as_stream(stream, tensors.index))
 
 
 def dcr_set_kernel_events(start=None, stop=None) -> None:

@@ -330,3 +330,35 @@ def test_small_decays(bits):
         want = p.astype(np.float64) * (1 - lr * decay)
         half = np.spacing(np.abs(want).astype(np.float32)).astype(np.float64) / 2
         assert (np.abs(f64(T.params[0]) - want) <= half * (1 + 2.0 ** -20) + np.abs(p) * lr * decay * 2.0 ** -22).all(), (lr, decay)
+
+
+def test_live_arguments_of_several_graphs_stay():
+    """What a captured step reads stays with the tensors, of every graph."""
+    import gc
+    import weakref
+    T = tensors_of([1000], "fp32", "fp32", 32, np.random.default_rng(6))
+    seen = []
+    for _ in range(2):
+        live = torch.tensor([1.0, 1e-3, 0.5], dtype=torch.float64, device="cuda")
+        seen.append(weakref.ref(live))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dcr.dcr_adamw_step(T, 1, live=live)
+        del live
+    gc.collect()
+    assert all(r() is not None for r in seen)
+    # an eager step's is the caller's: nothing grows from step to step
+    live = torch.tensor([1.0, 1e-3, 0.5], dtype=torch.float64, device="cuda")
+    r = weakref.ref(live)
+    dcr.dcr_adamw_step(T, 1, live=live)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream, torch.cuda.default_stream(), 0):
+        dcr.dcr_adamw_step(T, 1, live=live, stream=stream)
+        torch.cuda.synchronize()
+    del live
+    gc.collect()
+    assert r() is None
+    del T
+    gc.collect()
+    assert all(r() is None for r in seen)
