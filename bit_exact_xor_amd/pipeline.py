@@ -330,8 +330,11 @@ class Fp4Refit:
     def step(self, tensors, number, calibrate=False, **hyper):
         """AdamW step `number` (see dcr_adamw_step) on the trainer's weights,
         the parameters of `tensors` (a dcr.AdamWTensors, one for each shape),
-        and a refit with them; returns the payload bytes sent.  Where the refit
-        raises, the step has been taken: recover() finishes it."""
+        and a refit with them, which waits for a step that is put on another
+        stream; returns the payload bytes sent.  Where the refit raises, the step
+        has been taken and must not be taken again: recover() finishes a refit
+        that was interrupted, and one that had not begun to send is made up for by
+        refit() with the parameters."""
         import torch
         if [p.numel() for p in tensors.params] != [t.rows * t.cols for t in self.next]:
             raise ValueError("step: one parameter of each weight's size expected")
@@ -340,6 +343,8 @@ class Fp4Refit:
         self.recover()
         with torch.cuda.device(self.device):
             dcr.dcr_adamw_step(tensors, number, **hyper)
+            if hyper.get("stream") is not None:
+                torch.cuda.current_stream().wait_stream(dcr._as_stream(hyper["stream"], tensors.index))
         return self.refit([p.view(t.rows, t.cols) for p, t in zip(tensors.params, self.next)], calibrate)
 
     def _ready(self, what):

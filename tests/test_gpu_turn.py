@@ -238,3 +238,56 @@ def test_interrupted_refits_refuse():
     refit.interrupted = False
     with pytest.raises(ValueError):
         refit.step(dcr.AdamWTensors(masters[:1], [torch.zeros_like(masters[0])]), 1)
+
+
+def quantised(masters, refit):
+    """Whether the receiver holds what the trainer's weights quantise to."""
+    for w, q in zip(masters, refit.held):
+        mine = dcr.Fp4Tensor(q.rows, q.cols, dcr.FP4_NV, tensor_scale=q.tensor_scale)
+        dcr.dcr_fp4_quantize(w, mine)
+        if not (torch.equal(mine.codes, q.codes) and torch.equal(mine.scales, q.scales)):
+            return False
+    return True
+
+
+def test_step_on_another_stream():
+    """The refit waits for a step that is put on a stream of the caller's, which is busy for a while before it."""
+    rng = np.random.default_rng(5)
+    shapes, masters = weights(rng)
+    refit = pipeline.Fp4Refit(shapes, dcr.FP4_NV)
+    refit.refit(masters)
+    grads = [torch.from_numpy(rng.standard_normal(w.shape).astype(np.float32)).cuda() for w in masters]
+    tensors = dcr.AdamWTensors(masters, grads)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for number, stream in ((1, s), (2, s.cuda_stream)):
+        before = [w.clone() for w in masters]
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        assert refit.step(tensors, number, lr=2e-2, stream=stream) > 0
+        torch.cuda.synchronize()
+        assert not any(torch.equal(a, b) for a, b in zip(before, masters))
+        assert quantised(masters, refit)
+
+
+def test_step_whose_refit_has_not_begun(monkeypatch):
+    """An error before anything is sent: the step has been taken, nothing is interrupted, and refit() sends the weights."""
+    rng = np.random.default_rng(6)
+    shapes, masters = weights(rng)
+    refit = pipeline.Fp4Refit(shapes, dcr.FP4_NV)
+    refit.refit(masters)
+    tensors = dcr.AdamWTensors(masters, [torch.from_numpy(rng.standard_normal(w.shape).astype(np.float32)).cuda() for w in masters])
+    before = [w.clone() for w in masters]
+
+    def fails(*args, **kw):
+        raise MemoryError("as if there were none")
+    with monkeypatch.context() as m:
+        m.setattr(dcr, "dcr_fp4_quantize", fails)
+        with pytest.raises(MemoryError):
+            refit.step(tensors, 1, lr=2e-2)
+    assert not refit.interrupted and refit.version == 1
+    assert not any(torch.equal(a, b) for a, b in zip(before, masters))
+    refit.recover()
+    assert not quantised(masters, refit)
+    assert refit.refit(masters) > 0
+    assert quantised(masters, refit)
