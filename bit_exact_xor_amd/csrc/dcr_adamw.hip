@@ -39,7 +39,8 @@ namespace {
 
 constexpr uint32_t kAT = 128;                 // threads of a workgroup
 constexpr uint32_t kAChunk = 4 * kAT;         // elements of a workgroup
-constexpr uint64_t kAMostGroups = (uint64_t(1) << 32) / kAT - 1;      // of a launch
+constexpr uint32_t kAShare = 8;               // workgroups of an entry of the table
+constexpr uint64_t kAMostGroups = (uint64_t(1) << 32) / kAT / kAShare * kAShare - kAShare;      // of a launch
 constexpr uint32_t kStateBlock = DCR_ADAMW_BLOCK;
 // Tensors of more bytes than this (the last cache holds 256 MiB) go past the
 // caches (1 to 3 %).
@@ -64,7 +65,10 @@ __device__ __forceinline__ float root_of(float x) {
 }
 
 // What a workgroup does: everything of its elements in one entry, so that a small
-// tensor's time is two loads behind one another, not three.
+// tensor's time is two loads behind one another, not three.  Eight consecutive
+// workgroups share an entry, of 4096 elements; what is left of a tensor has entries
+// of up to 512, behind those (176 M elements 3.4 MB of table, with an entry a
+// workgroup 27.5, in the same time).
 struct DevAdam {
     uint8_t *param, *m, *v, *m_scales, *v_scales;
     const uint8_t* grad;
@@ -169,11 +173,14 @@ __device__ __forceinline__ uint32_t block_top(const float* v) {
 }
 
 template <typename TP, typename TG, uint32_t BITS, bool FAR>
-__global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* chunks, AdamArgs args, const AdamArgs* live) {
-    const DevAdam t = chunks[blockIdx.x];
+__global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* entries, uint32_t shared, AdamArgs args, const AdamArgs* live) {
+    // the first `shared` workgroups share entries
+    const bool shares = blockIdx.x < shared;
+    const uint32_t from = shares ? blockIdx.x % kAShare * kAChunk : 0;      // the workgroup's first element of the entry's
+    const DevAdam t = entries[shares ? blockIdx.x / kAShare : blockIdx.x - shared + shared / kAShare];
     const AdamArgs a = live ? *live : args;
     const float decay = t.no_decay ? 0.0f : a.decay;
-    const uint32_t i = threadIdx.x * 4;
+    const uint32_t i = from + threadIdx.x * 4;
     const int n = i < t.numel ? int(min(4u, t.numel - i)) : 0;
     TP* pp = reinterpret_cast<TP*>(t.param) + i;
     const TG* gp = reinterpret_cast<const TG*>(t.grad) + i;
@@ -333,9 +340,9 @@ constexpr uint32_t kVariants = 8;             // param type | gradient type | bi
 }  // namespace dcr
 
 struct dcr_adamw_plan {
-    std::vector<uint8_t> blob;                // AdamArgs of a live step | chunks, by variant
-    uint64_t off_chunks = 0;
-    uint64_t chunk_first[dcr::kVariants + 1] = {};
+    std::vector<uint8_t> blob;                // AdamArgs of a live step | entries, by variant: shared ones, then others
+    uint64_t off_entries = 0;
+    uint64_t first[dcr::kVariants + 1] = {}, shared[dcr::kVariants] = {};      // entries
     uint8_t* dev = nullptr;
     bool far = false;                         // more than the caches hold
 };
@@ -388,21 +395,32 @@ bool overlaps(const dcr_adamw_tensor* tensors, uint64_t n) {
 }
 
 int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan& p) {
-    std::vector<DevAdam> by[kVariants];
-    uint64_t chunks = 0, bytes = 0;
+    constexpr uint64_t kEntry = uint64_t(kAChunk) * kAShare;
+    uint64_t chunks = 0, bytes = 0, others[kVariants] = {};
+    const auto variant = [](const dcr_adamw_tensor& t) { return t.param_type | t.grad_type << 1 | (t.state_bits == 8 ? 4u : 0u); };
     for (uint64_t i = 0; i < n; ++i) {
         const dcr_adamw_tensor& t = tensors[i];
         if (int32_t rc = check_adam(t, i)) return rc;
         chunks += (t.numel + kAChunk - 1) / kAChunk;
         if (chunks >= (uint64_t(1) << 28)) return step_fail(DCR_E_INVAL, "2^37 elements or more");
+        p.shared[variant(t)] += t.numel / kEntry;
+        others[variant(t)] += (t.numel % kEntry + kAChunk - 1) / kAChunk;
     }
     if (overlaps(tensors, n)) return step_fail(DCR_E_INVAL, "buffers of the tensors overlap");
+    p.off_entries = (sizeof(AdamArgs) + 15) / 16 * 16;
+    uint64_t to[kVariants][2];                // where the next entry goes
+    for (uint32_t k = 0; k < kVariants; ++k) {
+        to[k][0] = p.first[k], to[k][1] = p.first[k] + p.shared[k];
+        p.first[k + 1] = to[k][1] + others[k];
+    }
+    p.blob.resize(p.off_entries + p.first[kVariants] * sizeof(DevAdam));
     for (uint64_t i = 0; i < n; ++i) {
         const dcr_adamw_tensor& t = tensors[i];
         const uint32_t p_bytes = type_bytes(t.param_type), g_bytes = type_bytes(t.grad_type), s_bytes = t.state_bits / 8;
         bytes += t.numel * (p_bytes + g_bytes + 2 * s_bytes + (t.copy ? 2 : 0));
-        std::vector<DevAdam>& to = by[t.param_type | t.grad_type << 1 | (t.state_bits == 8 ? 4u : 0u)];
-        for (uint64_t at = 0; at < t.numel; at += kAChunk) {
+        for (uint64_t at = 0, size; at < t.numel; at += size) {
+            const bool shares = t.numel - at >= kEntry;
+            size = shares ? kEntry : std::min<uint64_t>(kAChunk, t.numel - at);
             DevAdam d{};
             d.param = static_cast<uint8_t*>(t.param) + at * p_bytes, d.grad = static_cast<const uint8_t*>(t.grad) + at * g_bytes;
             d.m = static_cast<uint8_t*>(t.m) + at * s_bytes, d.v = static_cast<uint8_t*>(t.v) + at * s_bytes;
@@ -411,19 +429,12 @@ int32_t adamw_build(const dcr_adamw_tensor* tensors, uint64_t n, dcr_adamw_plan&
                 d.v_scales = static_cast<uint8_t*>(t.v_scales) + at / kStateBlock;
             }
             if (t.copy) d.copy = static_cast<uint16_t*>(t.copy) + at;
-            d.first = t.first + at, d.numel = uint32_t(std::min<uint64_t>(kAChunk, t.numel - at));
+            d.first = t.first + at, d.numel = uint32_t(size);
             d.no_decay = t.flags & DCR_ADAMW_NO_DECAY;
-            to.push_back(d);
+            memcpy(p.blob.data() + p.off_entries + to[variant(t)][!shares]++ * sizeof(DevAdam), &d, sizeof(d));
         }
     }
     p.far = bytes > kFarBytes;
-    p.off_chunks = (sizeof(AdamArgs) + 15) / 16 * 16;
-    p.blob.resize(p.off_chunks + chunks * sizeof(DevAdam));
-    for (uint32_t k = 0; k < kVariants; ++k) {
-        p.chunk_first[k + 1] = p.chunk_first[k] + by[k].size();
-        if (!by[k].empty())
-            memcpy(p.blob.data() + p.off_chunks + p.chunk_first[k] * sizeof(DevAdam), by[k].data(), by[k].size() * sizeof(DevAdam));
-    }
     return DCR_OK;
 }
 
@@ -448,16 +459,20 @@ int32_t adamw_step(const dcr_adamw_plan* p, const dcr_adamw_args* h, hipStream_t
     } else {
         a = adam_args(*h, double(h->step), h->lr, h->grad_scale);
     }
-    const DevAdam* chunks = reinterpret_cast<const DevAdam*>(p->dev + p->off_chunks);
+    const DevAdam* entries = reinterpret_cast<const DevAdam*>(p->dev + p->off_entries);
     for (uint32_t k = 0; k < kVariants; ++k) {
         with_type(k & 1, [&](auto tp) {
             with_type(k >> 1 & 1, [&](auto tg) {
                 typedef decltype(tp) TP;
                 typedef decltype(tg) TG;
                 const auto go = [&](auto kernel) {
-                    for (uint64_t c = p->chunk_first[k]; c < p->chunk_first[k + 1]; c += kAMostGroups) {
-                        const uint32_t n = uint32_t(std::min(kAMostGroups, p->chunk_first[k + 1] - c));
-                        hipLaunchKernelGGL(kernel, dim3(n), dim3(kAT), 0, st, chunks + c, a, live);
+                    // entries that are shared, then the others, as many as a launch takes
+                    for (uint64_t e = p->first[k], left = p->shared[k]; e < p->first[k + 1];) {
+                        const uint64_t both = std::min(left, kAMostGroups / kAShare);
+                        const uint64_t one = both < left ? 0 : std::min(p->first[k + 1] - e - both, kAMostGroups - both * kAShare);
+                        hipLaunchKernelGGL(kernel, dim3(uint32_t(both * kAShare + one)), dim3(kAT), 0, st, entries + e,
+                                           uint32_t(both * kAShare), a, live);
+                        e += both + one, left -= both;
                     }
                 };
                 if (k & 4)

@@ -362,3 +362,26 @@ def test_live_arguments_of_several_graphs_stay():
     del T
     gc.collect()
     assert all(r() is None for r in seen)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_tensors_of_every_length_round_a_table_entry(bits):
+    """Lengths on both sides of what an entry of the table and a workgroup have, in one plan, against each by itself."""
+    sizes = [1, 511, 512, 513, 4095, 4096, 4097, 4608, 8192, 8193, 0, 12287, 12289, 36864, 40000]
+    one = lambda n, s: up(np.random.default_rng(s).standard_normal(n).astype(np.float32))  # noqa: E731
+    first = [1 << 20 | i << 16 for i in range(len(sizes))]
+    decay = [i % 2 == 0 for i in range(len(sizes))]
+    copies = lambda ns: [torch.full((n,), 7.0, dtype=torch.bfloat16, device="cuda") for n in ns]  # noqa: E731
+    A = dcr.AdamWTensors([one(n, i) for i, n in enumerate(sizes)], [one(n, 100 + i) for i, n in enumerate(sizes)], bits=bits,
+                         copies=copies(sizes), first=first, decay=decay)
+    B = [dcr.AdamWTensors([one(n, i)], [one(n, 100 + i)], bits=bits, copies=copies([n]), first=[first[i]], decay=[decay[i]])
+         for i, n in enumerate(sizes)]
+    for t in (1, 2):
+        for x in (A, *B):
+            dcr.dcr_adamw_step(x, t, dither=9, weight_decay=0.1, lr=3e-3)
+    for i, b in enumerate(B):
+        for x, y in ((A.params, b.params), (A.m, b.m), (A.v, b.v), (A.copies, b.copies)):
+            raw = torch.int32 if x[i].element_size() == 4 else torch.int16 if x[i].element_size() == 2 else torch.uint8
+            assert torch.equal(x[i].view(raw), y[0].view(raw)), sizes[i]
+        if bits == 8:
+            assert torch.equal(A.m_scales[i], b.m_scales[0]) and torch.equal(A.v_scales[i], b.v_scales[0])

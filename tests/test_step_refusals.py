@@ -188,3 +188,17 @@ def test_dither_is_even():
         for x in (a, b, (a + b) % 1.0, (a[1:] - a[:-1]) % 1.0, (b[32:] - b[:-32]) % 1.0):
             count = np.histogram(x, 16, (0, 1))[0]
             assert np.abs(count - len(x) / 16).max() < 5 * np.sqrt(len(x) / 16), (base, seed, step)
+
+
+def test_adamw_tables_are_small():
+    """An entry of 80 bytes for 4096 elements, and at most eight for what is left of a tensor."""
+    lib = dcr.load_library()
+    far = lambda i: 1 << 44 | i << 40  # noqa: E731
+    for n in (1, 511, 4096, 1 << 30, (1 << 30) + 4095, (1 << 33) + 1):
+        for bits in (8, 32):
+            rc, handle = build(dcr.AdamWDesc(far(0), far(1), far(2), far(3), far(4), far(5), far(6), n, 0, 0, 1, bits, 0))
+            assert rc == dcr.DCR_OK
+            size = ctypes.c_uint64()
+            assert lib.dcr_adamw_plan_bytes(handle, ctypes.byref(size)) == dcr.DCR_OK
+            assert size.value <= 80 * (n // 4096 + 8) + 64, n
+            lib.dcr_adamw_plan_destroy(handle)
