@@ -385,3 +385,44 @@ def test_tensors_of_every_length_round_a_table_entry(bits):
             assert torch.equal(x[i].view(raw), y[0].view(raw)), sizes[i]
         if bits == 8:
             assert torch.equal(A.m_scales[i], b.m_scales[0]) and torch.equal(A.v_scales[i], b.v_scales[0])
+
+
+def test_live_arguments_are_those_passed():
+    """The bias corrections and rates that the GPU makes of `live` are the host's, bit by bit, for many step numbers."""
+    rng = np.random.default_rng(75)
+    n = 256
+    p, g = rng.standard_normal(n).astype(np.float32), rng.standard_normal(n).astype(np.float32)
+    T = dcr.AdamWTensors([up(p)], [up(g)])
+    steps = sorted({int(x) for x in np.exp(rng.uniform(0, np.log(1e6), 120))}) + [1 << 53]
+    for beta1, beta2 in ((0.9, 0.999), (0.93, 0.9501), (0.5, 0.99999)):
+        for t in steps:
+            lr, scale = float(rng.uniform(1e-6, 1e-2)), float(rng.uniform(0.1, 2))
+            got = []
+            for live in (None, torch.tensor([t, lr, scale], dtype=torch.float64, device="cuda")):
+                T.params[0].copy_(up(p))
+                T.m[0].fill_(0.01), T.v[0].fill_(0.02)
+                dcr.dcr_adamw_step(T, t, lr=lr, grad_scale=scale, beta1=beta1, beta2=beta2, weight_decay=0.1, live=live)
+                got.append(T.params[0].clone())
+            assert torch.equal(*got), (t, beta1)
+
+
+def test_types_mixed_in_one_plan():
+    """Parameters and gradients of both types, moments and lengths of all kinds in one plan, against each by itself."""
+    sizes = [300, 9000, 4096, 70001, 0, 512, 13000, 1, 8192, 5000]
+    pt = [TYPES["fp32" if i % 3 else "bf16"] for i in range(len(sizes))]
+    gt = [TYPES["bf16" if i % 2 else "fp32"] for i in range(len(sizes))]
+    one = lambda i, s: up(np.random.default_rng(s + i).standard_normal(sizes[i]).astype(np.float32))  # noqa: E731
+    copy = lambda i: torch.full((sizes[i],), 7.0, dtype=torch.bfloat16, device="cuda") if pt[i] is torch.float32 else None  # noqa: E731
+    first = [1 << 20 | i << 17 for i in range(len(sizes))]
+    for bits in (8, 32):
+        make = lambda at: dcr.AdamWTensors([one(i, 0).to(pt[i]) for i in at], [one(i, 50).to(gt[i]) for i in at], bits=bits,  # noqa: E731
+                                           copies=[copy(i) for i in at], first=[first[i] for i in at])
+        A, B = make(range(len(sizes))), [make([i]) for i in range(len(sizes))]
+        for t in (1, 2):
+            for x in (A, *B):
+                dcr.dcr_adamw_step(x, t, dither=4, weight_decay=0.1)
+        for i, b in enumerate(B):
+            assert torch.equal(A.params[i], b.params[0]), (bits, sizes[i])
+            assert A.copies[i] is None or torch.equal(A.copies[i], b.copies[0])
+            raw = torch.int32 if bits == 32 else torch.uint8
+            assert torch.equal(A.m[i].view(raw), b.m[0].view(raw)) and torch.equal(A.v[i].view(raw), b.v[0].view(raw))
