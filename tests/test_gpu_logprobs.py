@@ -483,3 +483,31 @@ def test_grad_with_a_foreign_lse():
             want[:, 3] += 1
             tol = np.exp(l) * ((3 * np.abs(l) + 8) * 2.0 ** -23)
             assert (np.abs(f64(d) - want) <= tol + 2.0 ** -23).all(), (rows, base)
+
+
+@pytest.mark.parametrize("rows,vocab", [(9, 700), (9, 5001), (5, 70000)])
+def test_scales_up_to_the_largest_number(rows, vocab):
+    """A temperature near 0: the largest logit (the equal ones in equal parts) has all of the probability, no sum is lost to
+    a scale that leaves the numbers of 32 bits in another base; and a scale near 0 makes all alike."""
+    rng = np.random.default_rng(vocab)
+    x = rng.integers(-50, 50, (rows, vocab)).astype(np.float32)
+    x[:, :3] = -60
+    x[1] = 7
+    x[2, :vocab // 2] = -np.inf
+    t = x.argmax(1)
+    most = x.max(1)
+    equal = (x == most[:, None]).sum(1)
+    for scale in (3.4e38, 2.0 ** 127, 2.4e38, 1e30):
+        lp, lse, ent = (torch.full((rows,), 77.0, device="cuda") for _ in range(3))
+        logits = up(x)
+        dcr.dcr_logprobs(logits, up(t), lp, lse, ent, scale=scale, workspace=dcr.step_workspace())
+        for got, want in ((lp, -np.log(equal)), (ent, np.log(equal))):
+            assert (np.abs(f64(got) - want) <= 2.0 ** -20 + (vocab / 256 + 40) * 2.0 ** -24).all(), scale
+        assert torch.isfinite(lse).all()
+        d, one = torch.empty_like(logits), torch.ones(rows, device="cuda")
+        dcr.dcr_logprobs_grad(logits, torch.full((rows,), -1, device="cuda"), lse, one, d, entropy=ent, dentropy=one * 0, scale=scale)
+        assert (d == 0).all()                              # (no target, no weight of the entropy)
+    lp, lse, ent = (torch.full((rows,), 77.0, device="cuda") for _ in range(3))
+    dcr.dcr_logprobs(up(x), up(t), lp, lse, ent, scale=2.0 ** -140, workspace=dcr.step_workspace())
+    n = np.isfinite(x).sum(1)
+    assert (np.abs(f64(lp) + np.log(n)) <= 2.0 ** -19 + (vocab / 256 + 40) * 2.0 ** -24).all()
