@@ -49,7 +49,7 @@ struct Sums {
 };
 
 // the scale in base 2, a finite number (0 times infinity is none)
-__device__ __forceinline__ float unit_of(float scale) { return fminf(scale * kLog2e, 0x1.fffffep127f); }
+__device__ __forceinline__ float base2_of(float scale) { return fminf(scale * kLog2e, 0x1.fffffep127f); }
 
 // the difference of a largest logit to a larger one; held to -160 (2^-160 is 0,
 // and -infinity times that is not)
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kLT, !TOP ? 8 : sizeof(T) == 2 ? 6 : 5) logpro
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
     const uint32_t from = part * a.part_len, to = min(a.vocab, from + a.part_len);
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
-    const float unit = unit_of(a.scale);
+    const float unit = base2_of(a.scale);
     Sums sum = {-INFINITY, 0.0f, 0.0f};
     uint64_t least = 0;
     Raw8<T> raw[2];
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kLT, TOP ? 6 : 8) logprobs_wave_kernel(LpArgs 
     if (row >= a.rows) return;
     const uint32_t from = part * a.part_len, to = min(a.vocab, from + a.part_len);
     const T* x = static_cast<const T*>(a.logits) + uint64_t(row) * a.stride;
-    const float unit = unit_of(a.scale);
+    const float unit = base2_of(a.scale);
     constexpr uint32_t STEP = 64 * kPiece;
     Sums sum = {-INFINITY, 0.0f, 0.0f};
     const uint32_t wave = unit_of % kLWaves;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kLT) logprobs_join_kernel(LpArgs a) {
     __shared__ std::conditional_t<TOP, TopLds, uint32_t> lds;
     __shared__ RowOf row_of;
     const uint32_t row = blockIdx.x;
-    const float unit = unit_of(a.scale);
+    const float unit = base2_of(a.scale);
     const uint32_t n = a.parts * a.top;
     constexpr uint32_t MOST = kMostKeys / kLT;
     uint64_t keys[TOP ? MOST : 1];
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kLT) logprobs_grad_kernel(LpGradArgs a) {
     }
     if (piece) return;
     __shared__ Sums of_wave[kLWaves];
-    const float unit = unit_of(a.scale);
+    const float unit = base2_of(a.scale);
     Sums sum = part_of_row<kLT>(static_cast<const T*>(a.logits) + uint64_t(row) * a.stride, a.vocab, unit);
     sum = join_wave(sum, unit);
     if ((threadIdx.x & 63u) == 0) of_wave[threadIdx.x >> 6] = sum;
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kLT, 8) logprobs_grad_short_kernel(LpGradArgs 
     const bool far = row < a.rows && grad_of<T, 1>(a, row, &at);
     for (uint64_t some = __ballot(far && at == 0); some; some &= some - 1) {
         const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(row), __ffsll((unsigned long long)some) - 1));
-        const float unit = unit_of(a.scale);
+        const float unit = base2_of(a.scale);
         const Sums sum = part_of_row<64>(static_cast<const T*>(a.logits) + uint64_t(r) * a.stride, a.vocab, unit);
         const RowOf of = row_of_far(join_wave(sum, unit), a.lse[r], a.scale);
         for (uint32_t c = (threadIdx.x & 63u) * 8; c < a.vocab; c += 64 * 8) grad_of<T, 1, true>(a, r, &c, of);
