@@ -8,13 +8,13 @@
 // (the decay as a part of p that is taken off: a factor 1 - lr decay comes in steps
 // of 6e-8, and at lr = 1e-6 and decay = 0.1 the decay itself is 1e-7)
 //
-// Bound by memory: everything is read once and written once, 30 bytes an
+// Bound by memory: everything is read once and written once, 28 bytes an
 // element with fp32 states, bf16 gradients and a bf16 copy, 16.1 with states in
 // 8 bits.  A workgroup takes 512 consecutive elements of a tensor and ends, so
 // small tensors cost a workgroup each and no launch, and what runs at once covers
-// a short stretch of every buffer (176 M elements with fp32 states 803 us; 1024
-// elements 820, in two steps 857; 4096 in four 922).  With states in 8 bits the
-// arithmetic comes near: about 80 instructions an element, where 151 M take 390 us
+// a short stretch of every buffer (176 M elements with fp32 states 796 to 810 us;
+// 1024 elements 820, in two steps 857; 4096 in four 922).  With states in 8 bits the
+// arithmetic comes near: about 80 instructions an element, where 151 M take 393 us
 // (with the compiler's division and root and every code's two ways 100, and 413).
 //
 // States in 8 bits: blocks of 32 elements under one power of two (an e8m0

@@ -773,9 +773,10 @@ int32_t logprobs(const void* logits, uint32_t type, uint64_t stride, uint64_t ro
     // Who takes a row (us; `top` 0 and 20).  A wave, where a row is one step of
     // it (16384 x 1000: 12 and 29, a workgroup 33 and 95) or rows fill the GPU
     // (4096 x 16384: 26 and 54, a workgroup 29 and 67; of longest rows only with
-    // `top`: 4096 x 151936 214 and 273, a workgroup 197 and 373); several, so that
-    // 4096 run, where fewer rows are long (1024 x 151936: 60 and 91, workgroups
-    // 61 and 131; but 1024 x 32000 18, workgroups 16) and, with `top`, of 256 rows
+    // `top`: 4096 x 151936 214 and 273, a workgroup 197 and 373); several, up to 4096
+    // in all, where fewer rows are long (1024 x 151936: 60 and 91, workgroups 61 and
+    // 131; but 1024 x 32000 18, workgroups 16; above 2048 rows that is one a row:
+    // 2048 x 151936 110 and 152, 2049 121 and 187) and, with `top`, of 256 rows
     // or more (256 x 151936: 42, workgroups 48; 512 x 32000: 28.6 and 29.5; but 2500
     // x 20000, a wave each, 55 and 51).  Else at least 1024 workgroups, each with a
     // step or more (8 x 151936: 6.5 and 14 in 38 parts, 8.2 and 27 in 10; 256 rows

@@ -868,7 +868,7 @@ void dcr_adamw_plan_destroy(dcr_adamw_plan* plan);
  *   param = param (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * in fp32 (DCR_ADAMW_NO_DECAY: without weight_decay); the update takes the moments before they are rounded
  * to 8 bits.  A block of an 8-bit state that holds a NaN or an infinity becomes
- * NaN; a nonzero second moment never becomes 0.  0 <= beta < 1, eps at least
+ * NaN; the code of a second moment that is not 0 is not 0.  0 <= beta < 1, eps at least
  * 2^-100. */
 int32_t dcr_adamw_step(const dcr_adamw_plan* plan, const dcr_adamw_args* args, void* stream);
 
