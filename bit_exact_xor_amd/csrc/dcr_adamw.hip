@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kAT) adamw_kernel(const DevAdam* entries, uint
         // near a bound as the memory; with fp32 states the division costs no time)
         const float den = __fmaf_rn(w[j], a.root, a.eps);
         const float u = BITS == 8 ? a.rate * m[j] * __builtin_amdgcn_rcpf(den) : a.rate * m[j] / den;
-        p[j] -= __fmaf_rn(p[j], decay, u);
+        // (an infinite parameter stays what it is, as one that a mask is held in)
+        p[j] -= __fmaf_rn(__builtin_amdgcn_fmed3f(p[j], -0x1.fffffep127f, 0x1.fffffep127f), decay, u);
     }
     if (n == 4)
         save4<FAR>(pp, p);

@@ -426,3 +426,24 @@ def test_types_mixed_in_one_plan():
             assert A.copies[i] is None or torch.equal(A.copies[i], b.copies[0])
             raw = torch.int32 if bits == 32 else torch.uint8
             assert torch.equal(A.m[i].view(raw), b.m[0].view(raw)) and torch.equal(A.v[i].view(raw), b.v[0].view(raw))
+
+
+@pytest.mark.parametrize("pt", ["fp32", "bf16"])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_infinite_parameters_stay(bits, pt):
+    """p (1 - lr decay) of an infinite parameter, as a mask that is held among others, is what it was; NaN stays NaN."""
+    n = 1000
+    p = torch.ones(n, device="cuda").to(TYPES[pt])
+    p[3], p[500], p[700] = float("-inf"), float("inf"), float("nan")
+    for decay in (0.0, 0.1):
+        for flag in (True, False):
+            g = torch.zeros(n, device="cuda")
+            g[4] = 1.0
+            T = dcr.AdamWTensors([p.clone()], [g], bits=bits, decay=[flag])
+            for t in (1, 2):
+                dcr.dcr_adamw_step(T, t, weight_decay=decay)
+            q = T.params[0]
+            assert q[3] == float("-inf") and q[500] == float("inf") and torch.isnan(q[700])
+            assert torch.isfinite(q).sum() == n - 3
+            if pt == "fp32":                 # (a step of 1e-3 is less than half of bf16's below 1, 2^-9)
+                assert q[4] < q[5]
