@@ -511,3 +511,37 @@ def test_scales_up_to_the_largest_number(rows, vocab):
     dcr.dcr_logprobs(up(x), up(t), lp, lse, ent, scale=2.0 ** -140, workspace=dcr.step_workspace())
     n = np.isfinite(x).sum(1)
     assert (np.abs(f64(lp) + np.log(n)) <= 2.0 ** -19 + (vocab / 256 + 40) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("vocab", [1, 5, 8, 9, 30, 95, 96, 97, 104, 511])
+def test_grad_of_short_rows_with_a_far_lse(vocab, dtype):
+    """Rows of a thread's and of a wave's, near and far ones side by side, as given and in place.  (Off as above, and what
+    an exponential below 2^-126 leaves.)"""
+    rng = np.random.default_rng(vocab)
+    rows = 137
+    x = rng.standard_normal((rows, vocab)) * 2 + rng.choice([0, 0, 50, -90, 3000, -1e5, 1e20], (rows, 1))
+    x[::9] = -np.inf
+    x[4::9, vocab // 2:] = -np.inf
+    logits = torch.empty(rows, vocab + 3, dtype=TYPES[dtype], device="cuda")[:, 1:vocab + 1].copy_(up(x.astype(np.float32)))
+    x = f64(logits)
+    t = rng.integers(-1, vocab, rows)
+    lse = torch.empty(rows, device="cuda")
+    dcr.dcr_logprobs(logits, None, lse=lse, workspace=dcr.step_workspace())
+    lp, lse64, ent64, p = R.logprobs(x, 1.0)
+    a, b = up(rng.standard_normal(rows).astype(np.float32)), up(rng.standard_normal(rows).astype(np.float32))
+    ent = up(ent64.astype(np.float32))
+    out = torch.full((rows, vocab + 3), 9.0, dtype=TYPES[dtype], device="cuda")
+    dcr.dcr_logprobs_grad(logits, up(t), lse, a, out[:, :vocab], entropy=ent, dentropy=b)
+    hot = np.zeros_like(x)
+    hot[np.arange(rows), np.maximum(t, 0)] = 1
+    aa, be, h = np.where(t < 0, 0, f64(a))[:, None], f64(b)[:, None], f64(ent)[:, None]
+    ll = np.where(p > 0, lp, 0)
+    want = (aa * (hot - p) - be * p * (ll + h)) * ~np.isneginf(lse64)[:, None]
+    off = (3 * np.abs(ll) + 8) * 2.0 ** -23 + 2.0 ** -19 + (vocab / 256 + 40) * 2.0 ** -24 + 2.0 ** -20
+    size = np.abs(aa) + np.abs(be) * (np.abs(ll) + np.abs(h))
+    tol = p * (size + np.abs(be)) * off + 2.0 ** -23 * hot * np.abs(aa) + 2.0 ** -126 * (size + 1)
+    assert (np.abs(f64(out[:, :vocab]) - want) <= tol + HALF[dtype] * (np.abs(want) + tol)).all()
+    assert (out[:, vocab:] == 9).all()
+    dcr.dcr_logprobs_grad(logits, up(t), lse, a, logits, entropy=ent, dentropy=b)
+    assert torch.equal(logits, out[:, :vocab])
