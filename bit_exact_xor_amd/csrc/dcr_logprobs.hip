@@ -621,9 +621,9 @@ constexpr uint32_t kGU = 2;                      // eights of a thread in a row 
 // 1000 and all of it at the lowest finite number, a mask.  From 64 on a row's
 // largest logit and log S are taken apart from one another again, from the logits
 // (log p = scale (x - m) - log S, as the forward call has it), by one workgroup, or
-// wave of short rows, which reads them twice (4096 x 151936 918 us for 399, 10000 x
-// 1264 33 for 13.9, 8 x 151936 87 for 7).  An lse that the logits do not give (of
-// a vocabulary that is held in parts) is taken as it is.
+// of short rows one wave or thread, which reads them twice (4096 x 151936 915 us for
+// 399, 10000 x 1264 33 for 13.9, 8 x 151936 88 for 7).  An lse that the logits do
+// not give (of a vocabulary that is held in parts) is taken as it is.
 constexpr float kFarLse = 64.0f, kOwnLse = 0x1p-22f;
 __device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY; }
 
