@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
 // and of renormalised weights, with r_j = s_j over the sum of the chosen scores:
 //   dl = scale r_j (dw_j - sum dw r)  times 1 - s_j for a sigmoid
 // of the chosen experts alone.  There the scores as such do not occur: r is taken
-// from the chosen logits by their largest, so that scores of any size (at -100 all
+// from the chosen logits by their largest, so that scores of any size (at -104 all
 // are 0 in 32 bits, the weights are not) give derivatives of the weights' size.
 // Only where the scores of the forward call vanish, in 64 bits, do these.
 // A lane has the pairs j = lane, lane + LANES, ..., whose logits it fetches.
