@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kET, R == 1 ? 8 : 4) experts_select_kernel(Sel
 // Only where the scores of the forward call vanish, in 64 bits, do these.
 // A lane has the pairs j = lane, lane + LANES, ..., whose logits it fetches.
 constexpr float kGoneSigmoid = -709.7828f, kGoneSoftmax = -745.1332f;      // below these e^x overflows, or is 0, in 64 bits
-template <typename T, int LANES, int R>
+template <typename T, int LANES, int R, bool RENORM>
 __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) {
     constexpr int N = 8 * R, ROWS = kET / LANES, KEEP = DCR_EXPERTS_MAX_K / LANES;
     const uint32_t lane = threadIdx.x % LANES, at = blockIdx.x * ROWS + threadIdx.x / LANES;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
         top = lanes_max<LANES>(top);
         if (top == -INFINITY) top = 0.0f;
         if (top == INFINITY) top = NAN;        // (as in the choice)
-        if (!a.renormalize) {
+        if (!RENORM) {
             float z = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) z += d[i] = expf(v[i] - top);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
     // the row's scalars in 64 bits: dw and its mean are often nearly the same
     double all = 0.0, dot = 0.0;
     float most = -INFINITY, rest[KEEP];        // largest of the chosen logits (a sigmoid's up to 0); 1 - s
-    if (a.renormalize) {
+    if (RENORM) {
 #pragma unroll
         for (int q = 0; q < KEEP; ++q) {
             if (id[q] == ~0u) continue;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
         rest[q] = 1.0f;
         if (id[q] == ~0u) continue;
         const float l = s[q];
-        if (!a.renormalize) {
+        if (!RENORM) {
             s[q] = a.sigmoid ? 1.0f : expf(l - top) * inv;
         } else if (a.sigmoid) {
             const float e = expf(-fabsf(l));
@@ -495,21 +495,21 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
         } else {
             s[q] = expf(l - most);
         }
-        if (a.renormalize && gone) s[q] = 0.0f;
+        if (RENORM && gone) s[q] = 0.0f;
         all += double(s[q]);
         dot += double(dw[q]) * double(s[q]);
     }
     dot = lanes_sum<LANES>(dot);
     double mean = 0.0;                         // what the renormalisation takes off dw
-    if (a.renormalize) {
+    if (RENORM) {
         all = lanes_sum<LANES>(all);
         if (all == 0.0) all = 1.0;
         mean = dot / all;
     }
-    const float off = a.sigmoid || a.renormalize ? 0.0f : float(dot * double(a.scale));
+    const float off = a.sigmoid || RENORM ? 0.0f : float(dot * double(a.scale));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (a.renormalize) {
+        if (RENORM) {
             v[i] = top == top ? 1.0f : NAN;
         } else if (a.sigmoid) {
             const float q = expf(-fabsf(v[i]));    // s (1 - s) = q / (1 + q)^2
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kET) experts_select_grad_kernel(SelectArgs a) 
     for (int q = 0; q < KEEP; ++q) {
         if (uint32_t(q) * LANES >= a.k) break;
         float ds = dw[q] * a.scale;
-        if (a.renormalize) ds = float((double(dw[q]) - mean) * double(a.scale) * (double(s[q]) / all * double(rest[q])));
+        if (RENORM) ds = float((double(dw[q]) - mean) * double(a.scale) * (double(s[q]) / all * double(rest[q])));
         for (uint32_t j = 0; j < min(uint32_t(LANES), a.k - q * LANES); ++j) {
             const uint32_t e = uint32_t(__shfl(int(id[q]), base + int(j), 64));
             const float of = __shfl(ds, base + int(j), 64);
@@ -785,7 +785,9 @@ int32_t select_grad(const void* logits, uint32_t type, uint64_t stride, uint64_t
         with_lanes(experts, 0, rows, [&](auto lanes, auto r) {
             constexpr int L = decltype(lanes)::value, ROWS = kET / L;
             const uint32_t grid = uint32_t((rows + ROWS - 1) / ROWS);      // (rows: see check_select)
-            hipLaunchKernelGGL((experts_select_grad_kernel<decltype(t), L, decltype(r)::value>), dim3(grid), dim3(kET), 0, st, a);
+            const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kET), 0, st, a); };
+            a.renormalize ? go(experts_select_grad_kernel<decltype(t), L, decltype(r)::value, true>)
+                          : go(experts_select_grad_kernel<decltype(t), L, decltype(r)::value, false>);
         });
     });
     return step_launched();
